@@ -412,6 +412,115 @@ cr_status cr_calibrate_noalloc(const double* d_S, int lds, int n_p, int M, const
                                uint8_t* d_cout, int32_t* d_count, double* d_psi, double* d_phi,
                                cr_calib_info* out, cr_stream stream);
 
+/* ---------------------------------------------------------------- trend network
+ * Operators of a learned trend: a network over space-time covariates whose outputs are columns
+ * of the universal-kriging designs Xo, Xp (the paper takes the design as given; these have no
+ * counterpart there).  The operators are an affine product with its epilogue, the
+ * root-mean-square norm, and a gated recurrence along time, each with its gradient, and the
+ * forms that answer single columns or time steps.
+ *
+ * Conventions, next to those at the top of this file:
+ *  - A matrix is features x columns, column-major: a column is one site at one time and is
+ *    contiguous.  Leading dimensions count elements of the matrix's own type and are >= the
+ *    number of rows (any value is right; multiples of 16 bytes at 16-byte aligned addresses
+ *    are fastest).  Inputs are only read, and outputs overlap no input unless a call says so.
+ *  - Elements are FP32, FP16, BF16 or e4m3 (FP8, largest value 448) as a CR_TYPE_* argument
+ *    says; arithmetic, sums and states are FP32, and each output is rounded once, to nearest.
+ *  - Scratch comes from the pools of cr_workspace_trim.  Calls are asynchronous, and results do
+ *    not depend on timing: the same call on the same inputs gives the same bits.
+ *  - Zero columns (M, T, B or n_seq = 0) are allowed: sums over them are zero.
+ *  - A device-side wait that runs out (CR_OPT_WAIT_LIMIT_US; never in normal operation)
+ *    invalidates the outputs of its call and makes the next call of this section on any
+ *    stream return CR_ERR_TIMEOUT once. */
+enum { CR_TYPE_F32 = 0, CR_TYPE_F16 = 1, CR_TYPE_BF16 = 2, CR_TYPE_E4M3 = 3 };
+
+/* Activations: z, max(z, 0), z sigmoid(z), z Phi(z) (Phi the normal distribution function). */
+enum { CR_ACT_NONE = 0, CR_ACT_RELU = 1, CR_ACT_SILU = 2, CR_ACT_GELU = 3 };
+
+/* Gates of the recurrence h_t = a_t h_{t-1} + c_t x_t, from the gate input g_t:
+ *  CR_GATE_COEFF     a = g, c = 1                               (g is the coefficient)
+ *  CR_GATE_CONVEX    a = sigmoid(g), c = 1 - a                  (a running mean)
+ *  CR_GATE_VARIANCE  a = sigmoid(g), c = sqrt(1 - a^2)          (AR(1) with the variance of x) */
+enum { CR_GATE_COEFF = 0, CR_GATE_CONVEX = 1, CR_GATE_VARIANCE = 2 };
+
+/* Affine product with its epilogue: Y = act(Z) + R, Z = diag(wscale) W^T X diag(xscale) + b 1^T,
+ * for W (K x N, ldw), X (K x M, ldx), b (N), R, Z and Y (N x M); K, N >= 1.  `type` is that of
+ * W and X: CR_TYPE_F16, CR_TYPE_BF16 or CR_TYPE_E4M3; out_type that of R, Z and Y: CR_TYPE_F32,
+ * CR_TYPE_F16 or CR_TYPE_BF16.  d_wscale (N) and d_xscale (M) are FP32 and belong to e4m3 (both
+ * NULL otherwise, either may be NULL there).  d_bias (FP32), d_R and d_Z may be NULL; a non-NULL d_Z
+ * receives Z, which cr_affine_backward reads.  Products are accumulated in FP32; d_R may be
+ * d_Y (with ldr = ldy). */
+cr_status cr_affine(int type, const void* d_W, int ldw, const void* d_X, int ldx, int K, int N,
+                    int M, const float* d_wscale, const float* d_xscale, const float* d_bias,
+                    int act, int out_type, const void* d_R, int ldr, void* d_Z, int ldz,
+                    void* d_Y, int ldy, cr_stream stream);
+
+/* Gradient of cr_affine (FP16 or BF16, no scales) for dY (N x M): with G = dY .* act'(Z),
+ * dX = W G (K x M), dW = X G^T (K x N), db = G 1 (N, FP32).  W, X, dY, Z and dX have `type`, dW has
+ * dw_type (`type` or CR_TYPE_F32).  Each of d_dX, d_dW, d_db may be NULL (not wanted); d_W may be
+ * NULL without d_dX, d_X without d_dW, d_Z with CR_ACT_NONE.  The gradient of R is dY itself.
+ * G is rounded to `type` before the two products (not for db) and held in 2 N M bytes of scratch
+ * when act is not CR_ACT_NONE. */
+cr_status cr_affine_backward(int type, const void* d_W, int ldw, const void* d_X, int ldx,
+                             const void* d_dY, int lddy, const void* d_Z, int ldz, int K, int N,
+                             int M, int act, void* d_dX, int lddx, int dw_type, void* d_dW,
+                             int lddw, float* d_db, cr_stream stream);
+
+/* Root-mean-square norm of each column, with the residual's addition: H = X + R (X when d_R is
+ * NULL), y = gamma .* h / sqrt(mean(h^2) + eps), for X, R, H, Y D x T and gamma (D, FP32);
+ * D >= 1, eps >= 0.  `type` (CR_TYPE_F32, CR_TYPE_F16, CR_TYPE_BF16) is that of X, R and H.
+ * d_H (may be NULL) receives H and may be d_X or d_R (with the same leading dimension).  y is
+ * formed from the unrounded sum.
+ * out_type = type: Y holds y, d_scale is NULL.  out_type = CR_TYPE_E4M3: column t of Y holds
+ * y / scale_t with scale_t = max(max|y|, 2^-100) / 448, and d_scale (T, FP32) receives the
+ * scales; a column with a NaN or infinite sum is NaN and has a NaN scale. */
+cr_status cr_rmsnorm(int type, const void* d_X, int ldx, const void* d_R, int ldr,
+                     const float* d_gamma, int D, int T, double eps, void* d_H, int ldh,
+                     int out_type, void* d_Y, int ldy, float* d_scale, cr_stream stream);
+
+/* Gradient of the norm at H (the sum, as cr_rmsnorm wrote it): with r = 1 / sqrt(mean(h^2) + eps)
+ * and u = gamma .* dy, dX = r u - h r^3 mean(u .* h) + dH, dgamma = sum_t dy .* h r (FP32).
+ * H, dY, dH, dX (D x T) have `type`.  d_dH (may be NULL) is the gradient that reaches H past the
+ * norm; dX is the gradient of X and of R alike.  d_dX and d_dgamma may each be NULL; d_dX may
+ * be d_dY or d_dH (with the same leading dimension). */
+cr_status cr_rmsnorm_backward(int type, const void* d_H, int ldh, const float* d_gamma,
+                              const void* d_dY, int lddy, const void* d_dH, int lddh, int D,
+                              int T, double eps, void* d_dX, int lddx, float* d_dgamma,
+                              cr_stream stream);
+
+/* Gated recurrence along time over packed series: series s holds the columns
+ * off[s] .. off[s+1]-1 (d_off: n_seq + 1 int32 on the device, off[0] = 0, ascending, off[n_seq] = T;
+ * empty series allowed; NULL means one series of T columns).  Within a series h_t = a_t h_{t-1} +
+ * c_t x_t (CR_GATE_*), starting from its column of h0 (D x n_seq FP32; NULL: zero).  G, X, H are
+ * D x T of `type` (CR_TYPE_F32, CR_TYPE_F16, CR_TYPE_BF16); states are FP32 and H is rounded
+ * from them.  hT (D x n_seq FP32, may be NULL) receives the last state of each series, h0 where
+ * it is empty.  d_H may be NULL.  d_saved (may be NULL) receives the states that
+ * cr_gated_scan_backward restarts from: *count of cr_gated_scan_saved FP32 values.
+ * Series do not mix: a NaN or infinity in one leaves the others alone. */
+cr_status cr_gated_scan_saved(int D, int T, size_t* count);
+cr_status cr_gated_scan(int type, int gate, const void* d_G, int ldg, const void* d_X, int ldx,
+                        int D, int T, const int32_t* d_off, int n_seq, const float* d_h0,
+                        int ldh0, void* d_H, int ldh, float* d_hT, int ldhT, float* d_saved,
+                        cr_stream stream);
+
+/* Gradient of cr_gated_scan for dH (D x T of `type`) and dhT (D x n_seq FP32; NULL: zero): with
+ * q_t = dh_t + a_{t+1} q_{t+1} (plus dhT at a series' last step), dX = c q, dG = q (h_{t-1} da/dg
+ * + x dc/dg), dh0 = a q at the series' first step (dhT where it is empty).  d_dG, d_dX, d_dh0
+ * may each be NULL.  d_saved is the forward call's; NULL: recomputed into scratch. */
+cr_status cr_gated_scan_backward(int type, int gate, const void* d_G, int ldg, const void* d_X,
+                                 int ldx, const void* d_dH, int lddh, int D, int T,
+                                 const int32_t* d_off, int n_seq, const float* d_h0, int ldh0,
+                                 const float* d_dhT, int lddhT, const float* d_saved, void* d_dG,
+                                 int lddg, void* d_dX, int lddx, float* d_dh0, int lddh0,
+                                 cr_stream stream);
+
+/* One step of the recurrence for B series: hnext = a h + c x, for G, X (D x B of `type`) and h,
+ * hnext (D x B FP32; d_hnext may be d_h with the same leading dimension).  d_H (D x B of `type`,
+ * may be NULL) receives hnext rounded. */
+cr_status cr_gated_step(int type, int gate, const void* d_G, int ldg, const void* d_X, int ldx,
+                        const float* d_h, int ldh, int D, int B, void* d_H, int ldo,
+                        float* d_hnext, int ldn, cr_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -23,6 +23,13 @@ The functions mirror include/cr.h:
   correct_calibrate_prepared(Wp, ...)    cr_correct_calibrate_prepared
   calibrate(S, zhat, v, u, level)        cr_calibrate (negative=True: cr_calibrate_negative)
   morton_order(xy)                       cr_morton_order (host only)
+  affine(W, X, bias, act, residual)      cr_affine
+  affine_backward(W, X, dY, Z, act)      cr_affine_backward
+  rmsnorm(X, gamma, residual)            cr_rmsnorm (rmsnorm_e4m3: the 8-bit output)
+  rmsnorm_backward(H, gamma, dY, dH)     cr_rmsnorm_backward
+  gated_scan(G, X, gate, offsets, h0)    cr_gated_scan
+  gated_scan_backward(G, X, dH, ...)     cr_gated_scan_backward
+  gated_step(G, X, h, gate)              cr_gated_step
 The library is never replaced by a fallback: if libcr.so is missing or fails to load, every
 call raises.
 """
@@ -44,6 +51,9 @@ CR_TRMM_FP16_DEST, CR_TRMM_GENERATE, CR_TRMM_SPLIT_L, CR_TRMM_FP16_PER_GEMM = 1,
 CR_OPT_WAIT_LIMIT_US, CR_OPT_DIAG_ARITH, CR_OPT_FP64_GEMM = 1, 2, 4
 CR_DIAG_AUTO, CR_DIAG_FP64, CR_DIAG_DF = 0, 1, 2
 CR_GEMM_DF, CR_GEMM_OZAKI = 0, 1
+CR_TYPE_F32, CR_TYPE_F16, CR_TYPE_BF16, CR_TYPE_E4M3 = 0, 1, 2, 3
+CR_ACT_NONE, CR_ACT_RELU, CR_ACT_SILU, CR_ACT_GELU = 0, 1, 2, 3
+CR_GATE_COEFF, CR_GATE_CONVEX, CR_GATE_VARIANCE = 0, 1, 2
 CR_PEAK_DFMA, CR_PEAK_FFMA, CR_PEAK_DF_MAC, CR_PEAK_DMMA = 1, 2, 3, 4
 STATUS = {0: "CR_OK", 1: "CR_ERR_ARG", 2: "CR_ERR_CUDA", 3: "CR_ERR_NOMEM", 4: "CR_ERR_NOT_SPD",
           5: "CR_ERR_EMPTY_SAMPLE", 6: "CR_ERR_NONPOS_MSPE", 7: "CR_ERR_TIMEOUT", 8: "CR_ERR_STATE",
@@ -121,6 +131,15 @@ _SIGNATURES = {
     "cr_krige_correct_prepared": (_I, [_P, _P, _P, _I, _I, _P, _I, _P]),
     "cr_correct_calibrate_prepared": (_I, [_P, _P, _P, _I, _I, _P, _P, _D, _D, _I, _P, _P, _P, _P, _P,
                                            ctypes.POINTER(CalibInfo), _P]),
+    "cr_affine": (_I, [_I, _P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P, _I, _P, _I, _P, _I, _P]),
+    "cr_affine_backward": (_I, [_I, _P, _I, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _P, _I, _I, _P, _I, _P, _P]),
+    "cr_rmsnorm": (_I, [_I, _P, _I, _P, _I, _P, _I, _I, _D, _P, _I, _I, _P, _I, _P, _P]),
+    "cr_rmsnorm_backward": (_I, [_I, _P, _I, _P, _P, _I, _P, _I, _I, _I, _D, _P, _I, _P, _P]),
+    "cr_gated_scan_saved": (_I, [_I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    "cr_gated_scan": (_I, [_I, _I, _P, _I, _P, _I, _I, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _P]),
+    "cr_gated_scan_backward": (_I, [_I, _I, _P, _I, _P, _I, _P, _I, _I, _I, _P, _I, _P, _I, _P, _I, _P, _P, _I, _P, _I,
+                                    _P, _I, _P]),
+    "cr_gated_step": (_I, [_I, _I, _P, _I, _P, _I, _P, _I, _I, _I, _P, _I, _P, _I, _P]),
 }
 
 
@@ -488,3 +507,279 @@ def calibrate(S, zhat, v, u: float, level: float, counts: bool = True, extrema: 
     if extrema:
         out["psi"], out["phi"] = psi, phi
     return out
+
+
+# ---------------------------------------------------------------- trend network
+
+_ACTS = {"none": CR_ACT_NONE, "relu": CR_ACT_RELU, "silu": CR_ACT_SILU, "gelu": CR_ACT_GELU}
+_GATES = {"coeff": CR_GATE_COEFF, "convex": CR_GATE_CONVEX, "variance": CR_GATE_VARIANCE}
+_types = None
+
+
+def _type_of(t, what: str) -> int:
+    """CR_TYPE_* of a CUDA tensor."""
+    global _types
+    if _types is None:
+        import torch
+        _types = {torch.float32: CR_TYPE_F32, torch.float16: CR_TYPE_F16, torch.bfloat16: CR_TYPE_BF16,
+                  torch.float8_e4m3fn: CR_TYPE_E4M3}
+    k = _types.get(t.dtype)
+    if k is None or not t.is_cuda:
+        raise CrError(1, f"{what}: a CUDA tensor of FP32, FP16, BF16 or e4m3 is needed, not {t.dtype} on {t.device}")
+    return k
+
+
+def _matrix(t, shape, dtype, what: str):
+    """(tensor, address, leading dimension) of a column-major matrix argument, copied if it is
+    not column-major; (None, None, rows) for None."""
+    if t is None:
+        return None, None, shape[0]
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda:
+        raise CrError(1, f"{what}: a CUDA matrix of shape {tuple(shape)} and {dtype} is needed, not "
+                         f"{tuple(t.shape)} and {t.dtype} on {t.device}")
+    n, m = shape
+    s0, s1 = t.stride()
+    if (s0 != 1 and n > 1) or (s1 < n and m > 1):
+        t = t.T.contiguous().T
+        s1 = n
+    return t, t.data_ptr(), s1 if m > 1 else n
+
+
+def _vector(t, n: int, what: str):
+    """(tensor, address) of an FP32 vector argument, copied if it is strided."""
+    if t is None:
+        return None, None
+    _type_of(t, what)
+    if t.dim() != 1 or t.shape[0] != n or t.element_size() != 4:
+        raise CrError(1, f"{what}: an FP32 vector of {n} is needed, not {tuple(t.shape)} and {t.dtype}")
+    t = t.contiguous()
+    return t, t.data_ptr()
+
+
+def _empty(n: int, m: int, like, dtype=None):
+    return like.new_empty((m, n), dtype=dtype or like.dtype).T
+
+
+def _on_stream(fn):
+    """Runs the call with `stream` as the current stream, so that its outputs and copies belong
+    to it, and keeps the memory of its arguments until the stream has passed the call."""
+    import functools
+
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        import torch
+        with torch.cuda.stream(stream):
+            for t in (*args, *kw.values()):
+                if isinstance(t, torch.Tensor) and t.is_cuda:
+                    t.record_stream(stream)
+            return fn(*args, **kw)
+    return call
+
+
+def _raw_stream(device) -> int:
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _code(table, name, what: str) -> int:
+    k = table.get(name)
+    if k is None:
+        raise CrError(1, f"{what} is one of {sorted(table)}, not {name!r}")
+    return k
+
+
+def _matrix_shape(t, what: str):
+    if t.dim() != 2:
+        raise CrError(1, f"{what}: a matrix is needed, not {t.dim()} dimensions")
+    return t.shape
+
+
+@_on_stream
+def affine(W, X, bias=None, act: str = "none", residual=None, w_scale=None, x_scale=None, out_dtype=None,
+           save: bool = False, out=None):
+    """cr_affine: Y = act(W^T X + bias) + residual for W (K, N) and X (K, M); e4m3 operands take
+    w_scale (N) and x_scale (M).  out_dtype: FP32, FP16 or BF16 (default: X's, BF16 for e4m3).
+    save=True returns (Y, Z) with Z the pre-activation that affine_backward reads."""
+    load()
+    kind = _type_of(X, "affine X")
+    K, M = _matrix_shape(X, "affine X")
+    N = _matrix_shape(W, "affine W")[1]
+    X, px, ldx = _matrix(X, (K, M), X.dtype, "affine X")
+    W, pw, ldw = _matrix(W, (K, N), X.dtype, "affine W")
+    if out is None:
+        if out_dtype is None:
+            if kind == CR_TYPE_E4M3:
+                import torch
+                out_dtype = torch.bfloat16
+            else:
+                out_dtype = X.dtype
+        out = _empty(N, M, X, out_dtype)
+    y, py, ldy = _matrix(out, (N, M), out_dtype or out.dtype, "affine out")
+    if y is not out:
+        raise CrError(1, "affine out: a column-major matrix is needed")
+    R, pr, ldr = _matrix(residual, (N, M), out.dtype, "affine residual")
+    Z = _empty(N, M, X, out.dtype) if save else None
+    bias, pb = _vector(bias, N, "affine bias")
+    w_scale, pws = _vector(w_scale, N, "affine w_scale")
+    x_scale, pxs = _vector(x_scale, M, "affine x_scale")
+    _check(_lib.cr_affine(kind, pw, ldw, px, ldx, K, N, M, pws, pxs, pb, _code(_ACTS, act, "affine act"),
+                          _type_of(out, "affine out"), pr, ldr, Z.data_ptr() if save else None, N, py, ldy,
+                          _raw_stream(X.device)))
+    return (out, Z) if save else out
+
+
+@_on_stream
+def affine_backward(W, X, dY, Z=None, act: str = "none", need=(True, True, True), dw_dtype=None):
+    """cr_affine_backward: (dX, dW, dbias) of affine at the saved Z; need says which of the three
+    are wanted (None for the others).  dw_dtype: X's type (default) or FP32."""
+    load()
+    kind = _type_of(X, "affine_backward X")
+    K, M = _matrix_shape(X, "affine_backward X")
+    N = _matrix_shape(W, "affine_backward W")[1]
+    X, px, ldx = _matrix(X, (K, M), X.dtype, "affine_backward X")
+    W, pw, ldw = _matrix(W, (K, N), X.dtype, "affine_backward W")
+    dY, pdy, lddy = _matrix(dY, (N, M), X.dtype, "affine_backward dY")
+    Z, pz, ldz = _matrix(Z, (N, M), X.dtype, "affine_backward Z")
+    dX = _empty(K, M, X) if need[0] else None
+    dW = _empty(K, N, X, dw_dtype) if need[1] else None
+    db = X.new_empty(N, dtype=_f32()) if need[2] else None
+    _check(_lib.cr_affine_backward(kind, pw, ldw, px, ldx, pdy, lddy, pz, ldz, K, N, M,
+                                   _code(_ACTS, act, "affine_backward act"), _ptr(dX), K,
+                                   _type_of(dW, "affine_backward dw_dtype") if need[1] else kind, _ptr(dW), K, _ptr(db),
+                                   _raw_stream(X.device)))
+    return dX, dW, db
+
+
+def _f32():
+    import torch
+    return torch.float32
+
+
+def _rmsnorm(X, gamma, residual, eps, e4m3: bool):
+    load()
+    kind = _type_of(X, "rmsnorm X")
+    D, T = _matrix_shape(X, "rmsnorm X")
+    X, px, ldx = _matrix(X, (D, T), X.dtype, "rmsnorm X")
+    R, pr, ldr = _matrix(residual, (D, T), X.dtype, "rmsnorm residual")
+    gamma, pg = _vector(gamma, D, "rmsnorm gamma")
+    H = _empty(D, T, X) if R is not None else None
+    Y, scale, out = X, None, kind
+    if e4m3:
+        import torch
+        Y, out = _empty(D, T, X, torch.float8_e4m3fn), CR_TYPE_E4M3
+        scale = X.new_empty(T, dtype=torch.float32)
+    else:
+        Y = _empty(D, T, X)
+    _check(_lib.cr_rmsnorm(kind, px, ldx, pr, ldr, pg, D, T, eps, _ptr(H), D, out, Y.data_ptr(), D, _ptr(scale),
+                           _raw_stream(X.device)))
+    return Y, scale, H
+
+
+@_on_stream
+def rmsnorm(X, gamma, residual=None, eps: float = 1e-6):
+    """cr_rmsnorm: (Y, H) with H = X + residual (None without one) and Y its normalised columns."""
+    Y, _, H = _rmsnorm(X, gamma, residual, eps, False)
+    return Y, H
+
+
+@_on_stream
+def rmsnorm_e4m3(X, gamma, residual=None, eps: float = 1e-6):
+    """cr_rmsnorm with the 8-bit output: (Y in e4m3, scale per column, H)."""
+    return _rmsnorm(X, gamma, residual, eps, True)
+
+
+@_on_stream
+def rmsnorm_backward(H, gamma, dY, dH=None, eps: float = 1e-6):
+    """cr_rmsnorm_backward: (dX, dgamma) at the sum H that rmsnorm returned (or its X)."""
+    load()
+    kind = _type_of(H, "rmsnorm_backward H")
+    D, T = _matrix_shape(H, "rmsnorm_backward H")
+    H, ph, ldh = _matrix(H, (D, T), H.dtype, "rmsnorm_backward H")
+    dY, pdy, lddy = _matrix(dY, (D, T), H.dtype, "rmsnorm_backward dY")
+    dH, pdh, lddh = _matrix(dH, (D, T), H.dtype, "rmsnorm_backward dH")
+    gamma, pg = _vector(gamma, D, "rmsnorm_backward gamma")
+    dX = _empty(D, T, H)
+    dgamma = H.new_empty(D, dtype=_f32())
+    _check(_lib.cr_rmsnorm_backward(kind, ph, ldh, pg, pdy, lddy, pdh, lddh, D, T, eps, dX.data_ptr(), D,
+                                    dgamma.data_ptr(), _raw_stream(H.device)))
+    return dX, dgamma
+
+
+def _series(offsets, what: str):
+    """(tensor, address, number of series) of the offsets."""
+    if offsets is None:
+        return None, None, 1
+    import torch
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 1 or not offsets.is_cuda:
+        raise CrError(1, f"{what}: int32 CUDA offsets (series + 1) are needed")
+    offsets = offsets.contiguous()
+    return offsets, offsets.data_ptr(), offsets.shape[0] - 1
+
+
+@_on_stream
+def gated_scan(G, X, gate: str = "convex", offsets=None, h0=None, save: bool = False):
+    """cr_gated_scan: (H, hT) for G and X (D, T) with packed series in the T columns; save=True
+    returns (H, hT, saved), saved being what gated_scan_backward restarts from."""
+    import torch
+    load()
+    kind = _type_of(X, "gated_scan X")
+    D, T = _matrix_shape(X, "gated_scan X")
+    X, px, ldx = _matrix(X, (D, T), X.dtype, "gated_scan X")
+    G, pg, ldg = _matrix(G, (D, T), X.dtype, "gated_scan G")
+    offsets, po, n = _series(offsets, "gated_scan offsets")
+    h0, p0, ld0 = _matrix(h0, (D, n), torch.float32, "gated_scan h0")
+    H, hT = _empty(D, T, X), _empty(D, n, X, torch.float32)
+    saved = None
+    if save:
+        count = ctypes.c_size_t(0)
+        _check(_lib.cr_gated_scan_saved(D, T, ctypes.byref(count)))
+        saved = X.new_empty(count.value, dtype=torch.float32)
+    _check(_lib.cr_gated_scan(kind, _code(_GATES, gate, "gated_scan gate"), pg, ldg, px, ldx, D, T, po, n, p0, ld0,
+                              H.data_ptr(), D, hT.data_ptr(), D, _ptr(saved), _raw_stream(X.device)))
+    return (H, hT, saved) if save else (H, hT)
+
+
+@_on_stream
+def gated_scan_backward(G, X, dH, gate: str = "convex", offsets=None, h0=None, dhT=None, saved=None):
+    """cr_gated_scan_backward: (dG, dX, dh0); saved is gated_scan's (None: recomputed)."""
+    import torch
+    load()
+    kind = _type_of(X, "gated_scan_backward X")
+    D, T = _matrix_shape(X, "gated_scan_backward X")
+    X, px, ldx = _matrix(X, (D, T), X.dtype, "gated_scan_backward X")
+    G, pg, ldg = _matrix(G, (D, T), X.dtype, "gated_scan_backward G")
+    dH, pd, ldd = _matrix(dH, (D, T), X.dtype, "gated_scan_backward dH")
+    offsets, po, n = _series(offsets, "gated_scan_backward offsets")
+    h0, p0, ld0 = _matrix(h0, (D, n), torch.float32, "gated_scan_backward h0")
+    dhT, pt, ldt = _matrix(dhT, (D, n), torch.float32, "gated_scan_backward dhT")
+    if saved is not None:
+        count = ctypes.c_size_t(0)
+        _check(_lib.cr_gated_scan_saved(D, T, ctypes.byref(count)))
+        _vector(saved, count.value, "gated_scan_backward saved")
+    dG, dX, dh0 = _empty(D, T, X), _empty(D, T, X), _empty(D, n, X, torch.float32)
+    _check(_lib.cr_gated_scan_backward(kind, _code(_GATES, gate, "gated_scan_backward gate"), pg, ldg, px, ldx, pd, ldd,
+                                       D, T, po, n, p0, ld0, pt, ldt, _ptr(saved), dG.data_ptr(), D, dX.data_ptr(), D,
+                                       dh0.data_ptr(), D, _raw_stream(X.device)))
+    return dG, dX, dh0
+
+
+@_on_stream
+def gated_step(G, X, h, gate: str = "convex", out=None):
+    """cr_gated_step: (H, hnext) for one step of B series; out receives hnext and may be h."""
+    import torch
+    load()
+    kind = _type_of(X, "gated_step X")
+    D, B = _matrix_shape(X, "gated_step X")
+    X, px, ldx = _matrix(X, (D, B), X.dtype, "gated_step X")
+    G, pg, ldg = _matrix(G, (D, B), X.dtype, "gated_step G")
+    h, ph, ldh = _matrix(h, (D, B), torch.float32, "gated_step h")
+    hn = _empty(D, B, X, torch.float32) if out is None else out
+    n, pn, ldn = _matrix(hn, (D, B), torch.float32, "gated_step out")
+    if n is not hn:
+        raise CrError(1, "gated_step out: a column-major matrix is needed")
+    H = _empty(D, B, X)
+    _check(_lib.cr_gated_step(kind, _code(_GATES, gate, "gated_step gate"), pg, ldg, px, ldx, ph, ldh, D, B,
+                              H.data_ptr(), D, pn, ldn, _raw_stream(X.device)))
+    return H, hn

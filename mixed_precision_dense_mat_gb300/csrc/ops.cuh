@@ -1,0 +1,127 @@
+// Shared by the trend-network operators (affine.cu, norm.cu, scan.cu): element types,
+// activations, and the guards of their C entries.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <new>
+
+#include "common.cuh"
+
+namespace cr {
+
+cr_status fail_literal(cr_status code, const char* msg);
+
+// Sticky word in mapped host memory that a kernel sets when one of its bounded waits runs out;
+// the next operator call reports and clears it.  Reading it costs no synchronisation.
+cr_status wait_word(int** d_word);
+
+// C++ exceptions end at the C entries.
+#define CR_ENTRY_BEGIN try {
+#define CR_ENTRY_END(what)                                                                    \
+  }                                                                                           \
+  catch (const std::bad_alloc&) { return ::cr::fail_literal(CR_ERR_NOMEM, what ": host memory"); } \
+  catch (...) { return ::cr::fail_literal(CR_ERR_STATE, what ": unexpected host exception"); }
+
+#define CR_REQUIRE(cond, msg) \
+  do {                        \
+    if (!(cond)) return ::cr::fail_literal(CR_ERR_ARG, msg); \
+  } while (0)
+
+// ---------------------------------------------------------------- element types
+template <class T> __device__ __forceinline__ float to_float(T x);
+template <> __device__ __forceinline__ float to_float<float>(float x) { return x; }
+template <> __device__ __forceinline__ float to_float<__half>(__half x) { return __half2float(x); }
+template <> __device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <> __device__ __forceinline__ float to_float<__nv_fp8_e4m3>(__nv_fp8_e4m3 x) { return float(x); }
+
+template <class T> __device__ __forceinline__ T from_float(float x);
+template <> __device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <> __device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <> __device__ __forceinline__ __nv_fp8_e4m3 from_float<__nv_fp8_e4m3>(float x) { return __nv_fp8_e4m3(x); }
+
+inline int type_bytes(int type) {
+  return type == CR_TYPE_F32 ? 4 : type == CR_TYPE_E4M3 ? 1 : 2;
+}
+
+// Calls f(T{}) with the element type of `type`, one of FP32, FP16, BF16 (checked before).
+template <class F>
+cr_status with_type(int type, F&& f) {
+  if (type == CR_TYPE_F32) return f(float{});
+  if (type == CR_TYPE_F16) return f(__half{});
+  return f(__nv_bfloat16{});
+}
+
+// ---------------------------------------------------------------- activations
+// e = exp(-|x|) never overflows; sigmoid of both signs without cancellation.
+__device__ __forceinline__ void sigmoid_pair(float x, float& p, float& q) {   // p = sigmoid(x), q = sigmoid(-x)
+  const float e = expf(-fabsf(x));
+  const float big = __fdividef(1.0f, 1.0f + e), small = e * big;
+  p = x >= 0.0f ? big : small;
+  q = x >= 0.0f ? small : big;
+  if (x != x) p = q = x;
+}
+
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+  if (ACT == CR_ACT_RELU) return z < 0.0f ? 0.0f : z;   // NaN stays
+  if (ACT == CR_ACT_SILU) {
+    // z e^z -> -0 as z -> -inf, where z sigmoid(z) would be inf * 0
+    float p, q;
+    sigmoid_pair(z, p, q);
+    return z == -INFINITY ? -0.0f : z * p;
+  }
+  if (ACT == CR_ACT_GELU) return z == -INFINITY ? -0.0f : 0.5f * z * erfcf(-z * 0.70710678118654752f);
+  return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float activation_slope(float z) {
+  if (ACT == CR_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+  if (ACT == CR_ACT_SILU) {
+    float p, q;
+    sigmoid_pair(z, p, q);
+    return fabsf(z) == INFINITY ? p : p * fmaf(z, q, 1.0f);
+  }
+  if (ACT == CR_ACT_GELU) {
+    const float cdf = 0.5f * erfcf(-z * 0.70710678118654752f);
+    return fabsf(z) == INFINITY ? cdf : fmaf(z * 0.39894228040143268f, expf(-0.5f * z * z), cdf);
+  }
+  return 1.0f;
+}
+
+template <class F>
+cr_status with_act(int act, F&& f) {
+  switch (act) {
+    case CR_ACT_RELU: return f(std::integral_constant<int, CR_ACT_RELU>{});
+    case CR_ACT_SILU: return f(std::integral_constant<int, CR_ACT_SILU>{});
+    case CR_ACT_GELU: return f(std::integral_constant<int, CR_ACT_GELU>{});
+    default: return f(std::integral_constant<int, CR_ACT_NONE>{});
+  }
+}
+
+// ---------------------------------------------------------------- gates
+struct Gate {
+  float a, c;   // h_t = a h_{t-1} + c x_t
+};
+// Products that feed a sum are written as fmaf or __fmul_rn, so that every variant of a kernel
+// rounds alike.
+template <int GATE>
+__device__ __forceinline__ Gate gate_of(float g) {
+  if (GATE == CR_GATE_COEFF) return {g, 1.0f};
+  float p, q;
+  sigmoid_pair(g, p, q);
+  return {p, GATE == CR_GATE_CONVEX ? q : sqrtf(q * (1.0f + p))};   // 1 - p^2 = q (1 + p), no cancellation
+}
+// da/dg and dc/dg.  Variance gate: dc/dg = -a (a q) / c = -a^2 sqrt(q / (1 + a)), finite at a = 1.
+template <int GATE>
+__device__ __forceinline__ Gate gate_slope(float g) {
+  if (GATE == CR_GATE_COEFF) return {1.0f, 0.0f};
+  float p, q;
+  sigmoid_pair(g, p, q);
+  if (GATE == CR_GATE_CONVEX) return {p * q, -p * q};
+  return {p * q, -p * p * sqrtf(__fdividef(q, 1.0f + p))};
+}
+
+}  // namespace cr
