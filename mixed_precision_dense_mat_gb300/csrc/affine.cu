@@ -1,70 +1,532 @@
 // Affine product with bias, activation and residual in its epilogue, and its gradient
 // (cr_affine, cr_affine_backward).
+#include <algorithm>
 #include <type_traits>
 
 #include "ops.cuh"
+#include "ptx.cuh"
 
 namespace cr {
 namespace {
 
 constexpr int NT = 256;
 
-// C(i, j) = epilogue(sum_k A(i, k) B(j, k)), C column-major: i runs along C's columns.  Element
-// (i, k) of A is at i * ai + k * ak, element (j, k) of B at j * bj + k * bk.
-template <class E, class O>
-struct Prod {
-  const E *A, *B;
-  long long ai, ak, bj, bk;
-  int I, J, K;
+// A product C(i, j) = epilogue(sum_k P(i, k) Q(j, k)), C column-major: i runs along C's columns.
+// P and Q are matrices in memory of which k or the row is the contiguous index.
+struct Operand {
+  const void* ptr;
+  int rows, ld;
+  bool k_major;   // k contiguous, rows ld apart; otherwise rows contiguous, k ld apart
+};
+struct Epilogue {
   const float *iscale, *jscale, *bias;
-  const O* R;
+  int act;
+  const void* R;
   int ldr;
-  O* Z;
+  void* Z;
   int ldz;
-  O* C;
+  void* C;
   int ldc;
 };
+struct Params {
+  int I, J, kblocks;
+  int pk, qk;            // operand P, Q is k-major
+  uint32_t idesc;        // MMA instruction descriptor
+  int ti, tj;            // output tiles
+  int bn;                // thin kernel: columns of its tile
+  int vec;               // C, R and Z allow 16-byte accesses
+  int vecb;              // bias and iscale do
+  Epilogue e;
+  unsigned long long limit;
+  int* err;
+};
 
-// 64 x 64 outputs per block, 4 x 4 per thread, operands through shared memory in FP32.
-template <class E, class O, int ACT>
-__global__ void __launch_bounds__(NT) k_prod(const Prod<E, O> p) {
-  __shared__ float sa[16][65], sb[16][65];
-  const int i0 = blockIdx.x * 64, j0 = blockIdx.y * 64;
-  const int ti = threadIdx.x % 16, tj = threadIdx.x / 16;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < p.K; k0 += 16) {
-    for (int e = threadIdx.x; e < 64 * 16; e += NT) {
-      const int k = p.ak == 1 ? e % 16 : e / 64, i = p.ak == 1 ? e / 16 : e % 64;
-      const bool in = i0 + i < p.I && k0 + k < p.K;
-      sa[k][i] = in ? to_float(p.A[(i0 + i) * p.ai + (k0 + k) * p.ak]) : 0.0f;
+constexpr int KBYTES = 128;                      // one stage holds 128 bytes of k per row
+constexpr int ATOM = 64 * 128;                   // rows-contiguous operand: 64 rows x 64 k
+__host__ __device__ constexpr uint32_t idesc_of(int M, int N, bool bf16, bool a_rows, bool b_rows) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_rows ? 1u : 0u) << 15) |
+         ((b_rows ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// Shared-memory descriptor of an operand tile in the 128-byte swizzle.  k-major: rows of 128 bytes
+// in 8-row groups 1024 apart.  Rows contiguous: 64-row blocks 8192 bytes apart, each 64 k of 128
+// bytes in 8-k groups 1024 apart.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t saddr, bool k_major) {
+  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+  return d | (uint64_t)(k_major ? 1 : ATOM >> 4) << 16;
+}
+// From one MMA's k to the next inside a stage, in descriptor units of 16 bytes: 32 bytes along k,
+// or 16 k of 128 bytes.
+__device__ __forceinline__ uint32_t desc_step(bool k_major) { return k_major ? 2 : 128; }
+
+__device__ __forceinline__ void gave_up(const Params& p, volatile int* abort) {
+  *abort = 1;
+  *(volatile int*)p.err = 1;
+  __threadfence_system();
+}
+
+template <class O>
+__device__ __forceinline__ void load8(const O* p, float* v) {   // 8 elements, 16-byte aligned for 2-byte types
+  if (sizeof(O) == 2) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      O h[2];
+      memcpy(h, &u[q], 4);
+      v[2 * q] = to_float(h[0]);
+      v[2 * q + 1] = to_float(h[1]);
     }
-    for (int e = threadIdx.x; e < 64 * 16; e += NT) {
-      const int k = p.bk == 1 ? e % 16 : e / 64, j = p.bk == 1 ? e / 16 : e % 64;
-      const bool in = j0 + j < p.J && k0 + k < p.K;
-      sb[k][j] = in ? to_float(p.B[(j0 + j) * p.bj + (k0 + k) * p.bk]) : 0.0f;
+  } else {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const float4 w = reinterpret_cast<const float4*>(p)[q];
+      v[4 * q] = w.x;
+      v[4 * q + 1] = w.y;
+      v[4 * q + 2] = w.z;
+      v[4 * q + 3] = w.w;
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) acc[a][b] = fmaf(sa[k][ti + 16 * a], sb[k][tj + 16 * b], acc[a][b]);
-    __syncthreads();
   }
-  for (int a = 0; a < 4; ++a)
-    for (int b = 0; b < 4; ++b) {
-      const int i = i0 + ti + 16 * a, j = j0 + tj + 16 * b;
-      if (i >= p.I || j >= p.J) continue;
-      float z = acc[a][b];
-      if (p.iscale) z *= p.iscale[i];
-      if (p.jscale) z *= p.jscale[j];
-      if (p.bias) z += p.bias[i];
-      if (p.Z) p.Z[(size_t)j * p.ldz + i] = from_float<O>(z);
-      float y = activate<ACT>(z);
-      if (p.R) y += to_float(p.R[(size_t)j * p.ldr + i]);
-      p.C[(size_t)j * p.ldc + i] = from_float<O>(y);
+}
+template <class O>
+__device__ __forceinline__ void store8(O* p, const float* v) {
+  if (sizeof(O) == 2) {
+    uint32_t u[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const O h[2] = {from_float<O>(v[2 * q]), from_float<O>(v[2 * q + 1])};
+      memcpy(&u[q], h, 4);
     }
+    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      reinterpret_cast<float4*>(p)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  }
+}
+
+// z (a finished sum) to the output (i, j).
+template <class O>
+__device__ __forceinline__ void finish(const Params& p, int i, int j, float z) {
+  if (p.e.iscale) z *= p.e.iscale[i];
+  if (p.e.jscale) z *= p.e.jscale[j];
+  if (p.e.bias) z += p.e.bias[i];
+  if (p.e.Z) ((O*)p.e.Z)[(size_t)j * p.e.ldz + i] = from_float<O>(z);
+  float v[1] = {z};
+  activate_all(v, p.e.act);
+  if (p.e.R) v[0] += to_float(((const O*)p.e.R)[(size_t)j * p.e.ldr + i]);
+  ((O*)p.e.C)[(size_t)j * p.e.ldc + i] = from_float<O>(v[0]);
+}
+
+// One i and 16 columns from j0.
+template <class O>
+__device__ __forceinline__ void thin_store16(const Params& p, int i, int j0, float (&v)[16]) {
+  const int n = min(16, p.J - j0);
+  const float is = p.e.iscale ? p.e.iscale[i] : 1.0f, b = p.e.bias ? p.e.bias[i] : 0.0f;
+#pragma unroll
+  for (int q = 0; q < 16; ++q)
+    if (q < n) {
+      v[q] = fmaf(v[q] * is, p.e.jscale ? p.e.jscale[j0 + q] : 1.0f, b);
+      if (p.e.Z) ((O*)p.e.Z)[(size_t)(j0 + q) * p.e.ldz + i] = from_float<O>(v[q]);
+    }
+  activate_all(v, p.e.act);
+#pragma unroll
+  for (int q = 0; q < 16; ++q)
+    if (q < n) {
+      if (p.e.R) v[q] += to_float(((const O*)p.e.R)[(size_t)(j0 + q) * p.e.ldr + i]);
+      ((O*)p.e.C)[(size_t)(j0 + q) * p.e.ldc + i] = from_float<O>(v[q]);
+    }
+}
+
+// One j and 32 consecutive i.
+template <class O>
+__device__ __forceinline__ void wide_store(const Params& p, int i0, int j, float js, float (&v)[32]) {
+  const Epilogue& e = p.e;
+  if (p.vec && p.vecb && i0 + 32 <= p.I) {
+    if (e.iscale) {
+#pragma unroll
+      for (int q = 0; q < 32; q += 4) {
+        const float4 s = *reinterpret_cast<const float4*>(e.iscale + i0 + q);
+        v[q] *= s.x;
+        v[q + 1] *= s.y;
+        v[q + 2] *= s.z;
+        v[q + 3] *= s.w;
+      }
+    }
+    if (e.jscale) {
+#pragma unroll
+      for (int q = 0; q < 32; ++q) v[q] *= js;
+    }
+    if (e.bias) {
+#pragma unroll
+      for (int q = 0; q < 32; q += 4) {
+        const float4 s = *reinterpret_cast<const float4*>(e.bias + i0 + q);
+        v[q] += s.x;
+        v[q + 1] += s.y;
+        v[q + 2] += s.z;
+        v[q + 3] += s.w;
+      }
+    }
+    if (e.Z) {
+      O* z = (O*)e.Z + (size_t)j * e.ldz + i0;
+#pragma unroll
+      for (int q = 0; q < 32; q += 8) store8(z + q, v + q);
+    }
+    activate_all(v, e.act);
+    if (e.R) {
+      const O* r = (const O*)e.R + (size_t)j * e.ldr + i0;
+#pragma unroll
+      for (int q = 0; q < 32; q += 8) {
+        float w[8];
+        load8(r + q, w);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[q + x] += w[x];
+      }
+    }
+    O* c = (O*)e.C + (size_t)j * e.ldc + i0;
+#pragma unroll
+    for (int q = 0; q < 32; q += 8) store8(c + q, v + q);
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < 32; ++q)
+    if (i0 + q < p.I) finish<O>(p, i0 + q, j, v[q]);
+}
+
+// ---------------------------------------------------------------- wide kernel
+// 256 x 256 outputs per CTA pair (cta_group::2): the pair's MMA has M = 256 rows j (128 per CTA, its
+// operand A = Q) and N = 256 columns i (operand B = P, half of it in each CTA).  Persistent;
+// warp 0 loads by TMA into a ring of stages, warp 1 of the first CTA issues the MMAs, warps 2-9
+// take the accumulator (two of them in TMEM, so the epilogue of one tile overlaps the next
+// tile's products) through the epilogue: a thread holds one j and 32 consecutive i.
+constexpr int WSTAGES = 6;
+constexpr int WTILE = 128 * KBYTES;              // one operand's half tile of a stage, 16 KB
+constexpr int WSTAGE = 2 * WTILE;
+constexpr int WTHREADS = 320;
+constexpr int WEPI = 8;                          // epilogue warps
+struct WideBars {
+  uint64_t full[WSTAGES], empty[WSTAGES], tfull[2], tempty[2];
+  uint32_t tmem;
+  int abort;
+};
+constexpr int WSMEM = WSTAGES * WSTAGE + 1024 + 256;
+static_assert(sizeof(WideBars) <= 256, "barrier area");
+
+// Tile t: column tiles j in groups of 8 and all row tiles i inside a group, so that the tiles in
+// flight share operands in L2.
+__device__ __forceinline__ void wide_tile(const Params& p, int t, int& i, int& j) {
+  const int per = 8 * p.ti, g = t / per, gj = min(8, p.tj - g * 8), r = t - g * per;
+  i = r / gj;
+  j = g * 8 + r % gj;
+}
+
+template <bool F8, class O>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
+    k_affine_wide(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  WideBars* bars = reinterpret_cast<WideBars*>(smem + WSTAGES * WSTAGE);
+  volatile int* abort_flag = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int ntiles = p.ti * p.tj, ncl = gridDim.x >> 1, cl = blockIdx.x >> 1;
+  constexpr int KE = F8 ? 128 : 64;   // k elements per stage
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < WSTAGES; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars->tfull[b], 1);
+      mbar_init(&bars->tempty[b], 2 * WEPI);   // one arrival per epilogue warp of the pair
+    }
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_pair(&bars->tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      prefetch_tmap(&tmP);
+      prefetch_tmap(&tmQ);
+      uint32_t st = 0, ph = 0;
+      int issued = 0;
+      for (int t = cl; t < ntiles && !*abort_flag; t += ncl) {
+        int ti, tj;
+        wide_tile(p, t, ti, tj);
+        const int i0 = ti * 256 + (int)rank * 128, j0 = tj * 256 + (int)rank * 128;
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          if (*abort_flag) break;
+          if (!mbar_wait(&bars->empty[st], ph ^ 1u, p.limit)) {
+            gave_up(p, abort_flag);
+            break;
+          }
+          uint8_t* sa = smem + st * WSTAGE;
+          uint8_t* sb = sa + WTILE;
+          if (rank == 0) mbar_arrive_expect_tx(&bars->full[st], 2 * WSTAGE);
+          const uint32_t bar = cluster_addr(smem_u32(&bars->full[st]), 0);
+          const int k0 = kb * KE;
+          if (p.qk) {
+            tma_load_2d_pair(sa, &tmQ, bar, k0, j0);
+          } else {
+            tma_load_2d_pair(sa, &tmQ, bar, j0, k0);
+            tma_load_2d_pair(sa + ATOM, &tmQ, bar, j0 + 64, k0);
+          }
+          if (p.pk) {
+            tma_load_2d_pair(sb, &tmP, bar, k0, i0);
+          } else {
+            tma_load_2d_pair(sb, &tmP, bar, i0, k0);
+            tma_load_2d_pair(sb + ATOM, &tmP, bar, i0 + 64, k0);
+          }
+          ++issued;
+          if (++st == WSTAGES) st = 0, ph ^= 1u;
+        }
+      }
+      if (*abort_flag && rank == 0) {   // the pair's copies in flight land before either CTA leaves
+        for (int q = min(issued, WSTAGES); q > 0; --q) {
+          const int n = issued - q;
+          mbar_wait(&bars->full[n % WSTAGES], (uint32_t)(n / WSTAGES) & 1u, p.limit);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      uint32_t st = 0, ph = 0;
+      int u = 0;
+      const uint32_t ps = desc_step(p.pk), qs = desc_step(p.qk);
+      for (int t = cl; t < ntiles && !*abort_flag; t += ncl, ++u) {
+        const int b = u & 1;
+        if (!mbar_wait_cluster(&bars->tempty[b], ((uint32_t)(u >> 1) & 1u) ^ 1u, p.limit)) {
+          gave_up(p, abort_flag);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t acc = tmem + (uint32_t)(b * 256);
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          if (*abort_flag) break;
+          if (!mbar_wait_cluster(&bars->full[st], ph, p.limit)) {
+            gave_up(p, abort_flag);
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + st * WSTAGE);
+          const uint64_t da = tile_desc(sa, p.qk), db = tile_desc(sa + WTILE, p.pk);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_any<true, F8>(acc, da + kk * qs, db + kk * ps, p.idesc, (kb | kk) != 0);
+          mma_commit_pair(&bars->empty[st]);
+          if (++st == WSTAGES) st = 0, ph ^= 1u;
+        }
+        if (*abort_flag) break;
+        mma_commit_pair(&bars->tfull[b]);
+      }
+    }
+  } else {
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t tempty[2] = {cluster_addr(smem_u32(&bars->tempty[0]), 0), cluster_addr(smem_u32(&bars->tempty[1]), 0)};
+    int u = 0;
+    for (int t = cl; t < ntiles; t += ncl, ++u) {
+      const int b = u & 1;
+      if (*abort_flag) break;
+      if (!mbar_wait(&bars->tfull[b], (uint32_t)(u >> 1) & 1u, p.limit)) {
+        gave_up(p, abort_flag);
+        break;
+      }
+      tc_fence_after();
+      int ti, tj;
+      wide_tile(p, t, ti, tj);
+      const int j = tj * 256 + (int)rank * 128 + quad * 32 + lane;
+      const int ibase = ti * 256 + half * 128;
+      const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * 256 + half * 128);
+      const float js = p.e.jscale && j < p.J ? p.e.jscale[j] : 1.0f;
+      for (int c = 0; c < 128; c += 32) {
+        const int i0 = ibase + c;
+        float v[32];
+        __syncwarp();   // lanes without an output skipped the store
+        tmem_ld32(tq + (uint32_t)c, v);
+        if (i0 >= p.I || j >= p.J) continue;
+        wide_store<O>(p, i0, j, js, v);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tempty[b]);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // neither CTA leaves while the other's MMAs, copies or arrivals may reach it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- thin kernel
+// 128 outputs i x bn columns j per cluster (operand A = P, B = Q): few columns, where the product is
+// bound by reading P.  The CTAs of a cluster take equal parts of k; their partial sums meet in
+// shared memory and are added in the order of the parts, each CTA finishing a part of the
+// outputs.
+constexpr int TTHREADS = 192;
+constexpr int TMAXSTAGES = 8;
+struct ThinBars {
+  uint64_t full[TMAXSTAGES], empty[TMAXSTAGES], done;
+  uint32_t tmem;
+  int abort;
+};
+
+template <bool F8, class O>
+__global__ void __launch_bounds__(TTHREADS)
+    k_affine_thin(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const Params p, int split, int stages) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int qbytes = p.qk ? p.bn * KBYTES : (p.bn + 63) / 64 * ATOM;
+  const int stage_bytes = WTILE + qbytes;
+  ThinBars* bars = reinterpret_cast<ThinBars*>(smem + stages * stage_bytes);
+  volatile int* abort_flag = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % split, tile = blockIdx.x / split;
+  const int i0 = tile / p.tj * 128, j0 = tile % p.tj * p.bn;
+  const int kb0 = (int)((long long)p.kblocks * rank / split), kb1 = (int)((long long)p.kblocks * (rank + 1) / split);
+  const uint32_t cols = p.bn <= 32 ? 32 : p.bn <= 64 ? 64 : p.bn <= 128 ? 128 : 256;
+  constexpr int KE = F8 ? 128 : 64;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
+    }
+    mbar_init(&bars->done, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(&bars->tmem, cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+  float* part = reinterpret_cast<float*>(smem);   // the stages again, after the last MMA: [column][128]
+
+  if (warp == 0) {
+    if (lane == 0) {
+      prefetch_tmap(&tmP);
+      prefetch_tmap(&tmQ);
+      int st = 0, issued = 0;
+      uint32_t ph = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (*abort_flag) break;
+        if (!mbar_wait(&bars->empty[st], ph ^ 1u, p.limit)) {
+          gave_up(p, abort_flag);
+          break;
+        }
+        uint8_t* sp = smem + st * stage_bytes;
+        uint8_t* sq = sp + WTILE;
+        mbar_arrive_expect_tx(&bars->full[st], stage_bytes);
+        const int k0 = kb * KE;
+        if (p.pk) {
+          tma_load_2d(sp, &tmP, &bars->full[st], k0, i0);
+        } else {
+          tma_load_2d(sp, &tmP, &bars->full[st], i0, k0);
+          tma_load_2d(sp + ATOM, &tmP, &bars->full[st], i0 + 64, k0);
+        }
+        if (p.qk) {
+          tma_load_2d(sq, &tmQ, &bars->full[st], k0, j0);
+        } else {
+          for (int h = 0; h < qbytes / ATOM; ++h) tma_load_2d(sq + h * ATOM, &tmQ, &bars->full[st], j0 + h * 64, k0);
+        }
+        ++issued;
+        if (++st == stages) st = 0, ph ^= 1u;
+      }
+      if (*abort_flag)
+        for (int q = min(issued, stages); q > 0; --q) {   // copies in flight land before the CTA leaves
+          const int n = issued - q;
+          mbar_wait(&bars->full[n % stages], (uint32_t)(n / stages) & 1u, p.limit);
+        }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && kb1 > kb0) {
+      int st = 0;
+      uint32_t ph = 0;
+      const uint32_t ps = desc_step(p.pk), qs = desc_step(p.qk);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (*abort_flag) break;
+        if (!mbar_wait(&bars->full[st], ph, p.limit)) {
+          gave_up(p, abort_flag);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sp = smem_u32(smem + st * stage_bytes);
+        const uint64_t da = tile_desc(sp, p.pk), db = tile_desc(sp + WTILE, p.qk);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) mma_any<false, F8>(tmem, da + kk * ps, db + kk * qs, p.idesc, kb != kb0 || kk != 0);
+        mma_commit(&bars->empty[st]);
+        if (++st == stages) st = 0, ph ^= 1u;
+      }
+      mma_commit(&bars->done);   // after an abort too: it completes once the issued MMAs have
+    }
+    __syncwarp();
+  } else {
+    const int f = (warp & 3) * 32 + lane, i = i0 + f;
+    bool ok = true;
+    if (kb1 > kb0) {
+      ok = mbar_wait(&bars->done, 0, p.limit);
+      if (!ok) gave_up(p, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const int ncols = min(p.bn, p.J - j0);
+    for (int c = 0; c < ncols; c += 16) {
+      float v[16];
+      __syncwarp();
+      if (kb1 > kb0 && ok) {
+        tmem_ld16(tq + (uint32_t)c, v);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) v[q] = 0.0f;
+      }
+      if (split > 1) {
+        if (ok) {
+#pragma unroll
+          for (int q = 0; q < 16; ++q) part[(c + q) * 128 + f] = v[q];
+        }
+      } else if (i < p.I) {
+        thin_store16<O>(p, i, j0 + c, v);
+      }
+    }
+  }
+  if (split > 1) {
+    __syncthreads();
+    cluster_sync_all();
+    const int ncols = min(p.bn, p.J - j0), total = ncols * 128;
+    const int e0 = (int)((long long)total * rank / split), e1 = (int)((long long)total * (rank + 1) / split);
+    const uint32_t base = smem_u32(part);
+    for (int e = e0 + (int)threadIdx.x; e < e1; e += TTHREADS) {
+      float z = 0.0f;
+      for (int r = 0; r < split; ++r) z += ld_cluster(cluster_addr(base + 4u * (uint32_t)e, (uint32_t)r));
+      const int i = i0 + (e & 127);
+      if (i < p.I) finish<O>(p, i, j0 + (e >> 7), z);
+    }
+    cluster_sync_all();   // partial sums stay until every CTA has read them
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, cols);
+  }
+}
+
+// Copies a matrix whose columns of n elements start at any address into columns ld apart.
+template <class E>
+__global__ void __launch_bounds__(NT) k_pack(const E* src, int lds, int n, int m, E* dst, int ld) {
+  for (int c = blockIdx.y; c < m; c += gridDim.y)
+    for (int i = blockIdx.x * NT + threadIdx.x; i < n; i += gridDim.x * NT) dst[(size_t)c * ld + i] = src[(size_t)c * lds + i];
 }
 
 // G = dY .* act'(Z), and the row sums of its unrounded values; one block per 32 features.
@@ -88,12 +550,114 @@ __global__ void __launch_bounds__(NT) k_affine_g(const E* dY, int lddy, const E*
   }
 }
 
-template <class E, class O>
-cr_status product(const Prod<E, O>& p, int act, cudaStream_t stream) {
-  return with_act(act, [&](auto a0) -> cr_status {
-    k_prod<E, O, decltype(a0)::value><<<dim3((p.I + 63) / 64, (p.J + 63) / 64), NT, 0, stream>>>(p);
-    CR_CHECK_LAUNCH("k_prod");
+// An operand as TMA can read it: a 16-byte aligned base and leading dimension, copied into
+// scratch where the caller's is not.
+struct Packed {
+  void* own = nullptr;
+  cudaStream_t stream = nullptr;
+  ~Packed() { scratch_free(own, stream); }
+  cr_status make(Operand& o, int type, int K, cudaStream_t s) {
+    const int eb = type_bytes(type);
+    if (((uintptr_t)o.ptr & 15) == 0 && (long long)o.ld * eb % 16 == 0) return CR_OK;
+    stream = s;
+    const int n = o.k_major ? K : o.rows, m = o.k_major ? o.rows : K;
+    const int ld = (int)(((long long)n * eb + 15) / 16 * 16 / eb);
+    CR_CUDA(scratch_alloc(&own, (size_t)ld * m * eb, s));
+    const dim3 grid((n + NT - 1) / NT, m < 32768 ? m : 32768);
+    if (eb == 2) k_pack<uint16_t><<<grid, NT, 0, s>>>((const uint16_t*)o.ptr, o.ld, n, m, (uint16_t*)own, ld);
+    else k_pack<uint8_t><<<grid, NT, 0, s>>>((const uint8_t*)o.ptr, o.ld, n, m, (uint8_t*)own, ld);
+    CR_CHECK_LAUNCH("k_pack");
+    o.ptr = own;
+    o.ld = ld;
     return CR_OK;
+  }
+};
+
+cr_status map_of(CUtensorMap* tm, const Operand& o, int type, int K, int rows_per_box) {
+  if (o.k_major) return make_tensor_map_2d(tm, type, o.ptr, K, o.rows, o.ld, KBYTES / type_bytes(type), rows_per_box);
+  return make_tensor_map_2d(tm, type, o.ptr, o.rows, K, o.ld, 64, 64);
+}
+
+int sm_count() {
+  static const int n = [] {
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+  }();
+  return n;
+}
+
+template <bool F8, class O>
+cr_status launch(const CUtensorMap& tmP, const CUtensorMap& tmQ, const Params& p, bool wide, int split, int stages, cudaStream_t stream) {
+  if (wide) {
+    static const cudaError_t set = cudaFuncSetAttribute(k_affine_wide<F8, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, WSMEM);
+    CR_CUDA(set);
+    const int pairs = std::min((long long)sm_count() / 2, (long long)p.ti * p.tj);
+    TimedScope ts("k_affine_wide", stream);
+    k_affine_wide<F8, O><<<2 * pairs, WTHREADS, WSMEM, stream>>>(tmP, tmQ, p);
+    CR_CHECK_LAUNCH("k_affine_wide");
+    return CR_OK;
+  }
+  static const cudaError_t set = cudaFuncSetAttribute(k_affine_thin<F8, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  CR_CUDA(set);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)((long long)p.ti * p.tj * split));
+  cfg.blockDim = dim3(TTHREADS);
+  const int stage = WTILE + (p.qk ? p.bn * KBYTES : (p.bn + 63) / 64 * ATOM);
+  cfg.dynamicSmemBytes = (size_t)stages * stage + 1024 + 256;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  TimedScope ts("k_affine_thin", stream);
+  CR_CUDA(cudaLaunchKernelEx(&cfg, k_affine_thin<F8, O>, tmP, tmQ, p, split, stages));
+  CR_CHECK_LAUNCH("k_affine_thin");
+  return CR_OK;
+}
+
+cr_status product(Operand P, Operand Q, int type, int K, int out_type, const Epilogue& e, cudaStream_t stream) {
+  Params p = {};
+  CR_TRY(wait_word(&p.err));
+  p.limit = option_wait_ns();
+  p.I = P.rows;
+  p.J = Q.rows;
+  p.e = e;
+  p.pk = P.k_major;
+  p.qk = Q.k_major;
+  const int ke = KBYTES / type_bytes(type), ob = type_bytes(out_type);
+  p.kblocks = (K + ke - 1) / ke;
+  const auto ok16 = [&](const void* q, int ld) { return !q || (((uintptr_t)q & 15) == 0 && (long long)ld * ob % 16 == 0); };
+  p.vec = ok16(e.C, e.ldc) && ok16(e.R, e.ldr) && ok16(e.Z, e.ldz);
+  p.vecb = (((uintptr_t)e.bias | (uintptr_t)e.iscale) & 15) == 0;
+  Packed ownP, ownQ;
+  CR_TRY(ownP.make(P, type, K, stream));
+  CR_TRY(ownQ.make(Q, type, K, stream));
+  const long long wt = ((long long)p.I + 255) / 256 * (((long long)p.J + 255) / 256);
+  const bool wide = p.J > 128 && wt >= 24;
+  int split = 1, stages = 0;
+  if (wide) {
+    p.ti = (p.I + 255) / 256;
+    p.tj = (p.J + 255) / 256;
+    p.idesc = idesc_of(256, 256, type == CR_TYPE_BF16, !p.qk, !p.pk);
+  } else {
+    p.bn = p.J <= 16 ? 16 : p.J <= 32 ? 32 : p.J <= 64 ? 64 : 128;
+    p.ti = (p.I + 127) / 128;
+    p.tj = (p.J + p.bn - 1) / p.bn;
+    p.idesc = idesc_of(128, p.bn, type == CR_TYPE_BF16, !p.pk, !p.qk);
+    while (split < 8 && (long long)p.ti * p.tj * split < 2 * sm_count() && p.kblocks >= 4 * split) split *= 2;
+    stages = std::min(p.bn <= 32 ? 5 : p.bn == 64 ? 4 : 3, 8);
+  }
+  CUtensorMap tmP, tmQ;
+  CR_TRY(map_of(&tmP, P, type, K, 128));
+  CR_TRY(map_of(&tmQ, Q, type, K, wide ? 128 : p.bn));
+  return with_type(out_type, [&](auto o0) -> cr_status {
+    using O = decltype(o0);
+    return type == CR_TYPE_E4M3 ? launch<true, O>(tmP, tmQ, p, wide, split, stages, stream)
+                                : launch<false, O>(tmP, tmQ, p, wide, split, stages, stream);
   });
 }
 
@@ -115,18 +679,8 @@ extern "C" cr_status cr_affine(int type, const void* d_W, int ldw, const void* d
   CR_REQUIRE(ldw >= K && ldx >= K && ldy >= N && (!d_R || ldr >= N) && (!d_Z || ldz >= N), "cr_affine: leading dimension too small");
   if (M == 0) return CR_OK;
   CR_REQUIRE(d_W && d_X && d_Y, "cr_affine: NULL argument");
-  const auto go = [&](auto e0, auto o0) -> cr_status {
-    using E = decltype(e0);
-    using O = decltype(o0);
-    const Prod<E, O> p{(const E*)d_W, (const E*)d_X, ldw, 1, ldx, 1, N, M, K, d_wscale, d_xscale, d_bias,
-                       (const O*)d_R, ldr, (O*)d_Z, ldz, (O*)d_Y, ldy};
-    return product(p, act, stream);
-  };
-  return with_type(out_type, [&](auto o0) -> cr_status {
-    if (type == CR_TYPE_F16) return go(__half{}, o0);
-    if (type == CR_TYPE_BF16) return go(__nv_bfloat16{}, o0);
-    return go(__nv_fp8_e4m3{}, o0);
-  });
+  const Epilogue e{d_wscale, d_xscale, d_bias, act, d_R, ldr, d_Z, ldz, d_Y, ldy};
+  return product(Operand{d_W, N, ldw, true}, Operand{d_X, M, ldx, true}, type, K, out_type, e, stream);
   CR_ENTRY_END("cr_affine")
 }
 
@@ -147,30 +701,26 @@ extern "C" cr_status cr_affine_backward(int type, const void* d_W, int ldw, cons
     return CR_OK;
   }
   void* own = nullptr;
-  if (act != CR_ACT_NONE && (d_dX || d_dW)) CR_CUDA(scratch_alloc(&own, (size_t)N * M * 2, stream));
+  const int ldown = (N + 7) & ~7;   // columns on 16-byte boundaries
+  if (act != CR_ACT_NONE && (d_dX || d_dW)) CR_CUDA(scratch_alloc(&own, (size_t)ldown * M * 2, stream));
   const auto go = [&](auto e0) -> cr_status {
     using E = decltype(e0);
     const E* G = own ? (const E*)own : (const E*)d_dY;
-    const int ldg = own ? N : lddy;
+    const int ldg = own ? ldown : lddy;
     if (own || d_db)
       CR_TRY(with_act(act, [&](auto a0) -> cr_status {
         k_affine_g<E, decltype(a0)::value><<<(N + 31) / 32, NT, 0, stream>>>((const E*)d_dY, lddy, (const E*)d_Z, ldz, N, M,
-                                                                            (E*)own, N, d_db);
+                                                                            (E*)own, ldown, d_db);
         CR_CHECK_LAUNCH("k_affine_g");
         return CR_OK;
       }));
     if (d_dX) {   // dX(i, j) = sum_n W(i, n) G(n, j)
-      const Prod<E, E> p{(const E*)d_W, G, 1, ldw, ldg, 1, K, M, N, nullptr, nullptr, nullptr, nullptr, 0, nullptr, 0, (E*)d_dX, lddx};
-      CR_TRY(product(p, CR_ACT_NONE, stream));
+      const Epilogue e{nullptr, nullptr, nullptr, CR_ACT_NONE, nullptr, 0, nullptr, 0, d_dX, lddx};
+      CR_TRY(product(Operand{d_W, K, ldw, false}, Operand{G, M, ldg, true}, type, N, type, e, stream));
     }
     if (d_dW) {   // dW(i, n) = sum_j X(i, j) G(n, j)
-      if (dw_type == CR_TYPE_F32) {
-        const Prod<E, float> p{(const E*)d_X, G, 1, ldx, 1, ldg, K, N, M, nullptr, nullptr, nullptr, nullptr, 0, nullptr, 0, (float*)d_dW, lddw};
-        CR_TRY(product(p, CR_ACT_NONE, stream));
-      } else {
-        const Prod<E, E> p{(const E*)d_X, G, 1, ldx, 1, ldg, K, N, M, nullptr, nullptr, nullptr, nullptr, 0, nullptr, 0, (E*)d_dW, lddw};
-        CR_TRY(product(p, CR_ACT_NONE, stream));
-      }
+      const Epilogue e{nullptr, nullptr, nullptr, CR_ACT_NONE, nullptr, 0, nullptr, 0, d_dW, lddw};
+      CR_TRY(product(Operand{d_X, K, ldx, false}, Operand{G, N, ldg, false}, type, M, dw_type, e, stream));
     }
     return CR_OK;
   };

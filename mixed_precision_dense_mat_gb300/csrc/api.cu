@@ -165,6 +165,47 @@ cr_status free_class_storage(cr_tilemat V) {
   return CR_OK;
 }
 
+// Any 2-byte or 1-byte element type; box_inner elements are 128 bytes.
+cr_status make_tensor_map_2d(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
+                             int box_outer) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail_literal(CR_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  const CUtensorMapDataType dt = type == CR_TYPE_E4M3  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                 : type == CR_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * (type == CR_TYPE_E4M3 ? 1 : 2)};
+  cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer};
+  cuuint32_t es[2] = {1, 1};
+  const CUresult r = fn(tm, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(CR_ERR_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
+  return CR_OK;
+}
+
+// The word that a bounded wait of an operator kernel sets (mapped host memory, one per process).
+cr_status wait_word(int** d_word) {
+  static std::once_flag once;
+  static volatile int* host = nullptr;
+  static int* dev = nullptr;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    if (cudaHostAlloc(&p, sizeof(int), cudaHostAllocMapped | cudaHostAllocPortable) != cudaSuccess) return;
+    *(int*)p = 0;
+    void* d = nullptr;
+    if (cudaHostGetDevicePointer(&d, p, 0) != cudaSuccess) return;
+    host = (volatile int*)p;
+    dev = (int*)d;
+  });
+  if (!dev) return fail_literal(CR_ERR_NOMEM, "no mapped host memory for the wait word");
+  *d_word = dev;
+  if (*host) {
+    *host = 0;
+    return fail_literal(CR_ERR_TIMEOUT, "a device-side wait of an earlier operator call ran out; its outputs are invalid");
+  }
+  return CR_OK;
+}
+
 }  // namespace cr
 
 using namespace cr;

@@ -16,6 +16,10 @@ cr_status fail_literal(cr_status code, const char* msg);
 // the next operator call reports and clears it.  Reading it costs no synchronisation.
 cr_status wait_word(int** d_word);
 
+// Tensor map of a 2-D operand (inner contiguous, leading dimension ld) for 128-byte swizzled boxes.
+cr_status make_tensor_map_2d(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
+                             int box_outer);
+
 // C++ exceptions end at the C entries.
 #define CR_ENTRY_BEGIN try {
 #define CR_ENTRY_END(what)                                                                    \
@@ -89,6 +93,21 @@ __device__ __forceinline__ float activation_slope(float z) {
     return fabsf(z) == INFINITY ? cdf : fmaf(z * 0.39894228040143268f, expf(-0.5f * z * z), cdf);
   }
   return 1.0f;
+}
+
+// v[] = act(v[]) with one test of `act` for all of them.
+template <int N>
+__device__ __forceinline__ void activate_all(float (&v)[N], int act) {
+  if (act == CR_ACT_RELU) {
+#pragma unroll
+    for (int q = 0; q < N; ++q) v[q] = activate<CR_ACT_RELU>(v[q]);
+  } else if (act == CR_ACT_SILU) {
+#pragma unroll
+    for (int q = 0; q < N; ++q) v[q] = activate<CR_ACT_SILU>(v[q]);
+  } else if (act == CR_ACT_GELU) {
+#pragma unroll
+    for (int q = 0; q < N; ++q) v[q] = activate<CR_ACT_GELU>(v[q]);
+  }
 }
 
 template <class F>
