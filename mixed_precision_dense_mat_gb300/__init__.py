@@ -36,6 +36,7 @@ call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -514,15 +515,23 @@ def calibrate(S, zhat, v, u: float, level: float, counts: bool = True, extrema: 
 _ACTS = {"none": CR_ACT_NONE, "relu": CR_ACT_RELU, "silu": CR_ACT_SILU, "gelu": CR_ACT_GELU}
 _GATES = {"coeff": CR_GATE_COEFF, "convex": CR_GATE_CONVEX, "variance": CR_GATE_VARIANCE}
 _types = None
+_torch = None
+
+
+def _ready() -> None:
+    """Loads the library, and torch once for this section: a call is a few microseconds, in
+    which import statements would show."""
+    global _torch, _types
+    if _torch is None:
+        load()
+        import torch
+        _types = {torch.float32: CR_TYPE_F32, torch.float16: CR_TYPE_F16, torch.bfloat16: CR_TYPE_BF16,
+                  torch.float8_e4m3fn: CR_TYPE_E4M3}
+        _torch = torch
 
 
 def _type_of(t, what: str) -> int:
     """CR_TYPE_* of a CUDA tensor."""
-    global _types
-    if _types is None:
-        import torch
-        _types = {torch.float32: CR_TYPE_F32, torch.float16: CR_TYPE_F16, torch.bfloat16: CR_TYPE_BF16,
-                  torch.float8_e4m3fn: CR_TYPE_E4M3}
     k = _types.get(t.dtype)
     if k is None or not t.is_cuda:
         raise CrError(1, f"{what}: a CUDA tensor of FP32, FP16, BF16 or e4m3 is needed, not {t.dtype} on {t.device}")
@@ -556,31 +565,28 @@ def _vector(t, n: int, what: str):
     return t, t.data_ptr()
 
 
-def _empty(n: int, m: int, like, dtype=None):
-    return like.new_empty((m, n), dtype=dtype or like.dtype).T
+def _empty(n: int, m: int, dtype, device):
+    return _torch.empty_strided((n, m), (1, n), dtype=dtype, device=device)
 
 
 def _on_stream(fn):
     """Runs the call with `stream` as the current stream, so that its outputs and copies belong
     to it, and keeps the memory of its arguments until the stream has passed the call."""
-    import functools
-
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
         if stream is None:
             return fn(*args, **kw)
-        import torch
-        with torch.cuda.stream(stream):
+        _ready()
+        with _torch.cuda.stream(stream):
             for t in (*args, *kw.values()):
-                if isinstance(t, torch.Tensor) and t.is_cuda:
+                if isinstance(t, _torch.Tensor) and t.is_cuda:
                     t.record_stream(stream)
             return fn(*args, **kw)
     return call
 
 
 def _raw_stream(device) -> int:
-    import torch
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return _torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _code(table, name, what: str) -> int:
@@ -602,7 +608,7 @@ def affine(W, X, bias=None, act: str = "none", residual=None, w_scale=None, x_sc
     """cr_affine: Y = act(W^T X + bias) + residual for W (K, N) and X (K, M); e4m3 operands take
     w_scale (N) and x_scale (M).  out_dtype: FP32, FP16 or BF16 (default: X's, BF16 for e4m3).
     save=True returns (Y, Z) with Z the pre-activation that affine_backward reads."""
-    load()
+    _ready()
     kind = _type_of(X, "affine X")
     K, M = _matrix_shape(X, "affine X")
     N = _matrix_shape(W, "affine W")[1]
@@ -610,17 +616,13 @@ def affine(W, X, bias=None, act: str = "none", residual=None, w_scale=None, x_sc
     W, pw, ldw = _matrix(W, (K, N), X.dtype, "affine W")
     if out is None:
         if out_dtype is None:
-            if kind == CR_TYPE_E4M3:
-                import torch
-                out_dtype = torch.bfloat16
-            else:
-                out_dtype = X.dtype
-        out = _empty(N, M, X, out_dtype)
+            out_dtype = _torch.bfloat16 if kind == CR_TYPE_E4M3 else X.dtype
+        out = _empty(N, M, out_dtype, X.device)
     y, py, ldy = _matrix(out, (N, M), out_dtype or out.dtype, "affine out")
     if y is not out:
         raise CrError(1, "affine out: a column-major matrix is needed")
     R, pr, ldr = _matrix(residual, (N, M), out.dtype, "affine residual")
-    Z = _empty(N, M, X, out.dtype) if save else None
+    Z = _empty(N, M, out.dtype, X.device) if save else None
     bias, pb = _vector(bias, N, "affine bias")
     w_scale, pws = _vector(w_scale, N, "affine w_scale")
     x_scale, pxs = _vector(x_scale, M, "affine x_scale")
@@ -634,7 +636,7 @@ def affine(W, X, bias=None, act: str = "none", residual=None, w_scale=None, x_sc
 def affine_backward(W, X, dY, Z=None, act: str = "none", need=(True, True, True), dw_dtype=None):
     """cr_affine_backward: (dX, dW, dbias) of affine at the saved Z; need says which of the three
     are wanted (None for the others).  dw_dtype: X's type (default) or FP32."""
-    load()
+    _ready()
     kind = _type_of(X, "affine_backward X")
     K, M = _matrix_shape(X, "affine_backward X")
     N = _matrix_shape(W, "affine_backward W")[1]
@@ -642,9 +644,9 @@ def affine_backward(W, X, dY, Z=None, act: str = "none", need=(True, True, True)
     W, pw, ldw = _matrix(W, (K, N), X.dtype, "affine_backward W")
     dY, pdy, lddy = _matrix(dY, (N, M), X.dtype, "affine_backward dY")
     Z, pz, ldz = _matrix(Z, (N, M), X.dtype, "affine_backward Z")
-    dX = _empty(K, M, X) if need[0] else None
-    dW = _empty(K, N, X, dw_dtype) if need[1] else None
-    db = X.new_empty(N, dtype=_f32()) if need[2] else None
+    dX = _empty(K, M, X.dtype, X.device) if need[0] else None
+    dW = _empty(K, N, dw_dtype or X.dtype, X.device) if need[1] else None
+    db = _torch.empty(N, dtype=_torch.float32, device=X.device) if need[2] else None
     _check(_lib.cr_affine_backward(kind, pw, ldw, px, ldx, pdy, lddy, pz, ldz, K, N, M,
                                    _code(_ACTS, act, "affine_backward act"), _ptr(dX), K,
                                    _type_of(dW, "affine_backward dw_dtype") if need[1] else kind, _ptr(dW), K, _ptr(db),
@@ -652,26 +654,19 @@ def affine_backward(W, X, dY, Z=None, act: str = "none", need=(True, True, True)
     return dX, dW, db
 
 
-def _f32():
-    import torch
-    return torch.float32
-
-
 def _rmsnorm(X, gamma, residual, eps, e4m3: bool):
-    load()
+    _ready()
     kind = _type_of(X, "rmsnorm X")
     D, T = _matrix_shape(X, "rmsnorm X")
     X, px, ldx = _matrix(X, (D, T), X.dtype, "rmsnorm X")
     R, pr, ldr = _matrix(residual, (D, T), X.dtype, "rmsnorm residual")
     gamma, pg = _vector(gamma, D, "rmsnorm gamma")
-    H = _empty(D, T, X) if R is not None else None
-    Y, scale, out = X, None, kind
+    H = _empty(D, T, X.dtype, X.device) if R is not None else None
     if e4m3:
-        import torch
-        Y, out = _empty(D, T, X, torch.float8_e4m3fn), CR_TYPE_E4M3
-        scale = X.new_empty(T, dtype=torch.float32)
+        Y, out = _empty(D, T, _torch.float8_e4m3fn, X.device), CR_TYPE_E4M3
+        scale = _torch.empty(T, dtype=_torch.float32, device=X.device)
     else:
-        Y = _empty(D, T, X)
+        Y, scale, out = _empty(D, T, X.dtype, X.device), None, kind
     _check(_lib.cr_rmsnorm(kind, px, ldx, pr, ldr, pg, D, T, eps, _ptr(H), D, out, Y.data_ptr(), D, _ptr(scale),
                            _raw_stream(X.device)))
     return Y, scale, H
@@ -693,15 +688,15 @@ def rmsnorm_e4m3(X, gamma, residual=None, eps: float = 1e-6):
 @_on_stream
 def rmsnorm_backward(H, gamma, dY, dH=None, eps: float = 1e-6):
     """cr_rmsnorm_backward: (dX, dgamma) at the sum H that rmsnorm returned (or its X)."""
-    load()
+    _ready()
     kind = _type_of(H, "rmsnorm_backward H")
     D, T = _matrix_shape(H, "rmsnorm_backward H")
     H, ph, ldh = _matrix(H, (D, T), H.dtype, "rmsnorm_backward H")
     dY, pdy, lddy = _matrix(dY, (D, T), H.dtype, "rmsnorm_backward dY")
     dH, pdh, lddh = _matrix(dH, (D, T), H.dtype, "rmsnorm_backward dH")
     gamma, pg = _vector(gamma, D, "rmsnorm_backward gamma")
-    dX = _empty(D, T, H)
-    dgamma = H.new_empty(D, dtype=_f32())
+    dX = _empty(D, T, H.dtype, H.device)
+    dgamma = _torch.empty(D, dtype=_torch.float32, device=H.device)
     _check(_lib.cr_rmsnorm_backward(kind, ph, ldh, pg, pdy, lddy, pdh, lddh, D, T, eps, dX.data_ptr(), D,
                                     dgamma.data_ptr(), _raw_stream(H.device)))
     return dX, dgamma
@@ -711,8 +706,7 @@ def _series(offsets, what: str):
     """(tensor, address, number of series) of the offsets."""
     if offsets is None:
         return None, None, 1
-    import torch
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 1 or not offsets.is_cuda:
+    if offsets.dtype != _torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 1 or not offsets.is_cuda:
         raise CrError(1, f"{what}: int32 CUDA offsets (series + 1) are needed")
     offsets = offsets.contiguous()
     return offsets, offsets.data_ptr(), offsets.shape[0] - 1
@@ -722,20 +716,19 @@ def _series(offsets, what: str):
 def gated_scan(G, X, gate: str = "convex", offsets=None, h0=None, save: bool = False):
     """cr_gated_scan: (H, hT) for G and X (D, T) with packed series in the T columns; save=True
     returns (H, hT, saved), saved being what gated_scan_backward restarts from."""
-    import torch
-    load()
+    _ready()
     kind = _type_of(X, "gated_scan X")
     D, T = _matrix_shape(X, "gated_scan X")
     X, px, ldx = _matrix(X, (D, T), X.dtype, "gated_scan X")
     G, pg, ldg = _matrix(G, (D, T), X.dtype, "gated_scan G")
     offsets, po, n = _series(offsets, "gated_scan offsets")
-    h0, p0, ld0 = _matrix(h0, (D, n), torch.float32, "gated_scan h0")
-    H, hT = _empty(D, T, X), _empty(D, n, X, torch.float32)
+    h0, p0, ld0 = _matrix(h0, (D, n), _torch.float32, "gated_scan h0")
+    H, hT = _empty(D, T, X.dtype, X.device), _empty(D, n, _torch.float32, X.device)
     saved = None
     if save:
         count = ctypes.c_size_t(0)
         _check(_lib.cr_gated_scan_saved(D, T, ctypes.byref(count)))
-        saved = X.new_empty(count.value, dtype=torch.float32)
+        saved = _torch.empty(count.value, dtype=_torch.float32, device=X.device)
     _check(_lib.cr_gated_scan(kind, _code(_GATES, gate, "gated_scan gate"), pg, ldg, px, ldx, D, T, po, n, p0, ld0,
                               H.data_ptr(), D, hT.data_ptr(), D, _ptr(saved), _raw_stream(X.device)))
     return (H, hT, saved) if save else (H, hT)
@@ -744,21 +737,21 @@ def gated_scan(G, X, gate: str = "convex", offsets=None, h0=None, save: bool = F
 @_on_stream
 def gated_scan_backward(G, X, dH, gate: str = "convex", offsets=None, h0=None, dhT=None, saved=None):
     """cr_gated_scan_backward: (dG, dX, dh0); saved is gated_scan's (None: recomputed)."""
-    import torch
-    load()
+    _ready()
     kind = _type_of(X, "gated_scan_backward X")
     D, T = _matrix_shape(X, "gated_scan_backward X")
     X, px, ldx = _matrix(X, (D, T), X.dtype, "gated_scan_backward X")
     G, pg, ldg = _matrix(G, (D, T), X.dtype, "gated_scan_backward G")
     dH, pd, ldd = _matrix(dH, (D, T), X.dtype, "gated_scan_backward dH")
     offsets, po, n = _series(offsets, "gated_scan_backward offsets")
-    h0, p0, ld0 = _matrix(h0, (D, n), torch.float32, "gated_scan_backward h0")
-    dhT, pt, ldt = _matrix(dhT, (D, n), torch.float32, "gated_scan_backward dhT")
+    h0, p0, ld0 = _matrix(h0, (D, n), _torch.float32, "gated_scan_backward h0")
+    dhT, pt, ldt = _matrix(dhT, (D, n), _torch.float32, "gated_scan_backward dhT")
     if saved is not None:
         count = ctypes.c_size_t(0)
         _check(_lib.cr_gated_scan_saved(D, T, ctypes.byref(count)))
         _vector(saved, count.value, "gated_scan_backward saved")
-    dG, dX, dh0 = _empty(D, T, X), _empty(D, T, X), _empty(D, n, X, torch.float32)
+    dG, dX = _empty(D, T, X.dtype, X.device), _empty(D, T, X.dtype, X.device)
+    dh0 = _empty(D, n, _torch.float32, X.device)
     _check(_lib.cr_gated_scan_backward(kind, _code(_GATES, gate, "gated_scan_backward gate"), pg, ldg, px, ldx, pd, ldd,
                                        D, T, po, n, p0, ld0, pt, ldt, _ptr(saved), dG.data_ptr(), D, dX.data_ptr(), D,
                                        dh0.data_ptr(), D, _raw_stream(X.device)))
@@ -768,18 +761,17 @@ def gated_scan_backward(G, X, dH, gate: str = "convex", offsets=None, h0=None, d
 @_on_stream
 def gated_step(G, X, h, gate: str = "convex", out=None):
     """cr_gated_step: (H, hnext) for one step of B series; out receives hnext and may be h."""
-    import torch
-    load()
+    _ready()
     kind = _type_of(X, "gated_step X")
     D, B = _matrix_shape(X, "gated_step X")
     X, px, ldx = _matrix(X, (D, B), X.dtype, "gated_step X")
     G, pg, ldg = _matrix(G, (D, B), X.dtype, "gated_step G")
-    h, ph, ldh = _matrix(h, (D, B), torch.float32, "gated_step h")
-    hn = _empty(D, B, X, torch.float32) if out is None else out
-    n, pn, ldn = _matrix(hn, (D, B), torch.float32, "gated_step out")
+    h, ph, ldh = _matrix(h, (D, B), _torch.float32, "gated_step h")
+    hn = _empty(D, B, _torch.float32, X.device) if out is None else out
+    n, pn, ldn = _matrix(hn, (D, B), _torch.float32, "gated_step out")
     if n is not hn:
         raise CrError(1, "gated_step out: a column-major matrix is needed")
-    H = _empty(D, B, X)
+    H = _empty(D, B, X.dtype, X.device)
     _check(_lib.cr_gated_step(kind, _code(_GATES, gate, "gated_step gate"), pg, ldg, px, ldx, ph, ldh, D, B,
                               H.data_ptr(), D, pn, ldn, _raw_stream(X.device)))
     return H, hn

@@ -34,8 +34,10 @@ struct Params {
   uint32_t idesc;        // MMA instruction descriptor
   int ti, tj;            // output tiles
   int bn;                // thin kernel: columns of its tile
-  int vec;               // C, R and Z allow 16-byte accesses
+  int tma_c, tma_z;      // C, Z can be stored by TMA
+  int vec_r;             // R allows 16-byte accesses
   int vecb;              // bias and iscale do
+  int vec4;              // four consecutive i of everything in the epilogue can be accessed at once
   Epilogue e;
   unsigned long long limit;
   int* err;
@@ -87,23 +89,6 @@ __device__ __forceinline__ void load8(const O* p, float* v) {   // 8 elements, 1
     }
   }
 }
-template <class O>
-__device__ __forceinline__ void store8(O* p, const float* v) {
-  if (sizeof(O) == 2) {
-    uint32_t u[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const O h[2] = {from_float<O>(v[2 * q]), from_float<O>(v[2 * q + 1])};
-      memcpy(&u[q], h, 4);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-  } else {
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      reinterpret_cast<float4*>(p)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-  }
-}
-
 // z (a finished sum) to the output (i, j).
 template <class O>
 __device__ __forceinline__ void finish(const Params& p, int i, int j, float z) {
@@ -115,6 +100,43 @@ __device__ __forceinline__ void finish(const Params& p, int i, int j, float z) {
   activate_all(v, p.e.act);
   if (p.e.R) v[0] += to_float(((const O*)p.e.R)[(size_t)j * p.e.ldr + i]);
   ((O*)p.e.C)[(size_t)j * p.e.ldc + i] = from_float<O>(v[0]);
+}
+
+// Four consecutive i of column j.
+template <class O>
+__device__ __forceinline__ void thin_finish4(const Params& p, int i, int j, float (&v)[4]) {
+  const Epilogue& e = p.e;
+  if (!p.vec4 || i + 4 > p.I) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (i + q < p.I) finish<O>(p, i + q, j, v[q]);
+    return;
+  }
+  const float js = e.jscale ? e.jscale[j] : 1.0f;
+  float4 is = make_float4(1, 1, 1, 1), b = make_float4(0, 0, 0, 0);
+  if (e.iscale) is = *reinterpret_cast<const float4*>(e.iscale + i);
+  if (e.bias) b = *reinterpret_cast<const float4*>(e.bias + i);
+  v[0] = fmaf(v[0] * is.x, js, b.x);
+  v[1] = fmaf(v[1] * is.y, js, b.y);
+  v[2] = fmaf(v[2] * is.z, js, b.z);
+  v[3] = fmaf(v[3] * is.w, js, b.w);
+  struct alignas(4 * sizeof(O)) Four {
+    O x[4];
+  };
+  const auto put = [&](void* out, int ld) {
+    Four o;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) o.x[q] = from_float<O>(v[q]);
+    *reinterpret_cast<Four*>((O*)out + (size_t)j * ld + i) = o;
+  };
+  if (e.Z) put(e.Z, e.ldz);
+  activate_all(v, e.act);
+  if (e.R) {
+    const Four r = *reinterpret_cast<const Four*>((const O*)e.R + (size_t)j * e.ldr + i);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] += to_float(r.x[q]);
+  }
+  put(e.C, e.ldc);
 }
 
 // One i and 16 columns from j0.
@@ -137,59 +159,95 @@ __device__ __forceinline__ void thin_store16(const Params& p, int i, int j0, flo
     }
 }
 
-// One j and 32 consecutive i.
-template <class O>
-__device__ __forceinline__ void wide_store(const Params& p, int i0, int j, float js, float (&v)[32]) {
+// A float vector's entries from i0 on, the same for all lanes (0 past the end).
+template <int N>
+__device__ __forceinline__ void load_row(const float* x, int i0, int I, int vec, float (&w)[N]) {
+  if (vec && i0 + N <= I) {
+#pragma unroll
+    for (int q = 0; q < N; q += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(x + i0 + q);
+      w[q] = f.x;
+      w[q + 1] = f.y;
+      w[q + 2] = f.z;
+      w[q + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < N; ++q) w[q] = i0 + q < I ? x[i0 + q] : 0.0f;
+  }
+}
+
+// The warp's 32 rows j of N = 128 / sizeof(O) values from (i0, j0): through shared memory (rows of 128
+// bytes in the 128-byte swizzle) and by TMA, or element by element where TMA cannot address them.
+template <class O, int N>
+__device__ __forceinline__ void put_rows(const CUtensorMap* tm, int tma, O* out, int ld, int I, int J, int i0, int j0, uint8_t* buf,
+                                         const float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+  if (tma) {
+    if (lane == 0) tma_store_wait_read();   // the buffer's last tile has been read
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      O h[16 / sizeof(O)];
+#pragma unroll
+      for (int x = 0; x < (int)(16 / sizeof(O)); ++x) h[x] = from_float<O>(v[q * (16 / sizeof(O)) + x]);
+      uint4 w;
+      memcpy(&w, h, 16);
+      *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) = w;
+    }
+    fence_smem_to_tma();
+    __syncwarp();
+    if (lane == 0 && j0 < J) tma_store_2d(tm, buf, i0, j0);
+  } else if (j0 + lane < J) {
+    O* o = out + (size_t)(j0 + lane) * ld + i0;
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+      if (i0 + q < I) o[q] = from_float<O>(v[q]);
+  }
+}
+
+// Epilogue of the warp's 32 rows j and N columns i; v holds the sums.
+template <class O, int N>
+__device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* tmC, const CUtensorMap* tmZ, int i0, int j0, float js,
+                                            uint8_t* buf, float (&v)[N]) {
   const Epilogue& e = p.e;
-  if (p.vec && p.vecb && i0 + 32 <= p.I) {
-    if (e.iscale) {
+  const int j = j0 + (threadIdx.x & 31);
+  if (e.iscale) {
+    float w[N];
+    load_row(e.iscale, i0, p.I, p.vecb, w);
 #pragma unroll
-      for (int q = 0; q < 32; q += 4) {
-        const float4 s = *reinterpret_cast<const float4*>(e.iscale + i0 + q);
-        v[q] *= s.x;
-        v[q + 1] *= s.y;
-        v[q + 2] *= s.z;
-        v[q + 3] *= s.w;
-      }
-    }
-    if (e.jscale) {
+    for (int q = 0; q < N; ++q) v[q] *= w[q];
+  }
+  if (e.jscale) {
 #pragma unroll
-      for (int q = 0; q < 32; ++q) v[q] *= js;
-    }
-    if (e.bias) {
+    for (int q = 0; q < N; ++q) v[q] *= js;
+  }
+  if (e.bias) {
+    float w[N];
+    load_row(e.bias, i0, p.I, p.vecb, w);
 #pragma unroll
-      for (int q = 0; q < 32; q += 4) {
-        const float4 s = *reinterpret_cast<const float4*>(e.bias + i0 + q);
-        v[q] += s.x;
-        v[q + 1] += s.y;
-        v[q + 2] += s.z;
-        v[q + 3] += s.w;
-      }
-    }
-    if (e.Z) {
-      O* z = (O*)e.Z + (size_t)j * e.ldz + i0;
+    for (int q = 0; q < N; ++q) v[q] += w[q];
+  }
+  if (e.Z) put_rows<O, N>(tmZ, p.tma_z, (O*)e.Z, e.ldz, p.I, p.J, i0, j0, buf, v);
+  activate_all(v, e.act);
+  if (e.R && j < p.J) {
+    const O* r = (const O*)e.R + (size_t)j * e.ldr + i0;
+    if (p.vec_r && i0 + N <= p.I) {
 #pragma unroll
-      for (int q = 0; q < 32; q += 8) store8(z + q, v + q);
-    }
-    activate_all(v, e.act);
-    if (e.R) {
-      const O* r = (const O*)e.R + (size_t)j * e.ldr + i0;
-#pragma unroll
-      for (int q = 0; q < 32; q += 8) {
+      for (int q = 0; q < N; q += 8) {
         float w[8];
         load8(r + q, w);
 #pragma unroll
         for (int x = 0; x < 8; ++x) v[q + x] += w[x];
       }
+    } else {
+#pragma unroll
+      for (int q = 0; q < N; ++q)
+        if (i0 + q < p.I) v[q] += to_float(r[q]);
     }
-    O* c = (O*)e.C + (size_t)j * e.ldc + i0;
-#pragma unroll
-    for (int q = 0; q < 32; q += 8) store8(c + q, v + q);
-    return;
   }
-#pragma unroll
-  for (int q = 0; q < 32; ++q)
-    if (i0 + q < p.I) finish<O>(p, i0 + q, j, v[q]);
+  __syncwarp();
+  put_rows<O, N>(tmC, p.tma_c, (O*)e.C, e.ldc, p.I, p.J, i0, j0, buf, v);
 }
 
 // ---------------------------------------------------------------- wide kernel
@@ -208,7 +266,8 @@ struct WideBars {
   uint32_t tmem;
   int abort;
 };
-constexpr int WSMEM = WSTAGES * WSTAGE + 1024 + 256;
+constexpr int WBUF = 32 * 128;                   // an epilogue warp's rows on their way out
+constexpr int WSMEM = WSTAGES * WSTAGE + WEPI * WBUF + 1024 + 256;
 static_assert(sizeof(WideBars) <= 256, "barrier area");
 
 // Tile t: column tiles j in groups of 8 and all row tiles i inside a group, so that the tiles in
@@ -221,10 +280,11 @@ __device__ __forceinline__ void wide_tile(const Params& p, int t, int& i, int& j
 
 template <bool F8, class O>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
-    k_affine_wide(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, const Params p) {
+    k_affine_wide(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
+                  const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmZ, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  WideBars* bars = reinterpret_cast<WideBars*>(smem + WSTAGES * WSTAGE);
+  WideBars* bars = reinterpret_cast<WideBars*>(smem + WSTAGES * WSTAGE + WEPI * WBUF);
   volatile int* abort_flag = &bars->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -301,7 +361,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
       const uint32_t ps = desc_step(p.pk), qs = desc_step(p.qk);
       for (int t = cl; t < ntiles && !*abort_flag; t += ncl, ++u) {
         const int b = u & 1;
-        if (!mbar_wait_cluster(&bars->tempty[b], ((uint32_t)(u >> 1) & 1u) ^ 1u, p.limit)) {
+        if (!mbar_wait(&bars->tempty[b], ((uint32_t)(u >> 1) & 1u) ^ 1u, p.limit)) {
           gave_up(p, abort_flag);
           break;
         }
@@ -309,7 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
         const uint32_t acc = tmem + (uint32_t)(b * 256);
         for (int kb = 0; kb < p.kblocks; ++kb) {
           if (*abort_flag) break;
-          if (!mbar_wait_cluster(&bars->full[st], ph, p.limit)) {
+          if (!mbar_wait(&bars->full[st], ph, p.limit)) {
             gave_up(p, abort_flag);
             break;
           }
@@ -327,6 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
     }
   } else {
     const int quad = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* buf = smem + WSTAGES * WSTAGE + (warp - 2) * WBUF;
     const uint32_t tempty[2] = {cluster_addr(smem_u32(&bars->tempty[0]), 0), cluster_addr(smem_u32(&bars->tempty[1]), 0)};
     int u = 0;
     for (int t = cl; t < ntiles; t += ncl, ++u) {
@@ -339,22 +400,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
       tc_fence_after();
       int ti, tj;
       wide_tile(p, t, ti, tj);
-      const int j = tj * 256 + (int)rank * 128 + quad * 32 + lane;
-      const int ibase = ti * 256 + half * 128;
+      const int j0 = tj * 256 + (int)rank * 128 + quad * 32, ibase = ti * 256 + half * 128;
       const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * 256 + half * 128);
-      const float js = p.e.jscale && j < p.J ? p.e.jscale[j] : 1.0f;
-      for (int c = 0; c < 128; c += 32) {
-        const int i0 = ibase + c;
-        float v[32];
-        __syncwarp();   // lanes without an output skipped the store
-        tmem_ld32(tq + (uint32_t)c, v);
-        if (i0 >= p.I || j >= p.J) continue;
-        wide_store<O>(p, i0, j, js, v);
+      const float js = p.e.jscale && j0 + lane < p.J ? p.e.jscale[j0 + lane] : 1.0f;
+      constexpr int N = 128 / (int)sizeof(O);
+      for (int c = 0; c < 128; c += N) {
+        float v[N];
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < N; q += 32) tmem_ld32(tq + (uint32_t)(c + q), v + q);
+        if (c + N == 128) {   // the accumulator is read: the next tile but one may have it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty[b]);
+        }
+        if (ibase + c < p.I) wide_finish<O, N>(p, &tmC, &tmZ, ibase + c, j0, js, buf, v);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tempty[b]);
     }
+    if (lane == 0) tma_store_wait_all();
   }
   __syncwarp();
   tc_fence_before();
@@ -368,13 +431,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
 
 // ---------------------------------------------------------------- thin kernel
 // 128 outputs i x bn columns j per cluster (operand A = P, B = Q): few columns, where the product is
-// bound by reading P.  The CTAs of a cluster take equal parts of k; their partial sums meet in
-// shared memory and are added in the order of the parts, each CTA finishing a part of the
-// outputs.
+// bound by reading P.  The CTAs of a cluster take equal parts of k.  Each finishes 128 / split of
+// the i: the others copy their partial sums for these into its shared memory, and it adds them in the
+// order of the parts.  (Stores of single sums to another CTA took 16 us where the bulk copies
+// take THINCOPY, at K = N = 2048, M = 64.)
 constexpr int TTHREADS = 192;
 constexpr int TMAXSTAGES = 8;
 struct ThinBars {
-  uint64_t full[TMAXSTAGES], empty[TMAXSTAGES], done;
+  uint64_t full[TMAXSTAGES], empty[TMAXSTAGES], done, got;
   uint32_t tmem;
   int abort;
 };
@@ -393,6 +457,7 @@ __global__ void __launch_bounds__(TTHREADS)
   const int i0 = tile / p.tj * 128, j0 = tile % p.tj * p.bn;
   const int kb0 = (int)((long long)p.kblocks * rank / split), kb1 = (int)((long long)p.kblocks * (rank + 1) / split);
   const uint32_t cols = p.bn <= 32 ? 32 : p.bn <= 64 ? 64 : p.bn <= 128 ? 128 : 256;
+  const int ncols = min(p.bn, p.J - j0);
   constexpr int KE = F8 ? 128 : 64;
 
   if (threadIdx.x == 0) {
@@ -401,15 +466,23 @@ __global__ void __launch_bounds__(TTHREADS)
       mbar_init(&bars->empty[s], 1);
     }
     mbar_init(&bars->done, 1);
+    mbar_init(&bars->got, 1);
     bars->abort = 0;
     fence_mbar_init();
+    if (split > 1) mbar_arrive_expect_tx(&bars->got, 512u * (uint32_t)ncols);
   }
   if (warp == 1) tmem_alloc(&bars->tmem, cols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
-  float* part = reinterpret_cast<float*>(smem);   // the stages again, after the last MMA: [column][128]
+  if (split > 1) cluster_arrive_relaxed();   // waited for before the first copy to another CTA
+  // Partial sums in blocks of sb consecutive i, [block][column][sb]: this CTA's own ones in the
+  // stages' memory once its MMAs are done, those that it receives, [part of k] of them, after the
+  // barriers, because other CTAs may be done before this one's last MMA.
+  const int own = 128 / split, sb = min(own, 32);
+  float* sent = reinterpret_cast<float*>(smem);
+  float* received = reinterpret_cast<float*>(smem + stages * stage_bytes + 256);
 
   if (warp == 0) {
     if (lane == 0) {
@@ -448,6 +521,7 @@ __global__ void __launch_bounds__(TTHREADS)
         }
     }
     __syncwarp();
+    if (split > 1) cluster_wait();
   } else if (warp == 1) {
     if (lane == 0 && kb1 > kb0) {
       int st = 0;
@@ -470,6 +544,7 @@ __global__ void __launch_bounds__(TTHREADS)
       mma_commit(&bars->done);   // after an abort too: it completes once the issued MMAs have
     }
     __syncwarp();
+    if (split > 1) cluster_wait();
   } else {
     const int f = (warp & 3) * 32 + lane, i = i0 + f;
     bool ok = true;
@@ -479,8 +554,9 @@ __global__ void __launch_bounds__(TTHREADS)
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     }
+    if (split > 1) cluster_wait();
     const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const int ncols = min(p.bn, p.J - j0);
+    float* to = sent + (size_t)(f / sb * ncols) * sb + f % sb;
     for (int c = 0; c < ncols; c += 16) {
       float v[16];
       __syncwarp();
@@ -491,28 +567,45 @@ __global__ void __launch_bounds__(TTHREADS)
         for (int q = 0; q < 16; ++q) v[q] = 0.0f;
       }
       if (split > 1) {
-        if (ok) {
 #pragma unroll
-          for (int q = 0; q < 16; ++q) part[(c + q) * 128 + f] = v[q];
-        }
+        for (int q = 0; q < 16; ++q)
+          if (c + q < ncols) to[(c + q) * sb] = v[q];
       } else if (i < p.I) {
         thin_store16<O>(p, i, j0 + c, v);
       }
     }
+    if (split > 1) {
+      fence_smem_to_tma();
+      __syncwarp();
+      const int f0 = (warp & 3) * 32 + lane * sb;   // lanes 0 .. 32 / sb - 1 send one block each
+      if (lane < 32 / sb) {
+        const uint32_t owner = (uint32_t)(f0 / own), bytes = 4u * (uint32_t)(ncols * sb);
+        const uint32_t at = (uint32_t)(rank * own + f0 % own) / (uint32_t)sb * bytes;
+        copy_to_cluster(cluster_addr(smem_u32(received), owner) + at, sent + (size_t)(f0 / sb * ncols) * sb, bytes,
+                        cluster_addr(smem_u32(&bars->got), owner));
+      }
+    }
   }
   if (split > 1) {
-    __syncthreads();
-    cluster_sync_all();
-    const int ncols = min(p.bn, p.J - j0), total = ncols * 128;
-    const int e0 = (int)((long long)total * rank / split), e1 = (int)((long long)total * (rank + 1) / split);
-    const uint32_t base = smem_u32(part);
-    for (int e = e0 + (int)threadIdx.x; e < e1; e += TTHREADS) {
-      float z = 0.0f;
-      for (int r = 0; r < split; ++r) z += ld_cluster(cluster_addr(base + 4u * (uint32_t)e, (uint32_t)r));
-      const int i = i0 + (e & 127);
-      if (i < p.I) finish<O>(p, i, j0 + (e >> 7), z);
+    const bool got = mbar_wait(&bars->got, 0, p.limit);
+    if (!got) gave_up(p, abort_flag);
+    const int total = ncols * own;
+    for (int e = 4 * (int)threadIdx.x; got && e < total; e += 4 * TTHREADS) {
+      float4 z = *reinterpret_cast<const float4*>(received + e);
+      for (int r = 1; r < split; ++r) {
+        const float4 x = *reinterpret_cast<const float4*>(received + r * total + e);
+        z.x += x.x;
+        z.y += x.y;
+        z.z += x.z;
+        z.w += x.w;
+      }
+      const int block = e / (ncols * sb), in = e - block * ncols * sb;
+      const int i = i0 + rank * own + block * sb + in % sb, j = j0 + in / sb;
+      float v[4] = {z.x, z.y, z.z, z.w};
+      thin_finish4<O>(p, i, j, v);
     }
-    cluster_sync_all();   // partial sums stay until every CTA has read them
+    __syncwarp();
+    cluster_sync_all();   // copies read this CTA's memory until their receivers have them
   }
   tc_fence_before();
   __syncthreads();
@@ -589,13 +682,13 @@ int sm_count() {
 }
 
 template <bool F8, class O>
-cr_status launch(const CUtensorMap& tmP, const CUtensorMap& tmQ, const Params& p, bool wide, int split, int stages, cudaStream_t stream) {
+cr_status launch(const CUtensorMap& tmP, const CUtensorMap& tmQ, const CUtensorMap& tmC, const CUtensorMap& tmZ, const Params& p, bool wide, int split, int stages, cudaStream_t stream) {
   if (wide) {
     static const cudaError_t set = cudaFuncSetAttribute(k_affine_wide<F8, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, WSMEM);
     CR_CUDA(set);
     const int pairs = std::min((long long)sm_count() / 2, (long long)p.ti * p.tj);
     TimedScope ts("k_affine_wide", stream);
-    k_affine_wide<F8, O><<<2 * pairs, WTHREADS, WSMEM, stream>>>(tmP, tmQ, p);
+    k_affine_wide<F8, O><<<2 * pairs, WTHREADS, WSMEM, stream>>>(tmP, tmQ, tmC, tmZ, p);
     CR_CHECK_LAUNCH("k_affine_wide");
     return CR_OK;
   }
@@ -609,7 +702,7 @@ cr_status launch(const CUtensorMap& tmP, const CUtensorMap& tmQ, const Params& p
   cfg.gridDim = dim3((unsigned)((long long)p.ti * p.tj * split));
   cfg.blockDim = dim3(TTHREADS);
   const int stage = WTILE + (p.qk ? p.bn * KBYTES : (p.bn + 63) / 64 * ATOM);
-  cfg.dynamicSmemBytes = (size_t)stages * stage + 1024 + 256;
+  cfg.dynamicSmemBytes = (size_t)stages * stage + 1024 + 256 + (split > 1 ? 512 * p.bn : 0);
   cfg.stream = stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
@@ -631,8 +724,12 @@ cr_status product(Operand P, Operand Q, int type, int K, int out_type, const Epi
   const int ke = KBYTES / type_bytes(type), ob = type_bytes(out_type);
   p.kblocks = (K + ke - 1) / ke;
   const auto ok16 = [&](const void* q, int ld) { return !q || (((uintptr_t)q & 15) == 0 && (long long)ld * ob % 16 == 0); };
-  p.vec = ok16(e.C, e.ldc) && ok16(e.R, e.ldr) && ok16(e.Z, e.ldz);
+  p.tma_c = ok16(e.C, e.ldc);
+  p.tma_z = ok16(e.Z, e.ldz);
+  p.vec_r = ok16(e.R, e.ldr);
   p.vecb = (((uintptr_t)e.bias | (uintptr_t)e.iscale) & 15) == 0;
+  const auto ok4 = [&](const void* q, int ld) { return !q || (((uintptr_t)q & (4 * ob - 1)) == 0 && ld % 4 == 0); };
+  p.vec4 = p.vecb && ok4(e.C, e.ldc) && ok4(e.R, e.ldr) && ok4(e.Z, e.ldz);
   Packed ownP, ownQ;
   CR_TRY(ownP.make(P, type, K, stream));
   CR_TRY(ownQ.make(Q, type, K, stream));
@@ -651,13 +748,15 @@ cr_status product(Operand P, Operand Q, int type, int K, int out_type, const Epi
     while (split < 8 && (long long)p.ti * p.tj * split < 2 * sm_count() && p.kblocks >= 4 * split) split *= 2;
     stages = std::min(p.bn <= 32 ? 5 : p.bn == 64 ? 4 : 3, 8);
   }
-  CUtensorMap tmP, tmQ;
+  CUtensorMap tmP = {}, tmQ = {}, tmC = {}, tmZ = {};
+  if (wide && p.tma_c) CR_TRY(make_tensor_map_2d(&tmC, out_type, e.C, p.I, p.J, e.ldc, KBYTES / ob, 32));
+  if (wide && e.Z && p.tma_z) CR_TRY(make_tensor_map_2d(&tmZ, out_type, e.Z, p.I, p.J, e.ldz, KBYTES / ob, 32));
   CR_TRY(map_of(&tmP, P, type, K, 128));
   CR_TRY(map_of(&tmQ, Q, type, K, wide ? 128 : p.bn));
   return with_type(out_type, [&](auto o0) -> cr_status {
     using O = decltype(o0);
-    return type == CR_TYPE_E4M3 ? launch<true, O>(tmP, tmQ, p, wide, split, stages, stream)
-                                : launch<false, O>(tmP, tmQ, p, wide, split, stages, stream);
+    return type == CR_TYPE_E4M3 ? launch<true, O>(tmP, tmQ, tmC, tmZ, p, wide, split, stages, stream)
+                                : launch<false, O>(tmP, tmQ, tmC, tmZ, p, wide, split, stages, stream);
   });
 }
 

@@ -165,16 +165,17 @@ cr_status free_class_storage(cr_tilemat V) {
   return CR_OK;
 }
 
-// Any 2-byte or 1-byte element type; box_inner elements are 128 bytes.
+// box_inner elements are 128 bytes.
 cr_status make_tensor_map_2d(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
                              int box_outer) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail_literal(CR_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
   const CUtensorMapDataType dt = type == CR_TYPE_E4M3  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                 : type == CR_TYPE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                  : type == CR_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
-  cuuint64_t strides[1] = {(cuuint64_t)ld * (type == CR_TYPE_E4M3 ? 1 : 2)};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * (type == CR_TYPE_E4M3 ? 1 : type == CR_TYPE_F32 ? 4 : 2)};
   cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer};
   cuuint32_t es[2] = {1, 1};
   const CUresult r = fn(tm, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
