@@ -165,9 +165,8 @@ cr_status free_class_storage(cr_tilemat V) {
   return CR_OK;
 }
 
-// box_inner elements are 128 bytes.
-cr_status make_tensor_map_2d(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
-                             int box_outer) {
+static cr_status tensor_map_2d(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
+                               int box_outer, CUtensorMapSwizzle swizzle) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail_literal(CR_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
   const CUtensorMapDataType dt = type == CR_TYPE_E4M3  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
@@ -178,10 +177,19 @@ cr_status make_tensor_map_2d(CUtensorMap* tm, int type, const void* base, int in
   cuuint64_t strides[1] = {(cuuint64_t)ld * (type == CR_TYPE_E4M3 ? 1 : type == CR_TYPE_F32 ? 4 : 2)};
   cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_outer};
   cuuint32_t es[2] = {1, 1};
-  const CUresult r = fn(tm, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = fn(tm, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(CR_ERR_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
   return CR_OK;
+}
+
+cr_status make_tensor_map_2d(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
+                             int box_outer) {
+  return tensor_map_2d(tm, type, base, inner, outer, ld, box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+cr_status make_tensor_map_2d_plain(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
+                                   int box_outer) {
+  return tensor_map_2d(tm, type, base, inner, outer, ld, box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 // The word that a bounded wait of an operator kernel sets (mapped host memory, one per process).

@@ -20,6 +20,10 @@ cr_status wait_word(int** d_word);
 cr_status make_tensor_map_2d(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
                              int box_outer);
 
+// The same without a swizzle, for tiles that threads read.
+cr_status make_tensor_map_2d_plain(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
+                                   int box_outer);
+
 // C++ exceptions end at the C entries.
 #define CR_ENTRY_BEGIN try {
 #define CR_ENTRY_END(what)                                                                    \
@@ -121,26 +125,47 @@ cr_status with_act(int act, F&& f) {
 }
 
 // ---------------------------------------------------------------- gates
-struct Gate {
-  float a, c;   // h_t = a h_{t-1} + c x_t
+// h_t = a h_{t-1} + c x_t.  Products that feed a sum are written as fmaf or __fmul_rn, so that every
+// variant of a kernel rounds alike.
+struct GateParts {
+  float a, rest;   // sigmoid(g) and sigmoid(-g); coefficient gate: g and 1
 };
-// Products that feed a sum are written as fmaf or __fmul_rn, so that every variant of a kernel
-// rounds alike.
+// sigmoid(g) = 1 / (1 + e^-g) and sigmoid(-g) = e^-g / (1 + e^-g), which has no cancellation.  -g is kept
+// below 87 so that e^-g is finite (at 87 sigmoid(g) is 1e-38); NaN stays.  The hardware's 2^x and
+// reciprocal err by about 2^-22, and g log2(e) rounds to 2^-24 of itself: 2^-20 in all for |g| < 16.
+template <int GATE>
+__device__ __forceinline__ GateParts gate_parts(float g) {
+  if (GATE == CR_GATE_COEFF) return {g, 1.0f};
+  float m, e, r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(-g), "f"(87.0f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(m * 1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return {r, e * r};
+}
+__device__ __forceinline__ float sqrt_fast(float x) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+template <int GATE>
+__device__ __forceinline__ float gate_input(const GateParts& p) {   // c; 1 - a^2 = rest (1 + a)
+  return GATE == CR_GATE_VARIANCE ? sqrt_fast(p.rest * (1.0f + p.a)) : p.rest;
+}
+struct Gate {
+  float a, c;
+};
 template <int GATE>
 __device__ __forceinline__ Gate gate_of(float g) {
-  if (GATE == CR_GATE_COEFF) return {g, 1.0f};
-  float p, q;
-  sigmoid_pair(g, p, q);
-  return {p, GATE == CR_GATE_CONVEX ? q : sqrtf(q * (1.0f + p))};   // 1 - p^2 = q (1 + p), no cancellation
+  const GateParts p = gate_parts<GATE>(g);
+  return {p.a, gate_input<GATE>(p)};
 }
-// da/dg and dc/dg.  Variance gate: dc/dg = -a (a q) / c = -a^2 sqrt(q / (1 + a)), finite at a = 1.
+// h' da/dg + x dc/dg.  Variance gate: dc/dg = -a (a rest) / c = -a^2 sqrt(rest / (1 + a)), finite at a = 1.
 template <int GATE>
-__device__ __forceinline__ Gate gate_slope(float g) {
-  if (GATE == CR_GATE_COEFF) return {1.0f, 0.0f};
-  float p, q;
-  sigmoid_pair(g, p, q);
-  if (GATE == CR_GATE_CONVEX) return {p * q, -p * q};
-  return {p * q, -p * p * sqrtf(__fdividef(q, 1.0f + p))};
+__device__ __forceinline__ float gate_slope(const GateParts& p, float before, float x) {
+  if (GATE == CR_GATE_COEFF) return before;
+  if (GATE == CR_GATE_CONVEX) return __fmul_rn(__fmul_rn(p.a, p.rest), __fadd_rn(before, -x));
+  const float s = sqrt_fast(__fdividef(p.rest, 1.0f + p.a));
+  return __fmul_rn(p.a, fmaf(before, p.rest, -__fmul_rn(__fmul_rn(x, p.a), s)));
 }
 
 }  // namespace cr

@@ -2,6 +2,7 @@
 // (cr_gated_scan, cr_gated_scan_backward, cr_gated_step).
 #include <limits.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "ops.cuh"
@@ -10,26 +11,41 @@
 namespace cr {
 namespace {
 
-// How the scan is split.  A block owns 32 VEC features and CH consecutive steps (a chunk); each of its
-// 8 warps owns SUB of the steps, each thread VEC features of them, in registers, so that G and X
-// are read once and H is written once.  The map of a run of steps on the state is h -> A h + B,
-// and such maps compose; "start from h0" is the map A = 0, B = h0, so that packed series need
-// no other care (A = 0 is taken as "forget", not multiplied, so that nothing crosses into the
-// next series).  Warps join their maps in shared memory, chunks through global memory in two
-// levels: a chunk composes the maps of the earlier chunks of its group, and takes the state
-// before the group from the group's predecessor.  Every composition has a fixed order, so results
-// do not depend on which block is done first.  Blocks take their place from a counter: whatever a
-// block waits for was taken earlier and is running.
-constexpr int WARPS = 8, NT = 32 * WARPS;
-constexpr int FSUB = 16, BSUB = 8;        // steps per thread, forward and backward
+// How the scan is split.  A work item is a chunk of consecutive steps by a tile of W features (128
+// bytes of each column).  Resident blocks take items in order of time from a counter: whatever an
+// item waits for was taken earlier and is being worked on.  Warp 8 of a block takes the items and
+// loads them by TMA into a ring of stages, so that loads stay in flight while the other 8 warps
+// work; each of these owns SUB of the chunk's steps and each of its lanes VEC features, in
+// registers, so that the inputs are read once.
+// The map of a run of steps on the state is h -> A h + B, and such maps compose; "start from
+// h0" is the map A = 0, B = h0, so that packed series need no other care (A = 0 is taken as "forget",
+// not multiplied, so that nothing crosses into the next series).  Warps join their maps in
+// shared memory, chunks through global memory in two levels: a chunk composes the maps of the
+// earlier chunks of its group, and takes the state before the group from the group's
+// predecessor.  Every composition has a fixed order, so results do not depend on timing.
+constexpr int WARPS = 8, NT = 32 * (WARPS + 1);
+constexpr int FSUB = 16, BSUB = 8;        // steps per warp, forward and backward
 constexpr int BLOCK = WARPS * BSUB;       // steps between saved states: a chunk of the backward pass
+constexpr int STAGES = 3;
 constexpr int MAXGROUP = 64;
+constexpr int ROW = 128;                  // bytes of a column in a tile
+template <class T>
+constexpr int vec_of() { return 4 / (int)sizeof(T); }
 
+template <class T, int VEC>
+struct alignas(sizeof(T) * VEC) Pack {
+  T x[VEC];
+};
+
+// What chunks tell each other, cleared before the call.  Every entry is one 64-bit word, written
+// and read whole, that is 0 until it is there, so that no fence stands between data and flag: a
+// map is A in the low half, with +0 written as -0, and B in the high one; a state has 1 in the low half.
+typedef unsigned long long Word;
 struct Lookback {
-  int chunks, tiles, group;
-  int* flags;      // counter, then [tile][chunk] map written, then [tile][group] state written
-  float2* maps;    // [chunk][feature]
-  float* states;   // [group][feature]: the state that the group hands on
+  int chunks, tiles, group, width;   // width: features rounded up to whole tiles
+  int* counter;
+  Word* maps;      // [chunk][feature]
+  Word* states;    // [group][feature]: the state that the group hands on
   unsigned long long limit;
   int* err;
 };
@@ -40,36 +56,40 @@ __device__ __forceinline__ void forget_or(float& A, float& B, float a, float b) 
 }
 __device__ __forceinline__ float apply_map(float A, float B, float h) { return A == 0.0f ? B : fmaf(A, h, B); }
 
-__device__ __forceinline__ int ld_flag(const int* p) {
-  int v;
-  asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
+__device__ __forceinline__ Word map_word(float A, float B) {
+  return (Word)__float_as_uint(B) << 32 | __float_as_uint(A == 0.0f ? -0.0f : A);
 }
-// Marks data that the warp's lanes have stored as readable.
-__device__ __forceinline__ void raise_flag(int* p) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) {
-    __threadfence();
-    asm volatile("st.relaxed.gpu.global.s32 [%0], 1;" ::"l"(p) : "memory");
-  }
+__device__ __forceinline__ void post(Word* p, Word w) {
+  asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(w) : "memory");
 }
-// Waits until flags[0 .. n) are raised (n <= 32, one per lane); false when the limit runs out.
-__device__ __forceinline__ bool wait_flags(const int* flags, int n, const Lookback& lb) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ Word peek(const Word* p) {
+  Word w;
+  asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(w) : "l"(p) : "memory");
+  return w;
+}
+// Reads N words, `stride` apart, of which the first n are waited for (the others stay 0); false when
+// the limit runs out.
+template <int N>
+__device__ __forceinline__ bool await(const Word* p, size_t stride, int n, const Lookback& lb, Word (&w)[N]) {
+#pragma unroll
+  for (int q = 0; q < N; ++q) w[q] = 0;
   unsigned long long t0 = 0;
   while (true) {
-    const bool up = lane >= n || ld_flag(flags + lane) != 0;
-    if (__all_sync(0xffffffffu, up)) break;
+    bool there = true;
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+      if (q < n && w[q] == 0) w[q] = peek(p + q * stride);
+#pragma unroll
+    for (int q = 0; q < N; ++q) there = there && (q >= n || w[q] != 0);
+    if (there) return true;
     const unsigned long long t = global_timer_ns();
     if (t0 == 0) t0 = t;
-    if (__any_sync(0xffffffffu, t - t0 > lb.limit)) {
+    if (t - t0 > lb.limit) {
       *(volatile int*)lb.err = 1;
       __threadfence_system();
       return false;
     }
   }
-  __threadfence();
-  return true;
 }
 
 // First s in [0, n] with off[s] >= t, found by the 32 lanes together.
@@ -87,20 +107,20 @@ __device__ __forceinline__ int first_at_least(const int32_t* off, int n, int t) 
   return lo;
 }
 
-// Series that start or end in the chunk [t0, t0 + len): first[t - t0], last[t - t0] = the series or -1.
-// empty(s) is called (by a whole warp) for the empty series that belong to the chunk.
+// By one warp: series that start or end in the chunk [t0, t0 + len): first[t - t0], last[t - t0] = the
+// series or -1.  empty(s) is called for the empty series that belong to the chunk.
 template <class F>
 __device__ __forceinline__ void mark_series(const int32_t* off, int n, int t0, int len, int T, int* first, int* last, F&& empty) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int q = threadIdx.x; q < len; q += NT) {
+  const int lane = threadIdx.x & 31;
+  for (int q = lane; q < len; q += 32) {
     first[q] = !off && t0 + q == 0 ? 0 : -1;
     last[q] = !off && t0 + q == T - 1 ? 0 : -1;
   }
   if (!off) return;
   const int lo = first_at_least(off, n, t0);
   const bool final = t0 + len >= T;   // empty series at T belong to the last chunk
-  __syncthreads();
-  for (int base = max(lo - 1, 0) + warp * 32; base < n; base += NT) {
+  __syncwarp();
+  for (int base = max(lo - 1, 0); base < n; base += 32) {
     const int s = base + lane;
     const int b = s < n ? off[s] : INT_MAX, e = s < n ? off[s + 1] : INT_MAX;
     const bool in = s < n && (b < t0 + len || final);
@@ -110,79 +130,10 @@ __device__ __forceinline__ void mark_series(const int32_t* off, int n, int t0, i
     }
     uint32_t none = __ballot_sync(0xffffffffu, in && s >= lo && e <= b);
     for (; none; none &= none - 1) empty(base + __ffs(none) - 1);
-    if (!__any_sync(0xffffffffu, in)) break;
+    if (!__all_sync(0xffffffffu, in)) break;
   }
+  __syncwarp();
 }
-
-// The state that enters this block's chunk k of its tile, for the features f .. f + VEC - 1 of the
-// thread: (A, B) is the chunk's own map, the same in all warps.  fold and state are shared memory.
-// All threads call it; false when a wait ran out.
-template <int VEC>
-__device__ __forceinline__ bool state_in(const Lookback& lb, int tile, int k, int f, int D, const float (&A)[VEC], const float (&B)[VEC],
-                                         float2 (*fold)[32 * VEC], float* state, int* bad, float (&h)[VEC]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = k / lb.group, in = k % lb.group, c0 = g * lb.group;
-  int* flags = lb.flags + 1 + (size_t)tile * lb.chunks;
-  int* gflags = lb.flags + 1 + (size_t)lb.tiles * lb.chunks + (size_t)tile * ((lb.chunks + lb.group - 1) / lb.group);
-  const bool lastin = in == lb.group - 1;
-  if (warp == 0 && !lastin && k + 1 < lb.chunks) {
-#pragma unroll
-    for (int v = 0; v < VEC; ++v)
-      if (f + v < D) lb.maps[(size_t)k * D + f + v] = make_float2(A[v], B[v]);
-    raise_flag(flags + k);
-  }
-  // the earlier chunks of the group, a fixed part of them per warp
-  const int per = lb.group / WARPS, c1 = min(in, (warp + 1) * per);
-  float FA[VEC], FB[VEC];
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) FA[v] = 1.0f, FB[v] = 0.0f;
-  bool ok = true;
-  if (warp * per < c1) {
-    ok = wait_flags(flags + c0 + warp * per, c1 - warp * per, lb);
-    if (ok) {
-      float2 m[MAXGROUP / WARPS][VEC];
-#pragma unroll
-      for (int q = 0; q < MAXGROUP / WARPS; ++q)
-#pragma unroll
-        for (int v = 0; v < VEC; ++v)
-          m[q][v] = warp * per + q < c1 && f + v < D ? __ldcg(lb.maps + (size_t)(c0 + warp * per + q) * D + f + v) : make_float2(1.0f, 0.0f);
-#pragma unroll
-      for (int q = 0; q < MAXGROUP / WARPS; ++q)
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) forget_or(FA[v], FB[v], m[q][v].x, m[q][v].y);
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) fold[warp][lane * VEC + v] = make_float2(FA[v], FB[v]);
-  if (warp == 0) {
-    if (g > 0) ok = wait_flags(gflags + g - 1, 1, lb) && ok;
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) state[lane * VEC + v] = g > 0 && ok && f + v < D ? __ldcg(lb.states + (size_t)(g - 1) * D + f + v) : 0.0f;
-  }
-  if (!ok) *bad = 1;
-  __syncthreads();
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) {
-    h[v] = state[lane * VEC + v];
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      const float2 m = fold[w][lane * VEC + v];
-      h[v] = apply_map(m.x, m.y, h[v]);
-    }
-  }
-  if (warp == 0 && lastin && k + 1 < lb.chunks) {
-#pragma unroll
-    for (int v = 0; v < VEC; ++v)
-      if (f + v < D) lb.states[(size_t)g * D + f + v] = apply_map(A[v], B[v], h[v]);
-    raise_flag(gflags + g);
-  }
-  return *(volatile int*)bad == 0;
-}
-
-template <class T, int VEC>
-struct alignas(sizeof(T) * VEC) Pack {
-  T x[VEC];
-};
 
 // The features' h0 (or its gradient's seed) of series s.
 template <int VEC>
@@ -197,10 +148,161 @@ __device__ __forceinline__ void store_state(float* hT, int ld, int s, int f, int
     if (hT && f + v < D) hT[(size_t)s * ld + f + v] = h[v];
 }
 
+__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Shared memory of a block: ring of stages of NIN input tiles, then this.
+template <int CH, int W>
+struct Shared {
+  uint64_t full[STAGES], empty[STAGES];
+  int place[STAGES];
+  int first[STAGES][CH], last[STAGES][CH];
+  float2 maps[WARPS][W], fold[WARPS][W];
+  float start[WARPS][W], state[W];
+  int bad;
+};
+
+struct Input {
+  const void* p;
+  int ld;
+};
+
+// Warp 8: takes work items and fills stages.  item(place, tile, t0) gives an item's tile and first
+// step, empty(tile, s) handles an empty series.
+template <class T, int CH, int NIN, int W, class Item, class Empty>
+__device__ __forceinline__ void feed(const Lookback& lb, Shared<CH, W>* sh, uint8_t* ring, const CUtensorMap* const (&tm)[NIN], bool tma,
+                                     const int32_t* off, int series, int n, Item&& item, Empty&& empty) {
+  const int lane = threadIdx.x & 31, total = lb.chunks * lb.tiles;
+  int it = 0;
+  for (;; ++it) {
+    const int st = it % STAGES;
+    if (!mbar_wait(&sh->empty[st], ((uint32_t)(it / STAGES) & 1u) ^ 1u, lb.limit) || *(volatile int*)&sh->bad) break;
+    int place = 0;
+    if (lane == 0) place = lb.chunks > 1 ? atomicAdd(lb.counter, 1) : (int)blockIdx.x + it * (int)gridDim.x;
+    place = __shfl_sync(0xffffffffu, place, 0);
+    if (place >= total) {
+      if (lane == 0) {
+        sh->place[st] = -1;
+        mbar_arrive(&sh->full[st]);
+      }
+      return;
+    }
+    int tile, t0;
+    item(place, tile, t0);
+    if (lane == 0) {
+      sh->place[st] = place;
+      if (tma) {
+        mbar_expect_tx(&sh->full[st], NIN * CH * ROW);
+#pragma unroll
+        for (int q = 0; q < NIN; ++q) tma_load_2d(ring + (st * NIN + q) * CH * ROW, tm[q], &sh->full[st], tile * W, t0);
+      }
+    }
+    mark_series(off, series, t0, CH, n, sh->first[st], sh->last[st], [&](int s) { empty(tile, s); });
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->full[st]);
+  }
+  // gave up: copies in flight land before the block leaves
+  __syncwarp();
+  if (lane == 0) {
+    *(volatile int*)lb.err = 1;
+    __threadfence_system();
+    for (int q = 1; tma && q <= STAGES && q <= it; ++q)
+      mbar_wait(&sh->full[(it - q) % STAGES], (uint32_t)((it - q) / STAGES) & 1u, lb.limit);
+  }
+}
+
+// Without TMA (a matrix whose columns are not on 16-byte boundaries): each warp copies its own rows.
+template <class T, int W>
+__device__ __forceinline__ void copy_rows(const Input& in, uint8_t* tile, int row0, int rows, int f0, int t0, int D, int n) {
+  T* to = reinterpret_cast<T*>(tile);
+  for (int r = 0; r < rows; ++r)
+    for (int x = threadIdx.x & 31; x < W; x += 32)
+      to[(row0 + r) * W + x] = f0 + x < D && t0 + r < n ? ((const T*)in.p)[(size_t)(t0 + r) * in.ld + f0 + x] : from_float<T>(0.0f);
+}
+
+// The item in the stage of round `it`; -1 when there is none or the wait for it ran out.  sh->bad is
+// written before a barrier of the workers and read before the next, so that they agree.
+template <class S>
+__device__ __forceinline__ int next_item(const Lookback& lb, S* sh, int it) {
+  if (!mbar_wait(&sh->full[it % STAGES], (uint32_t)(it / STAGES) & 1u, lb.limit)) {
+    *(volatile int*)&sh->bad = 1;
+    *(volatile int*)lb.err = 1;
+    __threadfence_system();
+  }
+  workers_sync();
+  return *(volatile int*)&sh->bad ? -1 : sh->place[it % STAGES];
+}
+
+// Joins the workers' maps (A, B) of a chunk (position k in the order of work): the state that enters the
+// part of each warp, in sh->start.  Warps compose in the order 0 .. 7, or 7 .. 0 with REVERSE.  All
+// workers call it; false when a wait ran out.
+template <bool REVERSE, int VEC, int CH, int W>
+__device__ __forceinline__ bool join(const Lookback& lb, Shared<CH, W>* sh, int tile, int k, int D, const float (&A)[VEC], const float (&B)[VEC]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) sh->maps[warp][lane * VEC + v] = make_float2(A[v], B[v]);
+  workers_sync();
+  const int g = k / lb.group, in = k % lb.group, c0 = g * lb.group;
+  const bool more = k + 1 < lb.chunks, lastin = in == lb.group - 1;
+  // one thread per feature: the chunk's map
+  const int x = threadIdx.x, fx = tile * W + x;
+  float TA = 1.0f, TB = 0.0f;
+  if (x < W) {
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float2 m = sh->maps[REVERSE ? WARPS - 1 - w : w][x];
+      forget_or(TA, TB, m.x, m.y);
+    }
+    if (more && !lastin) post(lb.maps + (size_t)k * lb.width + fx, map_word(TA, TB));
+  }
+  bool fine = true;
+  float h = 0.0f;
+  if (lb.chunks > 1) {
+    // the earlier chunks of the group, a fixed part of them per warp
+    const int per = lb.group / WARPS, q0 = warp * per, n = min(in - q0, per);
+    bool ok = true;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      float FA = 1.0f, FB = 0.0f;
+      for (int q = 0; q < n; q += 4) {
+        Word w[4];
+        ok = await(lb.maps + (size_t)(c0 + q0 + q) * lb.width + tile * W + 32 * v + lane, lb.width, n - q, lb, w) && ok;
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (q + y < n) forget_or(FA, FB, __uint_as_float((uint32_t)w[y]), __uint_as_float((uint32_t)(w[y] >> 32)));
+      }
+      sh->fold[warp][32 * v + lane] = make_float2(FA, FB);
+    }
+    if (x < W && g > 0) {
+      Word w[1];
+      ok = await(lb.states + (size_t)(g - 1) * lb.width + fx, 0, 1, lb, w) && ok;
+      h = __uint_as_float((uint32_t)(w[0] >> 32));
+    }
+    if (!ok) *(volatile int*)&sh->bad = 1;
+    workers_sync();
+    fine = *(volatile int*)&sh->bad == 0;
+  }
+  if (x < W) {
+    if (lb.chunks > 1) {
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) h = apply_map(sh->fold[w][x].x, sh->fold[w][x].y, h);
+      if (lastin && more)
+        post(lb.states + (size_t)g * lb.width + fx, (Word)__float_as_uint(apply_map(TA, TB, h)) << 32 | 1u);
+    }
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const int u = REVERSE ? WARPS - 1 - w : w;
+      sh->start[u][x] = h;
+      h = apply_map(sh->maps[u][x].x, sh->maps[u][x].y, h);
+    }
+  }
+  workers_sync();
+  return fine;
+}
+
 template <class T>
 struct FwdArgs {
-  const T *G, *X;
-  int ldg, ldx, D, n;   // n columns
+  Input G, X;
+  int D, n;   // n columns
   const int32_t* off;
   int series;
   const float* h0;
@@ -210,100 +312,134 @@ struct FwdArgs {
   float* hT;
   int ldhT;
   float* saved;
+  int tma, pairs;   // inputs by TMA; H takes accesses of VEC elements
 };
 
-// Forward scan.  Bound by HBM (G and X read, H written).
-template <class T, int GATE, int VEC>
-__global__ void __launch_bounds__(NT, 2) k_scan_fwd(const FwdArgs<T> p, const Lookback lb) {
-  constexpr int CH = WARPS * FSUB, W = 32 * VEC;
-  __shared__ int first[CH], last[CH], s_place, s_bad;
-  __shared__ float2 maps[WARPS][W], fold[WARPS][W];
-  __shared__ float state[W];
+template <class T, int VEC>
+__device__ __forceinline__ void put(T* out, int ld, int t, int f, int D, bool vec, const float (&v)[VEC]) {
+  T* o = out + (size_t)t * ld + f;
+  if (vec) {
+    Pack<T, VEC> w;
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) w.x[q] = from_float<T>(v[q]);
+    *reinterpret_cast<Pack<T, VEC>*>(o) = w;
+  } else {
+#pragma unroll
+    for (int q = 0; q < VEC; ++q)
+      if (f + q < D) o[q] = from_float<T>(v[q]);
+  }
+}
+
+// Forward scan.  Bound by HBM (G and X read, H written).  Steps past the end and features past D hold
+// zeros: their states are never used.
+template <class T, int GATE>
+__global__ void __launch_bounds__(NT, 2)
+    k_scan_fwd(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmX, const FwdArgs<T> p, const Lookback lb) {
+  constexpr int CH = WARPS * FSUB, VEC = vec_of<T>(), W = 32 * VEC;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~(uintptr_t)127);
+  auto* sh = reinterpret_cast<Shared<CH, W>*>(ring + STAGES * 2 * CH * ROW);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    s_place = lb.chunks > 1 ? atomicAdd(lb.flags, 1) : (int)blockIdx.x;
-    s_bad = 0;
+    for (int q = 0; q < STAGES; ++q) {
+      mbar_init(&sh->full[q], 1);
+      mbar_init(&sh->empty[q], WARPS);
+    }
+    sh->bad = 0;
+    fence_mbar_init();
   }
   __syncthreads();
-  const int k = s_place / lb.tiles, tile = s_place % lb.tiles, t0 = k * CH + warp * FSUB, f = tile * W + lane * VEC;
-  const bool on = f < p.D;
-  Pack<T, VEC> rg[FSUB], rx[FSUB];
-#pragma unroll
-  for (int i = 0; i < FSUB; ++i)
-    if (on && t0 + i < p.n) {
-      rg[i] = *reinterpret_cast<const Pack<T, VEC>*>(p.G + (size_t)(t0 + i) * p.ldg + f);
-      rx[i] = *reinterpret_cast<const Pack<T, VEC>*>(p.X + (size_t)(t0 + i) * p.ldx + f);
+  if (warp == WARPS) {
+    const CUtensorMap* const tm[2] = {&tmG, &tmX};
+    feed<T, CH, 2, W>(
+        lb, sh, ring, tm, p.tma, p.off, p.series, p.n,
+        [&](int place, int& tile, int& t0) {
+          tile = place % lb.tiles;
+          t0 = place / lb.tiles * CH;
+        },
+        [&](int tile, int s) {
+          float h[VEC];
+          load_state<VEC>(p.h0, p.ldh0, s, tile * W + lane * VEC, p.D, h);
+          store_state<VEC>(p.hT, p.ldhT, s, tile * W + lane * VEC, p.D, h);
+        });
+    return;
+  }
+  for (int it = 0;; ++it) {
+    const int st = it % STAGES;
+    const int place = next_item(lb, sh, it);
+    if (place < 0) break;
+    const int k = place / lb.tiles, tile = place % lb.tiles, t0 = k * CH + warp * FSUB, f = tile * W + lane * VEC;
+    uint8_t* in = ring + st * 2 * CH * ROW;
+    if (!p.tma) {
+      copy_rows<T, W>(p.G, in, warp * FSUB, FSUB, tile * W, t0, p.D, p.n);
+      copy_rows<T, W>(p.X, in + CH * ROW, warp * FSUB, FSUB, tile * W, t0, p.D, p.n);
+      __syncwarp();
     }
-  mark_series(p.off, p.series, k * CH, CH, p.n, first, last, [&](int s) {
-    float h[VEC];
-    load_state<VEC>(p.h0, p.ldh0, s, f, p.D, h);
-    store_state<VEC>(p.hT, p.ldhT, s, f, p.D, h);
-  });
-  __syncthreads();
-  const uint32_t starts = __ballot_sync(0xffffffffu, lane < FSUB && first[warp * FSUB + (lane & (FSUB - 1))] >= 0);
-  const uint32_t ends = __ballot_sync(0xffffffffu, lane < FSUB && last[warp * FSUB + (lane & (FSUB - 1))] >= 0);
+    const int* first = sh->first[st] + warp * FSUB;
+    const int* last = sh->last[st] + warp * FSUB;
+    const uint32_t starts = __ballot_sync(0xffffffffu, lane < FSUB && first[lane & (FSUB - 1)] >= 0);
+    const uint32_t ends = __ballot_sync(0xffffffffu, lane < FSUB && last[lane & (FSUB - 1)] >= 0);
+    const uint8_t* row = in + warp * FSUB * ROW + lane * 4;
 
-  float a[FSUB][VEC], b[FSUB][VEC], A[VEC], B[VEC];
+    float a[FSUB][VEC], b[FSUB][VEC], A[VEC], B[VEC];
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) A[v] = 1.0f, B[v] = 0.0f;
+    for (int v = 0; v < VEC; ++v) A[v] = 1.0f, B[v] = 0.0f;
 #pragma unroll
-  for (int i = 0; i < FSUB; ++i) {
-    if (starts >> i & 1u) {
-      load_state<VEC>(p.h0, p.ldh0, first[warp * FSUB + i], f, p.D, B);
+    for (int i = 0; i < FSUB; ++i) {
+      const auto g = *reinterpret_cast<const Pack<T, VEC>*>(row + i * ROW);
+      const auto x = *reinterpret_cast<const Pack<T, VEC>*>(row + CH * ROW + i * ROW);
+      if (starts >> i & 1u) {
+        load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, B);
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) A[v] = 0.0f;
+        for (int v = 0; v < VEC; ++v) A[v] = 0.0f;
+      }
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const Gate c = gate_of<GATE>(to_float(g.x[v]));
+        a[i][v] = c.a;
+        b[i][v] = __fmul_rn(c.c, to_float(x.x[v]));
+        A[v] *= a[i][v];
+        B[v] = fmaf(a[i][v], B[v], b[i][v]);
+      }
     }
+    if (!join<false, VEC, CH, W>(lb, sh, tile, k, p.D, A, B)) return;
+    float h[VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      const bool in = on && t0 + i < p.n;
-      const Gate g = gate_of<GATE>(in ? to_float(rg[i].x[v]) : 0.0f);
-      a[i][v] = in ? g.a : 1.0f;
-      b[i][v] = in ? __fmul_rn(g.c, to_float(rx[i].x[v])) : 0.0f;
-      A[v] *= a[i][v];
-      B[v] = fmaf(a[i][v], B[v], b[i][v]);
+    for (int v = 0; v < VEC; ++v) h[v] = sh->start[warp][lane * VEC + v];
+    if (p.saved && warp * FSUB % BLOCK == 0 && t0 < p.n) store_state<VEC>(p.saved, p.D, t0 / BLOCK, f, p.D, h);
+    const int steps = f < p.D ? p.n - t0 : 0;
+    if (!(starts | ends) && p.H && p.pairs && p.n - t0 >= FSUB) {   // inside a series
+      T* o = p.H + (size_t)t0 * p.ldh + f;
+#pragma unroll
+      for (int i = 0; i < FSUB; ++i) {
+        Pack<T, VEC> w;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+          h[v] = fmaf(a[i][v], h[v], b[i][v]);
+          w.x[v] = from_float<T>(h[v]);
+        }
+        if (f < p.D) *reinterpret_cast<Pack<T, VEC>*>(o) = w;
+        o += p.ldh;
+      }
+    } else {
+#pragma unroll
+    for (int i = 0; i < FSUB; ++i) {
+      if (starts >> i & 1u) load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, h);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) h[v] = fmaf(a[i][v], h[v], b[i][v]);
+      if (p.H && i < steps) put<T, VEC>(p.H, p.ldh, t0 + i, f, p.D, p.pairs, h);
+      if (ends >> i & 1u) store_state<VEC>(p.hT, p.ldhT, last[i], f, p.D, h);
     }
-  }
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) maps[warp][lane * VEC + v] = make_float2(A[v], B[v]);
-  __syncthreads();
-  // the map of the warps before this one, and the whole chunk's
-  float PA[VEC], PB[VEC];
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) {
-    A[v] = PA[v] = 1.0f, B[v] = PB[v] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      const float2 m = maps[w][lane * VEC + v];
-      forget_or(A[v], B[v], m.x, m.y);
-      if (w < warp) PA[v] = A[v], PB[v] = B[v];
     }
-  }
-  float h[VEC];
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) h[v] = 0.0f;
-  if (lb.chunks > 1 && !state_in<VEC>(lb, tile, k, f, p.D, A, B, fold, state, &s_bad, h)) return;
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) h[v] = apply_map(PA[v], PB[v], h[v]);
-  if (p.saved && warp * FSUB % BLOCK == 0 && t0 < p.n) store_state<VEC>(p.saved, p.D, t0 / BLOCK, f, p.D, h);
-#pragma unroll
-  for (int i = 0; i < FSUB; ++i) {
-    if (starts >> i & 1u) load_state<VEC>(p.h0, p.ldh0, first[warp * FSUB + i], f, p.D, h);
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) h[v] = fmaf(a[i][v], h[v], b[i][v]);
-    if (p.H && on && t0 + i < p.n) {
-      Pack<T, VEC> o;
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) o.x[v] = from_float<T>(h[v]);
-      *reinterpret_cast<Pack<T, VEC>*>(p.H + (size_t)(t0 + i) * p.ldh + f) = o;
-    }
-    if (ends >> i & 1u) store_state<VEC>(p.hT, p.ldhT, last[warp * FSUB + i], f, p.D, h);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->empty[st]);
   }
 }
 
 template <class T>
 struct BwdArgs {
-  const T *G, *X, *dH;
-  int ldg, ldx, lddh, D, n;
+  Input G, X, dH;
+  int D, n;
   const int32_t* off;
   int series;
   const float *h0, *dhT, *saved;
@@ -312,135 +448,148 @@ struct BwdArgs {
   int lddg, lddx;
   float* dh0;
   int lddh0;
+  int tma, pairs;
 };
 
 // Backward scan, from the last chunk to the first: r_t = a_t q_t, q_t = dh_t + r_{t+1}, with "take dhT" at
 // a series' last step.  The states inside a chunk are recomputed from the saved one before
 // it, which reads G and X (needed anyway) in place of H.  Bound by HBM (G, X, dH read, dG, dX written).
-template <class T, int GATE, int VEC>
-__global__ void __launch_bounds__(NT, 2) k_scan_bwd(const BwdArgs<T> p, const Lookback lb) {
-  constexpr int CH = BLOCK, SUB = BSUB, W = 32 * VEC;
-  __shared__ int first[CH], last[CH], s_place, s_bad;
-  __shared__ float2 maps[WARPS][W], back[WARPS][W], fold[WARPS][W];
-  __shared__ float state[W];
+template <class T, int GATE>
+__global__ void __launch_bounds__(NT, 2)
+    k_scan_bwd(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmD,
+               const BwdArgs<T> p, const Lookback lb) {
+  constexpr int CH = BLOCK, SUB = BSUB, VEC = vec_of<T>(), W = 32 * VEC;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~(uintptr_t)127);
+  auto* sh = reinterpret_cast<Shared<CH, W>*>(ring + STAGES * 3 * CH * ROW);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    s_place = lb.chunks > 1 ? atomicAdd(lb.flags, 1) : (int)blockIdx.x;
-    s_bad = 0;
+    for (int q = 0; q < STAGES; ++q) {
+      mbar_init(&sh->full[q], 1);
+      mbar_init(&sh->empty[q], WARPS);
+    }
+    sh->bad = 0;
+    fence_mbar_init();
   }
   __syncthreads();
-  const int k = s_place / lb.tiles, tile = s_place % lb.tiles, chunk = lb.chunks - 1 - k;
-  const int t0 = chunk * CH + warp * SUB, f = tile * W + lane * VEC;
-  const bool on = f < p.D;
-  Pack<T, VEC> rg[SUB], rx[SUB], rd[SUB];
-#pragma unroll
-  for (int i = 0; i < SUB; ++i)
-    if (on && t0 + i < p.n) {
-      rg[i] = *reinterpret_cast<const Pack<T, VEC>*>(p.G + (size_t)(t0 + i) * p.ldg + f);
-      rx[i] = *reinterpret_cast<const Pack<T, VEC>*>(p.X + (size_t)(t0 + i) * p.ldx + f);
-      rd[i] = *reinterpret_cast<const Pack<T, VEC>*>(p.dH + (size_t)(t0 + i) * p.lddh + f);
+  if (warp == WARPS) {
+    const CUtensorMap* const tm[3] = {&tmG, &tmX, &tmD};
+    feed<T, CH, 3, W>(
+        lb, sh, ring, tm, p.tma, p.off, p.series, p.n,
+        [&](int place, int& tile, int& t0) {
+          tile = place % lb.tiles;
+          t0 = (lb.chunks - 1 - place / lb.tiles) * CH;
+        },
+        [&](int tile, int s) {
+          float q[VEC];
+          load_state<VEC>(p.dhT, p.lddhT, s, tile * W + lane * VEC, p.D, q);
+          store_state<VEC>(p.dh0, p.lddh0, s, tile * W + lane * VEC, p.D, q);
+        });
+    return;
+  }
+  for (int it = 0;; ++it) {
+    const int st = it % STAGES;
+    const int place = next_item(lb, sh, it);
+    if (place < 0) break;
+    const int k = place / lb.tiles, tile = place % lb.tiles, chunk = lb.chunks - 1 - k;
+    const int t0 = chunk * CH + warp * SUB, f = tile * W + lane * VEC;
+    uint8_t* in = ring + st * 3 * CH * ROW;
+    float h[VEC];
+    load_state<VEC>(p.saved, p.D, chunk, f, p.D, h);
+    if (!p.tma) {
+      copy_rows<T, W>(p.G, in, warp * SUB, SUB, tile * W, t0, p.D, p.n);
+      copy_rows<T, W>(p.X, in + CH * ROW, warp * SUB, SUB, tile * W, t0, p.D, p.n);
+      copy_rows<T, W>(p.dH, in + 2 * CH * ROW, warp * SUB, SUB, tile * W, t0, p.D, p.n);
+      __syncwarp();
     }
-  float h[VEC];
-  load_state<VEC>(p.saved, p.D, chunk, f, p.D, h);
-  mark_series(p.off, p.series, chunk * CH, CH, p.n, first, last, [&](int s) {
-    float q[VEC];
-    load_state<VEC>(p.dhT, p.lddhT, s, f, p.D, q);
-    store_state<VEC>(p.dh0, p.lddh0, s, f, p.D, q);
-  });
-  __syncthreads();
-  const uint32_t starts = __ballot_sync(0xffffffffu, lane < SUB && first[warp * SUB + (lane & (SUB - 1))] >= 0);
-  const uint32_t ends = __ballot_sync(0xffffffffu, lane < SUB && last[warp * SUB + (lane & (SUB - 1))] >= 0);
+    const int* first = sh->first[st] + warp * SUB;
+    const int* last = sh->last[st] + warp * SUB;
+    const uint32_t starts = __ballot_sync(0xffffffffu, lane < SUB && first[lane & (SUB - 1)] >= 0);
+    const uint32_t ends = __ballot_sync(0xffffffffu, lane < SUB && last[lane & (SUB - 1)] >= 0);
+    const uint8_t* row = in + warp * SUB * ROW + lane * 4;
 
-  float a[SUB][VEC], b[SUB][VEC], A[VEC], B[VEC], RA[VEC], RB[VEC];   // b: c x, then the state before the step
+    // b: c x, then the state before the step; r: what c and the slopes are made of
+    float a[SUB][VEC], r[SUB][VEC], b[SUB][VEC], A[VEC], B[VEC], RA[VEC], RB[VEC];
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) A[v] = RA[v] = 1.0f, B[v] = RB[v] = 0.0f;
+    for (int v = 0; v < VEC; ++v) A[v] = RA[v] = 1.0f, B[v] = RB[v] = 0.0f;
 #pragma unroll
-  for (int i = 0; i < SUB; ++i) {
-    if (starts >> i & 1u) {
-      load_state<VEC>(p.h0, p.ldh0, first[warp * SUB + i], f, p.D, B);
+    for (int i = 0; i < SUB; ++i) {
+      const auto g = *reinterpret_cast<const Pack<T, VEC>*>(row + i * ROW);
+      const auto x = *reinterpret_cast<const Pack<T, VEC>*>(row + CH * ROW + i * ROW);
+      if (starts >> i & 1u) {
+        load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, B);
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) A[v] = 0.0f;
-    }
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      const bool in = on && t0 + i < p.n;
-      const Gate g = gate_of<GATE>(in ? to_float(rg[i].x[v]) : 0.0f);
-      a[i][v] = in ? g.a : 1.0f;
-      b[i][v] = in ? __fmul_rn(g.c, to_float(rx[i].x[v])) : 0.0f;
-      A[v] *= a[i][v];
-      B[v] = fmaf(a[i][v], B[v], b[i][v]);
-    }
-  }
-#pragma unroll
-  for (int i = SUB - 1; i >= 0; --i) {
-    if (ends >> i & 1u) {
-      load_state<VEC>(p.dhT, p.lddhT, last[warp * SUB + i], f, p.D, RB);
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) RA[v] = 0.0f;
-    }
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      const float d = on && t0 + i < p.n ? to_float(rd[i].x[v]) : 0.0f;
-      RB[v] = __fmul_rn(a[i][v], __fadd_rn(d, RB[v]));
-      RA[v] *= a[i][v];
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) {
-    maps[warp][lane * VEC + v] = make_float2(A[v], B[v]);
-    back[warp][lane * VEC + v] = make_float2(RA[v], RB[v]);
-  }
-  __syncthreads();
-  float PA[VEC], PB[VEC];
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) {
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      const float2 m = maps[w][lane * VEC + v];
-      if (w < warp) h[v] = apply_map(m.x, m.y, h[v]);
-    }
-    RA[v] = PA[v] = 1.0f, RB[v] = PB[v] = 0.0f;
-#pragma unroll
-    for (int w = WARPS - 1; w >= 0; --w) {
-      const float2 m = back[w][lane * VEC + v];
-      forget_or(RA[v], RB[v], m.x, m.y);
-      if (w > warp) PA[v] = RA[v], PB[v] = RB[v];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < SUB; ++i) {
-    if (starts >> i & 1u) load_state<VEC>(p.h0, p.ldh0, first[warp * SUB + i], f, p.D, h);
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      const float next = fmaf(a[i][v], h[v], b[i][v]);
-      b[i][v] = h[v];
-      h[v] = next;
-    }
-  }
-  float r[VEC];
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) r[v] = 0.0f;
-  if (lb.chunks > 1 && !state_in<VEC>(lb, tile, k, f, p.D, RA, RB, fold, state, &s_bad, r)) return;
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) r[v] = apply_map(PA[v], PB[v], r[v]);
-#pragma unroll
-  for (int i = SUB - 1; i >= 0; --i) {
-    if (ends >> i & 1u) load_state<VEC>(p.dhT, p.lddhT, last[warp * SUB + i], f, p.D, r);
-    if (on && t0 + i < p.n) {
-      Pack<T, VEC> og, ox;
+        for (int v = 0; v < VEC; ++v) A[v] = 0.0f;
+      }
 #pragma unroll
       for (int v = 0; v < VEC; ++v) {
-        const float gl = to_float(rg[i].x[v]), x = to_float(rx[i].x[v]);
-        const Gate g = gate_of<GATE>(gl), sl = gate_slope<GATE>(gl);
-        const float q = __fadd_rn(to_float(rd[i].x[v]), r[v]);
-        ox.x[v] = from_float<T>(__fmul_rn(g.c, q));
-        og.x[v] = from_float<T>(__fmul_rn(q, fmaf(b[i][v], sl.a, __fmul_rn(x, sl.c))));
-        r[v] = __fmul_rn(a[i][v], q);
+        const GateParts c = gate_parts<GATE>(to_float(g.x[v]));
+        a[i][v] = c.a;
+        r[i][v] = c.rest;
+        b[i][v] = __fmul_rn(gate_input<GATE>(c), to_float(x.x[v]));
+        A[v] *= a[i][v];
+        B[v] = fmaf(a[i][v], B[v], b[i][v]);
       }
-      if (p.dX) *reinterpret_cast<Pack<T, VEC>*>(p.dX + (size_t)(t0 + i) * p.lddx + f) = ox;
-      if (p.dG) *reinterpret_cast<Pack<T, VEC>*>(p.dG + (size_t)(t0 + i) * p.lddg + f) = og;
     }
-    if (starts >> i & 1u) store_state<VEC>(p.dh0, p.lddh0, first[warp * SUB + i], f, p.D, r);
+#pragma unroll
+    for (int i = SUB - 1; i >= 0; --i) {
+      const auto d = *reinterpret_cast<const Pack<T, VEC>*>(row + 2 * CH * ROW + i * ROW);
+      if (ends >> i & 1u) {
+        load_state<VEC>(p.dhT, p.lddhT, last[i], f, p.D, RB);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) RA[v] = 0.0f;
+      }
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        RB[v] = __fmul_rn(a[i][v], __fadd_rn(to_float(d.x[v]), RB[v]));
+        RA[v] *= a[i][v];
+      }
+    }
+    // the states before each step: the maps of the earlier warps on the saved state
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) sh->maps[warp][lane * VEC + v] = make_float2(A[v], B[v]);
+    workers_sync();
+#pragma unroll
+    for (int v = 0; v < VEC; ++v)
+      for (int w = 0; w < warp; ++w) h[v] = apply_map(sh->maps[w][lane * VEC + v].x, sh->maps[w][lane * VEC + v].y, h[v]);
+    workers_sync();
+#pragma unroll
+    for (int i = 0; i < SUB; ++i) {
+      if (starts >> i & 1u) load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, h);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const float next = fmaf(a[i][v], h[v], b[i][v]);
+        b[i][v] = h[v];
+        h[v] = next;
+      }
+    }
+    if (!join<true, VEC, CH, W>(lb, sh, tile, k, p.D, RA, RB)) return;
+    float q[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) q[v] = sh->start[warp][lane * VEC + v];
+    const int steps = f < p.D ? p.n - t0 : 0;
+#pragma unroll
+    for (int i = SUB - 1; i >= 0; --i) {
+      const auto d = *reinterpret_cast<const Pack<T, VEC>*>(row + 2 * CH * ROW + i * ROW);
+      const auto x = *reinterpret_cast<const Pack<T, VEC>*>(row + CH * ROW + i * ROW);
+      if (ends >> i & 1u) load_state<VEC>(p.dhT, p.lddhT, last[i], f, p.D, q);
+      float dx[VEC], dg[VEC];
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) {
+        const GateParts c = {a[i][v], r[i][v]};
+        q[v] = __fadd_rn(to_float(d.x[v]), q[v]);
+        dx[v] = __fmul_rn(gate_input<GATE>(c), q[v]);
+        dg[v] = __fmul_rn(q[v], gate_slope<GATE>(c, b[i][v], to_float(x.x[v])));
+        q[v] = __fmul_rn(a[i][v], q[v]);
+      }
+      if (i < steps) {
+        if (p.dX) put<T, VEC>(p.dX, p.lddx, t0 + i, f, p.D, p.pairs, dx);
+        if (p.dG) put<T, VEC>(p.dG, p.lddg, t0 + i, f, p.D, p.pairs, dg);
+      }
+      if (starts >> i & 1u) store_state<VEC>(p.dh0, p.lddh0, first[i], f, p.D, q);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->empty[st]);
   }
 }
 
@@ -479,37 +628,49 @@ struct Scratch {
   void* mem = nullptr;
   cudaStream_t stream = nullptr;
   ~Scratch() { scratch_free(mem, stream); }
-  cr_status make(int T, int chunk, int tiles, int D, cudaStream_t s) {
+  cr_status make(int T, int chunk, int tiles, int w, cudaStream_t s) {
     CR_TRY(wait_word(&lb.err));
     lb.limit = option_wait_ns();
     lb.chunks = (int)(((long long)T + chunk - 1) / chunk);
     lb.tiles = tiles;
+    lb.width = tiles * w;
     // Groups: few hand-overs along the series against few maps to compose per chunk.
     lb.group = lb.chunks <= 256 ? 16 : lb.chunks <= 1024 ? 32 : MAXGROUP;
     if (lb.chunks <= 1) return CR_OK;
     const size_t groups = ((size_t)lb.chunks + lb.group - 1) / lb.group;
-    const size_t flags = (1 + (size_t)tiles * (lb.chunks + groups)) * sizeof(int), up = (flags + 255) / 256 * 256;
-    const size_t maps = (size_t)lb.chunks * D * sizeof(float2);
+    const size_t maps = (size_t)lb.chunks * lb.width, bytes = 256 + (maps + groups * lb.width) * sizeof(Word);
     stream = s;
-    CR_CUDA(scratch_alloc(&mem, up + maps + groups * D * sizeof(float), s));
-    lb.flags = (int*)mem;
-    lb.maps = (float2*)((char*)mem + up);
-    lb.states = (float*)((char*)mem + up + maps);
-    CR_CUDA(cudaMemsetAsync(mem, 0, flags, s));
+    CR_CUDA(scratch_alloc(&mem, bytes, s));
+    lb.counter = (int*)mem;
+    lb.maps = (Word*)((char*)mem + 256);
+    lb.states = lb.maps + maps;
+    CR_CUDA(cudaMemsetAsync(mem, 0, bytes, s));
     return CR_OK;
   }
 };
 
-// Two features per thread where every matrix allows accesses of two elements.
-struct Pairs {
-  size_t bytes;
-  bool ok;
-  Pairs(int D, size_t eb) : bytes(2 * eb), ok(D % 2 == 0) {}
-  Pairs& with(const void* p, int ld) {
-    if (p && ((uintptr_t)p % bytes || ld % 2)) ok = false;
-    return *this;
-  }
-};
+template <class T>
+bool tma_ok(const Input& in) { return ((uintptr_t)in.p & 15) == 0 && (long long)in.ld * (int)sizeof(T) % 16 == 0; }
+template <class T>
+bool vec_ok(const void* p, int ld, int D) {
+  return !p || ((uintptr_t)p % (vec_of<T>() * sizeof(T)) == 0 && ld % vec_of<T>() == 0 && D % vec_of<T>() == 0);
+}
+template <class T>
+constexpr int type_of() { return std::is_same<T, float>::value ? CR_TYPE_F32 : std::is_same<T, __half>::value ? CR_TYPE_F16 : CR_TYPE_BF16; }
+template <class T>
+cr_status map_in(CUtensorMap* tm, const Input& in, int D, int n, int steps) {
+  return make_tensor_map_2d_plain(tm, type_of<T>(), in.p, D, n, in.ld, ROW / (int)sizeof(T), steps);
+}
+
+int resident_blocks() {   // two per SM (registers and shared memory allow it)
+  static const int n = [] {
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return 2 * sms;
+  }();
+  return n;
+}
 
 cr_status states_only(const float* from, int ldf, float* to, int ldt, int D, int n, cudaStream_t stream) {
   if (!to || n == 0) return CR_OK;
@@ -519,31 +680,46 @@ cr_status states_only(const float* from, int ldf, float* to, int ldt, int D, int
 }
 
 template <class E, int GATE>
-cr_status forward(const FwdArgs<E>& p, cudaStream_t stream) {
-  const bool two = Pairs(p.D, sizeof(E)).with(p.G, p.ldg).with(p.X, p.ldx).with(p.H, p.ldh).ok;
-  const int w = two ? 64 : 32, tiles = (p.D + w - 1) / w;
+cr_status forward(FwdArgs<E> p, cudaStream_t stream) {
+  constexpr int CH = WARPS * FSUB, W = 32 * vec_of<E>(), SMEM = STAGES * 2 * CH * ROW + sizeof(Shared<CH, W>) + 128;
+  const int tiles = (p.D + W - 1) / W;
   Scratch sc;
-  CR_TRY(sc.make(p.n, WARPS * FSUB, tiles, p.D, stream));
-  const long long blocks = (long long)sc.lb.chunks * tiles;
-  CR_REQUIRE(blocks < INT_MAX, "cr_gated_scan: more than 2^31 blocks");
+  CR_TRY(sc.make(p.n, CH, tiles, W, stream));
+  CR_REQUIRE((long long)sc.lb.chunks * tiles < INT_MAX / 2, "cr_gated_scan: more than 2^30 work items");
+  static const cudaError_t set = cudaFuncSetAttribute(k_scan_fwd<E, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  CR_CUDA(set);
+  p.tma = tma_ok<E>(p.G) && tma_ok<E>(p.X);
+  p.pairs = vec_ok<E>(p.H, p.ldh, p.D);
+  CUtensorMap tmG = {}, tmX = {};
+  if (p.tma) {
+    CR_TRY(map_in<E>(&tmG, p.G, p.D, p.n, CH));
+    CR_TRY(map_in<E>(&tmX, p.X, p.D, p.n, CH));
+  }
   TimedScope ts("k_scan_fwd", stream);
-  if (two) k_scan_fwd<E, GATE, 2><<<(unsigned)blocks, NT, 0, stream>>>(p, sc.lb);
-  else k_scan_fwd<E, GATE, 1><<<(unsigned)blocks, NT, 0, stream>>>(p, sc.lb);
+  k_scan_fwd<E, GATE><<<std::min(resident_blocks(), sc.lb.chunks * tiles), NT, SMEM, stream>>>(tmG, tmX, p, sc.lb);
   CR_CHECK_LAUNCH("k_scan_fwd");
   return CR_OK;
 }
 
 template <class E, int GATE>
-cr_status backward(const BwdArgs<E>& p, cudaStream_t stream) {
-  const bool two = Pairs(p.D, sizeof(E)).with(p.G, p.ldg).with(p.X, p.ldx).with(p.dH, p.lddh).with(p.dG, p.lddg).with(p.dX, p.lddx).ok;
-  const int w = two ? 64 : 32, tiles = (p.D + w - 1) / w;
+cr_status backward(BwdArgs<E> p, cudaStream_t stream) {
+  constexpr int W = 32 * vec_of<E>(), SMEM = STAGES * 3 * BLOCK * ROW + sizeof(Shared<BLOCK, W>) + 128;
+  const int tiles = (p.D + W - 1) / W;
   Scratch sc;
-  CR_TRY(sc.make(p.n, BLOCK, tiles, p.D, stream));
-  const long long blocks = (long long)sc.lb.chunks * tiles;
-  CR_REQUIRE(blocks < INT_MAX, "cr_gated_scan_backward: more than 2^31 blocks");
+  CR_TRY(sc.make(p.n, BLOCK, tiles, W, stream));
+  CR_REQUIRE((long long)sc.lb.chunks * tiles < INT_MAX / 2, "cr_gated_scan_backward: more than 2^30 work items");
+  static const cudaError_t set = cudaFuncSetAttribute(k_scan_bwd<E, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  CR_CUDA(set);
+  p.tma = tma_ok<E>(p.G) && tma_ok<E>(p.X) && tma_ok<E>(p.dH);
+  p.pairs = vec_ok<E>(p.dG, p.lddg, p.D) && vec_ok<E>(p.dX, p.lddx, p.D);
+  CUtensorMap tmG = {}, tmX = {}, tmD = {};
+  if (p.tma) {
+    CR_TRY(map_in<E>(&tmG, p.G, p.D, p.n, BLOCK));
+    CR_TRY(map_in<E>(&tmX, p.X, p.D, p.n, BLOCK));
+    CR_TRY(map_in<E>(&tmD, p.dH, p.D, p.n, BLOCK));
+  }
   TimedScope ts("k_scan_bwd", stream);
-  if (two) k_scan_bwd<E, GATE, 2><<<(unsigned)blocks, NT, 0, stream>>>(p, sc.lb);
-  else k_scan_bwd<E, GATE, 1><<<(unsigned)blocks, NT, 0, stream>>>(p, sc.lb);
+  k_scan_bwd<E, GATE><<<std::min(resident_blocks(), sc.lb.chunks * tiles), NT, SMEM, stream>>>(tmG, tmX, tmD, p, sc.lb);
   CR_CHECK_LAUNCH("k_scan_bwd");
   return CR_OK;
 }
@@ -576,7 +752,7 @@ extern "C" cr_status cr_gated_scan(int type, int gate, const void* d_G, int ldg,
     using E = decltype(t0);
     return with_gate(gate, [&](auto g0) -> cr_status {
       return forward<E, decltype(g0)::value>(
-          FwdArgs<E>{(const E*)d_G, (const E*)d_X, ldg, ldx, D, T, d_off, n_seq, d_h0, ldh0, (E*)d_H, ldh, d_hT, ldhT, d_saved}, stream);
+          FwdArgs<E>{{d_G, ldg}, {d_X, ldx}, D, T, d_off, n_seq, d_h0, ldh0, (E*)d_H, ldh, d_hT, ldhT, d_saved, 0, 0}, stream);
     });
   });
   CR_ENTRY_END("cr_gated_scan")
@@ -615,8 +791,8 @@ extern "C" cr_status cr_gated_scan_backward(int type, int gate, const void* d_G,
     using E = decltype(t0);
     return with_gate(gate, [&](auto g0) -> cr_status {
       return backward<E, decltype(g0)::value>(
-          BwdArgs<E>{(const E*)d_G, (const E*)d_X, (const E*)d_dH, ldg, ldx, lddh, D, T, d_off, n_seq, d_h0, d_dhT, d_saved, ldh0, lddhT,
-                     (E*)d_dG, (E*)d_dX, lddg, lddx, d_dh0, lddh0}, stream);
+          BwdArgs<E>{{d_G, ldg}, {d_X, ldx}, {d_dH, lddh}, D, T, d_off, n_seq, d_h0, d_dhT, d_saved, ldh0, lddhT, (E*)d_dG,
+                     (E*)d_dX, lddg, lddx, d_dh0, lddh0, 0, 0}, stream);
     });
   });
   scratch_free(own, stream);
