@@ -127,45 +127,88 @@ cr_status with_act(int act, F&& f) {
 // ---------------------------------------------------------------- gates
 // h_t = a h_{t-1} + c x_t.  Products that feed a sum are written as fmaf or __fmul_rn, so that every
 // variant of a kernel rounds alike.
-struct GateParts {
-  float a, rest;   // sigmoid(g) and sigmoid(-g); coefficient gate: g and 1
+template <int VEC>
+struct alignas(4 * VEC) Floats {   // one float, or two in the halves of a register pair
+  float x[VEC];
 };
-// sigmoid(g) = 1 / (1 + e^-g) and sigmoid(-g) = e^-g / (1 + e^-g), which has no cancellation.  -g is kept
-// below 87 so that e^-g is finite (at 87 sigmoid(g) is 1e-38); NaN stays.  The hardware's 2^x and
-// reciprocal err by about 2^-22, and g log2(e) rounds to 2^-24 of itself: 2^-20 in all for |g| < 16.
-template <int GATE>
-__device__ __forceinline__ GateParts gate_parts(float g) {
-  if (GATE == CR_GATE_COEFF) return {g, 1.0f};
-  float m, e, r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(-g), "f"(87.0f));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(m * 1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-  return {r, e * r};
-}
-__device__ __forceinline__ float sqrt_fast(float x) {
-  float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+__device__ __forceinline__ uint64_t pair_of(const Floats<2>& v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x[0]), "f"(v.x[1]));
   return r;
 }
-template <int GATE>
-__device__ __forceinline__ float gate_input(const GateParts& p) {   // c; 1 - a^2 = rest (1 + a)
-  return GATE == CR_GATE_VARIANCE ? sqrt_fast(p.rest * (1.0f + p.a)) : p.rest;
+__device__ __forceinline__ Floats<2> floats_of(uint64_t p) {
+  Floats<2> v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x[0]), "=f"(v.x[1]) : "l"(p));
+  return v;
 }
-struct Gate {
-  float a, c;
+// Rounded to nearest, two at a time in one instruction.
+__device__ __forceinline__ Floats<1> mul(Floats<1> a, Floats<1> b) { return {{__fmul_rn(a.x[0], b.x[0])}}; }
+__device__ __forceinline__ Floats<1> add(Floats<1> a, Floats<1> b) { return {{__fadd_rn(a.x[0], b.x[0])}}; }
+__device__ __forceinline__ Floats<1> fma(Floats<1> a, Floats<1> b, Floats<1> c) { return {{fmaf(a.x[0], b.x[0], c.x[0])}}; }
+__device__ __forceinline__ Floats<2> mul(Floats<2> a, Floats<2> b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_of(a)), "l"(pair_of(b)));
+  return floats_of(r);
+}
+__device__ __forceinline__ Floats<2> add(Floats<2> a, Floats<2> b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_of(a)), "l"(pair_of(b)));
+  return floats_of(r);
+}
+__device__ __forceinline__ Floats<2> fma(Floats<2> a, Floats<2> b, Floats<2> c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair_of(a)), "l"(pair_of(b)), "l"(pair_of(c)));
+  return floats_of(r);
+}
+template <int VEC>
+__device__ __forceinline__ Floats<VEC> all_of(float x) {
+  Floats<VEC> v;
+#pragma unroll
+  for (int q = 0; q < VEC; ++q) v.x[q] = x;
+  return v;
+}
+
+template <int VEC>
+struct GateParts {
+  Floats<VEC> a, rest;   // sigmoid(g) and sigmoid(-g); coefficient gate: g and 1
 };
-template <int GATE>
-__device__ __forceinline__ Gate gate_of(float g) {
-  const GateParts p = gate_parts<GATE>(g);
-  return {p.a, gate_input<GATE>(p)};
+// sigmoid(g) = 1 / (1 + e^-g) and sigmoid(-g) = e^-g / (1 + e^-g), which has no cancellation.  e^-g is kept
+// below 2^125.5 so that it stays finite (sigmoid(g) is then 1e-38); NaN stays.  The hardware's 2^x
+// and reciprocal err by about 2^-22, and g log2(e) rounds to 2^-24 of itself: 2^-20 in all for |g| < 16.
+template <int GATE, int VEC>
+__device__ __forceinline__ GateParts<VEC> gate_parts(Floats<VEC> g) {
+  if (GATE == CR_GATE_COEFF) return {g, all_of<VEC>(1.0f)};
+  Floats<VEC> e = mul(g, all_of<VEC>(-1.4426950408889634f));
+#pragma unroll
+  for (int q = 0; q < VEC; ++q) {
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(e.x[q]) : "f"(125.5f));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x[q]));
+  }
+  Floats<VEC> r = add(e, all_of<VEC>(1.0f));
+#pragma unroll
+  for (int q = 0; q < VEC; ++q) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(r.x[q]));
+  return {r, mul(e, r)};
+}
+template <int VEC>
+__device__ __forceinline__ Floats<VEC> sqrt_of(Floats<VEC> v) {
+#pragma unroll
+  for (int q = 0; q < VEC; ++q) asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(v.x[q]));
+  return v;
+}
+template <int GATE, int VEC>
+__device__ __forceinline__ Floats<VEC> gate_input(const GateParts<VEC>& p) {   // c; 1 - a^2 = rest (1 + a)
+  return GATE == CR_GATE_VARIANCE ? sqrt_of(mul(p.rest, add(p.a, all_of<VEC>(1.0f)))) : p.rest;
 }
 // h' da/dg + x dc/dg.  Variance gate: dc/dg = -a (a rest) / c = -a^2 sqrt(rest / (1 + a)), finite at a = 1.
-template <int GATE>
-__device__ __forceinline__ float gate_slope(const GateParts& p, float before, float x) {
+template <int GATE, int VEC>
+__device__ __forceinline__ Floats<VEC> gate_slope(const GateParts<VEC>& p, Floats<VEC> before, Floats<VEC> x) {
   if (GATE == CR_GATE_COEFF) return before;
-  if (GATE == CR_GATE_CONVEX) return __fmul_rn(__fmul_rn(p.a, p.rest), __fadd_rn(before, -x));
-  const float s = sqrt_fast(__fdividef(p.rest, 1.0f + p.a));
-  return __fmul_rn(p.a, fmaf(before, p.rest, -__fmul_rn(__fmul_rn(x, p.a), s)));
+  const Floats<VEC> minus = all_of<VEC>(-1.0f);
+  if (GATE == CR_GATE_CONVEX) return mul(mul(p.a, p.rest), fma(x, minus, before));
+  Floats<VEC> s = add(p.a, all_of<VEC>(1.0f));
+#pragma unroll
+  for (int q = 0; q < VEC; ++q) s.x[q] = __fdividef(p.rest.x[q], s.x[q]);
+  return mul(p.a, fma(before, p.rest, mul(mul(mul(x, minus), p.a), sqrt_of(s))));
 }
 
 }  // namespace cr

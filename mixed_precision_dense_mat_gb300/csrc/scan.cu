@@ -15,8 +15,10 @@ namespace {
 // bytes of each column).  Resident blocks take items in order of time from a counter: whatever an
 // item waits for was taken earlier and is being worked on.  Warp 8 of a block takes the items and
 // loads them by TMA into a ring of stages, so that loads stay in flight while the other 8 warps
-// work; each of these owns SUB of the chunk's steps and each of its lanes VEC features, in
-// registers, so that the inputs are read once.
+// work; each of these owns SUB of the chunk's steps and each of its lanes VEC features.  They go over
+// the tile in shared memory twice, for its map and, once the state before it is known, for
+// the outputs, so that HBM is read once and few registers are held meanwhile: three blocks fit
+// on an SM, which covers the time that a block waits for its predecessors.
 // The map of a run of steps on the state is h -> A h + B, and such maps compose; "start from
 // h0" is the map A = 0, B = h0, so that packed series need no other care (A = 0 is taken as "forget",
 // not multiplied, so that nothing crosses into the next series).  Warps join their maps in
@@ -26,7 +28,7 @@ namespace {
 constexpr int WARPS = 8, NT = 32 * (WARPS + 1);
 constexpr int FSUB = 16, BSUB = 8;        // steps per warp, forward and backward
 constexpr int BLOCK = WARPS * BSUB;       // steps between saved states: a chunk of the backward pass
-constexpr int STAGES = 3;
+constexpr int STAGES = 2;
 constexpr int MAXGROUP = 64;
 constexpr int ROW = 128;                  // bytes of a column in a tile
 template <class T>
@@ -137,15 +139,15 @@ __device__ __forceinline__ void mark_series(const int32_t* off, int n, int t0, i
 
 // The features' h0 (or its gradient's seed) of series s.
 template <int VEC>
-__device__ __forceinline__ void load_state(const float* h0, int ld, int s, int f, int D, float (&h)[VEC]) {
+__device__ __forceinline__ void load_state(const float* h0, int ld, int s, int f, int D, Floats<VEC>& h) {
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) h[v] = h0 && f + v < D ? h0[(size_t)s * ld + f + v] : 0.0f;
+  for (int v = 0; v < VEC; ++v) h.x[v] = h0 && f + v < D ? h0[(size_t)s * ld + f + v] : 0.0f;
 }
 template <int VEC>
-__device__ __forceinline__ void store_state(float* hT, int ld, int s, int f, int D, const float (&h)[VEC]) {
+__device__ __forceinline__ void store_state(float* hT, int ld, int s, int f, int D, const Floats<VEC>& h) {
 #pragma unroll
   for (int v = 0; v < VEC; ++v)
-    if (hT && f + v < D) hT[(size_t)s * ld + f + v] = h[v];
+    if (hT && f + v < D) hT[(size_t)s * ld + f + v] = h.x[v];
 }
 
 __device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -156,8 +158,7 @@ struct Shared {
   uint64_t full[STAGES], empty[STAGES];
   int place[STAGES];
   int first[STAGES][CH], last[STAGES][CH];
-  float2 maps[WARPS][W], fold[WARPS][W];
-  float start[WARPS][W], state[W];
+  float2 maps[WARPS][W], fold[WARPS][W];   // fold[.].x: then the states that enter the warps
   int bad;
 };
 
@@ -175,10 +176,10 @@ __device__ __forceinline__ void feed(const Lookback& lb, Shared<CH, W>* sh, uint
   int it = 0;
   for (;; ++it) {
     const int st = it % STAGES;
-    if (!mbar_wait(&sh->empty[st], ((uint32_t)(it / STAGES) & 1u) ^ 1u, lb.limit) || *(volatile int*)&sh->bad) break;
-    int place = 0;
+    int place = 0;   // taken before the stage is free
     if (lane == 0) place = lb.chunks > 1 ? atomicAdd(lb.counter, 1) : (int)blockIdx.x + it * (int)gridDim.x;
     place = __shfl_sync(0xffffffffu, place, 0);
+    if (!mbar_wait(&sh->empty[st], ((uint32_t)(it / STAGES) & 1u) ^ 1u, lb.limit) || *(volatile int*)&sh->bad) break;
     if (place >= total) {
       if (lane == 0) {
         sh->place[st] = -1;
@@ -233,13 +234,13 @@ __device__ __forceinline__ int next_item(const Lookback& lb, S* sh, int it) {
 }
 
 // Joins the workers' maps (A, B) of a chunk (position k in the order of work): the state that enters the
-// part of each warp, in sh->start.  Warps compose in the order 0 .. 7, or 7 .. 0 with REVERSE.  All
+// part of each warp, in sh->fold[warp][feature].x.  Warps compose in the order 0 .. 7, or 7 .. 0 with REVERSE.  All
 // workers call it; false when a wait ran out.
 template <bool REVERSE, int VEC, int CH, int W>
-__device__ __forceinline__ bool join(const Lookback& lb, Shared<CH, W>* sh, int tile, int k, int D, const float (&A)[VEC], const float (&B)[VEC]) {
+__device__ __forceinline__ bool join(const Lookback& lb, Shared<CH, W>* sh, int tile, int k, int D, const Floats<VEC>& A, const Floats<VEC>& B) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) sh->maps[warp][lane * VEC + v] = make_float2(A[v], B[v]);
+  for (int v = 0; v < VEC; ++v) sh->maps[warp][lane * VEC + v] = make_float2(A.x[v], B.x[v]);
   workers_sync();
   const int g = k / lb.group, in = k % lb.group, c0 = g * lb.group;
   const bool more = k + 1 < lb.chunks, lastin = in == lb.group - 1;
@@ -291,7 +292,7 @@ __device__ __forceinline__ bool join(const Lookback& lb, Shared<CH, W>* sh, int 
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
       const int u = REVERSE ? WARPS - 1 - w : w;
-      sh->start[u][x] = h;
+      sh->fold[u][x].x = h;
       h = apply_map(sh->maps[u][x].x, sh->maps[u][x].y, h);
     }
   }
@@ -315,25 +316,35 @@ struct FwdArgs {
   int tma, pairs;   // inputs by TMA; H takes accesses of VEC elements
 };
 
+// VEC consecutive elements in FP32.
 template <class T, int VEC>
-__device__ __forceinline__ void put(T* out, int ld, int t, int f, int D, bool vec, const float (&v)[VEC]) {
+__device__ __forceinline__ Floats<VEC> widened(const uint8_t* at) {
+  const auto w = *reinterpret_cast<const Pack<T, VEC>*>(at);
+  Floats<VEC> v;
+#pragma unroll
+  for (int q = 0; q < VEC; ++q) v.x[q] = to_float(w.x[q]);
+  return v;
+}
+
+template <class T, int VEC>
+__device__ __forceinline__ void put(T* out, int ld, int t, int f, int D, bool vec, const Floats<VEC>& v) {
   T* o = out + (size_t)t * ld + f;
   if (vec) {
     Pack<T, VEC> w;
 #pragma unroll
-    for (int q = 0; q < VEC; ++q) w.x[q] = from_float<T>(v[q]);
+    for (int q = 0; q < VEC; ++q) w.x[q] = from_float<T>(v.x[q]);
     *reinterpret_cast<Pack<T, VEC>*>(o) = w;
   } else {
 #pragma unroll
     for (int q = 0; q < VEC; ++q)
-      if (f + q < D) o[q] = from_float<T>(v[q]);
+      if (f + q < D) o[q] = from_float<T>(v.x[q]);
   }
 }
 
 // Forward scan.  Bound by HBM (G and X read, H written).  Steps past the end and features past D hold
 // zeros: their states are never used.
 template <class T, int GATE>
-__global__ void __launch_bounds__(NT, 2)
+__global__ void __launch_bounds__(NT, 3)
     k_scan_fwd(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmX, const FwdArgs<T> p, const Lookback lb) {
   constexpr int CH = WARPS * FSUB, VEC = vec_of<T>(), W = 32 * VEC;
   extern __shared__ uint8_t smem_raw[];
@@ -358,7 +369,7 @@ __global__ void __launch_bounds__(NT, 2)
           t0 = place / lb.tiles * CH;
         },
         [&](int tile, int s) {
-          float h[VEC];
+          Floats<VEC> h;
           load_state<VEC>(p.h0, p.ldh0, s, tile * W + lane * VEC, p.D, h);
           store_state<VEC>(p.hT, p.ldhT, s, tile * W + lane * VEC, p.D, h);
         });
@@ -381,55 +392,47 @@ __global__ void __launch_bounds__(NT, 2)
     const uint32_t ends = __ballot_sync(0xffffffffu, lane < FSUB && last[lane & (FSUB - 1)] >= 0);
     const uint8_t* row = in + warp * FSUB * ROW + lane * 4;
 
-    float a[FSUB][VEC], b[FSUB][VEC], A[VEC], B[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) A[v] = 1.0f, B[v] = 0.0f;
+    const auto step = [&](int i, Floats<VEC>& a, Floats<VEC>& b) {   // h -> a h + b
+      const auto c = gate_parts<GATE>(widened<T, VEC>(row + i * ROW));
+      a = c.a;
+      b = mul(gate_input<GATE>(c), widened<T, VEC>(row + CH * ROW + i * ROW));
+    };
+    Floats<VEC> A = all_of<VEC>(1.0f), B = all_of<VEC>(0.0f), a, b;
 #pragma unroll
     for (int i = 0; i < FSUB; ++i) {
-      const auto g = *reinterpret_cast<const Pack<T, VEC>*>(row + i * ROW);
-      const auto x = *reinterpret_cast<const Pack<T, VEC>*>(row + CH * ROW + i * ROW);
       if (starts >> i & 1u) {
+        A = all_of<VEC>(0.0f);
         load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, B);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) A[v] = 0.0f;
       }
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const Gate c = gate_of<GATE>(to_float(g.x[v]));
-        a[i][v] = c.a;
-        b[i][v] = __fmul_rn(c.c, to_float(x.x[v]));
-        A[v] *= a[i][v];
-        B[v] = fmaf(a[i][v], B[v], b[i][v]);
-      }
+      step(i, a, b);
+      A = mul(A, a);
+      B = fma(a, B, b);
     }
     if (!join<false, VEC, CH, W>(lb, sh, tile, k, p.D, A, B)) return;
-    float h[VEC];
+    Floats<VEC> h;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) h[v] = sh->start[warp][lane * VEC + v];
+    for (int v = 0; v < VEC; ++v) h.x[v] = sh->fold[warp][lane * VEC + v].x;
     if (p.saved && warp * FSUB % BLOCK == 0 && t0 < p.n) store_state<VEC>(p.saved, p.D, t0 / BLOCK, f, p.D, h);
-    const int steps = f < p.D ? p.n - t0 : 0;
     if (!(starts | ends) && p.H && p.pairs && p.n - t0 >= FSUB) {   // inside a series
-      T* o = p.H + (size_t)t0 * p.ldh + f;
+      if (f < p.D) {
+        T* o = p.H + (size_t)t0 * p.ldh + f;
 #pragma unroll
-      for (int i = 0; i < FSUB; ++i) {
-        Pack<T, VEC> w;
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          h[v] = fmaf(a[i][v], h[v], b[i][v]);
-          w.x[v] = from_float<T>(h[v]);
+        for (int i = 0; i < FSUB; ++i, o += p.ldh) {
+          step(i, a, b);
+          h = fma(a, h, b);
+          put<T, VEC>(o, 0, 0, 0, VEC, true, h);
         }
-        if (f < p.D) *reinterpret_cast<Pack<T, VEC>*>(o) = w;
-        o += p.ldh;
       }
     } else {
+      const int steps = f < p.D ? p.n - t0 : 0;
 #pragma unroll
-    for (int i = 0; i < FSUB; ++i) {
-      if (starts >> i & 1u) load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, h);
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) h[v] = fmaf(a[i][v], h[v], b[i][v]);
-      if (p.H && i < steps) put<T, VEC>(p.H, p.ldh, t0 + i, f, p.D, p.pairs, h);
-      if (ends >> i & 1u) store_state<VEC>(p.hT, p.ldhT, last[i], f, p.D, h);
-    }
+      for (int i = 0; i < FSUB; ++i) {
+        if (starts >> i & 1u) load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, h);
+        step(i, a, b);
+        h = fma(a, h, b);
+        if (p.H && i < steps) put<T, VEC>(p.H, p.ldh, t0 + i, f, p.D, p.pairs, h);
+        if (ends >> i & 1u) store_state<VEC>(p.hT, p.ldhT, last[i], f, p.D, h);
+      }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh->empty[st]);
@@ -455,7 +458,7 @@ struct BwdArgs {
 // a series' last step.  The states inside a chunk are recomputed from the saved one before
 // it, which reads G and X (needed anyway) in place of H.  Bound by HBM (G, X, dH read, dG, dX written).
 template <class T, int GATE>
-__global__ void __launch_bounds__(NT, 2)
+__global__ void __launch_bounds__(NT, 3)
     k_scan_bwd(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmD,
                const BwdArgs<T> p, const Lookback lb) {
   constexpr int CH = BLOCK, SUB = BSUB, VEC = vec_of<T>(), W = 32 * VEC;
@@ -481,7 +484,7 @@ __global__ void __launch_bounds__(NT, 2)
           t0 = (lb.chunks - 1 - place / lb.tiles) * CH;
         },
         [&](int tile, int s) {
-          float q[VEC];
+          Floats<VEC> q;
           load_state<VEC>(p.dhT, p.lddhT, s, tile * W + lane * VEC, p.D, q);
           store_state<VEC>(p.dh0, p.lddh0, s, tile * W + lane * VEC, p.D, q);
         });
@@ -494,7 +497,7 @@ __global__ void __launch_bounds__(NT, 2)
     const int k = place / lb.tiles, tile = place % lb.tiles, chunk = lb.chunks - 1 - k;
     const int t0 = chunk * CH + warp * SUB, f = tile * W + lane * VEC;
     uint8_t* in = ring + st * 3 * CH * ROW;
-    float h[VEC];
+    Floats<VEC> h;
     load_state<VEC>(p.saved, p.D, chunk, f, p.D, h);
     if (!p.tma) {
       copy_rows<T, W>(p.G, in, warp * SUB, SUB, tile * W, t0, p.D, p.n);
@@ -508,85 +511,82 @@ __global__ void __launch_bounds__(NT, 2)
     const uint32_t ends = __ballot_sync(0xffffffffu, lane < SUB && last[lane & (SUB - 1)] >= 0);
     const uint8_t* row = in + warp * SUB * ROW + lane * 4;
 
-    // b: c x, then the state before the step; r: what c and the slopes are made of
-    float a[SUB][VEC], r[SUB][VEC], b[SUB][VEC], A[VEC], B[VEC], RA[VEC], RB[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) A[v] = RA[v] = 1.0f, B[v] = RB[v] = 0.0f;
+    // b: c x, then the state before the step
+    Floats<VEC> a[SUB], b[SUB], A = all_of<VEC>(1.0f), B = all_of<VEC>(0.0f), RA = A, RB = B;
 #pragma unroll
     for (int i = 0; i < SUB; ++i) {
-      const auto g = *reinterpret_cast<const Pack<T, VEC>*>(row + i * ROW);
-      const auto x = *reinterpret_cast<const Pack<T, VEC>*>(row + CH * ROW + i * ROW);
       if (starts >> i & 1u) {
+        A = all_of<VEC>(0.0f);
         load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, B);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) A[v] = 0.0f;
       }
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const GateParts c = gate_parts<GATE>(to_float(g.x[v]));
-        a[i][v] = c.a;
-        r[i][v] = c.rest;
-        b[i][v] = __fmul_rn(gate_input<GATE>(c), to_float(x.x[v]));
-        A[v] *= a[i][v];
-        B[v] = fmaf(a[i][v], B[v], b[i][v]);
-      }
+      const auto c = gate_parts<GATE>(widened<T, VEC>(row + i * ROW));
+      a[i] = c.a;
+      b[i] = mul(gate_input<GATE>(c), widened<T, VEC>(row + CH * ROW + i * ROW));
+      A = mul(A, a[i]);
+      B = fma(a[i], B, b[i]);
     }
 #pragma unroll
     for (int i = SUB - 1; i >= 0; --i) {
-      const auto d = *reinterpret_cast<const Pack<T, VEC>*>(row + 2 * CH * ROW + i * ROW);
       if (ends >> i & 1u) {
+        RA = all_of<VEC>(0.0f);
         load_state<VEC>(p.dhT, p.lddhT, last[i], f, p.D, RB);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) RA[v] = 0.0f;
       }
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        RB[v] = __fmul_rn(a[i][v], __fadd_rn(to_float(d.x[v]), RB[v]));
-        RA[v] *= a[i][v];
-      }
+      RB = mul(a[i], add(widened<T, VEC>(row + 2 * CH * ROW + i * ROW), RB));
+      RA = mul(RA, a[i]);
     }
     // the states before each step: the maps of the earlier warps on the saved state
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) sh->maps[warp][lane * VEC + v] = make_float2(A[v], B[v]);
+    for (int v = 0; v < VEC; ++v) sh->maps[warp][lane * VEC + v] = make_float2(A.x[v], B.x[v]);
     workers_sync();
 #pragma unroll
-    for (int v = 0; v < VEC; ++v)
-      for (int w = 0; w < warp; ++w) h[v] = apply_map(sh->maps[w][lane * VEC + v].x, sh->maps[w][lane * VEC + v].y, h[v]);
+    for (int w = 0; w < WARPS - 1; ++w)
+      if (w < warp) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) h.x[v] = apply_map(sh->maps[w][lane * VEC + v].x, sh->maps[w][lane * VEC + v].y, h.x[v]);
+      }
     workers_sync();
 #pragma unroll
     for (int i = 0; i < SUB; ++i) {
       if (starts >> i & 1u) load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, h);
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const float next = fmaf(a[i][v], h[v], b[i][v]);
-        b[i][v] = h[v];
-        h[v] = next;
-      }
+      const Floats<VEC> next = fma(a[i], h, b[i]);
+      b[i] = h;
+      h = next;
     }
     if (!join<true, VEC, CH, W>(lb, sh, tile, k, p.D, RA, RB)) return;
-    float q[VEC];
+    Floats<VEC> q;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) q[v] = sh->start[warp][lane * VEC + v];
-    const int steps = f < p.D ? p.n - t0 : 0;
+    for (int v = 0; v < VEC; ++v) q.x[v] = sh->fold[warp][lane * VEC + v].x;
+    const auto step = [&](int i, Floats<VEC>& dx, Floats<VEC>& dg) {   // gradients of step i; q passes on
+      const auto c = gate_parts<GATE>(widened<T, VEC>(row + i * ROW));
+      q = add(widened<T, VEC>(row + 2 * CH * ROW + i * ROW), q);
+      dx = mul(gate_input<GATE>(c), q);
+      dg = mul(q, gate_slope<GATE>(c, b[i], widened<T, VEC>(row + CH * ROW + i * ROW)));
+      q = mul(a[i], q);
+    };
+    Floats<VEC> dx, dg;
+    if (!(starts | ends) && p.dX && p.dG && p.pairs && p.n - t0 >= SUB) {   // inside a series
+      if (f < p.D) {
+        T* ox = p.dX + (size_t)(t0 + SUB - 1) * p.lddx + f;
+        T* og = p.dG + (size_t)(t0 + SUB - 1) * p.lddg + f;
 #pragma unroll
-    for (int i = SUB - 1; i >= 0; --i) {
-      const auto d = *reinterpret_cast<const Pack<T, VEC>*>(row + 2 * CH * ROW + i * ROW);
-      const auto x = *reinterpret_cast<const Pack<T, VEC>*>(row + CH * ROW + i * ROW);
-      if (ends >> i & 1u) load_state<VEC>(p.dhT, p.lddhT, last[i], f, p.D, q);
-      float dx[VEC], dg[VEC];
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const GateParts c = {a[i][v], r[i][v]};
-        q[v] = __fadd_rn(to_float(d.x[v]), q[v]);
-        dx[v] = __fmul_rn(gate_input<GATE>(c), q[v]);
-        dg[v] = __fmul_rn(q[v], gate_slope<GATE>(c, b[i][v], to_float(x.x[v])));
-        q[v] = __fmul_rn(a[i][v], q[v]);
+        for (int i = SUB - 1; i >= 0; --i, ox -= p.lddx, og -= p.lddg) {
+          step(i, dx, dg);
+          put<T, VEC>(ox, 0, 0, 0, VEC, true, dx);
+          put<T, VEC>(og, 0, 0, 0, VEC, true, dg);
+        }
       }
-      if (i < steps) {
-        if (p.dX) put<T, VEC>(p.dX, p.lddx, t0 + i, f, p.D, p.pairs, dx);
-        if (p.dG) put<T, VEC>(p.dG, p.lddg, t0 + i, f, p.D, p.pairs, dg);
+    } else {
+      const int steps = f < p.D ? p.n - t0 : 0;
+#pragma unroll
+      for (int i = SUB - 1; i >= 0; --i) {
+        if (ends >> i & 1u) load_state<VEC>(p.dhT, p.lddhT, last[i], f, p.D, q);
+        step(i, dx, dg);
+        if (i < steps) {
+          if (p.dX) put<T, VEC>(p.dX, p.lddx, t0 + i, f, p.D, p.pairs, dx);
+          if (p.dG) put<T, VEC>(p.dG, p.lddg, t0 + i, f, p.D, p.pairs, dg);
+        }
+        if (starts >> i & 1u) store_state<VEC>(p.dh0, p.lddh0, first[i], f, p.D, q);
       }
-      if (starts >> i & 1u) store_state<VEC>(p.dh0, p.lddh0, first[i], f, p.D, q);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh->empty[st]);
@@ -605,8 +605,8 @@ __global__ void __launch_bounds__(NT) k_scan_step(const T* G, int ldg, const T* 
   const int d = blockIdx.x * NT + threadIdx.x;
   if (d >= D) return;
   const size_t b = blockIdx.y;
-  const Gate g = gate_of<GATE>(to_float(G[b * ldg + d]));
-  const float v = fmaf(g.a, h[b * ldh + d], __fmul_rn(g.c, to_float(X[b * ldx + d])));
+  const auto g = gate_parts<GATE>(Floats<1>{{to_float(G[b * ldg + d])}});
+  const float v = fmaf(g.a.x[0], h[b * ldh + d], __fmul_rn(gate_input<GATE>(g).x[0], to_float(X[b * ldx + d])));
   hn[b * ldn + d] = v;
   if (H) H[b * ldo + d] = from_float<T>(v);
 }
@@ -662,12 +662,12 @@ cr_status map_in(CUtensorMap* tm, const Input& in, int D, int n, int steps) {
   return make_tensor_map_2d_plain(tm, type_of<T>(), in.p, D, n, in.ld, ROW / (int)sizeof(T), steps);
 }
 
-int resident_blocks() {   // two per SM (registers and shared memory allow it)
+int resident_blocks() {   // three per SM (registers and shared memory allow it)
   static const int n = [] {
     int dev = 0, sms = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return 2 * sms;
+    return 3 * sms;
   }();
   return n;
 }
