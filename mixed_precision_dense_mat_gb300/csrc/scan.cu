@@ -34,11 +34,6 @@ constexpr int ROW = 128;                  // bytes of a column in a tile
 template <class T>
 constexpr int vec_of() { return 4 / (int)sizeof(T); }
 
-template <class T, int VEC>
-struct alignas(sizeof(T) * VEC) Pack {
-  T x[VEC];
-};
-
 // What chunks tell each other, cleared before the call.  Every entry is one 64-bit word, written
 // and read whole, that is 0 until it is there, so that no fence stands between data and flag: a
 // map is A in the low half, with +0 written as -0, and B in the high one; a state has 1 in the low half.
@@ -318,22 +313,32 @@ struct FwdArgs {
 
 // VEC consecutive elements in FP32.
 template <class T, int VEC>
-__device__ __forceinline__ Floats<VEC> widened(const uint8_t* at) {
-  const auto w = *reinterpret_cast<const Pack<T, VEC>*>(at);
-  Floats<VEC> v;
-#pragma unroll
-  for (int q = 0; q < VEC; ++q) v.x[q] = to_float(w.x[q]);
-  return v;
+__device__ __forceinline__ Floats<VEC> widened(const uint8_t* at);
+template <>
+__device__ __forceinline__ Floats<1> widened<float, 1>(const uint8_t* at) { return {{*reinterpret_cast<const float*>(at)}}; }
+template <>
+__device__ __forceinline__ Floats<2> widened<__half, 2>(const uint8_t* at) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(at));
+  return {{f.x, f.y}};
+}
+template <>
+__device__ __forceinline__ Floats<2> widened<__nv_bfloat16, 2>(const uint8_t* at) {   // BF16 is the upper half of FP32
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(at);
+  return {{__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)}};
+}
+__device__ __forceinline__ void put_all(float* o, const Floats<1>& v) { *o = v.x[0]; }
+__device__ __forceinline__ void put_all(__half* o, const Floats<2>& v) {
+  *reinterpret_cast<__half2*>(o) = __floats2half2_rn(v.x[0], v.x[1]);
+}
+__device__ __forceinline__ void put_all(__nv_bfloat16* o, const Floats<2>& v) {
+  *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(v.x[0], v.x[1]);
 }
 
 template <class T, int VEC>
 __device__ __forceinline__ void put(T* out, int ld, int t, int f, int D, bool vec, const Floats<VEC>& v) {
   T* o = out + (size_t)t * ld + f;
   if (vec) {
-    Pack<T, VEC> w;
-#pragma unroll
-    for (int q = 0; q < VEC; ++q) w.x[q] = from_float<T>(v.x[q]);
-    *reinterpret_cast<Pack<T, VEC>*>(o) = w;
+    put_all(o, v);
   } else {
 #pragma unroll
     for (int q = 0; q < VEC; ++q)
@@ -398,15 +403,24 @@ __global__ void __launch_bounds__(NT, 3)
       b = mul(gate_input<GATE>(c), widened<T, VEC>(row + CH * ROW + i * ROW));
     };
     Floats<VEC> A = all_of<VEC>(1.0f), B = all_of<VEC>(0.0f), a, b;
+    if (!starts) {   // without branches, so that steps overlap
 #pragma unroll
-    for (int i = 0; i < FSUB; ++i) {
-      if (starts >> i & 1u) {
-        A = all_of<VEC>(0.0f);
-        load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, B);
+      for (int i = 0; i < FSUB; ++i) {
+        step(i, a, b);
+        A = mul(A, a);
+        B = fma(a, B, b);
       }
-      step(i, a, b);
-      A = mul(A, a);
-      B = fma(a, B, b);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < FSUB; ++i) {
+        if (starts >> i & 1u) {
+          A = all_of<VEC>(0.0f);
+          load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, B);
+        }
+        step(i, a, b);
+        A = mul(A, a);
+        B = fma(a, B, b);
+      }
     }
     if (!join<false, VEC, CH, W>(lb, sh, tile, k, p.D, A, B)) return;
     Floats<VEC> h;
@@ -420,12 +434,12 @@ __global__ void __launch_bounds__(NT, 3)
         for (int i = 0; i < FSUB; ++i, o += p.ldh) {
           step(i, a, b);
           h = fma(a, h, b);
-          put<T, VEC>(o, 0, 0, 0, VEC, true, h);
+          put_all(o, h);
         }
       }
     } else {
       const int steps = f < p.D ? p.n - t0 : 0;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < FSUB; ++i) {
         if (starts >> i & 1u) load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, h);
         step(i, a, b);
@@ -571,8 +585,8 @@ __global__ void __launch_bounds__(NT, 3)
 #pragma unroll
         for (int i = SUB - 1; i >= 0; --i, ox -= p.lddx, og -= p.lddg) {
           step(i, dx, dg);
-          put<T, VEC>(ox, 0, 0, 0, VEC, true, dx);
-          put<T, VEC>(og, 0, 0, 0, VEC, true, dg);
+          put_all(ox, dx);
+          put_all(og, dg);
         }
       }
     } else {
