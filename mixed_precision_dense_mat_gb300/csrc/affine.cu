@@ -622,25 +622,70 @@ __global__ void __launch_bounds__(NT) k_pack(const E* src, int lds, int n, int m
     for (int i = blockIdx.x * NT + threadIdx.x; i < n; i += gridDim.x * NT) dst[(size_t)c * ld + i] = src[(size_t)c * lds + i];
 }
 
-// G = dY .* act'(Z), and the row sums of its unrounded values; one block per 32 features.
-template <class E, int ACT>
-__global__ void __launch_bounds__(NT) k_affine_g(const E* dY, int lddy, const E* Z, int ldz, int N, int M, E* G, int ldg, float* db) {
-  __shared__ float red[NT / 32][32];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
-  float s = 0.0f;
-  if (i < N)
-    for (int j = w; j < M; j += NT / 32) {
-      float g = to_float(dY[(size_t)j * lddy + i]);
-      if (ACT != CR_ACT_NONE) g = __fmul_rn(g, activation_slope<ACT>(to_float(Z[(size_t)j * ldz + i])));
-      s += g;
-      if (G) G[(size_t)j * ldg + i] = from_float<E>(g);
+// G = dY .* act'(Z), and the row sums of its unrounded values: a block takes 32 V features and every
+// gridDim.y-th 8 columns, a thread V features of a column (V = 8: 16-byte accesses), and leaves its sums
+// in part[blockIdx.y][N].  Bound by HBM (dY and Z read, G written).
+template <class E, int ACT, int V>
+__global__ void __launch_bounds__(NT) k_affine_g(const E* dY, int lddy, const E* Z, int ldz, int N, int M, E* G, int ldg, float* part) {
+  struct alignas(sizeof(E) * V) Raw {
+    E x[V];
+  };
+  __shared__ float red[NT / 32][32 * V + V];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, i = (blockIdx.x * 32 + lane) * V;
+  float s[V] = {};
+  if (i < N) {
+#pragma unroll 4
+    for (int j = blockIdx.y * (NT / 32) + w; j < M; j += gridDim.y * (NT / 32)) {
+      const Raw d = *reinterpret_cast<const Raw*>(dY + (size_t)j * lddy + i);
+      Raw z = {};
+      if (ACT != CR_ACT_NONE) z = *reinterpret_cast<const Raw*>(Z + (size_t)j * ldz + i);
+      Raw o;
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        float g = to_float(d.x[q]);
+        if (ACT != CR_ACT_NONE) g = __fmul_rn(g, activation_slope<ACT>(to_float(z.x[q])));
+        s[q] += g;
+        o.x[q] = from_float<E>(g);
+      }
+      if (G) *reinterpret_cast<Raw*>(G + (size_t)j * ldg + i) = o;
     }
-  red[w][lane] = s;
-  __syncthreads();
-  if (w == 0 && i < N && db) {
-    for (int v = 1; v < NT / 32; ++v) s += red[v][lane];
-    db[i] = s;
   }
+  if (!part) return;
+#pragma unroll
+  for (int q = 0; q < V; ++q) red[w][lane * V + q] = s[q];
+  __syncthreads();
+  for (int x = threadIdx.x; x < 32 * V; x += NT) {
+    const int f = blockIdx.x * 32 * V + x;
+    float t = red[0][x];
+    for (int y = 1; y < NT / 32; ++y) t += red[y][x];
+    if (f < N) part[(size_t)blockIdx.y * N + f] = t;
+  }
+}
+
+int sm_count() {
+  static const int n = [] {
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+  }();
+  return n;
+}
+
+template <class E, int V>
+cr_status gradient_at_z(const E* dY, int lddy, const E* Z, int ldz, int N, int M, int act, E* G, int ldg, float* db, cudaStream_t stream) {
+  const int bx = (N + 32 * V - 1) / (32 * V), by = std::max(1, std::min({(M + 7) / 8, 4 * sm_count() / bx, 65535}));
+  float* part = nullptr;
+  if (db) CR_CUDA(scratch_alloc((void**)&part, (size_t)by * N * sizeof(float), stream));
+  cr_status st = with_act(act, [&](auto a0) -> cr_status {
+    TimedScope ts("k_affine_g", stream);
+    k_affine_g<E, decltype(a0)::value, V><<<dim3(bx, by), NT, 0, stream>>>(dY, lddy, Z, ldz, N, M, G, ldg, part);
+    CR_CHECK_LAUNCH("k_affine_g");
+    return CR_OK;
+  });
+  if (st == CR_OK && db) st = add_rows(part, by, N, db, stream);
+  scratch_free(part, stream);
+  return st;
 }
 
 // An operand as TMA can read it: a 16-byte aligned base and leading dimension, copied into
@@ -669,16 +714,6 @@ struct Packed {
 cr_status map_of(CUtensorMap* tm, const Operand& o, int type, int K, int rows_per_box) {
   if (o.k_major) return make_tensor_map_2d(tm, type, o.ptr, K, o.rows, o.ld, KBYTES / type_bytes(type), rows_per_box);
   return make_tensor_map_2d(tm, type, o.ptr, o.rows, K, o.ld, 64, 64);
-}
-
-int sm_count() {
-  static const int n = [] {
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-  }();
-  return n;
 }
 
 template <bool F8, class O>
@@ -806,13 +841,12 @@ extern "C" cr_status cr_affine_backward(int type, const void* d_W, int ldw, cons
     using E = decltype(e0);
     const E* G = own ? (const E*)own : (const E*)d_dY;
     const int ldg = own ? ldown : lddy;
-    if (own || d_db)
-      CR_TRY(with_act(act, [&](auto a0) -> cr_status {
-        k_affine_g<E, decltype(a0)::value><<<(N + 31) / 32, NT, 0, stream>>>((const E*)d_dY, lddy, (const E*)d_Z, ldz, N, M,
-                                                                            (E*)own, ldown, d_db);
-        CR_CHECK_LAUNCH("k_affine_g");
-        return CR_OK;
-      }));
+    if (own || d_db) {
+      const auto ok16 = [](const void* q, int ld) { return ((uintptr_t)q & 15) == 0 && ld % 8 == 0; };
+      const bool vec = N % 8 == 0 && ok16(d_dY, lddy) && (act == CR_ACT_NONE || ok16(d_Z, ldz));
+      if (vec) CR_TRY((gradient_at_z<E, 8>((const E*)d_dY, lddy, (const E*)d_Z, ldz, N, M, act, (E*)own, ldown, d_db, stream)));
+      else CR_TRY((gradient_at_z<E, 1>((const E*)d_dY, lddy, (const E*)d_Z, ldz, N, M, act, (E*)own, ldown, d_db, stream)));
+    }
     if (d_dX) {   // dX(i, j) = sum_n W(i, n) G(n, j)
       const Epilogue e{nullptr, nullptr, nullptr, CR_ACT_NONE, nullptr, 0, nullptr, 0, d_dX, lddx};
       CR_TRY(product(Operand{d_W, K, ldw, false}, Operand{G, M, ldg, true}, type, N, type, e, stream));

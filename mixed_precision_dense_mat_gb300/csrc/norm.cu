@@ -1,5 +1,6 @@
 // Root-mean-square norm of columns with the residual's addition and an optional e4m3 output,
 // and its gradient (cr_rmsnorm, cr_rmsnorm_backward).
+#include <algorithm>
 #include <type_traits>
 
 #include "ops.cuh"
@@ -7,8 +8,247 @@
 namespace cr {
 namespace {
 
+// Both are bound by HBM: the forward pass reads X and R and writes H and Y, the backward reads H, dY
+// and dH and writes dX.  A group of G threads holds one column in registers (8 VPT elements per
+// thread), so that memory is read once, and needs one exchange among its threads: the sum of squares
+// together with max|h gamma| (max|y| is that times r), or with the sum of u h.  Blocks are
+// resident and go from column to column with gamma in registers; the next column's loads are
+// issued before the present one is finished.
 constexpr int NT = 256;
+constexpr int MAXD = 16384;   // longer columns: the kernels that go over memory again
 
+// maximum that keeps NaN
+__device__ __forceinline__ float nan_max(float a, float b) { return (a != a || a > b) ? a : b; }
+
+// Two values reduced over the group: x by sum, y by sum or by maximum.  `red` is used alternately
+// (turn) so that one barrier per column is enough.
+template <int G, bool MAX>
+__device__ __forceinline__ void reduce2(float& x, float& y, float2 (*red)[32], int turn) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    x += __shfl_xor_sync(0xffffffffu, x, o);
+    const float z = __shfl_xor_sync(0xffffffffu, y, o);
+    y = MAX ? nan_max(y, z) : y + z;
+  }
+  if (G == 32) return;
+  const int warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0) red[turn][warp] = make_float2(x, y);
+  __syncthreads();
+  x = red[turn][0].x;
+  y = red[turn][0].y;
+#pragma unroll
+  for (int w = 1; w < G / 32; ++w) {
+    x += red[turn][w].x;
+    y = MAX ? nan_max(y, red[turn][w].y) : y + red[turn][w].y;
+  }
+}
+
+// The thread's elements of a column: 8 consecutive ones VPT times (VEC: 16-byte accesses), or single
+// ones G apart.
+template <int G, int VPT, bool VEC>
+__device__ __forceinline__ int element(int v, int e) {
+  const int t = threadIdx.x % G;
+  return VEC ? (v * G + t) * 8 + e : t + G * (v * 8 + e);
+}
+template <class T>
+struct alignas(16) Raw {   // 8 elements as they are in memory
+  T x[8];
+};
+template <class T, int G, int VPT, bool VEC>
+__device__ __forceinline__ void load_col(const T* p, int D, Raw<T> (&w)[VPT]) {
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    if (VEC) {
+      const int i = element<G, VPT, VEC>(v, 0);
+      if (i < D) w[v] = *reinterpret_cast<const Raw<T>*>(p + i);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = element<G, VPT, VEC>(v, e);
+        if (i < D) w[v].x[e] = p[i];
+      }
+    }
+  }
+}
+template <class O>
+struct alignas(8 * sizeof(O) > 16 ? 16 : 8 * sizeof(O)) Out {
+  O x[8];
+};
+template <class O, int G, int VPT, bool VEC>
+__device__ __forceinline__ void store8(O* p, int D, int v, const float (&y)[8]) {
+  if (VEC) {
+    const int i = element<G, VPT, VEC>(v, 0);
+    if (i >= D) return;
+    Out<O> w;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w.x[e] = from_float<O>(y[e]);
+    *reinterpret_cast<Out<O>*>(p + i) = w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = element<G, VPT, VEC>(v, e);
+      if (i < D) p[i] = from_float<O>(y[e]);
+    }
+  }
+}
+template <int G, int VPT, bool VEC>
+__device__ __forceinline__ void load_gamma(const float* gamma, int D, float (&g)[VPT][8]) {
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = element<G, VPT, VEC>(v, e);
+      g[v][e] = i < D ? gamma[i] : 0.0f;
+    }
+}
+
+constexpr int threads_of(int G) { return G == 32 ? NT : G; }
+
+template <class T, class O, int G, int VPT, bool VEC>
+__global__ void __launch_bounds__(threads_of(G))
+    k_rmsnorm(const T* X, int ldx, const T* R, int ldr, const float* gamma, int D, int n, float eps, T* H, int ldh, O* Y, int ldy,
+              float* scale) {
+  constexpr bool Q = std::is_same<O, __nv_fp8_e4m3>::value;
+  constexpr int PER = threads_of(G) / G;   // columns per block at a time
+  __shared__ float2 red[2][32];
+  float g[VPT][8];
+  load_gamma<G, VPT, VEC>(gamma, D, g);
+  const int step = gridDim.x * PER;
+  int t = blockIdx.x * PER + threadIdx.x / G;
+  Raw<T> x[VPT], r[VPT];
+  if (t < n) {
+    load_col<T, G, VPT, VEC>(X + (size_t)t * ldx, D, x);
+    if (R) load_col<T, G, VPT, VEC>(R + (size_t)t * ldr, D, r);
+  }
+  for (int turn = 0; t < n; t += step, turn ^= 1) {
+    float h[VPT][8], ss = 0.0f, mx = 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const bool in = element<G, VPT, VEC>(v, e) < D;
+        h[v][e] = in ? to_float(x[v].x[e]) : 0.0f;
+        if (R && in) h[v][e] += to_float(r[v].x[e]);
+        ss = fmaf(h[v][e], h[v][e], ss);
+        if (Q) mx = nan_max(fabsf(h[v][e] * g[v][e]), mx);
+      }
+    const int next = t + step;
+    if (next < n) {
+      load_col<T, G, VPT, VEC>(X + (size_t)next * ldx, D, x);
+      if (R) load_col<T, G, VPT, VEC>(R + (size_t)next * ldr, D, r);
+    }
+    reduce2<G, true>(ss, mx, red, turn);
+    const float rs = 1.0f / sqrtf(ss / (float)D + eps);
+    float inv = 1.0f;
+    if (Q) {
+      const float s = nan_max(mx * rs, 0x1p-100f) / 448.0f;
+      if (threadIdx.x % G == 0) scale[t] = s;
+      inv = 1.0f / s;
+    }
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      if (H) store8<T, G, VPT, VEC>(H + (size_t)t * ldh, D, v, h[v]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[v][e] = h[v][e] * g[v][e] * rs * inv;
+      store8<O, G, VPT, VEC>(Y + (size_t)t * ldy, D, v, h[v]);
+    }
+  }
+}
+
+// The block's sums for dgamma go to part[block][D], to be added by k_add_rows.
+template <class T, int G, int VPT, bool VEC>
+__global__ void __launch_bounds__(threads_of(G))
+    k_rmsnorm_bwd(const T* H, int ldh, const float* gamma, const T* dY, int lddy, const T* dH, int lddh, int D, int n, float eps, T* dX,
+                  int lddx, float* part) {
+  constexpr int PER = threads_of(G) / G;
+  __shared__ float2 red[2][32];
+  float g[VPT][8], dg[VPT][8] = {};
+  load_gamma<G, VPT, VEC>(gamma, D, g);
+  const int step = gridDim.x * PER;
+  int t = blockIdx.x * PER + threadIdx.x / G;
+  Raw<T> rh[VPT], rd[VPT];
+  if (t < n) {
+    load_col<T, G, VPT, VEC>(H + (size_t)t * ldh, D, rh);
+    load_col<T, G, VPT, VEC>(dY + (size_t)t * lddy, D, rd);
+  }
+  for (int turn = 0; t < n; t += step, turn ^= 1) {
+    Raw<T> rr[VPT];
+    if (dH) load_col<T, G, VPT, VEC>(dH + (size_t)t * lddh, D, rr);
+    float h[VPT][8], d[VPT][8], ss = 0.0f, dot = 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const bool in = element<G, VPT, VEC>(v, e) < D;
+        h[v][e] = in ? to_float(rh[v].x[e]) : 0.0f;
+        d[v][e] = in ? to_float(rd[v].x[e]) : 0.0f;
+        ss = fmaf(h[v][e], h[v][e], ss);
+        dot = fmaf(__fmul_rn(g[v][e], d[v][e]), h[v][e], dot);
+      }
+    const int next = t + step;
+    if (next < n) {
+      load_col<T, G, VPT, VEC>(H + (size_t)next * ldh, D, rh);
+      load_col<T, G, VPT, VEC>(dY + (size_t)next * lddy, D, rd);
+    }
+    reduce2<G, false>(ss, dot, red, turn);
+    const float rs = 1.0f / sqrtf(ss / (float)D + eps), m = dot / (float)D * rs * rs * rs;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dg[v][e] = fmaf(__fmul_rn(d[v][e], h[v][e]), rs, dg[v][e]);
+        o[e] = fmaf(-h[v][e], m, __fmul_rn(rs, __fmul_rn(g[v][e], d[v][e])));
+        if (dH) o[e] += element<G, VPT, VEC>(v, e) < D ? to_float(rr[v].x[e]) : 0.0f;
+      }
+      if (dX) store8<T, G, VPT, VEC>(dX + (size_t)t * lddx, D, v, o);
+    }
+  }
+  if (!part) return;
+  float* out = part + (size_t)blockIdx.x * D;
+  if (G != 32) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = element<G, VPT, VEC>(v, e);
+        if (i < D) out[i] = dg[v][e];
+      }
+  } else {   // the block's columns, one after the other
+    __shared__ float sum[NT / 32][33];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        __syncthreads();
+        sum[threadIdx.x >> 5][threadIdx.x & 31] = dg[v][e];
+        __syncthreads();
+        const int i = element<G, VPT, VEC>(v, e);
+        if (threadIdx.x < 32 && i < D) {
+          float x = 0.0f;
+          for (int w = 0; w < NT / 32; ++w) x += sum[w][threadIdx.x];
+          out[i] = x;
+        }
+      }
+  }
+}
+
+// The sum of `rows` partial vectors (gradients of vectors), in a fixed order: 32 features per block, 32 threads each.
+__global__ void __launch_bounds__(1024) k_add_rows(const float* part, int rows, int D, float* total) {
+  __shared__ float sum[32][33];
+  const int i = blockIdx.x * 32 + threadIdx.x;
+  float s = 0.0f;
+  if (i < D)
+    for (int r = threadIdx.y; r < rows; r += 32) s += part[(size_t)r * D + i];
+  sum[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y == 0 && i < D) {
+    for (int y = 1; y < 32; ++y) s += sum[y][threadIdx.x];
+    total[i] = s;
+  }
+}
+
+// ---------------------------------------------------------------- columns longer than MAXD
 __device__ __forceinline__ float block_sum(float v, float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -20,8 +260,6 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   for (int w = 0; w < NT / 32; ++w) s += red[w];
   return s;
 }
-// maximum that keeps NaN
-__device__ __forceinline__ float nan_max(float a, float b) { return (a != a || a > b) ? a : b; }
 __device__ __forceinline__ float block_max(float v, float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = nan_max(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -36,8 +274,8 @@ __device__ __forceinline__ float block_max(float v, float* red) {
 
 // One block per column, the column read once for each of its reductions.
 template <class T, class O>
-__global__ void __launch_bounds__(NT) k_rmsnorm(const T* X, int ldx, const T* R, int ldr, const float* gamma, int D,
-                                                float eps, T* H, int ldh, O* Y, int ldy, float* scale) {
+__global__ void __launch_bounds__(NT) k_rmsnorm_long(const T* X, int ldx, const T* R, int ldr, const float* gamma, int D,
+                                                     float eps, T* H, int ldh, O* Y, int ldy, float* scale) {
   __shared__ float red[NT / 32];
   const size_t t = blockIdx.x;
   const T* x = X + t * ldx;
@@ -68,7 +306,7 @@ __global__ void __launch_bounds__(NT) k_rmsnorm(const T* X, int ldx, const T* R,
 }
 
 template <class T>
-__global__ void __launch_bounds__(NT) k_rmsnorm_dx(const T* H, int ldh, const float* gamma, const T* dY, int lddy,
+__global__ void __launch_bounds__(NT) k_rmsnorm_dx_long(const T* H, int ldh, const float* gamma, const T* dY, int lddy,
                                                    const T* dH, int lddh, int D, float eps, T* dX, int lddx, float* rs_out) {
   __shared__ float red[NT / 32];
   const size_t t = blockIdx.x;
@@ -91,7 +329,7 @@ __global__ void __launch_bounds__(NT) k_rmsnorm_dx(const T* H, int ldh, const fl
 }
 
 template <class T>
-__global__ void __launch_bounds__(NT) k_rmsnorm_dgamma(const T* H, int ldh, const T* dY, int lddy, const float* rs, int D,
+__global__ void __launch_bounds__(NT) k_rmsnorm_dgamma_long(const T* H, int ldh, const T* dY, int lddy, const float* rs, int D,
                                                        int T_, float* dgamma) {
   const int i = blockIdx.x * NT + threadIdx.x;
   if (i >= D) return;
@@ -100,9 +338,102 @@ __global__ void __launch_bounds__(NT) k_rmsnorm_dgamma(const T* H, int ldh, cons
   dgamma[i] = s;
 }
 
+// Calls f(group, vectors per thread, 16-byte accesses) as integral constants for columns of D.  A warp
+// per column up to 1024, then blocks with 8, 16 or 32 elements per thread.
+template <class F>
+cr_status with_split(int D, bool vec, F&& f) {
+  const auto go = [&](auto g, auto v) -> cr_status {
+    return vec ? f(g, v, std::true_type{}) : f(g, v, std::false_type{});
+  };
+  using std::integral_constant;
+  if (D <= 256) return go(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  if (D <= 512) return go(integral_constant<int, 32>{}, integral_constant<int, 2>{});
+  if (D <= 1024) return go(integral_constant<int, 32>{}, integral_constant<int, 4>{});
+  if (D <= 2048) return go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+  if (D <= 4096) return go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  if (D <= 8192) return go(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+  return go(integral_constant<int, 512>{}, integral_constant<int, 4>{});
+}
+
+int sm_count() {
+  static const int n = [] {
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+  }();
+  return n;
+}
+struct Fwd {
+  const void *X, *R;
+  int ldx, ldr;
+  const float* gamma;
+  int D, n;
+  float eps;
+  void *H, *Y;
+  int ldh, ldy;
+  float* scale;
+};
+template <class T, class O, int G, int VPT, bool VEC>
+cr_status launch_fwd(const Fwd& p, cudaStream_t stream) {
+  constexpr int TH = threads_of(G), PER = TH / G;
+  static const int resident = [] {
+    int b = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, k_rmsnorm<T, O, G, VPT, VEC>, TH, 0);
+    return std::max(b, 1) * sm_count();
+  }();
+  TimedScope ts("k_rmsnorm", stream);
+  k_rmsnorm<T, O, G, VPT, VEC><<<std::min(resident, (p.n + PER - 1) / PER), TH, 0, stream>>>(
+      (const T*)p.X, p.ldx, (const T*)p.R, p.ldr, p.gamma, p.D, p.n, p.eps, (T*)p.H, p.ldh, (O*)p.Y, p.ldy, p.scale);
+  CR_CHECK_LAUNCH("k_rmsnorm");
+  return CR_OK;
+}
+
+struct Bwd {
+  const void *H, *dY, *dH;
+  int ldh, lddy, lddh;
+  const float* gamma;
+  int D, n;
+  float eps;
+  void* dX;
+  int lddx;
+  float* dgamma;
+};
+template <class T, int G, int VPT, bool VEC>
+cr_status launch_bwd(const Bwd& p, cudaStream_t stream) {
+  constexpr int TH = threads_of(G), PER = TH / G;
+  static const int resident = [] {
+    int b = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, k_rmsnorm_bwd<T, G, VPT, VEC>, TH, 0);
+    return std::max(b, 1) * sm_count();
+  }();
+  const int blocks = std::min(resident, (p.n + PER - 1) / PER);
+  float* part = nullptr;
+  if (p.dgamma) CR_CUDA(scratch_alloc((void**)&part, (size_t)blocks * p.D * sizeof(float), stream));
+  {
+    TimedScope ts("k_rmsnorm_bwd", stream);
+    k_rmsnorm_bwd<T, G, VPT, VEC><<<blocks, TH, 0, stream>>>((const T*)p.H, p.ldh, p.gamma, (const T*)p.dY, p.lddy, (const T*)p.dH,
+                                                             p.lddh, p.D, p.n, p.eps, (T*)p.dX, p.lddx, part);
+    count_launch();
+  }
+  const cudaError_t e = cudaGetLastError();
+  const cr_status st = e != cudaSuccess ? cuda_fail(e, "k_rmsnorm_bwd") : p.dgamma ? add_rows(part, blocks, p.D, p.dgamma, stream) : CR_OK;
+  scratch_free(part, stream);
+  return st;
+}
+
+bool ok16(const void* p, int ld, int eb) { return !p || (((uintptr_t)p & 15) == 0 && (long long)ld * eb % 16 == 0); }
+
 bool float_type(int t) { return t == CR_TYPE_F32 || t == CR_TYPE_F16 || t == CR_TYPE_BF16; }
 
 }  // namespace
+
+cr_status add_rows(const float* part, int rows, int D, float* total, cudaStream_t stream) {
+  k_add_rows<<<(D + 31) / 32, dim3(32, 32), 0, stream>>>(part, rows, D, total);
+  CR_CHECK_LAUNCH("k_add_rows");
+  return CR_OK;
+}
+
 }  // namespace cr
 
 using namespace cr;
@@ -121,14 +452,23 @@ extern "C" cr_status cr_rmsnorm(int type, const void* d_X, int ldx, const void* 
   CR_REQUIRE(d_X && d_gamma && d_Y, "cr_rmsnorm: NULL argument");
   return with_type(type, [&](auto t0) -> cr_status {
     using E = decltype(t0);
-    if (out_type == CR_TYPE_E4M3)
-      k_rmsnorm<E, __nv_fp8_e4m3><<<T, NT, 0, stream>>>((const E*)d_X, ldx, (const E*)d_R, ldr, d_gamma, D, (float)eps, (E*)d_H,
-                                                        ldh, (__nv_fp8_e4m3*)d_Y, ldy, d_scale);
-    else
-      k_rmsnorm<E, E><<<T, NT, 0, stream>>>((const E*)d_X, ldx, (const E*)d_R, ldr, d_gamma, D, (float)eps, (E*)d_H, ldh,
-                                            (E*)d_Y, ldy, nullptr);
-    CR_CHECK_LAUNCH("k_rmsnorm");
-    return CR_OK;
+    const int eb = sizeof(E);
+    const auto run = [&](auto o0) -> cr_status {
+      using O = decltype(o0);
+      if (D > MAXD) {
+        k_rmsnorm_long<E, O><<<T, NT, 0, stream>>>((const E*)d_X, ldx, (const E*)d_R, ldr, d_gamma, D, (float)eps, (E*)d_H, ldh,
+                                                   (O*)d_Y, ldy, d_scale);
+        CR_CHECK_LAUNCH("k_rmsnorm_long");
+        return CR_OK;
+      }
+      const bool vec = D % 8 == 0 && ok16(d_X, ldx, eb) && ok16(d_R, ldr, eb) && ok16(d_H, ldh, eb) &&
+                       (sizeof(O) == 1 ? ((uintptr_t)d_Y & 7) == 0 && ldy % 8 == 0 : ok16(d_Y, ldy, sizeof(O)));
+      return with_split(D, vec, [&](auto g, auto v, auto w) -> cr_status {
+        return launch_fwd<E, O, decltype(g)::value, decltype(v)::value, decltype(w)::value>(
+            Fwd{d_X, d_R, ldx, ldr, d_gamma, D, T, (float)eps, d_H, d_Y, ldh, ldy, d_scale}, stream);
+      });
+    };
+    return out_type == CR_TYPE_E4M3 ? run(__nv_fp8_e4m3{}) : run(t0);
   });
   CR_ENTRY_END("cr_rmsnorm")
 }
@@ -147,25 +487,34 @@ extern "C" cr_status cr_rmsnorm_backward(int type, const void* d_H, int ldh, con
     return CR_OK;
   }
   CR_REQUIRE(d_H && d_gamma && d_dY, "cr_rmsnorm_backward: NULL argument");
-  float* rs = nullptr;
-  CR_CUDA(scratch_alloc((void**)&rs, (size_t)T * sizeof(float), stream));
+  if (!d_dX && !d_dgamma) return CR_OK;
+  float* mem = nullptr;
   const cr_status st = with_type(type, [&](auto t0) -> cr_status {
     using E = decltype(t0);
-    // dgamma first: dX may overwrite dY, so the columns' r are found without writing dX, then dX
-    k_rmsnorm_dx<E><<<T, NT, 0, stream>>>((const E*)d_H, ldh, d_gamma, (const E*)d_dY, lddy, nullptr, 0, D, (float)eps, nullptr, 0, rs);
-    CR_CHECK_LAUNCH("k_rmsnorm_dx");
-    if (d_dgamma) {
-      k_rmsnorm_dgamma<E><<<(D + NT - 1) / NT, NT, 0, stream>>>((const E*)d_H, ldh, (const E*)d_dY, lddy, rs, D, T, d_dgamma);
-      CR_CHECK_LAUNCH("k_rmsnorm_dgamma");
+    if (D > MAXD) {
+      CR_CUDA(scratch_alloc((void**)&mem, (size_t)T * sizeof(float), stream));
+      // dgamma first: dX may overwrite dY, so the columns' r are found without writing dX, then dX
+      k_rmsnorm_dx_long<E><<<T, NT, 0, stream>>>((const E*)d_H, ldh, d_gamma, (const E*)d_dY, lddy, nullptr, 0, D, (float)eps, nullptr, 0, mem);
+      CR_CHECK_LAUNCH("k_rmsnorm_dx_long");
+      if (d_dgamma) {
+        k_rmsnorm_dgamma_long<E><<<(D + NT - 1) / NT, NT, 0, stream>>>((const E*)d_H, ldh, (const E*)d_dY, lddy, mem, D, T, d_dgamma);
+        CR_CHECK_LAUNCH("k_rmsnorm_dgamma_long");
+      }
+      if (d_dX) {
+        k_rmsnorm_dx_long<E><<<T, NT, 0, stream>>>((const E*)d_H, ldh, d_gamma, (const E*)d_dY, lddy, (const E*)d_dH, lddh, D,
+                                                   (float)eps, (E*)d_dX, lddx, mem);
+        CR_CHECK_LAUNCH("k_rmsnorm_dx_long");
+      }
+      return CR_OK;
     }
-    if (d_dX) {
-      k_rmsnorm_dx<E><<<T, NT, 0, stream>>>((const E*)d_H, ldh, d_gamma, (const E*)d_dY, lddy, (const E*)d_dH, lddh, D,
-                                            (float)eps, (E*)d_dX, lddx, rs);
-      CR_CHECK_LAUNCH("k_rmsnorm_dx");
-    }
-    return CR_OK;
+    const int eb = sizeof(E);
+    const bool vec = D % 8 == 0 && ok16(d_H, ldh, eb) && ok16(d_dY, lddy, eb) && ok16(d_dH, lddh, eb) && ok16(d_dX, lddx, eb);
+    return with_split(D, vec, [&](auto g, auto v, auto w) -> cr_status {
+      return launch_bwd<E, decltype(g)::value, decltype(v)::value, decltype(w)::value>(
+          Bwd{d_H, d_dY, d_dH, ldh, lddy, lddh, d_gamma, D, T, (float)eps, d_dX, lddx, d_dgamma}, stream);
+    });
   });
-  scratch_free(rs, stream);
+  scratch_free(mem, stream);
   return st;
   CR_ENTRY_END("cr_rmsnorm_backward")
 }

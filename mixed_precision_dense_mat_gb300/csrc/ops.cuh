@@ -24,6 +24,9 @@ cr_status make_tensor_map_2d(CUtensorMap* tm, int type, const void* base, int in
 cr_status make_tensor_map_2d_plain(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
                                    int box_outer);
 
+// total[D] = the sum of the rows of part (rows x D, row-major), in a fixed order.
+cr_status add_rows(const float* part, int rows, int D, float* total, cudaStream_t stream);
+
 // C++ exceptions end at the C entries.
 #define CR_ENTRY_BEGIN try {
 #define CR_ENTRY_END(what)                                                                    \

@@ -14,11 +14,11 @@ namespace {
 // How the scan is split.  A work item is a chunk of consecutive steps by a tile of W features (128
 // bytes of each column).  Resident blocks take items in order of time from a counter: whatever an
 // item waits for was taken earlier and is being worked on.  Warp 8 of a block takes the items and
-// loads them by TMA into a ring of stages, so that loads stay in flight while the other 8 warps
-// work; each of these owns SUB of the chunk's steps and each of its lanes VEC features.  They go over
-// the tile in shared memory twice, for its map and, once the state before it is known, for
-// the outputs, so that HBM is read once and few registers are held meanwhile: three blocks fit
-// on an SM, which covers the time that a block waits for its predecessors.
+// loads them by TMA into stages while the other 8 warps work; each of these owns SUB of the
+// chunk's steps and each of its lanes VEC features.  They go over the tile in shared memory twice,
+// for its map and, once the state before it is known, for the outputs, so that HBM is read once
+// and few registers are held meanwhile: several blocks fit on an SM, which covers the time that
+// a block waits for its predecessors.
 // The map of a run of steps on the state is h -> A h + B, and such maps compose; "start from
 // h0" is the map A = 0, B = h0, so that packed series need no other care (A = 0 is taken as "forget",
 // not multiplied, so that nothing crosses into the next series).  Warps join their maps in
@@ -28,7 +28,10 @@ namespace {
 constexpr int WARPS = 8, NT = 32 * (WARPS + 1);
 constexpr int FSUB = 16, BSUB = 8;        // steps per warp, forward and backward
 constexpr int BLOCK = WARPS * BSUB;       // steps between saved states: a chunk of the backward pass
-constexpr int STAGES = 2;
+// Stages per block and blocks per SM.  More blocks hide the waits for predecessors, more stages the
+// loads; forward 2048 x 65536 BF16: 1 and 5 186 us, 1 and 4 192 us, 2 and 3 195 us, 3 and 2 245 us;
+// backward 1 and 4 423 us, 2 and 3 400 us.
+constexpr int FSTAGES = 1, FBLOCKS = 5, BSTAGES = 2, BBLOCKS = 3;
 constexpr int MAXGROUP = 64;
 constexpr int ROW = 128;                  // bytes of a column in a tile
 template <class T>
@@ -148,7 +151,7 @@ __device__ __forceinline__ void store_state(float* hT, int ld, int s, int f, int
 __device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // Shared memory of a block: ring of stages of NIN input tiles, then this.
-template <int CH, int W>
+template <int CH, int W, int STAGES>
 struct Shared {
   uint64_t full[STAGES], empty[STAGES];
   int place[STAGES];
@@ -164,17 +167,17 @@ struct Input {
 
 // Warp 8: takes work items and fills stages.  item(place, tile, t0) gives an item's tile and first
 // step, empty(tile, s) handles an empty series.
-template <class T, int CH, int NIN, int W, class Item, class Empty>
-__device__ __forceinline__ void feed(const Lookback& lb, Shared<CH, W>* sh, uint8_t* ring, const CUtensorMap* const (&tm)[NIN], bool tma,
+template <class T, int CH, int NIN, int W, int STAGES, class Item, class Empty>
+__device__ __forceinline__ void feed(const Lookback& lb, Shared<CH, W, STAGES>* sh, uint8_t* ring, const CUtensorMap* const (&tm)[NIN], bool tma,
                                      const int32_t* off, int series, int n, Item&& item, Empty&& empty) {
   const int lane = threadIdx.x & 31, total = lb.chunks * lb.tiles;
   int it = 0;
   for (;; ++it) {
     const int st = it % STAGES;
-    int place = 0;   // taken before the stage is free
+    if (!mbar_wait(&sh->empty[st], ((uint32_t)(it / STAGES) & 1u) ^ 1u, lb.limit) || *(volatile int*)&sh->bad) break;
+    int place = 0;   // taken late: an item held back here holds up the blocks that wait for its map
     if (lane == 0) place = lb.chunks > 1 ? atomicAdd(lb.counter, 1) : (int)blockIdx.x + it * (int)gridDim.x;
     place = __shfl_sync(0xffffffffu, place, 0);
-    if (!mbar_wait(&sh->empty[st], ((uint32_t)(it / STAGES) & 1u) ^ 1u, lb.limit) || *(volatile int*)&sh->bad) break;
     if (place >= total) {
       if (lane == 0) {
         sh->place[st] = -1;
@@ -217,7 +220,7 @@ __device__ __forceinline__ void copy_rows(const Input& in, uint8_t* tile, int ro
 
 // The item in the stage of round `it`; -1 when there is none or the wait for it ran out.  sh->bad is
 // written before a barrier of the workers and read before the next, so that they agree.
-template <class S>
+template <int STAGES, class S>
 __device__ __forceinline__ int next_item(const Lookback& lb, S* sh, int it) {
   if (!mbar_wait(&sh->full[it % STAGES], (uint32_t)(it / STAGES) & 1u, lb.limit)) {
     *(volatile int*)&sh->bad = 1;
@@ -231,8 +234,8 @@ __device__ __forceinline__ int next_item(const Lookback& lb, S* sh, int it) {
 // Joins the workers' maps (A, B) of a chunk (position k in the order of work): the state that enters the
 // part of each warp, in sh->fold[warp][feature].x.  Warps compose in the order 0 .. 7, or 7 .. 0 with REVERSE.  All
 // workers call it; false when a wait ran out.
-template <bool REVERSE, int VEC, int CH, int W>
-__device__ __forceinline__ bool join(const Lookback& lb, Shared<CH, W>* sh, int tile, int k, int D, const Floats<VEC>& A, const Floats<VEC>& B) {
+template <bool REVERSE, int VEC, int W, class S>
+__device__ __forceinline__ bool join(const Lookback& lb, S* sh, int tile, int k, int D, const Floats<VEC>& A, const Floats<VEC>& B) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int v = 0; v < VEC; ++v) sh->maps[warp][lane * VEC + v] = make_float2(A.x[v], B.x[v]);
@@ -349,15 +352,15 @@ __device__ __forceinline__ void put(T* out, int ld, int t, int f, int D, bool ve
 // Forward scan.  Bound by HBM (G and X read, H written).  Steps past the end and features past D hold
 // zeros: their states are never used.
 template <class T, int GATE>
-__global__ void __launch_bounds__(NT, 3)
+__global__ void __launch_bounds__(NT, FBLOCKS)
     k_scan_fwd(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmX, const FwdArgs<T> p, const Lookback lb) {
   constexpr int CH = WARPS * FSUB, VEC = vec_of<T>(), W = 32 * VEC;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~(uintptr_t)127);
-  auto* sh = reinterpret_cast<Shared<CH, W>*>(ring + STAGES * 2 * CH * ROW);
+  auto* sh = reinterpret_cast<Shared<CH, W, FSTAGES>*>(ring + FSTAGES * 2 * CH * ROW);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int q = 0; q < STAGES; ++q) {
+    for (int q = 0; q < FSTAGES; ++q) {
       mbar_init(&sh->full[q], 1);
       mbar_init(&sh->empty[q], WARPS);
     }
@@ -381,8 +384,8 @@ __global__ void __launch_bounds__(NT, 3)
     return;
   }
   for (int it = 0;; ++it) {
-    const int st = it % STAGES;
-    const int place = next_item(lb, sh, it);
+    const int st = it % FSTAGES;
+    const int place = next_item<FSTAGES>(lb, sh, it);
     if (place < 0) break;
     const int k = place / lb.tiles, tile = place % lb.tiles, t0 = k * CH + warp * FSUB, f = tile * W + lane * VEC;
     uint8_t* in = ring + st * 2 * CH * ROW;
@@ -404,7 +407,7 @@ __global__ void __launch_bounds__(NT, 3)
     };
     Floats<VEC> A = all_of<VEC>(1.0f), B = all_of<VEC>(0.0f), a, b;
     if (!starts) {   // without branches, so that steps overlap
-#pragma unroll
+#pragma unroll 4
       for (int i = 0; i < FSUB; ++i) {
         step(i, a, b);
         A = mul(A, a);
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(NT, 3)
         B = fma(a, B, b);
       }
     }
-    if (!join<false, VEC, CH, W>(lb, sh, tile, k, p.D, A, B)) return;
+    if (!join<false, VEC, W>(lb, sh, tile, k, p.D, A, B)) return;
     Floats<VEC> h;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) h.x[v] = sh->fold[warp][lane * VEC + v].x;
@@ -430,7 +433,7 @@ __global__ void __launch_bounds__(NT, 3)
     if (!(starts | ends) && p.H && p.pairs && p.n - t0 >= FSUB) {   // inside a series
       if (f < p.D) {
         T* o = p.H + (size_t)t0 * p.ldh + f;
-#pragma unroll
+#pragma unroll 4
         for (int i = 0; i < FSUB; ++i, o += p.ldh) {
           step(i, a, b);
           h = fma(a, h, b);
@@ -472,16 +475,16 @@ struct BwdArgs {
 // a series' last step.  The states inside a chunk are recomputed from the saved one before
 // it, which reads G and X (needed anyway) in place of H.  Bound by HBM (G, X, dH read, dG, dX written).
 template <class T, int GATE>
-__global__ void __launch_bounds__(NT, 3)
+__global__ void __launch_bounds__(NT, BBLOCKS)
     k_scan_bwd(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmD,
                const BwdArgs<T> p, const Lookback lb) {
   constexpr int CH = BLOCK, SUB = BSUB, VEC = vec_of<T>(), W = 32 * VEC;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~(uintptr_t)127);
-  auto* sh = reinterpret_cast<Shared<CH, W>*>(ring + STAGES * 3 * CH * ROW);
+  auto* sh = reinterpret_cast<Shared<CH, W, BSTAGES>*>(ring + BSTAGES * 3 * CH * ROW);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int q = 0; q < STAGES; ++q) {
+    for (int q = 0; q < BSTAGES; ++q) {
       mbar_init(&sh->full[q], 1);
       mbar_init(&sh->empty[q], WARPS);
     }
@@ -505,8 +508,8 @@ __global__ void __launch_bounds__(NT, 3)
     return;
   }
   for (int it = 0;; ++it) {
-    const int st = it % STAGES;
-    const int place = next_item(lb, sh, it);
+    const int st = it % BSTAGES;
+    const int place = next_item<BSTAGES>(lb, sh, it);
     if (place < 0) break;
     const int k = place / lb.tiles, tile = place % lb.tiles, chunk = lb.chunks - 1 - k;
     const int t0 = chunk * CH + warp * SUB, f = tile * W + lane * VEC;
@@ -566,7 +569,7 @@ __global__ void __launch_bounds__(NT, 3)
       b[i] = h;
       h = next;
     }
-    if (!join<true, VEC, CH, W>(lb, sh, tile, k, p.D, RA, RB)) return;
+    if (!join<true, VEC, W>(lb, sh, tile, k, p.D, RA, RB)) return;
     Floats<VEC> q;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) q.x[v] = sh->fold[warp][lane * VEC + v].x;
@@ -676,12 +679,12 @@ cr_status map_in(CUtensorMap* tm, const Input& in, int D, int n, int steps) {
   return make_tensor_map_2d_plain(tm, type_of<T>(), in.p, D, n, in.ld, ROW / (int)sizeof(T), steps);
 }
 
-int resident_blocks() {   // three per SM (registers and shared memory allow it)
+int sm_count() {
   static const int n = [] {
     int dev = 0, sms = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return 3 * sms;
+    return sms;
   }();
   return n;
 }
@@ -695,7 +698,7 @@ cr_status states_only(const float* from, int ldf, float* to, int ldt, int D, int
 
 template <class E, int GATE>
 cr_status forward(FwdArgs<E> p, cudaStream_t stream) {
-  constexpr int CH = WARPS * FSUB, W = 32 * vec_of<E>(), SMEM = STAGES * 2 * CH * ROW + sizeof(Shared<CH, W>) + 128;
+  constexpr int CH = WARPS * FSUB, W = 32 * vec_of<E>(), SMEM = FSTAGES * 2 * CH * ROW + sizeof(Shared<CH, W, FSTAGES>) + 128;
   const int tiles = (p.D + W - 1) / W;
   Scratch sc;
   CR_TRY(sc.make(p.n, CH, tiles, W, stream));
@@ -710,14 +713,14 @@ cr_status forward(FwdArgs<E> p, cudaStream_t stream) {
     CR_TRY(map_in<E>(&tmX, p.X, p.D, p.n, CH));
   }
   TimedScope ts("k_scan_fwd", stream);
-  k_scan_fwd<E, GATE><<<std::min(resident_blocks(), sc.lb.chunks * tiles), NT, SMEM, stream>>>(tmG, tmX, p, sc.lb);
+  k_scan_fwd<E, GATE><<<std::min(FBLOCKS * sm_count(), sc.lb.chunks * tiles), NT, SMEM, stream>>>(tmG, tmX, p, sc.lb);
   CR_CHECK_LAUNCH("k_scan_fwd");
   return CR_OK;
 }
 
 template <class E, int GATE>
 cr_status backward(BwdArgs<E> p, cudaStream_t stream) {
-  constexpr int W = 32 * vec_of<E>(), SMEM = STAGES * 3 * BLOCK * ROW + sizeof(Shared<BLOCK, W>) + 128;
+  constexpr int W = 32 * vec_of<E>(), SMEM = BSTAGES * 3 * BLOCK * ROW + sizeof(Shared<BLOCK, W, BSTAGES>) + 128;
   const int tiles = (p.D + W - 1) / W;
   Scratch sc;
   CR_TRY(sc.make(p.n, BLOCK, tiles, W, stream));
@@ -733,7 +736,7 @@ cr_status backward(BwdArgs<E> p, cudaStream_t stream) {
     CR_TRY(map_in<E>(&tmD, p.dH, p.D, p.n, BLOCK));
   }
   TimedScope ts("k_scan_bwd", stream);
-  k_scan_bwd<E, GATE><<<std::min(resident_blocks(), sc.lb.chunks * tiles), NT, SMEM, stream>>>(tmG, tmX, tmD, p, sc.lb);
+  k_scan_bwd<E, GATE><<<std::min(BBLOCKS * sm_count(), sc.lb.chunks * tiles), NT, SMEM, stream>>>(tmG, tmX, tmD, p, sc.lb);
   CR_CHECK_LAUNCH("k_scan_bwd");
   return CR_OK;
 }
