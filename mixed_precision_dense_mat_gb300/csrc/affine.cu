@@ -66,29 +66,8 @@ __device__ __forceinline__ void gave_up(const Params& p, volatile int* abort) {
   __threadfence_system();
 }
 
-template <class O>
-__device__ __forceinline__ void load8(const O* p, float* v) {   // 8 elements, 16-byte aligned for 2-byte types
-  if (sizeof(O) == 2) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      O h[2];
-      memcpy(h, &u[q], 4);
-      v[2 * q] = to_float(h[0]);
-      v[2 * q + 1] = to_float(h[1]);
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const float4 w = reinterpret_cast<const float4*>(p)[q];
-      v[4 * q] = w.x;
-      v[4 * q + 1] = w.y;
-      v[4 * q + 2] = w.z;
-      v[4 * q + 3] = w.w;
-    }
-  }
-}
+constexpr int OROW = 64, WBUF = 2 * 32 * OROW;   // an epilogue warp's rows on their way out: two tiles of 64-byte rows
+
 // z (a finished sum) to the output (i, j).
 template <class O>
 __device__ __forceinline__ void finish(const Params& p, int i, int j, float z) {
@@ -177,27 +156,27 @@ __device__ __forceinline__ void load_row(const float* x, int i0, int I, int vec,
   }
 }
 
-// The warp's 32 rows j of N = 128 / sizeof(O) values from (i0, j0): through shared memory (rows of 128
-// bytes in the 128-byte swizzle) and by TMA, or element by element where TMA cannot address them.
+// The warp's 32 rows j of N = OROW / sizeof(O) values from (i0, j0): through shared memory (rows of 64
+// bytes in the 64-byte swizzle) and by TMA, or element by element where TMA cannot address them.
 template <class O, int N>
-__device__ __forceinline__ void put_rows(const CUtensorMap* tm, int tma, O* out, int ld, int I, int J, int i0, int j0, uint8_t* buf,
+__device__ __forceinline__ void put_rows(const CUtensorMap* tm, int tma, O* out, int ld, int I, int J, int i0, int j0, uint8_t*& buf,
                                          const float (&v)[N]) {
   const int lane = threadIdx.x & 31;
   if (tma) {
-    if (lane == 0) tma_store_wait_read();   // the buffer's last tile has been read
+    if (lane == 0) tma_store_wait_read();   // this buffer's last tile has been read (the other's may not)
     __syncwarp();
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      O h[16 / sizeof(O)];
+    for (int q = 0; q < N / 8; ++q) {
+      const Eight<O> w = narrow8<O>(v + 8 * q);
 #pragma unroll
-      for (int x = 0; x < (int)(16 / sizeof(O)); ++x) h[x] = from_float<O>(v[q * (16 / sizeof(O)) + x]);
-      uint4 w;
-      memcpy(&w, h, 16);
-      *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) = w;
+      for (int x = 0; x < (int)sizeof(O) / 2; ++x)
+        *reinterpret_cast<uint4*>(buf + lane * OROW + (((int)sizeof(O) / 2 * q + x) ^ (lane >> 1 & 3)) * 16) =
+            make_uint4(w.w[4 * x], w.w[4 * x + 1], w.w[4 * x + 2], w.w[4 * x + 3]);
     }
     fence_smem_to_tma();
     __syncwarp();
-    if (lane == 0 && j0 < J) tma_store_2d(tm, buf, i0, j0);
+    if (lane == 0) tma_store_2d(tm, buf, i0, j0, j0 < J);
+    buf = reinterpret_cast<uint8_t*>(reinterpret_cast<uintptr_t>(buf) ^ (WBUF / 2));
   } else if (j0 + lane < J) {
     O* o = out + (size_t)(j0 + lane) * ld + i0;
 #pragma unroll
@@ -209,7 +188,7 @@ __device__ __forceinline__ void put_rows(const CUtensorMap* tm, int tma, O* out,
 // Epilogue of the warp's 32 rows j and N columns i; v holds the sums.
 template <class O, int N>
 __device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* tmC, const CUtensorMap* tmZ, int i0, int j0, float js,
-                                            uint8_t* buf, float (&v)[N]) {
+                                            uint8_t*& buf, float (&v)[N]) {
   const Epilogue& e = p.e;
   const int j = j0 + (threadIdx.x & 31);
   if (e.iscale) {
@@ -236,7 +215,7 @@ __device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* 
 #pragma unroll
       for (int q = 0; q < N; q += 8) {
         float w[8];
-        load8(r + q, w);
+        widen8(*reinterpret_cast<const Eight<O>*>(r + q), w);
 #pragma unroll
         for (int x = 0; x < 8; ++x) v[q + x] += w[x];
       }
@@ -266,7 +245,6 @@ struct WideBars {
   uint32_t tmem;
   int abort;
 };
-constexpr int WBUF = 32 * 128;                   // an epilogue warp's rows on their way out
 constexpr int WSMEM = WSTAGES * WSTAGE + WEPI * WBUF + 1024 + 256;
 static_assert(sizeof(WideBars) <= 256, "barrier area");
 
@@ -403,12 +381,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
       const int j0 = tj * 256 + (int)rank * 128 + quad * 32, ibase = ti * 256 + half * 128;
       const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * 256 + half * 128);
       const float js = p.e.jscale && j0 + lane < p.J ? p.e.jscale[j0 + lane] : 1.0f;
-      constexpr int N = 128 / (int)sizeof(O);
+      constexpr int N = OROW / (int)sizeof(O);
       for (int c = 0; c < 128; c += N) {
         float v[N];
         __syncwarp();
-#pragma unroll
-        for (int q = 0; q < N; q += 32) tmem_ld32(tq + (uint32_t)(c + q), v + q);
+        if constexpr (N == 32) tmem_ld32(tq + (uint32_t)c, v);
+        else tmem_ld16(tq + (uint32_t)c, v);
         if (c + N == 128) {   // the accumulator is read: the next tile but one may have it
           tc_fence_before();
           __syncwarp();
@@ -627,27 +605,30 @@ __global__ void __launch_bounds__(NT) k_pack(const E* src, int lds, int n, int m
 // in part[blockIdx.y][N].  Bound by HBM (dY and Z read, G written).
 template <class E, int ACT, int V>
 __global__ void __launch_bounds__(NT) k_affine_g(const E* dY, int lddy, const E* Z, int ldz, int N, int M, E* G, int ldg, float* part) {
-  struct alignas(sizeof(E) * V) Raw {
-    E x[V];
-  };
   __shared__ float red[NT / 32][32 * V + V];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, i = (blockIdx.x * 32 + lane) * V;
   float s[V] = {};
   if (i < N) {
 #pragma unroll 4
     for (int j = blockIdx.y * (NT / 32) + w; j < M; j += gridDim.y * (NT / 32)) {
-      const Raw d = *reinterpret_cast<const Raw*>(dY + (size_t)j * lddy + i);
-      Raw z = {};
-      if (ACT != CR_ACT_NONE) z = *reinterpret_cast<const Raw*>(Z + (size_t)j * ldz + i);
-      Raw o;
+      const E *dy = dY + (size_t)j * lddy + i, *zz = Z + (size_t)j * ldz + i;
+      float g[V], z[V];
+      if constexpr (V == 8) {
+        widen8(*reinterpret_cast<const Eight<E>*>(dy), g);
+        if (ACT != CR_ACT_NONE) widen8(*reinterpret_cast<const Eight<E>*>(zz), z);
+      } else {
+        g[0] = to_float(*dy);
+        if (ACT != CR_ACT_NONE) z[0] = to_float(*zz);
+      }
 #pragma unroll
       for (int q = 0; q < V; ++q) {
-        float g = to_float(d.x[q]);
-        if (ACT != CR_ACT_NONE) g = __fmul_rn(g, activation_slope<ACT>(to_float(z.x[q])));
-        s[q] += g;
-        o.x[q] = from_float<E>(g);
+        if (ACT != CR_ACT_NONE) g[q] = __fmul_rn(g[q], activation_slope<ACT>(z[q]));
+        s[q] += g[q];
       }
-      if (G) *reinterpret_cast<Raw*>(G + (size_t)j * ldg + i) = o;
+      if (G) {
+        if constexpr (V == 8) *reinterpret_cast<Eight<E>*>(G + (size_t)j * ldg + i) = narrow8<E>(g);
+        else G[(size_t)j * ldg + i] = from_float<E>(g[0]);
+      }
     }
   }
   if (!part) return;
@@ -784,8 +765,8 @@ cr_status product(Operand P, Operand Q, int type, int K, int out_type, const Epi
     stages = std::min(p.bn <= 32 ? 5 : p.bn == 64 ? 4 : 3, 8);
   }
   CUtensorMap tmP = {}, tmQ = {}, tmC = {}, tmZ = {};
-  if (wide && p.tma_c) CR_TRY(make_tensor_map_2d(&tmC, out_type, e.C, p.I, p.J, e.ldc, KBYTES / ob, 32));
-  if (wide && e.Z && p.tma_z) CR_TRY(make_tensor_map_2d(&tmZ, out_type, e.Z, p.I, p.J, e.ldz, KBYTES / ob, 32));
+  if (wide && p.tma_c) CR_TRY(make_tensor_map_2d_out(&tmC, out_type, e.C, p.I, p.J, e.ldc, OROW / ob, 32));
+  if (wide && e.Z && p.tma_z) CR_TRY(make_tensor_map_2d_out(&tmZ, out_type, e.Z, p.I, p.J, e.ldz, OROW / ob, 32));
   CR_TRY(map_of(&tmP, P, type, K, 128));
   CR_TRY(map_of(&tmQ, Q, type, K, wide ? 128 : p.bn));
   return with_type(out_type, [&](auto o0) -> cr_status {

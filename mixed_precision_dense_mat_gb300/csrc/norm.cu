@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "ops.cuh"
+#include "ptx.cuh"
 
 namespace cr {
 namespace {
@@ -12,16 +13,22 @@ namespace {
 // and dH and writes dX.  A group of G threads holds one column in registers (8 VPT elements per
 // thread), so that memory is read once, and needs one exchange among its threads: the sum of squares
 // together with max|h gamma| (max|y| is that times r), or with the sum of u h.  Blocks are
-// resident and go from column to column with gamma in registers; the next column's loads are
-// issued before the present one is finished.
+// resident and go from column to column with gamma in registers.  Each group has a ring of columns in
+// shared memory, filled by bulk copies several columns ahead: loads into registers, one column
+// ahead, kept too few bytes in flight (4096 x 32768 BF16 -> e4m3 with residual: RINGNOTE).
 constexpr int NT = 256;
 constexpr int MAXD = 16384;   // longer columns: the kernels that go over memory again
 
 // maximum that keeps NaN
-__device__ __forceinline__ float nan_max(float a, float b) { return (a != a || a > b) ? a : b; }
+__device__ __forceinline__ float nan_max(float a, float b) { return clamp_low(a, b); }
 
 // Two values reduced over the group: x by sum, y by sum or by maximum.  `red` is used alternately
 // (turn) so that one barrier per column is enough.
+// G = 32: a warp per column; G = 0: the block.
+template <int G>
+__device__ __forceinline__ int group_size() { return G ? G : (int)blockDim.x; }
+template <int G>
+__device__ __forceinline__ int in_group() { return G ? (int)threadIdx.x % G : (int)threadIdx.x; }
 template <int G, bool MAX>
 __device__ __forceinline__ void reduce2(float& x, float& y, float2 (*red)[32], int turn) {
 #pragma unroll
@@ -36,8 +43,7 @@ __device__ __forceinline__ void reduce2(float& x, float& y, float2 (*red)[32], i
   __syncthreads();
   x = red[turn][0].x;
   y = red[turn][0].y;
-#pragma unroll
-  for (int w = 1; w < G / 32; ++w) {
+  for (int w = 1; w < (int)blockDim.x / 32; ++w) {
     x += red[turn][w].x;
     y = MAX ? nan_max(y, red[turn][w].y) : y + red[turn][w].y;
   }
@@ -47,42 +53,32 @@ __device__ __forceinline__ void reduce2(float& x, float& y, float2 (*red)[32], i
 // ones G apart.
 template <int G, int VPT, bool VEC>
 __device__ __forceinline__ int element(int v, int e) {
-  const int t = threadIdx.x % G;
-  return VEC ? (v * G + t) * 8 + e : t + G * (v * 8 + e);
+  const int t = in_group<G>(), n = group_size<G>();
+  return VEC ? (v * n + t) * 8 + e : t + n * (v * 8 + e);
 }
-template <class T>
-struct alignas(16) Raw {   // 8 elements as they are in memory
-  T x[8];
-};
 template <class T, int G, int VPT, bool VEC>
-__device__ __forceinline__ void load_col(const T* p, int D, Raw<T> (&w)[VPT]) {
+__device__ __forceinline__ void load_col(const T* p, int D, float (&h)[VPT][8]) {
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     if (VEC) {
       const int i = element<G, VPT, VEC>(v, 0);
-      if (i < D) w[v] = *reinterpret_cast<const Raw<T>*>(p + i);
+      Eight<T> w = {};
+      if (i < D) w = *reinterpret_cast<const Eight<T>*>(p + i);
+      widen8(w, h[v]);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int i = element<G, VPT, VEC>(v, e);
-        if (i < D) w[v].x[e] = p[i];
+        h[v][e] = i < D ? to_float(p[i]) : 0.0f;
       }
     }
   }
 }
-template <class O>
-struct alignas(8 * sizeof(O) > 16 ? 16 : 8 * sizeof(O)) Out {
-  O x[8];
-};
 template <class O, int G, int VPT, bool VEC>
 __device__ __forceinline__ void store8(O* p, int D, int v, const float (&y)[8]) {
   if (VEC) {
     const int i = element<G, VPT, VEC>(v, 0);
-    if (i >= D) return;
-    Out<O> w;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w.x[e] = from_float<O>(y[e]);
-    *reinterpret_cast<Out<O>*>(p + i) = w;
+    if (i < D) *reinterpret_cast<Eight<O>*>(p + i) = narrow8<O>(y);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -102,54 +98,111 @@ __device__ __forceinline__ void load_gamma(const float* gamma, int D, float (&g)
     }
 }
 
-constexpr int threads_of(int G) { return G == 32 ? NT : G; }
+// The group's ring: `stages` stages of the NIN inputs' columns, in the block's dynamic shared memory
+// after the barriers.  The group's first thread refills the stage of the column before the present
+// one, after the exchange that all threads reach only when they are done with that column.
+struct Wait {
+  unsigned long long limit;
+  int* err;
+};
+template <class T, int G, int NIN>
+struct Ring {
+  uint64_t* full;
+  uint8_t* mem;
+  int stages, bytes, st = 0;   // bytes of one column
+  uint32_t ph = 0;
+  unsigned long long limit;
+  __device__ Ring(uint8_t* smem, int stages_, int D, const Wait& w) : stages(stages_), bytes(D * (int)sizeof(T)), limit(w.limit) {
+    const int group = G ? threadIdx.x / 32 : 0, groups = G ? blockDim.x / 32 : 1;
+    full = reinterpret_cast<uint64_t*>(smem) + group * stages;
+    mem = smem + (groups * stages * 8 + 127) / 128 * 128 + (size_t)group * stages * NIN * bytes;
+    if (in_group<G>() == 0) {
+      for (int q = 0; q < stages; ++q) mbar_init(&full[q], 1);
+      fence_mbar_init();
+    }
+    if (G == 32) __syncwarp();
+    else __syncthreads();
+  }
+  __device__ void fill(int stage, const T* const (&col)[NIN]) {   // by the group's first thread; NULL: not there
+    uint32_t n = 0;
+#pragma unroll
+    for (int q = 0; q < NIN; ++q)
+      if (col[q]) n += bytes;
+    mbar_arrive_expect_tx(&full[stage], n);
+#pragma unroll
+    for (int q = 0; q < NIN; ++q)
+      if (col[q]) bulk_load(mem + ((size_t)stage * NIN + q) * bytes, col[q], bytes, &full[stage]);
+  }
+  // Waits for the current stage.  When the limit runs out the call's results are invalid and no
+  // later wait is waited for.
+  __device__ const T* take(int q, const Wait& w) {
+    if (q == 0 && !mbar_wait(&full[st], ph, limit)) {
+      limit = 0;
+      *(volatile int*)w.err = 1;
+      __threadfence_system();
+    }
+    return reinterpret_cast<const T*>(mem + ((size_t)st * NIN + q) * bytes);
+  }
+  __device__ void next() {
+    if (++st == stages) st = 0, ph ^= 1u;
+  }
+};
 
 template <class T, class O, int G, int VPT, bool VEC>
-__global__ void __launch_bounds__(threads_of(G))
+__global__ void __launch_bounds__(G ? NT : 512)
     k_rmsnorm(const T* X, int ldx, const T* R, int ldr, const float* gamma, int D, int n, float eps, T* H, int ldh, O* Y, int ldy,
-              float* scale) {
+              float* scale, int stages, const Wait wait) {
   constexpr bool Q = std::is_same<O, __nv_fp8_e4m3>::value;
-  constexpr int PER = threads_of(G) / G;   // columns per block at a time
+  constexpr int PER = G ? NT / 32 : 1;   // columns per block at a time
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 red[2][32];
+  Ring<T, G, 2> ring(smem, VEC ? stages : 0, D, wait);
   float g[VPT][8];
+  const int step = gridDim.x * PER, t0 = blockIdx.x * PER + (G ? threadIdx.x / 32 : 0);
+  const auto fill = [&](int stage, long long t) {
+    if (t < n) ring.fill(stage, {X + (size_t)t * ldx, R ? R + (size_t)t * ldr : nullptr});
+  };
+  if (VEC && in_group<G>() == 0)
+    for (int q = 0; q < stages - 1; ++q) fill(q, t0 + (long long)q * step);
   load_gamma<G, VPT, VEC>(gamma, D, g);
-  const int step = gridDim.x * PER;
-  int t = blockIdx.x * PER + threadIdx.x / G;
-  Raw<T> x[VPT], r[VPT];
-  if (t < n) {
-    load_col<T, G, VPT, VEC>(X + (size_t)t * ldx, D, x);
-    if (R) load_col<T, G, VPT, VEC>(R + (size_t)t * ldr, D, r);
-  }
-  for (int turn = 0; t < n; t += step, turn ^= 1) {
+  for (int t = t0, turn = 0; t < n; t += step, turn ^= 1) {
     float h[VPT][8], ss = 0.0f, mx = 0.0f;
+    load_col<T, G, VPT, VEC>(VEC ? ring.take(0, wait) : X + (size_t)t * ldx, D, h);
+    if (R) {
+      float r[VPT][8];
+      load_col<T, G, VPT, VEC>(VEC ? ring.take(1, wait) : R + (size_t)t * ldr, D, r);
 #pragma unroll
-    for (int v = 0; v < VPT; ++v)
+      for (int v = 0; v < VPT; ++v)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const bool in = element<G, VPT, VEC>(v, e) < D;
-        h[v][e] = in ? to_float(x[v].x[e]) : 0.0f;
-        if (R && in) h[v][e] += to_float(r[v].x[e]);
-        ss = fmaf(h[v][e], h[v][e], ss);
-        if (Q) mx = nan_max(fabsf(h[v][e] * g[v][e]), mx);
-      }
-    const int next = t + step;
-    if (next < n) {
-      load_col<T, G, VPT, VEC>(X + (size_t)next * ldx, D, x);
-      if (R) load_col<T, G, VPT, VEC>(R + (size_t)next * ldr, D, r);
-    }
-    reduce2<G, true>(ss, mx, red, turn);
-    const float rs = 1.0f / sqrtf(ss / (float)D + eps);
-    float inv = 1.0f;
-    if (Q) {
-      const float s = nan_max(mx * rs, 0x1p-100f) / 448.0f;
-      if (threadIdx.x % G == 0) scale[t] = s;
-      inv = 1.0f / s;
+        for (int e = 0; e < 8; ++e) h[v][e] += r[v][e];
     }
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       if (H) store8<T, G, VPT, VEC>(H + (size_t)t * ldh, D, v, h[v]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[v][e] = h[v][e] * g[v][e] * rs * inv;
+      for (int e = 0; e < 8; ++e) {
+        ss = fmaf(h[v][e], h[v][e], ss);
+        h[v][e] *= g[v][e];
+        if (Q) mx = nan_max(mx, fabsf(h[v][e]));
+      }
+    }
+    reduce2<G, true>(ss, mx, red, turn);
+    if (VEC) {
+      if (G == 32) __syncwarp();
+      if (in_group<G>() == 0) fill((ring.st ? ring.st : stages) - 1, t + (long long)(stages - 1) * step);
+      ring.next();
+    }
+    const float rs = 1.0f / sqrtf(ss / (float)D + eps);
+    float f = rs;
+    if (Q) {
+      const float s = nan_max(mx * rs, 0x1p-100f) / 448.0f;
+      if (in_group<G>() == 0) scale[t] = s;
+      f = clamp_high(rs * (1.0f / s), 3.0e38f);   // kept finite, for columns of zeros
+    }
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[v][e] *= f;
       store8<O, G, VPT, VEC>(Y + (size_t)t * ldy, D, v, h[v]);
     }
   }
@@ -157,52 +210,65 @@ __global__ void __launch_bounds__(threads_of(G))
 
 // The block's sums for dgamma go to part[block][D], to be added by k_add_rows.
 template <class T, int G, int VPT, bool VEC>
-__global__ void __launch_bounds__(threads_of(G))
+__global__ void __launch_bounds__(G ? NT : 512)
     k_rmsnorm_bwd(const T* H, int ldh, const float* gamma, const T* dY, int lddy, const T* dH, int lddh, int D, int n, float eps, T* dX,
-                  int lddx, float* part) {
-  constexpr int PER = threads_of(G) / G;
+                  int lddx, float* part, int stages, const Wait wait) {
+  constexpr int PER = G ? NT / 32 : 1;
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 red[2][32];
+  Ring<T, G, 3> ring(smem, VEC ? stages : 0, D, wait);
   float g[VPT][8], dg[VPT][8] = {};
+  const int step = gridDim.x * PER, t0 = blockIdx.x * PER + (G ? threadIdx.x / 32 : 0);
+  const auto fill = [&](int stage, long long t) {
+    if (t < n) ring.fill(stage, {H + (size_t)t * ldh, dY + (size_t)t * lddy, dH ? dH + (size_t)t * lddh : nullptr});
+  };
+  if (VEC && in_group<G>() == 0)
+    for (int q = 0; q < stages - 1; ++q) fill(q, t0 + (long long)q * step);
   load_gamma<G, VPT, VEC>(gamma, D, g);
-  const int step = gridDim.x * PER;
-  int t = blockIdx.x * PER + threadIdx.x / G;
-  Raw<T> rh[VPT], rd[VPT];
-  if (t < n) {
-    load_col<T, G, VPT, VEC>(H + (size_t)t * ldh, D, rh);
-    load_col<T, G, VPT, VEC>(dY + (size_t)t * lddy, D, rd);
-  }
-  for (int turn = 0; t < n; t += step, turn ^= 1) {
-    Raw<T> rr[VPT];
-    if (dH) load_col<T, G, VPT, VEC>(dH + (size_t)t * lddh, D, rr);
+  for (int t = t0, turn = 0; t < n; t += step, turn ^= 1) {
+    const T *ch = VEC ? ring.take(0, wait) : H + (size_t)t * ldh, *cd = VEC ? ring.take(1, wait) : dY + (size_t)t * lddy;
     float h[VPT][8], d[VPT][8], ss = 0.0f, dot = 0.0f;
+    load_col<T, G, VPT, VEC>(ch, D, h);
+    load_col<T, G, VPT, VEC>(cd, D, d);
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const bool in = element<G, VPT, VEC>(v, e) < D;
-        h[v][e] = in ? to_float(rh[v].x[e]) : 0.0f;
-        d[v][e] = in ? to_float(rd[v].x[e]) : 0.0f;
         ss = fmaf(h[v][e], h[v][e], ss);
         dot = fmaf(__fmul_rn(g[v][e], d[v][e]), h[v][e], dot);
       }
-    const int next = t + step;
-    if (next < n) {
-      load_col<T, G, VPT, VEC>(H + (size_t)next * ldh, D, rh);
-      load_col<T, G, VPT, VEC>(dY + (size_t)next * lddy, D, rd);
-    }
+    const T* cr = !dH ? nullptr : VEC ? ring.take(2, wait) : dH + (size_t)t * lddh;
     reduce2<G, false>(ss, dot, red, turn);
+    if (VEC) {
+      if (G == 32) __syncwarp();
+      if (in_group<G>() == 0) fill((ring.st ? ring.st : stages) - 1, t + (long long)(stages - 1) * step);
+    }
     const float rs = 1.0f / sqrtf(ss / (float)D + eps), m = dot / (float)D * rs * rs * rs;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      float o[8];
+      float o[8] = {};
+      if (cr) {
+        if (VEC) {
+          const int i = element<G, VPT, VEC>(v, 0);
+          Eight<T> w = {};
+          if (i < D) w = *reinterpret_cast<const Eight<T>*>(cr + i);
+          widen8(w, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int i = element<G, VPT, VEC>(v, e);
+            o[e] = i < D ? to_float(cr[i]) : 0.0f;
+          }
+        }
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         dg[v][e] = fmaf(__fmul_rn(d[v][e], h[v][e]), rs, dg[v][e]);
-        o[e] = fmaf(-h[v][e], m, __fmul_rn(rs, __fmul_rn(g[v][e], d[v][e])));
-        if (dH) o[e] += element<G, VPT, VEC>(v, e) < D ? to_float(rr[v].x[e]) : 0.0f;
+        o[e] += fmaf(-h[v][e], m, __fmul_rn(rs, __fmul_rn(g[v][e], d[v][e])));
       }
       if (dX) store8<T, G, VPT, VEC>(dX + (size_t)t * lddx, D, v, o);
     }
+    if (VEC) ring.next();
   }
   if (!part) return;
   float* out = part + (size_t)blockIdx.x * D;
@@ -338,8 +404,8 @@ __global__ void __launch_bounds__(NT) k_rmsnorm_dgamma_long(const T* H, int ldh,
   dgamma[i] = s;
 }
 
-// Calls f(group, vectors per thread, 16-byte accesses) as integral constants for columns of D.  A warp
-// per column up to 1024, then blocks with 8, 16 or 32 elements per thread.
+// Calls f(group, vectors per thread, 16-byte accesses) as integral constants for columns of D: a warp
+// per column up to 1024, then a block of as many warps as the column fills.
 template <class F>
 cr_status with_split(int D, bool vec, F&& f) {
   const auto go = [&](auto g, auto v) -> cr_status {
@@ -347,13 +413,15 @@ cr_status with_split(int D, bool vec, F&& f) {
   };
   using std::integral_constant;
   if (D <= 256) return go(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  if (!vec && D <= 1024) return f(integral_constant<int, 0>{}, integral_constant<int, 1>{}, std::false_type{});
   if (D <= 512) return go(integral_constant<int, 32>{}, integral_constant<int, 2>{});
+  if (D <= 768) return go(integral_constant<int, 32>{}, integral_constant<int, 3>{});
   if (D <= 1024) return go(integral_constant<int, 32>{}, integral_constant<int, 4>{});
-  if (D <= 2048) return go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
-  if (D <= 4096) return go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-  if (D <= 8192) return go(integral_constant<int, 512>{}, integral_constant<int, 2>{});
-  return go(integral_constant<int, 512>{}, integral_constant<int, 4>{});
+  if (D <= 4096) return go(integral_constant<int, 0>{}, integral_constant<int, 1>{});
+  if (D <= 8192) return go(integral_constant<int, 0>{}, integral_constant<int, 2>{});
+  return go(integral_constant<int, 0>{}, integral_constant<int, 4>{});
 }
+constexpr int threads_for(int G, int VPT, int D) { return G ? NT : (D + 256 * VPT - 1) / (256 * VPT) * 32; }
 
 int sm_count() {
   static const int n = [] {
@@ -364,6 +432,29 @@ int sm_count() {
   }();
   return n;
 }
+// Whether two stages of a column's inputs fit; longer ones are read directly.
+bool ring_fits(int nin, int D, int eb) { return 2ll * nin * D * eb <= 200 * 1024; }
+// Stages of the rings of a block with `per` groups, and the block's shared memory: about 50 KB, so that
+// several blocks share an SM.
+struct Plan {
+  int stages;
+  size_t smem;
+  Plan(bool vec, int per, int nin, int D, int eb) : stages(0), smem(0) {
+    if (!vec) return;
+    const size_t stage = (size_t)per * nin * D * eb;
+    stages = (int)std::min<size_t>(8, std::max<size_t>(2, (size_t)50 * 1024 / stage));
+    smem = ((size_t)per * stages * 8 + 127) / 128 * 128 + stages * stage;
+  }
+};
+template <class K>
+cr_status resident_blocks(K kernel, int threads, size_t smem, int* blocks) {
+  int b = 0;
+  if (smem > 48 * 1024) CR_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  CR_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, kernel, threads, smem));
+  *blocks = std::max(b, 1) * sm_count();
+  return CR_OK;
+}
+
 struct Fwd {
   const void *X, *R;
   int ldx, ldr;
@@ -376,15 +467,16 @@ struct Fwd {
 };
 template <class T, class O, int G, int VPT, bool VEC>
 cr_status launch_fwd(const Fwd& p, cudaStream_t stream) {
-  constexpr int TH = threads_of(G), PER = TH / G;
-  static const int resident = [] {
-    int b = 0;
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, k_rmsnorm<T, O, G, VPT, VEC>, TH, 0);
-    return std::max(b, 1) * sm_count();
-  }();
+  constexpr int PER = G ? NT / 32 : 1;
+  const int TH = threads_for(G, VPT, p.D);
+  const Plan plan(VEC, PER, 2, p.D, sizeof(T));
+  Wait wait = {option_wait_ns(), nullptr};
+  CR_TRY(wait_word(&wait.err));
+  int resident = 0;
+  CR_TRY(resident_blocks(k_rmsnorm<T, O, G, VPT, VEC>, TH, plan.smem, &resident));
   TimedScope ts("k_rmsnorm", stream);
-  k_rmsnorm<T, O, G, VPT, VEC><<<std::min(resident, (p.n + PER - 1) / PER), TH, 0, stream>>>(
-      (const T*)p.X, p.ldx, (const T*)p.R, p.ldr, p.gamma, p.D, p.n, p.eps, (T*)p.H, p.ldh, (O*)p.Y, p.ldy, p.scale);
+  k_rmsnorm<T, O, G, VPT, VEC><<<std::min(resident, (p.n + PER - 1) / PER), TH, plan.smem, stream>>>(
+      (const T*)p.X, p.ldx, (const T*)p.R, p.ldr, p.gamma, p.D, p.n, p.eps, (T*)p.H, p.ldh, (O*)p.Y, p.ldy, p.scale, plan.stages, wait);
   CR_CHECK_LAUNCH("k_rmsnorm");
   return CR_OK;
 }
@@ -401,19 +493,20 @@ struct Bwd {
 };
 template <class T, int G, int VPT, bool VEC>
 cr_status launch_bwd(const Bwd& p, cudaStream_t stream) {
-  constexpr int TH = threads_of(G), PER = TH / G;
-  static const int resident = [] {
-    int b = 0;
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, k_rmsnorm_bwd<T, G, VPT, VEC>, TH, 0);
-    return std::max(b, 1) * sm_count();
-  }();
+  constexpr int PER = G ? NT / 32 : 1;
+  const int TH = threads_for(G, VPT, p.D);
+  const Plan plan(VEC, PER, 3, p.D, sizeof(T));
+  Wait wait = {option_wait_ns(), nullptr};
+  CR_TRY(wait_word(&wait.err));
+  int resident = 0;
+  CR_TRY(resident_blocks(k_rmsnorm_bwd<T, G, VPT, VEC>, TH, plan.smem, &resident));
   const int blocks = std::min(resident, (p.n + PER - 1) / PER);
   float* part = nullptr;
   if (p.dgamma) CR_CUDA(scratch_alloc((void**)&part, (size_t)blocks * p.D * sizeof(float), stream));
   {
     TimedScope ts("k_rmsnorm_bwd", stream);
-    k_rmsnorm_bwd<T, G, VPT, VEC><<<blocks, TH, 0, stream>>>((const T*)p.H, p.ldh, p.gamma, (const T*)p.dY, p.lddy, (const T*)p.dH,
-                                                             p.lddh, p.D, p.n, p.eps, (T*)p.dX, p.lddx, part);
+    k_rmsnorm_bwd<T, G, VPT, VEC><<<blocks, TH, plan.smem, stream>>>((const T*)p.H, p.ldh, p.gamma, (const T*)p.dY, p.lddy, (const T*)p.dH,
+                                                             p.lddh, p.D, p.n, p.eps, (T*)p.dX, p.lddx, part, plan.stages, wait);
     count_launch();
   }
   const cudaError_t e = cudaGetLastError();
@@ -461,7 +554,7 @@ extern "C" cr_status cr_rmsnorm(int type, const void* d_X, int ldx, const void* 
         CR_CHECK_LAUNCH("k_rmsnorm_long");
         return CR_OK;
       }
-      const bool vec = D % 8 == 0 && ok16(d_X, ldx, eb) && ok16(d_R, ldr, eb) && ok16(d_H, ldh, eb) &&
+      const bool vec = D % 8 == 0 && ring_fits(2, D, eb) && ok16(d_X, ldx, eb) && ok16(d_R, ldr, eb) && ok16(d_H, ldh, eb) &&
                        (sizeof(O) == 1 ? ((uintptr_t)d_Y & 7) == 0 && ldy % 8 == 0 : ok16(d_Y, ldy, sizeof(O)));
       return with_split(D, vec, [&](auto g, auto v, auto w) -> cr_status {
         return launch_fwd<E, O, decltype(g)::value, decltype(v)::value, decltype(w)::value>(
@@ -508,7 +601,7 @@ extern "C" cr_status cr_rmsnorm_backward(int type, const void* d_H, int ldh, con
       return CR_OK;
     }
     const int eb = sizeof(E);
-    const bool vec = D % 8 == 0 && ok16(d_H, ldh, eb) && ok16(d_dY, lddy, eb) && ok16(d_dH, lddh, eb) && ok16(d_dX, lddx, eb);
+    const bool vec = D % 8 == 0 && ring_fits(3, D, eb) && ok16(d_H, ldh, eb) && ok16(d_dY, lddy, eb) && ok16(d_dH, lddh, eb) && ok16(d_dX, lddx, eb);
     return with_split(D, vec, [&](auto g, auto v, auto w) -> cr_status {
       return launch_bwd<E, decltype(g)::value, decltype(v)::value, decltype(w)::value>(
           Bwd{d_H, d_dY, d_dH, ldh, lddy, lddh, d_gamma, D, T, (float)eps, d_dX, lddx, d_dgamma}, stream);

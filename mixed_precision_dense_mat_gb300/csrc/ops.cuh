@@ -20,7 +20,9 @@ cr_status wait_word(int** d_word);
 cr_status make_tensor_map_2d(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
                              int box_outer);
 
-// The same without a swizzle, for tiles that threads read.
+// The same in the 64-byte swizzle, for output tiles, and without one, for tiles that threads read.
+cr_status make_tensor_map_2d_out(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
+                                 int box_outer);
 cr_status make_tensor_map_2d_plain(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
                                    int box_outer);
 
@@ -52,6 +54,64 @@ template <> __device__ __forceinline__ __half from_float<__half>(float x) { retu
 template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 template <> __device__ __forceinline__ __nv_fp8_e4m3 from_float<__nv_fp8_e4m3>(float x) { return __nv_fp8_e4m3(x); }
 
+// Two neighbours at a time: one conversion instruction, where element by element each needs one and
+// the halves have to be put together.
+__device__ __forceinline__ float2 widen2(uint32_t w, __half) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+__device__ __forceinline__ float2 widen2(uint32_t w, __nv_bfloat16) {   // BF16 is the upper half of FP32
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t narrow2(float a, float b, __half) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t narrow2(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t narrow2(float a, float b, __nv_fp8_e4m3) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+// 8 consecutive elements as they are in memory.
+template <class T>
+struct alignas(sizeof(T) == 1 ? 8 : 16) Eight {
+  uint32_t w[2 * sizeof(T)];
+};
+template <class T>
+__device__ __forceinline__ void widen8(const Eight<T>& p, float (&v)[8]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float2 f = widen2(p.w[q], T{});
+    v[2 * q] = f.x;
+    v[2 * q + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void widen8(const Eight<float>& p, float (&v)[8]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(p.w[q]);
+}
+template <class T>
+__device__ __forceinline__ Eight<T> narrow8(const float* v) {
+  Eight<T> p;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) p.w[q] = narrow2(v[2 * q], v[2 * q + 1], T{});
+  return p;
+}
+template <>
+__device__ __forceinline__ Eight<__nv_fp8_e4m3> narrow8<__nv_fp8_e4m3>(const float* v) {
+  Eight<__nv_fp8_e4m3> p;
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    p.w[q] = narrow2(v[4 * q], v[4 * q + 1], __nv_fp8_e4m3{}) | narrow2(v[4 * q + 2], v[4 * q + 3], __nv_fp8_e4m3{}) << 16;
+  return p;
+}
+template <>
+__device__ __forceinline__ Eight<float> narrow8<float>(const float* v) {
+  Eight<float> p;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) p.w[q] = __float_as_uint(v[q]);
+  return p;
+}
+
 inline int type_bytes(int type) {
   return type == CR_TYPE_F32 ? 4 : type == CR_TYPE_E4M3 ? 1 : 2;
 }
@@ -65,25 +125,53 @@ cr_status with_type(int type, F&& f) {
 }
 
 // ---------------------------------------------------------------- activations
-// e = exp(-|x|) never overflows; sigmoid of both signs without cancellation.
-__device__ __forceinline__ void sigmoid_pair(float x, float& p, float& q) {   // p = sigmoid(x), q = sigmoid(-x)
-  const float e = expf(-fabsf(x));
-  const float big = __fdividef(1.0f, 1.0f + e), small = e * big;
-  p = x >= 0.0f ? big : small;
-  q = x >= 0.0f ? small : big;
-  if (x != x) p = q = x;
+// Written from the hardware's 2^x and reciprocal (each within about 2^-22), because a product's
+// epilogue shares the SM's issue slots and power with the MMAs: with expf and erfcf the K = 4096,
+// N = 16384, M = 8192 product took ACTNOTE.  Arguments are clamped where the
+// function has reached its limit, so that infinities give limits; NaN stays.
+__device__ __forceinline__ float clamp_low(float x, float low) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(low));
+  return x;
+}
+__device__ __forceinline__ float clamp_high(float x, float high) {
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(high));
+  return x;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x));
+  return x;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x));
+  return x;
+}
+constexpr float LOG2E = 1.4426950408889634f;
+
+// 1 - Phi(|z|) times 2, and g = e^(-z^2 / 2): erfc by Hastings' rational-exponential formula (Abramowitz and
+// Stegun, Handbook of Mathematical Functions, 7.1.26), absolute error 1.5e-7.
+__device__ __forceinline__ float normal_tail(float z, float& g) {
+  const float t = rcp_fast(fmaf(fabsf(z), 0.3275911f * 0.70710678118654752f, 1.0f));
+  g = exp2_fast(z * z * (-0.5f * LOG2E));
+  float p = fmaf(t, 1.061405429f, -1.453152027f);
+  p = fmaf(t, p, 1.421413741f);
+  p = fmaf(t, p, -0.284496736f);
+  p = fmaf(t, p, 0.254829592f);
+  return t * p * g;
 }
 
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
-  if (ACT == CR_ACT_RELU) return z < 0.0f ? 0.0f : z;   // NaN stays
+  if (ACT == CR_ACT_RELU) return clamp_low(z, 0.0f);
   if (ACT == CR_ACT_SILU) {
-    // z e^z -> -0 as z -> -inf, where z sigmoid(z) would be inf * 0
-    float p, q;
-    sigmoid_pair(z, p, q);
-    return z == -INFINITY ? -0.0f : z * p;
+    z = clamp_low(z, -87.0f);
+    return z * rcp_fast(1.0f + exp2_fast(z * -LOG2E));
   }
-  if (ACT == CR_ACT_GELU) return z == -INFINITY ? -0.0f : 0.5f * z * erfcf(-z * 0.70710678118654752f);
+  if (ACT == CR_ACT_GELU) {
+    z = clamp_low(z, -30.0f);
+    float g;
+    const float half = 0.5f * normal_tail(z, g);
+    return z * (z < 0.0f ? half : 1.0f - half);
+  }
   return z;
 }
 
@@ -91,13 +179,15 @@ template <int ACT>
 __device__ __forceinline__ float activation_slope(float z) {
   if (ACT == CR_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
   if (ACT == CR_ACT_SILU) {
-    float p, q;
-    sigmoid_pair(z, p, q);
-    return fabsf(z) == INFINITY ? p : p * fmaf(z, q, 1.0f);
+    z = clamp_high(clamp_low(z, -87.0f), 87.0f);
+    const float e = exp2_fast(z * -LOG2E), p = rcp_fast(1.0f + e);
+    return p * fmaf(z, e * p, 1.0f);
   }
   if (ACT == CR_ACT_GELU) {
-    const float cdf = 0.5f * erfcf(-z * 0.70710678118654752f);
-    return fabsf(z) == INFINITY ? cdf : fmaf(z * 0.39894228040143268f, expf(-0.5f * z * z), cdf);
+    z = clamp_high(clamp_low(z, -30.0f), 30.0f);
+    float g;
+    const float half = 0.5f * normal_tail(z, g);
+    return fmaf(z * 0.39894228040143268f, g, z < 0.0f ? half : 1.0f - half);
   }
   return 1.0f;
 }
@@ -181,15 +271,14 @@ struct GateParts {
 template <int GATE, int VEC>
 __device__ __forceinline__ GateParts<VEC> gate_parts(Floats<VEC> g) {
   if (GATE == CR_GATE_COEFF) return {g, all_of<VEC>(1.0f)};
-  Floats<VEC> e = mul(g, all_of<VEC>(-1.4426950408889634f));
+  Floats<VEC> e = mul(g, all_of<VEC>(-LOG2E));
 #pragma unroll
   for (int q = 0; q < VEC; ++q) {
-    asm("min.NaN.f32 %0, %0, %1;" : "+f"(e.x[q]) : "f"(125.5f));
-    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x[q]));
+    e.x[q] = exp2_fast(clamp_high(e.x[q], 125.5f));
   }
   Floats<VEC> r = add(e, all_of<VEC>(1.0f));
 #pragma unroll
-  for (int q = 0; q < VEC; ++q) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(r.x[q]));
+  for (int q = 0; q < VEC; ++q) r.x[q] = rcp_fast(r.x[q]);
   return {r, mul(e, r)};
 }
 template <int VEC>
