@@ -66,7 +66,7 @@ __device__ __forceinline__ void gave_up(const Params& p, volatile int* abort) {
   __threadfence_system();
 }
 
-constexpr int OROW = 64, WBUF = 2 * 32 * OROW;   // an epilogue warp's rows on their way out: two tiles of 64-byte rows
+constexpr int OROW = 128, WBUF = 32 * OROW;      // an epilogue warp's rows on their way out: one tile of 128-byte rows
 
 // z (a finished sum) to the output (i, j).
 template <class O>
@@ -76,7 +76,7 @@ __device__ __forceinline__ void finish(const Params& p, int i, int j, float z) {
   if (p.e.bias) z += p.e.bias[i];
   if (p.e.Z) ((O*)p.e.Z)[(size_t)j * p.e.ldz + i] = from_float<O>(z);
   float v[1] = {z};
-  activate_all(v, p.e.act);
+  activate_all<1>(v, p.e.act);
   if (p.e.R) v[0] += to_float(((const O*)p.e.R)[(size_t)j * p.e.ldr + i]);
   ((O*)p.e.C)[(size_t)j * p.e.ldc + i] = from_float<O>(v[0]);
 }
@@ -109,7 +109,7 @@ __device__ __forceinline__ void thin_finish4(const Params& p, int i, int j, floa
     *reinterpret_cast<Four*>((O*)out + (size_t)j * ld + i) = o;
   };
   if (e.Z) put(e.Z, e.ldz);
-  activate_all(v, e.act);
+  activate_all<4>(v, e.act);
   if (e.R) {
     const Four r = *reinterpret_cast<const Four*>((const O*)e.R + (size_t)j * e.ldr + i);
 #pragma unroll
@@ -129,7 +129,7 @@ __device__ __forceinline__ void thin_store16(const Params& p, int i, int j0, flo
       v[q] = fmaf(v[q] * is, p.e.jscale ? p.e.jscale[j0 + q] : 1.0f, b);
       if (p.e.Z) ((O*)p.e.Z)[(size_t)(j0 + q) * p.e.ldz + i] = from_float<O>(v[q]);
     }
-  activate_all(v, p.e.act);
+  activate_all<16>(v, p.e.act);
 #pragma unroll
   for (int q = 0; q < 16; ++q)
     if (q < n) {
@@ -156,27 +156,29 @@ __device__ __forceinline__ void load_row(const float* x, int i0, int I, int vec,
   }
 }
 
-// The warp's 32 rows j of N = OROW / sizeof(O) values from (i0, j0): through shared memory (rows of 64
-// bytes in the 64-byte swizzle) and by TMA, or element by element where TMA cannot address them.
+// The warp's 32 rows j of N = OROW / sizeof(O) values from (i0, j0): through shared memory (rows of 128
+// bytes in the 128-byte swizzle) and by TMA, or element by element where TMA cannot address them.
 template <class O, int N>
-__device__ __forceinline__ void put_rows(const CUtensorMap* tm, int tma, O* out, int ld, int I, int J, int i0, int j0, uint8_t*& buf,
-                                         const float (&v)[N]) {
+__device__ __forceinline__ void put_rows(const CUtensorMap* tm, int tma, O* out, int ld, int I, int J, int i0, int j0, uint8_t* buf,
+                                         const float* v) {
   const int lane = threadIdx.x & 31;
   if (tma) {
-    if (lane == 0) tma_store_wait_read();   // this buffer's last tile has been read (the other's may not)
+    if (lane == 0) tma_store_wait_read();   // the buffer's last tile has been read
     __syncwarp();
 #pragma unroll
     for (int q = 0; q < N / 8; ++q) {
       const Eight<O> w = narrow8<O>(v + 8 * q);
 #pragma unroll
       for (int x = 0; x < (int)sizeof(O) / 2; ++x)
-        *reinterpret_cast<uint4*>(buf + lane * OROW + (((int)sizeof(O) / 2 * q + x) ^ (lane >> 1 & 3)) * 16) =
+        *reinterpret_cast<uint4*>(buf + lane * OROW + (((int)sizeof(O) / 2 * q + x) ^ (lane & 7)) * 16) =
             make_uint4(w.w[4 * x], w.w[4 * x + 1], w.w[4 * x + 2], w.w[4 * x + 3]);
     }
     fence_smem_to_tma();
     __syncwarp();
-    if (lane == 0) tma_store_2d(tm, buf, i0, j0, j0 < J);
-    buf = reinterpret_cast<uint8_t*>(reinterpret_cast<uintptr_t>(buf) ^ (WBUF / 2));
+    if (lane == 0 && j0 < J) {
+      tma_store_2d(tm, buf, i0, j0);
+      tma_store_commit();
+    }
   } else if (j0 + lane < J) {
     O* o = out + (size_t)(j0 + lane) * ld + i0;
 #pragma unroll
@@ -188,27 +190,33 @@ __device__ __forceinline__ void put_rows(const CUtensorMap* tm, int tma, O* out,
 // Epilogue of the warp's 32 rows j and N columns i; v holds the sums.
 template <class O, int N>
 __device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* tmC, const CUtensorMap* tmZ, int i0, int j0, float js,
-                                            uint8_t*& buf, float (&v)[N]) {
+                                            uint8_t* buf, float* v) {
   const Epilogue& e = p.e;
   const int j = j0 + (threadIdx.x & 31);
   if (e.iscale) {
-    float w[N];
-    load_row(e.iscale, i0, p.I, p.vecb, w);
 #pragma unroll
-    for (int q = 0; q < N; ++q) v[q] *= w[q];
+    for (int q = 0; q < N; q += 8) {
+      float w[8];
+      load_row(e.iscale, i0 + q, p.I, p.vecb, w);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[q + x] *= w[x];
+    }
   }
   if (e.jscale) {
 #pragma unroll
     for (int q = 0; q < N; ++q) v[q] *= js;
   }
   if (e.bias) {
-    float w[N];
-    load_row(e.bias, i0, p.I, p.vecb, w);
 #pragma unroll
-    for (int q = 0; q < N; ++q) v[q] += w[q];
+    for (int q = 0; q < N; q += 8) {
+      float w[8];
+      load_row(e.bias, i0 + q, p.I, p.vecb, w);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[q + x] += w[x];
+    }
   }
   if (e.Z) put_rows<O, N>(tmZ, p.tma_z, (O*)e.Z, e.ldz, p.I, p.J, i0, j0, buf, v);
-  activate_all(v, e.act);
+  activate_all<N>(v, e.act);
   if (e.R && j < p.J) {
     const O* r = (const O*)e.R + (size_t)j * e.ldr + i0;
     if (p.vec_r && i0 + N <= p.I) {
@@ -383,19 +391,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
       const float js = p.e.jscale && j0 + lane < p.J ? p.e.jscale[j0 + lane] : 1.0f;
       constexpr int N = OROW / (int)sizeof(O);
       for (int c = 0; c < 128; c += N) {
-        float v[N];
+        uint32_t v[N / 32][32];
         __syncwarp();
-        if constexpr (N == 32) tmem_ld32(tq + (uint32_t)c, v);
-        else tmem_ld16(tq + (uint32_t)c, v);
+#pragma unroll
+        for (int q = 0; q < N / 32; ++q) tmem_ld32(tq + (uint32_t)(c + 32 * q), v[q]);
+        tmem_ld_wait();
         if (c + N == 128) {   // the accumulator is read: the next tile but one may have it
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(tempty[b]);
         }
-        if (ibase + c < p.I) wide_finish<O, N>(p, &tmC, &tmZ, ibase + c, j0, js, buf, v);
+        if (ibase + c < p.I) wide_finish<O, N>(p, &tmC, &tmZ, ibase + c, j0, js, buf, reinterpret_cast<float*>(v));
       }
     }
-    if (lane == 0) tma_store_wait_all();
+    if (lane == 0) tma_store_wait_read();
   }
   __syncwarp();
   tc_fence_before();
@@ -728,6 +737,27 @@ cr_status launch(const CUtensorMap& tmP, const CUtensorMap& tmQ, const CUtensorM
   return CR_OK;
 }
 
+// Parts of k and stages for the thin kernel: the most parts for which all CTAs are resident at once, up
+// to three per SM with three stages each and two stages' worth of k for each; a second wave of
+// CTAs, or an SM with none, costs more than longer parts (K = 4096, N = 12288, M = 16 FP16: 96 CTAs
+// with 8 stages 23.5 us, 192 with 4 22.2 us, 384 with 3 20.8 us, 384 with 4, no longer resident at
+// once, 25.8 us).
+void thin_split(const Params& p, int& split, int& stages) {
+  const long long tiles = (long long)p.ti * p.tj;
+  const int stage = WTILE + (p.qk ? p.bn * KBYTES : (p.bn + 63) / 64 * ATOM);
+  const auto fits = [&](int s, int per_sm) {
+    return std::min<long long>(TMAXSTAGES, (227 * 1024 / per_sm - 2560 - (s > 1 ? 512 * p.bn : 0)) / stage);
+  };
+  split = 1;
+  stages = (int)fits(1, tiles > sm_count() ? 2 : 1);
+  for (int s = 2; s <= 8; s *= 2) {
+    const long long per_sm = (tiles * s + sm_count() - 1) / sm_count();
+    if (per_sm > 3 || p.kblocks < 2 * s || fits(s, (int)per_sm) < 3 || stage * fits(s, (int)per_sm) < 512 * p.bn) continue;
+    split = s;
+    stages = (int)fits(s, (int)per_sm);
+  }
+}
+
 cr_status product(Operand P, Operand Q, int type, int K, int out_type, const Epilogue& e, cudaStream_t stream) {
   Params p = {};
   CR_TRY(wait_word(&p.err));
@@ -757,16 +787,16 @@ cr_status product(Operand P, Operand Q, int type, int K, int out_type, const Epi
     p.tj = (p.J + 255) / 256;
     p.idesc = idesc_of(256, 256, type == CR_TYPE_BF16, !p.qk, !p.pk);
   } else {
-    p.bn = p.J <= 16 ? 16 : p.J <= 32 ? 32 : p.J <= 64 ? 64 : 128;
     p.ti = (p.I + 127) / 128;
+    p.bn = p.J <= 16 ? 16 : p.J <= 32 ? 32 : 64;
+    if (p.J > 64 && (long long)p.ti * ((p.J + 127) / 128) >= sm_count()) p.bn = 128;
     p.tj = (p.J + p.bn - 1) / p.bn;
     p.idesc = idesc_of(128, p.bn, type == CR_TYPE_BF16, !p.pk, !p.qk);
-    while (split < 8 && (long long)p.ti * p.tj * split < 2 * sm_count() && p.kblocks >= 4 * split) split *= 2;
-    stages = std::min(p.bn <= 32 ? 5 : p.bn == 64 ? 4 : 3, 8);
+    thin_split(p, split, stages);
   }
   CUtensorMap tmP = {}, tmQ = {}, tmC = {}, tmZ = {};
-  if (wide && p.tma_c) CR_TRY(make_tensor_map_2d_out(&tmC, out_type, e.C, p.I, p.J, e.ldc, OROW / ob, 32));
-  if (wide && e.Z && p.tma_z) CR_TRY(make_tensor_map_2d_out(&tmZ, out_type, e.Z, p.I, p.J, e.ldz, OROW / ob, 32));
+  if (wide && p.tma_c) CR_TRY(make_tensor_map_2d(&tmC, out_type, e.C, p.I, p.J, e.ldc, OROW / ob, 32));
+  if (wide && e.Z && p.tma_z) CR_TRY(make_tensor_map_2d(&tmZ, out_type, e.Z, p.I, p.J, e.ldz, OROW / ob, 32));
   CR_TRY(map_of(&tmP, P, type, K, 128));
   CR_TRY(map_of(&tmQ, Q, type, K, wide ? 128 : p.bn));
   return with_type(out_type, [&](auto o0) -> cr_status {

@@ -187,10 +187,6 @@ cr_status make_tensor_map_2d(CUtensorMap* tm, int type, const void* base, int in
                              int box_outer) {
   return tensor_map_2d(tm, type, base, inner, outer, ld, box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_128B);
 }
-cr_status make_tensor_map_2d_out(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
-                                 int box_outer) {
-  return tensor_map_2d(tm, type, base, inner, outer, ld, box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_64B);
-}
 cr_status make_tensor_map_2d_plain(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
                                    int box_outer) {
   return tensor_map_2d(tm, type, base, inner, outer, ld, box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_NONE);

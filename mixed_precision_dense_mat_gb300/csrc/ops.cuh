@@ -20,9 +20,7 @@ cr_status wait_word(int** d_word);
 cr_status make_tensor_map_2d(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
                              int box_outer);
 
-// The same in the 64-byte swizzle, for output tiles, and without one, for tiles that threads read.
-cr_status make_tensor_map_2d_out(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
-                                 int box_outer);
+// The same without a swizzle, for tiles that threads read.
 cr_status make_tensor_map_2d_plain(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
                                    int box_outer);
 
@@ -194,7 +192,7 @@ __device__ __forceinline__ float activation_slope(float z) {
 
 // v[] = act(v[]) with one test of `act` for all of them.
 template <int N>
-__device__ __forceinline__ void activate_all(float (&v)[N], int act) {
+__device__ __forceinline__ void activate_all(float* v, int act) {
   if (act == CR_ACT_RELU) {
 #pragma unroll
     for (int q = 0; q < N; ++q) v[q] = activate<CR_ACT_RELU>(v[q]);
