@@ -33,7 +33,7 @@ struct Params {
   int pk, qk;            // operand P, Q is k-major
   uint32_t idesc;        // MMA instruction descriptor
   int ti, tj;            // output tiles
-  int bn;                // thin kernel: columns of its tile
+  int bn;                // thin kernel: columns j of its tile
   int tma_c, tma_z;      // C, Z can be stored by TMA
   int vec_r;             // R allows 16-byte accesses
   int vecb;              // bias and iscale do
@@ -239,7 +239,8 @@ __device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* 
 
 // ---------------------------------------------------------------- wide kernel
 // 256 x 256 outputs per CTA pair (cta_group::2): the pair's MMA has M = 256 rows j (128 per CTA, its
-// operand A = Q) and N = 256 columns i (operand B = P, half of it in each CTA).  Persistent;
+// operand A = Q) and N = 256 columns i (operand B = P, half of it in each CTA; N = 128 takes as long per
+// k-block, 0.27 us).  Persistent;
 // warp 0 loads by TMA into a ring of stages, warp 1 of the first CTA issues the MMAs, warps 2-9
 // take the accumulator (two of them in TMEM, so the epilogue of one tile overlaps the next
 // tile's products) through the epilogue: a thread holds one j and 32 consecutive i.
@@ -602,6 +603,59 @@ __global__ void __launch_bounds__(TTHREADS)
   }
 }
 
+// ---------------------------------------------------------------- a few columns
+// One warp per output i, one or two columns: P is read once, straight into registers, with no
+// shared-memory pipeline, tensor memory or cluster to set up, whose latency is most of a small
+// call's time (K = N = 2048, M = 1 BF16: 3.6 us, the thin kernel 6.2 us).  With more columns reading Q
+// again for each output costs more than that (M = 4: 7.7 and 6.4 us), and with more outputs than
+// resident warps a second round does (K = 4096, N = 12288, M = 1: 28.6 and 19.9 us).  V = 16 / sizeof(E)
+// elements at a time where P and Q are aligned, else one.
+constexpr int FEW = 2;
+template <class E, int V>
+__device__ __forceinline__ void widen(const E* p, float (&v)[V]) {
+  if constexpr (V == 1) {
+    v[0] = to_float(*p);
+  } else if constexpr (sizeof(E) == 2) {
+    widen8(*reinterpret_cast<const Eight<E>*>(p), v);
+  } else {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u[q / 2] >> (16 * (q & 1))), __NV_E4M3);
+      const float2 f = __half22float2(__half2(h));
+      v[2 * q] = f.x;
+      v[2 * q + 1] = f.y;
+    }
+  }
+}
+template <class E, class O, int V, int M>
+__global__ void __launch_bounds__(NT) k_affine_few(const E* P, int ldp, const E* Q, int ldq, int K, const Params p) {
+  const int lane = threadIdx.x & 31, i = blockIdx.x * (NT / 32) + (threadIdx.x >> 5);
+  if (i >= p.I) return;
+  const E* row = P + (size_t)i * ldp;
+  float s[M] = {};
+#pragma unroll 4
+  for (int k = lane * V; k < K; k += 32 * V) {
+    float w[V];
+    widen<E, V>(row + k, w);
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      float x[V];
+      widen<E, V>(Q + (size_t)j * ldq + k, x);
+#pragma unroll
+      for (int q = 0; q < V; ++q) s[j] = fmaf(w[q], x[q], s[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < M; ++j)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
+#pragma unroll
+  for (int j = 0; j < M; ++j)
+    if (lane == j) finish<O>(p, i, j, s[j]);
+}
+
 // Copies a matrix whose columns of n elements start at any address into columns ld apart.
 template <class E>
 __global__ void __launch_bounds__(NT) k_pack(const E* src, int lds, int n, int m, E* dst, int ld) {
@@ -737,25 +791,99 @@ cr_status launch(const CUtensorMap& tmP, const CUtensorMap& tmQ, const CUtensorM
   return CR_OK;
 }
 
-// Parts of k and stages for the thin kernel: the most parts for which all CTAs are resident at once, up
-// to three per SM with three stages each and two stages' worth of k for each; a second wave of
-// CTAs, or an SM with none, costs more than longer parts (K = 4096, N = 12288, M = 16 FP16: 96 CTAs
-// with 8 stages 23.5 us, 192 with 4 22.2 us, 384 with 3 20.8 us, 384 with 4, no longer resident at
-// once, 25.8 us).
-void thin_split(const Params& p, int& split, int& stages) {
-  const long long tiles = (long long)p.ti * p.tj;
-  const int stage = WTILE + (p.qk ? p.bn * KBYTES : (p.bn + 63) / 64 * ATOM);
-  const auto fits = [&](int s, int per_sm) {
-    return std::min<long long>(TMAXSTAGES, (227 * 1024 / per_sm - 2560 - (s > 1 ? 512 * p.bn : 0)) / stage);
+// Clusters of s CTAs that are resident at once with c CTAs per SM: fewer than SMs x c / s (15 of 8, 36 of 4
+// on a GB300's 152 SMs), because a cluster's CTAs share a GPC.
+int resident_clusters(int s, int c) {
+  struct Table {
+    int n[4] = {};
+    Table() {
+      const auto kernel = k_affine_thin<false, __half>;
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+      for (int e = 0; e < 4; ++e) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 1 << e;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(4096 << e);
+        cfg.blockDim = dim3(TTHREADS);
+        cfg.dynamicSmemBytes = 200 * 1024;   // one CTA per SM
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n[e], kernel, &cfg) != cudaSuccess) {
+          cudaGetLastError();
+          n[e] = sm_count() / (1 << e);
+        }
+      }
+    }
   };
-  split = 1;
-  stages = (int)fits(1, tiles > sm_count() ? 2 : 1);
-  for (int s = 2; s <= 8; s *= 2) {
-    const long long per_sm = (tiles * s + sm_count() - 1) / sm_count();
-    if (per_sm > 3 || p.kblocks < 2 * s || fits(s, (int)per_sm) < 3 || stage * fits(s, (int)per_sm) < 512 * p.bn) continue;
-    split = s;
-    stages = (int)fits(s, (int)per_sm);
+  static const Table table;
+  return c * table.n[s == 1 ? 0 : s == 2 ? 1 : s == 4 ? 2 : 3];
+}
+
+// Which kernel, with which tiles.  Times in microseconds from the rates measured on GB300 (K = 1024 to
+// 8192, N = 1024 to 16384, M = 1 to 8192); the choice only has to be right where they differ.
+struct Choice {
+  bool wide;
+  int bn, split, stages;
+  double us;
+};
+Choice choose(int I, int J, int kblocks, bool qk) {
+  Choice best = {false, 0, 1, 0, 1e30};
+  const auto tiles = [](int n, int t) { return (n + t - 1) / t; };
+  // Wide: rounds of tiles over the CTA pairs, 0.27 to 0.3 us per k-block.
+  if (J > 128) {
+    const long long t = (long long)tiles(I, 256) * tiles(J, 256), rounds = (t + sm_count() / 2 - 1) / (sm_count() / 2);
+    best = {true, 0, 1, 0, 9.4 + rounds * (kblocks * 0.29 + 1.0)};
   }
+  // Thin: parts of k for which all clusters are resident at once, with three stages or more and two
+  // k-blocks or more for each CTA; a second wave of CTAs costs more than longer parts (K = 4096,
+  // N = 12288, M = 16 FP16: 96 CTAs with 8 stages 23.5 us, 192 with 4 22.2 us, 384 with 3 20.8 us, 384
+  // with 4, no longer resident at once, 25.8 us).  An SM takes in about 100 KB per microsecond, HBM
+  // gives less to fewer CTAs, and joining the parts costs 1 us at 16 columns, 5 at 128.
+  for (int bn = J <= 16 ? 16 : J <= 32 ? 32 : 64; bn <= (J > 64 ? 128 : 64); bn *= 2) {
+    const int stage = WTILE + (qk ? bn * KBYTES : (bn + 63) / 64 * ATOM);
+    const long long t = (long long)tiles(I, 128) * tiles(J, bn);
+    for (int split = 8; split >= 1; split /= 2) {
+      if (split > 1 && kblocks < 2 * split) continue;
+      int per = 1;
+      while (per < 3 && t > resident_clusters(split, per)) ++per;
+      if (t > resident_clusters(split, per)) {
+        if (split > 1) continue;
+        per = 2;
+      }
+      const int received = split > 1 ? 512 * bn : 0;
+      const int stages = std::min(TMAXSTAGES, (227 * 1024 / per - 3584 - received) / stage);
+      if (stages < (split > 1 ? 3 : 2) || (split > 1 && stages * stage < received)) continue;
+      const double ctas = (double)t * split, waves = std::max(1.0, ctas / sm_count());
+      const double hbm = (double)I * kblocks * KBYTES / 5.5e6 * (1.0 + 0.25 * std::max(0.0, 1.0 - ctas / (2.5 * sm_count())));
+      const double us = 5.0 + (split > 1 ? 0.3 + 0.04 * bn : 0.0) + std::max(waves * tiles(kblocks, split) * stage / 100e3, hbm);
+      if (us < best.us) best = {false, bn, split, stages, us};
+    }
+    if (J <= 64) break;
+  }
+  return best;
+}
+
+template <class E, class O>
+cr_status few(const Operand& P, const Operand& Q, int K, const Params& p, cudaStream_t stream) {
+  const E *a = (const E*)P.ptr, *b = (const E*)Q.ptr;
+  constexpr int V = 16 / (int)sizeof(E);
+  const bool vec = (((uintptr_t)a | (uintptr_t)b) & 15) == 0 && P.ld % V == 0 && Q.ld % V == 0 && K % V == 0;
+  const unsigned grid = (unsigned)((p.I + NT / 32 - 1) / (NT / 32));
+  const auto run = [&](auto v, auto m) {
+    k_affine_few<E, O, decltype(v)::value, decltype(m)::value><<<grid, NT, 0, stream>>>(a, P.ld, b, Q.ld, K, p);
+  };
+  const auto by_m = [&](auto v) {
+    using std::integral_constant;
+    if (p.J == 1) run(v, integral_constant<int, 1>{});
+    else run(v, integral_constant<int, 2>{});
+  };
+  TimedScope ts("k_affine_few", stream);
+  if (vec) by_m(std::integral_constant<int, V>{});
+  else by_m(std::integral_constant<int, 1>{});
+  CR_CHECK_LAUNCH("k_affine_few");
+  return CR_OK;
 }
 
 cr_status product(Operand P, Operand Q, int type, int K, int out_type, const Epilogue& e, cudaStream_t stream) {
@@ -776,24 +904,22 @@ cr_status product(Operand P, Operand Q, int type, int K, int out_type, const Epi
   p.vecb = (((uintptr_t)e.bias | (uintptr_t)e.iscale) & 15) == 0;
   const auto ok4 = [&](const void* q, int ld) { return !q || (((uintptr_t)q & (4 * ob - 1)) == 0 && ld % 4 == 0); };
   p.vec4 = p.vecb && ok4(e.C, e.ldc) && ok4(e.R, e.ldr) && ok4(e.Z, e.ldz);
+  if (p.J <= FEW && p.pk && p.qk && p.I <= 64 * sm_count())
+    return with_type(out_type, [&](auto o0) -> cr_status {
+      using O = decltype(o0);
+      if (type == CR_TYPE_F16) return few<__half, O>(P, Q, K, p, stream);
+      if (type == CR_TYPE_BF16) return few<__nv_bfloat16, O>(P, Q, K, p, stream);
+      return few<__nv_fp8_e4m3, O>(P, Q, K, p, stream);
+    });
   Packed ownP, ownQ;
   CR_TRY(ownP.make(P, type, K, stream));
   CR_TRY(ownQ.make(Q, type, K, stream));
-  const long long wt = ((long long)p.I + 255) / 256 * (((long long)p.J + 255) / 256);
-  const bool wide = p.J > 128 && wt >= 24;
-  int split = 1, stages = 0;
-  if (wide) {
-    p.ti = (p.I + 255) / 256;
-    p.tj = (p.J + 255) / 256;
-    p.idesc = idesc_of(256, 256, type == CR_TYPE_BF16, !p.qk, !p.pk);
-  } else {
-    p.ti = (p.I + 127) / 128;
-    p.bn = p.J <= 16 ? 16 : p.J <= 32 ? 32 : 64;
-    if (p.J > 64 && (long long)p.ti * ((p.J + 127) / 128) >= sm_count()) p.bn = 128;
-    p.tj = (p.J + p.bn - 1) / p.bn;
-    p.idesc = idesc_of(128, p.bn, type == CR_TYPE_BF16, !p.pk, !p.qk);
-    thin_split(p, split, stages);
-  }
+  const Choice ch = choose(p.I, p.J, p.kblocks, p.qk);
+  const bool wide = ch.wide, bf16 = type == CR_TYPE_BF16;
+  p.bn = ch.bn;
+  p.ti = wide ? (p.I + 255) / 256 : (p.I + 127) / 128;
+  p.tj = wide ? (p.J + 255) / 256 : (p.J + p.bn - 1) / p.bn;
+  p.idesc = wide ? idesc_of(256, 256, bf16, !p.qk, !p.pk) : idesc_of(128, p.bn, bf16, !p.pk, !p.qk);
   CUtensorMap tmP = {}, tmQ = {}, tmC = {}, tmZ = {};
   if (wide && p.tma_c) CR_TRY(make_tensor_map_2d(&tmC, out_type, e.C, p.I, p.J, e.ldc, OROW / ob, 32));
   if (wide && e.Z && p.tma_z) CR_TRY(make_tensor_map_2d(&tmZ, out_type, e.Z, p.I, p.J, e.ldz, OROW / ob, 32));
@@ -801,8 +927,8 @@ cr_status product(Operand P, Operand Q, int type, int K, int out_type, const Epi
   CR_TRY(map_of(&tmQ, Q, type, K, wide ? 128 : p.bn));
   return with_type(out_type, [&](auto o0) -> cr_status {
     using O = decltype(o0);
-    return type == CR_TYPE_E4M3 ? launch<true, O>(tmP, tmQ, tmC, tmZ, p, wide, split, stages, stream)
-                                : launch<false, O>(tmP, tmQ, tmC, tmZ, p, wide, split, stages, stream);
+    return type == CR_TYPE_E4M3 ? launch<true, O>(tmP, tmQ, tmC, tmZ, p, wide, ch.split, ch.stages, stream)
+                                : launch<false, O>(tmP, tmQ, tmC, tmZ, p, wide, ch.split, ch.stages, stream);
   });
 }
 
