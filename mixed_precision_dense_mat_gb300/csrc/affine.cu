@@ -273,7 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   WideBars* bars = reinterpret_cast<WideBars*>(smem + WSTAGES * WSTAGE + WEPI * WBUF);
   volatile int* abort_flag = &bars->abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform: the loops below keep their state in uniform registers
   const uint32_t rank = cluster_rank();
   const int ntiles = p.ti * p.tj, ncl = gridDim.x >> 1, cl = blockIdx.x >> 1;
   constexpr int KE = F8 ? 128 : 64;   // k elements per stage
@@ -295,28 +295,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
   __syncthreads();
   cluster_sync_all();
   tc_fence_after();
-  const uint32_t tmem = bars->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem, 0);
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       prefetch_tmap(&tmP);
       prefetch_tmap(&tmQ);
-      uint32_t st = 0, ph = 0;
-      int issued = 0;
-      for (int t = cl; t < ntiles && !*abort_flag; t += ncl) {
-        int ti, tj;
-        wide_tile(p, t, ti, tj);
-        const int i0 = ti * 256 + (int)rank * 128, j0 = tj * 256 + (int)rank * 128;
-        for (int kb = 0; kb < p.kblocks; ++kb) {
-          if (*abort_flag) break;
-          if (!mbar_wait(&bars->empty[st], ph ^ 1u, p.limit)) {
-            gave_up(p, abort_flag);
-            break;
-          }
+    }
+    uint32_t st = 0, ph = 0;
+    int issued = 0;
+    bool ok = true;
+    const uint32_t full0 = cluster_addr(smem_u32(&bars->full[0]), 0);
+    for (int t = cl; t < ntiles && ok; t += ncl) {
+      int ti, tj;
+      wide_tile(p, t, ti, tj);
+      const int i0 = ti * 256 + (int)rank * 128, j0 = tj * 256 + (int)rank * 128;
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        ok = mbar_wait_warp(&bars->empty[st], ph ^ 1u, p.limit);
+        if (!ok) break;
+        if (elect_one()) {
           uint8_t* sa = smem + st * WSTAGE;
           uint8_t* sb = sa + WTILE;
           if (rank == 0) mbar_arrive_expect_tx(&bars->full[st], 2 * WSTAGE);
-          const uint32_t bar = cluster_addr(smem_u32(&bars->full[st]), 0);
+          const uint32_t bar = full0 + 8 * st;
           const int k0 = kb * KE;
           if (p.qk) {
             tma_load_2d_pair(sa, &tmQ, bar, k0, j0);
@@ -330,47 +331,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
             tma_load_2d_pair(sb, &tmP, bar, i0, k0);
             tma_load_2d_pair(sb + ATOM, &tmP, bar, i0 + 64, k0);
           }
-          ++issued;
-          if (++st == WSTAGES) st = 0, ph ^= 1u;
         }
+        ++issued;
+        if (++st == WSTAGES) st = 0, ph ^= 1u;
       }
-      if (*abort_flag && rank == 0) {   // the pair's copies in flight land before either CTA leaves
-        for (int q = min(issued, WSTAGES); q > 0; --q) {
-          const int n = issued - q;
-          mbar_wait(&bars->full[n % WSTAGES], (uint32_t)(n / WSTAGES) & 1u, p.limit);
-        }
+    }
+    if (!ok) {   // gave up: the pair's copies in flight land before either CTA leaves
+      if (lane == 0) gave_up(p, abort_flag);
+      for (int q = min(issued, WSTAGES); rank == 0 && q > 0; --q) {
+        const int n = issued - q;
+        mbar_wait(&bars->full[n % WSTAGES], (uint32_t)(n / WSTAGES) & 1u, p.limit);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       uint32_t st = 0, ph = 0;
       int u = 0;
-      const uint32_t ps = desc_step(p.pk), qs = desc_step(p.qk);
-      for (int t = cl; t < ntiles && !*abort_flag; t += ncl, ++u) {
+      bool ok = true;
+      const uint32_t ps = desc_step(p.pk), qs = desc_step(p.qk), s0 = smem_u32(smem);
+      const uint64_t da0 = tile_desc(s0, p.qk), db0 = tile_desc(s0 + WTILE, p.pk);
+      for (int t = cl; t < ntiles && ok; t += ncl, ++u) {
         const int b = u & 1;
-        if (!mbar_wait(&bars->tempty[b], ((uint32_t)(u >> 1) & 1u) ^ 1u, p.limit)) {
-          gave_up(p, abort_flag);
-          break;
-        }
+        ok = mbar_wait_warp(&bars->tempty[b], ((uint32_t)(u >> 1) & 1u) ^ 1u, p.limit);
+        if (!ok) break;
         tc_fence_after();
         const uint32_t acc = tmem + (uint32_t)(b * 256);
         for (int kb = 0; kb < p.kblocks; ++kb) {
-          if (*abort_flag) break;
-          if (!mbar_wait(&bars->full[st], ph, p.limit)) {
-            gave_up(p, abort_flag);
-            break;
-          }
+          ok = mbar_wait_warp(&bars->full[st], ph, p.limit);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + st * WSTAGE);
-          const uint64_t da = tile_desc(sa, p.qk), db = tile_desc(sa + WTILE, p.pk);
+          if (elect_one()) {
+            const uint64_t da = da0 + st * (WSTAGE >> 4), db = db0 + st * (WSTAGE >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_any<true, F8>(acc, da + kk * qs, db + kk * ps, p.idesc, (kb | kk) != 0);
-          mma_commit_pair(&bars->empty[st]);
+            for (int kk = 0; kk < 4; ++kk) mma_any<true, F8>(acc, da + kk * qs, db + kk * ps, p.idesc, (kb | kk) != 0);
+            mma_commit_pair(&bars->empty[st]);
+            if (kb + 1 == p.kblocks) mma_commit_pair(&bars->tfull[b]);
+          }
+          __syncwarp();
           if (++st == WSTAGES) st = 0, ph ^= 1u;
         }
-        if (*abort_flag) break;
-        mma_commit_pair(&bars->tfull[b]);
       }
+      if (!ok && lane == 0) gave_up(p, abort_flag);
     }
   } else {
     const int quad = warp & 3, half = (warp - 2) >> 2;
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(TTHREADS)
   const int stage_bytes = WTILE + qbytes;
   ThinBars* bars = reinterpret_cast<ThinBars*>(smem + stages * stage_bytes);
   volatile int* abort_flag = &bars->abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = blockIdx.x % split, tile = blockIdx.x / split;
   const int i0 = tile / p.tj * 128, j0 = tile % p.tj * p.bn;
   const int kb0 = (int)((long long)p.kblocks * rank / split), kb1 = (int)((long long)p.kblocks * (rank + 1) / split);
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(TTHREADS)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bars->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem, 0);
   if (split > 1) cluster_arrive_relaxed();   // waited for before the first copy to another CTA
   // Partial sums in blocks of sb consecutive i, [block][column][sb]: this CTA's own ones in the
   // stages' memory once its MMAs are done, those that it receives, [part of k] of them, after the
@@ -473,17 +474,17 @@ __global__ void __launch_bounds__(TTHREADS)
   float* received = reinterpret_cast<float*>(smem + stages * stage_bytes + 256);
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       prefetch_tmap(&tmP);
       prefetch_tmap(&tmQ);
-      int st = 0, issued = 0;
-      uint32_t ph = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (*abort_flag) break;
-        if (!mbar_wait(&bars->empty[st], ph ^ 1u, p.limit)) {
-          gave_up(p, abort_flag);
-          break;
-        }
+    }
+    int st = 0, issued = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      ok = mbar_wait_warp(&bars->empty[st], ph ^ 1u, p.limit);
+      if (!ok) break;
+      if (elect_one()) {
         uint8_t* sp = smem + st * stage_bytes;
         uint8_t* sq = sp + WTILE;
         mbar_arrive_expect_tx(&bars->full[st], stage_bytes);
@@ -499,37 +500,42 @@ __global__ void __launch_bounds__(TTHREADS)
         } else {
           for (int h = 0; h < qbytes / ATOM; ++h) tma_load_2d(sq + h * ATOM, &tmQ, &bars->full[st], j0 + h * 64, k0);
         }
-        ++issued;
-        if (++st == stages) st = 0, ph ^= 1u;
       }
-      if (*abort_flag)
-        for (int q = min(issued, stages); q > 0; --q) {   // copies in flight land before the CTA leaves
-          const int n = issued - q;
-          mbar_wait(&bars->full[n % stages], (uint32_t)(n / stages) & 1u, p.limit);
-        }
+      ++issued;
+      if (++st == stages) st = 0, ph ^= 1u;
+    }
+    if (!ok) {   // gave up: copies in flight land before the CTA leaves
+      if (lane == 0) gave_up(p, abort_flag);
+      for (int q = min(issued, stages); q > 0; --q) {
+        const int n = issued - q;
+        mbar_wait(&bars->full[n % stages], (uint32_t)(n / stages) & 1u, p.limit);
+      }
     }
     __syncwarp();
     if (split > 1) cluster_wait();
   } else if (warp == 1) {
-    if (lane == 0 && kb1 > kb0) {
+    if (kb1 > kb0) {
       int st = 0;
       uint32_t ph = 0;
-      const uint32_t ps = desc_step(p.pk), qs = desc_step(p.qk);
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (*abort_flag) break;
-        if (!mbar_wait(&bars->full[st], ph, p.limit)) {
-          gave_up(p, abort_flag);
-          break;
-        }
+      bool ok = true;
+      const uint32_t ps = desc_step(p.pk), qs = desc_step(p.qk), s0 = smem_u32(smem);
+      const uint64_t da0 = tile_desc(s0, p.pk), db0 = tile_desc(s0 + WTILE, p.qk);
+      for (int kb = kb0; kb < kb1 && ok; ++kb) {
+        ok = mbar_wait_warp(&bars->full[st], ph, p.limit);
         tc_fence_after();
-        const uint32_t sp = smem_u32(smem + st * stage_bytes);
-        const uint64_t da = tile_desc(sp, p.pk), db = tile_desc(sp + WTILE, p.qk);
+        if (elect_one()) {
+          if (ok) {
+            const uint64_t da = da0 + (uint32_t)(st * stage_bytes >> 4), db = db0 + (uint32_t)(st * stage_bytes >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_any<false, F8>(tmem, da + kk * ps, db + kk * qs, p.idesc, kb != kb0 || kk != 0);
-        mma_commit(&bars->empty[st]);
+            for (int kk = 0; kk < 4; ++kk) mma_any<false, F8>(tmem, da + kk * ps, db + kk * qs, p.idesc, kb != kb0 || kk != 0);
+            mma_commit(&bars->empty[st]);
+          }
+          if (kb + 1 == kb1 || !ok) mma_commit(&bars->done);   // after giving up too: it completes once the issued MMAs have
+        }
+        __syncwarp();
         if (++st == stages) st = 0, ph ^= 1u;
       }
-      mma_commit(&bars->done);   // after an abort too: it completes once the issued MMAs have
+      if (!ok && lane == 0) gave_up(p, abort_flag);
     }
     __syncwarp();
     if (split > 1) cluster_wait();
