@@ -36,7 +36,6 @@ call raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import re
 
@@ -538,30 +537,31 @@ def _type_of(t, what: str) -> int:
     return k
 
 
-def _matrix(t, shape, dtype, what: str):
-    """(tensor, address, leading dimension) of a column-major matrix argument, copied if it is
-    not column-major; (None, None, rows) for None."""
+def _matrix(t, n: int, m: int, dtype, what: str):
+    """(tensor, address, leading dimension) of a column-major n x m matrix argument, copied if it
+    is not column-major; (None, None, n) for None."""
     if t is None:
-        return None, None, shape[0]
-    if t.shape != shape or t.dtype != dtype or not t.is_cuda:
-        raise CrError(1, f"{what}: a CUDA matrix of shape {tuple(shape)} and {dtype} is needed, not "
+        return None, None, n
+    if t.dtype is not dtype or not t.is_cuda or t.shape != (n, m):
+        raise CrError(1, f"{what}: a CUDA matrix of shape {(n, m)} and {dtype} is needed, not "
                          f"{tuple(t.shape)} and {t.dtype} on {t.device}")
-    n, m = shape
     s0, s1 = t.stride()
-    if (s0 != 1 and n > 1) or (s1 < n and m > 1):
+    if m == 1:
+        s1 = n
+    if (s0 != 1 and n > 1) or s1 < n:
         t = t.T.contiguous().T
         s1 = n
-    return t, t.data_ptr(), s1 if m > 1 else n
+    return t, t.data_ptr(), s1
 
 
 def _vector(t, n: int, what: str):
     """(tensor, address) of an FP32 vector argument, copied if it is strided."""
     if t is None:
         return None, None
-    _type_of(t, what)
-    if t.dim() != 1 or t.shape[0] != n or t.element_size() != 4:
-        raise CrError(1, f"{what}: an FP32 vector of {n} is needed, not {tuple(t.shape)} and {t.dtype}")
-    t = t.contiguous()
+    if t.dtype is not _torch.float32 or not t.is_cuda or t.shape != (n,):
+        raise CrError(1, f"{what}: an FP32 CUDA vector of {n} is needed, not {tuple(t.shape)} and {t.dtype} on {t.device}")
+    if not t.is_contiguous():
+        t = t.contiguous()
     return t, t.data_ptr()
 
 
@@ -569,20 +569,15 @@ def _empty(n: int, m: int, dtype, device):
     return _torch.empty_strided((n, m), (1, n), dtype=dtype, device=device)
 
 
-def _on_stream(fn):
-    """Runs the call with `stream` as the current stream, so that its outputs and copies belong
-    to it, and keeps the memory of its arguments until the stream has passed the call."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        _ready()
-        with _torch.cuda.stream(stream):
-            for t in (*args, *kw.values()):
-                if isinstance(t, _torch.Tensor) and t.is_cuda:
-                    t.record_stream(stream)
-            return fn(*args, **kw)
-    return call
+def _on(stream, fn, *args, **kw):
+    """fn with `stream` as the current stream, so that its outputs and copies belong to it; the
+    memory of its arguments is kept until the stream has passed the call."""
+    _ready()
+    with _torch.cuda.stream(stream):
+        for t in (*args, *kw.values()):
+            if isinstance(t, _torch.Tensor) and t.is_cuda:
+                t.record_stream(stream)
+        return fn(*args, **kw)
 
 
 def _raw_stream(device) -> int:
@@ -596,109 +591,125 @@ def _code(table, name, what: str) -> int:
     return k
 
 
-def _matrix_shape(t, what: str):
+def _shape(t, what: str):
     if t.dim() != 2:
         raise CrError(1, f"{what}: a matrix is needed, not {t.dim()} dimensions")
     return t.shape
 
 
-@_on_stream
 def affine(W, X, bias=None, act: str = "none", residual=None, w_scale=None, x_scale=None, out_dtype=None,
-           save: bool = False, out=None):
+           save: bool = False, out=None, stream=None):
     """cr_affine: Y = act(W^T X + bias) + residual for W (K, N) and X (K, M); e4m3 operands take
     w_scale (N) and x_scale (M).  out_dtype: FP32, FP16 or BF16 (default: X's, BF16 for e4m3).
     save=True returns (Y, Z) with Z the pre-activation that affine_backward reads."""
-    _ready()
+    if stream is not None:
+        return _on(stream, affine, W, X, bias, act, residual, w_scale, x_scale, out_dtype, save, out)
+    if _torch is None:
+        _ready()
     kind = _type_of(X, "affine X")
-    K, M = _matrix_shape(X, "affine X")
-    N = _matrix_shape(W, "affine W")[1]
-    X, px, ldx = _matrix(X, (K, M), X.dtype, "affine X")
-    W, pw, ldw = _matrix(W, (K, N), X.dtype, "affine W")
+    dtype, device = X.dtype, X.device
+    K, M = _shape(X, "affine X")
+    N = _shape(W, "affine W")[1]
+    X, px, ldx = _matrix(X, K, M, dtype, "affine X")
+    W, pw, ldw = _matrix(W, K, N, dtype, "affine W")
     if out is None:
-        if out_dtype is None:
-            out_dtype = _torch.bfloat16 if kind == CR_TYPE_E4M3 else X.dtype
-        out = _empty(N, M, out_dtype, X.device)
-    y, py, ldy = _matrix(out, (N, M), out_dtype or out.dtype, "affine out")
-    if y is not out:
-        raise CrError(1, "affine out: a column-major matrix is needed")
-    R, pr, ldr = _matrix(residual, (N, M), out.dtype, "affine residual")
-    Z = _empty(N, M, out.dtype, X.device) if save else None
+        out_dtype = out_dtype or (_torch.bfloat16 if kind == CR_TYPE_E4M3 else dtype)
+        out = _empty(N, M, out_dtype, device)
+        py, ldy = out.data_ptr(), N
+    else:
+        out_dtype = out_dtype or out.dtype
+        y, py, ldy = _matrix(out, N, M, out_dtype, "affine out")
+        if y is not out:
+            raise CrError(1, "affine out: a column-major matrix is needed")
+    residual, pr, ldr = _matrix(residual, N, M, out_dtype, "affine residual")
+    Z = _empty(N, M, out_dtype, device) if save else None
     bias, pb = _vector(bias, N, "affine bias")
     w_scale, pws = _vector(w_scale, N, "affine w_scale")
     x_scale, pxs = _vector(x_scale, M, "affine x_scale")
     _check(_lib.cr_affine(kind, pw, ldw, px, ldx, K, N, M, pws, pxs, pb, _code(_ACTS, act, "affine act"),
                           _type_of(out, "affine out"), pr, ldr, Z.data_ptr() if save else None, N, py, ldy,
-                          _raw_stream(X.device)))
+                          _raw_stream(device)))
     return (out, Z) if save else out
 
 
-@_on_stream
-def affine_backward(W, X, dY, Z=None, act: str = "none", need=(True, True, True), dw_dtype=None):
+def affine_backward(W, X, dY, Z=None, act: str = "none", need=(True, True, True), dw_dtype=None, stream=None):
     """cr_affine_backward: (dX, dW, dbias) of affine at the saved Z; need says which of the three
     are wanted (None for the others).  dw_dtype: X's type (default) or FP32."""
+    if stream is not None:
+        return _on(stream, affine_backward, W, X, dY, Z, act, need, dw_dtype)
     _ready()
     kind = _type_of(X, "affine_backward X")
-    K, M = _matrix_shape(X, "affine_backward X")
-    N = _matrix_shape(W, "affine_backward W")[1]
-    X, px, ldx = _matrix(X, (K, M), X.dtype, "affine_backward X")
-    W, pw, ldw = _matrix(W, (K, N), X.dtype, "affine_backward W")
-    dY, pdy, lddy = _matrix(dY, (N, M), X.dtype, "affine_backward dY")
-    Z, pz, ldz = _matrix(Z, (N, M), X.dtype, "affine_backward Z")
-    dX = _empty(K, M, X.dtype, X.device) if need[0] else None
-    dW = _empty(K, N, dw_dtype or X.dtype, X.device) if need[1] else None
-    db = _torch.empty(N, dtype=_torch.float32, device=X.device) if need[2] else None
+    dtype, device = X.dtype, X.device
+    K, M = _shape(X, "affine_backward X")
+    N = _shape(W, "affine_backward W")[1]
+    X, px, ldx = _matrix(X, K, M, dtype, "affine_backward X")
+    W, pw, ldw = _matrix(W, K, N, dtype, "affine_backward W")
+    dY, pdy, lddy = _matrix(dY, N, M, dtype, "affine_backward dY")
+    Z, pz, ldz = _matrix(Z, N, M, dtype, "affine_backward Z")
+    dX = _empty(K, M, dtype, device) if need[0] else None
+    dW = _empty(K, N, dw_dtype or dtype, device) if need[1] else None
+    db = _torch.empty(N, dtype=_torch.float32, device=device) if need[2] else None
     _check(_lib.cr_affine_backward(kind, pw, ldw, px, ldx, pdy, lddy, pz, ldz, K, N, M,
                                    _code(_ACTS, act, "affine_backward act"), _ptr(dX), K,
                                    _type_of(dW, "affine_backward dw_dtype") if need[1] else kind, _ptr(dW), K, _ptr(db),
-                                   _raw_stream(X.device)))
+                                   _raw_stream(device)))
     return dX, dW, db
 
 
 def _rmsnorm(X, gamma, residual, eps, e4m3: bool):
-    _ready()
+    if _torch is None:
+        _ready()
     kind = _type_of(X, "rmsnorm X")
-    D, T = _matrix_shape(X, "rmsnorm X")
-    X, px, ldx = _matrix(X, (D, T), X.dtype, "rmsnorm X")
-    R, pr, ldr = _matrix(residual, (D, T), X.dtype, "rmsnorm residual")
+    dtype, device = X.dtype, X.device
+    D, T = _shape(X, "rmsnorm X")
+    X, px, ldx = _matrix(X, D, T, dtype, "rmsnorm X")
+    residual, pr, ldr = _matrix(residual, D, T, dtype, "rmsnorm residual")
     gamma, pg = _vector(gamma, D, "rmsnorm gamma")
-    H = _empty(D, T, X.dtype, X.device) if R is not None else None
+    H = ph = scale = ps = None
+    if residual is not None:
+        H = _empty(D, T, dtype, device)
+        ph = H.data_ptr()
     if e4m3:
-        Y, out = _empty(D, T, _torch.float8_e4m3fn, X.device), CR_TYPE_E4M3
-        scale = _torch.empty(T, dtype=_torch.float32, device=X.device)
+        Y, out = _empty(D, T, _torch.float8_e4m3fn, device), CR_TYPE_E4M3
+        scale = _torch.empty(T, dtype=_torch.float32, device=device)
+        ps = scale.data_ptr()
     else:
-        Y, scale, out = _empty(D, T, X.dtype, X.device), None, kind
-    _check(_lib.cr_rmsnorm(kind, px, ldx, pr, ldr, pg, D, T, eps, _ptr(H), D, out, Y.data_ptr(), D, _ptr(scale),
-                           _raw_stream(X.device)))
+        Y, out = _empty(D, T, dtype, device), kind
+    _check(_lib.cr_rmsnorm(kind, px, ldx, pr, ldr, pg, D, T, eps, ph, D, out, Y.data_ptr(), D, ps, _raw_stream(device)))
     return Y, scale, H
 
 
-@_on_stream
-def rmsnorm(X, gamma, residual=None, eps: float = 1e-6):
+def rmsnorm(X, gamma, residual=None, eps: float = 1e-6, stream=None):
     """cr_rmsnorm: (Y, H) with H = X + residual (None without one) and Y its normalised columns."""
+    if stream is not None:
+        return _on(stream, rmsnorm, X, gamma, residual, eps)
     Y, _, H = _rmsnorm(X, gamma, residual, eps, False)
     return Y, H
 
 
-@_on_stream
-def rmsnorm_e4m3(X, gamma, residual=None, eps: float = 1e-6):
+def rmsnorm_e4m3(X, gamma, residual=None, eps: float = 1e-6, stream=None):
     """cr_rmsnorm with the 8-bit output: (Y in e4m3, scale per column, H)."""
+    if stream is not None:
+        return _on(stream, rmsnorm_e4m3, X, gamma, residual, eps)
     return _rmsnorm(X, gamma, residual, eps, True)
 
 
-@_on_stream
-def rmsnorm_backward(H, gamma, dY, dH=None, eps: float = 1e-6):
+def rmsnorm_backward(H, gamma, dY, dH=None, eps: float = 1e-6, stream=None):
     """cr_rmsnorm_backward: (dX, dgamma) at the sum H that rmsnorm returned (or its X)."""
+    if stream is not None:
+        return _on(stream, rmsnorm_backward, H, gamma, dY, dH, eps)
     _ready()
     kind = _type_of(H, "rmsnorm_backward H")
-    D, T = _matrix_shape(H, "rmsnorm_backward H")
-    H, ph, ldh = _matrix(H, (D, T), H.dtype, "rmsnorm_backward H")
-    dY, pdy, lddy = _matrix(dY, (D, T), H.dtype, "rmsnorm_backward dY")
-    dH, pdh, lddh = _matrix(dH, (D, T), H.dtype, "rmsnorm_backward dH")
+    dtype, device = H.dtype, H.device
+    D, T = _shape(H, "rmsnorm_backward H")
+    H, ph, ldh = _matrix(H, D, T, dtype, "rmsnorm_backward H")
+    dY, pdy, lddy = _matrix(dY, D, T, dtype, "rmsnorm_backward dY")
+    dH, pdh, lddh = _matrix(dH, D, T, dtype, "rmsnorm_backward dH")
     gamma, pg = _vector(gamma, D, "rmsnorm_backward gamma")
-    dX = _empty(D, T, H.dtype, H.device)
-    dgamma = _torch.empty(D, dtype=_torch.float32, device=H.device)
+    dX = _empty(D, T, dtype, device)
+    dgamma = _torch.empty(D, dtype=_torch.float32, device=device)
     _check(_lib.cr_rmsnorm_backward(kind, ph, ldh, pg, pdy, lddy, pdh, lddh, D, T, eps, dX.data_ptr(), D,
-                                    dgamma.data_ptr(), _raw_stream(H.device)))
+                                    dgamma.data_ptr(), _raw_stream(device)))
     return dX, dgamma
 
 
@@ -706,72 +717,81 @@ def _series(offsets, what: str):
     """(tensor, address, number of series) of the offsets."""
     if offsets is None:
         return None, None, 1
-    if offsets.dtype != _torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 1 or not offsets.is_cuda:
+    if offsets.dtype is not _torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 1 or not offsets.is_cuda:
         raise CrError(1, f"{what}: int32 CUDA offsets (series + 1) are needed")
     offsets = offsets.contiguous()
     return offsets, offsets.data_ptr(), offsets.shape[0] - 1
 
 
-@_on_stream
-def gated_scan(G, X, gate: str = "convex", offsets=None, h0=None, save: bool = False):
+def _saved_count(D: int, T: int) -> int:
+    count = ctypes.c_size_t(0)
+    _check(_lib.cr_gated_scan_saved(D, T, ctypes.byref(count)))
+    return count.value
+
+
+def gated_scan(G, X, gate: str = "convex", offsets=None, h0=None, save: bool = False, stream=None):
     """cr_gated_scan: (H, hT) for G and X (D, T) with packed series in the T columns; save=True
     returns (H, hT, saved), saved being what gated_scan_backward restarts from."""
+    if stream is not None:
+        return _on(stream, gated_scan, G, X, gate, offsets, h0, save)
     _ready()
     kind = _type_of(X, "gated_scan X")
-    D, T = _matrix_shape(X, "gated_scan X")
-    X, px, ldx = _matrix(X, (D, T), X.dtype, "gated_scan X")
-    G, pg, ldg = _matrix(G, (D, T), X.dtype, "gated_scan G")
+    dtype, device, f32 = X.dtype, X.device, _torch.float32
+    D, T = _shape(X, "gated_scan X")
+    X, px, ldx = _matrix(X, D, T, dtype, "gated_scan X")
+    G, pg, ldg = _matrix(G, D, T, dtype, "gated_scan G")
     offsets, po, n = _series(offsets, "gated_scan offsets")
-    h0, p0, ld0 = _matrix(h0, (D, n), _torch.float32, "gated_scan h0")
-    H, hT = _empty(D, T, X.dtype, X.device), _empty(D, n, _torch.float32, X.device)
-    saved = None
-    if save:
-        count = ctypes.c_size_t(0)
-        _check(_lib.cr_gated_scan_saved(D, T, ctypes.byref(count)))
-        saved = _torch.empty(count.value, dtype=_torch.float32, device=X.device)
+    h0, p0, ld0 = _matrix(h0, D, n, f32, "gated_scan h0")
+    H, hT = _empty(D, T, dtype, device), _empty(D, n, f32, device)
+    saved = _torch.empty(_saved_count(D, T), dtype=f32, device=device) if save else None
     _check(_lib.cr_gated_scan(kind, _code(_GATES, gate, "gated_scan gate"), pg, ldg, px, ldx, D, T, po, n, p0, ld0,
-                              H.data_ptr(), D, hT.data_ptr(), D, _ptr(saved), _raw_stream(X.device)))
+                              H.data_ptr(), D, hT.data_ptr(), D, _ptr(saved), _raw_stream(device)))
     return (H, hT, saved) if save else (H, hT)
 
 
-@_on_stream
-def gated_scan_backward(G, X, dH, gate: str = "convex", offsets=None, h0=None, dhT=None, saved=None):
+def gated_scan_backward(G, X, dH, gate: str = "convex", offsets=None, h0=None, dhT=None, saved=None, stream=None):
     """cr_gated_scan_backward: (dG, dX, dh0); saved is gated_scan's (None: recomputed)."""
+    if stream is not None:
+        return _on(stream, gated_scan_backward, G, X, dH, gate, offsets, h0, dhT, saved)
     _ready()
     kind = _type_of(X, "gated_scan_backward X")
-    D, T = _matrix_shape(X, "gated_scan_backward X")
-    X, px, ldx = _matrix(X, (D, T), X.dtype, "gated_scan_backward X")
-    G, pg, ldg = _matrix(G, (D, T), X.dtype, "gated_scan_backward G")
-    dH, pd, ldd = _matrix(dH, (D, T), X.dtype, "gated_scan_backward dH")
+    dtype, device, f32 = X.dtype, X.device, _torch.float32
+    D, T = _shape(X, "gated_scan_backward X")
+    X, px, ldx = _matrix(X, D, T, dtype, "gated_scan_backward X")
+    G, pg, ldg = _matrix(G, D, T, dtype, "gated_scan_backward G")
+    dH, pd, ldd = _matrix(dH, D, T, dtype, "gated_scan_backward dH")
     offsets, po, n = _series(offsets, "gated_scan_backward offsets")
-    h0, p0, ld0 = _matrix(h0, (D, n), _torch.float32, "gated_scan_backward h0")
-    dhT, pt, ldt = _matrix(dhT, (D, n), _torch.float32, "gated_scan_backward dhT")
-    if saved is not None:
-        count = ctypes.c_size_t(0)
-        _check(_lib.cr_gated_scan_saved(D, T, ctypes.byref(count)))
-        _vector(saved, count.value, "gated_scan_backward saved")
-    dG, dX = _empty(D, T, X.dtype, X.device), _empty(D, T, X.dtype, X.device)
-    dh0 = _empty(D, n, _torch.float32, X.device)
+    h0, p0, ld0 = _matrix(h0, D, n, f32, "gated_scan_backward h0")
+    dhT, pt, ldt = _matrix(dhT, D, n, f32, "gated_scan_backward dhT")
+    saved, ps = _vector(saved, _saved_count(D, T), "gated_scan_backward saved")
+    dG, dX = _empty(D, T, dtype, device), _empty(D, T, dtype, device)
+    dh0 = _empty(D, n, f32, device)
     _check(_lib.cr_gated_scan_backward(kind, _code(_GATES, gate, "gated_scan_backward gate"), pg, ldg, px, ldx, pd, ldd,
-                                       D, T, po, n, p0, ld0, pt, ldt, _ptr(saved), dG.data_ptr(), D, dX.data_ptr(), D,
-                                       dh0.data_ptr(), D, _raw_stream(X.device)))
+                                       D, T, po, n, p0, ld0, pt, ldt, ps, dG.data_ptr(), D, dX.data_ptr(), D,
+                                       dh0.data_ptr(), D, _raw_stream(device)))
     return dG, dX, dh0
 
 
-@_on_stream
-def gated_step(G, X, h, gate: str = "convex", out=None):
+def gated_step(G, X, h, gate: str = "convex", out=None, stream=None):
     """cr_gated_step: (H, hnext) for one step of B series; out receives hnext and may be h."""
-    _ready()
+    if stream is not None:
+        return _on(stream, gated_step, G, X, h, gate, out)
+    if _torch is None:
+        _ready()
     kind = _type_of(X, "gated_step X")
-    D, B = _matrix_shape(X, "gated_step X")
-    X, px, ldx = _matrix(X, (D, B), X.dtype, "gated_step X")
-    G, pg, ldg = _matrix(G, (D, B), X.dtype, "gated_step G")
-    h, ph, ldh = _matrix(h, (D, B), _torch.float32, "gated_step h")
-    hn = _empty(D, B, _torch.float32, X.device) if out is None else out
-    n, pn, ldn = _matrix(hn, (D, B), _torch.float32, "gated_step out")
-    if n is not hn:
-        raise CrError(1, "gated_step out: a column-major matrix is needed")
-    H = _empty(D, B, X.dtype, X.device)
+    dtype, device, f32 = X.dtype, X.device, _torch.float32
+    D, B = _shape(X, "gated_step X")
+    X, px, ldx = _matrix(X, D, B, dtype, "gated_step X")
+    G, pg, ldg = _matrix(G, D, B, dtype, "gated_step G")
+    h, ph, ldh = _matrix(h, D, B, f32, "gated_step h")
+    if out is None:
+        out = _empty(D, B, f32, device)
+        pn, ldn = out.data_ptr(), D
+    else:
+        n, pn, ldn = _matrix(out, D, B, f32, "gated_step out")
+        if n is not out:
+            raise CrError(1, "gated_step out: a column-major matrix is needed")
+    H = _empty(D, B, dtype, device)
     _check(_lib.cr_gated_step(kind, _code(_GATES, gate, "gated_step gate"), pg, ldg, px, ldx, ph, ldh, D, B,
-                              H.data_ptr(), D, pn, ldn, _raw_stream(X.device)))
-    return H, hn
+                              H.data_ptr(), D, pn, ldn, _raw_stream(device)))
+    return H, out

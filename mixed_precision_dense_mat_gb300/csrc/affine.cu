@@ -257,12 +257,13 @@ struct WideBars {
 constexpr int WSMEM = WSTAGES * WSTAGE + WEPI * WBUF + 1024 + 256;
 static_assert(sizeof(WideBars) <= 256, "barrier area");
 
-// Tile t: column tiles j in groups of 8 and all row tiles i inside a group, so that the tiles in
-// flight share operands in L2.
+// Tile t: column tiles j in groups of 16 and all row tiles i inside a group, so that the tiles in
+// flight share operands in L2 (K = 4096, N = 16384, M = 8192 BF16: groups of 1 674 us, 4 592, 8 564, 16 555, 32 583).
 __device__ __forceinline__ void wide_tile(const Params& p, int t, int& i, int& j) {
-  const int per = 8 * p.ti, g = t / per, gj = min(8, p.tj - g * 8), r = t - g * per;
+  constexpr int GROUP = 16;
+  const int per = GROUP * p.ti, g = t / per, gj = min(GROUP, p.tj - g * GROUP), r = t - g * per;
   i = r / gj;
-  j = g * 8 + r % gj;
+  j = g * GROUP + r % gj;
 }
 
 template <bool F8, class O>

@@ -611,21 +611,38 @@ __global__ void __launch_bounds__(NT, BBLOCKS)
 }
 
 // No columns: every series is empty.
-__global__ void __launch_bounds__(NT) k_scan_states(const float* from, int ldf, float* to, int ldt, int D) {
-  for (int d = blockIdx.x * NT + threadIdx.x; d < D; d += gridDim.x * NT)
-    to[(size_t)blockIdx.y * ldt + d] = from ? from[(size_t)blockIdx.y * ldf + d] : 0.0f;
+__global__ void __launch_bounds__(256) k_scan_states(const float* from, int ldf, float* to, int ldt, int D, int n) {
+  for (int s = blockIdx.x; s < n; s += gridDim.x)
+    for (int d = threadIdx.x; d < D; d += 256) to[(size_t)s * ldt + d] = from ? from[(size_t)s * ldf + d] : 0.0f;
 }
 
-template <class T, int GATE>
-__global__ void __launch_bounds__(NT) k_scan_step(const T* G, int ldg, const T* X, int ldx, const float* h, int ldh, int D, T* H,
-                                                  int ldo, float* hn, int ldn) {
-  const int d = blockIdx.x * NT + threadIdx.x;
-  if (d >= D) return;
-  const size_t b = blockIdx.y;
-  const auto g = gate_parts<GATE>(Floats<1>{{to_float(G[b * ldg + d])}});
-  const float v = fmaf(g.a.x[0], h[b * ldh + d], __fmul_rn(gate_input<GATE>(g).x[0], to_float(X[b * ldx + d])));
-  hn[b * ldn + d] = v;
-  if (H) H[b * ldo + d] = from_float<T>(v);
+// One step: V consecutive features of one series per thread (V = 4: aligned matrices).  Bound by HBM
+// for many series, by the launch for few.
+template <class T, int GATE, int V>
+__global__ void __launch_bounds__(256) k_scan_step(const T* G, int ldg, const T* X, int ldx, const float* h, int ldh, int D, int B, T* H,
+                                                   int ldo, float* hn, int ldn) {
+  struct alignas(sizeof(T) * V) Elements {
+    T x[V];
+  };
+  struct alignas(sizeof(float) * V) States {
+    float x[V];
+  };
+  const int per = (D + V - 1) / V;
+  for (long long e = (long long)blockIdx.x * 256 + threadIdx.x; e < (long long)per * B; e += (long long)gridDim.x * 256) {
+    const size_t b = (size_t)(e / per);
+    const int d = (int)(e % per) * V;
+    const Elements g = *reinterpret_cast<const Elements*>(G + b * ldg + d), x = *reinterpret_cast<const Elements*>(X + b * ldx + d);
+    States s = *reinterpret_cast<const States*>(h + b * ldh + d);
+    Elements o;
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+      const auto c = gate_parts<GATE>(Floats<1>{{to_float(g.x[q])}});
+      s.x[q] = fmaf(c.a.x[0], s.x[q], __fmul_rn(gate_input<GATE>(c).x[0], to_float(x.x[q])));
+      o.x[q] = from_float<T>(s.x[q]);
+    }
+    *reinterpret_cast<States*>(hn + b * ldn + d) = s;
+    if (H) *reinterpret_cast<Elements*>(H + b * ldo + d) = o;
+  }
 }
 
 bool float_type(int t) { return t == CR_TYPE_F32 || t == CR_TYPE_F16 || t == CR_TYPE_BF16; }
@@ -691,7 +708,7 @@ int sm_count() {
 
 cr_status states_only(const float* from, int ldf, float* to, int ldt, int D, int n, cudaStream_t stream) {
   if (!to || n == 0) return CR_OK;
-  k_scan_states<<<dim3((D + NT - 1) / NT, n), NT, 0, stream>>>(from, ldf, to, ldt, D);
+  k_scan_states<<<std::min(n, 16 * sm_count()), 256, 0, stream>>>(from, ldf, to, ldt, D, n);
   CR_CHECK_LAUNCH("k_scan_states");
   return CR_OK;
 }
@@ -758,7 +775,7 @@ extern "C" cr_status cr_gated_scan(int type, int gate, const void* d_G, int ldg,
   CR_ENTRY_BEGIN
   CR_REQUIRE(float_type(type), "cr_gated_scan: type must be FP32, FP16 or BF16");
   CR_REQUIRE(gate >= CR_GATE_COEFF && gate <= CR_GATE_VARIANCE, "cr_gated_scan: unknown gate");
-  CR_REQUIRE(D >= 1 && T >= 0 && n_seq >= 0 && n_seq <= 65535, "cr_gated_scan: D >= 1, T >= 0, 0 <= n_seq <= 65535");
+  CR_REQUIRE(D >= 1 && T >= 0 && n_seq >= 0, "cr_gated_scan: D >= 1, T >= 0, n_seq >= 0");
   CR_REQUIRE(d_off || n_seq == 1, "cr_gated_scan: without offsets there is one series");
   CR_REQUIRE(n_seq > 0 || T == 0, "cr_gated_scan: columns without a series");
   CR_REQUIRE((T == 0 || (d_G && d_X && ldg >= D && ldx >= D)) && (!d_H || ldh >= D), "cr_gated_scan: NULL argument or leading dimension below D");
@@ -783,7 +800,7 @@ extern "C" cr_status cr_gated_scan_backward(int type, int gate, const void* d_G,
   CR_ENTRY_BEGIN
   CR_REQUIRE(float_type(type), "cr_gated_scan_backward: type must be FP32, FP16 or BF16");
   CR_REQUIRE(gate >= CR_GATE_COEFF && gate <= CR_GATE_VARIANCE, "cr_gated_scan_backward: unknown gate");
-  CR_REQUIRE(D >= 1 && T >= 0 && n_seq >= 0 && n_seq <= 65535, "cr_gated_scan_backward: D >= 1, T >= 0, 0 <= n_seq <= 65535");
+  CR_REQUIRE(D >= 1 && T >= 0 && n_seq >= 0, "cr_gated_scan_backward: D >= 1, T >= 0, n_seq >= 0");
   CR_REQUIRE(d_off || n_seq == 1, "cr_gated_scan_backward: without offsets there is one series");
   CR_REQUIRE(n_seq > 0 || T == 0, "cr_gated_scan_backward: columns without a series");
   CR_REQUIRE(T == 0 || (d_G && d_X && d_dH && ldg >= D && ldx >= D && lddh >= D),
@@ -822,15 +839,23 @@ extern "C" cr_status cr_gated_step(int type, int gate, const void* d_G, int ldg,
   CR_ENTRY_BEGIN
   CR_REQUIRE(float_type(type), "cr_gated_step: type must be FP32, FP16 or BF16");
   CR_REQUIRE(gate >= CR_GATE_COEFF && gate <= CR_GATE_VARIANCE, "cr_gated_step: unknown gate");
-  CR_REQUIRE(D >= 1 && B >= 0 && B <= 65535, "cr_gated_step: D >= 1, 0 <= B <= 65535");
+  CR_REQUIRE(D >= 1 && B >= 0, "cr_gated_step: D >= 1, B >= 0");
   if (B == 0) return CR_OK;
   CR_REQUIRE(d_G && d_X && d_h && d_hnext, "cr_gated_step: NULL argument");
   CR_REQUIRE(ldg >= D && ldx >= D && ldh >= D && ldn >= D && (!d_H || ldo >= D), "cr_gated_step: leading dimension below D");
   return with_type(type, [&](auto t0) -> cr_status {
     using E = decltype(t0);
     return with_gate(gate, [&](auto g0) -> cr_status {
-      k_scan_step<E, decltype(g0)::value><<<dim3((D + NT - 1) / NT, B), NT, 0, stream>>>(
-          (const E*)d_G, ldg, (const E*)d_X, ldx, d_h, ldh, D, (E*)d_H, ldo, d_hnext, ldn);
+      constexpr int GATE = decltype(g0)::value;
+      const auto ok4 = [](const void* p, int ld, size_t eb) { return !p || ((uintptr_t)p % (4 * eb) == 0 && ld % 4 == 0); };
+      const bool four = D % 4 == 0 && ok4(d_G, ldg, sizeof(E)) && ok4(d_X, ldx, sizeof(E)) && ok4(d_H, ldo, sizeof(E)) &&
+                        ok4(d_h, ldh, 4) && ok4(d_hnext, ldn, 4);
+      const long long items = (long long)(four ? D / 4 : D) * B;
+      const unsigned grid = (unsigned)std::min<long long>((items + 255) / 256, 16 * sm_count());
+      if (four)
+        k_scan_step<E, GATE, 4><<<grid, 256, 0, stream>>>((const E*)d_G, ldg, (const E*)d_X, ldx, d_h, ldh, D, B, (E*)d_H, ldo, d_hnext, ldn);
+      else
+        k_scan_step<E, GATE, 1><<<grid, 256, 0, stream>>>((const E*)d_G, ldg, (const E*)d_X, ldx, d_h, ldh, D, B, (E*)d_H, ldo, d_hnext, ldn);
       CR_CHECK_LAUNCH("k_scan_step");
       return CR_OK;
     });
