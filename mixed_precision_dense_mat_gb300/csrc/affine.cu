@@ -34,8 +34,10 @@ struct Params {
   uint32_t idesc;        // MMA instruction descriptor
   int ti, tj;            // output tiles
   int bn;                // thin kernel: columns j of its tile
+  int stages;            // wide kernel
   int tma_c, tma_z;      // C, Z can be stored by TMA
   int vec_r;             // R allows 16-byte accesses
+  int tma_r;             // wide kernel: R comes by TMA into the output buffers (16-bit outputs)
   int vecb;              // bias and iscale do
   int vec4;              // four consecutive i of everything in the epilogue can be accessed at once
   Epilogue e;
@@ -160,10 +162,10 @@ __device__ __forceinline__ void load_row(const float* x, int i0, int I, int vec,
 // bytes in the 128-byte swizzle) and by TMA, or element by element where TMA cannot address them.
 template <class O, int N>
 __device__ __forceinline__ void put_rows(const CUtensorMap* tm, int tma, O* out, int ld, int I, int J, int i0, int j0, uint8_t* buf,
-                                         const float* v) {
+                                         bool ready, const float* v) {
   const int lane = threadIdx.x & 31;
   if (tma) {
-    if (lane == 0) tma_store_wait_read();   // the buffer's last tile has been read
+    if (!ready && lane == 0) tma_store_wait_read();   // the buffer's last tile has been read
     __syncwarp();
 #pragma unroll
     for (int q = 0; q < N / 8; ++q) {
@@ -190,7 +192,7 @@ __device__ __forceinline__ void put_rows(const CUtensorMap* tm, int tma, O* out,
 // Epilogue of the warp's 32 rows j and N columns i; v holds the sums.
 template <class O, int N>
 __device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* tmC, const CUtensorMap* tmZ, int i0, int j0, float js,
-                                            uint8_t* buf, float* v) {
+                                            uint8_t* buf, const uint8_t* rows, float* v) {
   const Epilogue& e = p.e;
   const int j = j0 + (threadIdx.x & 31);
   if (e.iscale) {
@@ -215,9 +217,18 @@ __device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* 
       for (int x = 0; x < 8; ++x) v[q + x] += w[x];
     }
   }
-  if (e.Z) put_rows<O, N>(tmZ, p.tma_z, (O*)e.Z, e.ldz, p.I, p.J, i0, j0, buf, v);
+  if (e.Z) put_rows<O, N>(tmZ, p.tma_z, (O*)e.Z, e.ldz, p.I, p.J, i0, j0, buf, false, v);
   activate_all<N>(v, e.act);
-  if (e.R && j < p.J) {
+  if (rows) {   // R in the output buffer
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int q = 0; q < N / 8; ++q) {
+      float w[8];
+      widen8(*reinterpret_cast<const Eight<O>*>(rows + lane * OROW + ((q ^ (lane & 7)) << 4)), w);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[8 * q + x] += w[x];
+    }
+  } else if (e.R && j < p.J) {
     const O* r = (const O*)e.R + (size_t)j * e.ldr + i0;
     if (p.vec_r && i0 + N <= p.I) {
 #pragma unroll
@@ -234,7 +245,7 @@ __device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* 
     }
   }
   __syncwarp();
-  put_rows<O, N>(tmC, p.tma_c, (O*)e.C, e.ldc, p.I, p.J, i0, j0, buf, v);
+  put_rows<O, N>(tmC, p.tma_c, (O*)e.C, e.ldc, p.I, p.J, i0, j0, buf, rows != nullptr, v);
 }
 
 // ---------------------------------------------------------------- wide kernel
@@ -244,18 +255,19 @@ __device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* 
 // warp 0 loads by TMA into a ring of stages, warp 1 of the first CTA issues the MMAs, warps 2-9
 // take the accumulator (two of them in TMEM, so the epilogue of one tile overlaps the next
 // tile's products) through the epilogue: a thread holds one j and 32 consecutive i.
-constexpr int WSTAGES = 6;
+constexpr int WSTAGES = 6;                       // 5 with two output buffers per warp
 constexpr int WTILE = 128 * KBYTES;              // one operand's half tile of a stage, 16 KB
 constexpr int WSTAGE = 2 * WTILE;
 constexpr int WTHREADS = 320;
 constexpr int WEPI = 8;                          // epilogue warps
 struct WideBars {
-  uint64_t full[WSTAGES], empty[WSTAGES], tfull[2], tempty[2];
+  uint64_t full[WSTAGES], empty[WSTAGES], tfull[2], tempty[2], rows[WEPI][2];
   uint32_t tmem;
   int abort;
 };
-constexpr int WSMEM = WSTAGES * WSTAGE + WEPI * WBUF + 1024 + 256;
-static_assert(sizeof(WideBars) <= 256, "barrier area");
+constexpr int WSMEM = WSTAGES * WSTAGE + WEPI * WBUF + 1024 + 384;
+static_assert(WSTAGE == WEPI * WBUF, "a stage's memory is a second set of output buffers");
+static_assert(sizeof(WideBars) <= 384, "barrier area");
 
 // Tile t: column tiles j in groups of 16 and all row tiles i inside a group, so that the tiles in
 // flight share operands in L2 (K = 4096, N = 16384, M = 8192 BF16: groups of 1 674 us, 4 592, 8 564, 16 555, 32 583).
@@ -269,7 +281,8 @@ __device__ __forceinline__ void wide_tile(const Params& p, int t, int& i, int& j
 template <bool F8, class O>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
     k_affine_wide(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
-                  const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmZ, const Params p) {
+                  const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmZ,
+                  const __grid_constant__ CUtensorMap tmR, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   WideBars* bars = reinterpret_cast<WideBars*>(smem + WSTAGES * WSTAGE + WEPI * WBUF);
@@ -280,13 +293,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
   constexpr int KE = F8 ? 128 : 64;   // k elements per stage
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < WSTAGES; ++s) {
+    for (int s = 0; s < p.stages; ++s) {
       mbar_init(&bars->full[s], 1);
       mbar_init(&bars->empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->tfull[b], 1);
       mbar_init(&bars->tempty[b], 2 * WEPI);   // one arrival per epilogue warp of the pair
+      for (int x = 0; x < WEPI; ++x) mbar_init(&bars->rows[x][b], 1);
     }
     bars->abort = 0;
     fence_mbar_init();
@@ -334,14 +348,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
           }
         }
         ++issued;
-        if (++st == WSTAGES) st = 0, ph ^= 1u;
+        if (++st == (uint32_t)p.stages) st = 0, ph ^= 1u;
       }
     }
     if (!ok) {   // gave up: the pair's copies in flight land before either CTA leaves
       if (lane == 0) gave_up(p, abort_flag);
-      for (int q = min(issued, WSTAGES); rank == 0 && q > 0; --q) {
+      for (int q = min(issued, p.stages); rank == 0 && q > 0; --q) {
         const int n = issued - q;
-        mbar_wait(&bars->full[n % WSTAGES], (uint32_t)(n / WSTAGES) & 1u, p.limit);
+        mbar_wait(&bars->full[n % p.stages], (uint32_t)(n / p.stages) & 1u, p.limit);
       }
     }
   } else if (warp == 1) {
@@ -369,30 +383,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
             if (kb + 1 == p.kblocks) mma_commit_pair(&bars->tfull[b]);
           }
           __syncwarp();
-          if (++st == WSTAGES) st = 0, ph ^= 1u;
+          if (++st == (uint32_t)p.stages) st = 0, ph ^= 1u;
         }
       }
       if (!ok && lane == 0) gave_up(p, abort_flag);
     }
   } else {
     const int quad = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* buf = smem + WSTAGES * WSTAGE + (warp - 2) * WBUF;
+    uint8_t* buf = smem + p.stages * WSTAGE + (warp - 2) * WBUF;   // with R: a second one WSTAGE further
     const uint32_t tempty[2] = {cluster_addr(smem_u32(&bars->tempty[0]), 0), cluster_addr(smem_u32(&bars->tempty[1]), 0)};
     int u = 0;
+    uint32_t nrows = 0;   // parity of the two buffers' next R
     for (int t = cl; t < ntiles; t += ncl, ++u) {
       const int b = u & 1;
       if (*abort_flag) break;
+      int ti, tj;
+      wide_tile(p, t, ti, tj);
+      const int j0 = tj * 256 + (int)rank * 128 + quad * 32, ibase = ti * 256 + half * 128;
+      constexpr int N = OROW / (int)sizeof(O);
+      if (p.tma_r && j0 < p.J) {   // both chunks' R, before the wait for the products
+        if (lane == 0) {
+          tma_store_wait_read();
+          for (int c = 0; c < 2; ++c)
+            if (ibase + c * N < p.I) {
+              mbar_arrive_expect_tx(&bars->rows[warp - 2][c], WBUF);
+              tma_load_2d(buf + c * WSTAGE, &tmR, &bars->rows[warp - 2][c], ibase + c * N, j0);
+            }
+        }
+      }
       if (!mbar_wait(&bars->tfull[b], (uint32_t)(u >> 1) & 1u, p.limit)) {
         gave_up(p, abort_flag);
         break;
       }
       tc_fence_after();
-      int ti, tj;
-      wide_tile(p, t, ti, tj);
-      const int j0 = tj * 256 + (int)rank * 128 + quad * 32, ibase = ti * 256 + half * 128;
       const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * 256 + half * 128);
       const float js = p.e.jscale && j0 + lane < p.J ? p.e.jscale[j0 + lane] : 1.0f;
-      constexpr int N = OROW / (int)sizeof(O);
       for (int c = 0; c < 128; c += N) {
         uint32_t v[N / 32][32];
         __syncwarp();
@@ -404,7 +429,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(tempty[b]);
         }
-        if (ibase + c < p.I) wide_finish<O, N>(p, &tmC, &tmZ, ibase + c, j0, js, buf, reinterpret_cast<float*>(v));
+        if (ibase + c >= p.I) continue;
+        uint8_t* out = buf;
+        const uint8_t* rows = nullptr;
+        if (p.tma_r && j0 < p.J) {
+          const int x = c / N;
+          rows = out = buf + x * WSTAGE;
+          if (!mbar_wait(&bars->rows[warp - 2][x], (nrows >> x) & 1u, p.limit)) gave_up(p, abort_flag);
+          nrows ^= 1u << x;
+        }
+        wide_finish<O, N>(p, &tmC, &tmZ, ibase + c, j0, js, out, rows, reinterpret_cast<float*>(v));
       }
     }
     if (lane == 0) tma_store_wait_read();
@@ -768,13 +802,13 @@ cr_status map_of(CUtensorMap* tm, const Operand& o, int type, int K, int rows_pe
 }
 
 template <bool F8, class O>
-cr_status launch(const CUtensorMap& tmP, const CUtensorMap& tmQ, const CUtensorMap& tmC, const CUtensorMap& tmZ, const Params& p, bool wide, int split, int stages, cudaStream_t stream) {
+cr_status launch(const CUtensorMap& tmP, const CUtensorMap& tmQ, const CUtensorMap& tmC, const CUtensorMap& tmZ, const CUtensorMap& tmR, const Params& p, bool wide, int split, int stages, cudaStream_t stream) {
   if (wide) {
     static const cudaError_t set = cudaFuncSetAttribute(k_affine_wide<F8, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, WSMEM);
     CR_CUDA(set);
     const int pairs = std::min((long long)sm_count() / 2, (long long)p.ti * p.tj);
     TimedScope ts("k_affine_wide", stream);
-    k_affine_wide<F8, O><<<2 * pairs, WTHREADS, WSMEM, stream>>>(tmP, tmQ, tmC, tmZ, p);
+    k_affine_wide<F8, O><<<2 * pairs, WTHREADS, WSMEM, stream>>>(tmP, tmQ, tmC, tmZ, tmR, p);
     CR_CHECK_LAUNCH("k_affine_wide");
     return CR_OK;
   }
@@ -927,15 +961,18 @@ cr_status product(Operand P, Operand Q, int type, int K, int out_type, const Epi
   p.ti = wide ? (p.I + 255) / 256 : (p.I + 127) / 128;
   p.tj = wide ? (p.J + 255) / 256 : (p.J + p.bn - 1) / p.bn;
   p.idesc = wide ? idesc_of(256, 256, bf16, !p.qk, !p.pk) : idesc_of(128, p.bn, bf16, !p.pk, !p.qk);
-  CUtensorMap tmP = {}, tmQ = {}, tmC = {}, tmZ = {};
+  CUtensorMap tmP = {}, tmQ = {}, tmC = {}, tmZ = {}, tmR = {};
+  p.tma_r = wide && e.R && ob == 2 && p.tma_c && !e.Z && p.vec_r;   // with Z the buffer is in use before R is added
+  p.stages = p.tma_r ? WSTAGES - 1 : WSTAGES;
+  if (p.tma_r) CR_TRY(make_tensor_map_2d(&tmR, out_type, e.R, p.I, p.J, e.ldr, KBYTES / ob, 32));
   if (wide && p.tma_c) CR_TRY(make_tensor_map_2d(&tmC, out_type, e.C, p.I, p.J, e.ldc, OROW / ob, 32));
   if (wide && e.Z && p.tma_z) CR_TRY(make_tensor_map_2d(&tmZ, out_type, e.Z, p.I, p.J, e.ldz, OROW / ob, 32));
   CR_TRY(map_of(&tmP, P, type, K, 128));
   CR_TRY(map_of(&tmQ, Q, type, K, wide ? 128 : p.bn));
   return with_type(out_type, [&](auto o0) -> cr_status {
     using O = decltype(o0);
-    return type == CR_TYPE_E4M3 ? launch<true, O>(tmP, tmQ, tmC, tmZ, p, wide, ch.split, ch.stages, stream)
-                                : launch<false, O>(tmP, tmQ, tmC, tmZ, p, wide, ch.split, ch.stages, stream);
+    return type == CR_TYPE_E4M3 ? launch<true, O>(tmP, tmQ, tmC, tmZ, tmR, p, wide, ch.split, ch.stages, stream)
+                                : launch<false, O>(tmP, tmQ, tmC, tmZ, tmR, p, wide, ch.split, ch.stages, stream);
   });
 }
 

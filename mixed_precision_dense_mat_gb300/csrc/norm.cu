@@ -434,24 +434,27 @@ int sm_count() {
 }
 // Whether two stages of a column's inputs fit; longer ones are read directly.
 bool ring_fits(int nin, int D, int eb) { return 2ll * nin * D * eb <= 200 * 1024; }
-// Stages of the rings of a block with `per` groups, and the block's shared memory: about 50 KB, so that
-// several blocks share an SM.
+// Blocks for n columns, `per` at a time each, stages of their rings and shared memory: about 50 KB,
+// so that several blocks share an SM; no more stages than a block has columns.
 struct Plan {
-  int stages;
-  size_t smem;
-  Plan(bool vec, int per, int nin, int D, int eb) : stages(0), smem(0) {
-    if (!vec) return;
-    const size_t stage = (size_t)per * nin * D * eb;
-    stages = (int)std::min<size_t>(8, std::max<size_t>(2, (size_t)50 * 1024 / stage));
-    smem = ((size_t)per * stages * 8 + 127) / 128 * 128 + stages * stage;
-  }
+  int blocks = 0, stages = 0;
+  size_t smem = 0;
 };
 template <class K>
-cr_status resident_blocks(K kernel, int threads, size_t smem, int* blocks) {
+cr_status make_plan(Plan& plan, K kernel, int threads, int n, int per, bool ring, int nin, int D, int eb) {
+  const int items = (n + per - 1) / per;
+  const size_t stage = (size_t)per * nin * D * eb;
+  if (ring) {
+    plan.stages = (int)std::min<size_t>(8, std::max<size_t>(2, (size_t)50 * 1024 / stage));
+    if (items <= sm_count()) plan.stages = 2;
+    plan.smem = ((size_t)per * plan.stages * 8 + 127) / 128 * 128 + plan.stages * stage;
+    if (plan.smem > 48 * 1024) CR_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan.smem));
+  }
+  plan.blocks = items;
+  if (items <= sm_count()) return CR_OK;   // one each
   int b = 0;
-  if (smem > 48 * 1024) CR_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  CR_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, kernel, threads, smem));
-  *blocks = std::max(b, 1) * sm_count();
+  CR_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, kernel, threads, plan.smem));
+  plan.blocks = std::min(items, std::max(b, 1) * sm_count());
   return CR_OK;
 }
 
@@ -469,13 +472,12 @@ template <class T, class O, int G, int VPT, bool VEC>
 cr_status launch_fwd(const Fwd& p, cudaStream_t stream) {
   constexpr int PER = G ? NT / 32 : 1;
   const int TH = threads_for(G, VPT, p.D);
-  const Plan plan(VEC, PER, 2, p.D, sizeof(T));
   Wait wait = {option_wait_ns(), nullptr};
   CR_TRY(wait_word(&wait.err));
-  int resident = 0;
-  CR_TRY(resident_blocks(k_rmsnorm<T, O, G, VPT, VEC>, TH, plan.smem, &resident));
+  Plan plan;
+  CR_TRY(make_plan(plan, k_rmsnorm<T, O, G, VPT, VEC>, TH, p.n, PER, VEC, 2, p.D, sizeof(T)));
   TimedScope ts("k_rmsnorm", stream);
-  k_rmsnorm<T, O, G, VPT, VEC><<<std::min(resident, (p.n + PER - 1) / PER), TH, plan.smem, stream>>>(
+  k_rmsnorm<T, O, G, VPT, VEC><<<plan.blocks, TH, plan.smem, stream>>>(
       (const T*)p.X, p.ldx, (const T*)p.R, p.ldr, p.gamma, p.D, p.n, p.eps, (T*)p.H, p.ldh, (O*)p.Y, p.ldy, p.scale, plan.stages, wait);
   CR_CHECK_LAUNCH("k_rmsnorm");
   return CR_OK;
@@ -495,12 +497,11 @@ template <class T, int G, int VPT, bool VEC>
 cr_status launch_bwd(const Bwd& p, cudaStream_t stream) {
   constexpr int PER = G ? NT / 32 : 1;
   const int TH = threads_for(G, VPT, p.D);
-  const Plan plan(VEC, PER, 3, p.D, sizeof(T));
   Wait wait = {option_wait_ns(), nullptr};
   CR_TRY(wait_word(&wait.err));
-  int resident = 0;
-  CR_TRY(resident_blocks(k_rmsnorm_bwd<T, G, VPT, VEC>, TH, plan.smem, &resident));
-  const int blocks = std::min(resident, (p.n + PER - 1) / PER);
+  Plan plan;
+  CR_TRY(make_plan(plan, k_rmsnorm_bwd<T, G, VPT, VEC>, TH, p.n, PER, VEC, 3, p.D, sizeof(T)));
+  const int blocks = plan.blocks;
   float* part = nullptr;
   if (p.dgamma) CR_CUDA(scratch_alloc((void**)&part, (size_t)blocks * p.D * sizeof(float), stream));
   {
