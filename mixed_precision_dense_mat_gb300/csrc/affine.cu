@@ -158,35 +158,68 @@ __device__ __forceinline__ void load_row(const float* x, int i0, int I, int vec,
   }
 }
 
-// The warp's 32 rows j of N = OROW / sizeof(O) values from (i0, j0): through shared memory (rows of 128
-// bytes in the 128-byte swizzle) and by TMA, or element by element where TMA cannot address them.
+// A warp's 32 rows j of N = OROW / sizeof(O) values from (i0, j0) live in its buffer as rows of 128 bytes in the
+// 128-byte swizzle: 16-byte word q of row r is at word q ^ (r & 7).
+template <class O>
+__device__ __forceinline__ O* at_in(uint8_t* buf, int row, int col) {
+  const int byte = col * (int)sizeof(O);
+  return reinterpret_cast<O*>(buf + row * OROW + (((byte >> 4) ^ (row & 7)) << 4) + (byte & 15));
+}
+
+// To memory: through the buffer and by TMA, or, where TMA cannot address the output, with each row's
+// elements stored by neighbouring lanes.  `ready`: the buffer's last tile has been read.
 template <class O, int N>
 __device__ __forceinline__ void put_rows(const CUtensorMap* tm, int tma, O* out, int ld, int I, int J, int i0, int j0, uint8_t* buf,
                                          bool ready, const float* v) {
   const int lane = threadIdx.x & 31;
+  if (!ready && lane == 0) tma_store_wait_read();
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < N / 8; ++q) {
+    const Eight<O> w = narrow8<O>(v + 8 * q);
+#pragma unroll
+    for (int x = 0; x < (int)sizeof(O) / 2; ++x)
+      *reinterpret_cast<uint4*>(buf + lane * OROW + (((int)sizeof(O) / 2 * q + x) ^ (lane & 7)) * 16) =
+          make_uint4(w.w[4 * x], w.w[4 * x + 1], w.w[4 * x + 2], w.w[4 * x + 3]);
+  }
   if (tma) {
-    if (!ready && lane == 0) tma_store_wait_read();   // the buffer's last tile has been read
-    __syncwarp();
-#pragma unroll
-    for (int q = 0; q < N / 8; ++q) {
-      const Eight<O> w = narrow8<O>(v + 8 * q);
-#pragma unroll
-      for (int x = 0; x < (int)sizeof(O) / 2; ++x)
-        *reinterpret_cast<uint4*>(buf + lane * OROW + (((int)sizeof(O) / 2 * q + x) ^ (lane & 7)) * 16) =
-            make_uint4(w.w[4 * x], w.w[4 * x + 1], w.w[4 * x + 2], w.w[4 * x + 3]);
-    }
     fence_smem_to_tma();
     __syncwarp();
     if (lane == 0 && j0 < J) {
       tma_store_2d(tm, buf, i0, j0);
       tma_store_commit();
     }
-  } else if (j0 + lane < J) {
-    O* o = out + (size_t)(j0 + lane) * ld + i0;
+  } else {
+    __syncwarp();
+    for (int r = 0; r < 32 && j0 + r < J; ++r)
 #pragma unroll
-    for (int q = 0; q < N; ++q)
-      if (i0 + q < I) o[q] = from_float<O>(v[q]);
+      for (int c = lane; c < N; c += 32)
+        if (i0 + c < I) out[(size_t)(j0 + r) * ld + i0 + c] = *at_in<O>(buf, r, c);
+    __syncwarp();
   }
+}
+// From memory, added to v, where TMA cannot address the matrix.
+template <class O, int N>
+__device__ __forceinline__ void add_rows_of(const O* in, int ld, int I, int J, int i0, int j0, uint8_t* buf, float* v) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) tma_store_wait_read();
+  __syncwarp();
+  for (int r0 = 0; r0 < 32; r0 += 8) {   // the loads of 8 rows in flight at once
+    O w[8][N / 32];
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int c = 0; c < N / 32; ++c)
+        if (j0 + r0 + r < J && i0 + lane + 32 * c < I) w[r][c] = in[(size_t)(j0 + r0 + r) * ld + i0 + lane + 32 * c];
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+#pragma unroll
+      for (int c = 0; c < N / 32; ++c) *at_in<O>(buf, r0 + r, lane + 32 * c) = w[r][c];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < N; ++q) v[q] += to_float(*at_in<O>(buf, lane, q));
+  __syncwarp();
 }
 
 // Epilogue of the warp's 32 rows j and N columns i; v holds the sums.
@@ -228,9 +261,9 @@ __device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* 
 #pragma unroll
       for (int x = 0; x < 8; ++x) v[8 * q + x] += w[x];
     }
-  } else if (e.R && j < p.J) {
-    const O* r = (const O*)e.R + (size_t)j * e.ldr + i0;
-    if (p.vec_r && i0 + N <= p.I) {
+  } else if (e.R && p.vec_r && i0 + N <= p.I) {
+    if (j < p.J) {
+      const O* r = (const O*)e.R + (size_t)j * e.ldr + i0;
 #pragma unroll
       for (int q = 0; q < N; q += 8) {
         float w[8];
@@ -238,11 +271,9 @@ __device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* 
 #pragma unroll
         for (int x = 0; x < 8; ++x) v[q + x] += w[x];
       }
-    } else {
-#pragma unroll
-      for (int q = 0; q < N; ++q)
-        if (i0 + q < p.I) v[q] += to_float(r[q]);
     }
+  } else if (e.R) {
+    add_rows_of<O, N>((const O*)e.R, e.ldr, p.I, p.J, i0, j0, buf, v);
   }
   __syncwarp();
   put_rows<O, N>(tmC, p.tma_c, (O*)e.C, e.ldc, p.I, p.J, i0, j0, buf, rows != nullptr, v);
@@ -697,11 +728,23 @@ __global__ void __launch_bounds__(NT) k_affine_few(const E* P, int ldp, const E*
     if (lane == j) finish<O>(p, i, j, s[j]);
 }
 
-// Copies a matrix whose columns of n elements start at any address into columns ld apart.
+// Copies a matrix whose columns of n elements start at any address into columns ld apart on 16-byte
+// boundaries: a thread gathers 16 bytes and stores them at once (elements past n are zero).
 template <class E>
 __global__ void __launch_bounds__(NT) k_pack(const E* src, int lds, int n, int m, E* dst, int ld) {
-  for (int c = blockIdx.y; c < m; c += gridDim.y)
-    for (int i = blockIdx.x * NT + threadIdx.x; i < n; i += gridDim.x * NT) dst[(size_t)c * ld + i] = src[(size_t)c * lds + i];
+  constexpr int V = 16 / (int)sizeof(E);
+  struct alignas(16) Word {
+    E x[V];
+  };
+  const int per = ld / V;
+  for (long long e = (long long)blockIdx.x * NT + threadIdx.x; e < (long long)per * m; e += (long long)gridDim.x * NT) {
+    const size_t c = (size_t)(e / per);
+    const int i = (int)(e % per) * V;
+    Word w;
+#pragma unroll
+    for (int q = 0; q < V; ++q) w.x[q] = i + q < n ? src[c * lds + i + q] : E(0);
+    *reinterpret_cast<Word*>(dst + c * ld + i) = w;
+  }
 }
 
 // G = dY .* act'(Z), and the row sums of its unrounded values: a block takes 32 V features and every
@@ -786,7 +829,8 @@ struct Packed {
     const int n = o.k_major ? K : o.rows, m = o.k_major ? o.rows : K;
     const int ld = (int)(((long long)n * eb + 15) / 16 * 16 / eb);
     CR_CUDA(scratch_alloc(&own, (size_t)ld * m * eb, s));
-    const dim3 grid((n + NT - 1) / NT, m < 32768 ? m : 32768);
+    const long long words = (long long)ld * eb / 16 * m;
+    const unsigned grid = (unsigned)std::min<long long>((words + NT - 1) / NT, 8 * sm_count());
     if (eb == 2) k_pack<uint16_t><<<grid, NT, 0, s>>>((const uint16_t*)o.ptr, o.ld, n, m, (uint16_t*)own, ld);
     else k_pack<uint8_t><<<grid, NT, 0, s>>>((const uint8_t*)o.ptr, o.ld, n, m, (uint8_t*)own, ld);
     CR_CHECK_LAUNCH("k_pack");
