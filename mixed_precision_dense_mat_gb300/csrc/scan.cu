@@ -27,7 +27,7 @@ namespace {
 // predecessor.  Every composition has a fixed order, so results do not depend on timing.
 constexpr int WARPS = 8, NT = 32 * (WARPS + 1);
 constexpr int FSUB = 16, BSUB = 8;        // steps per warp, forward and backward
-constexpr int BLOCK = WARPS * BSUB;       // steps between saved states: a chunk of the backward pass
+constexpr int BLOCK = BSUB;               // steps between saved states: a warp's part of a backward chunk
 // Stages per block and blocks per SM.  More blocks hide the waits for predecessors, more stages the
 // loads; forward 2048 x 65536 BF16: 1 and 5 186 us, 1 and 4 192 us, 2 and 3 195 us, 3 and 2 245 us;
 // backward 1 and 4 423 us, 2 and 3 400 us.
@@ -429,12 +429,12 @@ __global__ void __launch_bounds__(NT, FBLOCKS)
     Floats<VEC> h;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) h.x[v] = sh->fold[warp][lane * VEC + v].x;
-    if (p.saved && warp * FSUB % BLOCK == 0 && t0 < p.n) store_state<VEC>(p.saved, p.D, t0 / BLOCK, f, p.D, h);
     if (!(starts | ends) && p.H && p.pairs && p.n - t0 >= FSUB) {   // inside a series
       if (f < p.D) {
         T* o = p.H + (size_t)t0 * p.ldh + f;
 #pragma unroll 4
         for (int i = 0; i < FSUB; ++i, o += p.ldh) {
+          if (i % BLOCK == 0) store_state<VEC>(p.saved, p.D, (t0 + i) / BLOCK, f, p.D, h);
           step(i, a, b);
           h = fma(a, h, b);
           put_all(o, h);
@@ -444,6 +444,7 @@ __global__ void __launch_bounds__(NT, FBLOCKS)
       const int steps = f < p.D ? p.n - t0 : 0;
 #pragma unroll 1
       for (int i = 0; i < FSUB; ++i) {
+        if (i % BLOCK == 0 && i < steps) store_state<VEC>(p.saved, p.D, (t0 + i) / BLOCK, f, p.D, h);
         if (starts >> i & 1u) load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, h);
         step(i, a, b);
         h = fma(a, h, b);
@@ -472,13 +473,14 @@ struct BwdArgs {
 };
 
 // Backward scan, from the last chunk to the first: r_t = a_t q_t, q_t = dh_t + r_{t+1}, with "take dhT" at
-// a series' last step.  The states inside a chunk are recomputed from the saved one before
-// it, which reads G and X (needed anyway) in place of H.  Bound by HBM (G, X, dH read, dG, dX written).
+// a series' last step.  Each warp recomputes the states of its steps from the one saved before
+// them, which reads G and X (needed anyway) in place of H: 0.5 bytes per element (one state in
+// 8 steps) against H's 2 or 4 and its rounding.  Bound by HBM (G, X, dH read, dG, dX written).
 template <class T, int GATE>
 __global__ void __launch_bounds__(NT, BBLOCKS)
     k_scan_bwd(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmD,
                const BwdArgs<T> p, const Lookback lb) {
-  constexpr int CH = BLOCK, SUB = BSUB, VEC = vec_of<T>(), W = 32 * VEC;
+  constexpr int CH = WARPS * BSUB, SUB = BSUB, VEC = vec_of<T>(), W = 32 * VEC;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~(uintptr_t)127);
   auto* sh = reinterpret_cast<Shared<CH, W, BSTAGES>*>(ring + BSTAGES * 3 * CH * ROW);
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(NT, BBLOCKS)
     const int t0 = chunk * CH + warp * SUB, f = tile * W + lane * VEC;
     uint8_t* in = ring + st * 3 * CH * ROW;
     Floats<VEC> h;
-    load_state<VEC>(p.saved, p.D, chunk, f, p.D, h);
+    load_state<VEC>(p.saved, p.D, t0 / BLOCK, f, t0 < p.n ? p.D : 0, h);
     if (!p.tma) {
       copy_rows<T, W>(p.G, in, warp * SUB, SUB, tile * W, t0, p.D, p.n);
       copy_rows<T, W>(p.X, in + CH * ROW, warp * SUB, SUB, tile * W, t0, p.D, p.n);
@@ -528,57 +530,48 @@ __global__ void __launch_bounds__(NT, BBLOCKS)
     const uint32_t ends = __ballot_sync(0xffffffffu, lane < SUB && last[lane & (SUB - 1)] >= 0);
     const uint8_t* row = in + warp * SUB * ROW + lane * 4;
 
-    // b: c x, then the state before the step
-    Floats<VEC> a[SUB], b[SUB], A = all_of<VEC>(1.0f), B = all_of<VEC>(0.0f), RA = A, RB = B;
+    Floats<VEC> RA = all_of<VEC>(1.0f), RB = all_of<VEC>(0.0f), before[SUB];
+    GateParts<VEC> c[SUB];
+    if (!(starts | ends)) {   // without branches, so that steps overlap
 #pragma unroll
-    for (int i = 0; i < SUB; ++i) {
-      if (starts >> i & 1u) {
-        A = all_of<VEC>(0.0f);
-        load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, B);
+      for (int i = SUB - 1; i >= 0; --i) {
+        c[i] = gate_parts<GATE>(widened<T, VEC>(row + i * ROW));
+        RB = mul(c[i].a, add(widened<T, VEC>(row + 2 * CH * ROW + i * ROW), RB));
+        RA = mul(RA, c[i].a);
       }
-      const auto c = gate_parts<GATE>(widened<T, VEC>(row + i * ROW));
-      a[i] = c.a;
-      b[i] = mul(gate_input<GATE>(c), widened<T, VEC>(row + CH * ROW + i * ROW));
-      A = mul(A, a[i]);
-      B = fma(a[i], B, b[i]);
-    }
 #pragma unroll
-    for (int i = SUB - 1; i >= 0; --i) {
-      if (ends >> i & 1u) {
-        RA = all_of<VEC>(0.0f);
-        load_state<VEC>(p.dhT, p.lddhT, last[i], f, p.D, RB);
+      for (int i = 0; i < SUB; ++i) {
+        before[i] = h;
+        h = fma(c[i].a, h, mul(gate_input<GATE>(c[i]), widened<T, VEC>(row + CH * ROW + i * ROW)));
       }
-      RB = mul(a[i], add(widened<T, VEC>(row + 2 * CH * ROW + i * ROW), RB));
-      RA = mul(RA, a[i]);
-    }
-    // the states before each step: the maps of the earlier warps on the saved state
+    } else {
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) sh->maps[warp][lane * VEC + v] = make_float2(A.x[v], B.x[v]);
-    workers_sync();
-#pragma unroll
-    for (int w = 0; w < WARPS - 1; ++w)
-      if (w < warp) {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) h.x[v] = apply_map(sh->maps[w][lane * VEC + v].x, sh->maps[w][lane * VEC + v].y, h.x[v]);
+      for (int i = SUB - 1; i >= 0; --i) {
+        if (ends >> i & 1u) {
+          RA = all_of<VEC>(0.0f);
+          load_state<VEC>(p.dhT, p.lddhT, last[i], f, p.D, RB);
+        }
+        c[i] = gate_parts<GATE>(widened<T, VEC>(row + i * ROW));
+        RB = mul(c[i].a, add(widened<T, VEC>(row + 2 * CH * ROW + i * ROW), RB));
+        RA = mul(RA, c[i].a);
       }
-    workers_sync();
 #pragma unroll
-    for (int i = 0; i < SUB; ++i) {
-      if (starts >> i & 1u) load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, h);
-      const Floats<VEC> next = fma(a[i], h, b[i]);
-      b[i] = h;
-      h = next;
+      for (int i = 0; i < SUB; ++i) {
+        if (starts >> i & 1u) load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, h);
+        before[i] = h;
+        h = fma(c[i].a, h, mul(gate_input<GATE>(c[i]), widened<T, VEC>(row + CH * ROW + i * ROW)));
+      }
     }
     if (!join<true, VEC, W>(lb, sh, tile, k, p.D, RA, RB)) return;
     Floats<VEC> q;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) q.x[v] = sh->fold[warp][lane * VEC + v].x;
     const auto step = [&](int i, Floats<VEC>& dx, Floats<VEC>& dg) {   // gradients of step i; q passes on
-      const auto c = gate_parts<GATE>(widened<T, VEC>(row + i * ROW));
+      const Floats<VEC> in = gate_input<GATE>(c[i]);
       q = add(widened<T, VEC>(row + 2 * CH * ROW + i * ROW), q);
-      dx = mul(gate_input<GATE>(c), q);
-      dg = mul(q, gate_slope<GATE>(c, b[i], widened<T, VEC>(row + CH * ROW + i * ROW)));
-      q = mul(a[i], q);
+      dx = mul(in, q);
+      dg = mul(q, gate_slope<GATE>(c[i], in, before[i], widened<T, VEC>(row + CH * ROW + i * ROW)));
+      q = mul(c[i].a, q);
     };
     Floats<VEC> dx, dg;
     if (!(starts | ends) && p.dX && p.dG && p.pairs && p.n - t0 >= SUB) {   // inside a series
@@ -737,10 +730,10 @@ cr_status forward(FwdArgs<E> p, cudaStream_t stream) {
 
 template <class E, int GATE>
 cr_status backward(BwdArgs<E> p, cudaStream_t stream) {
-  constexpr int W = 32 * vec_of<E>(), SMEM = BSTAGES * 3 * BLOCK * ROW + sizeof(Shared<BLOCK, W, BSTAGES>) + 128;
+  constexpr int W = 32 * vec_of<E>(), CH = WARPS * BSUB, SMEM = BSTAGES * 3 * CH * ROW + sizeof(Shared<CH, W, BSTAGES>) + 128;
   const int tiles = (p.D + W - 1) / W;
   Scratch sc;
-  CR_TRY(sc.make(p.n, BLOCK, tiles, W, stream));
+  CR_TRY(sc.make(p.n, CH, tiles, W, stream));
   CR_REQUIRE((long long)sc.lb.chunks * tiles < INT_MAX / 2, "cr_gated_scan_backward: more than 2^30 work items");
   static const cudaError_t set = cudaFuncSetAttribute(k_scan_bwd<E, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   CR_CUDA(set);
@@ -748,9 +741,9 @@ cr_status backward(BwdArgs<E> p, cudaStream_t stream) {
   p.pairs = vec_ok<E>(p.dG, p.lddg, p.D) && vec_ok<E>(p.dX, p.lddx, p.D);
   CUtensorMap tmG = {}, tmX = {}, tmD = {};
   if (p.tma) {
-    CR_TRY(map_in<E>(&tmG, p.G, p.D, p.n, BLOCK));
-    CR_TRY(map_in<E>(&tmX, p.X, p.D, p.n, BLOCK));
-    CR_TRY(map_in<E>(&tmD, p.dH, p.D, p.n, BLOCK));
+    CR_TRY(map_in<E>(&tmG, p.G, p.D, p.n, CH));
+    CR_TRY(map_in<E>(&tmX, p.X, p.D, p.n, CH));
+    CR_TRY(map_in<E>(&tmD, p.dH, p.D, p.n, CH));
   }
   TimedScope ts("k_scan_bwd", stream);
   k_scan_bwd<E, GATE><<<std::min(BBLOCKS * sm_count(), sc.lb.chunks * tiles), NT, SMEM, stream>>>(tmG, tmX, tmD, p, sc.lb);
