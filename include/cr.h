@@ -108,7 +108,10 @@ cr_status cr_kernel_launches(uint64_t* count);
  * block, all M unless a level's chunk products for all M would exceed 2 GiB), 2 GiB of chunk
  * products at most (one chunk's 4 n_p M_b bytes when that is more), 8 n_p M_b bytes of
  * accumulator, 8 n_o M bytes for R, and S (8 n_p M) in cr_correct_calibrate;
- * cr_krige_correct with CR_GEMM_DF takes 8 n_o (n_p + M) bytes.  Memory still used by work in flight stays in the pool.  No device
+ * cr_krige_correct with CR_GEMM_DF takes 8 n_o (n_p + M) bytes.  The trend-network operators take
+ * copies of operands that are not on 16-byte boundaries, G in cr_affine_backward, a few hundred rows
+ * of partial sums for vector gradients, and 8 bytes per feature and 128 (backward 64) columns for
+ * the recurrence.  Memory still used by work in flight stays in the pool.  No device
  * work; does not synchronise. */
 cr_status cr_workspace_trim(void);
 
@@ -123,6 +126,9 @@ cr_status cr_workspace_trim(void);
  *   "k_oz_slice", "oz_gemm", "k_oz_accum"   Ozaki product: operand slicing, the slice GEMMs of
  *                   one level (cuBLAS), the exact accumulation of one level
  *   "k_scan"        calibration scan
+ *   "k_affine_wide", "k_affine_thin", "k_affine_few", "k_affine_g"   affine product (CTA pairs; few
+ *                   columns; one or two columns) and the gradient at its pre-activation
+ *   "k_rmsnorm", "k_rmsnorm_bwd", "k_scan_fwd", "k_scan_bwd"   norm and gated recurrence
  * cr_timing_enable(on) switches recording on (1) or off (0); it does not clear the totals.
  * cr_timing_read(name, &ms, &n) synchronises the device, folds every recorded launch into the
  * totals and returns the total milliseconds and launch count of `name` (0 if never timed).
@@ -135,10 +141,11 @@ cr_status cr_timing_reset(void);
 /* Process-wide options (the paper has no counterpart: they control how this library runs
  * the method, not what it computes).  They apply to calls made after the change.
  *  CR_OPT_WAIT_LIMIT_US  wall-clock limit of every bounded device-side wait of the
- *                        factorisation's diagonal executor, in microseconds (default 2000000,
- *                        range [0, 600000000]).  A wait that runs out makes the factorisation
- *                        return CR_ERR_TIMEOUT; the tile matrix stays usable and the next
- *                        cr_potrf_adaptive starts from a clean state.
+ *                        factorisation's diagonal executor and of the trend-network operators, in
+ *                        microseconds (default 2000000, range [0, 600000000]).  A wait that
+ *                        runs out makes the factorisation return CR_ERR_TIMEOUT; the tile matrix
+ *                        stays usable and the next cr_potrf_adaptive starts from a clean state.
+ *                        For the operators see their section.
  *  CR_OPT_DIAG_ARITH     arithmetic of the FP64 diagonal tiles (Section IV-B keeps them FP64):
  *                        CR_DIAG_FP64 on the FP64 units; CR_DIAG_DF as double-float pairs of
  *                        FP32 numbers on the FP32 units (an FP64 emulation with about 48
@@ -427,7 +434,8 @@ cr_status cr_calibrate_noalloc(const double* d_S, int lds, int n_p, int M, const
  *  - Elements are FP32, FP16, BF16 or e4m3 (FP8, largest value 448) as a CR_TYPE_* argument
  *    says; arithmetic, sums and states are FP32, and each output is rounded once, to nearest.
  *  - Scratch comes from the pools of cr_workspace_trim.  Calls are asynchronous, and results do
- *    not depend on timing: the same call on the same inputs gives the same bits.
+ *    not depend on timing: the same call on the same inputs gives the same bits.  They can be
+ *    captured into CUDA graphs once the process has made a first call outside a capture.
  *  - Zero columns (M, T, B or n_seq = 0) are allowed: sums over them are zero.
  *  - A device-side wait that runs out (CR_OPT_WAIT_LIMIT_US; never in normal operation)
  *    invalidates the outputs of its call and makes the next call of this section on any
@@ -448,8 +456,8 @@ enum { CR_GATE_COEFF = 0, CR_GATE_CONVEX = 1, CR_GATE_VARIANCE = 2 };
  * W and X: CR_TYPE_F16, CR_TYPE_BF16 or CR_TYPE_E4M3; out_type that of R, Z and Y: CR_TYPE_F32,
  * CR_TYPE_F16 or CR_TYPE_BF16.  d_wscale (N) and d_xscale (M) are FP32 and belong to e4m3 (both
  * NULL otherwise, either may be NULL there).  d_bias (FP32), d_R and d_Z may be NULL; a non-NULL d_Z
- * receives Z, which cr_affine_backward reads.  Products are accumulated in FP32; d_R may be
- * d_Y (with ldr = ldy). */
+ * receives Z, which cr_affine_backward reads.  Products are accumulated in FP32; silu and gelu are
+ * evaluated to about 2^-20 |z|, with their limits at infinities; d_R may be d_Y (with ldr = ldy). */
 cr_status cr_affine(int type, const void* d_W, int ldw, const void* d_X, int ldx, int K, int N,
                     int M, const float* d_wscale, const float* d_xscale, const float* d_bias,
                     int act, int out_type, const void* d_R, int ldr, void* d_Z, int ldz,
@@ -493,7 +501,8 @@ cr_status cr_rmsnorm_backward(int type, const void* d_H, int ldh, const float* d
  * empty series allowed; NULL means one series of T columns).  Within a series h_t = a_t h_{t-1} +
  * c_t x_t (CR_GATE_*), starting from its column of h0 (D x n_seq FP32; NULL: zero).  G, X, H are
  * D x T of `type` (CR_TYPE_F32, CR_TYPE_F16, CR_TYPE_BF16); states are FP32 and H is rounded
- * from them.  hT (D x n_seq FP32, may be NULL) receives the last state of each series, h0 where
+ * from them.  Coefficients are evaluated to about 2^-20 of themselves for |g| < 16 (e^-g is cut at
+ * 2^125).  hT (D x n_seq FP32, may be NULL) receives the last state of each series, h0 where
  * it is empty.  d_H may be NULL.  d_saved (may be NULL) receives the states that
  * cr_gated_scan_backward restarts from: *count of cr_gated_scan_saved FP32 values.
  * Series do not mix: a NaN or infinity in one leaves the others alone. */

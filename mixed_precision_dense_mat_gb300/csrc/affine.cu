@@ -487,9 +487,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
 // ---------------------------------------------------------------- thin kernel
 // 128 outputs i x bn columns j per cluster (operand A = P, B = Q): few columns, where the product is
 // bound by reading P.  The CTAs of a cluster take equal parts of k.  Each finishes 128 / split of
-// the i: the others copy their partial sums for these into its shared memory, and it adds them in the
-// order of the parts.  (Stores of single sums to another CTA took 16 us where the bulk copies
-// take THINCOPY, at K = N = 2048, M = 64.)
+// the i: the others copy their partial sums for these into its shared memory in bulk, and it adds
+// them in the order of the parts.
 constexpr int TTHREADS = 192;
 constexpr int TMAXSTAGES = 8;
 struct ThinBars {

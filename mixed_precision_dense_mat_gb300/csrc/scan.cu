@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(NT, FBLOCKS)
         B = fma(a, B, b);
       }
     }
-    if (!join<false, VEC, W>(lb, sh, tile, k, p.D, A, B)) return;
+    if (!join<false, VEC, W>(lb, sh, tile, k, p.D, A, B)) return;   // (one stage: no copies in flight)
     Floats<VEC> h;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) h.x[v] = sh->fold[warp][lane * VEC + v].x;
@@ -562,7 +562,10 @@ __global__ void __launch_bounds__(NT, BBLOCKS)
         h = fma(c[i].a, h, mul(gate_input<GATE>(c[i]), widened<T, VEC>(row + CH * ROW + i * ROW)));
       }
     }
-    if (!join<true, VEC, W>(lb, sh, tile, k, p.D, RA, RB)) return;
+    if (!join<true, VEC, W>(lb, sh, tile, k, p.D, RA, RB)) {
+      mbar_wait(&sh->full[(it + 1) % BSTAGES], (uint32_t)((it + 1) / BSTAGES) & 1u, lb.limit);   // the next item's copies land first
+      return;
+    }
     Floats<VEC> q;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) q.x[v] = sh->fold[warp][lane * VEC + v].x;
