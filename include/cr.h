@@ -126,8 +126,8 @@ cr_status cr_workspace_trim(void);
  *   "k_oz_slice", "oz_gemm", "k_oz_accum"   Ozaki product: operand slicing, the slice GEMMs of
  *                   one level (cuBLAS), the exact accumulation of one level
  *   "k_scan"        calibration scan
- *   "k_affine_wide", "k_affine_thin", "k_affine_few", "k_affine_g"   affine product (CTA pairs; few
- *                   columns; one or two columns) and the gradient at its pre-activation
+ *   "k_affine_wide", "k_affine_thin", "k_affine_one", "k_affine_g"   affine product (CTA pairs; few
+ *                   columns; one column) and the gradient at its pre-activation
  *   "k_rmsnorm", "k_rmsnorm_bwd", "k_scan_fwd", "k_scan_bwd"   norm and gated recurrence
  * cr_timing_enable(on) switches recording on (1) or off (0); it does not clear the totals.
  * cr_timing_read(name, &ms, &n) synchronises the device, folds every recorded launch into the

@@ -310,7 +310,7 @@ __device__ __forceinline__ void wide_tile(const Params& p, int t, int& i, int& j
 }
 
 template <bool F8, class O>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
+__global__ void __launch_bounds__(WTHREADS, 1)
     k_affine_wide(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                   const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmZ,
                   const __grid_constant__ CUtensorMap tmR, const Params p) {
@@ -342,6 +342,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(WTHREADS, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem, 0);
+  let_next_start();
+  wait_for_previous();
 
   if (warp == 0) {
     if (elect_one()) {
@@ -530,6 +532,8 @@ __global__ void __launch_bounds__(TTHREADS)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem, 0);
+  let_next_start();
+  wait_for_previous();
   if (split > 1) cluster_arrive_relaxed();   // waited for before the first copy to another CTA
   // Partial sums in blocks of sb consecutive i, [block][column][sb]: this CTA's own ones in the
   // stages' memory once its MMAs are done, those that it receives, [part of k] of them, after the
@@ -674,14 +678,13 @@ __global__ void __launch_bounds__(TTHREADS)
   }
 }
 
-// ---------------------------------------------------------------- a few columns
-// One warp per output i, one or two columns: P is read once, straight into registers, with no
-// shared-memory pipeline, tensor memory or cluster to set up, whose latency is most of a small
-// call's time (K = N = 2048, M = 1 BF16: 3.6 us, the thin kernel 6.2 us).  With more columns reading Q
-// again for each output costs more than that (M = 4: 7.7 and 6.4 us), and with more outputs than
-// resident warps a second round does (K = 4096, N = 12288, M = 1: 28.6 and 19.9 us).  V = 16 / sizeof(E)
+// ---------------------------------------------------------------- one column
+// One warp per output i, one column: P is read once, straight into registers, with no shared-memory
+// pipeline, tensor memory or cluster to set up (K = N = 2048 BF16: 3.6 us a call in a row, the thin kernel
+// 4.3 us; launched to overlap with the previous kernel it takes 6.6 us).  With two columns reading Q again
+// for each output costs more than that (5.1 us), and with more outputs than resident warps a
+// second round does (K = 4096, N = 12288: 28.6 us, the thin kernel 18.3 us).  V = 16 / sizeof(E)
 // elements at a time where P and Q are aligned, else one.
-constexpr int FEW = 2;
 template <class E, int V>
 __device__ __forceinline__ void widen(const E* p, float (&v)[V]) {
   if constexpr (V == 1) {
@@ -700,31 +703,23 @@ __device__ __forceinline__ void widen(const E* p, float (&v)[V]) {
     }
   }
 }
-template <class E, class O, int V, int M>
-__global__ void __launch_bounds__(NT) k_affine_few(const E* P, int ldp, const E* Q, int ldq, int K, const Params p) {
+template <class E, class O, int V>
+__global__ void __launch_bounds__(NT) k_affine_one(const E* P, int ldp, const E* Q, int K, const Params p) {
   const int lane = threadIdx.x & 31, i = blockIdx.x * (NT / 32) + (threadIdx.x >> 5);
   if (i >= p.I) return;
   const E* row = P + (size_t)i * ldp;
-  float s[M] = {};
+  float s = 0.0f;
 #pragma unroll 4
   for (int k = lane * V; k < K; k += 32 * V) {
-    float w[V];
+    float w[V], x[V];
     widen<E, V>(row + k, w);
+    widen<E, V>(Q + k, x);
 #pragma unroll
-    for (int j = 0; j < M; ++j) {
-      float x[V];
-      widen<E, V>(Q + (size_t)j * ldq + k, x);
-#pragma unroll
-      for (int q = 0; q < V; ++q) s[j] = fmaf(w[q], x[q], s[j]);
-    }
+    for (int q = 0; q < V; ++q) s = fmaf(w[q], x[q], s);
   }
 #pragma unroll
-  for (int j = 0; j < M; ++j)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
-#pragma unroll
-  for (int j = 0; j < M; ++j)
-    if (lane == j) finish<O>(p, i, j, s[j]);
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) finish<O>(p, i, 0, s);
 }
 
 // Copies a matrix whose columns of n elements start at any address into columns ld apart on 16-byte
@@ -851,26 +846,17 @@ cr_status launch(const CUtensorMap& tmP, const CUtensorMap& tmQ, const CUtensorM
     CR_CUDA(set);
     const int pairs = std::min((long long)sm_count() / 2, (long long)p.ti * p.tj);
     TimedScope ts("k_affine_wide", stream);
-    k_affine_wide<F8, O><<<2 * pairs, WTHREADS, WSMEM, stream>>>(tmP, tmQ, tmC, tmZ, tmR, p);
+    CR_CUDA(launch_after(k_affine_wide<F8, O>, 2 * pairs, WTHREADS, WSMEM, 2, stream, tmP, tmQ, tmC, tmZ, tmR, p));
     CR_CHECK_LAUNCH("k_affine_wide");
     return CR_OK;
   }
   static const cudaError_t set = cudaFuncSetAttribute(k_affine_thin<F8, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   CR_CUDA(set);
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = split;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)((long long)p.ti * p.tj * split));
-  cfg.blockDim = dim3(TTHREADS);
   const int stage = WTILE + (p.qk ? p.bn * KBYTES : (p.bn + 63) / 64 * ATOM);
-  cfg.dynamicSmemBytes = (size_t)stages * stage + 1024 + 256 + (split > 1 ? 512 * p.bn : 0);
-  cfg.stream = stream;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  const size_t smem = (size_t)stages * stage + 1024 + 256 + (split > 1 ? 512 * p.bn : 0);
   TimedScope ts("k_affine_thin", stream);
-  CR_CUDA(cudaLaunchKernelEx(&cfg, k_affine_thin<F8, O>, tmP, tmQ, p, split, stages));
+  CR_CUDA(launch_after(k_affine_thin<F8, O>, (unsigned)((long long)p.ti * p.tj * split), TTHREADS, smem, split, stream, tmP, tmQ, p, split,
+                       stages));
   CR_CHECK_LAUNCH("k_affine_thin");
   return CR_OK;
 }
@@ -950,23 +936,15 @@ Choice choose(int I, int J, int kblocks, bool qk) {
 }
 
 template <class E, class O>
-cr_status few(const Operand& P, const Operand& Q, int K, const Params& p, cudaStream_t stream) {
+cr_status one_column(const Operand& P, const Operand& Q, int K, const Params& p, cudaStream_t stream) {
   const E *a = (const E*)P.ptr, *b = (const E*)Q.ptr;
   constexpr int V = 16 / (int)sizeof(E);
-  const bool vec = (((uintptr_t)a | (uintptr_t)b) & 15) == 0 && P.ld % V == 0 && Q.ld % V == 0 && K % V == 0;
+  const bool vec = (((uintptr_t)a | (uintptr_t)b) & 15) == 0 && P.ld % V == 0 && K % V == 0;
   const unsigned grid = (unsigned)((p.I + NT / 32 - 1) / (NT / 32));
-  const auto run = [&](auto v, auto m) {
-    k_affine_few<E, O, decltype(v)::value, decltype(m)::value><<<grid, NT, 0, stream>>>(a, P.ld, b, Q.ld, K, p);
-  };
-  const auto by_m = [&](auto v) {
-    using std::integral_constant;
-    if (p.J == 1) run(v, integral_constant<int, 1>{});
-    else run(v, integral_constant<int, 2>{});
-  };
-  TimedScope ts("k_affine_few", stream);
-  if (vec) by_m(std::integral_constant<int, V>{});
-  else by_m(std::integral_constant<int, 1>{});
-  CR_CHECK_LAUNCH("k_affine_few");
+  TimedScope ts("k_affine_one", stream);
+  if (vec) k_affine_one<E, O, V><<<grid, NT, 0, stream>>>(a, P.ld, b, K, p);
+  else k_affine_one<E, O, 1><<<grid, NT, 0, stream>>>(a, P.ld, b, K, p);
+  CR_CHECK_LAUNCH("k_affine_one");
   return CR_OK;
 }
 
@@ -988,12 +966,12 @@ cr_status product(Operand P, Operand Q, int type, int K, int out_type, const Epi
   p.vecb = (((uintptr_t)e.bias | (uintptr_t)e.iscale) & 15) == 0;
   const auto ok4 = [&](const void* q, int ld) { return !q || (((uintptr_t)q & (4 * ob - 1)) == 0 && ld % 4 == 0); };
   p.vec4 = p.vecb && ok4(e.C, e.ldc) && ok4(e.R, e.ldr) && ok4(e.Z, e.ldz);
-  if (p.J <= FEW && p.pk && p.qk && p.I <= 64 * sm_count())
+  if (p.J == 1 && p.pk && p.qk && p.I <= 64 * sm_count())   // one round of warps
     return with_type(out_type, [&](auto o0) -> cr_status {
       using O = decltype(o0);
-      if (type == CR_TYPE_F16) return few<__half, O>(P, Q, K, p, stream);
-      if (type == CR_TYPE_BF16) return few<__nv_bfloat16, O>(P, Q, K, p, stream);
-      return few<__nv_fp8_e4m3, O>(P, Q, K, p, stream);
+      if (type == CR_TYPE_F16) return one_column<__half, O>(P, Q, K, p, stream);
+      if (type == CR_TYPE_BF16) return one_column<__nv_bfloat16, O>(P, Q, K, p, stream);
+      return one_column<__nv_fp8_e4m3, O>(P, Q, K, p, stream);
     });
   Packed ownP, ownQ;
   CR_TRY(ownP.make(P, type, K, stream));

@@ -158,6 +158,8 @@ __global__ void __launch_bounds__(G ? NT : 512)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 red[2][32];
   Ring<T, G, 2> ring(smem, VEC ? stages : 0, D, wait);
+  let_next_start();
+  wait_for_previous();
   float g[VPT][8];
   const int step = gridDim.x * PER, t0 = blockIdx.x * PER + (G ? threadIdx.x / 32 : 0);
   const auto fill = [&](int stage, long long t) {
@@ -218,6 +220,8 @@ __global__ void __launch_bounds__(G ? NT : 512)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 red[2][32];
   Ring<T, G, 3> ring(smem, VEC ? stages : 0, D, wait);
+  let_next_start();
+  wait_for_previous();
   float g[VPT][8], dg[VPT][8] = {};
   const int step = gridDim.x * PER, t0 = blockIdx.x * PER + (G ? threadIdx.x / 32 : 0);
   const auto fill = [&](int stage, long long t) {
@@ -303,13 +307,15 @@ __global__ void __launch_bounds__(G ? NT : 512)
 // The sum of `rows` partial vectors (gradients of vectors), in a fixed order: 32 features per block, 32 threads each.
 __global__ void __launch_bounds__(1024) k_add_rows(const float* part, int rows, int D, float* total) {
   __shared__ float sum[32][33];
-  const int i = blockIdx.x * 32 + threadIdx.x;
+  let_next_start();
+  wait_for_previous();
+  const int i = blockIdx.x * 32 + threadIdx.x % 32, y0 = threadIdx.x / 32;
   float s = 0.0f;
   if (i < D)
-    for (int r = threadIdx.y; r < rows; r += 32) s += part[(size_t)r * D + i];
-  sum[threadIdx.y][threadIdx.x] = s;
+    for (int r = y0; r < rows; r += 32) s += part[(size_t)r * D + i];
+  sum[y0][threadIdx.x % 32] = s;
   __syncthreads();
-  if (threadIdx.y == 0 && i < D) {
+  if (y0 == 0 && i < D) {
     for (int y = 1; y < 32; ++y) s += sum[y][threadIdx.x];
     total[i] = s;
   }
@@ -478,8 +484,8 @@ cr_status launch_fwd(const Fwd& p, cudaStream_t stream) {
   Plan plan;
   CR_TRY(make_plan(plan, k_rmsnorm<T, O, G, VPT, VEC>, TH, p.n, PER, VEC, 2, p.D, sizeof(T)));
   TimedScope ts("k_rmsnorm", stream);
-  k_rmsnorm<T, O, G, VPT, VEC><<<plan.blocks, TH, plan.smem, stream>>>(
-      (const T*)p.X, p.ldx, (const T*)p.R, p.ldr, p.gamma, p.D, p.n, p.eps, (T*)p.H, p.ldh, (O*)p.Y, p.ldy, p.scale, plan.stages, wait);
+  CR_CUDA(launch_after(k_rmsnorm<T, O, G, VPT, VEC>, plan.blocks, TH, plan.smem, 1, stream, (const T*)p.X, p.ldx, (const T*)p.R, p.ldr,
+                       p.gamma, p.D, p.n, p.eps, (T*)p.H, p.ldh, (O*)p.Y, p.ldy, p.scale, plan.stages, wait));
   CR_CHECK_LAUNCH("k_rmsnorm");
   return CR_OK;
 }
@@ -505,13 +511,13 @@ cr_status launch_bwd(const Bwd& p, cudaStream_t stream) {
   const int blocks = plan.blocks;
   float* part = nullptr;
   if (p.dgamma) CR_CUDA(scratch_alloc((void**)&part, (size_t)blocks * p.D * sizeof(float), stream));
+  cudaError_t e;
   {
     TimedScope ts("k_rmsnorm_bwd", stream);
-    k_rmsnorm_bwd<T, G, VPT, VEC><<<blocks, TH, plan.smem, stream>>>((const T*)p.H, p.ldh, p.gamma, (const T*)p.dY, p.lddy, (const T*)p.dH,
-                                                             p.lddh, p.D, p.n, p.eps, (T*)p.dX, p.lddx, part, plan.stages, wait);
+    e = launch_after(k_rmsnorm_bwd<T, G, VPT, VEC>, blocks, TH, plan.smem, 1, stream, (const T*)p.H, p.ldh, p.gamma, (const T*)p.dY, p.lddy,
+                     (const T*)p.dH, p.lddh, p.D, p.n, p.eps, (T*)p.dX, p.lddx, part, plan.stages, wait);
     count_launch();
   }
-  const cudaError_t e = cudaGetLastError();
   const cr_status st = e != cudaSuccess ? cuda_fail(e, "k_rmsnorm_bwd") : p.dgamma ? add_rows(part, blocks, p.D, p.dgamma, stream) : CR_OK;
   scratch_free(part, stream);
   return st;
@@ -524,7 +530,7 @@ bool float_type(int t) { return t == CR_TYPE_F32 || t == CR_TYPE_F16 || t == CR_
 }  // namespace
 
 cr_status add_rows(const float* part, int rows, int D, float* total, cudaStream_t stream) {
-  k_add_rows<<<(D + 31) / 32, dim3(32, 32), 0, stream>>>(part, rows, D, total);
+  CR_CUDA(launch_after(k_add_rows, (unsigned)((D + 31) / 32), 1024, 0, 1, stream, part, rows, D, total));
   CR_CHECK_LAUNCH("k_add_rows");
   return CR_OK;
 }

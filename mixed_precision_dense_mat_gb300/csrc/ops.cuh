@@ -114,6 +114,26 @@ inline int type_bytes(int type) {
   return type == CR_TYPE_F32 ? 4 : type == CR_TYPE_E4M3 ? 1 : 2;
 }
 
+// Launches a kernel that may be set up (barriers, tensor memory, its first instructions) while the
+// stream's previous kernel finishes, and calls wait_for_previous() before it touches memory.
+template <class... Par, class... Arg>
+cudaError_t launch_after(void (*kernel)(Par...), unsigned grid, unsigned block, size_t smem, int cluster, cudaStream_t stream, Arg&&... arg) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, Par(arg)...);
+}
+
 // Calls f(T{}) with the element type of `type`, one of FP32, FP16, BF16 (checked before).
 template <class F>
 cr_status with_type(int type, F&& f) {

@@ -623,6 +623,8 @@ __global__ void __launch_bounds__(256) k_scan_step(const T* G, int ldg, const T*
   struct alignas(sizeof(float) * V) States {
     float x[V];
   };
+  let_next_start();
+  wait_for_previous();
   const int per = (D + V - 1) / V;
   for (long long e = (long long)blockIdx.x * 256 + threadIdx.x; e < (long long)per * B; e += (long long)gridDim.x * 256) {
     const size_t b = (size_t)(e / per);
@@ -849,9 +851,9 @@ extern "C" cr_status cr_gated_step(int type, int gate, const void* d_G, int ldg,
       const long long items = (long long)(four ? D / 4 : D) * B;
       const unsigned grid = (unsigned)std::min<long long>((items + 255) / 256, 16 * sm_count());
       if (four)
-        k_scan_step<E, GATE, 4><<<grid, 256, 0, stream>>>((const E*)d_G, ldg, (const E*)d_X, ldx, d_h, ldh, D, B, (E*)d_H, ldo, d_hnext, ldn);
+        CR_CUDA(launch_after(k_scan_step<E, GATE, 4>, grid, 256, 0, 1, stream, (const E*)d_G, ldg, (const E*)d_X, ldx, d_h, ldh, D, B, (E*)d_H, ldo, d_hnext, ldn));
       else
-        k_scan_step<E, GATE, 1><<<grid, 256, 0, stream>>>((const E*)d_G, ldg, (const E*)d_X, ldx, d_h, ldh, D, B, (E*)d_H, ldo, d_hnext, ldn);
+        CR_CUDA(launch_after(k_scan_step<E, GATE, 1>, grid, 256, 0, 1, stream, (const E*)d_G, ldg, (const E*)d_X, ldx, d_h, ldh, D, B, (E*)d_H, ldo, d_hnext, ldn));
       CR_CHECK_LAUNCH("k_scan_step");
       return CR_OK;
     });
