@@ -309,16 +309,17 @@ template <int GATE, int VEC>
 __device__ __forceinline__ Floats<VEC> gate_input(const GateParts<VEC>& p) {   // c; 1 - a^2 = rest (1 + a)
   return GATE == CR_GATE_VARIANCE ? sqrt_of(mul(p.rest, add(p.a, all_of<VEC>(1.0f)))) : p.rest;
 }
-// h' da/dg + x dc/dg, given c.  Variance gate: dc/dg = -a (a rest) / c = -a^2 c / (1 + a), finite at a = 1.
+// h' da/dg + x dc/dg from a and c.  Convex gate: c = 1 - a.  Variance gate: 1 - a = c^2 / (1 + a) gives
+// da/dg = a c^2 / (1 + a) and dc/dg = -a^2 c / (1 + a), finite at a = 1.
 template <int GATE, int VEC>
-__device__ __forceinline__ Floats<VEC> gate_slope(const GateParts<VEC>& p, Floats<VEC> c, Floats<VEC> before, Floats<VEC> x) {
+__device__ __forceinline__ Floats<VEC> gate_slope(Floats<VEC> a, Floats<VEC> c, Floats<VEC> before, Floats<VEC> x) {
   if (GATE == CR_GATE_COEFF) return before;
   const Floats<VEC> minus = all_of<VEC>(-1.0f);
-  if (GATE == CR_GATE_CONVEX) return mul(mul(p.a, p.rest), fma(x, minus, before));
-  Floats<VEC> r = add(p.a, all_of<VEC>(1.0f));
+  if (GATE == CR_GATE_CONVEX) return mul(mul(a, c), fma(x, minus, before));
+  Floats<VEC> r = add(a, all_of<VEC>(1.0f));
 #pragma unroll
   for (int q = 0; q < VEC; ++q) r.x[q] = rcp_fast(r.x[q]);
-  return mul(p.a, fma(before, p.rest, mul(mul(x, minus), mul(p.a, mul(c, r)))));
+  return mul(mul(mul(a, c), r), fma(before, c, mul(mul(x, minus), a)));
 }
 
 }  // namespace cr

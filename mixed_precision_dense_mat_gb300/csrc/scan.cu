@@ -30,7 +30,7 @@ constexpr int FSUB = 16, BSUB = 8;        // steps per warp, forward and backwar
 constexpr int BLOCK = BSUB;               // steps between saved states: a warp's part of a backward chunk
 // Stages per block and blocks per SM.  More blocks hide the waits for predecessors, more stages the
 // loads; forward 2048 x 65536 BF16: 1 and 5 186 us, 1 and 4 192 us, 2 and 3 195 us, 3 and 2 245 us;
-// backward 1 and 4 423 us, 2 and 3 400 us.
+// backward 1536 x 50021 FP16, variance gate: 1 and 4 225 us, 2 and 3 210 us.
 constexpr int FSTAGES = 1, FBLOCKS = 5, BSTAGES = 2, BBLOCKS = 3;
 constexpr int MAXGROUP = 64;
 constexpr int ROW = 128;                  // bytes of a column in a tile
@@ -233,9 +233,11 @@ __device__ __forceinline__ int next_item(const Lookback& lb, S* sh, int it) {
 
 // Joins the workers' maps (A, B) of a chunk (position k in the order of work): the state that enters the
 // part of each warp, in sh->fold[warp][feature].x.  Warps compose in the order 0 .. 7, or 7 .. 0 with REVERSE.  All
-// workers call it; false when a wait ran out.
-template <bool REVERSE, int VEC, int W, class S>
-__device__ __forceinline__ bool join(const Lookback& lb, S* sh, int tile, int k, int D, const Floats<VEC>& A, const Floats<VEC>& B) {
+// workers call it; meanwhile() runs between posting the chunk's map and waiting for others; false when a
+// wait ran out.
+template <bool REVERSE, int VEC, int W, class S, class Meanwhile>
+__device__ __forceinline__ bool join(const Lookback& lb, S* sh, int tile, int k, const Floats<VEC>& A, const Floats<VEC>& B,
+                                     Meanwhile&& meanwhile) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int v = 0; v < VEC; ++v) sh->maps[warp][lane * VEC + v] = make_float2(A.x[v], B.x[v]);
@@ -253,6 +255,7 @@ __device__ __forceinline__ bool join(const Lookback& lb, S* sh, int tile, int k,
     }
     if (more && !lastin) post(lb.maps + (size_t)k * lb.width + fx, map_word(TA, TB));
   }
+  meanwhile();
   bool fine = true;
   float h = 0.0f;
   if (lb.chunks > 1) {
@@ -425,7 +428,7 @@ __global__ void __launch_bounds__(NT, FBLOCKS)
         B = fma(a, B, b);
       }
     }
-    if (!join<false, VEC, W>(lb, sh, tile, k, p.D, A, B)) return;   // (one stage: no copies in flight)
+    if (!join<false, VEC, W>(lb, sh, tile, k, A, B, [] {})) return;   // (one stage: no copies in flight)
     Floats<VEC> h;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) h.x[v] = sh->fold[warp][lane * VEC + v].x;
@@ -475,7 +478,11 @@ struct BwdArgs {
 // Backward scan, from the last chunk to the first: r_t = a_t q_t, q_t = dh_t + r_{t+1}, with "take dhT" at
 // a series' last step.  Each warp recomputes the states of its steps from the one saved before
 // them, which reads G and X (needed anyway) in place of H: 0.5 bytes per element (one state in
-// 8 steps) against H's 2 or 4 and its rounding.  Bound by HBM (G, X, dH read, dG, dX written).
+// 8 steps) against H's 2 or 4 and its rounding.  The states and the slopes dg / q need no later step: they are
+// made between posting the chunk's map and waiting for the later chunks', and the slopes take the
+// inputs' place in shared memory, so that after the wait a step is four multiply-adds (all of it after the
+// wait: 289 us where this takes 210, 1536 x 50021 FP16, variance gate).  Bound by HBM (G, X, dH read, dG,
+// dX written) and, beyond it, by the wait for the chunks after it.
 template <class T, int GATE>
 __global__ void __launch_bounds__(NT, BBLOCKS)
     k_scan_bwd(const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmD,
@@ -528,22 +535,26 @@ __global__ void __launch_bounds__(NT, BBLOCKS)
     const int* last = sh->last[st] + warp * SUB;
     const uint32_t starts = __ballot_sync(0xffffffffu, lane < SUB && first[lane & (SUB - 1)] >= 0);
     const uint32_t ends = __ballot_sync(0xffffffffu, lane < SUB && last[lane & (SUB - 1)] >= 0);
-    const uint8_t* row = in + warp * SUB * ROW + lane * 4;
+    uint8_t* row = in + warp * SUB * ROW + lane * 4;
 
-    Floats<VEC> RA = all_of<VEC>(1.0f), RB = all_of<VEC>(0.0f), before[SUB];
-    GateParts<VEC> c[SUB];
-    if (!(starts | ends)) {   // without branches, so that steps overlap
+    Floats<VEC> RA = all_of<VEC>(1.0f), RB = all_of<VEC>(0.0f), a[SUB], c[SUB];
+    const auto gates = [&](int i) {
+      const auto parts = gate_parts<GATE>(widened<T, VEC>(row + i * ROW));
+      a[i] = parts.a;
+      c[i] = parts.rest;
+      RB = mul(a[i], add(widened<T, VEC>(row + 2 * CH * ROW + i * ROW), RB));
+      RA = mul(RA, a[i]);
+    };
+    const auto states = [&](int i) {
+      c[i] = gate_input<GATE>(GateParts<VEC>{a[i], c[i]});
+      const Floats<VEC> x = widened<T, VEC>(row + CH * ROW + i * ROW), slope = gate_slope<GATE>(a[i], c[i], h, x);
+      h = fma(a[i], h, mul(c[i], x));
 #pragma unroll
-      for (int i = SUB - 1; i >= 0; --i) {
-        c[i] = gate_parts<GATE>(widened<T, VEC>(row + i * ROW));
-        RB = mul(c[i].a, add(widened<T, VEC>(row + 2 * CH * ROW + i * ROW), RB));
-        RA = mul(RA, c[i].a);
-      }
+      for (int v = 0; v < VEC; ++v) *reinterpret_cast<float*>(row + v * CH * ROW + i * ROW) = slope.x[v];
+    };
+    if (!ends) {   // without branches, so that steps overlap
 #pragma unroll
-      for (int i = 0; i < SUB; ++i) {
-        before[i] = h;
-        h = fma(c[i].a, h, mul(gate_input<GATE>(c[i]), widened<T, VEC>(row + CH * ROW + i * ROW)));
-      }
+      for (int i = SUB - 1; i >= 0; --i) gates(i);
     } else {
 #pragma unroll
       for (int i = SUB - 1; i >= 0; --i) {
@@ -551,18 +562,22 @@ __global__ void __launch_bounds__(NT, BBLOCKS)
           RA = all_of<VEC>(0.0f);
           load_state<VEC>(p.dhT, p.lddhT, last[i], f, p.D, RB);
         }
-        c[i] = gate_parts<GATE>(widened<T, VEC>(row + i * ROW));
-        RB = mul(c[i].a, add(widened<T, VEC>(row + 2 * CH * ROW + i * ROW), RB));
-        RA = mul(RA, c[i].a);
-      }
-#pragma unroll
-      for (int i = 0; i < SUB; ++i) {
-        if (starts >> i & 1u) load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, h);
-        before[i] = h;
-        h = fma(c[i].a, h, mul(gate_input<GATE>(c[i]), widened<T, VEC>(row + CH * ROW + i * ROW)));
+        gates(i);
       }
     }
-    if (!join<true, VEC, W>(lb, sh, tile, k, p.D, RA, RB)) {
+    const bool fine = join<true, VEC, W>(lb, sh, tile, k, RA, RB, [&] {
+      if (!starts) {
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) states(i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) {
+          if (starts >> i & 1u) load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, h);
+          states(i);
+        }
+      }
+    });
+    if (!fine) {
       mbar_wait(&sh->full[(it + 1) % BSTAGES], (uint32_t)((it + 1) / BSTAGES) & 1u, lb.limit);   // the next item's copies land first
       return;
     }
@@ -570,11 +585,12 @@ __global__ void __launch_bounds__(NT, BBLOCKS)
 #pragma unroll
     for (int v = 0; v < VEC; ++v) q.x[v] = sh->fold[warp][lane * VEC + v].x;
     const auto step = [&](int i, Floats<VEC>& dx, Floats<VEC>& dg) {   // gradients of step i; q passes on
-      const Floats<VEC> in = gate_input<GATE>(c[i]);
       q = add(widened<T, VEC>(row + 2 * CH * ROW + i * ROW), q);
-      dx = mul(in, q);
-      dg = mul(q, gate_slope<GATE>(c[i], in, before[i], widened<T, VEC>(row + CH * ROW + i * ROW)));
-      q = mul(c[i].a, q);
+      dx = mul(c[i], q);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) dg.x[v] = *reinterpret_cast<const float*>(row + v * CH * ROW + i * ROW);
+      dg = mul(q, dg);
+      q = mul(a[i], q);
     };
     Floats<VEC> dx, dg;
     if (!(starts | ends) && p.dX && p.dG && p.pairs && p.n - t0 >= SUB) {   // inside a series
@@ -601,6 +617,7 @@ __global__ void __launch_bounds__(NT, BBLOCKS)
         if (starts >> i & 1u) store_state<VEC>(p.dh0, p.lddh0, first[i], f, p.D, q);
       }
     }
+    fence_smem_to_tma();   // the slopes were written where the next copy goes
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh->empty[st]);
   }
