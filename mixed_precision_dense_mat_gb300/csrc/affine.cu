@@ -35,6 +35,8 @@ struct Params {
   int ti, tj;            // output tiles
   int bn;                // thin kernel: columns j of its tile
   int stages;            // wide kernel
+  int second;            // wide kernel: follows another product of the call that it does not depend on
+  int early, ahead;      // then: pairs that are free before the others, and tiles that they can take until then
   int tma_c, tma_z;      // C, Z can be stored by TMA
   int vec_r;             // R allows 16-byte accesses
   int tma_r;             // wide kernel: R comes by TMA into the output buffers (16-bit outputs)
@@ -309,6 +311,12 @@ __device__ __forceinline__ void wide_tile(const Params& p, int t, int& i, int& j
   j = g * GROUP + r % gj;
 }
 
+// The i-th tile of pair cl of n.  The first `early` pairs take `ahead` tiles each before all pairs take turns.
+__device__ __forceinline__ int wide_turn(const Params& p, int cl, int n, int i) {
+  if (cl >= p.early) return p.early * p.ahead + i * n + cl;
+  return i < p.ahead ? i * p.early + cl : p.early * p.ahead + (i - p.ahead) * n + cl;
+}
+
 template <bool F8, class O>
 __global__ void __launch_bounds__(WTHREADS, 1)
     k_affine_wide(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
@@ -342,8 +350,10 @@ __global__ void __launch_bounds__(WTHREADS, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem, 0);
+  // The kernel before a second product is the first one, which lets this one start only after its own
+  // wait: the inputs are there.  It is waited for at the end, so that later kernels need not.
+  if (!p.second) wait_for_previous();
   let_next_start();
-  wait_for_previous();
 
   if (warp == 0) {
     if (elect_one()) {
@@ -354,7 +364,7 @@ __global__ void __launch_bounds__(WTHREADS, 1)
     int issued = 0;
     bool ok = true;
     const uint32_t full0 = cluster_addr(smem_u32(&bars->full[0]), 0);
-    for (int t = cl; t < ntiles && ok; t += ncl) {
+    for (int u = 0, t; ok && (t = wide_turn(p, cl, ncl, u)) < ntiles; ++u) {
       int ti, tj;
       wide_tile(p, t, ti, tj);
       const int i0 = ti * 256 + (int)rank * 128, j0 = tj * 256 + (int)rank * 128;
@@ -394,11 +404,10 @@ __global__ void __launch_bounds__(WTHREADS, 1)
   } else if (warp == 1) {
     if (rank == 0) {
       uint32_t st = 0, ph = 0;
-      int u = 0;
       bool ok = true;
       const uint32_t ps = desc_step(p.pk), qs = desc_step(p.qk), s0 = smem_u32(smem);
       const uint64_t da0 = tile_desc(s0, p.qk), db0 = tile_desc(s0 + WTILE, p.pk);
-      for (int t = cl; t < ntiles && ok; t += ncl, ++u) {
+      for (int u = 0; ok && wide_turn(p, cl, ncl, u) < ntiles; ++u) {
         const int b = u & 1;
         ok = mbar_wait_warp(&bars->tempty[b], ((uint32_t)(u >> 1) & 1u) ^ 1u, p.limit);
         if (!ok) break;
@@ -425,9 +434,8 @@ __global__ void __launch_bounds__(WTHREADS, 1)
     const int quad = warp & 3, half = (warp - 2) >> 2;
     uint8_t* buf = smem + p.stages * WSTAGE + (warp - 2) * WBUF;   // with R: a second one WSTAGE further
     const uint32_t tempty[2] = {cluster_addr(smem_u32(&bars->tempty[0]), 0), cluster_addr(smem_u32(&bars->tempty[1]), 0)};
-    int u = 0;
     uint32_t nrows = 0;   // parity of the two buffers' next R
-    for (int t = cl; t < ntiles; t += ncl, ++u) {
+    for (int u = 0, t; (t = wide_turn(p, cl, ncl, u)) < ntiles; ++u) {
       const int b = u & 1;
       if (*abort_flag) break;
       int ti, tj;
@@ -476,6 +484,7 @@ __global__ void __launch_bounds__(WTHREADS, 1)
     }
     if (lane == 0) tma_store_wait_read();
   }
+  if (p.second) wait_for_previous();
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -948,7 +957,15 @@ cr_status one_column(const Operand& P, const Operand& Q, int K, const Params& p,
   return CR_OK;
 }
 
-cr_status product(Operand P, Operand Q, int type, int K, int out_type, const Epilogue& e, cudaStream_t stream) {
+// A wide product that another one may follow which does not depend on it: its tiles and their length.  In
+// its last round some pairs are free, and the second product starts there (K = 2048, N = 8192, M = 4096 BF16,
+// dX and dW: 128 tiles of 128 k-blocks and 256 of 64 on 76 pairs, 7 rounds of 64 k-blocks for 4 + 4).
+struct First {
+  long long tiles = 0;
+  int kblocks = 0;
+};
+
+cr_status product(Operand P, Operand Q, int type, int K, int out_type, const Epilogue& e, cudaStream_t stream, First* first = nullptr) {
   Params p = {};
   CR_TRY(wait_word(&p.err));
   p.limit = option_wait_ns();
@@ -985,6 +1002,16 @@ cr_status product(Operand P, Operand Q, int type, int K, int out_type, const Epi
   CUtensorMap tmP = {}, tmQ = {}, tmC = {}, tmZ = {}, tmR = {};
   p.tma_r = wide && e.R && ob == 2 && p.tma_c && !e.Z && p.vec_r;   // with Z the buffer is in use before R is added
   p.stages = p.tma_r ? WSTAGES - 1 : WSTAGES;
+  if (first) {
+    const bool alone = wide && !ownP.own && !ownQ.own;   // nothing runs between the two
+    const long long pairs = sm_count() / 2, tiles = (long long)p.ti * p.tj;
+    p.second = alone && first->tiles > 0;
+    if (p.second) {
+      p.early = (int)std::min({(pairs - first->tiles % pairs) % pairs, pairs, tiles});
+      p.ahead = (2 * first->kblocks + p.kblocks) / (2 * p.kblocks);   // to the nearest
+    }
+    *first = {alone ? tiles : 0, p.kblocks};
+  }
   if (p.tma_r) CR_TRY(make_tensor_map_2d(&tmR, out_type, e.R, p.I, p.J, e.ldr, KBYTES / ob, 32));
   if (wide && p.tma_c) CR_TRY(make_tensor_map_2d(&tmC, out_type, e.C, p.I, p.J, e.ldc, OROW / ob, 32));
   if (wide && e.Z && p.tma_z) CR_TRY(make_tensor_map_2d(&tmZ, out_type, e.Z, p.I, p.J, e.ldz, OROW / ob, 32));
@@ -1049,13 +1076,17 @@ extern "C" cr_status cr_affine_backward(int type, const void* d_W, int ldw, cons
       if (vec) CR_TRY((gradient_at_z<E, 8>((const E*)d_dY, lddy, (const E*)d_Z, ldz, N, M, act, (E*)own, ldown, d_db, stream)));
       else CR_TRY((gradient_at_z<E, 1>((const E*)d_dY, lddy, (const E*)d_Z, ldz, N, M, act, (E*)own, ldown, d_db, stream)));
     }
-    if (d_dX) {   // dX(i, j) = sum_n W(i, n) G(n, j)
-      const Epilogue e{nullptr, nullptr, nullptr, CR_ACT_NONE, nullptr, 0, nullptr, 0, d_dX, lddx};
-      CR_TRY(product(Operand{d_W, K, ldw, false}, Operand{G, M, ldg, true}, type, N, type, e, stream));
-    }
-    if (d_dW) {   // dW(i, n) = sum_j X(i, j) G(n, j)
-      const Epilogue e{nullptr, nullptr, nullptr, CR_ACT_NONE, nullptr, 0, nullptr, 0, d_dW, lddw};
-      CR_TRY(product(Operand{d_X, K, ldx, false}, Operand{G, N, ldg, false}, type, M, dw_type, e, stream));
+    First first;
+    for (int part = 0; part < 2; ++part) {
+      if ((part == 0) == (N >= M)) {   // the one with the longer sums first
+        if (!d_dX) continue;           // dX(i, j) = sum_n W(i, n) G(n, j)
+        const Epilogue e{nullptr, nullptr, nullptr, CR_ACT_NONE, nullptr, 0, nullptr, 0, d_dX, lddx};
+        CR_TRY(product(Operand{d_W, K, ldw, false}, Operand{G, M, ldg, true}, type, N, type, e, stream, &first));
+      } else {
+        if (!d_dW) continue;           // dW(i, n) = sum_j X(i, j) G(n, j)
+        const Epilogue e{nullptr, nullptr, nullptr, CR_ACT_NONE, nullptr, 0, nullptr, 0, d_dW, lddw};
+        CR_TRY(product(Operand{d_X, K, ldx, false}, Operand{G, N, ldg, false}, type, M, dw_type, e, stream, &first));
+      }
     }
     return CR_OK;
   };

@@ -175,6 +175,22 @@ def test_affine_backward_parts(lib):
     assert dX.shape == (64, 0) and not dW.any() and not db.any()
 
 
+@pytest.mark.parametrize("K,N,M,dw", [(768, 2304, 1100, None), (768, 1100, 2304, None), (2048, 2600, 2600, None),
+                                      (600, 4100, 300, "f32"), (2048, 600, 5000, "f32")])
+def test_affine_backward_products_share_a_round(lib, K, N, M, dw):
+    """Both products of a call (the second starts where the first leaves pairs of SMs free) give what each gives alone."""
+    gen = torch.Generator("cuda").manual_seed(K + N + M)
+    draw = lambda a, b: torch.randn(b, a, device="cuda", generator=gen).bfloat16().T
+    W, X, dY, Z = draw(K, N), draw(K, M), draw(N, M), draw(N, M)
+    dtype = TYPES[dw] if dw else None
+    for act in ("none", "silu"):
+        for _ in range(3):
+            dX, dW, db = lib.affine_backward(W, X, dY, Z, act, dw_dtype=dtype)
+            aX = lib.affine_backward(W, X, dY, Z, act, need=(True, False, False), dw_dtype=dtype)[0]
+            aW = lib.affine_backward(W, X, dY, Z, act, need=(False, True, False), dw_dtype=dtype)[1]
+            assert torch.equal(dX, aX) and torch.equal(dW, aW)
+
+
 def test_affine_gradient_against_differences(lib):
     """The gradient of the library's own forward: FP32 outputs, a power-of-two step h along a random
     direction of W (entries of 8 bits, so W + h D is exact in FP16).  f = sum(dY * Y), f'' is
