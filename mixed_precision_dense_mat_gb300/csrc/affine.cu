@@ -284,10 +284,11 @@ __device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* 
 // ---------------------------------------------------------------- wide kernel
 // 256 x 256 outputs per CTA pair (cta_group::2): the pair's MMA has M = 256 rows j (128 per CTA, its
 // operand A = Q) and N = 256 columns i (operand B = P, half of it in each CTA; N = 128 takes as long per
-// k-block, 0.27 us).  Persistent;
-// warp 0 loads by TMA into a ring of stages, warp 1 of the first CTA issues the MMAs, warps 2-9
-// take the accumulator (two of them in TMEM, so the epilogue of one tile overlaps the next
-// tile's products) through the epilogue: a thread holds one j and 32 consecutive i.
+// k-block, 0.27 us).  Bound by the tensor cores: K = 4096, N = 8192, M = 4096 BF16 with bias and silu 149 us,
+// 1.84 PFLOP/s, the tensor pipe active 83 % of the time; e4m3 75 us, 3.64 PFLOP/s.  Persistent; warp 0
+// loads by TMA into a ring of stages, warp 1 of the first CTA issues the MMAs, warps 2-9 take the
+// accumulator (two of them in TMEM, so the epilogue of one tile overlaps the next tile's products)
+// through the epilogue: a thread holds one j and 32 consecutive i.
 constexpr int WSTAGES = 6;                       // 5 with two output buffers per warp
 constexpr int WTILE = 128 * KBYTES;              // one operand's half tile of a stage, 16 KB
 constexpr int WSTAGE = 2 * WTILE;
@@ -497,9 +498,9 @@ __global__ void __launch_bounds__(WTHREADS, 1)
 
 // ---------------------------------------------------------------- thin kernel
 // 128 outputs i x bn columns j per cluster (operand A = P, B = Q): few columns, where the product is
-// bound by reading P.  The CTAs of a cluster take equal parts of k.  Each finishes 128 / split of
-// the i: the others copy their partial sums for these into its shared memory in bulk, and it adds
-// them in the order of the parts.
+// bound by reading P (K = 4096, N = 12288, M = 16 FP16: 20 us, 5.0 TB/s).  The CTAs of a cluster take equal
+// parts of k.  Each finishes 128 / split of the i: the others copy their partial sums for these into
+// its shared memory in bulk, and it adds them in the order of the parts.
 constexpr int TTHREADS = 192;
 constexpr int TMAXSTAGES = 8;
 struct ThinBars {
@@ -732,7 +733,8 @@ __global__ void __launch_bounds__(NT) k_affine_one(const E* P, int ldp, const E*
 }
 
 // Copies a matrix whose columns of n elements start at any address into columns ld apart on 16-byte
-// boundaries: a thread gathers 16 bytes and stores them at once (elements past n are zero).
+// boundaries: a thread gathers 16 bytes and stores them at once (elements past n are zero).  Bound by the
+// gathers' narrow loads: K = 4095, N = 8192, M = 4096 BF16 takes 190 us, K = 4096 138 us.
 template <class E>
 __global__ void __launch_bounds__(NT) k_pack(const E* src, int lds, int n, int m, E* dst, int ld) {
   constexpr int V = 16 / (int)sizeof(E);
@@ -752,7 +754,8 @@ __global__ void __launch_bounds__(NT) k_pack(const E* src, int lds, int n, int m
 
 // G = dY .* act'(Z), and the row sums of its unrounded values: a block takes 32 V features and every
 // gridDim.y-th 8 columns, a thread V features of a column (V = 8: 16-byte accesses), and leaves its sums
-// in part[blockIdx.y][N].  Bound by HBM (dY and Z read, G written).
+// in part[blockIdx.y][N].  Bound by HBM (dY and Z read, G written): N = 8192, M = 2048 BF16
+// silu 18 us, 5.5 TB/s.
 template <class E, int ACT, int V>
 __global__ void __launch_bounds__(NT) k_affine_g(const E* dY, int lddy, const E* Z, int ldz, int N, int M, E* G, int ldg, float* part) {
   __shared__ float red[NT / 32][32 * V + V];

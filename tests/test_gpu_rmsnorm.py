@@ -123,6 +123,12 @@ def test_rmsnorm_backward(lib, kind, D, T):
     _backward(lib, D, T, kind, True)
 
 
+def test_rmsnorm_backward_long_columns(lib):
+    """Columns too long for registers, enough of them for the gradient of gamma to be summed in parts."""
+    _backward(lib, 17001, 70, "bf16", True)
+    _backward(lib, 16400, 37, "f32", False)
+
+
 @pytest.mark.parametrize("pad,shift", [(8, 0), (1, 0), (0, 1)])
 def test_rmsnorm_backward_strides(lib, pad, shift):
     for D in (48, 1000, 4096):
