@@ -40,7 +40,6 @@ struct Params {
   int tma_c, tma_z;      // C, Z can be stored by TMA
   int vec_r;             // R allows 16-byte accesses
   int tma_r;             // wide kernel: R comes by TMA into the output buffers (16-bit outputs)
-  int vecb;              // bias and iscale do
   int vec4;              // four consecutive i of everything in the epilogue can be accessed at once
   Epilogue e;
   unsigned long long limit;
@@ -142,23 +141,17 @@ __device__ __forceinline__ void thin_store16(const Params& p, int i, int j0, flo
     }
 }
 
-// A float vector's entries from i0 on, the same for all lanes (0 past the end).
+// A float vector's N entries from i0 on, spread over the warp's lanes (0 past the end): entry q is w[q / 32] of
+// lane q % 32, and every_entry gives it to all lanes.  Loaded ahead and handed round by shuffles: as loads of
+// the same address by all lanes, bias alone took 2.5 us per 256 x 256 tile.
 template <int N>
-__device__ __forceinline__ void load_row(const float* x, int i0, int I, int vec, float (&w)[N]) {
-  if (vec && i0 + N <= I) {
+__device__ __forceinline__ void load_row(const float* x, int i0, int I, float (&w)[N / 32]) {
+  const int i = i0 + (threadIdx.x & 31);
 #pragma unroll
-    for (int q = 0; q < N; q += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(x + i0 + q);
-      w[q] = f.x;
-      w[q + 1] = f.y;
-      w[q + 2] = f.z;
-      w[q + 3] = f.w;
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < N; ++q) w[q] = i0 + q < I ? x[i0 + q] : 0.0f;
-  }
+  for (int q = 0; q < N / 32; ++q) w[q] = x && i + 32 * q < I ? x[i + 32 * q] : 0.0f;
 }
+template <int N>
+__device__ __forceinline__ float every_entry(const float (&w)[N], int q) { return __shfl_sync(0xffffffffu, w[q / 32], q % 32); }
 
 // A warp's 32 rows j of N = OROW / sizeof(O) values from (i0, j0) live in its buffer as rows of 128 bytes in the
 // 128-byte swizzle: 16-byte word q of row r is at word q ^ (r & 7).
@@ -227,17 +220,12 @@ __device__ __forceinline__ void add_rows_of(const O* in, int ld, int I, int J, i
 // Epilogue of the warp's 32 rows j and N columns i; v holds the sums.
 template <class O, int N>
 __device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* tmC, const CUtensorMap* tmZ, int i0, int j0, float js,
-                                            uint8_t* buf, const uint8_t* rows, float* v) {
+                                            const float (&is)[N / 32], const float (&bias)[N / 32], uint8_t* buf, const uint8_t* rows, float* v) {
   const Epilogue& e = p.e;
   const int j = j0 + (threadIdx.x & 31);
   if (e.iscale) {
 #pragma unroll
-    for (int q = 0; q < N; q += 8) {
-      float w[8];
-      load_row(e.iscale, i0 + q, p.I, p.vecb, w);
-#pragma unroll
-      for (int x = 0; x < 8; ++x) v[q + x] *= w[x];
-    }
+    for (int q = 0; q < N; ++q) v[q] *= every_entry(is, q);
   }
   if (e.jscale) {
 #pragma unroll
@@ -245,12 +233,7 @@ __device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* 
   }
   if (e.bias) {
 #pragma unroll
-    for (int q = 0; q < N; q += 8) {
-      float w[8];
-      load_row(e.bias, i0 + q, p.I, p.vecb, w);
-#pragma unroll
-      for (int x = 0; x < 8; ++x) v[q + x] += w[x];
-    }
+    for (int q = 0; q < N; ++q) v[q] += every_entry(bias, q);
   }
   if (e.Z) put_rows<O, N>(tmZ, p.tma_z, (O*)e.Z, e.ldz, p.I, p.J, i0, j0, buf, false, v);
   activate_all<N>(v, e.act);
@@ -462,6 +445,9 @@ __global__ void __launch_bounds__(WTHREADS, 1)
       const float js = p.e.jscale && j0 + lane < p.J ? p.e.jscale[j0 + lane] : 1.0f;
       for (int c = 0; c < 128; c += N) {
         uint32_t v[N / 32][32];
+        float is[N / 32], bias[N / 32];
+        load_row<N>(p.e.iscale, ibase + c, p.I, is);
+        load_row<N>(p.e.bias, ibase + c, p.I, bias);
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < N / 32; ++q) tmem_ld32(tq + (uint32_t)(c + 32 * q), v[q]);
@@ -480,7 +466,7 @@ __global__ void __launch_bounds__(WTHREADS, 1)
           if (!mbar_wait(&bars->rows[warp - 2][x], (nrows >> x) & 1u, p.limit)) gave_up(p, abort_flag);
           nrows ^= 1u << x;
         }
-        wide_finish<O, N>(p, &tmC, &tmZ, ibase + c, j0, js, out, rows, reinterpret_cast<float*>(v));
+        wide_finish<O, N>(p, &tmC, &tmZ, ibase + c, j0, js, is, bias, out, rows, reinterpret_cast<float*>(v));
       }
     }
     if (lane == 0) tma_store_wait_read();
@@ -913,16 +899,18 @@ struct Choice {
 Choice choose(int I, int J, int kblocks, bool qk) {
   Choice best = {false, 0, 1, 0, 1e30};
   const auto tiles = [](int n, int t) { return (n + t - 1) / t; };
-  // Wide: rounds of tiles over the CTA pairs, 0.27 to 0.3 us per k-block.
+  // Wide: rounds of tiles over the CTA pairs, 0.27 to 0.3 us per k-block, or the epilogue of a tile.
   if (J > 128) {
     const long long t = (long long)tiles(I, 256) * tiles(J, 256), rounds = (t + sm_count() / 2 - 1) / (sm_count() / 2);
-    best = {true, 0, 1, 0, 9.4 + rounds * (kblocks * 0.29 + 1.0)};
+    best = {true, 0, 1, 0, 6.5 + rounds * std::max(kblocks * 0.29 + 0.6, 3.3)};
   }
   // Thin: parts of k for which all clusters are resident at once, with three stages or more and two
   // k-blocks or more for each CTA; a second wave of CTAs costs more than longer parts (K = 4096,
   // N = 12288, M = 16 FP16: 96 CTAs with 8 stages 23.5 us, 192 with 4 22.2 us, 384 with 3 20.8 us, 384
   // with 4, no longer resident at once, 25.8 us).  An SM takes in about 100 KB per microsecond, HBM
-  // gives less to fewer CTAs, and joining the parts costs 1 us at 16 columns, 5 at 128.
+  // gives less to fewer CTAs, joining the parts costs 1 us at 16 columns, 5 at 128, and so, nearly, does
+  // the epilogue of each tile that has to wait for an SM (K = 64, N = 8192, M = 4096 BF16 with
+  // bias and silu: thin 59 us, wide 34 us).
   for (int bn = J <= 16 ? 16 : J <= 32 ? 32 : 64; bn <= (J > 64 ? 128 : 64); bn *= 2) {
     const int stage = WTILE + (qk ? bn * KBYTES : (bn + 63) / 64 * ATOM);
     const long long t = (long long)tiles(I, 128) * tiles(J, bn);
@@ -939,7 +927,8 @@ Choice choose(int I, int J, int kblocks, bool qk) {
       if (stages < (split > 1 ? 3 : 2) || (split > 1 && stages * stage < received)) continue;
       const double ctas = (double)t * split, waves = std::max(1.0, ctas / sm_count());
       const double hbm = (double)I * kblocks * KBYTES / 5.5e6 * (1.0 + 0.25 * std::max(0.0, 1.0 - ctas / (2.5 * sm_count())));
-      const double us = 5.0 + (split > 1 ? 0.3 + 0.04 * bn : 0.0) + std::max(waves * tiles(kblocks, split) * stage / 100e3, hbm);
+      const double later = std::max(0.0, ctas / sm_count() - per) * 0.025 * bn;   // epilogues of tiles after the resident ones
+      const double us = 5.0 + later + (split > 1 ? 0.3 + 0.04 * bn : 0.0) + std::max(waves * tiles(kblocks, split) * stage / 100e3, hbm);
       if (us < best.us) best = {false, bn, split, stages, us};
     }
     if (J <= 64) break;
@@ -983,9 +972,8 @@ cr_status product(Operand P, Operand Q, int type, int K, int out_type, const Epi
   p.tma_c = ok16(e.C, e.ldc);
   p.tma_z = ok16(e.Z, e.ldz);
   p.vec_r = ok16(e.R, e.ldr);
-  p.vecb = (((uintptr_t)e.bias | (uintptr_t)e.iscale) & 15) == 0;
   const auto ok4 = [&](const void* q, int ld) { return !q || (((uintptr_t)q & (4 * ob - 1)) == 0 && ld % 4 == 0); };
-  p.vec4 = p.vecb && ok4(e.C, e.ldc) && ok4(e.R, e.ldr) && ok4(e.Z, e.ldz);
+  p.vec4 = (((uintptr_t)e.bias | (uintptr_t)e.iscale) & 15) == 0 && ok4(e.C, e.ldc) && ok4(e.R, e.ldr) && ok4(e.Z, e.ldz);
   if (p.J == 1 && p.pk && p.qk && p.I <= 64 * sm_count())   // one round of warps
     return with_type(out_type, [&](auto o0) -> cr_status {
       using O = decltype(o0);

@@ -142,102 +142,8 @@ cr_status with_type(int type, F&& f) {
   return f(__nv_bfloat16{});
 }
 
-// ---------------------------------------------------------------- activations
-// Written from the hardware's 2^x and reciprocal (each within about 2^-22), because a product's
-// epilogue shares the SM's issue slots and power with the MMAs: the K = 4096, N = 16384, M = 8192 BF16
-// product with silu took 666 us with expf and 634 us with these.  Arguments are clamped where
-// the function has reached its limit, so that infinities give limits; NaN stays.
-__device__ __forceinline__ float clamp_low(float x, float low) {
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(low));
-  return x;
-}
-__device__ __forceinline__ float clamp_high(float x, float high) {
-  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(high));
-  return x;
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x));
-  return x;
-}
-__device__ __forceinline__ float rcp_fast(float x) {
-  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x));
-  return x;
-}
-constexpr float LOG2E = 1.4426950408889634f;
-
-// 1 - Phi(|z|) times 2, and g = e^(-z^2 / 2): erfc by Hastings' rational-exponential formula (Abramowitz and
-// Stegun, Handbook of Mathematical Functions, 7.1.26), absolute error 1.5e-7.
-__device__ __forceinline__ float normal_tail(float z, float& g) {
-  const float t = rcp_fast(fmaf(fabsf(z), 0.3275911f * 0.70710678118654752f, 1.0f));
-  g = exp2_fast(z * z * (-0.5f * LOG2E));
-  float p = fmaf(t, 1.061405429f, -1.453152027f);
-  p = fmaf(t, p, 1.421413741f);
-  p = fmaf(t, p, -0.284496736f);
-  p = fmaf(t, p, 0.254829592f);
-  return t * p * g;
-}
-
-template <int ACT>
-__device__ __forceinline__ float activate(float z) {
-  if (ACT == CR_ACT_RELU) return clamp_low(z, 0.0f);
-  if (ACT == CR_ACT_SILU) {
-    z = clamp_low(z, -87.0f);
-    return z * rcp_fast(1.0f + exp2_fast(z * -LOG2E));
-  }
-  if (ACT == CR_ACT_GELU) {
-    z = clamp_low(z, -30.0f);
-    float g;
-    const float half = 0.5f * normal_tail(z, g);
-    return z * (z < 0.0f ? half : 1.0f - half);
-  }
-  return z;
-}
-
-template <int ACT>
-__device__ __forceinline__ float activation_slope(float z) {
-  if (ACT == CR_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
-  if (ACT == CR_ACT_SILU) {
-    z = clamp_high(clamp_low(z, -87.0f), 87.0f);
-    const float e = exp2_fast(z * -LOG2E), p = rcp_fast(1.0f + e);
-    return p * fmaf(z, e * p, 1.0f);
-  }
-  if (ACT == CR_ACT_GELU) {
-    z = clamp_high(clamp_low(z, -30.0f), 30.0f);
-    float g;
-    const float half = 0.5f * normal_tail(z, g);
-    return fmaf(z * 0.39894228040143268f, g, z < 0.0f ? half : 1.0f - half);
-  }
-  return 1.0f;
-}
-
-// v[] = act(v[]) with one test of `act` for all of them.
-template <int N>
-__device__ __forceinline__ void activate_all(float* v, int act) {
-  if (act == CR_ACT_RELU) {
-#pragma unroll
-    for (int q = 0; q < N; ++q) v[q] = activate<CR_ACT_RELU>(v[q]);
-  } else if (act == CR_ACT_SILU) {
-#pragma unroll
-    for (int q = 0; q < N; ++q) v[q] = activate<CR_ACT_SILU>(v[q]);
-  } else if (act == CR_ACT_GELU) {
-#pragma unroll
-    for (int q = 0; q < N; ++q) v[q] = activate<CR_ACT_GELU>(v[q]);
-  }
-}
-
-template <class F>
-cr_status with_act(int act, F&& f) {
-  switch (act) {
-    case CR_ACT_RELU: return f(std::integral_constant<int, CR_ACT_RELU>{});
-    case CR_ACT_SILU: return f(std::integral_constant<int, CR_ACT_SILU>{});
-    case CR_ACT_GELU: return f(std::integral_constant<int, CR_ACT_GELU>{});
-    default: return f(std::integral_constant<int, CR_ACT_NONE>{});
-  }
-}
-
-// ---------------------------------------------------------------- gates
-// h_t = a h_{t-1} + c x_t.  Products that feed a sum are written as fmaf or __fmul_rn, so that every
-// variant of a kernel rounds alike.
+// ---------------------------------------------------------------- one float, or two
+// Products that feed a sum are written as fmaf or __fmul_rn, so that every variant of a kernel rounds alike.
 template <int VEC>
 struct alignas(4 * VEC) Floats {   // one float, or two in the halves of a register pair
   float x[VEC];
@@ -279,6 +185,129 @@ __device__ __forceinline__ Floats<VEC> all_of(float x) {
   return v;
 }
 
+// ---------------------------------------------------------------- activations
+// Written from the hardware's 2^x and reciprocal (each within about 2^-22), because a product's
+// epilogue shares the SM's issue slots and power with the MMAs: the K = 4096, N = 16384, M = 8192 BF16
+// product with silu took 666 us with expf and 634 us with these.  Arguments are clamped where
+// the function has reached its limit, so that infinities give limits; NaN stays.
+__device__ __forceinline__ float clamp_low(float x, float low) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(low));
+  return x;
+}
+__device__ __forceinline__ float clamp_high(float x, float high) {
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(high));
+  return x;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x));
+  return x;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x));
+  return x;
+}
+constexpr float LOG2E = 1.4426950408889634f;
+
+template <int VEC>
+__device__ __forceinline__ Floats<VEC> exp2_fast(Floats<VEC> x) {
+#pragma unroll
+  for (int q = 0; q < VEC; ++q) x.x[q] = exp2_fast(x.x[q]);
+  return x;
+}
+template <int VEC>
+__device__ __forceinline__ Floats<VEC> rcp_fast(Floats<VEC> x) {
+#pragma unroll
+  for (int q = 0; q < VEC; ++q) x.x[q] = rcp_fast(x.x[q]);
+  return x;
+}
+
+// Phi(a) - 1 for a >= 0, and g = e^(-a^2 / 2): erfc by Hastings' rational-exponential formula (Abramowitz and
+// Stegun, Handbook of Mathematical Functions, 7.1.26; its coefficients here times -1/2), absolute error 7.5e-8.
+template <int VEC>
+__device__ __forceinline__ Floats<VEC> minus_tail(Floats<VEC> a, Floats<VEC>& g) {
+  const auto k = [](float x) { return all_of<VEC>(x); };
+  const Floats<VEC> t = rcp_fast(fma(a, k(0.3275911f * 0.70710678118654752f), k(1.0f)));
+  g = exp2_fast(mul(mul(a, a), k(-0.5f * LOG2E)));
+  Floats<VEC> p = fma(t, k(-0.5f * 1.061405429f), k(0.5f * 1.453152027f));
+  p = fma(t, p, k(-0.5f * 1.421413741f));
+  p = fma(t, p, k(0.5f * 0.284496736f));
+  p = fma(t, p, k(-0.5f * 0.254829592f));
+  return mul(mul(t, p), g);
+}
+
+template <int ACT, int VEC>
+__device__ __forceinline__ Floats<VEC> activate(Floats<VEC> z) {
+  if (ACT == CR_ACT_RELU) {
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) z.x[q] = clamp_low(z.x[q], 0.0f);
+  }
+  if (ACT == CR_ACT_SILU) {
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) z.x[q] = clamp_low(z.x[q], -87.0f);
+    return mul(z, rcp_fast(add(exp2_fast(mul(z, all_of<VEC>(-LOG2E))), all_of<VEC>(1.0f))));
+  }
+  if (ACT == CR_ACT_GELU) {   // z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|))
+    Floats<VEC> a, g;
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) {
+      a.x[q] = clamp_high(fabsf(z.x[q]), 30.0f);
+      z.x[q] = clamp_low(z.x[q], 0.0f);
+    }
+    return fma(a, minus_tail(a, g), z);
+  }
+  return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float activation_slope(float z) {
+  if (ACT == CR_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+  if (ACT == CR_ACT_SILU) {
+    z = clamp_high(clamp_low(z, -87.0f), 87.0f);
+    const float e = exp2_fast(z * -LOG2E), p = rcp_fast(1.0f + e);
+    return p * fmaf(z, e * p, 1.0f);
+  }
+  if (ACT == CR_ACT_GELU) {
+    z = clamp_high(clamp_low(z, -30.0f), 30.0f);
+    Floats<1> g;
+    const float m = minus_tail(Floats<1>{{fabsf(z)}}, g).x[0];
+    return fmaf(z * 0.39894228040143268f, g.x[0], z < 0.0f ? -m : 1.0f + m);
+  }
+  return 1.0f;
+}
+
+// v[] = act(v[]) with one test of `act` for all of them, two at a time.
+template <int ACT, int N>
+__device__ __forceinline__ void activate_each(float* v) {
+  constexpr int VEC = N % 2 == 0 ? 2 : 1;
+#pragma unroll
+  for (int q = 0; q < N; q += VEC) {
+    Floats<VEC> z;
+#pragma unroll
+    for (int x = 0; x < VEC; ++x) z.x[x] = v[q + x];
+    z = activate<ACT, VEC>(z);
+#pragma unroll
+    for (int x = 0; x < VEC; ++x) v[q + x] = z.x[x];
+  }
+}
+template <int N>
+__device__ __forceinline__ void activate_all(float* v, int act) {
+  if (act == CR_ACT_RELU) activate_each<CR_ACT_RELU, N>(v);
+  else if (act == CR_ACT_SILU) activate_each<CR_ACT_SILU, N>(v);
+  else if (act == CR_ACT_GELU) activate_each<CR_ACT_GELU, N>(v);
+}
+
+template <class F>
+cr_status with_act(int act, F&& f) {
+  switch (act) {
+    case CR_ACT_RELU: return f(std::integral_constant<int, CR_ACT_RELU>{});
+    case CR_ACT_SILU: return f(std::integral_constant<int, CR_ACT_SILU>{});
+    case CR_ACT_GELU: return f(std::integral_constant<int, CR_ACT_GELU>{});
+    default: return f(std::integral_constant<int, CR_ACT_NONE>{});
+  }
+}
+
+// ---------------------------------------------------------------- gates
+// h_t = a h_{t-1} + c x_t.
 template <int VEC>
 struct GateParts {
   Floats<VEC> a, rest;   // sigmoid(g) and sigmoid(-g); coefficient gate: g and 1
