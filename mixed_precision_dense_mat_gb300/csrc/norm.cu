@@ -16,7 +16,7 @@ namespace {
 // resident and go from column to column with gamma in registers.  Each group has a ring of columns in
 // shared memory, filled by bulk copies several columns ahead: loads into registers, one column
 // ahead, kept too few bytes in flight (4096 x 32768 BF16 to e4m3 with residual: 264 us,
-// with the ring 150 us, 6.3 TB/s).
+// with the ring 147 us, 6.4 TB/s).
 constexpr int NT = 256;
 constexpr int MAXD = 16384;   // longer columns: the kernels that go over memory again
 
@@ -99,6 +99,14 @@ __device__ __forceinline__ void load_gamma(const float* gamma, int D, float (&g)
     }
 }
 
+// Elements go through the arithmetic in pairs, two to an instruction (one by one: 150 us and 66 us where the kernels
+// below take 147 and 62).
+__device__ __forceinline__ Floats<2> two(const float* p) { return {{p[0], p[1]}}; }
+__device__ __forceinline__ void put(float* p, Floats<2> v) {
+  p[0] = v.x[0];
+  p[1] = v.x[1];
+}
+
 // The group's ring: `stages` stages of the NIN inputs' columns, in the block's dynamic shared memory
 // after the barriers.  The group's first thread refills the stage of the column before the present
 // one, after the exchange that all threads reach only when they are done with that column.
@@ -170,7 +178,8 @@ __global__ void __launch_bounds__(G ? NT : 512)
     for (int q = 0; q < stages - 1; ++q) fill(q, t0 + (long long)q * step);
   load_gamma<G, VPT, VEC>(gamma, D, g);
   for (int t = t0, turn = 0; t < n; t += step, turn ^= 1) {
-    float h[VPT][8], ss = 0.0f, mx = 0.0f;
+    float h[VPT][8], mx = 0.0f;
+    Floats<2> s2 = all_of<2>(0.0f);
     load_col<T, G, VPT, VEC>(VEC ? ring.take(0, wait) : X + (size_t)t * ldx, D, h);
     if (R) {
       float r[VPT][8];
@@ -178,18 +187,20 @@ __global__ void __launch_bounds__(G ? NT : 512)
 #pragma unroll
       for (int v = 0; v < VPT; ++v)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[v][e] += r[v][e];
+        for (int e = 0; e < 8; e += 2) put(&h[v][e], add(two(&h[v][e]), two(&r[v][e])));
     }
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       if (H) store8<T, G, VPT, VEC>(H + (size_t)t * ldh, D, v, h[v]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ss = fmaf(h[v][e], h[v][e], ss);
-        h[v][e] *= g[v][e];
-        if (Q) mx = nan_max(mx, fabsf(h[v][e]));
+      for (int e = 0; e < 8; e += 2) {
+        const Floats<2> x = two(&h[v][e]);
+        s2 = fma(x, x, s2);
+        put(&h[v][e], mul(x, two(&g[v][e])));
+        if (Q) mx = nan_max(nan_max(mx, fabsf(h[v][e])), fabsf(h[v][e + 1]));
       }
     }
+    float ss = s2.x[0] + s2.x[1];
     reduce2<G, true>(ss, mx, red, turn);
     if (VEC) {
       if (G == 32) __syncwarp();
@@ -206,14 +217,14 @@ __global__ void __launch_bounds__(G ? NT : 512)
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[v][e] *= f;
+      for (int e = 0; e < 8; e += 2) put(&h[v][e], mul(two(&h[v][e]), all_of<2>(f)));
       store8<O, G, VPT, VEC>(Y + (size_t)t * ldy, D, v, h[v]);
     }
   }
 }
 
 // dX = r (u - h r^2 mean(u h)) + dH with u = gamma dY, dgamma = sum dY h r.  The block's sums for dgamma go to
-// part[block][D], to be added by k_add_rows (2560 x 16411 BF16 with dH: 66 us in all, 5.1 TB/s).
+// part[block][D], to be added by k_add_rows (2560 x 16411 BF16 with dH: 62 us in all, 5.4 TB/s).
 template <class T, int G, int VPT, bool VEC>
 __global__ void __launch_bounds__(G ? NT : 512)
     k_rmsnorm_bwd(const T* H, int ldh, const float* gamma, const T* dY, int lddy, const T* dH, int lddh, int D, int n, float eps, T* dX,
@@ -234,16 +245,19 @@ __global__ void __launch_bounds__(G ? NT : 512)
   load_gamma<G, VPT, VEC>(gamma, D, g);
   for (int t = t0, turn = 0; t < n; t += step, turn ^= 1) {
     const T *ch = VEC ? ring.take(0, wait) : H + (size_t)t * ldh, *cd = VEC ? ring.take(1, wait) : dY + (size_t)t * lddy;
-    float h[VPT][8], d[VPT][8], ss = 0.0f, dot = 0.0f;
+    float h[VPT][8], d[VPT][8];
+    Floats<2> s2 = all_of<2>(0.0f), dot2 = all_of<2>(0.0f);
     load_col<T, G, VPT, VEC>(ch, D, h);
     load_col<T, G, VPT, VEC>(cd, D, d);
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ss = fmaf(h[v][e], h[v][e], ss);
-        dot = fmaf(__fmul_rn(g[v][e], d[v][e]), h[v][e], dot);
+      for (int e = 0; e < 8; e += 2) {
+        const Floats<2> x = two(&h[v][e]);
+        s2 = fma(x, x, s2);
+        dot2 = fma(mul(two(&g[v][e]), two(&d[v][e])), x, dot2);
       }
+    float ss = s2.x[0] + s2.x[1], dot = dot2.x[0] + dot2.x[1];
     const T* cr = !dH ? nullptr : VEC ? ring.take(2, wait) : dH + (size_t)t * lddh;
     reduce2<G, false>(ss, dot, red, turn);
     if (VEC) {
@@ -269,9 +283,10 @@ __global__ void __launch_bounds__(G ? NT : 512)
         }
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        dg[v][e] = fmaf(__fmul_rn(d[v][e], h[v][e]), rs, dg[v][e]);
-        o[e] += fmaf(-h[v][e], m, __fmul_rn(rs, __fmul_rn(g[v][e], d[v][e])));
+      for (int e = 0; e < 8; e += 2) {
+        const Floats<2> x = two(&h[v][e]), y = two(&d[v][e]);
+        put(&dg[v][e], fma(mul(y, x), all_of<2>(rs), two(&dg[v][e])));
+        put(&o[e], add(two(&o[e]), fma(x, all_of<2>(-m), mul(all_of<2>(rs), mul(two(&g[v][e]), y)))));
       }
       if (dX) store8<T, G, VPT, VEC>(dX + (size_t)t * lddx, D, v, o);
     }
