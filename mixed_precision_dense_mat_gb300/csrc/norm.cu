@@ -25,7 +25,7 @@ __device__ __forceinline__ float nan_max(float a, float b) { return clamp_low(a,
 
 // Two values reduced over the group: x by sum, y by sum or by maximum.  `red` is used alternately
 // (turn) so that one barrier per column is enough.
-// G = 32: a warp per column; G = 0: the block.
+// G = 8, 16 or 32: threads of a warp; G = 0: the block.
 template <int G>
 __device__ __forceinline__ int group_size() { return G ? G : (int)blockDim.x; }
 template <int G>
@@ -33,12 +33,12 @@ __device__ __forceinline__ int in_group() { return G ? (int)threadIdx.x % G : (i
 template <int G, bool MAX>
 __device__ __forceinline__ void reduce2(float& x, float& y, float2 (*red)[32], int turn) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = G ? G / 2 : 16; o > 0; o >>= 1) {
     x += __shfl_xor_sync(0xffffffffu, x, o);
     const float z = __shfl_xor_sync(0xffffffffu, y, o);
     y = MAX ? nan_max(y, z) : y + z;
   }
-  if (G == 32) return;
+  if (G) return;
   const int warp = threadIdx.x >> 5;
   if ((threadIdx.x & 31) == 0) red[turn][warp] = make_float2(x, y);
   __syncthreads();
@@ -107,6 +107,10 @@ __device__ __forceinline__ void put(float* p, Floats<2> v) {
   p[1] = v.x[1];
 }
 
+// Columns shorter than a warp's reach are read directly: a block has many of them in flight anyway.
+template <int G, bool VEC>
+__host__ __device__ constexpr bool uses_ring() { return VEC && (G == 0 || G == 32); }
+
 // The group's ring: `stages` stages of the NIN inputs' columns, in the block's dynamic shared memory
 // after the barriers.  The group's first thread refills the stage of the column before the present
 // one, after the exchange that all threads reach only when they are done with that column.
@@ -162,28 +166,30 @@ template <class T, class O, int G, int VPT, bool VEC>
 __global__ void __launch_bounds__(G ? NT : 512)
     k_rmsnorm(const T* X, int ldx, const T* R, int ldr, const float* gamma, int D, int n, float eps, T* H, int ldh, O* Y, int ldy,
               float* scale, int stages, const Wait wait) {
-  constexpr bool Q = std::is_same<O, __nv_fp8_e4m3>::value;
-  constexpr int PER = G ? NT / 32 : 1;   // columns per block at a time
+  constexpr bool Q = std::is_same<O, __nv_fp8_e4m3>::value, RING = uses_ring<G, VEC>();
+  constexpr int PER = G ? NT / G : 1;   // columns per block at a time
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 red[2][32];
-  Ring<T, G, 2> ring(smem, VEC ? stages : 0, D, wait);
+  Ring<T, G, 2> ring(smem, RING ? stages : 0, D, wait);
   let_next_start();
   wait_for_previous();
   float g[VPT][8];
-  const int step = gridDim.x * PER, t0 = blockIdx.x * PER + (G ? threadIdx.x / 32 : 0);
+  const int step = gridDim.x * PER, t0 = blockIdx.x * PER + (G ? threadIdx.x / G : 0), sub = G ? threadIdx.x % 32 / G : 0;
   const auto fill = [&](int stage, long long t) {
     if (t < n) ring.fill(stage, {X + (size_t)t * ldx, R ? R + (size_t)t * ldr : nullptr});
   };
-  if (VEC && in_group<G>() == 0)
+  if (RING && in_group<G>() == 0)
     for (int q = 0; q < stages - 1; ++q) fill(q, t0 + (long long)q * step);
   load_gamma<G, VPT, VEC>(gamma, D, g);
-  for (int t = t0, turn = 0; t < n; t += step, turn ^= 1) {
+  for (int t = t0, turn = 0; t - sub < n; t += step, turn ^= 1) {   // the groups of a warp stay together
+    const bool live = G == 0 || G == 32 || t < n;
+    const size_t c = live ? t : n - 1;
     float h[VPT][8], mx = 0.0f;
     Floats<2> s2 = all_of<2>(0.0f);
-    load_col<T, G, VPT, VEC>(VEC ? ring.take(0, wait) : X + (size_t)t * ldx, D, h);
+    load_col<T, G, VPT, VEC>(RING ? ring.take(0, wait) : X + c * ldx, D, h);
     if (R) {
       float r[VPT][8];
-      load_col<T, G, VPT, VEC>(VEC ? ring.take(1, wait) : R + (size_t)t * ldr, D, r);
+      load_col<T, G, VPT, VEC>(RING ? ring.take(1, wait) : R + c * ldr, D, r);
 #pragma unroll
       for (int v = 0; v < VPT; ++v)
 #pragma unroll
@@ -191,7 +197,7 @@ __global__ void __launch_bounds__(G ? NT : 512)
     }
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      if (H) store8<T, G, VPT, VEC>(H + (size_t)t * ldh, D, v, h[v]);
+      if (H && live) store8<T, G, VPT, VEC>(H + c * ldh, D, v, h[v]);
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
         const Floats<2> x = two(&h[v][e]);
@@ -202,7 +208,7 @@ __global__ void __launch_bounds__(G ? NT : 512)
     }
     float ss = s2.x[0] + s2.x[1];
     reduce2<G, true>(ss, mx, red, turn);
-    if (VEC) {
+    if (RING) {
       if (G == 32) __syncwarp();
       if (in_group<G>() == 0) fill((ring.st ? ring.st : stages) - 1, t + (long long)(stages - 1) * step);
       ring.next();
@@ -211,14 +217,14 @@ __global__ void __launch_bounds__(G ? NT : 512)
     float f = rs;
     if (Q) {
       const float s = nan_max(mx * rs, 0x1p-100f) / 448.0f;
-      if (in_group<G>() == 0) scale[t] = s;
+      if (in_group<G>() == 0 && live) scale[c] = s;
       f = clamp_high(rs * (1.0f / s), 3.0e38f);   // kept finite, for columns of zeros
     }
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
 #pragma unroll
       for (int e = 0; e < 8; e += 2) put(&h[v][e], mul(two(&h[v][e]), all_of<2>(f)));
-      store8<O, G, VPT, VEC>(Y + (size_t)t * ldy, D, v, h[v]);
+      if (live) store8<O, G, VPT, VEC>(Y + c * ldy, D, v, h[v]);
     }
   }
 }
@@ -229,22 +235,25 @@ template <class T, int G, int VPT, bool VEC>
 __global__ void __launch_bounds__(G ? NT : 512)
     k_rmsnorm_bwd(const T* H, int ldh, const float* gamma, const T* dY, int lddy, const T* dH, int lddh, int D, int n, float eps, T* dX,
                   int lddx, float* part, int stages, const Wait wait) {
-  constexpr int PER = G ? NT / 32 : 1;
+  constexpr bool RING = uses_ring<G, VEC>();
+  constexpr int PER = G ? NT / G : 1;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 red[2][32];
-  Ring<T, G, 3> ring(smem, VEC ? stages : 0, D, wait);
+  Ring<T, G, 3> ring(smem, RING ? stages : 0, D, wait);
   let_next_start();
   wait_for_previous();
   float g[VPT][8], dg[VPT][8] = {};
-  const int step = gridDim.x * PER, t0 = blockIdx.x * PER + (G ? threadIdx.x / 32 : 0);
+  const int step = gridDim.x * PER, t0 = blockIdx.x * PER + (G ? threadIdx.x / G : 0), sub = G ? threadIdx.x % 32 / G : 0;
   const auto fill = [&](int stage, long long t) {
     if (t < n) ring.fill(stage, {H + (size_t)t * ldh, dY + (size_t)t * lddy, dH ? dH + (size_t)t * lddh : nullptr});
   };
-  if (VEC && in_group<G>() == 0)
+  if (RING && in_group<G>() == 0)
     for (int q = 0; q < stages - 1; ++q) fill(q, t0 + (long long)q * step);
   load_gamma<G, VPT, VEC>(gamma, D, g);
-  for (int t = t0, turn = 0; t < n; t += step, turn ^= 1) {
-    const T *ch = VEC ? ring.take(0, wait) : H + (size_t)t * ldh, *cd = VEC ? ring.take(1, wait) : dY + (size_t)t * lddy;
+  for (int t = t0, turn = 0; t - sub < n; t += step, turn ^= 1) {
+    const bool live = G == 0 || G == 32 || t < n;
+    const size_t c = live ? t : n - 1;
+    const T *ch = RING ? ring.take(0, wait) : H + c * ldh, *cd = RING ? ring.take(1, wait) : dY + c * lddy;
     float h[VPT][8], d[VPT][8];
     Floats<2> s2 = all_of<2>(0.0f), dot2 = all_of<2>(0.0f);
     load_col<T, G, VPT, VEC>(ch, D, h);
@@ -258,9 +267,9 @@ __global__ void __launch_bounds__(G ? NT : 512)
         dot2 = fma(mul(two(&g[v][e]), two(&d[v][e])), x, dot2);
       }
     float ss = s2.x[0] + s2.x[1], dot = dot2.x[0] + dot2.x[1];
-    const T* cr = !dH ? nullptr : VEC ? ring.take(2, wait) : dH + (size_t)t * lddh;
+    const T* cr = !dH ? nullptr : RING ? ring.take(2, wait) : dH + c * lddh;
     reduce2<G, false>(ss, dot, red, turn);
-    if (VEC) {
+    if (RING) {
       if (G == 32) __syncwarp();
       if (in_group<G>() == 0) fill((ring.st ? ring.st : stages) - 1, t + (long long)(stages - 1) * step);
     }
@@ -285,16 +294,16 @@ __global__ void __launch_bounds__(G ? NT : 512)
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
         const Floats<2> x = two(&h[v][e]), y = two(&d[v][e]);
-        put(&dg[v][e], fma(mul(y, x), all_of<2>(rs), two(&dg[v][e])));
+        if (live) put(&dg[v][e], fma(mul(y, x), all_of<2>(rs), two(&dg[v][e])));
         put(&o[e], add(two(&o[e]), fma(x, all_of<2>(-m), mul(all_of<2>(rs), mul(two(&g[v][e]), y)))));
       }
-      if (dX) store8<T, G, VPT, VEC>(dX + (size_t)t * lddx, D, v, o);
+      if (dX && live) store8<T, G, VPT, VEC>(dX + c * lddx, D, v, o);
     }
-    if (VEC) ring.next();
+    if (RING) ring.next();
   }
   if (!part) return;
   float* out = part + (size_t)blockIdx.x * D;
-  if (G != 32) {
+  if (G == 0) {
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
 #pragma unroll
@@ -308,11 +317,14 @@ __global__ void __launch_bounds__(G ? NT : 512)
     for (int v = 0; v < VPT; ++v)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
+        float own = dg[v][e];
+#pragma unroll
+        for (int o = 16; o >= G && o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);   // the warp's groups
         __syncthreads();
-        sum[threadIdx.x >> 5][threadIdx.x & 31] = dg[v][e];
+        sum[threadIdx.x >> 5][threadIdx.x & 31] = own;
         __syncthreads();
         const int i = element<G, VPT, VEC>(v, e);
-        if (threadIdx.x < 32 && i < D) {
+        if (threadIdx.x < G && i < D) {
           float x = 0.0f;
           for (int w = 0; w < NT / 32; ++w) x += sum[w][threadIdx.x];
           out[i] = x;
@@ -436,7 +448,8 @@ __global__ void __launch_bounds__(NT) k_rmsnorm_dgamma_long(const T* H, int ldh,
   part[(size_t)blockIdx.y * D + i] = s;
 }
 
-// Calls f(group, vectors per thread, 16-byte accesses) as integral constants for columns of D: a warp
+// Calls f(group, vectors per thread, 16-byte accesses) as integral constants for columns of D: 8 or 16
+// threads per column up to 64 and 128 (64 x 1048576 BF16 with residual: 90 us, a warp per column 260 us), a warp
 // per column up to 1024, then a block of as many warps as the column fills.
 template <class F>
 cr_status with_split(int D, bool vec, F&& f) {
@@ -444,6 +457,8 @@ cr_status with_split(int D, bool vec, F&& f) {
     return vec ? f(g, v, std::true_type{}) : f(g, v, std::false_type{});
   };
   using std::integral_constant;
+  if (D <= 64) return go(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  if (D <= 128) return go(integral_constant<int, 16>{}, integral_constant<int, 1>{});
   if (D <= 256) return go(integral_constant<int, 32>{}, integral_constant<int, 1>{});
   if (!vec && D <= 1024) return f(integral_constant<int, 0>{}, integral_constant<int, 1>{}, std::false_type{});
   if (D <= 512) return go(integral_constant<int, 32>{}, integral_constant<int, 2>{});
@@ -502,12 +517,12 @@ struct Fwd {
 };
 template <class T, class O, int G, int VPT, bool VEC>
 cr_status launch_fwd(const Fwd& p, cudaStream_t stream) {
-  constexpr int PER = G ? NT / 32 : 1;
+  constexpr int PER = G ? NT / G : 1;
   const int TH = threads_for(G, VPT, p.D);
   Wait wait = {option_wait_ns(), nullptr};
   CR_TRY(wait_word(&wait.err));
   Plan plan;
-  CR_TRY(make_plan(plan, k_rmsnorm<T, O, G, VPT, VEC>, TH, p.n, PER, VEC, 2, p.D, sizeof(T)));
+  CR_TRY(make_plan(plan, k_rmsnorm<T, O, G, VPT, VEC>, TH, p.n, PER, uses_ring<G, VEC>(), 2, p.D, sizeof(T)));
   TimedScope ts("k_rmsnorm", stream);
   CR_CUDA(launch_after(k_rmsnorm<T, O, G, VPT, VEC>, plan.blocks, TH, plan.smem, 1, stream, (const T*)p.X, p.ldx, (const T*)p.R, p.ldr,
                        p.gamma, p.D, p.n, p.eps, (T*)p.H, p.ldh, (O*)p.Y, p.ldy, p.scale, plan.stages, wait));
@@ -527,12 +542,12 @@ struct Bwd {
 };
 template <class T, int G, int VPT, bool VEC>
 cr_status launch_bwd(const Bwd& p, cudaStream_t stream) {
-  constexpr int PER = G ? NT / 32 : 1;
+  constexpr int PER = G ? NT / G : 1;
   const int TH = threads_for(G, VPT, p.D);
   Wait wait = {option_wait_ns(), nullptr};
   CR_TRY(wait_word(&wait.err));
   Plan plan;
-  CR_TRY(make_plan(plan, k_rmsnorm_bwd<T, G, VPT, VEC>, TH, p.n, PER, VEC, 3, p.D, sizeof(T)));
+  CR_TRY(make_plan(plan, k_rmsnorm_bwd<T, G, VPT, VEC>, TH, p.n, PER, uses_ring<G, VEC>(), 3, p.D, sizeof(T)));
   const int blocks = plan.blocks;
   float* part = nullptr;
   if (p.dgamma) CR_CUDA(scratch_alloc((void**)&part, (size_t)blocks * p.D * sizeof(float), stream));
