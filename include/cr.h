@@ -505,7 +505,11 @@ cr_status cr_rmsnorm_backward(int type, const void* d_H, int ldh, const float* d
  * 2^125).  hT (D x n_seq FP32, may be NULL) receives the last state of each series, h0 where
  * it is empty.  d_H may be NULL.  d_saved (may be NULL) receives the states that
  * cr_gated_scan_backward restarts from: *count of cr_gated_scan_saved FP32 values.
- * Series do not mix: a NaN or infinity in one leaves the others alone. */
+ * Series do not mix: a NaN or infinity in one leaves the others alone; in its own it lasts to the end.
+ * With CR_GATE_COEFF g may have any size.  Products of up to 1024 consecutive coefficients (512 in the
+ * gradient) are formed in FP32: a state times one that underflows counts as zero, and a state
+ * times one that overflows, unless it is exactly zero, as infinite, even where the coefficients
+ * after it would have brought it back into range. */
 cr_status cr_gated_scan_saved(int D, int T, size_t* count);
 cr_status cr_gated_scan(int type, int gate, const void* d_G, int ldg, const void* d_X, int ldx,
                         int D, int T, const int32_t* d_off, int n_seq, const float* d_h0,

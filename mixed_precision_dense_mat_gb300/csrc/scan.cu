@@ -19,9 +19,9 @@ namespace {
 // for its map and, once the state before it is known, for the outputs, so that HBM is read once
 // and few registers are held meanwhile: several blocks fit on an SM, which covers the time that
 // a block waits for its predecessors.
-// The map of a run of steps on the state is h -> A h + B, and such maps compose; "start from
-// h0" is the map A = 0, B = h0, so that packed series need no other care (A = 0 is taken as "forget",
-// not multiplied, so that nothing crosses into the next series).  Warps join their maps in
+// The map of a run of steps on the state is h -> A h + B, and such maps compose; a run in which a
+// series starts has a mark of its own in place of A, so that nothing crosses into the next series and
+// everything else, NaN and infinities too, goes on.  Warps join their maps in
 // shared memory, chunks through global memory in two levels: a chunk composes the maps of the
 // earlier chunks of its group, and takes the state before the group from the group's
 // predecessor.  Every composition has a fixed order, so results do not depend on timing.
@@ -50,15 +50,6 @@ struct Lookback {
   int* err;
 };
 
-__device__ __forceinline__ void forget_or(float& A, float& B, float a, float b) {   // (a, b) after (A, B)
-  B = a == 0.0f ? b : fmaf(a, B, b);
-  A = a == 0.0f ? 0.0f : A * a;
-}
-__device__ __forceinline__ float apply_map(float A, float B, float h) { return A == 0.0f ? B : fmaf(A, h, B); }
-
-__device__ __forceinline__ Word map_word(float A, float B) {
-  return (Word)__float_as_uint(B) << 32 | __float_as_uint(A == 0.0f ? -0.0f : A);
-}
 __device__ __forceinline__ void post(Word* p, Word w) {
   asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(w) : "memory");
 }
@@ -66,6 +57,91 @@ __device__ __forceinline__ Word peek(const Word* p) {
   Word w;
   asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(w) : "l"(p) : "memory");
   return w;
+}
+// A of a map: 0, a series starts in the run and the state before it does not count; ZERO, one of the run's
+// coefficients is 0; +-TINY, their product underflowed; else the product, which may be infinite.  ZERO and TINY leave
+// nothing of a finite state, but infinities and NaN go on.  With sigmoids for coefficients there is no ZERO and
+// nothing grows, so that maps are multiply-adds throughout.  With coefficients of any size a state that is not
+// finite, and a map that makes it so, go by the rules of through_exactly: an infinite A leaves a state of exactly
+// zero alone, since the product may only have overflowed (a coefficient that is infinite or NaN is in B already).
+// Watching for that costs the coefficient gate 5 % (2048 x 65536 BF16: 175 us, without 166).
+constexpr float ZERO = 0x1p-149f, TINY = 0x1p-148f;
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+__device__ __forceinline__ float through_exactly(float2 m, float h) {   // the state after map m
+  const float a = fabsf(m.x);
+  if (a == 0.0f || h == 0.0f || (a <= TINY && is_finite(h))) return m.y;
+  return fmaf(a == ZERO ? 0.0f : m.x, h, m.y);
+}
+__device__ __forceinline__ float2 then_exactly(float2 m, float2 n) {   // n after m
+  const float B = through_exactly(n, m.y), p = m.x * n.x, low = fminf(fabsf(m.x), fabsf(n.x));
+  if (low == 0.0f) return make_float2(0.0f, B);
+  if (low == ZERO) return make_float2(is_finite(p) ? ZERO : p * 0.0f, B);
+  return make_float2(fabsf(p) <= TINY || (low == TINY && is_finite(p)) ? copysignf(TINY, p) : p, B);
+}
+// n maps in a row, `step` apart, of shared memory or of the words of chunks; and a state through n maps, with the
+// states before them left in before[k * step].x (NULL: not wanted).  Calls, to cost the usual path no registers.
+__device__ __noinline__ float2 joined_exactly(const float2* maps, int step, int n) {
+  float2 m = make_float2(1.0f, 0.0f);
+  for (int k = 0; k < n; ++k) m = then_exactly(m, maps[k * step]);
+  return m;
+}
+__device__ __noinline__ float2 joined_exactly(const Word* maps, size_t step, int n) {
+  float2 m = make_float2(1.0f, 0.0f);
+  for (int k = 0; k < n; ++k) {
+    const Word w = peek(maps + k * step);
+    m = then_exactly(m, make_float2(__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32))));
+  }
+  return m;
+}
+__device__ __noinline__ float carried_exactly(const float2* maps, int step, int n, float h, float2* before) {
+  for (int k = 0; k < n; ++k) {
+    if (before) before[k * step].x = h;
+    h = through_exactly(maps[k * step], h);
+  }
+  return h;
+}
+// Maps in a row as multiply-adds; exact(): no rule of then_exactly says anything else.
+template <int GATE>
+struct Joined {
+  static constexpr bool ANY = GATE == CR_GATE_COEFF;
+  float A = 1.0f, B = 0.0f, low = 1.0f, odd = 0.0f;
+  __device__ __forceinline__ void add(float a, float b) {
+    B = fabsf(a) <= (ANY ? TINY : 0.0f) ? b : fmaf(a, B, b);
+    A *= a;
+    low = fminf(low, fabsf(a));
+    if (ANY) odd = fmaf(B, 0.0f, odd);   // NaN from the first B on that is not finite
+  }
+  __device__ __forceinline__ bool exact() const { return !ANY || odd == 0.0f; }
+  __device__ __forceinline__ float2 map() const {
+    if (ANY) return make_float2(low <= TINY ? copysignf(low, A) : fabsf(A) <= TINY ? copysignf(TINY, A) : A, B);
+    return make_float2(low == 0.0f ? 0.0f : fmaxf(A, TINY), B);
+  }
+};
+// A state through maps as multiply-adds; exact(): it was finite before and after each.
+template <int GATE>
+struct Carried {
+  static constexpr bool ANY = GATE == CR_GATE_COEFF;
+  float h, odd;
+  __device__ __forceinline__ Carried(float h0) : h(h0), odd(ANY ? h0 * 0.0f : 0.0f) {}
+  __device__ __forceinline__ void go(float2 m) {
+    h = fabsf(m.x) <= (ANY ? TINY : 0.0f) ? m.y : fmaf(m.x, h, m.y);
+    if (ANY) odd = fmaf(h, 0.0f, odd);
+  }
+  __device__ __forceinline__ bool exact() const { return !ANY || odd == 0.0f; }
+};
+// A of a run of steps from the product of its coefficients, zero(v) saying whether one of them is 0.
+template <int GATE, int VEC, class Zero>
+__device__ __forceinline__ void mark_product(Floats<VEC>& A, bool start, Zero&& zero) {
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    if (start) A.x[v] = 0.0f;
+    else if (GATE != CR_GATE_COEFF) A.x[v] = fmaxf(A.x[v], TINY);   // (NaN is in B too)
+    else if (!(fabsf(A.x[v]) > TINY)) A.x[v] = zero(v) ? ZERO : A.x[v] == A.x[v] ? copysignf(TINY, A.x[v]) : A.x[v];
+  }
+}
+
+__device__ __forceinline__ Word map_word(float2 m) {
+  return (Word)__float_as_uint(m.y) << 32 | __float_as_uint(m.x == 0.0f ? -0.0f : m.x);
 }
 // Reads N words, `stride` apart, of which the first n are waited for (the others stay 0); false when
 // the limit runs out.
@@ -157,6 +233,7 @@ struct Shared {
   int place[STAGES];
   int first[STAGES][CH], last[STAGES][CH];
   float2 maps[WARPS][W], fold[WARPS][W];   // fold[.].x: then the states that enter the warps
+  float2 total[W];                         // the chunk's map, kept by a group's last chunk
   int bad;
 };
 
@@ -250,7 +327,7 @@ __device__ __forceinline__ int next_item(const Lookback& lb, S* sh, int it) {
 // part of each warp, in sh->fold[warp][feature].x.  Warps compose in the order 0 .. 7, or 7 .. 0 with REVERSE.  All
 // workers call it; meanwhile() runs between posting the chunk's map and waiting for others; false when a
 // wait ran out.
-template <bool REVERSE, int VEC, int W, class S, class Meanwhile>
+template <int GATE, bool REVERSE, int VEC, int W, class S, class Meanwhile>
 __device__ __forceinline__ bool join(const Lookback& lb, S* sh, int tile, int k, const Floats<VEC>& A, const Floats<VEC>& B,
                                      Meanwhile&& meanwhile) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -261,14 +338,18 @@ __device__ __forceinline__ bool join(const Lookback& lb, S* sh, int tile, int k,
   const bool more = k + 1 < lb.chunks, lastin = in == lb.group - 1;
   // one thread per feature: the chunk's map
   const int x = threadIdx.x, fx = tile * W + x;
-  float TA = 1.0f, TB = 0.0f;
+  constexpr int STEP = REVERSE ? -W : W;   // from one warp's maps to the next's
+  const int w0 = REVERSE ? WARPS - 1 : 0;
   if (x < W) {
+    Joined<GATE> all;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
       const float2 m = sh->maps[REVERSE ? WARPS - 1 - w : w][x];
-      forget_or(TA, TB, m.x, m.y);
+      all.add(m.x, m.y);
     }
-    if (more && !lastin) post(lb.maps + (size_t)k * lb.width + fx, map_word(TA, TB));
+    const float2 total = all.exact() ? all.map() : joined_exactly(&sh->maps[w0][x], STEP, WARPS);
+    if (lastin) sh->total[x] = total;
+    else if (more) post(lb.maps + (size_t)k * lb.width + fx, map_word(total));
   }
   meanwhile();
   bool fine = true;
@@ -279,15 +360,15 @@ __device__ __forceinline__ bool join(const Lookback& lb, S* sh, int tile, int k,
     bool ok = true;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
-      float FA = 1.0f, FB = 0.0f;
+      Joined<GATE> all;
       for (int q = 0; q < n; q += 4) {
         Word w[4];
         ok = await(lb.maps + (size_t)(c0 + q0 + q) * lb.width + tile * W + 32 * v + lane, lb.width, n - q, lb, w) && ok;
 #pragma unroll
         for (int y = 0; y < 4; ++y)
-          if (q + y < n) forget_or(FA, FB, __uint_as_float((uint32_t)w[y]), __uint_as_float((uint32_t)(w[y] >> 32)));
+          if (q + y < n) all.add(__uint_as_float((uint32_t)w[y]), __uint_as_float((uint32_t)(w[y] >> 32)));
       }
-      sh->fold[warp][32 * v + lane] = make_float2(FA, FB);
+      sh->fold[warp][32 * v + lane] = all.exact() ? all.map() : joined_exactly(lb.maps + (size_t)(c0 + q0) * lb.width + tile * W + 32 * v + lane, lb.width, n);
     }
     if (x < W && g > 0) {
       Word w[1];
@@ -300,17 +381,25 @@ __device__ __forceinline__ bool join(const Lookback& lb, S* sh, int tile, int k,
   }
   if (x < W) {
     if (lb.chunks > 1) {
+      Carried<GATE> state(h);
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) h = apply_map(sh->fold[w][x].x, sh->fold[w][x].y, h);
-      if (lastin && more)
-        post(lb.states + (size_t)g * lb.width + fx, (Word)__float_as_uint(apply_map(TA, TB, h)) << 32 | 1u);
+      for (int w = 0; w < WARPS; ++w) state.go(sh->fold[w][x]);
+      h = state.exact() ? state.h : carried_exactly(&sh->fold[0][x], W, WARPS, h, nullptr);
+      if (lastin && more) {
+        Carried<GATE> next(h);
+        next.go(sh->total[x]);
+        if (!next.exact()) next.h = through_exactly(sh->total[x], h);
+        post(lb.states + (size_t)g * lb.width + fx, (Word)__float_as_uint(next.h) << 32 | 1u);
+      }
     }
+    Carried<GATE> state(h);
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
       const int u = REVERSE ? WARPS - 1 - w : w;
-      sh->fold[u][x].x = h;
-      h = apply_map(sh->maps[u][x].x, sh->maps[u][x].y, h);
+      sh->fold[u][x].x = state.h;
+      if (w + 1 < WARPS) state.go(sh->maps[u][x]);
     }
+    if (!state.exact()) carried_exactly(&sh->maps[w0][x], STEP, WARPS, h, &sh->fold[w0][x]);
   }
   workers_sync();
   return fine;
@@ -367,8 +456,8 @@ __device__ __forceinline__ void put(T* out, int ld, int t, int f, int D, bool ve
   }
 }
 
-// Forward scan.  HBM (G and X read, H written) would take 119 us for 2048 x 65536 BF16; it takes 162 us with
-// coefficients, 192 with the convex gate, 218 with the variance gate: the gates' 2^x, reciprocal and square
+// Forward scan.  HBM (G and X read, H written) would take 119 us for 2048 x 65536 BF16; it takes 175 us with
+// coefficients, 196 with the convex gate, 222 with the variance gate: the gates' 2^x, reciprocal and square
 // root, made twice, and the waits for the chunks before.  Kept in registers and shared memory between the two passes
 // they cost more (204 us, convex): fewer blocks fit.  Steps past the end and features past D hold
 // zeros: their states are never used.
@@ -437,16 +526,17 @@ __global__ void __launch_bounds__(NT, FBLOCKS)
     } else {
 #pragma unroll 1
       for (int i = 0; i < FSUB; ++i) {
-        if (starts >> i & 1u) {
-          A = all_of<VEC>(0.0f);
-          load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, B);
-        }
+        if (starts >> i & 1u) load_state<VEC>(p.h0, p.ldh0, first[i], f, p.D, B);
         step(i, a, b);
-        A = mul(A, a);
         B = fma(a, B, b);
       }
     }
-    if (!join<false, VEC, W>(lb, sh, tile, k, A, B, [] {})) return;   // (one stage: no copies in flight)
+    mark_product<GATE>(A, starts != 0, [&](int v) {
+      bool zero = false;
+      for (int i = 0; i < FSUB; ++i) zero = zero || widened<T, VEC>(row + i * ROW).x[v] == 0.0f;
+      return zero;
+    });
+    if (!join<GATE, false, VEC, W>(lb, sh, tile, k, A, B, [] {})) return;   // (one stage: no copies in flight)
     Floats<VEC> h;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) h.x[v] = sh->fold[warp][lane * VEC + v].x;
@@ -576,14 +666,17 @@ __global__ void __launch_bounds__(NT, BBLOCKS)
     } else {
 #pragma unroll
       for (int i = SUB - 1; i >= 0; --i) {
-        if (ends >> i & 1u) {
-          RA = all_of<VEC>(0.0f);
-          load_state<VEC>(p.dhT, p.lddhT, last[i], f, p.D, RB);
-        }
+        if (ends >> i & 1u) load_state<VEC>(p.dhT, p.lddhT, last[i], f, p.D, RB);
         gates(i);
       }
     }
-    const bool fine = join<true, VEC, W>(lb, sh, tile, k, RA, RB, [&] {
+    mark_product<GATE>(RA, ends != 0, [&](int v) {
+      bool zero = false;
+#pragma unroll
+      for (int i = 0; i < SUB; ++i) zero = zero || a[i].x[v] == 0.0f;
+      return zero;
+    });
+    const bool fine = join<GATE, true, VEC, W>(lb, sh, tile, k, RA, RB, [&] {
       if (!starts) {
 #pragma unroll
         for (int i = 0; i < SUB; ++i) states(i);
