@@ -59,6 +59,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
   }
 }
 
+// After a wait that ran out, the limit for what is in flight all the same (copies into shared memory, MMAs) and lands
+// without anybody's help; the limits of waits for others may be shorter.
+constexpr uint64_t LANDING_NS = 2000000000ull;
+
 // The same by a whole warp: true on all lanes, or false on all.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns));

@@ -249,9 +249,11 @@ __device__ __forceinline__ void feed(const Lookback& lb, Shared<CH, W, STAGES>* 
                                      const int32_t* off, int series, int n, Item&& item, Empty&& empty) {
   const int lane = threadIdx.x & 31, total = lb.chunks * lb.tiles;
   int it = 0;
+  bool done = false;
   for (;; ++it) {
     const int st = it % STAGES;
-    if (!mbar_wait(&sh->empty[st], ((uint32_t)(it / STAGES) & 1u) ^ 1u, lb.limit) || *(volatile int*)&sh->bad) break;
+    const bool go = mbar_wait(&sh->empty[st], ((uint32_t)(it / STAGES) & 1u) ^ 1u, lb.limit) && !*(volatile int*)&sh->bad;
+    if (!__all_sync(0xffffffffu, go)) break;   // the lanes' clocks and reads differ: they leave together
     int place = 0;   // taken late: an item held back here holds up the blocks that wait for its map
     if (lane == 0) place = lb.chunks > 1 ? atomicAdd(lb.counter, 1) : (int)blockIdx.x + it * (int)gridDim.x;
     place = __shfl_sync(0xffffffffu, place, 0);
@@ -260,7 +262,8 @@ __device__ __forceinline__ void feed(const Lookback& lb, Shared<CH, W, STAGES>* 
         sh->place[st] = -1;
         mbar_arrive(&sh->full[st]);
       }
-      return;
+      done = true;
+      break;
     }
     int tile, t0;
     item(place, tile, t0);
@@ -276,13 +279,16 @@ __device__ __forceinline__ void feed(const Lookback& lb, Shared<CH, W, STAGES>* 
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh->full[st]);
   }
-  // gave up: copies in flight land before the block leaves
+  // Copies in flight land before the block leaves, whatever became of the workers.  (When all items are taken, the one
+  // before in the last stage is done with, and its barrier has gone on.)
   __syncwarp();
   if (lane == 0) {
-    *(volatile int*)lb.err = 1;
-    __threadfence_system();
-    for (int q = 1; tma && q <= STAGES && q <= it; ++q)
-      mbar_wait(&sh->full[(it - q) % STAGES], (uint32_t)((it - q) / STAGES) & 1u, lb.limit);
+    if (!done) {
+      *(volatile int*)lb.err = 1;
+      __threadfence_system();
+    }
+    for (int q = 1; tma && q <= STAGES - (done ? 1 : 0) && q <= it; ++q)
+      mbar_wait(&sh->full[(it - q) % STAGES], (uint32_t)((it - q) / STAGES) & 1u, LANDING_NS);
   }
 }
 
@@ -536,7 +542,7 @@ __global__ void __launch_bounds__(NT, FBLOCKS)
       for (int i = 0; i < FSUB; ++i) zero = zero || widened<T, VEC>(row + i * ROW).x[v] == 0.0f;
       return zero;
     });
-    if (!join<GATE, false, VEC, W>(lb, sh, tile, k, A, B, [] {})) return;   // (one stage: no copies in flight)
+    if (!join<GATE, false, VEC, W>(lb, sh, tile, k, A, B, [] {})) return;
     Floats<VEC> h;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) h.x[v] = sh->fold[warp][lane * VEC + v].x;
@@ -688,10 +694,7 @@ __global__ void __launch_bounds__(NT, BBLOCKS)
         }
       }
     });
-    if (!fine) {
-      mbar_wait(&sh->full[(it + 1) % BSTAGES], (uint32_t)((it + 1) / BSTAGES) & 1u, lb.limit);   // the next item's copies land first
-      return;
-    }
+    if (!fine) return;
     Floats<VEC> q;
 #pragma unroll
     for (int v = 0; v < VEC; ++v) q.x[v] = sh->fold[warp][lane * VEC + v].x;

@@ -1,0 +1,53 @@
+"""Bounded waits of the trend-network operators: with a limit of zero (CR_OPT_WAIT_LIMIT_US) they give up wherever
+they find something not yet there.  The calls end, the next one reports it once, and the operators work as before."""
+import pytest
+import torch
+
+from test_gpu_faults import option
+
+pytestmark = pytest.mark.gpu
+
+
+def _list(out):
+    return [t for t in (out if isinstance(out, tuple) else (out,)) if t is not None]
+
+
+def _expire(lib, call, tries=50):
+    """Whether a call with a zero limit was reported as expired by the one after it."""
+    with option(lib, lib.CR_OPT_WAIT_LIMIT_US, 0):
+        for _ in range(tries):
+            try:
+                call()
+            except lib.CrError as e:
+                assert e.name == "CR_ERR_TIMEOUT"
+                return True
+            torch.cuda.synchronize()
+    return False
+
+
+def _check(lib, call, surely=True):
+    want = [t.clone() for t in _list(call())]
+    torch.cuda.synchronize()
+    expired = _expire(lib, call)
+    assert expired or not surely
+    if not expired:   # nothing left to report, or the last try's
+        try:
+            call()
+        except lib.CrError as e:
+            assert e.name == "CR_ERR_TIMEOUT"
+    assert lib.get_option(lib.CR_OPT_WAIT_LIMIT_US) == 2000000
+    for _ in range(2):
+        for a, b in zip(_list(call()), want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [304, 301])   # by TMA, and without it
+def test_recurrence(lib, kind, D):
+    """Chunks that wait for earlier ones: some of the thousands are never there at once."""
+    T = 30000
+    g, x = torch.randn(T, D, device="cuda").to(kind).T, torch.randn(T, D, device="cuda").to(kind).T
+    off = torch.tensor([0, 11000, 11000, T], dtype=torch.int32, device="cuda")
+    _check(lib, lambda: lib.gated_scan(g, x, "convex", off, save=True))
+    saved = lib.gated_scan(g, x, "convex", off, save=True)[2]
+    _check(lib, lambda: lib.gated_scan_backward(g, x, x, "convex", off, saved=saved))
