@@ -51,3 +51,13 @@ def test_recurrence(lib, kind, D):
     _check(lib, lambda: lib.gated_scan(g, x, "convex", off, save=True))
     saved = lib.gated_scan(g, x, "convex", off, save=True)[2]
     _check(lib, lambda: lib.gated_scan_backward(g, x, x, "convex", off, saved=saved))
+
+
+@pytest.mark.parametrize("D", [512, 768, 4096, 10240])
+def test_norm(lib, D):
+    """Copies into shared memory: whether they are there at once is chance."""
+    T = 3000
+    x, d, g = torch.randn(T, D, device="cuda").half().T, torch.randn(T, D, device="cuda").half().T, torch.rand(D, device="cuda")
+    _check(lib, lambda: lib.rmsnorm(x, g, d), surely=False)
+    _check(lib, lambda: lib.rmsnorm_e4m3(x, g), surely=False)
+    _check(lib, lambda: lib.rmsnorm_backward(x, g, d, x), surely=False)
