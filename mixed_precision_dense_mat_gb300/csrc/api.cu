@@ -8,7 +8,7 @@
 #include <vector>
 #include <mutex>
 
-#include "common.cuh"
+#include "ops.cuh"
 
 namespace cr {
 
@@ -190,6 +190,16 @@ cr_status make_tensor_map_2d(CUtensorMap* tm, int type, const void* base, int in
 cr_status make_tensor_map_2d_plain(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
                                    int box_outer) {
   return tensor_map_2d(tm, type, base, inner, outer, ld, box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+cr_status allow_shared(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  CR_CUDA(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64) return fail_literal(CR_ERR_CUDA, "device number above 63");
+  if (done.load(std::memory_order_acquire) >> dev & 1) return CR_OK;
+  CR_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  done.fetch_or((uint64_t)1 << dev, std::memory_order_release);
+  return CR_OK;
 }
 
 // The word that a bounded wait of an operator kernel sets (mapped host memory, one per process).

@@ -496,6 +496,7 @@ int sm_count() {
 }
 // Whether two stages of a column's inputs fit; longer ones are read directly.
 bool ring_fits(int nin, int D, int eb) { return 2ll * nin * D * eb <= 200 * 1024; }
+constexpr int MAXSHARED = 224 * 1024;   // of the rings, next to at most 2 KB of static shared memory
 // Blocks for n columns, `per` at a time each, stages of their rings and shared memory: about 50 KB,
 // so that several blocks share an SM; no more stages than a block has columns.
 struct Plan {
@@ -510,7 +511,6 @@ cr_status make_plan(Plan& plan, K kernel, int threads, int n, int per, bool ring
     plan.stages = (int)std::min<size_t>(8, std::max<size_t>(2, (size_t)50 * 1024 / stage));
     if (items <= sm_count()) plan.stages = 2;
     plan.smem = ((size_t)per * plan.stages * 8 + 127) / 128 * 128 + plan.stages * stage;
-    if (plan.smem > 48 * 1024) CR_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan.smem));
   }
   plan.blocks = items;
   if (items <= sm_count()) return CR_OK;   // one each
@@ -536,6 +536,8 @@ cr_status launch_fwd(const Fwd& p, cudaStream_t stream) {
   const int TH = threads_for(G, VPT, p.D);
   Wait wait = {option_wait_ns(), nullptr};
   CR_TRY(wait_word(&wait.err));
+  static std::atomic<uint64_t> done{0};
+  CR_TRY(allow_shared((const void*)k_rmsnorm<T, O, G, VPT, VEC>, MAXSHARED, done));
   Plan plan;
   CR_TRY(make_plan(plan, k_rmsnorm<T, O, G, VPT, VEC>, TH, p.n, PER, uses_ring<G, VPT, VEC>(), 2, p.D, sizeof(T)));
   TimedScope ts("k_rmsnorm", stream);
@@ -561,6 +563,8 @@ cr_status launch_bwd(const Bwd& p, cudaStream_t stream) {
   const int TH = threads_for(G, VPT, p.D);
   Wait wait = {option_wait_ns(), nullptr};
   CR_TRY(wait_word(&wait.err));
+  static std::atomic<uint64_t> done{0};
+  CR_TRY(allow_shared((const void*)k_rmsnorm_bwd<T, G, VPT, VEC>, MAXSHARED, done));
   Plan plan;
   CR_TRY(make_plan(plan, k_rmsnorm_bwd<T, G, VPT, VEC>, TH, p.n, PER, uses_ring<G, VPT, VEC>(), 3, p.D, sizeof(T)));
   const int blocks = plan.blocks;

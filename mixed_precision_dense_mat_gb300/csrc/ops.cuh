@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
 #include <new>
 
 #include "common.cuh"
@@ -23,6 +24,10 @@ cr_status make_tensor_map_2d(CUtensorMap* tm, int type, const void* base, int in
 // The same without a swizzle, for tiles that threads read.
 cr_status make_tensor_map_2d_plain(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
                                    int box_outer);
+
+// Lets a kernel have `bytes` of dynamic shared memory, the same number at every call: once per kernel (which `done`
+// belongs to) and device, so that host threads do not take it from one another.
+cr_status allow_shared(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
 // total[D] = the sum of the rows of part (rows x D, row-major), in a fixed order.
 cr_status add_rows(const float* part, int rows, int D, float* total, cudaStream_t stream);
