@@ -1,6 +1,7 @@
 // Affine product with bias, activation and residual in its epilogue, and its gradient
 // (cr_affine, cr_affine_backward).
 #include <algorithm>
+#include <mutex>
 #include <type_traits>
 
 #include "ops.cuh"
@@ -798,16 +799,6 @@ __global__ void __launch_bounds__(NT) k_affine_g(const E* dY, int lddy, const E*
   }
 }
 
-int sm_count() {
-  static const int n = [] {
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-  }();
-  return n;
-}
-
 template <class E, int V>
 cr_status gradient_at_z(const E* dY, int lddy, const E* Z, int ldz, int N, int M, int act, E* G, int ldg, float* db, cudaStream_t stream) {
   const int bx = (N + 32 * V - 1) / (32 * V), by = std::max(1, std::min({(M + 7) / 8, 4 * sm_count() / bx, 65535}));
@@ -856,16 +847,16 @@ cr_status map_of(CUtensorMap* tm, const Operand& o, int type, int K, int rows_pe
 template <bool F8, class O>
 cr_status launch(const CUtensorMap& tmP, const CUtensorMap& tmQ, const CUtensorMap& tmC, const CUtensorMap& tmZ, const CUtensorMap& tmR, const Params& p, bool wide, int split, int stages, cudaStream_t stream) {
   if (wide) {
-    static const cudaError_t set = cudaFuncSetAttribute(k_affine_wide<F8, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, WSMEM);
-    CR_CUDA(set);
+    static std::atomic<uint64_t> done{0};
+    CR_TRY(allow_shared((const void*)k_affine_wide<F8, O>, WSMEM, done));
     const int pairs = std::min((long long)sm_count() / 2, (long long)p.ti * p.tj);
     TimedScope ts("k_affine_wide", stream);
     CR_CUDA(launch_after(k_affine_wide<F8, O>, 2 * pairs, WTHREADS, WSMEM, 2, stream, tmP, tmQ, tmC, tmZ, tmR, p));
     CR_CHECK_LAUNCH("k_affine_wide");
     return CR_OK;
   }
-  static const cudaError_t set = cudaFuncSetAttribute(k_affine_thin<F8, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-  CR_CUDA(set);
+  static std::atomic<uint64_t> done{0};
+  CR_TRY(allow_shared((const void*)k_affine_thin<F8, O>, 227 * 1024, done));
   const int stage = WTILE + (p.qk ? p.bn * KBYTES : (p.bn + 63) / 64 * ATOM);
   const size_t smem = (size_t)stages * stage + 1024 + 256 + (split > 1 ? 512 * p.bn : 0);
   TimedScope ts("k_affine_thin", stream);
@@ -879,8 +870,9 @@ cr_status launch(const CUtensorMap& tmP, const CUtensorMap& tmQ, const CUtensorM
 // on a GB300's 152 SMs), because a cluster's CTAs share a GPC.
 int resident_clusters(int s, int c) {
   struct Table {
+    std::once_flag once;
     int n[4] = {};
-    Table() {
+    void fill() {
       const auto kernel = k_affine_thin<false, __half>;
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
       for (int e = 0; e < 4; ++e) {
@@ -901,7 +893,11 @@ int resident_clusters(int s, int c) {
       }
     }
   };
-  static const Table table;
+  static Table tables[64];   // by device
+  int dev = 0;
+  cudaGetDevice(&dev);
+  Table& table = tables[dev & 63];
+  std::call_once(table.once, [&] { table.fill(); });
   return c * table.n[s == 1 ? 0 : s == 2 ? 1 : s == 4 ? 2 : 3];
 }
 
@@ -914,10 +910,11 @@ struct Choice {
 };
 Choice choose(int I, int J, int kblocks, bool qk) {
   Choice best = {false, 0, 1, 0, 1e30};
+  const int sms = sm_count();
   const auto tiles = [](int n, int t) { return (n + t - 1) / t; };
   // Wide: rounds of tiles over the CTA pairs, 0.27 to 0.3 us per k-block, or the epilogue of a tile.
   if (J > 128) {
-    const long long t = (long long)tiles(I, 256) * tiles(J, 256), rounds = (t + sm_count() / 2 - 1) / (sm_count() / 2);
+    const long long t = (long long)tiles(I, 256) * tiles(J, 256), rounds = (t + sms / 2 - 1) / (sms / 2);
     best = {true, 0, 1, 0, 6.5 + rounds * std::max(kblocks * 0.29 + 0.6, 3.3)};
   }
   // Thin: parts of k for which all clusters are resident at once, with three stages or more and two
@@ -941,9 +938,9 @@ Choice choose(int I, int J, int kblocks, bool qk) {
       const int received = split > 1 ? 512 * bn : 0;
       const int stages = std::min(TMAXSTAGES, (227 * 1024 / per - 3584 - received) / stage);
       if (stages < (split > 1 ? 3 : 2) || (split > 1 && stages * stage < received)) continue;
-      const double ctas = (double)t * split, waves = std::max(1.0, ctas / sm_count());
-      const double hbm = (double)I * kblocks * KBYTES / 5.5e6 * (1.0 + 0.25 * std::max(0.0, 1.0 - ctas / (2.5 * sm_count())));
-      const double later = std::max(0.0, ctas / sm_count() - per) * 0.025 * bn;   // epilogues of tiles after the resident ones
+      const double ctas = (double)t * split, waves = std::max(1.0, ctas / sms);
+      const double hbm = (double)I * kblocks * KBYTES / 5.5e6 * (1.0 + 0.25 * std::max(0.0, 1.0 - ctas / (2.5 * sms)));
+      const double later = std::max(0.0, ctas / sms - per) * 0.025 * bn;   // epilogues of tiles after the resident ones
       const double us = 5.0 + later + (split > 1 ? 0.3 + 0.04 * bn : 0.0) + std::max(waves * tiles(kblocks, split) * stage / 100e3, hbm);
       if (us < best.us) best = {false, bn, split, stages, us};
     }

@@ -192,6 +192,18 @@ cr_status make_tensor_map_2d_plain(CUtensorMap* tm, int type, const void* base, 
   return tensor_map_2d(tm, type, base, inner, outer, ld, box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64) n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 cr_status allow_shared(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
   int dev = 0;
   CR_CUDA(cudaGetDevice(&dev));

@@ -485,15 +485,6 @@ cr_status with_split(int D, bool vec, F&& f) {
 }
 constexpr int threads_for(int G, int VPT, int D) { return G ? NT : (D + 256 * VPT - 1) / (256 * VPT) * 32; }
 
-int sm_count() {
-  static const int n = [] {
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-  }();
-  return n;
-}
 // Whether two stages of a column's inputs fit; longer ones are read directly.
 bool ring_fits(int nin, int D, int eb) { return 2ll * nin * D * eb <= 200 * 1024; }
 constexpr int MAXSHARED = 224 * 1024;   // of the rings, next to at most 2 KB of static shared memory

@@ -25,6 +25,9 @@ cr_status make_tensor_map_2d(CUtensorMap* tm, int type, const void* base, int in
 cr_status make_tensor_map_2d_plain(CUtensorMap* tm, int type, const void* base, int inner, int outer, int ld, int box_inner,
                                    int box_outer);
 
+// Number of SMs of the current device.
+int sm_count();
+
 // Lets a kernel have `bytes` of dynamic shared memory, the same number at every call: once per kernel (which `done`
 // belongs to) and device, so that host threads do not take it from one another.
 cr_status allow_shared(const void* kernel, int bytes, std::atomic<uint64_t>& done);

@@ -825,16 +825,6 @@ cr_status map_in(CUtensorMap* tm, const Input& in, int D, int n, int steps) {
   return make_tensor_map_2d_plain(tm, type_of<T>(), in.p, D, n, in.ld, ROW / (int)sizeof(T), steps);
 }
 
-int sm_count() {
-  static const int n = [] {
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-  }();
-  return n;
-}
-
 cr_status states_only(const float* from, int ldf, float* to, int ldt, int D, int n, cudaStream_t stream) {
   if (!to || n == 0) return CR_OK;
   k_scan_states<<<std::min(n, 16 * sm_count()), 256, 0, stream>>>(from, ldf, to, ldt, D, n);
@@ -849,8 +839,8 @@ cr_status forward(FwdArgs<E> p, cudaStream_t stream) {
   Scratch sc;
   CR_TRY(sc.make(p.n, CH, tiles, W, stream));
   CR_REQUIRE((long long)sc.lb.chunks * tiles < INT_MAX / 2, "cr_gated_scan: more than 2^30 work items");
-  static const cudaError_t set = cudaFuncSetAttribute(k_scan_fwd<E, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-  CR_CUDA(set);
+  static std::atomic<uint64_t> done{0};
+  CR_TRY(allow_shared((const void*)k_scan_fwd<E, GATE>, SMEM, done));
   p.tma = tma_ok<E>(p.G) && tma_ok<E>(p.X);
   p.pairs = vec_ok<E>(p.H, p.ldh, p.D);
   CUtensorMap tmG = {}, tmX = {};
@@ -871,8 +861,8 @@ cr_status backward(BwdArgs<E> p, cudaStream_t stream) {
   Scratch sc;
   CR_TRY(sc.make(p.n, CH, tiles, W, stream));
   CR_REQUIRE((long long)sc.lb.chunks * tiles < INT_MAX / 2, "cr_gated_scan_backward: more than 2^30 work items");
-  static const cudaError_t set = cudaFuncSetAttribute(k_scan_bwd<E, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-  CR_CUDA(set);
+  static std::atomic<uint64_t> done{0};
+  CR_TRY(allow_shared((const void*)k_scan_bwd<E, GATE>, SMEM, done));
   p.tma = tma_ok<E>(p.G) && tma_ok<E>(p.X) && tma_ok<E>(p.dH);
   p.pairs = vec_ok<E>(p.dG, p.lddg, p.D) && vec_ok<E>(p.dX, p.lddx, p.D);
   CUtensorMap tmG = {}, tmX = {}, tmD = {};
