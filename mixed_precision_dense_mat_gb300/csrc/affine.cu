@@ -570,12 +570,10 @@ __global__ void __launch_bounds__(TTHREADS)
       ++issued;
       if (++st == stages) st = 0, ph ^= 1u;
     }
-    if (!ok) {   // gave up: copies in flight land before the CTA leaves
-      if (lane == 0) gave_up(p, abort_flag);
-      for (int q = min(issued, stages); q > 0; --q) {
-        const int n = issued - q;
-        mbar_wait(&bars->full[n % stages], (uint32_t)(n / stages) & 1u, p.limit);
-      }
+    if (!ok && lane == 0) gave_up(p, abort_flag);
+    for (int q = min(issued, stages); q > 0; --q) {   // copies land before the CTA leaves, whoever gave up
+      const int n = issued - q;
+      mbar_wait(&bars->full[n % stages], (uint32_t)(n / stages) & 1u, LANDING_NS);
     }
     __syncwarp();
     if (split > 1) cluster_wait();
@@ -610,7 +608,10 @@ __global__ void __launch_bounds__(TTHREADS)
     bool ok = true;
     if (kb1 > kb0) {
       ok = mbar_wait(&bars->done, 0, p.limit);
-      if (!ok) gave_up(p, abort_flag);
+      if (!ok) {
+        gave_up(p, abort_flag);
+        mbar_wait(&bars->done, 0, LANDING_NS);   // MMAs in flight read the stages and write tensor memory
+      }
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     }
@@ -648,7 +649,10 @@ __global__ void __launch_bounds__(TTHREADS)
   }
   if (split > 1) {
     const bool got = mbar_wait(&bars->got, 0, p.limit);
-    if (!got) gave_up(p, abort_flag);
+    if (!got) {
+      gave_up(p, abort_flag);
+      mbar_wait(&bars->got, 0, LANDING_NS);   // every CTA of the cluster sends, whatever became of its sums
+    }
     const int total = ncols * own;
     for (int e = 4 * (int)threadIdx.x; got && e < total; e += 4 * TTHREADS) {
       float4 z = *reinterpret_cast<const float4*>(received + e);

@@ -61,3 +61,11 @@ def test_norm(lib, D):
     _check(lib, lambda: lib.rmsnorm(x, g, d), surely=False)
     _check(lib, lambda: lib.rmsnorm_e4m3(x, g), surely=False)
     _check(lib, lambda: lib.rmsnorm_backward(x, g, d, x), surely=False)
+
+
+@pytest.mark.parametrize("K,N,M", [(4096, 2048, 16), (1024, 512, 60), (200, 300, 100), (515, 300, 7)])
+def test_affine_few_columns(lib, K, N, M):
+    """Copies, products and, between the CTAs of a cluster, partial sums: whether they are there at once is chance."""
+    w, x = torch.randn(N, K, device="cuda").half().T, torch.randn(M, K, device="cuda").half().T
+    b, r = torch.randn(N, device="cuda"), torch.randn(M, N, device="cuda").half().T
+    _check(lib, lambda: lib.affine(w, x, b, "silu", r, save=True), surely=False)
