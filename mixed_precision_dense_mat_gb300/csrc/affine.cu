@@ -279,9 +279,10 @@ constexpr int WSTAGE = 2 * WTILE;
 constexpr int WTHREADS = 320;
 constexpr int WEPI = 8;                          // epilogue warps
 struct WideBars {
-  uint64_t full[WSTAGES], empty[WSTAGES], tfull[2], tempty[2], rows[WEPI][2];
+  uint64_t full[WSTAGES], empty[WSTAGES], tfull[2], tempty[2], rows[WEPI][2], settled;
   uint32_t tmem;
   int abort;
+  int issued[2];   // in the first CTA: stages that the two CTAs' loaders have filled in all
 };
 constexpr int WSMEM = WSTAGES * WSTAGE + WEPI * WBUF + 1024 + 384;
 static_assert(WSTAGE == WEPI * WBUF, "a stage's memory is a second set of output buffers");
@@ -326,6 +327,7 @@ __global__ void __launch_bounds__(WTHREADS, 1)
       mbar_init(&bars->tempty[b], 2 * WEPI);   // one arrival per epilogue warp of the pair
       for (int x = 0; x < WEPI; ++x) mbar_init(&bars->rows[x][b], 1);
     }
+    mbar_init(&bars->settled, 1);
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -339,6 +341,10 @@ __global__ void __launch_bounds__(WTHREADS, 1)
   // wait: the inputs are there.  It is waited for at the end, so that later kernels need not.
   if (!p.second) wait_for_previous();
   let_next_start();
+  const auto give_up = [&] {   // both CTAs leave their loops at the flag
+    gave_up(p, abort_flag);
+    store_cluster(cluster_addr(smem_u32(&bars->abort), rank ^ 1u), 1);
+  };
 
   if (warp == 0) {
     if (elect_one()) {
@@ -379,12 +385,13 @@ __global__ void __launch_bounds__(WTHREADS, 1)
         if (++st == (uint32_t)p.stages) st = 0, ph ^= 1u;
       }
     }
-    if (!ok) {   // gave up: the pair's copies in flight land before either CTA leaves
-      if (lane == 0) gave_up(p, abort_flag);
-      for (int q = min(issued, p.stages); rank == 0 && q > 0; --q) {
-        const int n = issued - q;
-        mbar_wait(&bars->full[n % p.stages], (uint32_t)(n / p.stages) & 1u, p.limit);
-      }
+    for (int q = min(issued, p.stages); ok && q > 0; --q) {   // the stages' last arrivals come before the CTA leaves
+      const int n = issued - q;
+      ok = mbar_wait_warp(&bars->empty[n % p.stages], (uint32_t)(n / p.stages) & 1u, p.limit);
+    }
+    if (lane == 0) {
+      if (!ok) give_up();
+      store_cluster(cluster_addr(smem_u32(&bars->issued[rank]), 0), (uint32_t)issued);
     }
   } else if (warp == 1) {
     if (rank == 0) {
@@ -413,7 +420,10 @@ __global__ void __launch_bounds__(WTHREADS, 1)
           if (++st == (uint32_t)p.stages) st = 0, ph ^= 1u;
         }
       }
-      if (!ok && lane == 0) gave_up(p, abort_flag);
+      if (!ok && lane == 0) give_up();
+      __syncwarp();
+      if (elect_one()) mma_commit_own(&bars->settled);   // whoever gave up: MMAs in flight end before tensor memory is freed
+      mbar_wait_warp(&bars->settled, 0, LANDING_NS);
     }
   } else {
     const int quad = warp & 3, half = (warp - 2) >> 2;
@@ -422,11 +432,18 @@ __global__ void __launch_bounds__(WTHREADS, 1)
     uint32_t nrows = 0;   // parity of the two buffers' next R
     for (int u = 0, t; (t = wide_turn(p, cl, ncl, u)) < ntiles; ++u) {
       const int b = u & 1;
-      if (*abort_flag) break;
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
       int ti, tj;
       wide_tile(p, t, ti, tj);
       const int j0 = tj * 256 + (int)rank * 128 + quad * 32, ibase = ti * 256 + half * 128;
       constexpr int N = OROW / (int)sizeof(O);
+      // R of the chunk at buffer x or after it that has been asked for lands, so that the warp can leave
+      const auto r_landed = [&](int x) {
+        bool ok = true;
+        for (; p.tma_r && j0 < p.J && x < 2; ++x)
+          if (ibase + x * N < p.I) ok = mbar_wait_warp(&bars->rows[warp - 2][x], (nrows >> x) & 1u, LANDING_NS) && ok;
+        return ok;
+      };
       if (p.tma_r && j0 < p.J) {   // both chunks' R, before the wait for the products
         if (lane == 0) {
           tma_store_wait_read();
@@ -437,8 +454,9 @@ __global__ void __launch_bounds__(WTHREADS, 1)
             }
         }
       }
-      if (!mbar_wait(&bars->tfull[b], (uint32_t)(u >> 1) & 1u, p.limit)) {
-        gave_up(p, abort_flag);
+      if (!mbar_wait_warp(&bars->tfull[b], (uint32_t)(u >> 1) & 1u, p.limit)) {
+        if (lane == 0) give_up();
+        r_landed(0);
         break;
       }
       tc_fence_after();
@@ -464,7 +482,10 @@ __global__ void __launch_bounds__(WTHREADS, 1)
         if (p.tma_r && j0 < p.J) {
           const int x = c / N;
           rows = out = buf + x * WSTAGE;
-          if (!mbar_wait(&bars->rows[warp - 2][x], (nrows >> x) & 1u, p.limit)) gave_up(p, abort_flag);
+          if (!mbar_wait_warp(&bars->rows[warp - 2][x], (nrows >> x) & 1u, p.limit)) {
+            if (lane == 0) give_up();   // it goes on with what lands, and leaves at the next tile
+            if (!r_landed(x)) break;
+          }
           nrows ^= 1u << x;
         }
         wide_finish<O, N>(p, &tmC, &tmZ, ibase + c, j0, js, is, bias, out, rows, reinterpret_cast<float*>(v));
@@ -477,6 +498,22 @@ __global__ void __launch_bounds__(WTHREADS, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();   // neither CTA leaves while the other's MMAs, copies or arrivals may reach it
+  if (*abort_flag) {    // the same in both: operands in flight land too
+    if (rank == 0 && warp == 0) {
+      const int n0 = *(volatile int*)&bars->issued[0], n1 = *(volatile int*)&bars->issued[1], last = max(n0, n1);
+      for (int n = max(last - p.stages, 0); n < last; ++n) {
+        uint64_t* full = &bars->full[n % p.stages];
+        if (lane == 0) {   // a stage that only one of the two has filled: the barrier waits for its half
+          if (n >= n0) mbar_arrive_expect_tx(full, WSTAGE);
+          else if (n >= n1) mbar_complete_tx(full, WSTAGE);
+        }
+        __syncwarp();
+        mbar_wait_warp(full, (uint32_t)(n / p.stages) & 1u, LANDING_NS);
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);

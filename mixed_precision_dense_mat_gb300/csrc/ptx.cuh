@@ -207,6 +207,13 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) 
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
+__device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t v) {   // to an address of cluster_addr
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Takes `bytes` off what a barrier of this CTA waits for.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
 // Copies `bytes` (a multiple of 16) of this CTA's shared memory to another CTA's, counted on a
 // barrier of that CTA.
 __device__ __forceinline__ void copy_to_cluster(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -249,6 +256,10 @@ __device__ __forceinline__ void mma_any(uint32_t tmem_d, uint64_t adesc, uint64_
   else if (F8) CR_MMA("1", "f8f6f4");
   else CR_MMA("1", "f16");
 #undef CR_MMA
+}
+// Arrives on a barrier of this CTA when the pair's MMAs issued by it are done.
+__device__ __forceinline__ void mma_commit_own(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 // Arrives on the barrier at the same address in both CTAs of the pair when its MMAs are done.
 __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {

@@ -69,3 +69,14 @@ def test_affine_few_columns(lib, K, N, M):
     w, x = torch.randn(N, K, device="cuda").half().T, torch.randn(M, K, device="cuda").half().T
     b, r = torch.randn(N, device="cuda"), torch.randn(M, N, device="cuda").half().T
     _check(lib, lambda: lib.affine(w, x, b, "silu", r, save=True), surely=False)
+
+
+@pytest.mark.parametrize("K,N,M", [(1024, 2048, 1500), (64, 4096, 3000), (3000, 520, 700)])
+def test_affine_many_columns(lib, K, N, M):
+    """Pairs of CTAs: operands, products, residuals and outputs in flight when a warp gives up."""
+    w, x = torch.randn(N, K, device="cuda").half().T, torch.randn(M, K, device="cuda").half().T
+    b, r = torch.randn(N, device="cuda"), torch.randn(M, N, device="cuda").half().T
+    _check(lib, lambda: lib.affine(w, x, b, "silu", r), surely=False)
+    _check(lib, lambda: lib.affine(w, x, b, "silu", r, save=True), surely=False)
+    _check(lib, lambda: lib.affine(w, x, out_dtype=torch.float32), surely=False)
+    _check(lib, lambda: lib.affine_backward(w, x, r, r, "gelu"), surely=False)
