@@ -438,8 +438,10 @@ cr_status cr_calibrate_noalloc(const double* d_S, int lds, int n_p, int M, const
  *    captured into CUDA graphs once the process has made a first call outside a capture.
  *  - Zero columns (M, T, B or n_seq = 0) are allowed: sums over them are zero.
  *  - A device-side wait that runs out (CR_OPT_WAIT_LIMIT_US; never in normal operation)
- *    invalidates the outputs of its call and makes the next call of this section on any
- *    stream return CR_ERR_TIMEOUT once. */
+ *    invalidates the outputs of its call and makes the next call of this section that has any
+ *    columns, on any stream and from any host thread, return CR_ERR_TIMEOUT once, without
+ *    doing its work.  Copies and products in flight are given 2 s more to end.  After its last call
+ *    a program learns of it by one more, once the stream is synchronised. */
 enum { CR_TYPE_F32 = 0, CR_TYPE_F16 = 1, CR_TYPE_BF16 = 2, CR_TYPE_E4M3 = 3 };
 
 /* Activations: z, max(z, 0), z sigmoid(z), z Phi(z) (Phi the normal distribution function). */

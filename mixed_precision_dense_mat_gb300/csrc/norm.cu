@@ -520,20 +520,19 @@ struct Fwd {
   void *H, *Y;
   int ldh, ldy;
   float* scale;
+  Wait wait;
 };
 template <class T, class O, int G, int VPT, bool VEC>
 cr_status launch_fwd(const Fwd& p, cudaStream_t stream) {
   constexpr int PER = G ? NT / G : 1;
   const int TH = threads_for(G, VPT, p.D);
-  Wait wait = {option_wait_ns(), nullptr};
-  CR_TRY(wait_word(&wait.err));
   static std::atomic<uint64_t> done{0};
   CR_TRY(allow_shared((const void*)k_rmsnorm<T, O, G, VPT, VEC>, MAXSHARED, done));
   Plan plan;
   CR_TRY(make_plan(plan, k_rmsnorm<T, O, G, VPT, VEC>, TH, p.n, PER, uses_ring<G, VPT, VEC>(), 2, p.D, sizeof(T)));
   TimedScope ts("k_rmsnorm", stream);
   CR_CUDA(launch_after(k_rmsnorm<T, O, G, VPT, VEC>, plan.blocks, TH, plan.smem, 1, stream, (const T*)p.X, p.ldx, (const T*)p.R, p.ldr,
-                       p.gamma, p.D, p.n, p.eps, (T*)p.H, p.ldh, (O*)p.Y, p.ldy, p.scale, plan.stages, wait));
+                       p.gamma, p.D, p.n, p.eps, (T*)p.H, p.ldh, (O*)p.Y, p.ldy, p.scale, plan.stages, p.wait));
   CR_CHECK_LAUNCH("k_rmsnorm");
   return CR_OK;
 }
@@ -547,13 +546,12 @@ struct Bwd {
   void* dX;
   int lddx;
   float* dgamma;
+  Wait wait;
 };
 template <class T, int G, int VPT, bool VEC>
 cr_status launch_bwd(const Bwd& p, cudaStream_t stream) {
   constexpr int PER = G ? NT / G : 1;
   const int TH = threads_for(G, VPT, p.D);
-  Wait wait = {option_wait_ns(), nullptr};
-  CR_TRY(wait_word(&wait.err));
   static std::atomic<uint64_t> done{0};
   CR_TRY(allow_shared((const void*)k_rmsnorm_bwd<T, G, VPT, VEC>, MAXSHARED, done));
   Plan plan;
@@ -565,7 +563,7 @@ cr_status launch_bwd(const Bwd& p, cudaStream_t stream) {
   {
     TimedScope ts("k_rmsnorm_bwd", stream);
     e = launch_after(k_rmsnorm_bwd<T, G, VPT, VEC>, blocks, TH, plan.smem, 1, stream, (const T*)p.H, p.ldh, p.gamma, (const T*)p.dY, p.lddy,
-                     (const T*)p.dH, p.lddh, p.D, p.n, p.eps, (T*)p.dX, p.lddx, part, plan.stages, wait);
+                     (const T*)p.dH, p.lddh, p.D, p.n, p.eps, (T*)p.dX, p.lddx, part, plan.stages, p.wait);
     count_launch();
   }
   const cr_status st = e != cudaSuccess ? cuda_fail(e, "k_rmsnorm_bwd") : p.dgamma ? add_rows(part, blocks, p.D, p.dgamma, stream) : CR_OK;
@@ -601,6 +599,8 @@ extern "C" cr_status cr_rmsnorm(int type, const void* d_X, int ldx, const void* 
   CR_REQUIRE((out_type == CR_TYPE_E4M3) == (d_scale != nullptr) || T == 0, "cr_rmsnorm: d_scale belongs to the e4m3 output");
   if (T == 0) return CR_OK;
   CR_REQUIRE(d_X && d_gamma && d_Y, "cr_rmsnorm: NULL argument");
+  Wait wait = {option_wait_ns(), nullptr};
+  CR_TRY(wait_word(&wait.err));
   return with_type(type, [&](auto t0) -> cr_status {
     using E = decltype(t0);
     const int eb = sizeof(E);
@@ -616,7 +616,7 @@ extern "C" cr_status cr_rmsnorm(int type, const void* d_X, int ldx, const void* 
                        (sizeof(O) == 1 ? ((uintptr_t)d_Y & 7) == 0 && ldy % 8 == 0 : ok16(d_Y, ldy, sizeof(O)));
       return with_split(D, vec, [&](auto g, auto v, auto w) -> cr_status {
         return launch_fwd<E, O, decltype(g)::value, decltype(v)::value, decltype(w)::value>(
-            Fwd{d_X, d_R, ldx, ldr, d_gamma, D, T, (float)eps, d_H, d_Y, ldh, ldy, d_scale}, stream);
+            Fwd{d_X, d_R, ldx, ldr, d_gamma, D, T, (float)eps, d_H, d_Y, ldh, ldy, d_scale, wait}, stream);
       });
     };
     return out_type == CR_TYPE_E4M3 ? run(__nv_fp8_e4m3{}) : run(t0);
@@ -639,6 +639,8 @@ extern "C" cr_status cr_rmsnorm_backward(int type, const void* d_H, int ldh, con
   }
   CR_REQUIRE(d_H && d_gamma && d_dY, "cr_rmsnorm_backward: NULL argument");
   if (!d_dX && !d_dgamma) return CR_OK;
+  Wait wait = {option_wait_ns(), nullptr};
+  CR_TRY(wait_word(&wait.err));
   float* mem = nullptr;
   const cr_status st = with_type(type, [&](auto t0) -> cr_status {
     using E = decltype(t0);
@@ -664,7 +666,7 @@ extern "C" cr_status cr_rmsnorm_backward(int type, const void* d_H, int ldh, con
     const bool vec = D % 8 == 0 && ring_fits(3, D, eb) && ok16(d_H, ldh, eb) && ok16(d_dY, lddy, eb) && ok16(d_dH, lddh, eb) && ok16(d_dX, lddx, eb);
     return with_split(D, vec, [&](auto g, auto v, auto w) -> cr_status {
       return launch_bwd<E, decltype(g)::value, decltype(v)::value, decltype(w)::value>(
-          Bwd{d_H, d_dY, d_dH, ldh, lddy, lddh, d_gamma, D, T, (float)eps, d_dX, lddx, d_dgamma}, stream);
+          Bwd{d_H, d_dY, d_dH, ldh, lddy, lddh, d_gamma, D, T, (float)eps, d_dX, lddx, d_dgamma, wait}, stream);
     });
   });
   scratch_free(mem, stream);

@@ -962,6 +962,8 @@ extern "C" cr_status cr_gated_step(int type, int gate, const void* d_G, int ldg,
   if (B == 0) return CR_OK;
   CR_REQUIRE(d_G && d_X && d_h && d_hnext, "cr_gated_step: NULL argument");
   CR_REQUIRE(ldg >= D && ldx >= D && ldh >= D && ldn >= D && (!d_H || ldo >= D), "cr_gated_step: leading dimension below D");
+  int* word = nullptr;   // waits for nothing itself, but reports an earlier call
+  CR_TRY(wait_word(&word));
   return with_type(type, [&](auto t0) -> cr_status {
     using E = decltype(t0);
     return with_gate(gate, [&](auto g0) -> cr_status {

@@ -80,3 +80,26 @@ def test_affine_many_columns(lib, K, N, M):
     _check(lib, lambda: lib.affine(w, x, b, "silu", r, save=True), surely=False)
     _check(lib, lambda: lib.affine(w, x, out_dtype=torch.float32), surely=False)
     _check(lib, lambda: lib.affine_backward(w, x, r, r, "gelu"), surely=False)
+
+
+@pytest.mark.parametrize("reports", ["step", "long norm", "long norm backward"])
+def test_calls_without_waits_report_too(lib, reports):
+    g, x = torch.randn(30000, 304, device="cuda").T, torch.randn(30000, 304, device="cuda").T
+    y, c = torch.randn(2, 17000, device="cuda").T, torch.ones(17000, device="cuda")
+    call = {"step": lambda: lib.gated_step(x[:, :3], x[:, :3], g[:, :3]), "long norm": lambda: lib.rmsnorm(y, c),
+            "long norm backward": lambda: lib.rmsnorm_backward(y, c, y)}[reports]
+    lib.gated_scan(g, x)
+    call()
+    for _ in range(50):
+        with option(lib, lib.CR_OPT_WAIT_LIMIT_US, 0):
+            lib.gated_scan(g, x)
+        torch.cuda.synchronize()
+        try:
+            call()
+        except lib.CrError as e:
+            assert e.name == "CR_ERR_TIMEOUT"
+            break
+    else:
+        raise AssertionError("no call reported the recurrence's wait")
+    call()
+    lib.gated_scan(g, x)
