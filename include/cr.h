@@ -431,6 +431,7 @@ cr_status cr_calibrate_noalloc(const double* d_S, int lds, int n_p, int M, const
  *    contiguous.  Leading dimensions count elements of the matrix's own type and are >= the
  *    number of rows (any value is right; multiples of 16 bytes at 16-byte aligned addresses
  *    are fastest).  Inputs are only read, and outputs overlap no input unless a call says so.
+ *  - Sizes (K, N, M, D, T, B, n_seq) end at 2^31 - 2^16.
  *  - Elements are FP32, FP16, BF16 or e4m3 (FP8, largest value 448) as a CR_TYPE_* argument
  *    says; arithmetic, sums and states are FP32, and each output is rounded once, to nearest.
  *  - Scratch comes from the pools of cr_workspace_trim.  Calls are asynchronous, and results do

@@ -1084,6 +1084,7 @@ extern "C" cr_status cr_affine(int type, const void* d_W, int ldw, const void* d
   CR_REQUIRE(act >= CR_ACT_NONE && act <= CR_ACT_GELU, "cr_affine: unknown activation");
   CR_REQUIRE(type == CR_TYPE_E4M3 || (!d_wscale && !d_xscale), "cr_affine: scales belong to e4m3");
   CR_REQUIRE(K >= 1 && N >= 1 && M >= 0, "cr_affine: K >= 1, N >= 1, M >= 0");
+  CR_REQUIRE_SIZES("cr_affine", K, N, M);
   CR_REQUIRE(ldw >= K && ldx >= K && ldy >= N && (!d_R || ldr >= N) && (!d_Z || ldz >= N), "cr_affine: leading dimension too small");
   if (M == 0) return CR_OK;
   CR_REQUIRE(d_W && d_X && d_Y, "cr_affine: NULL argument");
@@ -1100,6 +1101,7 @@ extern "C" cr_status cr_affine_backward(int type, const void* d_W, int ldw, cons
   CR_REQUIRE(act >= CR_ACT_NONE && act <= CR_ACT_GELU, "cr_affine_backward: unknown activation");
   CR_REQUIRE(!d_dW || dw_type == type || dw_type == CR_TYPE_F32, "cr_affine_backward: dw_type must be type or FP32");
   CR_REQUIRE(K >= 1 && N >= 1 && M >= 0, "cr_affine_backward: K >= 1, N >= 1, M >= 0");
+  CR_REQUIRE_SIZES("cr_affine_backward", K, N, M);
   CR_REQUIRE((!d_dX || (ldw >= K && lddx >= K)) && (!d_dW || (ldx >= K && lddw >= K)) && lddy >= N &&
                  (act == CR_ACT_NONE || ldz >= N), "cr_affine_backward: leading dimension too small");
   CR_REQUIRE(M == 0 || (d_dY && (act == CR_ACT_NONE || d_Z) && (!d_dX || d_W) && (!d_dW || d_X)), "cr_affine_backward: NULL argument");

@@ -594,6 +594,7 @@ extern "C" cr_status cr_rmsnorm(int type, const void* d_X, int ldx, const void* 
   CR_REQUIRE(float_type(type), "cr_rmsnorm: type must be FP32, FP16 or BF16");
   CR_REQUIRE(out_type == type || out_type == CR_TYPE_E4M3, "cr_rmsnorm: out_type must be type or e4m3");
   CR_REQUIRE(D >= 1 && T >= 0, "cr_rmsnorm: D >= 1, T >= 0");
+  CR_REQUIRE_SIZES("cr_rmsnorm", D, T);
   CR_REQUIRE(eps >= 0.0 && eps < 1e30, "cr_rmsnorm: eps must be finite and not negative");
   CR_REQUIRE(ldx >= D && ldy >= D && (!d_R || ldr >= D) && (!d_H || ldh >= D), "cr_rmsnorm: leading dimension below D");
   CR_REQUIRE((out_type == CR_TYPE_E4M3) == (d_scale != nullptr) || T == 0, "cr_rmsnorm: d_scale belongs to the e4m3 output");
@@ -630,6 +631,7 @@ extern "C" cr_status cr_rmsnorm_backward(int type, const void* d_H, int ldh, con
   CR_ENTRY_BEGIN
   CR_REQUIRE(float_type(type), "cr_rmsnorm_backward: type must be FP32, FP16 or BF16");
   CR_REQUIRE(D >= 1 && T >= 0, "cr_rmsnorm_backward: D >= 1, T >= 0");
+  CR_REQUIRE_SIZES("cr_rmsnorm_backward", D, T);
   CR_REQUIRE(eps >= 0.0 && eps < 1e30, "cr_rmsnorm_backward: eps must be finite and not negative");
   CR_REQUIRE(ldh >= D && lddy >= D && (!d_dH || lddh >= D) && (!d_dX || lddx >= D),
              "cr_rmsnorm_backward: leading dimension below D");

@@ -5,6 +5,7 @@
 #include <cuda_fp8.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <new>
 
 #include "common.cuh"
@@ -46,6 +47,17 @@ cr_status add_rows(const float* part, int rows, int D, float* total, cudaStream_
   do {                        \
     if (!(cond)) return ::cr::fail_literal(CR_ERR_ARG, msg); \
   } while (0)
+
+// Sizes of the operators end 2^16 before 2^31: indices that run past them by a tile, a warp or the step of a
+// grid-wide loop stay below 2^31.
+constexpr int MAXSIZE = 0x7fffffff - 0xffff;
+#define CR_REQUIRE_SIZES(what, ...) \
+  CR_REQUIRE(::cr::largest({__VA_ARGS__}) <= ::cr::MAXSIZE, what ": sizes end at 2^31 - 2^16")
+inline int largest(std::initializer_list<int> sizes) {
+  int m = 0;
+  for (int s : sizes) m = s > m ? s : m;
+  return m;
+}
 
 // ---------------------------------------------------------------- element types
 template <class T> __device__ __forceinline__ float to_float(T x);

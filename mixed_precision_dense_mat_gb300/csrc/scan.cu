@@ -895,6 +895,7 @@ extern "C" cr_status cr_gated_scan(int type, int gate, const void* d_G, int ldg,
   CR_REQUIRE(float_type(type), "cr_gated_scan: type must be FP32, FP16 or BF16");
   CR_REQUIRE(gate >= CR_GATE_COEFF && gate <= CR_GATE_VARIANCE, "cr_gated_scan: unknown gate");
   CR_REQUIRE(D >= 1 && T >= 0 && n_seq >= 0, "cr_gated_scan: D >= 1, T >= 0, n_seq >= 0");
+  CR_REQUIRE_SIZES("cr_gated_scan", D, T, n_seq);
   CR_REQUIRE(d_off || n_seq == 1, "cr_gated_scan: without offsets there is one series");
   CR_REQUIRE(n_seq > 0 || T == 0, "cr_gated_scan: columns without a series");
   CR_REQUIRE((T == 0 || (d_G && d_X && ldg >= D && ldx >= D)) && (!d_H || ldh >= D), "cr_gated_scan: NULL argument or leading dimension below D");
@@ -920,6 +921,7 @@ extern "C" cr_status cr_gated_scan_backward(int type, int gate, const void* d_G,
   CR_REQUIRE(float_type(type), "cr_gated_scan_backward: type must be FP32, FP16 or BF16");
   CR_REQUIRE(gate >= CR_GATE_COEFF && gate <= CR_GATE_VARIANCE, "cr_gated_scan_backward: unknown gate");
   CR_REQUIRE(D >= 1 && T >= 0 && n_seq >= 0, "cr_gated_scan_backward: D >= 1, T >= 0, n_seq >= 0");
+  CR_REQUIRE_SIZES("cr_gated_scan_backward", D, T, n_seq);
   CR_REQUIRE(d_off || n_seq == 1, "cr_gated_scan_backward: without offsets there is one series");
   CR_REQUIRE(n_seq > 0 || T == 0, "cr_gated_scan_backward: columns without a series");
   CR_REQUIRE(T == 0 || (d_G && d_X && d_dH && ldg >= D && ldx >= D && lddh >= D),
@@ -959,6 +961,7 @@ extern "C" cr_status cr_gated_step(int type, int gate, const void* d_G, int ldg,
   CR_REQUIRE(float_type(type), "cr_gated_step: type must be FP32, FP16 or BF16");
   CR_REQUIRE(gate >= CR_GATE_COEFF && gate <= CR_GATE_VARIANCE, "cr_gated_step: unknown gate");
   CR_REQUIRE(D >= 1 && B >= 0, "cr_gated_step: D >= 1, B >= 0");
+  CR_REQUIRE_SIZES("cr_gated_step", D, B);
   if (B == 0) return CR_OK;
   CR_REQUIRE(d_G && d_X && d_h && d_hnext, "cr_gated_step: NULL argument");
   CR_REQUIRE(ldg >= D && ldx >= D && ldh >= D && ldn >= D && (!d_H || ldo >= D), "cr_gated_step: leading dimension below D");
