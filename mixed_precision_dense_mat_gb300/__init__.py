@@ -513,6 +513,7 @@ def calibrate(S, zhat, v, u: float, level: float, counts: bool = True, extrema: 
 
 _ACTS = {"none": CR_ACT_NONE, "relu": CR_ACT_RELU, "silu": CR_ACT_SILU, "gelu": CR_ACT_GELU}
 _GATES = {"coeff": CR_GATE_COEFF, "convex": CR_GATE_CONVEX, "variance": CR_GATE_VARIANCE}
+_INT_MAX = 2 ** 31 - 1   # the C entries' sizes: ctypes would cut larger ones to 32 bits
 _types = None
 _torch = None
 
@@ -539,7 +540,7 @@ def _type_of(t, what: str) -> int:
 
 def _matrix(t, n: int, m: int, dtype, what: str):
     """(tensor, address, leading dimension) of a column-major n x m matrix argument, copied if it
-    is not column-major; (None, None, n) for None."""
+    is not column-major or its leading dimension passes the C int; (None, None, n) for None."""
     if t is None:
         return None, None, n
     if t.dtype is not dtype or not t.is_cuda or t.shape != (n, m):
@@ -548,7 +549,7 @@ def _matrix(t, n: int, m: int, dtype, what: str):
     s0, s1 = t.stride()
     if m == 1:
         s1 = n
-    if (s0 != 1 and n > 1) or s1 < n:
+    if (s0 != 1 and n > 1) or not n <= s1 <= _INT_MAX:
         t = t.T.contiguous().T
         s1 = n
     return t, t.data_ptr(), s1
@@ -594,7 +595,10 @@ def _code(table, name, what: str) -> int:
 def _shape(t, what: str):
     if t.dim() != 2:
         raise CrError(1, f"{what}: a matrix is needed, not {t.dim()} dimensions")
-    return t.shape
+    n, m = t.shape
+    if n > _INT_MAX or m > _INT_MAX:
+        raise CrError(1, f"{what}: {n} x {m} is beyond the library's sizes, which end at 2^31 - 2^16")
+    return n, m
 
 
 def affine(W, X, bias=None, act: str = "none", residual=None, w_scale=None, x_scale=None, out_dtype=None,
@@ -719,6 +723,8 @@ def _series(offsets, what: str):
         return None, None, 1
     if offsets.dtype is not _torch.int32 or offsets.dim() != 1 or offsets.shape[0] < 1 or not offsets.is_cuda:
         raise CrError(1, f"{what}: int32 CUDA offsets (series + 1) are needed")
+    if offsets.shape[0] > _INT_MAX:
+        raise CrError(1, f"{what}: {offsets.shape[0]} is beyond the library's sizes, which end at 2^31 - 2^16")
     offsets = offsets.contiguous()
     return offsets, offsets.data_ptr(), offsets.shape[0] - 1
 
