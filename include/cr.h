@@ -481,7 +481,9 @@ cr_status cr_affine_backward(int type, const void* d_W, int ldw, const void* d_X
  * NULL), y = gamma .* h / sqrt(mean(h^2) + eps), for X, R, H, Y D x T and gamma (D, FP32);
  * D >= 1, eps >= 0.  `type` (CR_TYPE_F32, CR_TYPE_F16, CR_TYPE_BF16) is that of X, R and H.
  * d_H (may be NULL) receives H and may be d_X or d_R (with the same leading dimension).  y is
- * formed from the unrounded sum.
+ * formed from the unrounded sum.  mean(h^2) is FP32 like every sum: where the squares pass its
+ * largest value (|h| above 2^63) y is 0, and below 2^-75 they count as 0 (y is then infinite
+ * with eps = 0).
  * out_type = type: Y holds y, d_scale is NULL.  out_type = CR_TYPE_E4M3: column t of Y holds
  * y / scale_t with scale_t = max(max|y|, 2^-100) / 448, and d_scale (T, FP32) receives the
  * scales; a column with a NaN or infinite sum is NaN and has a NaN scale. */

@@ -510,6 +510,8 @@ def calibrate(S, zhat, v, u: float, level: float, counts: bool = True, extrema: 
 
 
 # ---------------------------------------------------------------- trend network
+# Plain functions of memory, without autograd: results of tensors that require gradients carry none.
+# The *_backward functions are the gradients, to be called by the user or from a torch.autograd.Function.
 
 _ACTS = {"none": CR_ACT_NONE, "relu": CR_ACT_RELU, "silu": CR_ACT_SILU, "gelu": CR_ACT_GELU}
 _GATES = {"coeff": CR_GATE_COEFF, "convex": CR_GATE_CONVEX, "variance": CR_GATE_VARIANCE}

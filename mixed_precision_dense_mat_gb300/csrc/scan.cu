@@ -797,7 +797,9 @@ struct Scratch {
     lb.chunks = (int)(((long long)T + chunk - 1) / chunk);
     lb.tiles = tiles;
     lb.width = tiles * w;
-    // Groups: few hand-overs along the series against few maps to compose per chunk.
+    // Groups: few hand-overs along the series against few maps to compose per chunk.  Groups of 16, 32 and 64, BF16, convex
+    // gate, backward: 64 chunks of 2048 features (4096 steps) 32.7, 32.1 and 34.5 us; 1024 chunks 332, 317 and 357; 4096
+    // chunks of 64 features 159, 91 and 81.
     lb.group = lb.chunks <= 256 ? 16 : lb.chunks <= 1024 ? 32 : MAXGROUP;
     if (lb.chunks <= 1) return CR_OK;
     const size_t groups = ((size_t)lb.chunks + lb.group - 1) / lb.group;
