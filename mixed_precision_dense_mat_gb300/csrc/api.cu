@@ -216,20 +216,25 @@ cr_status allow_shared(const void* kernel, int bytes, std::atomic<uint64_t>& don
 
 // The word that a bounded wait of an operator kernel sets (mapped host memory, one per process).
 cr_status wait_word(int** d_word) {
-  static std::once_flag once;
+  static std::mutex mu;
   static volatile int* host = nullptr;
-  static int* dev = nullptr;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    if (cudaHostAlloc(&p, sizeof(int), cudaHostAllocMapped | cudaHostAllocPortable) != cudaSuccess) return;
-    *(int*)p = 0;
-    void* d = nullptr;
-    if (cudaHostGetDevicePointer(&d, p, 0) != cudaSuccess) return;
-    host = (volatile int*)p;
-    dev = (int*)d;
-  });
-  if (!dev) return fail_literal(CR_ERR_NOMEM, "no mapped host memory for the wait word");
-  *d_word = dev;
+  static std::atomic<int*> word{nullptr};
+  if (!word.load(std::memory_order_acquire)) {   // where it fails (inside a capture, say) a later call tries again
+    std::lock_guard<std::mutex> lk(mu);
+    if (!word.load(std::memory_order_relaxed)) {
+      void *p = nullptr, *d = nullptr;
+      cudaError_t e = cudaHostAlloc(&p, sizeof(int), cudaHostAllocMapped | cudaHostAllocPortable);
+      if (e == cudaSuccess && (e = cudaHostGetDevicePointer(&d, p, 0)) != cudaSuccess) cudaFreeHost(p);
+      if (e != cudaSuccess) {
+        cudaGetLastError();
+        return cuda_fail(e, "mapped host memory for the wait word");
+      }
+      *(int*)p = 0;
+      host = (volatile int*)p;
+      word.store((int*)d, std::memory_order_release);
+    }
+  }
+  *d_word = word.load(std::memory_order_relaxed);
   if (*host) {
     *host = 0;
     return fail_literal(CR_ERR_TIMEOUT, "a device-side wait of an earlier operator call ran out; its outputs are invalid");
