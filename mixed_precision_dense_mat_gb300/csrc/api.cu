@@ -365,7 +365,12 @@ cudaError_t scratch_alloc(void** p, size_t bytes, cudaStream_t stream) {
     }
     pool = g_pool[dev];
   }
-  return cudaMallocFromPoolAsync(p, bytes, pool, stream);
+  e = cudaMallocFromPoolAsync(p, bytes, pool, stream);
+  if (e == cudaErrorMemoryAllocation) {   // the pool has taken what the device had on the way, and would keep it
+    cudaGetLastError();
+    cudaMemPoolTrimTo(pool, 0);
+  }
+  return e;
 }
 
 void scratch_free(void* p, cudaStream_t stream) {
