@@ -263,7 +263,7 @@ __device__ __forceinline__ Floats<VEC> activate(Floats<VEC> z) {
   }
   if (ACT == CR_ACT_SILU) {
 #pragma unroll
-    for (int q = 0; q < VEC; ++q) z.x[q] = clamp_low(z.x[q], -87.0f);
+    for (int q = 0; q < VEC; ++q) z.x[q] = clamp_low(z.x[q], -88.0f);   // e^88 is finite, and its reciprocal flushed to 0
     return mul(z, rcp_fast(add(exp2_fast(mul(z, all_of<VEC>(-LOG2E))), all_of<VEC>(1.0f))));
   }
   if (ACT == CR_ACT_GELU) {   // z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|))
@@ -282,7 +282,7 @@ template <int ACT>
 __device__ __forceinline__ float activation_slope(float z) {
   if (ACT == CR_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
   if (ACT == CR_ACT_SILU) {
-    z = clamp_high(clamp_low(z, -87.0f), 87.0f);
+    z = clamp_high(clamp_low(z, -88.0f), 88.0f);
     const float e = exp2_fast(z * -LOG2E), p = rcp_fast(1.0f + e);
     return p * fmaf(z, e * p, 1.0f);
   }
