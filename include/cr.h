@@ -477,6 +477,65 @@ cr_status cr_affine_backward(int type, const void* d_W, int ldw, const void* d_X
                              int M, int act, void* d_dX, int lddx, int dw_type, void* d_dW,
                              int lddw, float* d_db, cr_stream stream);
 
+/* Gated affine product: Y = act(Z1) .* Z2 with [Z1; Z2] = diag(wscale) W^T X diag(xscale) + b 1^T,
+ * for W (K x 2N, ldw: the gate's columns, then the others'), X (K x M, ldx), b (2N), Z (2N x M)
+ * and Y (N x M); K, N >= 1.  Types, scales (d_wscale has 2N entries), bias and accuracy as in
+ * cr_affine.  A non-NULL d_Z receives [Z1; Z2], which cr_gated_affine_backward reads; Y is formed from
+ * the unrounded values. */
+cr_status cr_gated_affine(int type, const void* d_W, int ldw, const void* d_X, int ldx, int K,
+                          int N, int M, const float* d_wscale, const float* d_xscale,
+                          const float* d_bias, int act, int out_type, void* d_Z, int ldz,
+                          void* d_Y, int ldy, cr_stream stream);
+
+/* Gradient of cr_gated_affine (FP16 or BF16, no scales) for dY (N x M): with
+ * G = [dY .* Z2 .* act'(Z1); dY .* act(Z1)], dX = W G (K x M), dW = X G^T (K x 2N), db = G 1 (2N, FP32).
+ * W, X, dY, Z and dX have `type`, dW has dw_type (`type` or CR_TYPE_F32).  Each of d_dX, d_dW,
+ * d_db may be NULL (not wanted); d_W may be NULL without d_dX, d_X without d_dW.  G is rounded to
+ * `type` before the two products (not for db) and held in 4 N M bytes of scratch. */
+cr_status cr_gated_affine_backward(int type, const void* d_W, int ldw, const void* d_X, int ldx,
+                                   const void* d_dY, int lddy, const void* d_Z, int ldz, int K,
+                                   int N, int M, int act, void* d_dX, int lddx, int dw_type,
+                                   void* d_dW, int lddw, float* d_db, cr_stream stream);
+
+/* Group norm over packed fields: field f holds the columns (sites) off[f] .. off[f+1]-1 of X
+ * (d_off: n_field + 1 int32 on the device, ascending from 0; empty fields allowed; NULL means one
+ * field of all T columns).  Features are divided into `groups` groups of D / groups consecutive ones.
+ * With the mean and the variance (mean squared deviation) over a field's columns and a group's
+ * features, y = act(gamma (x - mean) rstd + beta), rstd = 1 / sqrt(variance + eps), eps >= 0; gamma
+ * and beta (D, FP32) may be NULL (1 and 0).  `type` (CR_TYPE_F32, CR_TYPE_F16, CR_TYPE_BF16) is that of X
+ * and Y; d_Y may be d_X (with the same leading dimension).  Columns from off[n_field] on belong to no
+ * field: theirs of Y are left as they were.  d_mean and d_rstd (groups x n_field FP32, lds; both
+ * or neither) receive the statistics, zeros for empty fields.  A NaN or infinity makes its own group of
+ * its own field NaN and leaves the others alone.  The variance is FP32: deviations above 2^63 make it
+ * infinite (y is then act(beta)). */
+cr_status cr_group_norm(int type, const void* d_X, int ldx, int D, int T, int groups,
+                        const int32_t* d_off, int n_field, const float* d_gamma,
+                        const float* d_beta, double eps, int act, void* d_Y, int ldy,
+                        float* d_mean, float* d_rstd, int lds, cr_stream stream);
+
+/* Gradient of cr_group_norm at X for dY (D x T of `type`), with the statistics that it saved: with
+ * h = (x - mean) rstd, dz = dY act'(gamma h + beta), u = gamma dz, dX = rstd (u - mean(u) - h mean(u h))
+ * (means over the field's group), dgamma = sum dz h, dbeta = sum dz (D, FP32).  d_dX, d_dgamma and
+ * d_dbeta may each be NULL; d_dX may be d_dY or d_X (with the same leading dimension).  Columns of no
+ * field count for nothing, and theirs of dX are left as they were. */
+cr_status cr_group_norm_backward(int type, const void* d_X, int ldx, int D, int T, int groups,
+                                 const int32_t* d_off, int n_field, const float* d_gamma,
+                                 const float* d_beta, const void* d_dY, int lddy,
+                                 const float* d_mean, const float* d_rstd, int lds, int act,
+                                 void* d_dX, int lddx, float* d_dgamma, float* d_dbeta,
+                                 cr_stream stream);
+
+/* Orthogonalised update of a weight matrix: O = X after `steps` (1 to 100) times
+ * X <- a X + (b A + c A^2) X, A = X X^T (or, the same, X <- a X + X (b A + c A^2), A = X^T X, for K > N),
+ * from X = G / |G|_F, for G and O (K x N) of CR_TYPE_F32, CR_TYPE_F16 or CR_TYPE_BF16 each.  With the usual
+ * coefficients O has G's singular vectors and singular values near 1.  |a|, |b|, |c| <= 64.  A zero G gives
+ * zeros; one with a NaN or an infinity gives NaN.  Sums are FP32; between the products matrices are kept in
+ * FP16, scaled, for a BF16 output and in two FP16 parts (22 bits) for FP16 and FP32 ones; entries of
+ * X, A or b A + c A^2 beyond 63 (coefficients that make X grow) turn infinite or NaN.  d_O may be d_G. */
+cr_status cr_orthogonalize(int type, const void* d_G, int ldg, int K, int N, int steps, double a,
+                           double b, double c, int out_type, void* d_O, int ldo,
+                           cr_stream stream);
+
 /* Root-mean-square norm of each column, with the residual's addition: H = X + R (X when d_R is
  * NULL), y = gamma .* h / sqrt(mean(h^2) + eps), for X, R, H, Y D x T and gamma (D, FP32);
  * D >= 1, eps >= 0.  `type` (CR_TYPE_F32, CR_TYPE_F16, CR_TYPE_BF16) is that of X, R and H.

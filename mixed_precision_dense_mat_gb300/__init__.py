@@ -30,6 +30,11 @@ The functions mirror include/cr.h:
   gated_scan(G, X, gate, offsets, h0)    cr_gated_scan
   gated_scan_backward(G, X, dH, ...)     cr_gated_scan_backward
   gated_step(G, X, h, gate)              cr_gated_step
+  gated_affine(W, X, bias, act)          cr_gated_affine
+  gated_affine_backward(W, X, dY, Z)     cr_gated_affine_backward
+  group_norm(X, groups, gamma, beta)     cr_group_norm
+  group_norm_backward(X, groups, ...)    cr_group_norm_backward
+  orthogonalize(G, steps, coeffs)        cr_orthogonalize
 The library is never replaced by a fallback: if libcr.so is missing or fails to load, every
 call raises.
 """
@@ -140,6 +145,11 @@ _SIGNATURES = {
     "cr_gated_scan_backward": (_I, [_I, _I, _P, _I, _P, _I, _P, _I, _I, _I, _P, _I, _P, _I, _P, _I, _P, _P, _I, _P, _I,
                                     _P, _I, _P]),
     "cr_gated_step": (_I, [_I, _I, _P, _I, _P, _I, _P, _I, _I, _I, _P, _I, _P, _I, _P]),
+    "cr_gated_affine": (_I, [_I, _P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P, _I, _P, _I, _P]),
+    "cr_gated_affine_backward": (_I, [_I, _P, _I, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _P, _I, _I, _P, _I, _P, _P]),
+    "cr_group_norm": (_I, [_I, _P, _I, _I, _I, _I, _P, _I, _P, _P, _D, _I, _P, _I, _P, _P, _I, _P]),
+    "cr_group_norm_backward": (_I, [_I, _P, _I, _I, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _I, _I, _P, _I, _P, _P, _P]),
+    "cr_orthogonalize": (_I, [_I, _P, _I, _I, _I, _I, _D, _D, _D, _I, _P, _I, _P]),
 }
 
 
@@ -803,3 +813,175 @@ def gated_step(G, X, h, gate: str = "convex", out=None, stream=None):
     _check(_lib.cr_gated_step(kind, _code(_GATES, gate, "gated_step gate"), pg, ldg, px, ldx, ph, ldh, D, B,
                               H.data_ptr(), D, pn, ldn, _raw_stream(device)))
     return H, out
+
+
+def _on_device(device, fn, *args):
+    """fn with `device` as the current one: kernels, scratch and streams are the current device's."""
+    with _torch.cuda.device(device):
+        return fn(*args)
+
+
+def _together(device, what: str, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise CrError(1, f"{what}: all tensors are on one device, not {device} and {t.device}")
+
+
+def _output(out, n: int, m: int, dtype, device, what: str):
+    """(tensor, address, leading dimension) of an output, allocated if the caller has none."""
+    if out is None:
+        out = _empty(n, m, dtype, device)
+        return out, out.data_ptr(), n
+    t, p, ld = _matrix(out, n, m, dtype, what)
+    if t is not out:
+        raise CrError(1, f"{what}: a column-major matrix is needed")
+    return out, p, ld
+
+
+def gated_affine(W, X, bias=None, act: str = "silu", w_scale=None, x_scale=None, out_dtype=None, save: bool = False, out=None,
+                 stream=None):
+    """cr_gated_affine: Y = act(Z1) * Z2 with [Z1; Z2] = W^T X + bias for W (K, 2N), the gate's N columns first, X (K, M) and
+    bias (2N); e4m3 operands take w_scale (2N) and x_scale (M).  out_dtype as in affine.  save=True returns
+    (Y, Z) with Z (2N, M), which gated_affine_backward reads."""
+    if stream is not None:
+        return _on(stream, gated_affine, W, X, bias, act, w_scale, x_scale, out_dtype, save, out)
+    if _torch is None:
+        _ready()
+    kind = _type_of(X, "gated_affine X")
+    dtype, device = X.dtype, X.device
+    if device.index != _torch.cuda.current_device():
+        return _on_device(device, gated_affine, W, X, bias, act, w_scale, x_scale, out_dtype, save, out)
+    _together(device, "gated_affine", W, bias, w_scale, x_scale, out)
+    K, M = _shape(X, "gated_affine X")
+    two = _shape(W, "gated_affine W")[1]
+    if two % 2:
+        raise CrError(1, f"gated_affine W: an even number of columns is needed, not {two}")
+    N = two // 2
+    X, px, ldx = _matrix(X, K, M, dtype, "gated_affine X")
+    W, pw, ldw = _matrix(W, K, two, dtype, "gated_affine W")
+    out_dtype = out_dtype or (out.dtype if out is not None else _torch.bfloat16 if kind == CR_TYPE_E4M3 else dtype)
+    out, py, ldy = _output(out, N, M, out_dtype, device, "gated_affine out")
+    Z = _empty(two, M, out_dtype, device) if save else None
+    bias, pb = _vector(bias, two, "gated_affine bias")
+    w_scale, pws = _vector(w_scale, two, "gated_affine w_scale")
+    x_scale, pxs = _vector(x_scale, M, "gated_affine x_scale")
+    _check(_lib.cr_gated_affine(kind, pw, ldw, px, ldx, K, N, M, pws, pxs, pb, _code(_ACTS, act, "gated_affine act"),
+                                _type_of(out, "gated_affine out"), Z.data_ptr() if save else None, two, py, ldy,
+                                _raw_stream(device)))
+    return (out, Z) if save else out
+
+
+def gated_affine_backward(W, X, dY, Z, act: str = "silu", need=(True, True, True), dw_dtype=None, stream=None):
+    """cr_gated_affine_backward: (dX, dW, dbias) of gated_affine at the saved Z; need says which of the three are wanted
+    (None for the others).  dw_dtype: X's type (default) or FP32."""
+    if stream is not None:
+        return _on(stream, gated_affine_backward, W, X, dY, Z, act, need, dw_dtype)
+    _ready()
+    kind = _type_of(X, "gated_affine_backward X")
+    dtype, device = X.dtype, X.device
+    if device.index != _torch.cuda.current_device():
+        return _on_device(device, gated_affine_backward, W, X, dY, Z, act, need, dw_dtype)
+    _together(device, "gated_affine_backward", W, dY, Z)
+    K, M = _shape(X, "gated_affine_backward X")
+    two = _shape(W, "gated_affine_backward W")[1]
+    if two % 2:
+        raise CrError(1, f"gated_affine_backward W: an even number of columns is needed, not {two}")
+    N = two // 2
+    X, px, ldx = _matrix(X, K, M, dtype, "gated_affine_backward X")
+    W, pw, ldw = _matrix(W, K, two, dtype, "gated_affine_backward W")
+    dY, pdy, lddy = _matrix(dY, N, M, dtype, "gated_affine_backward dY")
+    Z, pz, ldz = _matrix(Z, two, M, dtype, "gated_affine_backward Z")
+    dX = _empty(K, M, dtype, device) if need[0] else None
+    dW = _empty(K, two, dw_dtype or dtype, device) if need[1] else None
+    db = _torch.empty(two, dtype=_torch.float32, device=device) if need[2] else None
+    _check(_lib.cr_gated_affine_backward(kind, pw, ldw, px, ldx, pdy, lddy, pz, ldz, K, N, M,
+                                         _code(_ACTS, act, "gated_affine_backward act"), _ptr(dX), K,
+                                         _type_of(dW, "gated_affine_backward dw_dtype") if need[1] else kind, _ptr(dW), K,
+                                         _ptr(db), _raw_stream(device)))
+    return dX, dW, db
+
+
+def group_norm(X, groups: int, gamma=None, beta=None, act: str = "none", offsets=None, eps: float = 1e-5, save: bool = False,
+               out=None, stream=None):
+    """cr_group_norm: Y for X (D, T) with packed fields in the T columns (offsets: int32, fields + 1; None: one field) and
+    `groups` groups of features; save=True returns (Y, mean, rstd), the statistics (groups, fields) that
+    group_norm_backward reads.  out receives Y and may be X; columns of no field are left as they are there."""
+    if stream is not None:
+        return _on(stream, group_norm, X, groups, gamma, beta, act, offsets, eps, save, out)
+    if _torch is None:
+        _ready()
+    kind = _type_of(X, "group_norm X")
+    dtype, device = X.dtype, X.device
+    if device.index != _torch.cuda.current_device():
+        return _on_device(device, group_norm, X, groups, gamma, beta, act, offsets, eps, save, out)
+    _together(device, "group_norm", gamma, beta, offsets, out)
+    D, T = _shape(X, "group_norm X")
+    X, px, ldx = _matrix(X, D, T, dtype, "group_norm X")
+    offsets, po, n = _series(offsets, "group_norm offsets")
+    gamma, pg = _vector(gamma, D, "group_norm gamma")
+    beta, pb = _vector(beta, D, "group_norm beta")
+    if not 1 <= groups <= D or D % groups:
+        raise CrError(1, f"group_norm: {groups} groups do not divide {D} features")
+    out, py, ldy = _output(out, D, T, dtype, device, "group_norm out")
+    mean = _empty(groups, n, _torch.float32, device) if save else None
+    rstd = _empty(groups, n, _torch.float32, device) if save else None
+    _check(_lib.cr_group_norm(kind, px, ldx, D, T, groups, po, n, pg, pb, eps, _code(_ACTS, act, "group_norm act"), py, ldy,
+                              mean.data_ptr() if save else None, rstd.data_ptr() if save else None, groups, _raw_stream(device)))
+    return (out, mean, rstd) if save else out
+
+
+def group_norm_backward(X, groups: int, gamma, beta, dY, mean, rstd, act: str = "none", offsets=None, need=(True, True, True), out=None,
+                        stream=None):
+    """cr_group_norm_backward: (dX, dgamma, dbeta) of group_norm with the statistics that it saved; need says which of the
+    three are wanted (None for the others).  out receives dX and may be dY or X; columns of no field are left as
+    they are there."""
+    if stream is not None:
+        return _on(stream, group_norm_backward, X, groups, gamma, beta, dY, mean, rstd, act, offsets, need, out)
+    _ready()
+    kind = _type_of(X, "group_norm_backward X")
+    dtype, device, f32 = X.dtype, X.device, _torch.float32
+    if device.index != _torch.cuda.current_device():
+        return _on_device(device, group_norm_backward, X, groups, gamma, beta, dY, mean, rstd, act, offsets, need, out)
+    _together(device, "group_norm_backward", gamma, beta, dY, mean, rstd, offsets, out)
+    D, T = _shape(X, "group_norm_backward X")
+    X, px, ldx = _matrix(X, D, T, dtype, "group_norm_backward X")
+    dY, pdy, lddy = _matrix(dY, D, T, dtype, "group_norm_backward dY")
+    offsets, po, n = _series(offsets, "group_norm_backward offsets")
+    gamma, pg = _vector(gamma, D, "group_norm_backward gamma")
+    beta, pb = _vector(beta, D, "group_norm_backward beta")
+    if not 1 <= groups <= D or D % groups:
+        raise CrError(1, f"group_norm_backward: {groups} groups do not divide {D} features")
+    mean, pm, ldm = _matrix(mean, groups, n, f32, "group_norm_backward mean")
+    rstd, pr, ldr = _matrix(rstd, groups, n, f32, "group_norm_backward rstd")
+    if ldm != ldr:
+        rstd = rstd.T.contiguous().T
+        mean = mean.T.contiguous().T
+        pm, pr, ldm = mean.data_ptr(), rstd.data_ptr(), groups
+    dX, pdx, lddx = _output(out, D, T, dtype, device, "group_norm_backward out") if need[0] else (None, None, D)
+    dgamma = _torch.empty(D, dtype=f32, device=device) if need[1] else None
+    dbeta = _torch.empty(D, dtype=f32, device=device) if need[2] else None
+    _check(_lib.cr_group_norm_backward(kind, px, ldx, D, T, groups, po, n, pg, pb, pdy, lddy, pm, pr, ldm,
+                                       _code(_ACTS, act, "group_norm_backward act"), pdx, lddx, _ptr(dgamma), _ptr(dbeta),
+                                       _raw_stream(device)))
+    return dX, dgamma, dbeta
+
+
+def orthogonalize(G, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), out_dtype=None, out=None, stream=None):
+    """cr_orthogonalize: G (K, N) with its singular values brought near 1 by `steps` Newton-Schulz products with `coeffs`
+    (a, b, c), for a step along an orthogonalised gradient.  out_dtype: FP32, FP16 or BF16 (default: G's)."""
+    if stream is not None:
+        return _on(stream, orthogonalize, G, steps, coeffs, out_dtype, out)
+    if _torch is None:
+        _ready()
+    kind = _type_of(G, "orthogonalize G")
+    dtype, device = G.dtype, G.device
+    if device.index != _torch.cuda.current_device():
+        return _on_device(device, orthogonalize, G, steps, coeffs, out_dtype, out)
+    _together(device, "orthogonalize", out)
+    K, N = _shape(G, "orthogonalize G")
+    G, pg, ldg = _matrix(G, K, N, dtype, "orthogonalize G")
+    out, po, ldo = _output(out, K, N, out_dtype or (out.dtype if out is not None else dtype), device, "orthogonalize out")
+    a, b, c = coeffs
+    _check(_lib.cr_orthogonalize(kind, pg, ldg, K, N, steps, a, b, c, _type_of(out, "orthogonalize out"), po, ldo,
+                                 _raw_stream(device)))
+    return out

@@ -1,5 +1,6 @@
 """Trend-network operators in FP64: the affine product with its epilogue, the root-mean-square
-norm, and the gated recurrence, each with its gradient (oracle; test infra).
+norm, the gated recurrence, the gated product and the group norm, each with its gradient, and the
+orthogonalised update (oracle; test infra).
 
 The paper takes the trend design of universal kriging as given, so these follow the formulas
 of include/cr.h alone.  Matrices are features x columns."""
@@ -115,3 +116,64 @@ def gated_scan_backward(G, X, dH, kind, offsets, h0, dhT):
             q = a[:, t] * q
         dh0[:, s] = q
     return dG, dX, dh0
+
+
+def gated_affine(W, X, bias=None, act="silu", w_scale=None, x_scale=None):
+    """(Y, Z): Z = [Z1; Z2] = diag(w_scale) W^T X diag(x_scale) + bias 1^T, Y = act(Z1) * Z2."""
+    _, Z = affine(W, X, bias, "none", None, w_scale, x_scale)
+    n = Z.shape[0] // 2
+    return activation(Z[:n], act) * Z[n:], Z
+
+
+def gated_affine_backward(W, X, dY, Z, act="silu"):
+    """(dX, dW, dbias) of sum(dY * gated_affine)."""
+    n = Z.shape[0] // 2
+    G = np.concatenate([dY * Z[n:] * activation_slope(Z[:n], act), dY * activation(Z[:n], act)])
+    return W @ G, X @ G.T, G.sum(axis=1)
+
+
+def group_norm(X, groups, gamma, beta, act, offsets, eps):
+    """(Y, mean, rstd) by field and group; columns of no field are NaN in Y, statistics of empty fields zero."""
+    D = X.shape[0]
+    Y = np.full(X.shape, np.nan)
+    mean, rstd = np.zeros((groups, len(offsets) - 1)), np.zeros((groups, len(offsets) - 1))
+    for f in range(len(offsets) - 1):
+        a, b = offsets[f], offsets[f + 1]
+        if a == b:
+            continue
+        block = X[:, a:b].reshape(groups, -1)
+        mean[:, f] = block.mean(axis=1)
+        rstd[:, f] = 1.0 / np.sqrt(block.var(axis=1) + eps)
+        h = ((block - mean[:, f:f + 1]) * rstd[:, f:f + 1]).reshape(D, b - a)
+        Y[:, a:b] = activation(gamma[:, None] * h + beta[:, None], act)
+    return Y, mean, rstd
+
+
+def group_norm_backward(X, groups, gamma, beta, dY, mean, rstd, act, offsets):
+    """(dX, dgamma, dbeta) of sum(dY * group_norm) over the fields' columns; dX is NaN outside them."""
+    D = X.shape[0]
+    dX, dgamma, dbeta = np.full(X.shape, np.nan), np.zeros(D), np.zeros(D)
+    for f in range(len(offsets) - 1):
+        a, b = offsets[f], offsets[f + 1]
+        if a == b:
+            continue
+        r = np.repeat(rstd[:, f], D // groups)[:, None]
+        h = (X[:, a:b] - np.repeat(mean[:, f], D // groups)[:, None]) * r
+        dz = dY[:, a:b] * activation_slope(gamma[:, None] * h + beta[:, None], act)
+        dgamma += np.sum(dz * h, axis=1)
+        dbeta += np.sum(dz, axis=1)
+        u = gamma[:, None] * dz
+        m1 = np.repeat(u.reshape(groups, -1).mean(axis=1), D // groups)[:, None]
+        m2 = np.repeat((u * h).reshape(groups, -1).mean(axis=1), D // groups)[:, None]
+        dX[:, a:b] = r * (u - m1 - h * m2)
+    return dX, dgamma, dbeta
+
+
+def orthogonalize(G, steps=5, coeffs=(3.4445, -4.7750, 2.0315)):
+    """G / |G|_F with its singular values s replaced `steps` times by a s + b s^3 + c s^5."""
+    a, b, c = coeffs
+    u, s, v = np.linalg.svd(G, full_matrices=False)
+    s = s / np.sqrt(np.sum(s * s)) if s.any() else s
+    for _ in range(steps):
+        s = s * (a + s * s * (b + c * s * s))
+    return (u * s) @ v
