@@ -14,6 +14,7 @@ namespace cr {
 namespace {
 
 constexpr int NT = 256;
+constexpr int RESIDENT = 3;   // blocks that share an SM (85 registers a thread)
 
 // Tile (fb, t): features fb * TX * V on, columns t * cols on.  Threads: TX along features, V consecutive ones each
 // (V = 8: 16-byte accesses for 16-bit types), NT / TX along columns.
@@ -46,26 +47,71 @@ __device__ __forceinline__ size_t share(const Fields& p, int t, int f, int fb, i
 }
 size_t shares(const Fields& p) { return (size_t)(p.tiles + p.n) * (p.blocks + p.groups); }
 
+// V elements as they are in memory.  They are loaded in batches of columns before any is used or stored: the compiler may not
+// move a load of X above a store to Y, which may be the same matrix.
 template <class T, int V>
-__device__ __forceinline__ void load(const T* p, float (&v)[V]) {
-  if constexpr (V == 8) widen8(*reinterpret_cast<const Eight<T>*>(p), v);
-  else v[0] = to_float(p[0]);
-}
+struct alignas(V * sizeof(T)) Raw {
+  uint32_t w[V * sizeof(T) / 4];
+  __device__ __forceinline__ void load(const T* p) { *this = *reinterpret_cast<const Raw*>(p); }
+  __device__ __forceinline__ void widen(float (&v)[V]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] = __uint_as_float(w[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; e += 2) {
+        const float2 f = widen2(w[e / 2], T{});
+        v[e] = f.x;
+        v[e + 1] = f.y;
+      }
+    }
+  }
+};
+template <class T>
+struct Raw<T, 1> {
+  T w;
+  __device__ __forceinline__ void load(const T* p) { w = *p; }
+  __device__ __forceinline__ void widen(float (&v)[1]) const { v[0] = to_float(w); }
+};
 template <class T, int V>
 __device__ __forceinline__ void store(T* p, const float (&v)[V]) {
-  if constexpr (V == 8) *reinterpret_cast<Eight<T>*>(p) = narrow8<T>(v);
-  else p[0] = from_float<T>(v[0]);
+  if constexpr (V == 1) {
+    p[0] = from_float<T>(v[0]);
+  } else {
+    Raw<T, V> o;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) o.w[e] = __float_as_uint(v[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; e += 2) o.w[e / 2] = narrow2(v[e], v[e + 1], T{});
+    }
+    *reinterpret_cast<Raw<T, V>*>(p) = o;
+  }
 }
-
-// n values of mean and sum of squared deviations m2; joined with those of m others (Chan, Golub and LeVeque's update).
-struct Moments {
-  float n, mean, m2;
+template <class T, int V>
+struct Pair {
+  Raw<T, V> x, d;
 };
-__device__ __forceinline__ Moments join(Moments a, Moments b) {
-  const float n = a.n + b.n;
-  if (b.n == 0.0f) return a;
-  const float d = b.mean - a.mean, w = b.n / n;
-  return {n, fmaf(d, w, a.mean), a.m2 + fmaf(d * a.n * w, d, b.m2)};
+// The thread's columns j = a, a + TY, .. < b in batches of B: each batch is loaded before the one before it is used,
+// use(batch, its first column).
+template <int B, int TY, class Buf, class L, class U>
+__device__ __forceinline__ void in_batches(int a, int b, L&& load, U&& use) {
+  Buf now[B], next[B];
+  int j = a;
+#pragma unroll
+  for (int q = 0; q < B; ++q)
+    if (j + q * TY < b) load(now[q], j + q * TY);
+  while (j < b) {
+    const int k = j + B * TY;
+#pragma unroll
+    for (int q = 0; q < B; ++q)
+      if (k + q * TY < b) load(next[q], k + q * TY);
+    use(now, j);
+#pragma unroll
+    for (int q = 0; q < B; ++q) now[q] = next[q];
+    j = k;
+  }
 }
 
 // Calls run(f, a, b) for the fields' columns a .. b - 1 inside the tile, and none(f) for empty fields, each by one tile.
@@ -84,7 +130,7 @@ __device__ __forceinline__ void each_field(const Fields& p, int t, R&& run, E&& 
 
 // ---------------------------------------------------------------- forward
 template <class T, int TX, int V>
-__global__ void __launch_bounds__(NT) k_gnorm_stats(const T* X, int ldx, const Fields p, float2* part) {
+__global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_stats(const T* X, int ldx, const Fields p, float2* part) {
   constexpr int TY = NT / TX, FW = TX * V;
   __shared__ float2 red[TY][FW];   // of a thread's features
   __shared__ float2 feature[FW];
@@ -96,48 +142,72 @@ __global__ void __launch_bounds__(NT) k_gnorm_stats(const T* X, int ldx, const F
   each_field(p, t, [&](int f, int a, int b) {
     float mean[V] = {}, m2[V] = {}, n = 0.0f;
     if (i < p.D) {
-      int j = a + ty;
-      for (; j + 3 * TY < b; j += 4 * TY) {   // four columns: their own mean and deviations, joined to what is there
-        float x[4][V];
+      constexpr int B = 4, P = V > 1 ? 2 : 1;
+      in_batches<B, TY, Raw<T, V>>(a + ty, b, [&](Raw<T, V>& raw, int j) { raw.load(X + (size_t)j * ldx + i); },
+                                   [&](const Raw<T, V>(&raw)[B], int j) {
+        if (j + (B - 1) * TY < b) {   // the batch's own mean and deviations, joined to what is there
+          float x[B][V];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) load<T, V>(X + (size_t)(j + q * TY) * ldx + i, x[q]);
-        const float w = 4.0f / (n + 4.0f), nw = n * w;
-        n += 4.0f;
+          for (int q = 0; q < B; ++q) raw[q].widen(x[q]);
+          const float w = __fdividef(B, n + B), nw = n * w;
+          n += B;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float m = ((x[0][e] + x[1][e]) + (x[2][e] + x[3][e])) * 0.25f;
-          float s = 0.0f;
+          for (int e = 0; e < V; e += P) {
+            Floats<P> v[B], d2 = all_of<P>(0.0f), old;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) s = fmaf(x[q][e] - m, x[q][e] - m, s);
-          const float d = m - mean[e];
-          mean[e] = fmaf(d, w, mean[e]);
-          m2[e] += fmaf(d * nw, d, s);
+            for (int q = 0; q < B; ++q)
+#pragma unroll
+              for (int o = 0; o < P; ++o) v[q].x[o] = x[q][e + o];
+            const Floats<P> minus = mul(add(add(v[0], v[1]), add(v[2], v[3])), all_of<P>(-1.0f / B));   // the batch's mean
+#pragma unroll
+            for (int q = 0; q < B; ++q) {
+              const Floats<P> d = add(v[q], minus);
+              d2 = fma(d, d, d2);
+            }
+#pragma unroll
+            for (int o = 0; o < P; ++o) old.x[o] = mean[e + o];
+            const Floats<P> dev = add(minus, old), up = fma(dev, all_of<P>(-w), old), t = fma(mul(dev, all_of<P>(nw)), dev, d2);
+#pragma unroll
+            for (int o = 0; o < P; ++o) {
+              mean[e + o] = up.x[o];
+              m2[e + o] += t.x[o];
+            }
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < B - 1; ++q)
+            if (j + q * TY < b) {
+              float x[V];
+              raw[q].widen(x);
+              const float w = __fdividef(1.0f, n + 1.0f), nw = n * w;
+              n += 1.0f;
+#pragma unroll
+              for (int e = 0; e < V; ++e) {
+                const float d = x[e] - mean[e];
+                mean[e] = fmaf(d, w, mean[e]);
+                m2[e] = fmaf(d * nw, d, m2[e]);
+              }
+            }
         }
-      }
-      for (; j < b; j += TY) {
-        float x[V];
-        load<T, V>(X + (size_t)j * ldx + i, x);
-        const float w = 1.0f / (n + 1.0f), nw = n * w;
-        n += 1.0f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float d = x[e] - mean[e];
-          mean[e] = fmaf(d, w, mean[e]);
-          m2[e] = fmaf(d * nw, d, m2[e]);
-        }
-      }
+      });
     }
     __syncthreads();   // the last field's sums have been read
 #pragma unroll
     for (int e = 0; e < V; ++e) red[ty][tx * V + e] = make_float2(mean[e], m2[e]);
     __syncthreads();
-    for (int x = threadIdx.x; x < width; x += NT) {
-      Moments m = {0.0f, 0.0f, 0.0f};
-      for (int y = 0; y < TY; ++y) {
-        const int cols = b - a > y ? (b - a - y + TY - 1) / TY : 0;
-        m = join(m, Moments{(float)cols, red[y][x].x, red[y][x].y});
+    for (int x = threadIdx.x; x < width; x += NT) {   // about the first thread's mean, which is no further off than a TY-th of the columns
+      const float at = red[0][x].x;
+      float s = 0.0f, s2 = red[0][x].y;
+#pragma unroll
+      for (int y = 1; y < TY; ++y) {
+        const float cols = (float)((max(b - a - y, 0) + TY - 1) / TY), d = red[y][x].x - at;
+        if (cols > 0.0f) {
+          s = fmaf(d, cols, s);
+          s2 += fmaf(d * cols, d, red[y][x].y);
+        }
       }
-      feature[x] = make_float2(m.mean, m.m2);
+      const float d = s / (float)(b - a);
+      feature[x] = make_float2(at + d, clamp_low(fmaf(-d, s, s2), 0.0f));
     }
     __syncthreads();
     // features of a group have the same number of columns: their mean, and their deviations about it
@@ -167,9 +237,9 @@ __device__ __forceinline__ void each_share(const Fields& p, int f, int g, G&& ge
   const int begin = field_begin(p, f), end = field_begin(p, f + 1);
   const int t0 = begin / p.cols, nt = (end - 1) / p.cols - t0 + 1;
   const int i0 = g * p.group, i1 = i0 + p.group, b0 = i0 / FW, nb = (i1 - 1) / FW - b0 + 1;
-  const long long total = (long long)nt * nb;
-  for (long long e = threadIdx.x & 31; e < total; e += 32) {
-    const int t = t0 + (int)(e / nb), fb = b0 + (int)(e % nb);
+  const int total = nt * nb;   // at most the tiles of the matrix
+  for (int e = threadIdx.x & 31; e < total; e += 32) {
+    const int t = nb == 1 ? t0 + e : t0 + e / nb, fb = nb == 1 ? b0 : b0 + e % nb;
     const int cols = min(end, (t + 1) * p.cols) - max(begin, t * p.cols), features = min(i1, (fb + 1) * FW) - max(i0, fb * FW);
     get(share(p, t, f, fb, g), cols, features);
   }
@@ -177,7 +247,7 @@ __device__ __forceinline__ void each_share(const Fields& p, int f, int g, G&& ge
 
 // Columns are t * cols + cols <= T + cols < 2^31.
 template <class T, int TX, int V, int ACT>
-__global__ void __launch_bounds__(NT) k_gnorm_apply(const T* X, int ldx, const Fields p, const float2* part, const float* gamma,
+__global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_apply(const T* X, int ldx, const Fields p, const float2* part, const float* gamma,
                                                     const float* beta, float eps, T* Y, int ldy, float* mean_out, float* rstd_out, int lds) {
   constexpr int TY = NT / TX, FW = TX * V;
   __shared__ float2 stat[FW];   // by group of the block
@@ -195,19 +265,26 @@ __global__ void __launch_bounds__(NT) k_gnorm_apply(const T* X, int ldx, const F
   each_field(p, t, [&](int f, int a, int b) {
     __syncthreads();
     for (int g = g0 + ((int)threadIdx.x >> 5); g <= g1; g += NT / 32) {
-      Moments m = {0.0f, 0.0f, 0.0f};
-      each_share<FW>(p, f, g, [&](size_t s, int cols, int features) { m = join(m, Moments{(float)cols * (float)features, part[s].x, part[s].y}); });
+      // the mean about one share's mean, then the deviations about it
+      const int begin = field_begin(p, f);
+      const float n = (float)(field_begin(p, f + 1) - begin) * (float)p.group;
+      const float at = part[share(p, begin / p.cols, f, g * p.group / FW, g)].x;
+      float s = 0.0f, d2 = 0.0f;
+      each_share<FW>(p, f, g, [&](size_t k, int cols, int features) { s = fmaf(part[k].x - at, (float)cols * (float)features, s); });
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const Moments other = {__shfl_down_sync(0xffffffffu, m.n, o), __shfl_down_sync(0xffffffffu, m.mean, o), __shfl_down_sync(0xffffffffu, m.m2, o)};
-        if (m.n == 0.0f) m = other;
-        else m = join(m, other);
-      }
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const float mean = at + s / n;
+      each_share<FW>(p, f, g, [&](size_t k, int cols, int features) {
+        const float d = part[k].x - mean;
+        d2 += fmaf(d * ((float)cols * (float)features), d, part[k].y);
+      });
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) d2 += __shfl_xor_sync(0xffffffffu, d2, o);
       if ((threadIdx.x & 31) == 0) {
-        const float r = 1.0f / sqrtf(m.m2 / m.n + eps);
-        stat[g - g0] = make_float2(m.mean, r);
-        if (mean_out && a == field_begin(p, f) && g * p.group >= i0) {   // the tile with the group's first element
-          mean_out[(size_t)f * lds + g] = m.mean;
+        const float r = 1.0f / sqrtf(d2 / n + eps);
+        stat[g - g0] = make_float2(mean, r);
+        if (mean_out && a == begin && g * p.group >= i0) {   // the tile with the group's first element
+          mean_out[(size_t)f * lds + g] = mean;
           rstd_out[(size_t)f * lds + g] = r;
         }
       }
@@ -221,15 +298,20 @@ __global__ void __launch_bounds__(NT) k_gnorm_apply(const T* X, int ldx, const F
         m[e] = st.x;
         s[e] = st.y * gm[e];
       }
-#pragma unroll 4
-      for (int j = a + ty; j < b; j += TY) {
-        float x[V];
-        load<T, V>(X + (size_t)j * ldx + i, x);
+      constexpr int B = 4;
+      in_batches<B, TY, Raw<T, V>>(a + ty, b, [&](Raw<T, V>& raw, int j) { raw.load(X + (size_t)j * ldx + i); },
+                                   [&](const Raw<T, V>(&raw)[B], int j) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) x[e] = fmaf(x[e] - m[e], s[e], bt[e]);
-        activate_each<ACT, V>(x);
-        store<T, V>(Y + (size_t)j * ldy + i, x);
-      }
+        for (int q = 0; q < B; ++q)
+          if (j + q * TY < b) {
+            float x[V];
+            raw[q].widen(x);
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[e] = fmaf(x[e] - m[e], s[e], bt[e]);
+            activate_each<ACT, V>(x);
+            store<T, V>(Y + (size_t)(j + q * TY) * ldy + i, x);
+          }
+      });
     }
   }, [&](int f) {
     if (!mean_out) return;
@@ -242,7 +324,7 @@ __global__ void __launch_bounds__(NT) k_gnorm_apply(const T* X, int ldx, const F
 // With h = (x - mean) r, dz = dY act'(gamma h + beta): a feature's sums over the tile of dz h and dz go to
 // psum[t][2 D], and the groups' shares of sum gamma dz and sum gamma dz h to part.
 template <class T, int TX, int V, int ACT>
-__global__ void __launch_bounds__(NT) k_gnorm_sums(const T* X, int ldx, const T* dY, int lddy, const Fields p, const float* gamma,
+__global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_sums(const T* X, int ldx, const T* dY, int lddy, const Fields p, const float* gamma,
                                                    const float* beta, const float* mean, const float* rstd, int lds, float2* part, float* pgamma,
                                                    float* pbeta) {
   constexpr int TY = NT / TX, FW = TX * V;
@@ -270,19 +352,26 @@ __global__ void __launch_bounds__(NT) k_gnorm_sums(const T* X, int ldx, const T*
         m[e] = mean[at];
         r[e] = rstd[at];
       }
-#pragma unroll 2
-      for (int j = a + ty; j < b; j += TY) {
-        float x[V], d[V];
-        load<T, V>(X + (size_t)j * ldx + i, x);
-        load<T, V>(dY + (size_t)j * lddy + i, d);
+      constexpr int B = sizeof(T) == 2 ? 4 : 2;
+      in_batches<B, TY, Pair<T, V>>(a + ty, b, [&](Pair<T, V>& raw, int j) {
+        raw.x.load(X + (size_t)j * ldx + i);
+        raw.d.load(dY + (size_t)j * lddy + i);
+      }, [&](const Pair<T, V>(&raw)[B], int j) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float h = __fmul_rn(x[e] - m[e], r[e]);
-          if (ACT != CR_ACT_NONE) d[e] = __fmul_rn(d[e], activation_slope<ACT>(fmaf(h, gm[e], bt[e])));
-          sb[e] += d[e];
-          sg[e] = fmaf(d[e], h, sg[e]);
-        }
-      }
+        for (int q = 0; q < B; ++q)
+          if (j + q * TY < b) {
+            float x[V], d[V];
+            raw[q].x.widen(x);
+            raw[q].d.widen(d);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              const float h = __fmul_rn(x[e] - m[e], r[e]);
+              if (ACT != CR_ACT_NONE) d[e] = __fmul_rn(d[e], activation_slope<ACT>(fmaf(h, gm[e], bt[e])));
+              sb[e] += d[e];
+              sg[e] = fmaf(d[e], h, sg[e]);
+            }
+          }
+      });
     }
     __syncthreads();
 #pragma unroll
@@ -327,7 +416,7 @@ __global__ void __launch_bounds__(NT) k_gnorm_sums(const T* X, int ldx, const T*
 
 // dX = r (gamma dz - mean(gamma dz) - h mean(gamma dz h)), means over the group.
 template <class T, int TX, int V, int ACT>
-__global__ void __launch_bounds__(NT) k_gnorm_dx(const T* X, int ldx, const T* dY, int lddy, const Fields p, const float2* part,
+__global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_dx(const T* X, int ldx, const T* dY, int lddy, const Fields p, const float2* part,
                                                  const float* gamma, const float* beta, const float* mean, const float* rstd, int lds, T* dX,
                                                  int lddx) {
   constexpr int TY = NT / TX, FW = TX * V;
@@ -371,38 +460,48 @@ __global__ void __launch_bounds__(NT) k_gnorm_dx(const T* X, int ldx, const T* d
         c1[e] = stat[g - g0].x;
         c2[e] = stat[g - g0].y;
       }
-#pragma unroll 2
-      for (int j = a + ty; j < b; j += TY) {
-        float x[V], d[V];
-        load<T, V>(X + (size_t)j * ldx + i, x);
-        load<T, V>(dY + (size_t)j * lddy + i, d);
+      constexpr int B = sizeof(T) == 2 ? 4 : 2;
+      in_batches<B, TY, Pair<T, V>>(a + ty, b, [&](Pair<T, V>& raw, int j) {
+        raw.x.load(X + (size_t)j * ldx + i);
+        raw.d.load(dY + (size_t)j * lddy + i);
+      }, [&](const Pair<T, V>(&raw)[B], int j) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float h = __fmul_rn(x[e] - m[e], r[e]);
-          if (ACT != CR_ACT_NONE) d[e] = __fmul_rn(d[e], activation_slope<ACT>(fmaf(h, gm[e], bt[e])));
-          x[e] = __fmul_rn(r[e], fmaf(-h, c2[e], fmaf(d[e], gm[e], -c1[e])));
-        }
-        store<T, V>(dX + (size_t)j * lddx + i, x);
-      }
+        for (int q = 0; q < B; ++q)
+          if (j + q * TY < b) {
+            float x[V], d[V];
+            raw[q].x.widen(x);
+            raw[q].d.widen(d);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              const float h = __fmul_rn(x[e] - m[e], r[e]);
+              if (ACT != CR_ACT_NONE) d[e] = __fmul_rn(d[e], activation_slope<ACT>(fmaf(h, gm[e], bt[e])));
+              x[e] = __fmul_rn(r[e], fmaf(-h, c2[e], fmaf(d[e], gm[e], -c1[e])));
+            }
+            store<T, V>(dX + (size_t)(j + q * TY) * lddx + i, x);
+          }
+      });
     }
   }, [](int) {});
 }
 
-bool ok16(const void* p, int ld, int eb) { return ((uintptr_t)p & 15) == 0 && (long long)ld * eb % 16 == 0; }
+// Columns of 16-bit types on 8- or 16-byte boundaries (bytes), of FP32 on 16-byte ones.
+bool aligned(const void* p, int ld, int eb, int bytes) { return ((uintptr_t)p & (bytes - 1)) == 0 && (long long)ld * eb % bytes == 0; }
 
-// Calls f(TX, V) for a matrix of D features: the widest of 256, 128 and 64 features that leaves least unused.
-template <class F>
+// Calls f(TX, V) for a matrix of D features, V of them to a thread (1 where 16-byte or, for V = 4 of 16-bit types, 8-byte accesses do
+// not apply): the widest of 32, 16 and 8 threads along them that leaves least unused.
+template <int V, class F>
 cr_status with_tile(int D, bool vec, F&& f) {
   using std::integral_constant;
   if (!vec) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
   const auto padded = [&](int w) { return (D + w - 1) / w * w; };
-  const int best = std::min({padded(256), padded(128), padded(64)});
-  if (padded(256) == best) return f(integral_constant<int, 32>{}, integral_constant<int, 8>{});
-  if (padded(128) == best) return f(integral_constant<int, 16>{}, integral_constant<int, 8>{});
-  return f(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+  const int best = std::min({padded(32 * V), padded(16 * V), padded(8 * V)});
+  if (padded(32 * V) == best) return f(integral_constant<int, 32>{}, integral_constant<int, V>{});
+  if (padded(16 * V) == best) return f(integral_constant<int, 16>{}, integral_constant<int, V>{});
+  return f(integral_constant<int, 8>{}, integral_constant<int, V>{});
 }
 
-// Columns of a tile: about four tiles to an SM, and 16 columns to a thread's lane of them at most.
+// Tiles that are resident at once, of whole batches of columns: a tile's set-up and its groups' sums cost about as much as
+// 64 KB of columns.
 Fields make_fields(const int32_t* off, int n, int T, int D, int groups, int width, int rows) {
   Fields p = {};
   p.off = off;
@@ -412,9 +511,8 @@ Fields make_fields(const int32_t* off, int n, int T, int D, int groups, int widt
   p.groups = groups;
   p.group = D / groups;
   p.blocks = (D + width - 1) / width;
-  const long long want = std::max(1ll, 4ll * sm_count() / p.blocks);
-  const long long per = (T + want - 1) / want;
-  p.cols = (int)std::min<long long>(std::max<long long>((per + 4 * rows - 1) / (4 * rows), 1) * 4 * rows, 32 * rows);
+  const long long want = std::max(1, RESIDENT * sm_count() / p.blocks), per = (T + want - 1) / want, batch = 4 * rows;
+  p.cols = (int)((per + batch - 1) / batch * batch);
   p.tiles = (T + p.cols - 1) / p.cols;
   return p;
 }
@@ -455,8 +553,9 @@ extern "C" cr_status cr_group_norm(int type, const void* d_X, int ldx, int D, in
   CR_TRY(wait_word(&err));
   return with_type(type, [&](auto t0) -> cr_status {
     using E = decltype(t0);
-    const bool vec = D % 8 == 0 && ok16(d_X, ldx, sizeof(E)) && ok16(d_Y, ldy, sizeof(E));
-    return with_tile(D, vec, [&](auto tx0, auto v0) -> cr_status {
+    constexpr int EB = sizeof(E), W = 16 / EB;
+    const bool vec = D % W == 0 && aligned(d_X, ldx, EB, 16) && aligned(d_Y, ldy, EB, 16);
+    return with_tile<W>(D, vec, [&](auto tx0, auto v0) -> cr_status {
       constexpr int TX = decltype(tx0)::value, V = decltype(v0)::value;
       const Fields p = make_fields(d_off, n_field, T, D, groups, TX * V, NT / TX);
       const unsigned grid = (unsigned)((long long)p.tiles * p.blocks);
@@ -504,8 +603,10 @@ extern "C" cr_status cr_group_norm_backward(int type, const void* d_X, int ldx, 
   CR_TRY(wait_word(&err));
   return with_type(type, [&](auto t0) -> cr_status {
     using E = decltype(t0);
-    const bool vec = D % 8 == 0 && ok16(d_X, ldx, sizeof(E)) && ok16(d_dY, lddy, sizeof(E)) && (!d_dX || ok16(d_dX, lddx, sizeof(E)));
-    return with_tile(D, vec, [&](auto tx0, auto v0) -> cr_status {
+    // four features to a thread: with eight, their six constants each do not fit into registers beside the columns on their way
+    constexpr int EB = sizeof(E), W = 4;
+    const bool vec = D % W == 0 && aligned(d_X, ldx, EB, W * EB) && aligned(d_dY, lddy, EB, W * EB) && (!d_dX || aligned(d_dX, lddx, EB, W * EB));
+    return with_tile<W>(D, vec, [&](auto tx0, auto v0) -> cr_status {
       constexpr int TX = decltype(tx0)::value, V = decltype(v0)::value;
       const Fields p = make_fields(d_off, n_field, T, D, groups, TX * V, NT / TX);
       const unsigned grid = (unsigned)((long long)p.tiles * p.blocks);
