@@ -14,6 +14,7 @@ namespace cr {
 namespace {
 
 constexpr int NT = 256;
+constexpr int SMALL = 12;   // k_gnorm_small: accesses of a thread, if one field had all columns
 constexpr int RESIDENT = 3;   // blocks that share an SM (85 registers a thread)
 
 // Tile (fb, t): features fb * TX * V on, columns t * cols on.  Threads: TX along features, V consecutive ones each
@@ -93,28 +94,68 @@ template <class T, int V>
 struct Pair {
   Raw<T, V> x, d;
 };
-// The thread's columns j = a, a + TY, .. < b in batches of B: each batch is loaded before the one before it is used,
-// use(batch, its first column).
+// The thread's columns a, a + TY, .. < b in batches of B, each loaded before the one before it is used: load(buffer, elements past
+// the first column's), use(batch, column, how many).
 template <int B, int TY, class Buf, class L, class U>
 __device__ __forceinline__ void in_batches(int a, int b, L&& load, U&& use) {
+  const int count = a < b ? (b - a + TY - 1) / TY : 0, full = count / B;
   Buf now[B], next[B];
-  int j = a;
+  if (full > 0) {
 #pragma unroll
-  for (int q = 0; q < B; ++q)
-    if (j + q * TY < b) load(now[q], j + q * TY);
-  while (j < b) {
-    const int k = j + B * TY;
+    for (int q = 0; q < B; ++q) load(now[q], q * TY);
+  }
+#pragma unroll 2
+  for (int k = 1; k <= full; ++k) {
+    if (k < full) {
 #pragma unroll
-    for (int q = 0; q < B; ++q)
-      if (k + q * TY < b) load(next[q], k + q * TY);
-    use(now, j);
+      for (int q = 0; q < B; ++q) load(next[q], (k * B + q) * TY);
+    }
+    use(now, (k - 1) * B * TY, std::integral_constant<int, B>{});
 #pragma unroll
     for (int q = 0; q < B; ++q) now[q] = next[q];
-    j = k;
+  }
+  const int left = count - full * B, at = full * B * TY;
+#pragma unroll
+  for (int q = 0; q < B - 1; ++q)
+    if (q < left) load(now[q], at + q * TY);
+#pragma unroll
+  for (int q = 0; q < B - 1; ++q)
+    if (q < left) use(reinterpret_cast<const Buf(&)[1]>(now[q]), at + q * TY, std::integral_constant<int, 1>{});
+}
+template <int V>
+__device__ __forceinline__ Floats<V == 1 ? 1 : 2> pair_at(const float (&v)[V], int e) {
+  if constexpr (V == 1) return {{v[0]}};
+  else return {{v[e], v[e + 1]}};
+}
+
+// Groups of the block are reduced by LANES threads each, all of them at once where the block has up to NT / LANES.
+constexpr int LANES = 8;
+__device__ __forceinline__ float lanes_sum(float x) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+// Calls use(g, lane) for every group g0 .. g1, all threads of a warp together; g may pass g1 in the last turn.
+template <class U>
+__device__ __forceinline__ void each_group(int g0, int g1, U&& use) {
+  const int lane = threadIdx.x % LANES;
+  for (int g = g0 + (int)threadIdx.x / LANES; g - (int)(threadIdx.x & 31) / LANES <= g1; g += NT / LANES) use(g, lane);
+}
+// The groups of V features from i on.
+template <int V, class U>
+__device__ __forceinline__ void each_feature(const Fields& p, int i, U&& use) {
+  int g = i / p.group, r = i - g * p.group;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    use(e, g);
+    if (++r == p.group) {
+      r = 0;
+      ++g;
+    }
   }
 }
 
-// Calls run(f, a, b) for the fields' columns a .. b - 1 inside the tile, and none(f) for empty fields, each by one tile.
+// Calls run(f, a, b, begin, end) for the columns a .. b - 1 inside the tile of field f, begin .. end - 1, and none(f) for empty fields, each by one tile.
 template <class R, class E>
 __device__ __forceinline__ void each_field(const Fields& p, int t, R&& run, E&& none) {
   const int c0 = t * p.cols, c1 = min(p.T, c0 + p.cols);
@@ -123,7 +164,7 @@ __device__ __forceinline__ void each_field(const Fields& p, int t, R&& run, E&& 
     const int begin = field_begin(p, f), end = field_begin(p, f + 1);
     if (begin >= c1 && !last) break;
     const int a = max(begin, c0), b = min(end, c1);
-    if (a < b) run(f, a, b);
+    if (a < b) run(f, a, b, begin, end);
     else if (begin >= end && begin >= c0) none(f);
   }
 }
@@ -139,55 +180,37 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_stats(const T* X, int ld
   const int width = min(FW, p.D - i0);
   let_next_start();
   wait_for_previous();
-  each_field(p, t, [&](int f, int a, int b) {
+  each_field(p, t, [&](int f, int a, int b, int begin, int end) {
     float mean[V] = {}, m2[V] = {}, n = 0.0f;
     if (i < p.D) {
       constexpr int B = 4, P = V > 1 ? 2 : 1;
-      in_batches<B, TY, Raw<T, V>>(a + ty, b, [&](Raw<T, V>& raw, int j) { raw.load(X + (size_t)j * ldx + i); },
-                                   [&](const Raw<T, V>(&raw)[B], int j) {
-        if (j + (B - 1) * TY < b) {   // the batch's own mean and deviations, joined to what is there
-          float x[B][V];
+      const T* from = X + (size_t)(a + ty) * ldx + i;
+      in_batches<B, TY, Raw<T, V>>(a + ty, b, [&](Raw<T, V>& raw, int j) { raw.load(from + (size_t)j * ldx); },
+                                   [&](const auto& raw, int, auto count) {   // the batch's own mean and deviations, joined to what is there
+        constexpr int C = decltype(count)::value;
+        float x[C][V];
 #pragma unroll
-          for (int q = 0; q < B; ++q) raw[q].widen(x[q]);
-          const float w = __fdividef(B, n + B), nw = n * w;
-          n += B;
+        for (int q = 0; q < C; ++q) raw[q].widen(x[q]);
+        const float w = __fdividef(C, n + C), nw = n * w;
+        n += C;
 #pragma unroll
-          for (int e = 0; e < V; e += P) {
-            Floats<P> v[B], d2 = all_of<P>(0.0f), old;
+        for (int e = 0; e < V; e += P) {
+          Floats<P> d2 = all_of<P>(0.0f), minus = mul(pair_at(x[0], e), all_of<P>(-1.0f));   // the batch's mean, negative
+          if constexpr (C == 4) {
+            minus = mul(add(add(pair_at(x[0], e), pair_at(x[1], e)), add(pair_at(x[2], e), pair_at(x[3], e))), all_of<P>(-0.25f));
 #pragma unroll
-            for (int q = 0; q < B; ++q)
-#pragma unroll
-              for (int o = 0; o < P; ++o) v[q].x[o] = x[q][e + o];
-            const Floats<P> minus = mul(add(add(v[0], v[1]), add(v[2], v[3])), all_of<P>(-1.0f / B));   // the batch's mean
-#pragma unroll
-            for (int q = 0; q < B; ++q) {
-              const Floats<P> d = add(v[q], minus);
+            for (int q = 0; q < C; ++q) {
+              const Floats<P> d = add(pair_at(x[q], e), minus);
               d2 = fma(d, d, d2);
             }
-#pragma unroll
-            for (int o = 0; o < P; ++o) old.x[o] = mean[e + o];
-            const Floats<P> dev = add(minus, old), up = fma(dev, all_of<P>(-w), old), t = fma(mul(dev, all_of<P>(nw)), dev, d2);
-#pragma unroll
-            for (int o = 0; o < P; ++o) {
-              mean[e + o] = up.x[o];
-              m2[e + o] += t.x[o];
-            }
           }
-        } else {
+          const Floats<P> old = pair_at(mean, e), dev = add(minus, old), up = fma(dev, all_of<P>(-w), old);
+          const Floats<P> t = add(pair_at(m2, e), fma(mul(dev, all_of<P>(nw)), dev, d2));
 #pragma unroll
-          for (int q = 0; q < B - 1; ++q)
-            if (j + q * TY < b) {
-              float x[V];
-              raw[q].widen(x);
-              const float w = __fdividef(1.0f, n + 1.0f), nw = n * w;
-              n += 1.0f;
-#pragma unroll
-              for (int e = 0; e < V; ++e) {
-                const float d = x[e] - mean[e];
-                mean[e] = fmaf(d, w, mean[e]);
-                m2[e] = fmaf(d * nw, d, m2[e]);
-              }
-            }
+          for (int o = 0; o < P; ++o) {
+            mean[e + o] = up.x[o];
+            m2[e + o] = t.x[o];
+          }
         }
       });
     }
@@ -211,37 +234,32 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_stats(const T* X, int ld
     }
     __syncthreads();
     // features of a group have the same number of columns: their mean, and their deviations about it
-    const int lane = threadIdx.x & 31, g0 = i0 / p.group, g1 = (i0 + width - 1) / p.group;
-    for (int g = g0 + ((int)threadIdx.x >> 5); g <= g1; g += NT / 32) {
+    each_group(i0 / p.group, (i0 + width - 1) / p.group, [&](int g, int lane) {
       const int x0 = max(0, g * p.group - i0), x1 = min(width, (g + 1) * p.group - i0);
       float s = 0.0f, d2 = 0.0f;
-      const float at = feature[x0].x;
-      for (int x = x0 + lane; x < x1; x += 32) s += feature[x].x - at;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      const float m = at + s / (float)(x1 - x0);
-      for (int x = x0 + lane; x < x1; x += 32) {
+      const float at = x0 < x1 ? feature[x0].x : 0.0f;
+      for (int x = x0 + lane; x < x1; x += LANES) s += feature[x].x - at;
+      const float m = at + lanes_sum(s) / (float)(x1 - x0);
+      for (int x = x0 + lane; x < x1; x += LANES) {
         const float d = feature[x].x - m;
         d2 += fmaf(d * (float)(b - a), d, feature[x].y);
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) d2 += __shfl_xor_sync(0xffffffffu, d2, o);
-      if (lane == 0) part[share(p, t, f, fb, g)] = make_float2(m, d2);
-    }
+      d2 = lanes_sum(d2);
+      if (lane == 0 && x0 < x1) part[share(p, t, f, fb, g)] = make_float2(m, d2);
+    });
   }, [](int) {});
 }
 
-// The feature blocks and tiles that field f's group g is spread over, visited by a warp: get(share, columns, features).
+// The tiles and feature blocks that group g of the field in columns begin .. end - 1 is spread over, by LANES threads:
+// get(share, columns, features).
 template <int FW, class G>
-__device__ __forceinline__ void each_share(const Fields& p, int f, int g, G&& get) {
-  const int begin = field_begin(p, f), end = field_begin(p, f + 1);
-  const int t0 = begin / p.cols, nt = (end - 1) / p.cols - t0 + 1;
+__device__ __forceinline__ void each_share(const Fields& p, int f, int begin, int end, int t0, int t1, int g, int lane, G&& get) {
   const int i0 = g * p.group, i1 = i0 + p.group, b0 = i0 / FW, nb = (i1 - 1) / FW - b0 + 1;
-  const int total = nt * nb;   // at most the tiles of the matrix
-  for (int e = threadIdx.x & 31; e < total; e += 32) {
-    const int t = nb == 1 ? t0 + e : t0 + e / nb, fb = nb == 1 ? b0 : b0 + e % nb;
-    const int cols = min(end, (t + 1) * p.cols) - max(begin, t * p.cols), features = min(i1, (fb + 1) * FW) - max(i0, fb * FW);
-    get(share(p, t, f, fb, g), cols, features);
+  for (int fb = b0; fb < b0 + nb; ++fb) {
+    const int features = min(i1, (fb + 1) * FW) - max(i0, fb * FW);
+#pragma unroll 4
+    for (int t = t0 + lane; t <= t1; t += LANES)
+      get(share(p, t, f, fb, g), min(end, (t + 1) * p.cols) - max(begin, t * p.cols), features);
   }
 }
 
@@ -262,25 +280,27 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_apply(const T* X, int ld
     gm[e] = gamma && i < p.D ? gamma[i + e] : 1.0f;
     bt[e] = beta && i < p.D ? beta[i + e] : 0.0f;
   }
-  each_field(p, t, [&](int f, int a, int b) {
+  each_field(p, t, [&](int f, int a, int b, int begin, int end) {
     __syncthreads();
-    for (int g = g0 + ((int)threadIdx.x >> 5); g <= g1; g += NT / 32) {
+    const int t0 = begin / p.cols, t1 = (end - 1) / p.cols;
+    each_group(g0, g1, [&](int g, int lane) {
       // the mean about one share's mean, then the deviations about it
-      const int begin = field_begin(p, f);
-      const float n = (float)(field_begin(p, f + 1) - begin) * (float)p.group;
-      const float at = part[share(p, begin / p.cols, f, g * p.group / FW, g)].x;
+      const bool there = g <= g1;
+      const float n = (float)(end - begin) * (float)p.group;
+      const float at = there ? part[share(p, t0, f, g * p.group / FW, g)].x : 0.0f;
       float s = 0.0f, d2 = 0.0f;
-      each_share<FW>(p, f, g, [&](size_t k, int cols, int features) { s = fmaf(part[k].x - at, (float)cols * (float)features, s); });
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      const float mean = at + s / n;
-      each_share<FW>(p, f, g, [&](size_t k, int cols, int features) {
-        const float d = part[k].x - mean;
-        d2 += fmaf(d * ((float)cols * (float)features), d, part[k].y);
-      });
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) d2 += __shfl_xor_sync(0xffffffffu, d2, o);
-      if ((threadIdx.x & 31) == 0) {
+      if (there)
+        each_share<FW>(p, f, begin, end, t0, t1, g, lane,
+                       [&](size_t k, int cols, int features) { s = fmaf(part[k].x - at, (float)cols * (float)features, s); });
+      const float mean = at + lanes_sum(s) / n;
+      if (there)
+        each_share<FW>(p, f, begin, end, t0, t1, g, lane, [&](size_t k, int cols, int features) {
+          const float2 w = part[k];
+          const float d = w.x - mean;
+          d2 += fmaf(d * ((float)cols * (float)features), d, w.y);
+        });
+      d2 = lanes_sum(d2);
+      if (there && lane == 0) {
         const float r = 1.0f / sqrtf(d2 / n + eps);
         stat[g - g0] = make_float2(mean, r);
         if (mean_out && a == begin && g * p.group >= i0) {   // the tile with the group's first element
@@ -288,29 +308,34 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_apply(const T* X, int ld
           rstd_out[(size_t)f * lds + g] = r;
         }
       }
-    }
+    });
     __syncthreads();
     if (i < p.D) {
       float m[V], s[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float2 st = stat[(i + e) / p.group - g0];
-        m[e] = st.x;
+      each_feature<V>(p, i, [&](int e, int g) {
+        const float2 st = stat[min(g, g1) - g0];
+        m[e] = -st.x;
         s[e] = st.y * gm[e];
-      }
-      constexpr int B = 4;
-      in_batches<B, TY, Raw<T, V>>(a + ty, b, [&](Raw<T, V>& raw, int j) { raw.load(X + (size_t)j * ldx + i); },
-                                   [&](const Raw<T, V>(&raw)[B], int j) {
+      });
+      constexpr int B = 4, P = V > 1 ? 2 : 1;
+      // from the last column to the first: the last ones that the first look read are the likeliest to be in L2 still
+      const int last = a + ty < b ? b - 1 - (b - 1 - a - ty) % TY : 0;
+      const T* from = X + (size_t)last * ldx + i;
+      T* to = Y + (size_t)last * ldy + i;
+      in_batches<B, TY, Raw<T, V>>(a + ty, b, [&](Raw<T, V>& raw, int j) { raw.load(from - (size_t)j * ldx); },
+                                   [&](const auto& raw, int j, auto count) {
 #pragma unroll
-        for (int q = 0; q < B; ++q)
-          if (j + q * TY < b) {
-            float x[V];
-            raw[q].widen(x);
+        for (int q = 0; q < decltype(count)::value; ++q) {
+          float x[V];
+          raw[q].widen(x);
 #pragma unroll
-            for (int e = 0; e < V; ++e) x[e] = fmaf(x[e] - m[e], s[e], bt[e]);
-            activate_each<ACT, V>(x);
-            store<T, V>(Y + (size_t)(j + q * TY) * ldy + i, x);
+          for (int e = 0; e < V; e += P) {   // m is minus the mean
+            const Floats<P> z = activate<ACT, P>(fma(add(pair_at(x, e), pair_at(m, e)), pair_at(s, e), pair_at(bt, e)));
+#pragma unroll
+            for (int o = 0; o < P; ++o) x[e + o] = z.x[o];
           }
+          store<T, V>(to - (size_t)(j + q * TY) * ldy, x);
+        }
       });
     }
   }, [&](int f) {
@@ -318,6 +343,85 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_apply(const T* X, int ld
     for (int g = g0 + (int)threadIdx.x; g <= g1; g += NT)
       if (g * p.group >= i0) mean_out[(size_t)f * lds + g] = rstd_out[(size_t)f * lds + g] = 0.0f;
   });
+}
+
+// A block per field and group, where one that had all T columns would be small: one launch, and the second look at X finds it
+// in L1 or L2.  Threads: TX = group / V along features, the others along columns.
+template <class T, int V, int ACT>
+__global__ void __launch_bounds__(NT) k_gnorm_small(const T* X, int ldx, const Fields p, const float* gamma, const float* beta, float eps, T* Y,
+                                                    int ldy, float* mean_out, float* rstd_out, int lds) {
+  __shared__ float red[2][NT / 32];
+  let_next_start();
+  wait_for_previous();
+  const int g = blockIdx.x % p.groups, f = blockIdx.x / p.groups, i0 = g * p.group;
+  const int begin = field_begin(p, f), end = field_begin(p, f + 1), TX = p.group / V;
+  if (begin >= end) {
+    if (mean_out && threadIdx.x == 0) mean_out[(size_t)f * lds + g] = rstd_out[(size_t)f * lds + g] = 0.0f;
+    return;
+  }
+  const int total = (end - begin) * TX, step = NT / TX * TX;   // a thread keeps its features
+  const int tx = threadIdx.x % TX, first = threadIdx.x < step ? (int)threadIdx.x : total;
+  const auto at = [&](int e) { return (size_t)(begin + e / TX); };
+  const auto block_sum = [&](float x, int k) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if ((threadIdx.x & 31) == 0) red[k][threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = red[k][0];
+#pragma unroll
+    for (int w = 1; w < NT / 32; ++w) x += red[k][w];
+    return x;
+  };
+  const float shift = to_float(X[(size_t)begin * ldx + i0]), n = (float)(end - begin) * (float)p.group;
+  float s = 0.0f, d2 = 0.0f;
+#pragma unroll 4
+  for (int e = first; e < total; e += step) {
+    Raw<T, V> raw;
+    raw.load(X + at(e) * ldx + i0 + tx * V);
+    float x[V];
+    raw.widen(x);
+#pragma unroll
+    for (int q = 0; q < V; ++q) s += x[q] - shift;
+  }
+  const float mean = shift + block_sum(s, 0) / n;
+#pragma unroll 4
+  for (int e = first; e < total; e += step) {
+    Raw<T, V> raw;
+    raw.load(X + at(e) * ldx + i0 + tx * V);
+    float x[V];
+    raw.widen(x);
+#pragma unroll
+    for (int q = 0; q < V; ++q) d2 = fmaf(x[q] - mean, x[q] - mean, d2);
+  }
+  const float r = 1.0f / sqrtf(block_sum(d2, 1) / n + eps);
+  if (mean_out && threadIdx.x == 0) {
+    mean_out[(size_t)f * lds + g] = mean;
+    rstd_out[(size_t)f * lds + g] = r;
+  }
+  float sc[V], bt[V];
+#pragma unroll
+  for (int q = 0; q < V; ++q) {
+    const int i = i0 + tx * V + q;
+    sc[q] = gamma ? r * gamma[i] : r;
+    bt[q] = beta ? beta[i] : 0.0f;
+  }
+  constexpr int B = 4;
+  for (int e = first; e < total; e += B * step) {
+    Raw<T, V> raw[B];
+#pragma unroll
+    for (int k = 0; k < B; ++k)
+      if (e + k * step < total) raw[k].load(X + at(e + k * step) * ldx + i0 + tx * V);
+#pragma unroll
+    for (int k = 0; k < B; ++k)
+      if (e + k * step < total) {
+        float x[V];
+        raw[k].widen(x);
+#pragma unroll
+        for (int q = 0; q < V; ++q) x[q] = fmaf(x[q] - mean, sc[q], bt[q]);
+        activate_each<ACT, V>(x);
+        store<T, V>(Y + at(e + k * step) * ldy + i0 + tx * V, x);
+      }
+  }
 }
 
 // ---------------------------------------------------------------- backward
@@ -342,35 +446,34 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_sums(const T* X, int ldx
     gm[e] = gamma && i < p.D ? gamma[i + e] : 1.0f;
     bt[e] = beta && i < p.D ? beta[i + e] : 0.0f;
   }
-  each_field(p, t, [&](int f, int a, int b) {
+  each_field(p, t, [&](int f, int a, int b, int begin, int end) {
     float sb[V] = {}, sg[V] = {};
     if (i < p.D) {
       float m[V], r[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const size_t at = (size_t)f * lds + (i + e) / p.group;
+      each_feature<V>(p, i, [&](int e, int g) {
+        const size_t at = (size_t)f * lds + min(g, p.groups - 1);
         m[e] = mean[at];
         r[e] = rstd[at];
-      }
+      });
       constexpr int B = sizeof(T) == 2 ? 4 : 2;
+      const T *xs = X + (size_t)(a + ty) * ldx + i, *ds = dY + (size_t)(a + ty) * lddy + i;
       in_batches<B, TY, Pair<T, V>>(a + ty, b, [&](Pair<T, V>& raw, int j) {
-        raw.x.load(X + (size_t)j * ldx + i);
-        raw.d.load(dY + (size_t)j * lddy + i);
-      }, [&](const Pair<T, V>(&raw)[B], int j) {
+        raw.x.load(xs + (size_t)j * ldx);
+        raw.d.load(ds + (size_t)j * lddy);
+      }, [&](const auto& raw, int j, auto count) {
 #pragma unroll
-        for (int q = 0; q < B; ++q)
-          if (j + q * TY < b) {
-            float x[V], d[V];
-            raw[q].x.widen(x);
-            raw[q].d.widen(d);
+        for (int q = 0; q < decltype(count)::value; ++q) {
+          float x[V], d[V];
+          raw[q].x.widen(x);
+          raw[q].d.widen(d);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-              const float h = __fmul_rn(x[e] - m[e], r[e]);
-              if (ACT != CR_ACT_NONE) d[e] = __fmul_rn(d[e], activation_slope<ACT>(fmaf(h, gm[e], bt[e])));
-              sb[e] += d[e];
-              sg[e] = fmaf(d[e], h, sg[e]);
-            }
+          for (int e = 0; e < V; ++e) {
+            const float h = __fmul_rn(x[e] - m[e], r[e]);
+            if (ACT != CR_ACT_NONE) d[e] = __fmul_rn(d[e], activation_slope<ACT>(fmaf(h, gm[e], bt[e])));
+            sb[e] += d[e];
+            sg[e] = fmaf(d[e], h, sg[e]);
           }
+        }
       });
     }
     __syncthreads();
@@ -389,22 +492,18 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_sums(const T* X, int ldx
     }
     __syncthreads();
     if (part) {
-      const int lane = threadIdx.x & 31, g0 = i0 / p.group, g1 = (i0 + width - 1) / p.group;
-      for (int g = g0 + ((int)threadIdx.x >> 5); g <= g1; g += NT / 32) {
+      each_group(i0 / p.group, (i0 + width - 1) / p.group, [&](int g, int lane) {
         const int x0 = max(0, g * p.group - i0), x1 = min(width, (g + 1) * p.group - i0);
         float2 s = make_float2(0.0f, 0.0f);
-        for (int x = x0 + lane; x < x1; x += 32) {
+        for (int x = x0 + lane; x < x1; x += LANES) {
           const float w = gamma ? gamma[i0 + x] : 1.0f;
           s.x = fmaf(w, feature[x].x, s.x);
           s.y = fmaf(w, feature[x].y, s.y);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
-          s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
-        }
-        if (lane == 0) part[share(p, t, f, fb, g)] = s;
-      }
+        s.x = lanes_sum(s.x);
+        s.y = lanes_sum(s.y);
+        if (lane == 0 && x0 < x1) part[share(p, t, f, fb, g)] = s;
+      });
     }
   }, [](int) {});
   __syncthreads();
@@ -432,53 +531,54 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_dx(const T* X, int ldx, 
     gm[e] = gamma && i < p.D ? gamma[i + e] : 1.0f;
     bt[e] = beta && i < p.D ? beta[i + e] : 0.0f;
   }
-  each_field(p, t, [&](int f, int a, int b) {
+  each_field(p, t, [&](int f, int a, int b, int begin, int end) {
     __syncthreads();
-    for (int g = g0 + ((int)threadIdx.x >> 5); g <= g1; g += NT / 32) {
+    const int t0 = begin / p.cols, t1 = (end - 1) / p.cols;
+    each_group(g0, g1, [&](int g, int lane) {
       float2 s = make_float2(0.0f, 0.0f);
-      each_share<FW>(p, f, g, [&](size_t k, int, int) {
-        s.x += part[k].x;
-        s.y += part[k].y;
-      });
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
-        s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
-      }
-      const float n = (float)(field_begin(p, f + 1) - field_begin(p, f)) * (float)p.group;
-      if ((threadIdx.x & 31) == 0) stat[g - g0] = make_float2(s.x / n, s.y / n);
-    }
+      if (g <= g1)
+        each_share<FW>(p, f, begin, end, t0, t1, g, lane, [&](size_t k, int, int) {
+          const float2 w = part[k];
+          s.x += w.x;
+          s.y += w.y;
+        });
+      s.x = lanes_sum(s.x);
+      s.y = lanes_sum(s.y);
+      const float n = (float)(end - begin) * (float)p.group;
+      if (lane == 0 && g <= g1) stat[g - g0] = make_float2(s.x / n, s.y / n);
+    });
     __syncthreads();
     if (i < p.D) {
       float m[V], r[V], c1[V], c2[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const int g = (i + e) / p.group;
-        const size_t at = (size_t)f * lds + g;
+      each_feature<V>(p, i, [&](int e, int g) {
+        const int k = min(g, g1);
+        const size_t at = (size_t)f * lds + k;
         m[e] = mean[at];
         r[e] = rstd[at];
-        c1[e] = stat[g - g0].x;
-        c2[e] = stat[g - g0].y;
-      }
+        c1[e] = stat[k - g0].x;
+        c2[e] = stat[k - g0].y;
+      });
       constexpr int B = sizeof(T) == 2 ? 4 : 2;
+      const int last = a + ty < b ? b - 1 - (b - 1 - a - ty) % TY : 0;   // from the last column to the first, as k_gnorm_apply
+      const T *xs = X + (size_t)last * ldx + i, *ds = dY + (size_t)last * lddy + i;
+      T* to = dX + (size_t)last * lddx + i;
       in_batches<B, TY, Pair<T, V>>(a + ty, b, [&](Pair<T, V>& raw, int j) {
-        raw.x.load(X + (size_t)j * ldx + i);
-        raw.d.load(dY + (size_t)j * lddy + i);
-      }, [&](const Pair<T, V>(&raw)[B], int j) {
+        raw.x.load(xs - (size_t)j * ldx);
+        raw.d.load(ds - (size_t)j * lddy);
+      }, [&](const auto& raw, int j, auto count) {
 #pragma unroll
-        for (int q = 0; q < B; ++q)
-          if (j + q * TY < b) {
-            float x[V], d[V];
-            raw[q].x.widen(x);
-            raw[q].d.widen(d);
+        for (int q = 0; q < decltype(count)::value; ++q) {
+          float x[V], d[V];
+          raw[q].x.widen(x);
+          raw[q].d.widen(d);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-              const float h = __fmul_rn(x[e] - m[e], r[e]);
-              if (ACT != CR_ACT_NONE) d[e] = __fmul_rn(d[e], activation_slope<ACT>(fmaf(h, gm[e], bt[e])));
-              x[e] = __fmul_rn(r[e], fmaf(-h, c2[e], fmaf(d[e], gm[e], -c1[e])));
-            }
-            store<T, V>(dX + (size_t)(j + q * TY) * lddx + i, x);
+          for (int e = 0; e < V; ++e) {
+            const float h = __fmul_rn(x[e] - m[e], r[e]);
+            if (ACT != CR_ACT_NONE) d[e] = __fmul_rn(d[e], activation_slope<ACT>(fmaf(h, gm[e], bt[e])));
+            x[e] = __fmul_rn(r[e], fmaf(-h, c2[e], fmaf(d[e], gm[e], -c1[e])));
           }
+          store<T, V>(to - (size_t)(j + q * TY) * lddx, x);
+        }
       });
     }
   }, [](int) {});
@@ -488,15 +588,16 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_dx(const T* X, int ldx, 
 bool aligned(const void* p, int ld, int eb, int bytes) { return ((uintptr_t)p & (bytes - 1)) == 0 && (long long)ld * eb % bytes == 0; }
 
 // Calls f(TX, V) for a matrix of D features, V of them to a thread (1 where 16-byte or, for V = 4 of 16-bit types, 8-byte accesses do
-// not apply): the widest of 32, 16 and 8 threads along them that leaves least unused.
+// not apply): the widest of 32, 16 and 8 threads along them that leaves least unused (64 and 128 threads,
+// which read whole rows, are no faster: 142 to 148 us for eight fields of 16384 x 1024).
 template <int V, class F>
 cr_status with_tile(int D, bool vec, F&& f) {
   using std::integral_constant;
   if (!vec) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-  const auto padded = [&](int w) { return (D + w - 1) / w * w; };
-  const int best = std::min({padded(32 * V), padded(16 * V), padded(8 * V)});
-  if (padded(32 * V) == best) return f(integral_constant<int, 32>{}, integral_constant<int, V>{});
-  if (padded(16 * V) == best) return f(integral_constant<int, 16>{}, integral_constant<int, V>{});
+  const auto padded = [&](int w) { return (D + w * V - 1) / (w * V) * (w * V); };
+  const int best = padded(8);
+  if (padded(32) == best) return f(integral_constant<int, 32>{}, integral_constant<int, V>{});
+  if (padded(16) == best) return f(integral_constant<int, 16>{}, integral_constant<int, V>{});
   return f(integral_constant<int, 8>{}, integral_constant<int, V>{});
 }
 
@@ -555,6 +656,27 @@ extern "C" cr_status cr_group_norm(int type, const void* d_X, int ldx, int D, in
     using E = decltype(t0);
     constexpr int EB = sizeof(E), W = 16 / EB;
     const bool vec = D % W == 0 && aligned(d_X, ldx, EB, 16) && aligned(d_Y, ldy, EB, 16);
+    const int group = D / groups;
+    if ((long long)T * (vec && group % W == 0 ? group / W : group) <= SMALL * NT && (long long)n * groups <= 8 * sm_count() && group <= NT) {
+      Fields p = {};
+      p.off = d_off;
+      p.n = n;
+      p.T = T;
+      p.D = D;
+      p.groups = groups;
+      p.group = D / groups;
+      return with_act(act, [&](auto a0) -> cr_status {
+        constexpr int ACT = decltype(a0)::value;
+        TimedScope ts("k_gnorm_small", stream);
+        const auto go = [&](auto v0) {
+          return launch_after(k_gnorm_small<E, decltype(v0)::value, ACT>, (unsigned)(n * groups), NT, 0, 1, stream, (const E*)d_X, ldx, p, d_gamma,
+                              d_beta, (float)eps, (E*)d_Y, ldy, d_mean, d_rstd, lds);
+        };
+        CR_CUDA(vec && p.group % W == 0 ? go(std::integral_constant<int, W>{}) : go(std::integral_constant<int, 1>{}));
+        CR_CHECK_LAUNCH("k_gnorm_small");
+        return CR_OK;
+      });
+    }
     return with_tile<W>(D, vec, [&](auto tx0, auto v0) -> cr_status {
       constexpr int TX = decltype(tx0)::value, V = decltype(v0)::value;
       const Fields p = make_fields(d_off, n_field, T, D, groups, TX * V, NT / TX);
