@@ -204,12 +204,13 @@ int sm_count() {
   return n;
 }
 
-cr_status allow_shared(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+cr_status allow_shared(const void* kernel, int bytes, std::atomic<uint64_t>& done, bool large_clusters) {
   int dev = 0;
   CR_CUDA(cudaGetDevice(&dev));
   if (dev < 0 || dev >= 64) return fail_literal(CR_ERR_CUDA, "device number above 63");
   if (done.load(std::memory_order_acquire) >> dev & 1) return CR_OK;
   CR_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  if (large_clusters) CR_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
   done.fetch_or((uint64_t)1 << dev, std::memory_order_release);
   return CR_OK;
 }

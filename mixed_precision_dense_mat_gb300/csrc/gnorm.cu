@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_dx(const T* X, int ldx, 
 bool aligned(const void* p, int ld, int eb, int bytes) { return ((uintptr_t)p & (bytes - 1)) == 0 && (long long)ld * eb % bytes == 0; }
 
 // Calls f(TX, V) for a matrix of D features, V of them to a thread (1 where 16-byte or, for V = 4 of 16-bit types, 8-byte accesses do
-// not apply): the widest of 32, 16 and 8 threads along them that leaves least unused (64 and 128 threads,
+// not apply): the widest of 32, 16 and 8 threads along them that leaves little unused (64 and 128 threads,
 // which read whole rows, are no faster: 142 to 148 us for eight fields of 16384 x 1024).
 template <int V, class F>
 cr_status with_tile(int D, bool vec, F&& f) {
@@ -596,7 +596,7 @@ cr_status with_tile(int D, bool vec, F&& f) {
   if (!vec) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
   const auto padded = [&](int w) { return (D + w * V - 1) / (w * V) * (w * V); };
   const int best = padded(8);
-  if (padded(32) == best) return f(integral_constant<int, 32>{}, integral_constant<int, V>{});
+  if (16ll * padded(32) <= 17ll * best) return f(integral_constant<int, 32>{}, integral_constant<int, V>{});
   if (padded(16) == best) return f(integral_constant<int, 16>{}, integral_constant<int, V>{});
   return f(integral_constant<int, 8>{}, integral_constant<int, V>{});
 }

@@ -30,8 +30,8 @@ cr_status make_tensor_map_2d_plain(CUtensorMap* tm, int type, const void* base, 
 int sm_count();
 
 // Lets a kernel have `bytes` of dynamic shared memory, the same number at every call: once per kernel (which `done`
-// belongs to) and device, so that host threads do not take it from one another.
-cr_status allow_shared(const void* kernel, int bytes, std::atomic<uint64_t>& done);
+// belongs to) and device, so that host threads do not take it from one another.  large_clusters: clusters of more than 8 too.
+cr_status allow_shared(const void* kernel, int bytes, std::atomic<uint64_t>& done, bool large_clusters = false);
 
 // total[D] = the sum of the rows of part (rows x D, row-major), in a fixed order.
 cr_status add_rows(const float* part, int rows, int D, float* total, cudaStream_t stream);

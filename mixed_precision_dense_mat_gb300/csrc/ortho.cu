@@ -20,6 +20,35 @@ constexpr int MAXPART = 1024;
 struct Squares {
   double big, mid, small;
 };
+__device__ __forceinline__ void add_square(float x, float& big, float& mid, float& small) {
+  const float a = fabsf(x);
+  const bool high = a > 0x1p50f, low = a < 0x1p-50f;
+  const float y = high ? a * 0x1p-90f : low ? a * 0x1p90f : a;
+  if (high) big = fmaf(y, y, big);
+  else if (low) small = fmaf(y, y, small);
+  else mid = fmaf(y, y, mid);
+}
+__device__ __forceinline__ Squares warp_sum(Squares s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s.big += __shfl_xor_sync(0xffffffffu, s.big, o);
+    s.mid += __shfl_xor_sync(0xffffffffu, s.mid, o);
+    s.small += __shfl_xor_sync(0xffffffffu, s.small, o);
+  }
+  return s;
+}
+// X = ((g f[1]) f[2]) f[0] is UNIT g / |G|_F, zero for a zero matrix and NaN where |G|_F is not finite: UNIT / |G|_F is m 2^e, and 2^e
+// is applied in two halves that are normal numbers.
+__device__ __forceinline__ void scale_of(const Squares& s, float* f) {
+  const double norm = sqrt(s.big * 0x1p180 + s.mid + s.small * 0x1p-180);
+  int e = 0;
+  double m = 0.0;
+  if (norm > 0.0 && norm < 1e300) m = frexp((double)UNIT / norm, &e);
+  else if (norm != 0.0) m = norm - norm;   // NaN
+  f[0] = (float)m;
+  f[1] = (float)ldexp(1.0, e / 2);
+  f[2] = (float)ldexp(1.0, e - e / 2);
+}
 template <class T, int V>
 __global__ void __launch_bounds__(NT) k_ortho_norm(const T* G, int ld, int K, int N, Squares* part) {
   __shared__ Squares red[NT / 32];
@@ -34,22 +63,9 @@ __global__ void __launch_bounds__(NT) k_ortho_norm(const T* G, int ld, int K, in
     if constexpr (V == 8) widen8(*reinterpret_cast<const Eight<T>*>(from), x);
     else x[0] = to_float(from[0]);
 #pragma unroll
-    for (int q = 0; q < V; ++q) {
-      const float a = fabsf(x[q]);
-      const bool high = a > 0x1p50f, low = a < 0x1p-50f;
-      const float y = high ? a * 0x1p-90f : low ? a * 0x1p90f : a;
-      if (high) big = fmaf(y, y, big);
-      else if (low) small = fmaf(y, y, small);
-      else mid = fmaf(y, y, mid);
-    }
+    for (int q = 0; q < V; ++q) add_square(x[q], big, mid, small);
   }
-  Squares s = {big, mid, small};
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    s.big += __shfl_xor_sync(0xffffffffu, s.big, o);
-    s.mid += __shfl_xor_sync(0xffffffffu, s.mid, o);
-    s.small += __shfl_xor_sync(0xffffffffu, s.small, o);
-  }
+  Squares s = warp_sum(Squares{big, mid, small});
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -62,8 +78,7 @@ __global__ void __launch_bounds__(NT) k_ortho_norm(const T* G, int ld, int K, in
   }
 }
 
-// X = UNIT G / |G|_F, zero for a zero matrix and NaN where |G|_F is not finite, as FP16 with the rest after it in X2 (may
-// be NULL).  UNIT / |G|_F is m 2^e, and 2^e is applied in two halves that are normal numbers.
+// X = UNIT G / |G|_F as FP16 with the rest after it in X2 (may be NULL).
 template <class T, int V>
 __global__ void __launch_bounds__(NT) k_ortho_scale(const T* G, int ld, int K, int N, const Squares* part, int parts, __half* X, __half* X2, int ldx) {
   __shared__ float factor[3];
@@ -74,22 +89,8 @@ __global__ void __launch_bounds__(NT) k_ortho_scale(const T* G, int ld, int K, i
       s.mid += part[q].mid;
       s.small += part[q].small;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      s.big += __shfl_xor_sync(0xffffffffu, s.big, o);
-      s.mid += __shfl_xor_sync(0xffffffffu, s.mid, o);
-      s.small += __shfl_xor_sync(0xffffffffu, s.small, o);
-    }
-    if (threadIdx.x == 0) {
-      const double norm = sqrt(s.big * 0x1p180 + s.mid + s.small * 0x1p-180);
-      int e = 0;
-      double m = 0.0;
-      if (norm > 0.0 && norm < 1e300) m = frexp((double)UNIT / norm, &e);
-      else if (norm != 0.0) m = norm - norm;   // NaN
-      factor[0] = (float)m;
-      factor[1] = (float)ldexp(1.0, e / 2);
-      factor[2] = (float)ldexp(1.0, e - e / 2);
-    }
+    s = warp_sum(s);
+    if (threadIdx.x == 0) scale_of(s, factor);
   }
   __syncthreads();
   const float m = factor[0], p1 = factor[1], p2 = factor[2];
@@ -235,6 +236,377 @@ cr_status start(const T* G, int ld, int K, int N, Squares* part, const Split& X,
   return vec ? go(std::integral_constant<int, 8>{}) : go(std::integral_constant<int, 1>{});
 }
 
+// ---------------------------------------------------------------- small matrices
+// Up to 128 rows on the short side: one cluster does all steps.  Each CTA keeps a slab of the long side's columns n of X (L,
+// a multiple of 128) in shared memory, [i / 64][n][i % 64] in the 128-byte swizzle, which the tensor cores read as rows i with
+// k = n (A = X X^T) and as rows n with k = i (X^T B).  The CTAs' parts of A are joined through shared memory of the cluster, in
+// the order of the CTAs: each sums the rows that it owns and hands them to all.  B takes A's place, X' X's.
+// Bound by the chain of products, exchanges and barriers (a step takes about 3 us with one CTA): launched separately, the 16
+// kernels of five steps take 160 us.
+constexpr int SROWS = 128, STHREADS = 256, SCLUSTER = 16;
+constexpr int SA = SROWS * SROWS * 2;   // bytes of A's FP16 part, [j / 64][i][j % 64]
+constexpr int SPARTS = 64 * 1024;       // A's two parts, or the FP32 sums of this CTA
+struct SmallBars {
+  uint64_t product, block[4];
+  uint32_t tmem;
+  double sums[SCLUSTER][3], warps[STHREADS / 32][3];
+  float factor[3];
+};
+struct Small {
+  const void* G;
+  int ldg, K, N, steps, L, ncta;
+  float a, b, c;
+  void* O;
+  int ldo;
+  unsigned long long limit;
+  int* err;
+};
+__host__ __device__ constexpr int small_smem(int L, bool pairs) { return 1024 + L * SROWS * 2 * (pairs ? 2 : 1) + SPARTS + (int)sizeof(SmallBars); }
+
+__device__ __forceinline__ void fence_proxies() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_cluster2(uint32_t addr, uint32_t x, uint32_t y) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
+// Descriptor of a rows-contiguous operand whose 64-row blocks are `stride` bytes apart (tile_desc's are ATOM apart).
+__device__ __forceinline__ uint64_t rows_desc(uint32_t saddr, int stride) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(stride >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// Byte of element col (a multiple of 8 for 16-byte accesses) of a 64-element row in the 128-byte swizzle.
+__device__ __forceinline__ int swizzled(int row, int col) { return row * 128 + (((col >> 3) ^ (row & 7)) << 4) + (col & 7) * 2; }
+
+// v to FP16, what is left to a second one.
+template <bool PAIRS>
+__device__ __forceinline__ void put8(uint8_t* hi, int lo, int at, float (&v)[8]) {
+  const Eight<__half> h = narrow8<__half>(v);
+  *reinterpret_cast<Eight<__half>*>(hi + at) = h;
+  if (PAIRS) {
+    float w[8];
+    widen8(h, w);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] -= w[q];
+    *reinterpret_cast<Eight<__half>*>(hi + lo + at) = narrow8<__half>(v);
+  }
+}
+template <bool PAIRS>
+__device__ __forceinline__ void get8(const uint8_t* hi, int lo, int at, float (&v)[8]) {
+  widen8(*reinterpret_cast<const Eight<__half>*>(hi + at), v);
+  if (PAIRS) {
+    float w[8];
+    widen8(*reinterpret_cast<const Eight<__half>*>(hi + lo + at), w);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] += w[q];
+  }
+}
+
+template <class T, class O, bool PAIRS>
+__global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int L = p.L, half = L * 128, xlo = 2 * half;   // bytes of 64 rows of X, of a part of X
+  uint8_t *X = smem, *A = X + (PAIRS ? 2 : 1) * xlo;
+  SmallBars* bars = reinterpret_cast<SmallBars*>(A + SPARTS);
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = p.ncta > 1 ? (int)cluster_rank() : 0;
+  const bool wide = p.K <= p.N;
+  const int s = wide ? p.K : p.N, l = wide ? p.N : p.K, n0 = rank * L, cols = max(0, min(L, l - n0));
+  const uint32_t tcols = L <= 128 ? 128 : L <= 256 ? 256 : 512;
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->product, 1);
+    for (int m = 0; m < 4; ++m) mbar_init(&bars->block[m], 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(&bars->tmem, tcols);
+  if (p.ncta > 1) cluster_arrive_relaxed();   // waited for before the first access to another CTA
+  for (int e = threadIdx.x; e < (PAIRS ? 2 : 1) * xlo / 16; e += STHREADS) reinterpret_cast<uint4*>(X)[e] = make_uint4(0, 0, 0, 0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem, 0);
+  wait_for_previous();
+  let_next_start();
+  const auto together = [&] {   // all threads of the cluster
+    if (p.ncta > 1) cluster_sync_all();
+    else __syncthreads();
+  };
+
+  // G's elements of the slab: lanes along its columns, warps across them; twice, the second time from L1 or L2.
+  const T* G = (const T*)p.G + (wide ? (size_t)n0 * p.ldg : n0);
+  const int inner = wide ? s : cols, outer = wide ? cols : s;
+  {
+    float big = 0.0f, mid = 0.0f, small = 0.0f;
+    for (int x = lane; x < inner; x += 32)
+#pragma unroll 8
+      for (int y = warp; y < outer; y += STHREADS / 32) add_square(to_float(G[(size_t)y * p.ldg + x]), big, mid, small);
+    Squares sum = warp_sum(Squares{big, mid, small});
+    if (lane == 0) {
+      bars->warps[warp][0] = sum.big;
+      bars->warps[warp][1] = sum.mid;
+      bars->warps[warp][2] = sum.small;
+    }
+    __syncthreads();
+    if (threadIdx.x < 3) {
+      double x = 0.0;
+      for (int w = 0; w < STHREADS / 32; ++w) x += bars->warps[w][threadIdx.x];
+      bars->sums[rank][threadIdx.x] = x;
+    }
+    if (p.ncta > 1) {
+      cluster_wait();
+      __syncthreads();
+      if ((int)threadIdx.x < 3 * p.ncta) {   // to every CTA
+        const double x = bars->sums[rank][threadIdx.x % 3];
+        const uint32_t to = cluster_addr(smem_u32(&bars->sums[rank][threadIdx.x % 3]), threadIdx.x / 3);
+        if ((int)threadIdx.x / 3 != rank) asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(x) : "memory");
+      }
+    }
+    together();
+    if (threadIdx.x == 0) {
+      Squares all = {0.0, 0.0, 0.0};
+      for (int r = 0; r < p.ncta; ++r) {
+        all.big += bars->sums[r][0];
+        all.mid += bars->sums[r][1];
+        all.small += bars->sums[r][2];
+      }
+      scale_of(all, bars->factor);
+    }
+    __syncthreads();
+    const float m = bars->factor[0], p1 = bars->factor[1], p2 = bars->factor[2];
+    for (int x = lane; x < inner; x += 32)
+#pragma unroll 8
+      for (int y = warp; y < outer; y += STHREADS / 32) {
+        const float v = to_float(G[(size_t)y * p.ldg + x]) * p1 * p2 * m;
+        const int i = wide ? x : y, n = wide ? y : x, at = i / 64 * half + swizzled(n, i % 64);
+        const __half hi = __float2half_rn(v);
+        *reinterpret_cast<__half*>(X + at) = hi;
+        if (PAIRS) *reinterpret_cast<__half*>(X + xlo + at) = __float2half_rn(v - __half2float(hi));
+      }
+  }
+  fence_proxies();
+  __syncthreads();
+
+  const uint32_t rows_id = idesc_of(128, 128, false, true, true), k_id = idesc_of(128, 128, false, false, false);
+  const uint32_t sx = smem_u32(X), sa = smem_u32(A);
+  constexpr int SEGS = PAIRS ? 3 : 1;
+  // parts of the first and second operand, the small products first
+  const auto first_lo = [](int seg) { return PAIRS && seg == 1; };
+  const auto second_lo = [](int seg) { return PAIRS && seg == 0; };
+  uint32_t turn = 0;
+  const auto landed = [&](uint64_t* bar, uint32_t parity) {   // MMAs need nobody's help: late ones are reported, and waited for
+    if (!mbar_wait(bar, parity, p.limit)) {
+      *(volatile int*)p.err = 1;
+      __threadfence_system();
+      mbar_wait(bar, parity, LANDING_NS);
+    }
+    tc_fence_after();
+    __syncwarp();
+  };
+  const float unit = 1.0f / UNIT;
+  const int quad = warp & 3, side = warp >> 2, row = quad * 32 + lane;   // TMEM lane, and which 64 columns
+  for (int step = 0; step < p.steps; ++step) {
+    // A's part of this slab
+    if (warp == 0 && elect_one()) {
+      const uint64_t d0 = rows_desc(sx, half);
+      const int ks = max(1, (cols + 15) / 16);   // columns that are not there are zero
+      for (int seg = 0; seg < SEGS; ++seg) {
+        const uint64_t da = d0 + (first_lo(seg) ? xlo >> 4 : 0), db = d0 + (second_lo(seg) ? xlo >> 4 : 0);
+        for (int k = 0; k < ks; ++k) mma_any<false, false>(tmem, da + k * 128, db + k * 128, rows_id, (seg | k) != 0);
+      }
+      mma_commit(&bars->product);
+    }
+    __syncwarp();
+    landed(&bars->product, turn);
+    turn ^= 1;
+    {
+      uint32_t u[2][32];
+      tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + side * 64, u[0]);
+      tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + side * 64 + 32, u[1]);
+      tmem_ld_wait();
+      const float* v = reinterpret_cast<const float*>(u);
+      if (p.ncta == 1) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          float w[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) w[x] = v[8 * q + x] * unit;
+          put8<PAIRS>(A, SA, side * SA / 2 + swizzled(row, 8 * q), w);
+        }
+      } else {   // 16-byte word w of row i at w ^ (i & 31)
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          *reinterpret_cast<float4*>(A + row * 512 + (((side * 16 + q) ^ (row & 31)) << 4)) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+      }
+    }
+    if (p.ncta > 1) {
+      cluster_sync_all();
+      const int own = SROWS / p.ncta, words = own * 32 / STHREADS;   // rows, and 16-byte words of a thread (1 to 8; ncta is 2 to 16)
+      float4 sum[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < words) {
+          const int e = threadIdx.x + q * STHREADS, i = rank * own + e / 32, w = e % 32;
+          const uint32_t at = sa + i * 512 + ((w ^ (i & 31)) << 4);
+          float4 z = make_float4(0, 0, 0, 0);
+          for (int r = 0; r < p.ncta; ++r) {
+            const float4 x = load_cluster4(cluster_addr(at, r));
+            z.x += x.x;
+            z.y += x.y;
+            z.z += x.z;
+            z.w += x.w;
+          }
+          sum[q] = z;
+        }
+      cluster_sync_all();   // the sums have been read: A may take their place
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < words) {
+          const int e = threadIdx.x + q * STHREADS, i = rank * own + e / 32, j = e % 32 * 4;
+          const int at = j / 64 * (SA / 2) + swizzled(i, j % 64);
+          const float v[4] = {sum[q].x * unit, sum[q].y * unit, sum[q].z * unit, sum[q].w * unit};
+          const uint32_t h0 = narrow2(v[0], v[1], __half{}), h1 = narrow2(v[2], v[3], __half{});
+          uint32_t l0 = 0, l1 = 0;
+          if (PAIRS) {
+            const float2 f0 = widen2(h0, __half{}), f1 = widen2(h1, __half{});
+            l0 = narrow2(v[0] - f0.x, v[1] - f0.y, __half{});
+            l1 = narrow2(v[2] - f1.x, v[3] - f1.y, __half{});
+          }
+          for (int r = 0; r < p.ncta; ++r) {
+            store_cluster2(cluster_addr(sa + at, r), h0, h1);
+            if (PAIRS) store_cluster2(cluster_addr(sa + SA + at, r), l0, l1);
+          }
+        }
+    }
+    fence_proxies();
+    tc_fence_before();
+    together();
+    tc_fence_after();
+    fence_proxies();
+    // A A
+    if (warp == 0 && elect_one()) {
+      const uint64_t d0 = tile_desc(sa, true);
+      for (int seg = 0; seg < SEGS; ++seg) {
+        const uint64_t da = d0 + (first_lo(seg) ? SA >> 4 : 0), db = d0 + (second_lo(seg) ? SA >> 4 : 0);
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t at = (k / 4 * (SA / 2) >> 4) + k % 4 * 2;
+          mma_any<false, false>(tmem, da + at, db + at, k_id, (seg | k) != 0);
+        }
+      }
+      mma_commit(&bars->product);
+    }
+    __syncwarp();
+    landed(&bars->product, turn);
+    turn ^= 1;
+    {   // B in A's place
+      uint32_t u[2][32];
+      tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + side * 64, u[0]);
+      tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + side * 64 + 32, u[1]);
+      tmem_ld_wait();
+      const float* v = reinterpret_cast<const float*>(u);
+      const float c = p.c * unit;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        float w[8];
+        const int at = side * SA / 2 + swizzled(row, 8 * q);
+        get8<PAIRS>(A, SA, at, w);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) w[x] = fmaf(p.b, w[x], c * v[8 * q + x]);
+        put8<PAIRS>(A, SA, at, w);
+      }
+    }
+    fence_proxies();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // X^T B, 128 columns of X at a time
+    const int blocks = max(1, (cols + 127) / 128);
+    if (warp == 0 && elect_one()) {
+      const uint64_t dx = tile_desc(sx, true), d0 = tile_desc(sa, true);
+      for (int m = 0; m < blocks; ++m) {
+        for (int seg = 0; seg < SEGS; ++seg) {
+          const uint64_t da = dx + (first_lo(seg) ? xlo >> 4 : 0) + m * (128 * 128 >> 4), db = d0 + (second_lo(seg) ? SA >> 4 : 0);
+          for (int k = 0; k < 8; ++k)
+            mma_any<false, false>(tmem + m * 128, da + (k / 4 * half >> 4) + k % 4 * 2, db + (k / 4 * (SA / 2) >> 4) + k % 4 * 2, k_id, (seg | k) != 0);
+        }
+        mma_commit(&bars->block[m]);
+      }
+    }
+    __syncwarp();
+    const bool last = step + 1 == p.steps;
+    for (int m = 0; m < blocks; ++m) {
+      landed(&bars->block[m], step & 1);
+      uint32_t u[2][32];
+      tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + m * 128 + side * 64, u[0]);
+      tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + m * 128 + side * 64 + 32, u[1]);
+      tmem_ld_wait();
+      const float* v = reinterpret_cast<const float*>(u);
+      const int n = m * 128 + row;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        float w[8];
+        const int at = side * half + swizzled(n, 8 * q);
+        get8<PAIRS>(X, xlo, at, w);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) w[x] = fmaf(p.a, w[x], unit * v[8 * q + x]);
+        if (!last) {
+          put8<PAIRS>(X, xlo, at, w);
+        } else if (n < cols) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int i = side * 64 + 8 * q + x;
+            if (i < s) ((O*)p.O)[wide ? (size_t)(n0 + n) * p.ldo + i : (size_t)i * p.ldo + n0 + n] = from_float<O>(w[x] * unit);
+          }
+        }
+      }
+    }
+    fence_proxies();
+    tc_fence_before();
+    together();   // nor do the slabs of a cluster run apart: A is written from all of them
+    tc_fence_after();
+  }
+  if (warp == 1) tmem_dealloc(tmem, tcols);
+}
+
+// The largest cluster that the current device can run with a CTA of this kernel per SM (16 is not portable; 8 is).
+int largest_cluster() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::atomic<int>& k = known[dev & 63];
+  if (k.load(std::memory_order_relaxed) == 0) {
+    const auto kernel = k_ortho_small<float, __nv_bfloat16, false>;
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, small_smem(512, false));
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = SCLUSTER;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(SCLUSTER);
+    cfg.blockDim = dim3(STHREADS);
+    cfg.dynamicSmemBytes = small_smem(512, false);
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) cudaGetLastError();
+    k.store(n > 0 ? SCLUSTER : SCLUSTER / 2, std::memory_order_relaxed);
+  }
+  return k.load(std::memory_order_relaxed);
+}
+
+template <class T, class O, bool PAIRS>
+cr_status launch_small(const Small& p, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  constexpr int most = 512 / (PAIRS ? 2 : 1);
+  CR_TRY(allow_shared((const void*)k_ortho_small<T, O, PAIRS>, small_smem(most, PAIRS), done, true));
+  TimedScope ts("k_ortho_small", stream);
+  CR_CUDA(launch_after(k_ortho_small<T, O, PAIRS>, p.ncta, STHREADS, small_smem(p.L, PAIRS), p.ncta, stream, p));
+  CR_CHECK_LAUNCH("k_ortho_small");
+  return CR_OK;
+}
+
 }  // namespace
 }  // namespace cr
 
@@ -254,6 +626,18 @@ extern "C" cr_status cr_orthogonalize(int type, const void* d_G, int ldg, int K,
   int* err = nullptr;
   CR_TRY(wait_word(&err));
   const bool two = out_type != CR_TYPE_BF16, wide = K <= N;
+  const int across = std::min(K, N), along = std::max(K, N);
+  if (across <= SROWS && along <= largest_cluster() * (two ? 256 : 512)) {
+    Small p = {d_G, ldg, K, N, steps, 0, 1, (float)a, (float)b, (float)c, d_O, ldo, option_wait_ns(), err};
+    while (p.ncta < largest_cluster() && along > 128 * p.ncta) p.ncta *= 2;
+    p.L = ((along + p.ncta - 1) / p.ncta + 127) / 128 * 128;
+    return with_type(type, [&](auto t0) -> cr_status {
+      using T = decltype(t0);
+      if (out_type == CR_TYPE_F32) return launch_small<T, float, true>(p, stream);
+      if (out_type == CR_TYPE_F16) return launch_small<T, __half, true>(p, stream);
+      return launch_small<T, __nv_bfloat16, false>(p, stream);
+    });
+  }
   const int s = wide ? K : N, ld = (K + 7) & ~7, lds = (s + 7) & ~7;
   const auto bytes = [](long long l, long long n) { return (size_t)((l * n * 2 + 255) & ~255ll); };
   const size_t bx = bytes(ld, N), bs = bytes(lds, s);
