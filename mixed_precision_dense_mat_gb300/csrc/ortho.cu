@@ -18,15 +18,15 @@ constexpr int MAXPART = 1024;
 // Sums of squares of a block's elements to part[block]: of those above 2^50 and below 2^-50 scaled by 2^-90 and 2^90, so
 // that no square overflows or underflows.
 struct Squares {
-  double big, mid, small;
+  float big, mid, small;
 };
 __device__ __forceinline__ void add_square(float x, float& big, float& mid, float& small) {
   const float a = fabsf(x);
   const bool high = a > 0x1p50f, low = a < 0x1p-50f;
-  const float y = high ? a * 0x1p-90f : low ? a * 0x1p90f : a;
-  if (high) big = fmaf(y, y, big);
-  else if (low) small = fmaf(y, y, small);
-  else mid = fmaf(y, y, mid);
+  const float b = high ? a * 0x1p-90f : 0.0f, m = high || low ? 0.0f : a, s = low ? a * 0x1p90f : 0.0f;   // NaN goes to the middle
+  big = fmaf(b, b, big);
+  mid = fmaf(m, m, mid);
+  small = fmaf(s, s, small);
 }
 __device__ __forceinline__ Squares warp_sum(Squares s) {
 #pragma unroll
@@ -37,17 +37,19 @@ __device__ __forceinline__ Squares warp_sum(Squares s) {
   }
   return s;
 }
-// X = ((g f[1]) f[2]) f[0] is UNIT g / |G|_F, zero for a zero matrix and NaN where |G|_F is not finite: UNIT / |G|_F is m 2^e, and 2^e
-// is applied in two halves that are normal numbers.
+// X = ((g f[1]) f[2]) f[0] is UNIT g / |G|_F, zero for a zero matrix and NaN where |G|_F is not finite.  The sum is t 2^U for the
+// highest range that holds anything (what is below it by more than FP32's digits drops out), and UNIT / |G|_F is f[0] times a
+// power of two that is applied in two halves, which are normal numbers.
 __device__ __forceinline__ void scale_of(const Squares& s, float* f) {
-  const double norm = sqrt(s.big * 0x1p180 + s.mid + s.small * 0x1p-180);
-  int e = 0;
-  double m = 0.0;
-  if (norm > 0.0 && norm < 1e300) m = frexp((double)UNIT / norm, &e);
-  else if (norm != 0.0) m = norm - norm;   // NaN
-  f[0] = (float)m;
-  f[1] = (float)ldexp(1.0, e / 2);
-  f[2] = (float)ldexp(1.0, e - e / 2);
+  const bool high = s.big != 0.0f, mid = s.mid != 0.0f;
+  const float t = high ? s.big + (s.mid * 0x1p-90f) * 0x1p-90f : mid ? s.mid + (s.small * 0x1p-90f) * 0x1p-90f : s.small;
+  const int U = high ? 180 : mid ? 0 : -180;
+  const int bits = __float_as_int(t), e = ((bits >> 23) - 127) & ~1;   // t / 2^e in [1, 4)
+  const float m = __int_as_float(bits - (e << 23));
+  f[0] = t == 0.0f ? 0.0f : t - t + 1.0f / sqrtf(m);   // infinity and NaN: NaN
+  const int E = 10 - (e + U) / 2, h = E / 2;           // UNIT = 2^10
+  f[1] = __int_as_float((h + 127) << 23);
+  f[2] = __int_as_float((E - h + 127) << 23);
 }
 template <class T, int V>
 __global__ void __launch_bounds__(NT) k_ortho_norm(const T* G, int ld, int K, int N, Squares* part) {
@@ -83,7 +85,7 @@ template <class T, int V>
 __global__ void __launch_bounds__(NT) k_ortho_scale(const T* G, int ld, int K, int N, const Squares* part, int parts, __half* X, __half* X2, int ldx) {
   __shared__ float factor[3];
   if (threadIdx.x < 32) {
-    Squares s = {0.0, 0.0, 0.0};
+    Squares s = {0.0f, 0.0f, 0.0f};
     for (int q = threadIdx.x; q < parts; q += 32) {
       s.big += part[q].big;
       s.mid += part[q].mid;
@@ -245,23 +247,27 @@ cr_status start(const T* G, int ld, int K, int N, Squares* part, const Split& X,
 // kernels of five steps take 160 us.
 constexpr int SROWS = 128, STHREADS = 256, SCLUSTER = 16;
 constexpr int SA = SROWS * SROWS * 2;   // bytes of A's FP16 part, [j / 64][i][j % 64]
-constexpr int SPARTS = 64 * 1024;       // A's two parts, or the FP32 sums of this CTA
+constexpr int SSUMS = SROWS * SROWS * 4;   // the CTA's sums for A
 struct SmallBars {
   uint64_t product, block[4];
   uint32_t tmem;
-  double sums[SCLUSTER][3], warps[STHREADS / 32][3];
+  float sums[SCLUSTER][3], warps[STHREADS / 32][3];
   float factor[3];
 };
 struct Small {
   const void* G;
   int ldg, K, N, steps, L, ncta;
+  int alias;   // the sums in A's two parts, where there is no room beside them: one more barrier per step
   float a, b, c;
   void* O;
   int ldo;
   unsigned long long limit;
   int* err;
 };
-__host__ __device__ constexpr int small_smem(int L, bool pairs) { return 1024 + L * SROWS * 2 * (pairs ? 2 : 1) + SPARTS + (int)sizeof(SmallBars); }
+__host__ __device__ constexpr int small_smem(int L, bool pairs, bool alias) {
+  return 1024 + (L * SROWS * 2 + (alias ? 0 : SA)) * (pairs ? 2 : 1) + SSUMS + (int)sizeof(SmallBars);
+}
+constexpr bool small_alias(int L, bool pairs) { return small_smem(L, pairs, false) > 227 * 1024; }
 
 __device__ __forceinline__ void fence_proxies() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
@@ -308,8 +314,8 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int L = p.L, half = L * 128, xlo = 2 * half;   // bytes of 64 rows of X, of a part of X
-  uint8_t *X = smem, *A = X + (PAIRS ? 2 : 1) * xlo;
-  SmallBars* bars = reinterpret_cast<SmallBars*>(A + SPARTS);
+  uint8_t *X = smem, *A = X + (PAIRS ? 2 : 1) * xlo, *P = p.alias ? A : A + (PAIRS ? 2 : 1) * SA;   // P: this CTA's sums for A
+  SmallBars* bars = reinterpret_cast<SmallBars*>(P + SSUMS);
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = p.ncta > 1 ? (int)cluster_rank() : 0;
   const bool wide = p.K <= p.N;
@@ -334,14 +340,33 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
     else __syncthreads();
   };
 
-  // G's elements of the slab: lanes along its columns, warps across them; twice, the second time from L1 or L2.
+  // G's elements of the slab, 128 x 128 at a time: lanes along its columns, warps across them, all of a thread's on their way at
+  // once.  The last ones stay in registers, the others come a second time from L2.
   const T* G = (const T*)p.G + (wide ? (size_t)n0 * p.ldg : n0);
   const int inner = wide ? s : cols, outer = wide ? cols : s;
   {
+    float g[4][16];
+    const auto load = [&](int x0, int y0) {
+#pragma unroll
+      for (int b = 0; b < 16; ++b)
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const int x = x0 + 32 * a + lane, y = y0 + 8 * b + warp;
+          g[a][b] = x < inner && y < outer ? to_float(G[(size_t)y * p.ldg + x]) : 0.0f;
+        }
+    };
     float big = 0.0f, mid = 0.0f, small = 0.0f;
-    for (int x = lane; x < inner; x += 32)
-#pragma unroll 8
-      for (int y = warp; y < outer; y += STHREADS / 32) add_square(to_float(G[(size_t)y * p.ldg + x]), big, mid, small);
+    int lx = -1, ly = -1;   // what is in g
+    for (int y0 = 0; y0 < outer; y0 += 128)
+      for (int x0 = 0; x0 < inner; x0 += 128) {
+        load(x0, y0);
+        lx = x0;
+        ly = y0;
+#pragma unroll
+        for (int b = 0; b < 16; ++b)
+#pragma unroll
+          for (int a = 0; a < 4; ++a) add_square(g[a][b], big, mid, small);
+      }
     Squares sum = warp_sum(Squares{big, mid, small});
     if (lane == 0) {
       bars->warps[warp][0] = sum.big;
@@ -350,7 +375,7 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
     }
     __syncthreads();
     if (threadIdx.x < 3) {
-      double x = 0.0;
+      float x = 0.0f;
       for (int w = 0; w < STHREADS / 32; ++w) x += bars->warps[w][threadIdx.x];
       bars->sums[rank][threadIdx.x] = x;
     }
@@ -358,14 +383,14 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
       cluster_wait();
       __syncthreads();
       if ((int)threadIdx.x < 3 * p.ncta) {   // to every CTA
-        const double x = bars->sums[rank][threadIdx.x % 3];
+        const float x = bars->sums[rank][threadIdx.x % 3];
         const uint32_t to = cluster_addr(smem_u32(&bars->sums[rank][threadIdx.x % 3]), threadIdx.x / 3);
-        if ((int)threadIdx.x / 3 != rank) asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(x) : "memory");
+        if ((int)threadIdx.x / 3 != rank) store_cluster(to, __float_as_uint(x));
       }
     }
     together();
     if (threadIdx.x == 0) {
-      Squares all = {0.0, 0.0, 0.0};
+      Squares all = {0.0f, 0.0f, 0.0f};
       for (int r = 0; r < p.ncta; ++r) {
         all.big += bars->sums[r][0];
         all.mid += bars->sums[r][1];
@@ -375,21 +400,29 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
     }
     __syncthreads();
     const float m = bars->factor[0], p1 = bars->factor[1], p2 = bars->factor[2];
-    for (int x = lane; x < inner; x += 32)
-#pragma unroll 8
-      for (int y = warp; y < outer; y += STHREADS / 32) {
-        const float v = to_float(G[(size_t)y * p.ldg + x]) * p1 * p2 * m;
-        const int i = wide ? x : y, n = wide ? y : x, at = i / 64 * half + swizzled(n, i % 64);
-        const __half hi = __float2half_rn(v);
-        *reinterpret_cast<__half*>(X + at) = hi;
-        if (PAIRS) *reinterpret_cast<__half*>(X + xlo + at) = __float2half_rn(v - __half2float(hi));
+    for (int y0 = ly; y0 >= 0; y0 -= 128)
+      for (int x0 = lx; x0 >= 0; x0 -= 128) {
+        if (x0 != lx || y0 != ly) load(x0, y0);
+#pragma unroll
+        for (int b = 0; b < 16; ++b)
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            const int x = x0 + 32 * a + lane, y = y0 + 8 * b + warp;
+            if (x < inner && y < outer) {
+              const float v = g[a][b] * p1 * p2 * m;
+              const int i = wide ? x : y, n = wide ? y : x, at = i / 64 * half + swizzled(n, i % 64);
+              const __half hi = __float2half_rn(v);
+              *reinterpret_cast<__half*>(X + at) = hi;
+              if (PAIRS) *reinterpret_cast<__half*>(X + xlo + at) = __float2half_rn(v - __half2float(hi));
+            }
+          }
       }
   }
   fence_proxies();
   __syncthreads();
 
   const uint32_t rows_id = idesc_of(128, 128, false, true, true), k_id = idesc_of(128, 128, false, false, false);
-  const uint32_t sx = smem_u32(X), sa = smem_u32(A);
+  const uint32_t sx = smem_u32(X), sa = smem_u32(A), sums = smem_u32(P);
   constexpr int SEGS = PAIRS ? 3 : 1;
   // parts of the first and second operand, the small products first
   const auto first_lo = [](int seg) { return PAIRS && seg == 1; };
@@ -437,35 +470,33 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
       } else {   // 16-byte word w of row i at w ^ (i & 31)
 #pragma unroll
         for (int q = 0; q < 16; ++q)
-          *reinterpret_cast<float4*>(A + row * 512 + (((side * 16 + q) ^ (row & 31)) << 4)) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          *reinterpret_cast<float4*>(P + row * 512 + (((side * 16 + q) ^ (row & 31)) << 4)) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
       }
     }
     if (p.ncta > 1) {
       cluster_sync_all();
-      const int own = SROWS / p.ncta, words = own * 32 / STHREADS;   // rows, and 16-byte words of a thread (1 to 8; ncta is 2 to 16)
-      float4 sum[8];
+      const auto exchange = [&](auto nc) {   // 16 words of 16 bytes from other CTAs to a thread, all on their way at once
+        constexpr int NC = decltype(nc)::value, OWN = SROWS / NC, WORDS = 16 / NC;
+        float4 x[WORDS][NC];
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q < words) {
-          const int e = threadIdx.x + q * STHREADS, i = rank * own + e / 32, w = e % 32;
-          const uint32_t at = sa + i * 512 + ((w ^ (i & 31)) << 4);
-          float4 z = make_float4(0, 0, 0, 0);
-          for (int r = 0; r < p.ncta; ++r) {
-            const float4 x = load_cluster4(cluster_addr(at, r));
-            z.x += x.x;
-            z.y += x.y;
-            z.z += x.z;
-            z.w += x.w;
-          }
-          sum[q] = z;
+        for (int q = 0; q < WORDS; ++q) {
+          const int e = threadIdx.x + q * STHREADS, i = rank * OWN + e / 32;
+#pragma unroll
+          for (int r = 0; r < NC; ++r) x[q][r] = load_cluster4(cluster_addr(sums + i * 512 + ((e % 32 ^ (i & 31)) << 4), r));
         }
-      cluster_sync_all();   // the sums have been read: A may take their place
+        if (p.alias) cluster_sync_all();   // the sums have been read: A may take their place
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q < words) {
-          const int e = threadIdx.x + q * STHREADS, i = rank * own + e / 32, j = e % 32 * 4;
-          const int at = j / 64 * (SA / 2) + swizzled(i, j % 64);
-          const float v[4] = {sum[q].x * unit, sum[q].y * unit, sum[q].z * unit, sum[q].w * unit};
+        for (int q = 0; q < WORDS; ++q) {
+          float4 z = x[q][0];
+#pragma unroll
+          for (int r = 1; r < NC; ++r) {
+            z.x += x[q][r].x;
+            z.y += x[q][r].y;
+            z.z += x[q][r].z;
+            z.w += x[q][r].w;
+          }
+          const int e = threadIdx.x + q * STHREADS, i = rank * OWN + e / 32, j = e % 32 * 4, at = j / 64 * (SA / 2) + swizzled(i, j % 64);
+          const float v[4] = {z.x * unit, z.y * unit, z.z * unit, z.w * unit};
           const uint32_t h0 = narrow2(v[0], v[1], __half{}), h1 = narrow2(v[2], v[3], __half{});
           uint32_t l0 = 0, l1 = 0;
           if (PAIRS) {
@@ -473,11 +504,17 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
             l0 = narrow2(v[0] - f0.x, v[1] - f0.y, __half{});
             l1 = narrow2(v[2] - f1.x, v[3] - f1.y, __half{});
           }
-          for (int r = 0; r < p.ncta; ++r) {
+#pragma unroll
+          for (int r = 0; r < NC; ++r) {
             store_cluster2(cluster_addr(sa + at, r), h0, h1);
             if (PAIRS) store_cluster2(cluster_addr(sa + SA + at, r), l0, l1);
           }
         }
+      };
+      if (p.ncta == 2) exchange(std::integral_constant<int, 2>{});
+      else if (p.ncta == 4) exchange(std::integral_constant<int, 4>{});
+      else if (p.ncta == 8) exchange(std::integral_constant<int, 8>{});
+      else exchange(std::integral_constant<int, 16>{});
     }
     fence_proxies();
     tc_fence_before();
@@ -552,20 +589,48 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
         for (int x = 0; x < 8; ++x) w[x] = fmaf(p.a, w[x], unit * v[8 * q + x]);
         if (!last) {
           put8<PAIRS>(X, xlo, at, w);
-        } else if (n < cols) {
+        } else if (!wide) {
+          if (n < cols) {
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const int i = side * 64 + 8 * q + x;
-            if (i < s) ((O*)p.O)[wide ? (size_t)(n0 + n) * p.ldo + i : (size_t)i * p.ldo + n0 + n] = from_float<O>(w[x] * unit);
+            for (int x = 0; x < 8; ++x) {
+              const int i = side * 64 + 8 * q + x;
+              if (i < s) ((O*)p.O)[(size_t)i * p.ldo + n0 + n] = from_float<O>(w[x] * unit);
+            }
           }
+        } else {   // to X's place, FP32 in halves, and from there with lanes along the columns
+          uint32_t hi[4], lo[4] = {};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if constexpr (sizeof(O) == 4) {
+              const uint32_t f0 = __float_as_uint(w[2 * x] * unit), f1 = __float_as_uint(w[2 * x + 1] * unit);
+              hi[x] = f0 >> 16 | (f1 & 0xffff0000u);
+              lo[x] = (f0 & 0xffffu) | f1 << 16;
+            } else {
+              hi[x] = narrow2(w[2 * x] * unit, w[2 * x + 1] * unit, O{});
+            }
+          }
+          *reinterpret_cast<uint4*>(X + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          if (sizeof(O) == 4) *reinterpret_cast<uint4*>(X + xlo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
     }
     fence_proxies();
     tc_fence_before();
-    together();   // nor do the slabs of a cluster run apart: A is written from all of them
+    __syncthreads();
     tc_fence_after();
   }
+  if (wide)
+#pragma unroll 4
+    for (int n = warp; n < cols; n += STHREADS / 32)
+#pragma unroll
+      for (int k = 0; k < SROWS / 32; ++k) {
+        const int i = lane + 32 * k, at = i / 64 * half + swizzled(n, i % 64);
+        if (i >= s) continue;
+        O* to = (O*)p.O + (size_t)(n0 + n) * p.ldo + i;
+        if constexpr (sizeof(O) == 4)
+          *to = __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(X + at) << 16 | *reinterpret_cast<const uint16_t*>(X + xlo + at));
+        else *to = *reinterpret_cast<const O*>(X + at);
+      }
   if (warp == 1) tmem_dealloc(tmem, tcols);
 }
 
@@ -578,7 +643,7 @@ int largest_cluster() {
   if (k.load(std::memory_order_relaxed) == 0) {
     const auto kernel = k_ortho_small<float, __nv_bfloat16, false>;
     cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, small_smem(512, false));
+    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -586,7 +651,7 @@ int largest_cluster() {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(SCLUSTER);
     cfg.blockDim = dim3(STHREADS);
-    cfg.dynamicSmemBytes = small_smem(512, false);
+    cfg.dynamicSmemBytes = 227 * 1024;
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int n = 0;
@@ -599,10 +664,9 @@ int largest_cluster() {
 template <class T, class O, bool PAIRS>
 cr_status launch_small(const Small& p, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  constexpr int most = 512 / (PAIRS ? 2 : 1);
-  CR_TRY(allow_shared((const void*)k_ortho_small<T, O, PAIRS>, small_smem(most, PAIRS), done, true));
+  CR_TRY(allow_shared((const void*)k_ortho_small<T, O, PAIRS>, 227 * 1024, done, true));
   TimedScope ts("k_ortho_small", stream);
-  CR_CUDA(launch_after(k_ortho_small<T, O, PAIRS>, p.ncta, STHREADS, small_smem(p.L, PAIRS), p.ncta, stream, p));
+  CR_CUDA(launch_after(k_ortho_small<T, O, PAIRS>, p.ncta, STHREADS, small_smem(p.L, PAIRS, p.alias), p.ncta, stream, p));
   CR_CHECK_LAUNCH("k_ortho_small");
   return CR_OK;
 }
@@ -628,9 +692,10 @@ extern "C" cr_status cr_orthogonalize(int type, const void* d_G, int ldg, int K,
   const bool two = out_type != CR_TYPE_BF16, wide = K <= N;
   const int across = std::min(K, N), along = std::max(K, N);
   if (across <= SROWS && along <= largest_cluster() * (two ? 256 : 512)) {
-    Small p = {d_G, ldg, K, N, steps, 0, 1, (float)a, (float)b, (float)c, d_O, ldo, option_wait_ns(), err};
+    Small p = {d_G, ldg, K, N, steps, 0, 1, 0, (float)a, (float)b, (float)c, d_O, ldo, option_wait_ns(), err};
     while (p.ncta < largest_cluster() && along > 128 * p.ncta) p.ncta *= 2;
     p.L = ((along + p.ncta - 1) / p.ncta + 127) / 128 * 128;
+    p.alias = small_alias(p.L, two);
     return with_type(type, [&](auto t0) -> cr_status {
       using T = decltype(t0);
       if (out_type == CR_TYPE_F32) return launch_small<T, float, true>(p, stream);
