@@ -122,24 +122,89 @@ __global__ void __launch_bounds__(NT) k_ortho_scale(const T* G, int ld, int K, i
   }
 }
 
-// O = (X + X2) / UNIT in FP32.
-__global__ void __launch_bounds__(NT) k_ortho_join(const __half* X, const __half* X2, int ldx, int K, int N, float* O, int ldo) {
+// C = alpha (sum of the parts) + beta R for 64 x 64 outputs, to FP16 with the rest after it in C2 (may be NULL), or to the
+// caller's matrix; TRI: C is symmetric, parts hold the 256-wide tiles ti <= tj, and C(j, i) is stored too.
+constexpr int JTILE = 64;
+template <class O, bool TRI>
+__global__ void __launch_bounds__(NT) k_ortho_sum(const float* part, int parts, int ldp, int jpad, int I, int J, const __half* R, const __half* R2,
+                                                  int ldr, float alpha, float beta, O* C, O* C2, int ldc, int vec) {
+  __shared__ float turned[TRI ? JTILE : 1][JTILE + 1];
+  const int i0 = blockIdx.x * JTILE, j0 = blockIdx.y * JTILE;
   let_next_start();
   wait_for_previous();
-  const int per = (K + 3) / 4;
-  const long long total = (long long)per * N;
-  const bool vec = ((uintptr_t)O & 15) == 0 && ldo % 4 == 0;
-  for (long long e = (long long)blockIdx.x * NT + threadIdx.x; e < total; e += (long long)gridDim.x * NT) {
-    const int col = e >> 32 ? (int)(e / per) : (int)((uint32_t)e / (uint32_t)per), i = (int)(e - (long long)col * per) * 4;
-    const uint2 a = *reinterpret_cast<const uint2*>(X + (size_t)col * ldx + i), b = *reinterpret_cast<const uint2*>(X2 + (size_t)col * ldx + i);
-    const float2 a0 = widen2(a.x, __half{}), a1 = widen2(a.y, __half{}), b0 = widen2(b.x, __half{}), b1 = widen2(b.y, __half{});
-    const float v[4] = {(a0.x + b0.x) / UNIT, (a0.y + b0.y) / UNIT, (a1.x + b1.x) / UNIT, (a1.y + b1.y) / UNIT};
-    float* to = O + (size_t)col * ldo + i;
-    if (vec && i + 4 <= K) *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
-    else
+  if (TRI && i0 / 256 > j0 / 256) return;
+  const bool twice = TRI && i0 / 256 != j0 / 256;
+  const int x = threadIdx.x % 16 * 4, i = i0 + x;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (i + q < K) to[q] = v[q];
+  for (int y = threadIdx.x / 16; y < JTILE; y += 16) {
+    const int j = j0 + y;
+    float v[4] = {};
+    if (j < J && i < I) {
+      const float* from = part + (size_t)j * ldp + i;
+      float4 z = *reinterpret_cast<const float4*>(from);
+#pragma unroll 4
+      for (int q = 1; q < parts; ++q) {
+        const float4 w = *reinterpret_cast<const float4*>(from + (size_t)q * jpad * ldp);
+        z.x += w.x;
+        z.y += w.y;
+        z.z += w.z;
+        z.w += w.w;
+      }
+      v[0] = z.x * alpha;
+      v[1] = z.y * alpha;
+      v[2] = z.z * alpha;
+      v[3] = z.w * alpha;
+      if (R) {
+        const auto four = [&](const __half* m, float (&f)[4]) {
+          const uint2 w = *reinterpret_cast<const uint2*>(m + (size_t)j * ldr + i);
+          const float2 a = widen2(w.x, __half{}), b = widen2(w.y, __half{});
+          f[0] = a.x;
+          f[1] = a.y;
+          f[2] = b.x;
+          f[3] = b.y;
+        };
+        float r[4], t[4] = {};
+        four(R, r);
+        if (R2) four(R2, t);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = fmaf(beta, r[q] + t[q], v[q]);
+      }
+      struct alignas(4 * sizeof(O)) Four {
+        O x[4];
+      } o, rest;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        o.x[q] = from_float<O>(v[q]);
+        rest.x[q] = from_float<O>(v[q] - to_float(o.x[q]));
+      }
+      const size_t at = (size_t)j * ldc + i;
+      if (vec && i + 4 <= I) {
+        *reinterpret_cast<Four*>(C + at) = o;
+        if (C2) *reinterpret_cast<Four*>(C2 + at) = rest;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (i + q < I) {
+            C[at + q] = o.x[q];
+            if (C2) C2[at + q] = rest.x[q];
+          }
+      }
+    }
+    if (twice) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) turned[x + q][y] = v[q];
+    }
+  }
+  if (!twice) return;
+  __syncthreads();
+  for (int e = threadIdx.x; e < JTILE * JTILE; e += NT) {
+    const int a = e / JTILE, b = e % JTILE, col = i0 + a, row = j0 + b;   // C(row, col)
+    if (col < I && row < J) {
+      const float v = turned[a][b];
+      const O o = from_float<O>(v);
+      C[(size_t)col * ldc + row] = o;
+      if (C2) C2[(size_t)col * ldc + row] = from_float<O>(v - to_float(o));
+    }
   }
 }
 
@@ -178,14 +243,21 @@ cr_status step_product(const Step& s, int* err, cudaStream_t stream) {
   p.e.ldc = s.out ? s.ldout : s.C.ld;
   p.C2 = s.out ? nullptr : s.C.lo;
   const int out_type = s.out ? s.out_type : CR_TYPE_F16;
-  p.tma_c = ((uintptr_t)p.e.C & 15) == 0 && p.e.ldc % 8 == 0;
-  const Choice ch = choose<STEP>(s.I, s.J, p.kblocks, s.q_major, s.symmetric);
+  p.tma_c = ((uintptr_t)p.e.C & 15) == 0 && p.e.ldc % 8 == 0;   // STEP's wide outputs are of 16 bits
+  p.vec4 = ((uintptr_t)p.e.C & (4 * type_bytes(out_type) - 1)) == 0 && p.e.ldc % 4 == 0;
+  // With two parts a sum has to keep FP32's digits, and the tensor cores' adders cut off what they cannot hold: they sum up 4
+  // k-blocks (16 additions) by themselves, 8 in the thin kernel, which has no registers to go on in (1001 x 2500 FP32, five
+  // steps: relative error 1.5e-5 with whole sums).
+  const Choice ch = choose<STEP>(s.I, s.J, p.kblocks, s.q_major, s.symmetric, s.P.lo != nullptr);
+  p.parts = ch.parts;
+  p.chunk = s.P.lo ? 4 : p.kblocks;
+  p.jpad = (s.J + 255) / 256 * 256;
   p.triangle = ch.wide && s.symmetric;
   p.bn = ch.bn;
   p.ti = ch.wide ? (s.I + 255) / 256 : (s.I + 127) / 128;
   p.tj = ch.wide ? (s.J + 255) / 256 : (s.J + p.bn - 1) / p.bn;
   p.idesc = ch.wide ? idesc_of(256, 256, false, !p.qk, !p.pk) : idesc_of(128, p.bn, false, !p.pk, !p.qk);
-  p.stages = WSTAGES - 1;   // two output buffers per warp
+  p.stages = ch.parts ? WSTAGES - 1 : WSTAGES;   // SUMS: twice as many output buffers
   const auto maps_of = [&](CUtensorMap* m, CUtensorMap* m2, const Split& x, int rows, bool major, int box) -> cr_status {
     CR_TRY(map_of(m, Operand{x.hi, rows, x.ld, major}, CR_TYPE_F16, s.K, box));
     return x.lo ? map_of(m2, Operand{x.lo, rows, x.ld, major}, CR_TYPE_F16, s.K, box) : CR_OK;
@@ -198,22 +270,44 @@ cr_status step_product(const Step& s, int* err, cudaStream_t stream) {
       CR_TRY(maps_of(&maps.Q, &maps.Q2, s.Q, s.J, s.q_major, p.bn));
       return launch_thin<STEP, false, O>(maps, p, ch.split, ch.stages, stream);
     }
-    Maps<STEP> maps = {};
-    CR_TRY(maps_of(&maps.P, &maps.P2, s.P, s.I, s.p_major, 128));
-    CR_TRY(maps_of(&maps.Q, &maps.Q2, s.Q, s.J, s.q_major, 128));
-    const auto tile = [&](CUtensorMap* m, const void* x, int type, int ld) { return make_tensor_map_2d(m, type, x, s.I, s.J, ld, 64, 32); };
-    if (p.tma_c) CR_TRY(tile(&maps.C, p.e.C, out_type, p.e.ldc));
-    if (p.C2) CR_TRY(tile(&maps.C2, p.C2, CR_TYPE_F16, p.e.ldc));
-    if (s.R.hi) CR_TRY(tile(&maps.R, s.R.hi, CR_TYPE_F16, s.R.ld));
-    if (s.R.lo) CR_TRY(tile(&maps.R2, s.R.lo, CR_TYPE_F16, s.R.ld));
-    if (p.triangle) {
-      CR_TRY(make_tensor_map_2d_plain(&maps.T, CR_TYPE_F16, p.e.C, s.J, s.I, p.e.ldc, 32, 64));
-      if (p.C2) CR_TRY(make_tensor_map_2d_plain(&maps.T2, CR_TYPE_F16, p.C2, s.J, s.I, p.e.ldc, 32, 64));
+    const long long n = p.tj, tiles = p.triangle ? n * (n + 1) / 2 : (long long)p.ti * p.tj;
+    if (p.parts > 0) {
+      Maps<SUMS> maps = {};
+      CR_TRY(maps_of(&maps.P, &maps.P2, s.P, s.I, s.p_major, 128));
+      CR_TRY(maps_of(&maps.Q, &maps.Q2, s.Q, s.J, s.q_major, 128));
+      const int ldp = (s.I + 3) & ~3;
+      float* part = nullptr;
+      CR_CUDA(scratch_alloc((void**)&part, (size_t)p.parts * p.jpad * ldp * sizeof(float), stream));
+      const auto run = [&]() -> cr_status {
+        CR_TRY(make_tensor_map_2d(&maps.C, CR_TYPE_F32, part, s.I, p.parts * p.jpad, ldp, 32, 32));
+        CR_TRY((launch_wide<SUMS, false, float>(maps, p, tiles * p.parts, stream)));
+        TimedScope ts("k_ortho_sum", stream);
+        const int vec = ((uintptr_t)p.e.C & (4 * sizeof(O) - 1)) == 0 && p.e.ldc % 4 == 0;
+        const dim3 grid((s.I + JTILE - 1) / JTILE, (s.J + JTILE - 1) / JTILE);
+        const auto sum = [&](auto tri) {
+          return launch_after(k_ortho_sum<O, decltype(tri)::value>, grid, NT, 0, 1, stream, part, p.parts, ldp, p.jpad, s.I, s.J, (const __half*)p.e.R,
+                              (const __half*)p.R2, s.R.ld, p.alpha, p.beta, (O*)p.e.C, (O*)p.C2, p.e.ldc, vec);
+        };
+        CR_CUDA(p.triangle ? sum(std::true_type{}) : sum(std::false_type{}));
+        CR_CHECK_LAUNCH("k_ortho_sum");
+        return CR_OK;
+      };
+      const cr_status st = run();
+      scratch_free(part, stream);
+      return st;
     }
-    const long long n = p.tj;
-    return launch_wide<STEP, false, O>(maps, p, p.triangle ? n * (n + 1) / 2 : (long long)p.ti * p.tj, stream);
+    if constexpr (sizeof(O) == 2) {
+      Maps<STEP> maps = {};
+      CR_TRY(map_of(&maps.P, Operand{s.P.hi, s.I, s.P.ld, s.p_major}, CR_TYPE_F16, s.K, 128));
+      CR_TRY(map_of(&maps.Q, Operand{s.Q.hi, s.J, s.Q.ld, s.q_major}, CR_TYPE_F16, s.K, 128));
+      if (p.tma_c) CR_TRY(make_tensor_map_2d(&maps.C, out_type, p.e.C, s.I, s.J, p.e.ldc, 64, 32));
+      if (s.R.hi) CR_TRY(make_tensor_map_2d(&maps.R, CR_TYPE_F16, s.R.hi, s.I, s.J, s.R.ld, 64, 32));
+      if (p.triangle) CR_TRY(make_tensor_map_2d_plain(&maps.T, CR_TYPE_F16, p.e.C, s.J, s.I, p.e.ldc, 32, 64));
+      return launch_wide<STEP, false, O>(maps, p, tiles, stream);
+    }
+    return fail_literal(CR_ERR_STATE, "cr_orthogonalize: FP32 comes from the sums");
   };
-  return out_type == CR_TYPE_BF16 ? go(__nv_bfloat16{}) : go(__half{});
+  return out_type == CR_TYPE_F32 ? go(float{}) : out_type == CR_TYPE_BF16 ? go(__nv_bfloat16{}) : go(__half{});
 }
 
 template <class T>
@@ -749,7 +843,7 @@ extern "C" cr_status cr_orthogonalize(int type, const void* d_G, int ldg, int K,
       m.symmetric = false;
       m.alpha = unit;
       m.beta = (float)a;
-      if (last && out_type != CR_TYPE_F32) {
+      if (last) {
         m.out = d_O;
         m.out_type = out_type;
         m.ldout = ldo;
@@ -758,13 +852,6 @@ extern "C" cr_status cr_orthogonalize(int type, const void* d_G, int ldg, int K,
       }
       CR_TRY(step_product(m, err, stream));
       std::swap(X, Y);
-    }
-    if (out_type == CR_TYPE_F32) {
-      const long long words = (long long)((K + 3) / 4) * N;
-      TimedScope ts("k_ortho_join", stream);
-      CR_CUDA(launch_after(k_ortho_join, (unsigned)std::min<long long>((words + NT - 1) / NT, 8ll * sm_count()), NT, 0, 1, stream, X.hi, X.lo,
-                           X.ld, K, N, (float*)d_O, ldo));
-      CR_CHECK_LAUNCH("k_ortho_join");
     }
     return CR_OK;
   };

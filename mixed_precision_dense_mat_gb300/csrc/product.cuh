@@ -44,9 +44,9 @@ namespace {
 constexpr int NT = 256;
 
 // Forms.  AFFINE: C = act(sum + bias) + R.  GATED: P has two halves of I rows, C = act(first half's sum) times the
-// second half's sum.  STEP: C = alpha sum + beta R, all matrices FP16 or sums of two (the second one small), C
-// symmetric where the form's tiles say so.
-enum Form { AFFINE, GATED, STEP };
+// second half's sum.  STEP: C = alpha sum + beta R, all matrices FP16, or, in the thin kernel, sums of two (the second one
+// small); C symmetric where the wide kernel's tiles say so.  SUMS (wide): the sums alone, in FP32, with P and Q as in STEP.
+enum Form { AFFINE, GATED, STEP, SUMS };
 
 struct Params {
   int I, J, kblocks;     // GATED: I of each half
@@ -61,9 +61,12 @@ struct Params {
   int vec_r;             // R allows 16-byte accesses
   int tma_r;             // wide kernel: R comes by TMA into the output buffers (16-bit outputs)
   int vec4;              // four consecutive i of everything in the epilogue can be accessed at once
-  // STEP
+  // STEP and SUMS
   int segments;          // 1, or 3: the products of P's and Q's first parts and of each one's first with the other's second part
-  int triangle;          // C symmetric: tiles ti <= tj are formed, and stored at (tj, ti) too (wide kernel)
+  int triangle;          // C symmetric: tiles ti <= tj alone are formed (STEP stores them at (tj, ti) too; wide kernel)
+  int parts;             // SUMS: tiles over as many parts of k, one matrix of jpad rows below the other
+  int jpad;
+  int chunk;             // SUMS: k-blocks that the tensor cores sum up by themselves; such sums are added in registers
   float alpha, beta;
   void *C2, *R2;         // second parts (NULL: none), laid out like C and R
   Epilogue e;
@@ -220,19 +223,47 @@ __device__ __forceinline__ void finish_gated4(const Params& p, int i, int j, flo
   *reinterpret_cast<Four*>((O*)e.C + (size_t)j * e.ldc + i) = o;
 }
 
-// STEP: n consecutive i of column j (R, R2 and C2 are the library's own matrices).
-template <class O, int N>
-__device__ __forceinline__ void finish_step(const Params& p, int i, int j, const float (&sum)[N]) {
+// STEP: four consecutive i of column j (R, R2 and C2 are the library's own matrices, with columns on 16-byte boundaries).
+template <class O>
+__device__ __forceinline__ void finish_step4(const Params& p, int i, int j, float (&v)[4]) {
+  if (i >= p.I) return;
   const size_t r = (size_t)j * p.e.ldr + i, c = (size_t)j * p.e.ldc + i;
 #pragma unroll
-  for (int q = 0; q < N; ++q)
-    if (i + q < p.I) {
-      float v = sum[q] * p.alpha;
-      if (p.e.R) v = fmaf(p.beta, to_float(((const __half*)p.e.R)[r + q]) + (p.R2 ? to_float(((const __half*)p.R2)[r + q]) : 0.0f), v);
-      const O hi = from_float<O>(v);
-      ((O*)p.e.C)[c + q] = hi;
-      if (p.C2) ((O*)p.C2)[c + q] = from_float<O>(v - to_float(hi));
-    }
+  for (int q = 0; q < 4; ++q) v[q] *= p.alpha;
+  if (p.e.R) {
+    const auto four = [&](const void* m, float (&f)[4]) {
+      const uint2 w = *reinterpret_cast<const uint2*>((const __half*)m + r);
+      const float2 a = widen2(w.x, __half{}), b = widen2(w.y, __half{});
+      f[0] = a.x;
+      f[1] = a.y;
+      f[2] = b.x;
+      f[3] = b.y;
+    };
+    float x[4], y[4] = {};
+    four(p.e.R, x);
+    if (p.R2) four(p.R2, y);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = fmaf(p.beta, x[q] + y[q], v[q]);
+  }
+  struct alignas(4 * sizeof(O)) Four {
+    O x[4];
+  } o, rest;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    o.x[q] = from_float<O>(v[q]);
+    rest.x[q] = from_float<O>(v[q] - to_float(o.x[q]));
+  }
+  if (p.vec4 && i + 4 <= p.I) {
+    *reinterpret_cast<Four*>((O*)p.e.C + c) = o;
+    if (p.C2) *reinterpret_cast<Four*>((O*)p.C2 + c) = rest;
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (i + q < p.I) {
+        ((O*)p.e.C)[c + q] = o.x[q];
+        if (p.C2) ((O*)p.C2)[c + q] = rest.x[q];
+      }
+  }
 }
 
 // A float vector's N entries from i0 on, spread over the warp's lanes (0 past the end): entry q is w[q / 32] of
@@ -369,8 +400,9 @@ __device__ __forceinline__ void wide_finish(const Params& p, const CUtensorMap* 
 constexpr int WSTAGES = 6;                       // 5 with two output buffers per warp
 constexpr int WTILE = 128 * KBYTES;              // one operand's half tile of a stage, 16 KB
 constexpr int WSTAGE = 2 * WTILE;
-constexpr int WTHREADS = 320;
 constexpr int WEPI = 8;                          // epilogue warps
+constexpr int epilogue_warps(int form) { return form == SUMS ? 2 * WEPI : WEPI; }   // SUMS: half the columns each, held in registers
+constexpr int wide_threads(int form) { return 64 + 32 * epilogue_warps(form); }
 struct WideBars {
   uint64_t full[WSTAGES], empty[WSTAGES], tfull[2], tempty[2], rows[WEPI][2], settled;
   uint32_t tmem;
@@ -381,8 +413,8 @@ constexpr int WSMEM = WSTAGES * WSTAGE + WEPI * WBUF + 1024 + 384;
 static_assert(WSTAGE == WEPI * WBUF, "a stage's memory is a second set of output buffers");
 static_assert(sizeof(WideBars) <= 384, "barrier area");
 
-// What the wide kernel reads and writes by TMA.  AFFINE: R is the residual; GATED: Z2 is Z's second half; STEP: P, Q, C
-// and R have second parts, and T, T2 are C's stores of transposed tiles.
+// What the wide kernel reads and writes by TMA.  AFFINE: R is the residual; GATED: Z2 is Z's second half; STEP: T
+// is C's store of transposed tiles; SUMS: P and Q have second parts.
 template <int FORM>
 struct Maps {
   CUtensorMap P, Q, C, Z, R;
@@ -393,7 +425,11 @@ struct Maps<GATED> {
 };
 template <>
 struct Maps<STEP> {
-  CUtensorMap P, Q, P2, Q2, C, C2, R, R2, T, T2;
+  CUtensorMap P, Q, C, R, T;
+};
+template <>
+struct Maps<SUMS> {
+  CUtensorMap P, Q, P2, Q2, C;
 };
 
 // Tile t of the triangle i <= j, column by column.
@@ -456,11 +492,10 @@ __device__ __forceinline__ void gated_finish(const Params& p, const Maps<GATED>&
   put_rows<O, N>(&maps.C, p.tma_c, (O*)e.C, e.ldc, p.I, p.J, i0, j0, buf, false, g);
 }
 
-// STEP: the warp's 32 rows j and N = 64 columns i; R's two parts are in buf and buf2 (with_r).  A tile off the diagonal
-// of a symmetric C goes out a second time, transposed: 64 rows of 32 elements.
+// STEP: the warp's 32 rows j and N = 64 columns i; R is in buf (with_r).  A tile off the diagonal of a symmetric C goes out
+// a second time, transposed: 64 rows of 32 elements.
 template <class O, int N>
-__device__ __forceinline__ void step_finish(const Params& p, const Maps<STEP>& maps, int i0, int j0, bool twice, uint8_t* buf, uint8_t* buf2,
-                                            bool with_r, float* v) {
+__device__ __forceinline__ void step_finish(const Params& p, const Maps<STEP>& maps, int i0, int j0, bool twice, uint8_t* buf, bool with_r, float* v) {
   static_assert(N == 64, "16-bit outputs");
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -469,59 +504,49 @@ __device__ __forceinline__ void step_finish(const Params& p, const Maps<STEP>& m
 #pragma unroll
     for (int q = 0; q < N / 8; ++q) {
       float r[8];
-      const int at = lane * OROW + ((q ^ (lane & 7)) << 4);
-      widen8(*reinterpret_cast<const Eight<__half>*>(buf + at), r);
-      if (p.R2) {
-        float s[8];
-        widen8(*reinterpret_cast<const Eight<__half>*>(buf2 + at), s);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) r[x] += s[x];
-      }
+      widen8(*reinterpret_cast<const Eight<__half>*>(buf + lane * OROW + ((q ^ (lane & 7)) << 4)), r);
 #pragma unroll
       for (int x = 0; x < 8; ++x) v[8 * q + x] = fmaf(p.beta, r[x], v[8 * q + x]);
     }
-    __syncwarp();
-  } else {
-    if (lane == 0) tma_store_wait_read();
-    __syncwarp();
+  } else if (lane == 0) {
+    tma_store_wait_read();
   }
+  __syncwarp();
   put_rows<O, N>(&maps.C, p.tma_c, (O*)p.e.C, p.e.ldc, p.I, p.J, i0, j0, buf, true, v);
-  if (!twice && !p.C2) return;
-  // what is left of v after its first part
-  float low[N];
-#pragma unroll
-  for (int q = 0; q < N; ++q) low[q] = v[q] - to_float(from_float<O>(v[q]));
-  if (p.C2) put_rows<O, N>(&maps.C2, 1, (O*)p.C2, p.e.ldc, p.I, p.J, i0, j0, buf2, true, low);
   if (!twice) return;
   if (lane == 0) tma_store_wait_read();
   __syncwarp();
 #pragma unroll
-  for (int q = 0; q < N; ++q) {
-    reinterpret_cast<O*>(buf)[q * 32 + lane] = from_float<O>(v[q]);
-    if (p.C2) reinterpret_cast<O*>(buf2)[q * 32 + lane] = from_float<O>(low[q]);
-  }
+  for (int q = 0; q < N; ++q) reinterpret_cast<O*>(buf)[q * 32 + lane] = from_float<O>(v[q]);
   fence_smem_to_tma();
   __syncwarp();
   if (lane == 0) {
     tma_store_2d(&maps.T, buf, j0, i0);
-    if (p.C2) tma_store_2d(&maps.T2, buf2, j0, i0);
     tma_store_commit();
   }
 }
 
 template <int FORM, bool F8, class O>
-__global__ void __launch_bounds__(WTHREADS, 1) k_wide(const __grid_constant__ Maps<FORM> maps, const Params p) {
+__global__ void __launch_bounds__(wide_threads(FORM), 1) k_wide(const __grid_constant__ Maps<FORM> maps, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   WideBars* bars = reinterpret_cast<WideBars*>(smem + WSTAGES * WSTAGE + WEPI * WBUF);
   volatile int* abort_flag = &bars->abort;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform: the loops below keep their state in uniform registers
   const uint32_t rank = cluster_rank();
-  const bool triangle = FORM == STEP && p.triangle;
-  const int ntiles = triangle ? (int)((long long)p.tj * (p.tj + 1) / 2) : p.ti * p.tj, ncl = gridDim.x >> 1, cl = blockIdx.x >> 1;
+  const bool triangle = (FORM == STEP || FORM == SUMS) && p.triangle;
+  const int tiles = triangle ? (int)((long long)p.tj * (p.tj + 1) / 2) : p.ti * p.tj, ncl = gridDim.x >> 1, cl = blockIdx.x >> 1;
+  const int ntiles = FORM == SUMS ? tiles * p.parts : tiles;
+  // SUMS: all tiles of a part of k before the next part
   const auto tile_at = [&](int t, int& i, int& j) {
+    if (FORM == SUMS) t %= tiles;
     if (triangle) triangle_tile(t, i, j);
     else wide_tile(p, t, i, j);
+  };
+  const auto k_range = [&](int t, int& k0, int& k1) {
+    const int part = FORM == SUMS ? t / tiles : 0;
+    k0 = FORM == SUMS ? (int)((long long)p.kblocks * part / p.parts) : 0;
+    k1 = FORM == SUMS ? (int)((long long)p.kblocks * (part + 1) / p.parts) : p.kblocks;
   };
   constexpr int KE = F8 ? 128 : 64;   // k elements per stage
 
@@ -532,7 +557,7 @@ __global__ void __launch_bounds__(WTHREADS, 1) k_wide(const __grid_constant__ Ma
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->tfull[b], 1);
-      mbar_init(&bars->tempty[b], 2 * WEPI);   // one arrival per epilogue warp of the pair
+      mbar_init(&bars->tempty[b], 2 * epilogue_warps(FORM));   // one arrival per epilogue warp of the pair
       for (int x = 0; x < WEPI; ++x) mbar_init(&bars->rows[x][b], 1);
     }
     mbar_init(&bars->settled, 1);
@@ -561,7 +586,7 @@ __global__ void __launch_bounds__(WTHREADS, 1) k_wide(const __grid_constant__ Ma
     }
     uint32_t st = 0, ph = 0;
     int issued = 0;
-    const int per = FORM == STEP ? p.kblocks / p.segments : p.kblocks;   // k-blocks of a segment
+    const int per = FORM == SUMS ? p.kblocks / p.segments : p.kblocks;   // k-blocks of a segment
     bool ok = true;
     const uint32_t full0 = cluster_addr(smem_u32(&bars->full[0]), 0);
     for (int u = 0, t; ok && (t = wide_turn(p, cl, ncl, u)) < ntiles; ++u) {
@@ -570,12 +595,14 @@ __global__ void __launch_bounds__(WTHREADS, 1) k_wide(const __grid_constant__ Ma
       // GATED: the second CTA's half of operand B is the same rows of P's second half
       const int i0 = FORM == GATED ? ti * 128 + (int)rank * p.I : ti * 256 + (int)rank * 128, j0 = tj * 256 + (int)rank * 128;
       const CUtensorMap *tmP = &maps.P, *tmQ = &maps.Q;
-      for (int kb = 0, kx = 0; kb < p.kblocks; ++kb, ++kx) {
-        if constexpr (FORM == STEP) {   // the small products first
+      int kb0, kb1;
+      k_range(t, kb0, kb1);
+      for (int kb = kb0, kx = FORM == SUMS ? kb0 % per : 0; kb < kb1; ++kb, ++kx) {
+        if constexpr (FORM == SUMS) {   // the small products first
           if (kx == per) kx = 0;
-          if (kx == 0 && p.segments == 3) {
-            tmP = kb == per ? &maps.P2 : &maps.P;
-            tmQ = kb == 0 ? &maps.Q2 : &maps.Q;
+          if (p.segments == 3) {
+            tmP = kb / per == 1 ? &maps.P2 : &maps.P;
+            tmQ = kb < per ? &maps.Q2 : &maps.Q;
           }
         }
         ok = mbar_wait_warp(&bars->empty[st], ph ^ 1u, p.limit);
@@ -617,6 +644,36 @@ __global__ void __launch_bounds__(WTHREADS, 1) k_wide(const __grid_constant__ Ma
       bool ok = true;
       const uint32_t ps = desc_step(p.pk), qs = desc_step(p.qk), s0 = smem_u32(smem);
       const uint64_t da0 = tile_desc(s0, p.qk), db0 = tile_desc(s0 + WTILE, p.pk);
+      if constexpr (FORM == SUMS) {
+        uint32_t run = 0;   // accumulators filled
+        for (int u = 0, t; ok && (t = wide_turn(p, cl, ncl, u)) < ntiles; ++u) {
+          int kb0, kb1;
+          k_range(t, kb0, kb1);
+          for (int kb = kb0, in = 0; kb < kb1; ++kb) {
+            const uint32_t b = run & 1u;
+            if (in == 0) {
+              ok = mbar_wait_warp(&bars->tempty[b], (run >> 1 & 1u) ^ 1u, p.limit);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            ok = mbar_wait_warp(&bars->full[st], ph, p.limit);
+            if (!ok) break;
+            tc_fence_after();
+            const bool end = in + 1 == p.chunk || kb + 1 == kb1;
+            if (elect_one()) {
+              const uint64_t da = da0 + st * (WSTAGE >> 4), db = db0 + st * (WSTAGE >> 4);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) mma_any<true, F8>(tmem + b * 256, da + kk * qs, db + kk * ps, p.idesc, (in | kk) != 0);
+              mma_commit_pair(&bars->empty[st]);
+              if (end) mma_commit_pair(&bars->tfull[b]);
+            }
+            __syncwarp();
+            in = end ? 0 : in + 1;
+            run += end;
+            if (++st == (uint32_t)p.stages) st = 0, ph ^= 1u;
+          }
+        }
+      } else
       for (int u = 0; ok && wide_turn(p, cl, ncl, u) < ntiles; ++u) {
         const int b = u & 1;
         ok = mbar_wait_warp(&bars->tempty[b], ((uint32_t)(u >> 1) & 1u) ^ 1u, p.limit);
@@ -645,15 +702,16 @@ __global__ void __launch_bounds__(WTHREADS, 1) k_wide(const __grid_constant__ Ma
     }
   } else {
     const int quad = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* buf = smem + p.stages * WSTAGE + (warp - 2) * WBUF;   // with R: a second one WSTAGE further
+    uint8_t* buf = smem + p.stages * WSTAGE + (warp - 2) * WBUF;   // AFFINE with R: a second one WSTAGE further
     const uint32_t tempty[2] = {cluster_addr(smem_u32(&bars->tempty[0]), 0), cluster_addr(smem_u32(&bars->tempty[1]), 0)};
     uint32_t nrows = 0;   // parity of the two buffers' next R
+    uint32_t run = 0;     // SUMS: accumulators read
     for (int u = 0, t; (t = wide_turn(p, cl, ncl, u)) < ntiles; ++u) {
       const int b = u & 1;
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
       int ti, tj;
       tile_at(t, ti, tj);
-      const int j0 = tj * 256 + (int)rank * 128 + quad * 32, ibase = FORM == GATED ? ti * 128 + half * 64 : ti * 256 + half * 128;
+      const int j0 = tj * 256 + (int)rank * 128 + quad * 32, ibase = FORM == GATED ? ti * 128 + half * 64 : ti * 256 + half * (FORM == SUMS ? 64 : 128);
       constexpr int N = OROW / (int)sizeof(O);
       const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * 256 + half * (FORM == GATED ? 64 : 128));
       const auto accumulator_read = [&] {   // the next tile but one may have it
@@ -686,17 +744,47 @@ __global__ void __launch_bounds__(WTHREADS, 1) k_wide(const __grid_constant__ Ma
           if (ibase + c >= p.I) continue;
           gated_finish<O, N>(p, maps, ibase + c, j0, js, gs, ws, gb, wb, buf, reinterpret_cast<float*>(g), reinterpret_cast<float*>(w));
         }
+      } else if constexpr (FORM == SUMS) {
+        int kb0, kb1;
+        k_range(t, kb0, kb1);
+        float sum[64];
+#pragma unroll
+        for (int q = 0; q < 64; ++q) sum[q] = 0.0f;
+        bool lost = false;
+#pragma unroll 1
+        for (int kb = kb0; kb < kb1; kb += p.chunk, ++run) {
+          const uint32_t acc = run & 1u;
+          if (!mbar_wait_warp(&bars->tfull[acc], run >> 1 & 1u, p.limit)) {
+            if (lane == 0) give_up();
+            lost = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + acc * 256 + (uint32_t)(half * 64);
+#pragma unroll
+          for (int c = 0; c < 64; c += 16) {
+            float v[16];
+            tmem_ld16(from + (uint32_t)c, v);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) sum[c + q] += v[q];
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty[acc]);
+        }
+        if (lost) break;
+#pragma unroll
+        for (int c = 0; c < 64; c += 32)
+          if (j0 < p.J && ibase + c < p.I) put_rows<float, 32>(&maps.C, 1, nullptr, 0, 0, 0x7fffffff, ibase + c, t / tiles * p.jpad + j0, buf, false, sum + c);
       } else if constexpr (FORM == STEP) {
-        uint8_t* buf2 = buf + WSTAGE;
         const auto there = [&](int c) { return j0 < p.J && ibase + c < p.I; };
-        bool pending = false;   // R of the chunk at c is on its way
+        bool pending = false;   // R of the columns at c is on its way
         const auto ask = [&](int c) {
           pending = p.e.R && there(c);
           if (pending && lane == 0) {
             tma_store_wait_read();
-            mbar_arrive_expect_tx(&bars->rows[warp - 2][0], p.R2 ? 2 * WBUF : WBUF);
+            mbar_arrive_expect_tx(&bars->rows[warp - 2][0], WBUF);
             tma_load_2d(buf, &maps.R, &bars->rows[warp - 2][0], ibase + c, j0);
-            if (p.R2) tma_load_2d(buf2, &maps.R2, &bars->rows[warp - 2][0], ibase + c, j0);
           }
         };
         ask(0);
@@ -724,7 +812,7 @@ __global__ void __launch_bounds__(WTHREADS, 1) k_wide(const __grid_constant__ Ma
             }
             nrows ^= 1u;
           }
-          step_finish<O, N>(p, maps, ibase + c, j0, triangle && ti != tj, buf, buf2, pending, reinterpret_cast<float*>(v));
+          step_finish<O, N>(p, maps, ibase + c, j0, triangle && ti != tj, buf, pending, reinterpret_cast<float*>(v));
         }
         if (lost) break;
       } else {
@@ -821,7 +909,7 @@ struct ThinBars {
 };
 
 // GATED: 64 outputs, the first 64 rows of the tile from P's first half and the others from its second; both sums of an
-// output meet in shared memory.
+// output meet in shared memory.  STEP goes through it too, for accesses of four elements.
 struct ThinMaps {
   CUtensorMap P, Q, P2, Q2;   // P2, Q2: STEP's second parts
 };
@@ -969,21 +1057,12 @@ __global__ void __launch_bounds__(TTHREADS) k_thin(const __grid_constant__ ThinM
 #pragma unroll
         for (int q = 0; q < 16; ++q) v[q] = 0.0f;
       }
-      if (FORM == GATED || split > 1) {
+      if (FORM != AFFINE || split > 1) {
 #pragma unroll
         for (int q = 0; q < 16; ++q)
           if (c + q < ncols) to[(c + q) * sb] = v[q];
       } else if (i < p.I) {
-        if constexpr (FORM == STEP) {
-#pragma unroll
-          for (int q = 0; q < 16; ++q)
-            if (c + q < ncols) {
-              const float one[1] = {v[q]};
-              finish_step<O, 1>(p, i, j0 + c + q, one);
-            }
-        } else {
-          thin_store16<O>(p, i, j0 + c, v);
-        }
+        thin_store16<O>(p, i, j0 + c, v);
       }
     }
     if (split > 1) {
@@ -999,7 +1078,7 @@ __global__ void __launch_bounds__(TTHREADS) k_thin(const __grid_constant__ ThinM
       }
     }
   }
-  if (FORM == GATED || split > 1) {
+  if (FORM != AFFINE || split > 1) {
     bool got = true;
     const float* parts = received;
     if (split > 1) {
@@ -1034,7 +1113,7 @@ __global__ void __launch_bounds__(TTHREADS) k_thin(const __grid_constant__ ThinM
         float w[4] = {y.x, y.y, y.z, y.w};
         finish_gated4<O>(p, i, j, v, w);
       } else if constexpr (FORM == STEP) {
-        finish_step<O, 4>(p, i, j, v);
+        finish_step4<O>(p, i, j, v);
       } else {
         thin_finish4<O>(p, i, j, v);
       }
@@ -1183,7 +1262,7 @@ cr_status launch_wide(const Maps<FORM>& maps, const Params& p, long long tiles, 
   CR_TRY(allow_shared((const void*)k_wide<FORM, F8, O>, WSMEM, done));
   const int pairs = std::min((long long)sm_count() / 2, tiles);
   TimedScope ts(Names<FORM>::wide, stream);
-  CR_CUDA(launch_after(k_wide<FORM, F8, O>, 2 * pairs, WTHREADS, WSMEM, 2, stream, maps, p));
+  CR_CUDA(launch_after(k_wide<FORM, F8, O>, 2 * pairs, wide_threads(FORM), WSMEM, 2, stream, maps, p));
   CR_CHECK_LAUNCH(Names<FORM>::wide);
   return CR_OK;
 }
@@ -1243,16 +1322,24 @@ struct Choice {
   bool wide;
   int bn, split, stages;
   double us;
+  int parts = 0;   // wide, of the FORM STEP: by way of SUMS, over so many parts of k
 };
+// sums: a STEP with two parts, whose wide form is SUMS and whose thin one is for short sums.
 template <int FORM>
-Choice choose(int I, int J, int kblocks, bool qk, bool triangle = false) {
+Choice choose(int I, int J, int kblocks, bool qk, bool triangle = false, bool sums = false) {
   Choice best = {false, 0, 1, 0, 1e30};
   const int sms = sm_count();
   const auto tiles = [](int n, int t) { return (n + t - 1) / t; };
   // Wide: rounds of tiles over the CTA pairs, 0.27 to 0.3 us per k-block, or the epilogue of a tile.
-  if (J > 128) {
+  if (J > 128 || sums) {
     const long long n = tiles(J, 256), t = triangle ? n * (n + 1) / 2 : tiles(I, 256) * n, rounds = (t + sms / 2 - 1) / (sms / 2);
     best = {true, 0, 1, 0, 6.5 + rounds * std::max(kblocks * 0.29 + 0.6, 3.3)};
+    // By way of SUMS: tiles over parts of k, which cost a launch and the way of every part's sums through L2.
+    for (int parts = 1; FORM == STEP && parts <= 16 && (parts == 1 || kblocks >= 4 * parts); ++parts) {
+      const double r = (double)((t * parts + sms / 2 - 1) / (sms / 2));
+      const double us = 11.0 + r * std::max(tiles(kblocks, parts) * 0.29 + 0.6, 2.0) + 1.2e-6 * parts * I * J * (triangle ? 0.5 : 1.0);
+      if (us < best.us || (sums && parts == 1)) best = {true, 0, 1, 0, us, parts};
+    }
   }
   // Thin: parts of k for which all clusters are resident at once, with three stages or more and two
   // k-blocks or more for each CTA; a second wave of CTAs costs more than longer parts (K = 4096,
@@ -1266,6 +1353,7 @@ Choice choose(int I, int J, int kblocks, bool qk, bool triangle = false) {
     const long long t = (long long)tiles(I, 128) * tiles(J, bn);
     for (int split = 8; split >= 1; split /= 2) {
       if (split > 1 && kblocks < 2 * split) continue;
+      if (sums && tiles(kblocks, split) > 8) continue;
       int per = 1;
       while (per < 3 && t > resident_clusters<FORM>(split, per)) ++per;
       if (t > resident_clusters<FORM>(split, per)) {
