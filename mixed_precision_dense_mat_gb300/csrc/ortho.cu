@@ -122,9 +122,35 @@ __global__ void __launch_bounds__(NT) k_ortho_scale(const T* G, int ld, int K, i
   }
 }
 
-// C = alpha (sum of the parts) + beta R for 64 x 64 outputs, to FP16 with the rest after it in C2 (may be NULL), or to the
-// caller's matrix; TRI: C is symmetric, parts hold the 256-wide tiles ti <= tj, and C(j, i) is stored too.
-constexpr int JTILE = 64;
+// C = alpha (sum of the parts) + beta R for 32 x 32 outputs, four to a thread, to FP16 with the rest after it in C2 (may be NULL), or
+// to the caller's matrix; TRI: C is symmetric, parts hold the 256-wide tiles ti <= tj, and C(j, i) is stored too.  Bound by
+// latency and L2: all parts of an output are on their way at once.
+constexpr int JTILE = 32;
+template <class O>
+struct alignas(4 * sizeof(O)) FourOf {
+  O x[4];
+};
+// Four elements of a column from `at` on, the first `n` of them if they are fewer.
+template <class O>
+__device__ __forceinline__ void put4(O* C, O* C2, size_t at, int n, bool vec, const float (&v)[4]) {
+  FourOf<O> o, rest;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    o.x[q] = from_float<O>(v[q]);
+    rest.x[q] = from_float<O>(v[q] - to_float(o.x[q]));
+  }
+  if (vec && n >= 4) {
+    *reinterpret_cast<FourOf<O>*>(C + at) = o;
+    if (C2) *reinterpret_cast<FourOf<O>*>(C2 + at) = rest;
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q < n) {
+        C[at + q] = o.x[q];
+        if (C2) C2[at + q] = rest.x[q];
+      }
+  }
+}
 template <class O, bool TRI>
 __global__ void __launch_bounds__(NT) k_ortho_sum(const float* part, int parts, int ldp, int jpad, int I, int J, const __half* R, const __half* R2,
                                                   int ldr, float alpha, float beta, O* C, O* C2, int ldc, int vec) {
@@ -133,78 +159,38 @@ __global__ void __launch_bounds__(NT) k_ortho_sum(const float* part, int parts, 
   let_next_start();
   wait_for_previous();
   if (TRI && i0 / 256 > j0 / 256) return;
-  const bool twice = TRI && i0 / 256 != j0 / 256;
-  const int x = threadIdx.x % 16 * 4, i = i0 + x;
-#pragma unroll
-  for (int y = threadIdx.x / 16; y < JTILE; y += 16) {
-    const int j = j0 + y;
-    float v[4] = {};
-    if (j < J && i < I) {
-      const float* from = part + (size_t)j * ldp + i;
-      float4 z = *reinterpret_cast<const float4*>(from);
-#pragma unroll 4
-      for (int q = 1; q < parts; ++q) {
-        const float4 w = *reinterpret_cast<const float4*>(from + (size_t)q * jpad * ldp);
-        z.x += w.x;
-        z.y += w.y;
-        z.z += w.z;
-        z.w += w.w;
-      }
-      v[0] = z.x * alpha;
-      v[1] = z.y * alpha;
-      v[2] = z.z * alpha;
-      v[3] = z.w * alpha;
-      if (R) {
-        const auto four = [&](const __half* m, float (&f)[4]) {
-          const uint2 w = *reinterpret_cast<const uint2*>(m + (size_t)j * ldr + i);
-          const float2 a = widen2(w.x, __half{}), b = widen2(w.y, __half{});
-          f[0] = a.x;
-          f[1] = a.y;
-          f[2] = b.x;
-          f[3] = b.y;
-        };
-        float r[4], t[4] = {};
-        four(R, r);
-        if (R2) four(R2, t);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = fmaf(beta, r[q] + t[q], v[q]);
-      }
-      struct alignas(4 * sizeof(O)) Four {
-        O x[4];
-      } o, rest;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        o.x[q] = from_float<O>(v[q]);
-        rest.x[q] = from_float<O>(v[q] - to_float(o.x[q]));
-      }
-      const size_t at = (size_t)j * ldc + i;
-      if (vec && i + 4 <= I) {
-        *reinterpret_cast<Four*>(C + at) = o;
-        if (C2) *reinterpret_cast<Four*>(C2 + at) = rest;
-      } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (i + q < I) {
-            C[at + q] = o.x[q];
-            if (C2) C2[at + q] = rest.x[q];
-          }
-      }
+  const int x = threadIdx.x % 8 * 4, y = threadIdx.x / 8, i = i0 + x, j = j0 + y;
+  float v[4] = {};
+  if (j < J && i < I) {
+    const float* from = part + (size_t)j * ldp + i;
+    const size_t step = (size_t)jpad * ldp;
+    uint2 r = make_uint2(0, 0), r2 = make_uint2(0, 0);
+    if (R) r = *reinterpret_cast<const uint2*>(R + (size_t)j * ldr + i);
+    if (R2) r2 = *reinterpret_cast<const uint2*>(R2 + (size_t)j * ldr + i);
+    float4 z = *reinterpret_cast<const float4*>(from);
+#pragma unroll 8
+    for (int q = 1; q < parts; ++q) {
+      const float4 w = *reinterpret_cast<const float4*>(from + q * step);
+      z.x += w.x;
+      z.y += w.y;
+      z.z += w.z;
+      z.w += w.w;
     }
-    if (twice) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) turned[x + q][y] = v[q];
-    }
+    const float2 a = widen2(r.x, __half{}), b = widen2(r.y, __half{}), c = widen2(r2.x, __half{}), d = widen2(r2.y, __half{});
+    v[0] = fmaf(beta, a.x + c.x, z.x * alpha);
+    v[1] = fmaf(beta, a.y + c.y, z.y * alpha);
+    v[2] = fmaf(beta, b.x + d.x, z.z * alpha);
+    v[3] = fmaf(beta, b.y + d.y, z.w * alpha);
+    put4(C, C2, (size_t)j * ldc + i, I - i, vec, v);
   }
-  if (!twice) return;
+  if (!TRI || i0 / 256 == j0 / 256) return;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) turned[x + q][y] = v[q];
   __syncthreads();
-  for (int e = threadIdx.x; e < JTILE * JTILE; e += NT) {
-    const int a = e / JTILE, b = e % JTILE, col = i0 + a, row = j0 + b;   // C(row, col)
-    if (col < I && row < J) {
-      const float v = turned[a][b];
-      const O o = from_float<O>(v);
-      C[(size_t)col * ldc + row] = o;
-      if (C2) C2[(size_t)col * ldc + row] = from_float<O>(v - to_float(o));
-    }
+  const int col = i0 + y, row = j0 + x;   // C(row .. row + 3, col)
+  if (col < I && row < J) {
+    const float t[4] = {turned[y][x], turned[y][x + 1], turned[y][x + 2], turned[y][x + 3]};
+    put4(C, C2, (size_t)col * ldc + row, J - row, vec, t);
   }
 }
 
