@@ -169,6 +169,55 @@ __device__ __forceinline__ void each_field(const Fields& p, int t, R&& run, E&& 
   }
 }
 
+// Activations and slopes as in ops.cuh, two at a time, with reciprocals shared between them; sigmoids end at 2^-62, so that their
+// products do not overflow: silu(z) for z below -43 is -43 2^-62.
+template <int P>
+__device__ __forceinline__ Floats<P> clamped(Floats<P> z, float low, float high) {
+#pragma unroll
+  for (int o = 0; o < P; ++o) z.x[o] = clamp_high(clamp_low(z.x[o], low), high);
+  return z;
+}
+template <int ACT, int P>
+__device__ __forceinline__ Floats<P> act_of(Floats<P> z) {
+  if constexpr (ACT == CR_ACT_SILU) {
+#pragma unroll
+    for (int o = 0; o < P; ++o) z.x[o] = clamp_low(z.x[o], -43.0f);
+    return mul(z, rcp_shared(add(exp2_fast(mul(z, all_of<P>(-LOG2E))), all_of<P>(1.0f))));
+  } else if constexpr (ACT == CR_ACT_GELU) {   // z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|))
+    Floats<P> a, g;
+#pragma unroll
+    for (int o = 0; o < P; ++o) {
+      a.x[o] = clamp_high(fabsf(z.x[o]), 30.0f);
+      z.x[o] = clamp_low(z.x[o], 0.0f);
+    }
+    return fma(a, minus_tail<P, true>(a, g), z);
+  } else {
+    return activate<ACT, P>(z);
+  }
+}
+template <int ACT, int P>
+__device__ __forceinline__ Floats<P> slope_of(Floats<P> z) {
+  const Floats<P> one = all_of<P>(1.0f);
+  if constexpr (ACT == CR_ACT_SILU) {
+    z = clamped(z, -43.0f, 88.0f);
+    const Floats<P> e = exp2_fast(mul(z, all_of<P>(-LOG2E))), s = rcp_shared(add(e, one));
+    return mul(s, fma(z, mul(e, s), one));
+  } else if constexpr (ACT == CR_ACT_GELU) {
+    z = clamped(z, -30.0f, 30.0f);
+    Floats<P> a, g, phi;
+#pragma unroll
+    for (int o = 0; o < P; ++o) a.x[o] = fabsf(z.x[o]);
+    const Floats<P> m = minus_tail<P, true>(a, g);
+#pragma unroll
+    for (int o = 0; o < P; ++o) phi.x[o] = z.x[o] < 0.0f ? -m.x[o] : 1.0f + m.x[o];
+    return fma(mul(z, all_of<P>(0.39894228040143268f)), g, phi);
+  } else {
+#pragma unroll
+    for (int o = 0; o < P; ++o) z.x[o] = activation_slope<ACT>(z.x[o]);
+    return z;
+  }
+}
+
 // ---------------------------------------------------------------- forward
 template <class T, int TX, int V>
 __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_stats(const T* X, int ldx, const Fields p, float2* part) {
@@ -330,7 +379,7 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_apply(const T* X, int ld
           raw[q].widen(x);
 #pragma unroll
           for (int e = 0; e < V; e += P) {   // m is minus the mean
-            const Floats<P> z = activate<ACT, P>(fma(add(pair_at(x, e), pair_at(m, e)), pair_at(s, e), pair_at(bt, e)));
+            const Floats<P> z = act_of<ACT, P>(fma(add(pair_at(x, e), pair_at(m, e)), pair_at(s, e), pair_at(bt, e)));
 #pragma unroll
             for (int o = 0; o < P; ++o) x[e + o] = z.x[o];
           }
@@ -418,7 +467,13 @@ __global__ void __launch_bounds__(NT) k_gnorm_small(const T* X, int ldx, const F
         raw[k].widen(x);
 #pragma unroll
         for (int q = 0; q < V; ++q) x[q] = fmaf(x[q] - mean, sc[q], bt[q]);
-        activate_each<ACT, V>(x);
+        constexpr int P = V > 1 ? 2 : 1;
+#pragma unroll
+        for (int q = 0; q < V; q += P) {
+          const Floats<P> z = act_of<ACT, P>(pair_at(x, q));
+#pragma unroll
+          for (int o = 0; o < P; ++o) x[q + o] = z.x[o];
+        }
         store<T, V>(Y + at(e + k * step) * ldy + i0 + tx * V, x);
       }
   }
@@ -452,10 +507,10 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_sums(const T* X, int ldx
       float m[V], r[V];
       each_feature<V>(p, i, [&](int e, int g) {
         const size_t at = (size_t)f * lds + min(g, p.groups - 1);
-        m[e] = mean[at];
+        m[e] = -mean[at];
         r[e] = rstd[at];
       });
-      constexpr int B = sizeof(T) == 2 ? 4 : 2;
+      constexpr int B = sizeof(T) == 2 ? 4 : 2, P = V > 1 ? 2 : 1;
       const T *xs = X + (size_t)(a + ty) * ldx + i, *ds = dY + (size_t)(a + ty) * lddy + i;
       in_batches<B, TY, Pair<T, V>>(a + ty, b, [&](Pair<T, V>& raw, int j) {
         raw.x.load(xs + (size_t)j * ldx);
@@ -467,11 +522,16 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_sums(const T* X, int ldx
           raw[q].x.widen(x);
           raw[q].d.widen(d);
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float h = __fmul_rn(x[e] - m[e], r[e]);
-            if (ACT != CR_ACT_NONE) d[e] = __fmul_rn(d[e], activation_slope<ACT>(fmaf(h, gm[e], bt[e])));
-            sb[e] += d[e];
-            sg[e] = fmaf(d[e], h, sg[e]);
+          for (int e = 0; e < V; e += P) {   // m is minus the mean
+            const Floats<P> h = mul(add(pair_at(x, e), pair_at(m, e)), pair_at(r, e));
+            Floats<P> dz = pair_at(d, e);
+            if (ACT != CR_ACT_NONE) dz = mul(dz, slope_of<ACT, P>(fma(h, pair_at(gm, e), pair_at(bt, e))));
+            const Floats<P> b1 = add(pair_at(sb, e), dz), g1 = fma(dz, h, pair_at(sg, e));
+#pragma unroll
+            for (int o = 0; o < P; ++o) {
+              sb[e + o] = b1.x[o];
+              sg[e + o] = g1.x[o];
+            }
           }
         }
       });
@@ -513,13 +573,40 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_sums(const T* X, int ldx
   }
 }
 
-// dX = r (gamma dz - mean(gamma dz) - h mean(gamma dz h)), means over the group.
+// total[D] = the sum of the rows of part (rows x D) for 32 features from i0 on, in a fixed order, by a block.
+__device__ __forceinline__ void sum_rows(const float* part, int rows, int D, int i0, float* total, float (&red)[NT / 32][33]) {
+  const int i = i0 + threadIdx.x % 32, w = threadIdx.x / 32;
+  float s = 0.0f;
+  if (i < D) {
+#pragma unroll 8
+    for (int r = w; r < rows; r += NT / 32) s += part[(size_t)r * D + i];
+  }
+  red[w][threadIdx.x % 32] = s;
+  __syncthreads();
+  if (w == 0 && i < D) {
+    for (int y = 1; y < NT / 32; ++y) s += red[y][threadIdx.x];
+    total[i] = s;
+  }
+}
+
+// dX = r (gamma dz - mean(gamma dz) - h mean(gamma dz h)), means over the group, by the first `tiles` blocks (0: not wanted); the
+// others sum up the tiles' parts of dgamma and dbeta, 32 features each.
 template <class T, int TX, int V, int ACT>
 __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_dx(const T* X, int ldx, const T* dY, int lddy, const Fields p, const float2* part,
                                                  const float* gamma, const float* beta, const float* mean, const float* rstd, int lds, T* dX,
-                                                 int lddx) {
+                                                 int lddx, unsigned tiles, const float* pgamma, const float* pbeta, float* dgamma,
+                                                 float* dbeta) {
   constexpr int TY = NT / TX, FW = TX * V;
   __shared__ float2 stat[FW];
+  __shared__ float red[NT / 32][33];
+  if (blockIdx.x >= tiles) {
+    let_next_start();
+    wait_for_previous();
+    const unsigned b = blockIdx.x - tiles, per = (p.D + 31) / 32;
+    const bool second = !dgamma || b >= per;
+    sum_rows(second ? pbeta : pgamma, p.tiles, p.D, (int)(b % per) * 32, second ? dbeta : dgamma, red);
+    return;
+  }
   const int fb = blockIdx.x % p.blocks, t = blockIdx.x / p.blocks;
   const int tx = threadIdx.x % TX, ty = threadIdx.x / TX, i0 = fb * FW, i = i0 + tx * V;
   const int width = min(FW, p.D - i0), g0 = i0 / p.group, g1 = (i0 + width - 1) / p.group;
@@ -553,12 +640,12 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_dx(const T* X, int ldx, 
       each_feature<V>(p, i, [&](int e, int g) {
         const int k = min(g, g1);
         const size_t at = (size_t)f * lds + k;
-        m[e] = mean[at];
+        m[e] = -mean[at];
         r[e] = rstd[at];
-        c1[e] = stat[k - g0].x;
-        c2[e] = stat[k - g0].y;
+        c1[e] = -r[e] * stat[k - g0].x;
+        c2[e] = -r[e] * stat[k - g0].y;
       });
-      constexpr int B = sizeof(T) == 2 ? 4 : 2;
+      constexpr int B = sizeof(T) == 2 ? 4 : 2, P = V > 1 ? 2 : 1;
       const int last = a + ty < b ? b - 1 - (b - 1 - a - ty) % TY : 0;   // from the last column to the first, as k_gnorm_apply
       const T *xs = X + (size_t)last * ldx + i, *ds = dY + (size_t)last * lddy + i;
       T* to = dX + (size_t)last * lddx + i;
@@ -572,10 +659,13 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_dx(const T* X, int ldx, 
           raw[q].x.widen(x);
           raw[q].d.widen(d);
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float h = __fmul_rn(x[e] - m[e], r[e]);
-            if (ACT != CR_ACT_NONE) d[e] = __fmul_rn(d[e], activation_slope<ACT>(fmaf(h, gm[e], bt[e])));
-            x[e] = __fmul_rn(r[e], fmaf(-h, c2[e], fmaf(d[e], gm[e], -c1[e])));
+          for (int e = 0; e < V; e += P) {   // m is minus the mean, c1 and c2 are the sums times -r
+            const Floats<P> h = mul(add(pair_at(x, e), pair_at(m, e)), pair_at(r, e));
+            Floats<P> dz = pair_at(d, e);
+            if (ACT != CR_ACT_NONE) dz = mul(dz, slope_of<ACT, P>(fma(h, pair_at(gm, e), pair_at(bt, e))));
+            const Floats<P> y = fma(h, pair_at(c2, e), fma(mul(dz, pair_at(gm, e)), pair_at(r, e), pair_at(c1, e)));
+#pragma unroll
+            for (int o = 0; o < P; ++o) x[e + o] = y.x[o];
           }
           store<T, V>(to - (size_t)(j + q * TY) * lddx, x);
         }
@@ -745,15 +835,13 @@ extern "C" cr_status cr_group_norm_backward(int type, const void* d_X, int ldx, 
                                  d_mean, d_rstd, lds, d_dX ? part : nullptr, d_dgamma ? pgamma : nullptr, d_dbeta ? pbeta : nullptr));
             CR_CHECK_LAUNCH("k_gnorm_sums");
           }
-          if (!d_dX) return CR_OK;
           TimedScope ts("k_gnorm_dx", stream);
-          CR_CUDA(launch_after(k_gnorm_dx<E, TX, V, ACT>, grid, NT, 0, 1, stream, (const E*)d_X, ldx, (const E*)d_dY, lddy, p, part, d_gamma, d_beta,
-                               d_mean, d_rstd, lds, (E*)d_dX, lddx));
+          const unsigned sums = (unsigned)((D + 31) / 32) * ((d_dgamma ? 1 : 0) + (d_dbeta ? 1 : 0)), tiles = d_dX ? grid : 0;
+          CR_CUDA(launch_after(k_gnorm_dx<E, TX, V, ACT>, tiles + sums, NT, 0, 1, stream, (const E*)d_X, ldx, (const E*)d_dY, lddy, p, part, d_gamma,
+                               d_beta, d_mean, d_rstd, lds, (E*)d_dX, lddx, tiles, pgamma, pbeta, d_dgamma, d_dbeta));
           CR_CHECK_LAUNCH("k_gnorm_dx");
           return CR_OK;
         }));
-        if (d_dgamma) CR_TRY(add_rows(pgamma, p.tiles, D, d_dgamma, stream));
-        if (d_dbeta) CR_TRY(add_rows(pbeta, p.tiles, D, d_dbeta, stream));
         return CR_OK;
       };
       const cr_status st = run();
