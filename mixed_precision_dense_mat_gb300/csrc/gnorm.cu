@@ -128,18 +128,19 @@ __device__ __forceinline__ Floats<V == 1 ? 1 : 2> pair_at(const float (&v)[V], i
   else return {{v[e], v[e + 1]}};
 }
 
-// Groups of the block are reduced by LANES threads each, all of them at once where the block has up to NT / LANES.
-constexpr int LANES = 8;
-__device__ __forceinline__ float lanes_sum(float x) {
+// A block's groups g0 .. g1 are reduced by as many threads each as there are, 8 to 32: use(g, lane, lanes), all threads of a warp
+// together; g may pass g1 in the last turn.
+__device__ __forceinline__ float lanes_sum(float x, int lanes) {
+  if (lanes > 16) x += __shfl_xor_sync(0xffffffffu, x, 16);
+  if (lanes > 8) x += __shfl_xor_sync(0xffffffffu, x, 8);
 #pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-// Calls use(g, lane) for every group g0 .. g1, all threads of a warp together; g may pass g1 in the last turn.
 template <class U>
 __device__ __forceinline__ void each_group(int g0, int g1, U&& use) {
-  const int lane = threadIdx.x % LANES;
-  for (int g = g0 + (int)threadIdx.x / LANES; g - (int)(threadIdx.x & 31) / LANES <= g1; g += NT / LANES) use(g, lane);
+  const int shift = g1 - g0 < NT / 32 ? 5 : g1 - g0 < NT / 16 ? 4 : 3, lanes = 1 << shift, lane = threadIdx.x & (lanes - 1);
+  for (int g = g0 + ((int)threadIdx.x >> shift); g - ((int)(threadIdx.x & 31) >> shift) <= g1; g += NT >> shift) use(g, lane, lanes);
 }
 // The groups of V features from i on.
 template <int V, class U>
@@ -283,31 +284,31 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_stats(const T* X, int ld
     }
     __syncthreads();
     // features of a group have the same number of columns: their mean, and their deviations about it
-    each_group(i0 / p.group, (i0 + width - 1) / p.group, [&](int g, int lane) {
+    each_group(i0 / p.group, (i0 + width - 1) / p.group, [&](int g, int lane, int lanes) {
       const int x0 = max(0, g * p.group - i0), x1 = min(width, (g + 1) * p.group - i0);
       float s = 0.0f, d2 = 0.0f;
       const float at = x0 < x1 ? feature[x0].x : 0.0f;
-      for (int x = x0 + lane; x < x1; x += LANES) s += feature[x].x - at;
-      const float m = at + lanes_sum(s) / (float)(x1 - x0);
-      for (int x = x0 + lane; x < x1; x += LANES) {
+      for (int x = x0 + lane; x < x1; x += lanes) s += feature[x].x - at;
+      const float m = at + lanes_sum(s, lanes) / (float)(x1 - x0);
+      for (int x = x0 + lane; x < x1; x += lanes) {
         const float d = feature[x].x - m;
         d2 += fmaf(d * (float)(b - a), d, feature[x].y);
       }
-      d2 = lanes_sum(d2);
+      d2 = lanes_sum(d2, lanes);
       if (lane == 0 && x0 < x1) part[share(p, t, f, fb, g)] = make_float2(m, d2);
     });
   }, [](int) {});
 }
 
-// The tiles and feature blocks that group g of the field in columns begin .. end - 1 is spread over, by LANES threads:
+// The tiles and feature blocks that group g of the field in columns begin .. end - 1 is spread over, by `lanes` threads:
 // get(share, columns, features).
 template <int FW, class G>
-__device__ __forceinline__ void each_share(const Fields& p, int f, int begin, int end, int t0, int t1, int g, int lane, G&& get) {
+__device__ __forceinline__ void each_share(const Fields& p, int f, int begin, int end, int t0, int t1, int g, int lane, int lanes, G&& get) {
   const int i0 = g * p.group, i1 = i0 + p.group, b0 = i0 / FW, nb = (i1 - 1) / FW - b0 + 1;
   for (int fb = b0; fb < b0 + nb; ++fb) {
     const int features = min(i1, (fb + 1) * FW) - max(i0, fb * FW);
 #pragma unroll 4
-    for (int t = t0 + lane; t <= t1; t += LANES)
+    for (int t = t0 + lane; t <= t1; t += lanes)
       get(share(p, t, f, fb, g), min(end, (t + 1) * p.cols) - max(begin, t * p.cols), features);
   }
 }
@@ -332,23 +333,23 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_apply(const T* X, int ld
   each_field(p, t, [&](int f, int a, int b, int begin, int end) {
     __syncthreads();
     const int t0 = begin / p.cols, t1 = (end - 1) / p.cols;
-    each_group(g0, g1, [&](int g, int lane) {
+    each_group(g0, g1, [&](int g, int lane, int lanes) {
       // the mean about one share's mean, then the deviations about it
       const bool there = g <= g1;
       const float n = (float)(end - begin) * (float)p.group;
       const float at = there ? part[share(p, t0, f, g * p.group / FW, g)].x : 0.0f;
       float s = 0.0f, d2 = 0.0f;
       if (there)
-        each_share<FW>(p, f, begin, end, t0, t1, g, lane,
+        each_share<FW>(p, f, begin, end, t0, t1, g, lane, lanes,
                        [&](size_t k, int cols, int features) { s = fmaf(part[k].x - at, (float)cols * (float)features, s); });
-      const float mean = at + lanes_sum(s) / n;
+      const float mean = at + lanes_sum(s, lanes) / n;
       if (there)
-        each_share<FW>(p, f, begin, end, t0, t1, g, lane, [&](size_t k, int cols, int features) {
+        each_share<FW>(p, f, begin, end, t0, t1, g, lane, lanes, [&](size_t k, int cols, int features) {
           const float2 w = part[k];
           const float d = w.x - mean;
           d2 += fmaf(d * ((float)cols * (float)features), d, w.y);
         });
-      d2 = lanes_sum(d2);
+      d2 = lanes_sum(d2, lanes);
       if (there && lane == 0) {
         const float r = 1.0f / sqrtf(d2 / n + eps);
         stat[g - g0] = make_float2(mean, r);
@@ -552,16 +553,16 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_sums(const T* X, int ldx
     }
     __syncthreads();
     if (part) {
-      each_group(i0 / p.group, (i0 + width - 1) / p.group, [&](int g, int lane) {
+      each_group(i0 / p.group, (i0 + width - 1) / p.group, [&](int g, int lane, int lanes) {
         const int x0 = max(0, g * p.group - i0), x1 = min(width, (g + 1) * p.group - i0);
         float2 s = make_float2(0.0f, 0.0f);
-        for (int x = x0 + lane; x < x1; x += LANES) {
+        for (int x = x0 + lane; x < x1; x += lanes) {
           const float w = gamma ? gamma[i0 + x] : 1.0f;
           s.x = fmaf(w, feature[x].x, s.x);
           s.y = fmaf(w, feature[x].y, s.y);
         }
-        s.x = lanes_sum(s.x);
-        s.y = lanes_sum(s.y);
+        s.x = lanes_sum(s.x, lanes);
+        s.y = lanes_sum(s.y, lanes);
         if (lane == 0 && x0 < x1) part[share(p, t, f, fb, g)] = s;
       });
     }
@@ -621,16 +622,16 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_dx(const T* X, int ldx, 
   each_field(p, t, [&](int f, int a, int b, int begin, int end) {
     __syncthreads();
     const int t0 = begin / p.cols, t1 = (end - 1) / p.cols;
-    each_group(g0, g1, [&](int g, int lane) {
+    each_group(g0, g1, [&](int g, int lane, int lanes) {
       float2 s = make_float2(0.0f, 0.0f);
       if (g <= g1)
-        each_share<FW>(p, f, begin, end, t0, t1, g, lane, [&](size_t k, int, int) {
+        each_share<FW>(p, f, begin, end, t0, t1, g, lane, lanes, [&](size_t k, int, int) {
           const float2 w = part[k];
           s.x += w.x;
           s.y += w.y;
         });
-      s.x = lanes_sum(s.x);
-      s.y = lanes_sum(s.y);
+      s.x = lanes_sum(s.x, lanes);
+      s.y = lanes_sum(s.y, lanes);
       const float n = (float)(end - begin) * (float)p.group;
       if (lane == 0 && g <= g1) stat[g - g0] = make_float2(s.x / n, s.y / n);
     });
@@ -686,7 +687,7 @@ cr_status with_tile(int D, bool vec, F&& f) {
   if (!vec) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
   const auto padded = [&](int w) { return (D + w * V - 1) / (w * V) * (w * V); };
   const int best = padded(8);
-  if (16ll * padded(32) <= 17ll * best) return f(integral_constant<int, 32>{}, integral_constant<int, V>{});
+  if (4ll * padded(32) <= 5ll * best) return f(integral_constant<int, 32>{}, integral_constant<int, V>{});
   if (padded(16) == best) return f(integral_constant<int, 16>{}, integral_constant<int, V>{});
   return f(integral_constant<int, 8>{}, integral_constant<int, V>{});
 }
@@ -747,7 +748,7 @@ extern "C" cr_status cr_group_norm(int type, const void* d_X, int ldx, int D, in
     constexpr int EB = sizeof(E), W = 16 / EB;
     const bool vec = D % W == 0 && aligned(d_X, ldx, EB, 16) && aligned(d_Y, ldy, EB, 16);
     const int group = D / groups;
-    if ((long long)T * (vec && group % W == 0 ? group / W : group) <= SMALL * NT && (long long)n * groups <= 8 * sm_count() && group <= NT) {
+    if ((long long)T * (vec && group % W == 0 ? group / W : group) <= SMALL * NT && (long long)n * groups <= 128 * sm_count() && group <= NT) {
       Fields p = {};
       p.off = d_off;
       p.n = n;

@@ -51,6 +51,24 @@ __device__ __forceinline__ void scale_of(const Squares& s, float* f) {
   f[1] = __int_as_float((h + 127) << 23);
   f[2] = __int_as_float((E - h + 127) << 23);
 }
+// V elements: 16 bytes, or one.
+template <class T, int V>
+__device__ __forceinline__ void load_some(const T* p, float* v) {
+  if constexpr (V == 1) {
+    v[0] = to_float(p[0]);
+  } else if constexpr (sizeof(T) == 4) {
+    const float4 w = *reinterpret_cast<const float4*>(p);
+    v[0] = w.x;
+    v[1] = w.y;
+    v[2] = w.z;
+    v[3] = w.w;
+  } else {
+    float w[8];
+    widen8(*reinterpret_cast<const Eight<T>*>(p), w);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = w[q];
+  }
+}
 template <class T, int V>
 __global__ void __launch_bounds__(NT) k_ortho_norm(const T* G, int ld, int K, int N, Squares* part) {
   __shared__ Squares red[NT / 32];
@@ -62,8 +80,7 @@ __global__ void __launch_bounds__(NT) k_ortho_norm(const T* G, int ld, int K, in
     const int col = e >> 32 ? (int)(e / per) : (int)((uint32_t)e / (uint32_t)per), i = (int)(e - (long long)col * per) * V;
     const T* from = G + (size_t)col * ld + i;
     float x[V];
-    if constexpr (V == 8) widen8(*reinterpret_cast<const Eight<T>*>(from), x);
-    else x[0] = to_float(from[0]);
+    load_some<T, V>(from, x);
 #pragma unroll
     for (int q = 0; q < V; ++q) add_square(x[q], big, mid, small);
   }
@@ -102,11 +119,12 @@ __global__ void __launch_bounds__(NT) k_ortho_scale(const T* G, int ld, int K, i
     const int col = e >> 32 ? (int)(e / per) : (int)((uint32_t)e / (uint32_t)per), i = (int)(e - (long long)col * per) * 8;
     const T* from = G + (size_t)col * ld + i;
     float x[8];
-    if constexpr (V == 8) {
-      widen8(*reinterpret_cast<const Eight<T>*>(from), x);
-    } else {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) x[q] = i + q < K ? to_float(from[q]) : 0.0f;
+    for (int q = 0; q < 8; q += V) {
+      if (i + q < K) load_some<T, V>(from + q, x + q);
+      else
+#pragma unroll
+        for (int r = 0; r < V; ++r) x[q + r] = 0.0f;
     }
 #pragma unroll
     for (int q = 0; q < 8; ++q) x[q] = x[q] * p1 * p2 * m;
@@ -183,7 +201,8 @@ __global__ void __launch_bounds__(NT) k_ortho_sum(const float* part, int parts, 
     v[3] = fmaf(beta, b.y + d.y, z.w * alpha);
     put4(C, C2, (size_t)j * ldc + i, I - i, vec, v);
   }
-  if (!TRI || i0 / 256 == j0 / 256) return;
+  if constexpr (!TRI) return;
+  if (i0 / 256 == j0 / 256) return;
 #pragma unroll
   for (int q = 0; q < 4; ++q) turned[x + q][y] = v[q];
   __syncthreads();
@@ -298,8 +317,9 @@ cr_status step_product(const Step& s, int* err, cudaStream_t stream) {
 
 template <class T>
 cr_status start(const T* G, int ld, int K, int N, Squares* part, const Split& X, cudaStream_t stream) {
-  const bool vec = ((uintptr_t)G & 15) == 0 && (long long)ld * sizeof(T) % 16 == 0 && K % 8 == 0;
-  const long long items = (long long)(vec ? K / 8 : K) * N;
+  constexpr int W = 16 / (int)sizeof(T);
+  const bool vec = ((uintptr_t)G & 15) == 0 && ld % W == 0 && K % W == 0;
+  const long long items = (long long)(vec ? K / W : K) * N;
   const int blocks = (int)std::max<long long>(1, std::min<long long>({(items + 2 * NT - 1) / (2 * NT), 4ll * sm_count(), MAXPART}));
   const auto go = [&](auto v0) -> cr_status {
     constexpr int V = decltype(v0)::value;
@@ -315,7 +335,7 @@ cr_status start(const T* G, int ld, int K, int N, Squares* part, const Split& X,
     CR_CHECK_LAUNCH("k_ortho_scale");
     return CR_OK;
   };
-  return vec ? go(std::integral_constant<int, 8>{}) : go(std::integral_constant<int, 1>{});
+  return vec ? go(std::integral_constant<int, W>{}) : go(std::integral_constant<int, 1>{});
 }
 
 // ---------------------------------------------------------------- small matrices

@@ -224,27 +224,25 @@ __device__ __forceinline__ void finish_gated4(const Params& p, int i, int j, flo
 }
 
 // STEP: four consecutive i of column j (R, R2 and C2 are the library's own matrices, with columns on 16-byte boundaries).
+struct StepR {
+  uint2 hi, lo;
+};
+__device__ __forceinline__ StepR step_r(const Params& p, int i, int j) {
+  StepR r = {make_uint2(0, 0), make_uint2(0, 0)};
+  const size_t at = (size_t)j * p.e.ldr + i;
+  if (p.e.R && i < p.I) r.hi = *reinterpret_cast<const uint2*>((const __half*)p.e.R + at);
+  if (p.R2 && i < p.I) r.lo = *reinterpret_cast<const uint2*>((const __half*)p.R2 + at);
+  return r;
+}
 template <class O>
-__device__ __forceinline__ void finish_step4(const Params& p, int i, int j, float (&v)[4]) {
+__device__ __forceinline__ void finish_step4(const Params& p, int i, int j, const StepR& r, float (&v)[4]) {
   if (i >= p.I) return;
-  const size_t r = (size_t)j * p.e.ldr + i, c = (size_t)j * p.e.ldc + i;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) v[q] *= p.alpha;
-  if (p.e.R) {
-    const auto four = [&](const void* m, float (&f)[4]) {
-      const uint2 w = *reinterpret_cast<const uint2*>((const __half*)m + r);
-      const float2 a = widen2(w.x, __half{}), b = widen2(w.y, __half{});
-      f[0] = a.x;
-      f[1] = a.y;
-      f[2] = b.x;
-      f[3] = b.y;
-    };
-    float x[4], y[4] = {};
-    four(p.e.R, x);
-    if (p.R2) four(p.R2, y);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = fmaf(p.beta, x[q] + y[q], v[q]);
-  }
+  const size_t c = (size_t)j * p.e.ldc + i;
+  const float2 a = widen2(r.hi.x, __half{}), b = widen2(r.hi.y, __half{}), x = widen2(r.lo.x, __half{}), y = widen2(r.lo.y, __half{});
+  v[0] = fmaf(p.beta, a.x + x.x, v[0] * p.alpha);
+  v[1] = fmaf(p.beta, a.y + x.y, v[1] * p.alpha);
+  v[2] = fmaf(p.beta, b.x + y.x, v[2] * p.alpha);
+  v[3] = fmaf(p.beta, b.y + y.y, v[3] * p.alpha);
   struct alignas(4 * sizeof(O)) Four {
     O x[4];
   } o, rest;
@@ -1103,19 +1101,46 @@ __global__ void __launch_bounds__(TTHREADS) k_thin(const __grid_constant__ ThinM
       }
       return z;
     };
-    for (int e = 4 * (int)threadIdx.x; got && e < outputs; e += 4 * TTHREADS) {
-      const float4 z = joined(e);
+    const auto place = [&](int e, int& i, int& j) {
       const int block = e / (ncols * sb), in = e - block * ncols * sb;
-      const int i = i0 + rank * outs + block * sb + in % sb, j = j0 + in / sb;
-      float v[4] = {z.x, z.y, z.z, z.w};
-      if constexpr (FORM == GATED) {
-        const float4 y = joined(outputs + e);
-        float w[4] = {y.x, y.y, y.z, y.w};
-        finish_gated4<O>(p, i, j, v, w);
-      } else if constexpr (FORM == STEP) {
-        finish_step4<O>(p, i, j, v);
-      } else {
-        thin_finish4<O>(p, i, j, v);
+      i = i0 + rank * outs + block * sb + in % sb;
+      j = j0 + in / sb;
+    };
+    if constexpr (FORM == STEP) {   // R of four outputs' eights on its way at once: stores to C hold up later loads
+      constexpr int U = 4;
+      for (int e0 = 4 * (int)threadIdx.x; got && e0 < outputs; e0 += U * 4 * TTHREADS) {
+        StepR r[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const int e = e0 + k * 4 * TTHREADS;
+          int i, j;
+          place(e, i, j);
+          if (e < outputs) r[k] = step_r(p, i, j);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const int e = e0 + k * 4 * TTHREADS;
+          if (e >= outputs) break;
+          int i, j;
+          place(e, i, j);
+          const float4 z = joined(e);
+          float v[4] = {z.x, z.y, z.z, z.w};
+          finish_step4<O>(p, i, j, r[k], v);
+        }
+      }
+    } else {
+      for (int e = 4 * (int)threadIdx.x; got && e < outputs; e += 4 * TTHREADS) {
+        const float4 z = joined(e);
+        int i, j;
+        place(e, i, j);
+        float v[4] = {z.x, z.y, z.z, z.w};
+        if constexpr (FORM == GATED) {
+          const float4 y = joined(outputs + e);
+          float w[4] = {y.x, y.y, y.z, y.w};
+          finish_gated4<O>(p, i, j, v, w);
+        } else {
+          thin_finish4<O>(p, i, j, v);
+        }
       }
     }
     __syncwarp();
@@ -1363,9 +1388,13 @@ Choice choose(int I, int J, int kblocks, bool qk, bool triangle = false, bool su
       const int received = split > 1 ? 512 * bn : 0;
       const int stages = std::min(TMAXSTAGES, (227 * 1024 / per - 3584 - received) / stage);
       if (stages < (split > 1 ? 3 : 2) || (split > 1 && stages * stage < received)) continue;
-      const double ctas = (double)t * split, waves = std::max(1.0, ctas / sms);
+      const double ctas = (double)t * split;
+      double waves = std::max(1.0, ctas / sms);
       const double hbm = (double)I * kblocks * KBYTES / 5.5e6 * (1.0 + 0.25 * std::max(0.0, 1.0 - ctas / (2.5 * sms)));
       const double later = std::max(0.0, ctas / sms - per) * 0.025 * bn;   // epilogues of tiles after the resident ones
+      // STEP: what more than half of the SMs take in at that rate is more than L2 gives (1200 x 1200: 100 CTAs 14.5 us, wide 12.5;
+      // 1000 x 1000: 64 CTAs 11.8, wide 13.7).
+      if (FORM == STEP) waves = std::max(waves, ctas / (0.5 * sms));
       const double us = 5.0 + later + (split > 1 ? 0.3 + 0.04 * bn : 0.0) + std::max(waves * tiles(kblocks, split) * stage / 100e3, hbm);
       if (us < best.us) best = {false, bn, split, stages, us};
     }
