@@ -251,8 +251,7 @@ cr_status step_product(const Step& s, int* err, cudaStream_t stream) {
   p.tma_c = ((uintptr_t)p.e.C & 15) == 0 && p.e.ldc % 8 == 0;   // STEP's wide outputs are of 16 bits
   p.vec4 = ((uintptr_t)p.e.C & (4 * type_bytes(out_type) - 1)) == 0 && p.e.ldc % 4 == 0;
   // With two parts a sum has to keep FP32's digits, and the tensor cores' adders cut off what they cannot hold: they sum up 4
-  // k-blocks (16 additions) by themselves, 8 in the thin kernel, which has no registers to go on in (1001 x 2500 FP32, five
-  // steps: relative error 1.5e-5 with whole sums).
+  // k-blocks (16 additions) by themselves (1001 x 2500 FP32, five steps: relative error 1.5e-5 with whole sums, 5e-6).
   const Choice ch = choose<STEP>(s.I, s.J, p.kblocks, s.q_major, s.symmetric, s.P.lo != nullptr);
   p.parts = ch.parts;
   p.chunk = s.P.lo ? 4 : p.kblocks;

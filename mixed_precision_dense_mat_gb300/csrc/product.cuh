@@ -924,7 +924,10 @@ __global__ void __launch_bounds__(TTHREADS) k_thin(const __grid_constant__ ThinM
   constexpr int OUT = FORM == GATED ? 64 : 128;   // outputs i of a tile
   const int i0 = tile / p.tj * OUT, j0 = tile % p.tj * p.bn;
   const int kb0 = (int)((long long)p.kblocks * rank / split), kb1 = (int)((long long)p.kblocks * (rank + 1) / split);
-  const uint32_t cols = p.bn <= 32 ? 32 : p.bn <= 64 ? 64 : p.bn <= 128 ? 128 : 256;
+  // STEP with two parts: four k-blocks at most to an accumulator, and two of them, so that the tensor cores' chains stay short
+  const uint32_t bcols = p.bn <= 32 ? 32 : p.bn <= 64 ? 64 : p.bn <= 128 ? 128 : 256;
+  const bool two_sums = FORM == STEP && p.segments == 3;
+  const uint32_t cols = two_sums ? 2 * bcols : bcols;
   const int ncols = min(p.bn, p.J - j0);
   constexpr int KE = F8 ? 128 : 64;
 
@@ -1019,7 +1022,9 @@ __global__ void __launch_bounds__(TTHREADS) k_thin(const __grid_constant__ ThinM
           if (ok) {
             const uint64_t da = da0 + (uint32_t)(st * stage_bytes >> 4), db = db0 + (uint32_t)(st * stage_bytes >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mma_any<false, F8>(tmem, da + kk * ps, db + kk * qs, p.idesc, kb != kb0 || kk != 0);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_any<false, F8>(two_sums && kb >= kb0 + 4 ? tmem + bcols : tmem, da + kk * ps, db + kk * qs, p.idesc,
+                                 (kb != kb0 && !(two_sums && kb == kb0 + 4)) || kk != 0);
             mma_commit(&bars->empty[st]);
           }
           if (kb + 1 == kb1 || !ok) mma_commit(&bars->done);   // after giving up too: it completes once the issued MMAs have
@@ -1051,6 +1056,12 @@ __global__ void __launch_bounds__(TTHREADS) k_thin(const __grid_constant__ ThinM
       __syncwarp();
       if (kb1 > kb0 && ok) {
         tmem_ld16(tq + (uint32_t)c, v);
+        if (two_sums && kb1 > kb0 + 4) {
+          float w[16];
+          tmem_ld16(tq + bcols + (uint32_t)c, w);
+#pragma unroll
+          for (int q = 0; q < 16; ++q) v[q] += w[q];
+        }
       } else {
 #pragma unroll
         for (int q = 0; q < 16; ++q) v[q] = 0.0f;
