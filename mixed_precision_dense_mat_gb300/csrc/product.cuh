@@ -1400,13 +1400,13 @@ Choice choose(int I, int J, int kblocks, bool qk, bool triangle = false, bool su
       const int stages = std::min(TMAXSTAGES, (227 * 1024 / per - 3584 - received) / stage);
       if (stages < (split > 1 ? 3 : 2) || (split > 1 && stages * stage < received)) continue;
       const double ctas = (double)t * split;
-      double waves = std::max(1.0, ctas / sms);
+      const double waves = std::max(1.0, ctas / sms);
       const double hbm = (double)I * kblocks * KBYTES / 5.5e6 * (1.0 + 0.25 * std::max(0.0, 1.0 - ctas / (2.5 * sms)));
       const double later = std::max(0.0, ctas / sms - per) * 0.025 * bn;   // epilogues of tiles after the resident ones
-      // STEP: what more than half of the SMs take in at that rate is more than L2 gives (1200 x 1200: 100 CTAs 14.5 us, wide 12.5;
-      // 1000 x 1000: 64 CTAs 11.8, wide 13.7).
-      if (FORM == STEP) waves = std::max(waves, ctas / (0.5 * sms));
-      const double us = 5.0 + later + (split > 1 ? 0.3 + 0.04 * bn : 0.0) + std::max(waves * tiles(kblocks, split) * stage / 100e3, hbm);
+      // STEP: a CTA's outputs by four, R read with them, are what takes long (five steps of 1400 x 1400 without this term 293 us,
+      // 238 with it; 700 x 2500 175 and 152; 512 x 512 124 and 114; 1000 x 1000 177 and 203).
+      const double ends = FORM == STEP ? 0.047 * bn / split + (split > 1 ? 0.02 * bn : 0.0) : split > 1 ? 0.3 + 0.04 * bn : 0.0;
+      const double us = 5.0 + later + ends + std::max(waves * tiles(kblocks, split) * stage / 100e3, hbm);
       if (us < best.us) best = {false, bn, split, stages, us};
     }
     if (J <= 64) break;
