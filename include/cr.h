@@ -109,9 +109,11 @@ cr_status cr_kernel_launches(uint64_t* count);
  * products at most (one chunk's 4 n_p M_b bytes when that is more), 8 n_p M_b bytes of
  * accumulator, 8 n_o M bytes for R, and S (8 n_p M) in cr_correct_calibrate;
  * cr_krige_correct with CR_GEMM_DF takes 8 n_o (n_p + M) bytes.  The trend-network operators take
- * copies of operands that are not on 16-byte boundaries, G in cr_affine_backward, a few hundred rows
- * of partial sums for vector gradients, and 8 bytes per feature and 128 (backward 64) columns for
- * the recurrence.  Memory still used by work in flight stays in the pool.  No device
+ * copies of operands that are not on 16-byte boundaries, G in the affine products' gradients, a few
+ * hundred rows of partial sums for vector gradients, 8 bytes per feature and 128 (backward 64) columns for
+ * the recurrence, 8 bytes per field and group (and tile of columns) for the group norm, and in
+ * cr_orthogonalize, above 128 on the short side s, 4 (K N + s^2) bytes, twice that for FP16 and FP32
+ * outputs, and up to 16 FP32 matrices of a product's sums.  Memory still used by work in flight stays in the pool.  No device
  * work; does not synchronise. */
 cr_status cr_workspace_trim(void);
 
@@ -129,6 +131,11 @@ cr_status cr_workspace_trim(void);
  *   "k_affine_wide", "k_affine_thin", "k_affine_one", "k_affine_g"   affine product (CTA pairs; few
  *                   columns; one column) and the gradient at its pre-activation
  *   "k_rmsnorm", "k_rmsnorm_bwd", "k_scan_fwd", "k_scan_bwd"   norm and gated recurrence
+ *   "k_gated_wide", "k_gated_thin", "k_gated_one", "k_gated_g"   gated affine product, as for the affine one
+ *   "k_gnorm_small", "k_gnorm_stats", "k_gnorm_apply", "k_gnorm_sums", "k_gnorm_dx"   group norm: small
+ *                   fields; first and second look; the gradient's
+ *   "k_ortho_small", "k_ortho_norm", "k_ortho_scale", "k_ortho_wide", "k_ortho_thin", "k_ortho_sum"
+ *                   orthogonalised update: small matrices; norm and scaling; products; joined parts of k
  * cr_timing_enable(on) switches recording on (1) or off (0); it does not clear the totals.
  * cr_timing_read(name, &ms, &n) synchronises the device, folds every recorded launch into the
  * totals and returns the total milliseconds and launch count of `name` (0 if never timed).
@@ -422,22 +429,23 @@ cr_status cr_calibrate_noalloc(const double* d_S, int lds, int n_p, int M, const
 /* ---------------------------------------------------------------- trend network
  * Operators of a learned trend: a network over space-time covariates whose outputs are columns
  * of the universal-kriging designs Xo, Xp (the paper takes the design as given; these have no
- * counterpart there).  The operators are an affine product with its epilogue, the
- * root-mean-square norm, and a gated recurrence along time, each with its gradient, and the
- * forms that answer single columns or time steps.
+ * counterpart there).  The operators are an affine product with its epilogue, a gated one (two
+ * projections), the root-mean-square norm of columns, the group norm of fields, and a gated recurrence
+ * along time, each with its gradient, and the forms that answer single columns or time steps; and
+ * the orthogonalised update of a weight matrix.
  *
  * Conventions, next to those at the top of this file:
  *  - A matrix is features x columns, column-major: a column is one site at one time and is
  *    contiguous.  Leading dimensions count elements of the matrix's own type and are >= the
  *    number of rows (any value is right; multiples of 16 bytes at 16-byte aligned addresses
  *    are fastest).  Inputs are only read, and outputs overlap no input unless a call says so.
- *  - Sizes (K, N, M, D, T, B, n_seq) end at 2^31 - 2^16.
+ *  - Sizes (K, N, M, D, T, B, n_seq, n_field; 2N in the gated product) end at 2^31 - 2^16.
  *  - Elements are FP32, FP16, BF16 or e4m3 (FP8, largest value 448) as a CR_TYPE_* argument
  *    says; arithmetic, sums and states are FP32, and each output is rounded once, to nearest.
  *  - Scratch comes from the pools of cr_workspace_trim.  Calls are asynchronous, and results do
  *    not depend on timing: the same call on the same inputs gives the same bits.  They can be
  *    captured into CUDA graphs once the process has made a first call outside a capture.
- *  - Zero columns (M, T, B or n_seq = 0) are allowed: sums over them are zero.
+ *  - Zero columns (M, T, B, n_seq or n_field = 0) are allowed: sums over them are zero.
  *  - A device-side wait that runs out (CR_OPT_WAIT_LIMIT_US; never in normal operation)
  *    invalidates the outputs of its call and makes the next call of this section that has any
  *    columns, on any stream and from any host thread, return CR_ERR_TIMEOUT once, without
