@@ -591,11 +591,11 @@ __device__ __forceinline__ void sum_rows(const float* part, int rows, int D, int
 }
 
 // dX = r (gamma dz - mean(gamma dz) - h mean(gamma dz h)), means over the group, by the first `tiles` blocks (0: not wanted); the
-// others sum up the tiles' parts of dgamma and dbeta, 32 features each.
+// others sum up the parts of dgamma and dbeta (rows of them), 32 features each.
 template <class T, int TX, int V, int ACT>
 __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_dx(const T* X, int ldx, const T* dY, int lddy, const Fields p, const float2* part,
                                                  const float* gamma, const float* beta, const float* mean, const float* rstd, int lds, T* dX,
-                                                 int lddx, unsigned tiles, const float* pgamma, const float* pbeta, float* dgamma,
+                                                 int lddx, unsigned tiles, int rows, const float* pgamma, const float* pbeta, float* dgamma,
                                                  float* dbeta) {
   constexpr int TY = NT / TX, FW = TX * V;
   __shared__ float2 stat[FW];
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_dx(const T* X, int ldx, 
     wait_for_previous();
     const unsigned b = blockIdx.x - tiles, per = (p.D + 31) / 32;
     const bool second = !dgamma || b >= per;
-    sum_rows(second ? pbeta : pgamma, p.tiles, p.D, (int)(b % per) * 32, second ? dbeta : dgamma, red);
+    sum_rows(second ? pbeta : pgamma, rows, p.D, (int)(b % per) * 32, second ? dbeta : dgamma, red);
     return;
   }
   const int fb = blockIdx.x % p.blocks, t = blockIdx.x / p.blocks;
@@ -673,6 +673,102 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_dx(const T* X, int ldx, 
       });
     }
   }, [](int) {});
+}
+
+// Small fields as in k_gnorm_small: a block per field and group forms both its sums and its dX, and leaves its features' sums for
+// dgamma and dbeta in pgamma[field][D] and pbeta[field][D].
+template <class T, int V, int ACT>
+__global__ void __launch_bounds__(NT) k_gnorm_small_bwd(const T* X, int ldx, const T* dY, int lddy, const Fields p, const float* gamma,
+                                                        const float* beta, const float* mean, const float* rstd, int lds, T* dX, int lddx,
+                                                        float* pgamma, float* pbeta) {
+  __shared__ float red[2][NT / 32];
+  __shared__ float2 feature[NT * V];
+  constexpr int P = V > 1 ? 2 : 1;
+  let_next_start();
+  wait_for_previous();
+  const int g = blockIdx.x % p.groups, f = blockIdx.x / p.groups, i0 = g * p.group;
+  const int begin = field_begin(p, f), end = max(begin, field_begin(p, f + 1)), TX = p.group / V, TY = NT / TX;
+  const int total = (end - begin) * TX, step = TY * TX;   // a thread keeps its features
+  const int tx = threadIdx.x % TX, first = threadIdx.x < step ? (int)threadIdx.x : total;
+  const float minus = begin < end ? -mean[(size_t)f * lds + g] : 0.0f, r = begin < end ? rstd[(size_t)f * lds + g] : 0.0f;
+  const float n = (float)(end - begin) * (float)p.group;
+  float gm[V], bt[V], sb[V] = {}, sg[V] = {};
+#pragma unroll
+  for (int q = 0; q < V; ++q) {
+    gm[q] = gamma ? gamma[i0 + tx * V + q] : 1.0f;
+    bt[q] = beta ? beta[i0 + tx * V + q] : 0.0f;
+  }
+  const auto look = [&](int e, auto&& use) {   // use(q, h, dz), P features at a time
+    Pair<T, V> raw;
+    const size_t j = (size_t)(begin + e / TX);
+    raw.x.load(X + j * ldx + i0 + tx * V);
+    raw.d.load(dY + j * lddy + i0 + tx * V);
+    float x[V], d[V];
+    raw.x.widen(x);
+    raw.d.widen(d);
+#pragma unroll
+    for (int q = 0; q < V; q += P) {
+      const Floats<P> h = mul(add(pair_at(x, q), all_of<P>(minus)), all_of<P>(r));
+      Floats<P> dz = pair_at(d, q);
+      if (ACT != CR_ACT_NONE) dz = mul(dz, slope_of<ACT, P>(fma(h, pair_at(gm, q), pair_at(bt, q))));
+      use(q, h, dz);
+    }
+  };
+#pragma unroll 2
+  for (int e = first; e < total; e += step)
+    look(e, [&](int q, Floats<P> h, Floats<P> dz) {
+      const Floats<P> b = add(pair_at(sb, q), dz), c = fma(dz, h, pair_at(sg, q));
+#pragma unroll
+      for (int o = 0; o < P; ++o) {
+        sb[q + o] = b.x[o];
+        sg[q + o] = c.x[o];
+      }
+    });
+  float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+  for (int q = 0; q < V; ++q) {
+    feature[threadIdx.x * V + q] = make_float2(sb[q], sg[q]);   // [ty][feature] of the step's threads
+    c1 = fmaf(gm[q], sb[q], c1);
+    c2 = fmaf(gm[q], sg[q], c2);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    c1 += __shfl_xor_sync(0xffffffffu, c1, o);
+    c2 += __shfl_xor_sync(0xffffffffu, c2, o);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    red[0][threadIdx.x >> 5] = c1;
+    red[1][threadIdx.x >> 5] = c2;
+  }
+  __syncthreads();
+  c1 = red[0][0];
+  c2 = red[1][0];
+#pragma unroll
+  for (int w = 1; w < NT / 32; ++w) {
+    c1 += red[0][w];
+    c2 += red[1][w];
+  }
+  for (int x = threadIdx.x; x < p.group; x += NT) {
+    float2 t = feature[x];
+    for (int y = 1; y < TY; ++y) {
+      t.x += feature[y * p.group + x].x;
+      t.y += feature[y * p.group + x].y;
+    }
+    if (pgamma) pgamma[(size_t)f * p.D + i0 + x] = t.y;
+    if (pbeta) pbeta[(size_t)f * p.D + i0 + x] = t.x;
+  }
+  if (!dX || begin == end) return;
+  const Floats<P> m1 = all_of<P>(-r * (c1 / n)), m2 = all_of<P>(-r * (c2 / n));
+#pragma unroll 2
+  for (int e = first; e < total; e += step) {
+    float y[V];
+    look(e, [&](int q, Floats<P> h, Floats<P> dz) {
+      const Floats<P> v = fma(h, m2, fma(mul(dz, pair_at(gm, q)), all_of<P>(r), m1));
+#pragma unroll
+      for (int o = 0; o < P; ++o) y[q + o] = v.x[o];
+    });
+    store<T, V>(dX + (size_t)(begin + e / TX) * lddx + i0 + tx * V, y);
+  }
 }
 
 // Columns of 16-bit types on 8- or 16-byte boundaries (bytes), of FP32 on 16-byte ones.
@@ -816,6 +912,45 @@ extern "C" cr_status cr_group_norm_backward(int type, const void* d_X, int ldx, 
   CR_TRY(wait_word(&err));
   return with_type(type, [&](auto t0) -> cr_status {
     using E = decltype(t0);
+    const int group = D / groups;
+    constexpr int WS = 16 / (int)sizeof(E);
+    const bool wide = group % WS == 0 && D % WS == 0 && aligned(d_X, ldx, sizeof(E), 16) && aligned(d_dY, lddy, sizeof(E), 16) &&
+                      (!d_dX || aligned(d_dX, lddx, sizeof(E), 16));
+    if ((long long)T * (wide ? group / WS : group) <= SMALL * NT && (long long)n * groups <= 128 * sm_count() && group <= NT) {
+      Fields p = {};
+      p.off = d_off;
+      p.n = n;
+      p.T = T;
+      p.D = D;
+      p.groups = groups;
+      p.group = group;
+      float* part = nullptr;
+      const size_t rows = (size_t)n * D;
+      if (d_dgamma || d_dbeta) CR_CUDA(scratch_alloc((void**)&part, 2 * rows * sizeof(float), stream));
+      const auto run = [&]() -> cr_status {
+        CR_TRY(with_act(act, [&](auto a0) -> cr_status {
+          constexpr int ACT = decltype(a0)::value;
+          TimedScope ts("k_gnorm_small", stream);
+          const auto go = [&](auto v0) {
+            return launch_after(k_gnorm_small_bwd<E, decltype(v0)::value, ACT>, (unsigned)(n * groups), NT, 0, 1, stream, (const E*)d_X, ldx,
+                                (const E*)d_dY, lddy, p, d_gamma, d_beta, d_mean, d_rstd, lds, (E*)d_dX, lddx, d_dgamma ? part : nullptr,
+                                d_dbeta ? part + rows : nullptr);
+          };
+          CR_CUDA(wide ? go(std::integral_constant<int, WS>{}) : go(std::integral_constant<int, 1>{}));
+          CR_CHECK_LAUNCH("k_gnorm_small_bwd");
+          return CR_OK;
+        }));
+        if (!part) return CR_OK;
+        const unsigned sums = (unsigned)((D + 31) / 32) * ((d_dgamma ? 1 : 0) + (d_dbeta ? 1 : 0));
+        CR_CUDA(launch_after(k_gnorm_dx<E, 32, 1, CR_ACT_NONE>, sums, NT, 0, 1, stream, (const E*)d_X, ldx, (const E*)d_dY, lddy, p,
+                             (const float2*)nullptr, d_gamma, d_beta, d_mean, d_rstd, lds, (E*)nullptr, D, 0u, n, part, part + rows, d_dgamma, d_dbeta));
+        CR_CHECK_LAUNCH("k_gnorm_dx");
+        return CR_OK;
+      };
+      const cr_status st = run();
+      scratch_free(part, stream);
+      return st;
+    }
     // four features to a thread: with eight, their six constants each do not fit into registers beside the columns on their way
     constexpr int EB = sizeof(E), W = 4;
     const bool vec = D % W == 0 && aligned(d_X, ldx, EB, W * EB) && aligned(d_dY, lddy, EB, W * EB) && (!d_dX || aligned(d_dX, lddx, EB, W * EB));
@@ -839,7 +974,7 @@ extern "C" cr_status cr_group_norm_backward(int type, const void* d_X, int ldx, 
           TimedScope ts("k_gnorm_dx", stream);
           const unsigned sums = (unsigned)((D + 31) / 32) * ((d_dgamma ? 1 : 0) + (d_dbeta ? 1 : 0)), tiles = d_dX ? grid : 0;
           CR_CUDA(launch_after(k_gnorm_dx<E, TX, V, ACT>, tiles + sums, NT, 0, 1, stream, (const E*)d_X, ldx, (const E*)d_dY, lddy, p, part, d_gamma,
-                               d_beta, d_mean, d_rstd, lds, (E*)d_dX, lddx, tiles, pgamma, pbeta, d_dgamma, d_dbeta));
+                               d_beta, d_mean, d_rstd, lds, (E*)d_dX, lddx, tiles, p.tiles, pgamma, pbeta, d_dgamma, d_dbeta));
           CR_CHECK_LAUNCH("k_gnorm_dx");
           return CR_OK;
         }));
