@@ -250,11 +250,12 @@ cr_status step_product(const Step& s, int* err, cudaStream_t stream) {
   const int out_type = s.out ? s.out_type : CR_TYPE_F16;
   p.tma_c = ((uintptr_t)p.e.C & 15) == 0 && p.e.ldc % 8 == 0;   // STEP's wide outputs are of 16 bits
   p.vec4 = ((uintptr_t)p.e.C & (4 * type_bytes(out_type) - 1)) == 0 && p.e.ldc % 4 == 0;
-  // With two parts a sum has to keep FP32's digits, and the tensor cores' adders cut off what they cannot hold: they sum up 4
-  // k-blocks (16 additions) by themselves (1001 x 2500 FP32, five steps: relative error 1.5e-5 with whole sums, 5e-6).
+  // With two parts a sum has to keep FP32's digits, and the tensor cores' adders cut off what they cannot hold: they sum up 3
+  // k-blocks (12 additions) by themselves (2500 x 1001 FP32, five steps: relative error 1.5e-5 with whole sums; by 4 k-blocks
+  // 5.4e-6 in 346 us, by 3 4.1e-6 in 369, by 2 3.0e-6 in 411; FP32 products 3.7e-6).
   const Choice ch = choose<STEP>(s.I, s.J, p.kblocks, s.q_major, s.symmetric, s.P.lo != nullptr);
   p.parts = ch.parts;
-  p.chunk = s.P.lo ? 4 : p.kblocks;
+  p.chunk = s.P.lo ? 3 : p.kblocks;
   p.jpad = (s.J + 255) / 256 * 256;
   p.triangle = ch.wide && s.symmetric;
   p.bn = ch.bn;
@@ -341,7 +342,9 @@ cr_status start(const T* G, int ld, int K, int N, Squares* part, const Split& X,
 // Up to 128 rows on the short side: one cluster does all steps.  Each CTA keeps a slab of the long side's columns n of X (L,
 // a multiple of 128) in shared memory, [i / 64][n][i % 64] in the 128-byte swizzle, which the tensor cores read as rows i with
 // k = n (A = X X^T) and as rows n with k = i (X^T B).  The CTAs' parts of A are joined through shared memory of the cluster, in
-// the order of the CTAs: each sums the rows that it owns and hands them to all.  B takes A's place, X' X's.
+// the order of the CTAs: each sums the rows that it owns and hands them to all.  B takes A's place, X' X's.  B has two parts for a BF16
+// output too: its rounding is a third of the error where one side is much longer than the other, and eight more MMAs are
+// little here (the second part takes the place of the sums, which have been read).
 // Bound by the chain of products, exchanges and barriers (a step takes about 3 us with one CTA): launched separately, the 16
 // kernels of five steps take 160 us.
 constexpr int SROWS = 128, STHREADS = 256, SCLUSTER = 16;
@@ -419,7 +422,9 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
   const int rank = p.ncta > 1 ? (int)cluster_rank() : 0;
   const bool wide = p.K <= p.N;
   const int s = wide ? p.K : p.N, l = wide ? p.N : p.K, n0 = rank * L, cols = max(0, min(L, l - n0));
-  const uint32_t tcols = L <= 128 ? 128 : L <= 256 ? 256 : 512;
+  // PAIRS: two accumulators for each sum, the second half of the large products in the second one: half as long a chain of the
+  // tensor cores' additions, which cut off what they cannot hold
+  const uint32_t second = L <= 128 ? 128 : 256, tcols = PAIRS ? 2 * second : L <= 128 ? 128 : L <= 256 ? 256 : 512;
   if (threadIdx.x == 0) {
     mbar_init(&bars->product, 1);
     for (int m = 0; m < 4; ++m) mbar_init(&bars->block[m], 1);
@@ -538,6 +543,24 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
   };
   const float unit = 1.0f / UNIT;
   const int quad = warp & 3, side = warp >> 2, row = quad * 32 + lane;   // TMEM lane, and which 64 columns
+  const auto sums_of = [&](int col, bool two, float (&v)[64]) {   // this thread's 64 columns of an accumulator, or of both
+    const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + col + side * 64;
+    uint32_t u[2][32];
+    tmem_ld32(from, u[0]);
+    tmem_ld32(from + 32, u[1]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int x = 0; x < 64; ++x) v[x] = __uint_as_float(u[x / 32][x % 32]);
+    if (PAIRS && two) {
+#pragma unroll
+      for (int y = 0; y < 64; y += 16) {
+        float w[16];
+        tmem_ld16(from + second + y, w);
+#pragma unroll
+        for (int x = 0; x < 16; ++x) v[y + x] += w[x];
+      }
+    }
+  };
   for (int step = 0; step < p.steps; ++step) {
     // A's part of this slab
     if (warp == 0 && elect_one()) {
@@ -545,7 +568,10 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
       const int ks = max(1, (cols + 15) / 16);   // columns that are not there are zero
       for (int seg = 0; seg < SEGS; ++seg) {
         const uint64_t da = d0 + (first_lo(seg) ? xlo >> 4 : 0), db = d0 + (second_lo(seg) ? xlo >> 4 : 0);
-        for (int k = 0; k < ks; ++k) mma_any<false, false>(tmem, da + k * 128, db + k * 128, rows_id, (seg | k) != 0);
+        for (int k = 0; k < ks; ++k) {
+          const bool late = PAIRS && seg == 2 && k >= (ks + 1) / 2;
+          mma_any<false, false>(late ? tmem + second : tmem, da + k * 128, db + k * 128, rows_id, late ? k > (ks + 1) / 2 : (seg | k) != 0);
+        }
       }
       mma_commit(&bars->product);
     }
@@ -553,11 +579,8 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
     landed(&bars->product, turn);
     turn ^= 1;
     {
-      uint32_t u[2][32];
-      tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + side * 64, u[0]);
-      tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + side * 64 + 32, u[1]);
-      tmem_ld_wait();
-      const float* v = reinterpret_cast<const float*>(u);
+      float v[64];
+      sums_of(0, (cols + 15) / 16 >= 2, v);
       if (p.ncta == 1) {
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
@@ -627,7 +650,8 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
         const uint64_t da = d0 + (first_lo(seg) ? SA >> 4 : 0), db = d0 + (second_lo(seg) ? SA >> 4 : 0);
         for (int k = 0; k < 8; ++k) {
           const uint32_t at = (k / 4 * (SA / 2) >> 4) + k % 4 * 2;
-          mma_any<false, false>(tmem, da + at, db + at, k_id, (seg | k) != 0);
+          const bool late = PAIRS && seg == 2 && k >= 4;
+          mma_any<false, false>(late ? tmem + second : tmem, da + at, db + at, k_id, late ? k > 4 : (seg | k) != 0);
         }
       }
       mma_commit(&bars->product);
@@ -636,11 +660,8 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
     landed(&bars->product, turn);
     turn ^= 1;
     {   // B in A's place
-      uint32_t u[2][32];
-      tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + side * 64, u[0]);
-      tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + side * 64 + 32, u[1]);
-      tmem_ld_wait();
-      const float* v = reinterpret_cast<const float*>(u);
+      float v[64];
+      sums_of(0, true, v);
       const float c = p.c * unit;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
@@ -649,7 +670,7 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
         get8<PAIRS>(A, SA, at, w);
 #pragma unroll
         for (int x = 0; x < 8; ++x) w[x] = fmaf(p.b, w[x], c * v[8 * q + x]);
-        put8<PAIRS>(A, SA, at, w);
+        put8<true>(A, SA, at, w);
       }
     }
     fence_proxies();
@@ -661,10 +682,13 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
     if (warp == 0 && elect_one()) {
       const uint64_t dx = tile_desc(sx, true), d0 = tile_desc(sa, true);
       for (int m = 0; m < blocks; ++m) {
-        for (int seg = 0; seg < SEGS; ++seg) {
-          const uint64_t da = dx + (first_lo(seg) ? xlo >> 4 : 0) + m * (128 * 128 >> 4), db = d0 + (second_lo(seg) ? SA >> 4 : 0);
-          for (int k = 0; k < 8; ++k)
-            mma_any<false, false>(tmem + m * 128, da + (k / 4 * half >> 4) + k % 4 * 2, db + (k / 4 * (SA / 2) >> 4) + k % 4 * 2, k_id, (seg | k) != 0);
+        for (int seg = 0; seg < (PAIRS ? 3 : 2); ++seg) {
+          const uint64_t da = dx + (first_lo(seg) ? xlo >> 4 : 0) + m * (128 * 128 >> 4), db = d0 + (seg == 0 ? SA >> 4 : 0);
+          for (int k = 0; k < 8; ++k) {
+            const bool late = PAIRS && seg == 2 && k >= 4;
+            mma_any<false, false>((late ? tmem + second : tmem) + m * 128, da + (k / 4 * half >> 4) + k % 4 * 2,
+                                  db + (k / 4 * (SA / 2) >> 4) + k % 4 * 2, k_id, late ? k > 4 : (seg | k) != 0);
+          }
         }
         mma_commit(&bars->block[m]);
       }
@@ -673,11 +697,8 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
     const bool last = step + 1 == p.steps;
     for (int m = 0; m < blocks; ++m) {
       landed(&bars->block[m], step & 1);
-      uint32_t u[2][32];
-      tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + m * 128 + side * 64, u[0]);
-      tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + m * 128 + side * 64 + 32, u[1]);
-      tmem_ld_wait();
-      const float* v = reinterpret_cast<const float*>(u);
+      float v[64];
+      sums_of(m * 128, true, v);
       const int n = m * 128 + row;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
