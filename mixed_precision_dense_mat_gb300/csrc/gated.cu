@@ -1,5 +1,9 @@
 // Gated affine product (two projections of the same columns, the first one's activation times the second one), and
 // its gradient (cr_gated_affine, cr_gated_affine_backward).
+//
+// The product is product.cuh's GATED form: both halves of W in one tile, so that X is read once for both and no sum leaves
+// the SM.  Bound by the tensor cores or by reading W like the affine product: K = N = M = 4096 BF16 with bias and silu 144 us,
+// 1.90 PFLOP/s, e4m3 77 us; K = 4096, N = 12288, M = 24 FP16 36 us, 5.6 TB/s; K = N = 2048, M = 1 BF16 5.6 us.
 #include "product.cuh"
 
 namespace cr {
@@ -7,7 +11,7 @@ namespace {
 
 // G = [dY .* Zu .* act'(Zg); dY .* act(Zg)] for Z = [Zg; Zu], and the row sums of its unrounded values: a block takes
 // 32 V outputs and every gridDim.y-th 8 columns, a thread V outputs of a column (V = 8: 16-byte accesses), and leaves
-// its sums in part[blockIdx.y][2 N].  Bound by HBM: dY and Z read, G written.
+// its sums in part[blockIdx.y][2 N].  Bound by HBM: dY and Z read, G written (N = 8192, M = 4099 BF16 silu 54 us, 6.2 TB/s).
 template <class E, int ACT, int V>
 __global__ void __launch_bounds__(NT) k_gated_g(const E* dY, int lddy, const E* Z, int ldz, int N, int M, E* G, int ldg, float* part) {
   __shared__ float red[2][NT / 32][32 * V + V];
