@@ -137,7 +137,7 @@ inline int type_bytes(int type) {
 // Launches a kernel that may be set up (barriers, tensor memory, its first instructions) while the
 // stream's previous kernel finishes, and calls wait_for_previous() before it touches memory.
 template <class... Par, class... Arg>
-cudaError_t launch_after(void (*kernel)(Par...), dim3 grid, unsigned block, size_t smem, int cluster, cudaStream_t stream, Arg&&... arg) {
+cudaError_t launch_after(void (*kernel)(Par...), unsigned grid, unsigned block, size_t smem, int cluster, cudaStream_t stream, Arg&&... arg) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -145,7 +145,7 @@ cudaError_t launch_after(void (*kernel)(Par...), dim3 grid, unsigned block, size
   at[1].id = cudaLaunchAttributeClusterDimension;
   at[1].val.clusterDim.x = (unsigned)cluster;
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.gridDim = grid;
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

@@ -5,6 +5,8 @@
 // of 2^-24 with 11 bits (X's are about 1 / sqrt(K N)).  FP16 holds three bits more than a BF16 output; for FP16 and FP32
 // outputs each matrix is a sum of two FP16 ones (22 bits), and a product three (the one of the two small parts is below
 // 2^-22 of it).  A and b A + c A^2 are symmetric: the wide kernel forms half of their tiles and stores them twice.
+// Bound by the tensor cores where the matrices are large (4096 x 8192 BF16, five steps: 1510 us, 1.6 PFLOP/s with symmetric products
+// counted by half), by the chain of 15 dependent products where they are not (512 x 512 114 us, 2048 x 2048 254 us).
 #include <cmath>
 
 #include "product.cuh"
@@ -173,7 +175,7 @@ template <class O, bool TRI>
 __global__ void __launch_bounds__(NT) k_ortho_sum(const float* part, int parts, int ldp, int jpad, int I, int J, const __half* R, const __half* R2,
                                                   int ldr, float alpha, float beta, O* C, O* C2, int ldc, int vec) {
   __shared__ float turned[TRI ? JTILE : 1][JTILE + 1];
-  const int i0 = blockIdx.x * JTILE, j0 = blockIdx.y * JTILE;
+  const int across = (I + JTILE - 1) / JTILE, i0 = (int)(blockIdx.x % across) * JTILE, j0 = (int)(blockIdx.x / across) * JTILE;
   let_next_start();
   wait_for_previous();
   if (TRI && i0 / 256 > j0 / 256) return;
@@ -288,7 +290,7 @@ cr_status step_product(const Step& s, int* err, cudaStream_t stream) {
         CR_TRY((launch_wide<SUMS, false, float>(maps, p, tiles * p.parts, stream)));
         TimedScope ts("k_ortho_sum", stream);
         const int vec = ((uintptr_t)p.e.C & (4 * sizeof(O) - 1)) == 0 && p.e.ldc % 4 == 0;
-        const dim3 grid((s.I + JTILE - 1) / JTILE, (s.J + JTILE - 1) / JTILE);
+        const unsigned grid = (unsigned)((long long)((s.I + JTILE - 1) / JTILE) * ((s.J + JTILE - 1) / JTILE));
         const auto sum = [&](auto tri) {
           return launch_after(k_ortho_sum<O, decltype(tri)::value>, grid, NT, 0, 1, stream, part, p.parts, ldp, p.jpad, s.I, s.J, (const __half*)p.e.R,
                               (const __half*)p.R2, s.R.ld, p.alpha, p.beta, (O*)p.e.C, (O*)p.C2, p.e.ldc, vec);
@@ -345,8 +347,8 @@ cr_status start(const T* G, int ld, int K, int N, Squares* part, const Split& X,
 // the order of the CTAs: each sums the rows that it owns and hands them to all.  B takes A's place, X' X's.  B has two parts for a BF16
 // output too: its rounding is a third of the error where one side is much longer than the other, and eight more MMAs are
 // little here (the second part takes the place of the sums, which have been read).
-// Bound by the chain of products, exchanges and barriers (a step takes about 3 us with one CTA): launched separately, the 16
-// kernels of five steps take 160 us.
+// Bound by the chain of products, exchanges and barriers: 128 x 128 to BF16 27 us, 3 us a step, to FP32 43 us; 128 x 2048, by 16
+// CTAs, 52 us, 8.5 us a step.  Launched separately, the 17 kernels of 128 x 128 took 166 us.
 constexpr int SROWS = 128, STHREADS = 256, SCLUSTER = 16;
 constexpr int SA = SROWS * SROWS * 2;   // bytes of A's FP16 part, [j / 64][i][j % 64]
 constexpr int SSUMS = SROWS * SROWS * 4;   // the CTA's sums for A

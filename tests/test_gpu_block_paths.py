@@ -78,3 +78,16 @@ def test_update_symmetry_and_order_of_columns(lib):
         c = values(lib.orthogonalize(matrix(g[:, order], torch.float32), 3))
         for other in (b, c[:, np.argsort(order)]):
             assert np.linalg.norm(other - a) <= 64 * 2.0 ** -21 * np.linalg.norm(a) * np.sqrt(3)
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_update_of_millions_of_columns(lib, out):
+    """r copies of H side by side: A is H's, X is H's over sqrt(r), and so is each copy's update.  Both sides carry the same roundings,
+    of other values: twice what the symmetry test allows for FP32, twice the BF16 test's bound below for BF16."""
+    H, r = matrix(_gradient(160, 1000), torch.float32), 2200
+    want = lib.orthogonalize(H, 1, out_dtype=out).float()
+    G = H.T.repeat(r, 1).T
+    got = lib.orthogonalize(G, 1, out_dtype=out)
+    limit = 2 * 64 * 2.0 ** -21 if out is torch.float32 else 2 * (2.0 ** -8 + 4 * 2.0 ** -11)
+    for block in (got[:, :1000], got[:, -1000:], got[:, 1000 * (r // 2):1000 * (r // 2 + 1)]):
+        assert float((block.float() * r ** 0.5 - want).norm()) <= limit * float(want.norm())
