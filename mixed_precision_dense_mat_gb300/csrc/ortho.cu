@@ -282,12 +282,23 @@ cr_status step_product(const Step& s, int* err, cudaStream_t stream) {
       Maps<SUMS> maps = {};
       CR_TRY(maps_of(&maps.P, &maps.P2, s.P, s.I, s.p_major, 128));
       CR_TRY(maps_of(&maps.Q, &maps.Q2, s.Q, s.J, s.q_major, 128));
+      if (p.parts == 1 && !p.triangle) {   // finished in the kernel
+        const auto tile = [&](CUtensorMap* m, const void* x, int type, int ld) {
+          return make_tensor_map_2d(m, type, x, s.I, s.J, ld, OROW / type_bytes(type), 32);
+        };
+        p.tma_c = ((uintptr_t)p.e.C & 15) == 0 && (long long)p.e.ldc * sizeof(O) % 16 == 0;
+        if (p.tma_c) CR_TRY(tile(&maps.C, p.e.C, out_type, p.e.ldc));
+        if (p.C2) CR_TRY(tile(&maps.C2, p.C2, CR_TYPE_F16, p.e.ldc));
+        if (s.R.hi) CR_TRY(tile(&maps.R, s.R.hi, CR_TYPE_F16, s.R.ld));
+        if (s.R.lo) CR_TRY(tile(&maps.R2, s.R.lo, CR_TYPE_F16, s.R.ld));
+        return launch_wide<SUMS, false, O>(maps, p, tiles, stream);
+      }
       const int ldp = (s.I + 3) & ~3;
       float* part = nullptr;
       CR_CUDA(scratch_alloc((void**)&part, (size_t)p.parts * p.jpad * ldp * sizeof(float), stream));
       const auto run = [&]() -> cr_status {
         CR_TRY(make_tensor_map_2d(&maps.C, CR_TYPE_F32, part, s.I, p.parts * p.jpad, ldp, 32, 32));
-        CR_TRY((launch_wide<SUMS, false, float>(maps, p, tiles * p.parts, stream)));
+        CR_TRY((launch_wide<SUMS, false, O>(maps, p, tiles * p.parts, stream)));
         TimedScope ts("k_ortho_sum", stream);
         const int vec = ((uintptr_t)p.e.C & (4 * sizeof(O) - 1)) == 0 && p.e.ldc % 4 == 0;
         const unsigned grid = (unsigned)((long long)((s.I + JTILE - 1) / JTILE) * ((s.J + JTILE - 1) / JTILE));

@@ -45,7 +45,7 @@ constexpr int NT = 256;
 
 // Forms.  AFFINE: C = act(sum + bias) + R.  GATED: P has two halves of I rows, C = act(first half's sum) times the
 // second half's sum.  STEP: C = alpha sum + beta R, all matrices FP16, or, in the thin kernel, sums of two (the second one
-// small); C symmetric where the wide kernel's tiles say so.  SUMS (wide): the sums alone, in FP32, with P and Q as in STEP.
+// small); C symmetric where the wide kernel's tiles say so.  SUMS (wide): STEP with sums of two, or the sums alone, in FP32.
 enum Form { AFFINE, GATED, STEP, SUMS };
 
 struct Params {
@@ -427,7 +427,7 @@ struct Maps<STEP> {
 };
 template <>
 struct Maps<SUMS> {
-  CUtensorMap P, Q, P2, Q2, C;
+  CUtensorMap P, Q, P2, Q2, C, C2, R, R2;   // C alone with parts: their FP32 matrices
 };
 
 // Tile t of the triangle i <= j, column by column.
@@ -746,6 +746,18 @@ __global__ void __launch_bounds__(wide_threads(FORM), 1) k_wide(const __grid_con
       } else if constexpr (FORM == SUMS) {
         int kb0, kb1;
         k_range(t, kb0, kb1);
+        // With one part of k the tile is finished here: R's first part is asked for before the products, the second one after.
+        const bool here = j0 < p.J && ibase < p.I, direct = p.parts == 1 && !triangle && here;
+        uint64_t* rbar = &bars->rows[(warp - 2) % WEPI][(warp - 2) / WEPI];
+        const auto ask = [&](const CUtensorMap* m) {
+          if (lane == 0) {
+            tma_store_wait_read();
+            mbar_arrive_expect_tx(rbar, WBUF);
+            tma_load_2d(buf, m, rbar, ibase, j0);
+          }
+        };
+        const bool with_r = direct && p.e.R;
+        if (with_r) ask(&maps.R);
         float sum[64];
 #pragma unroll
         for (int q = 0; q < 64; ++q) sum[q] = 0.0f;
@@ -771,10 +783,53 @@ __global__ void __launch_bounds__(wide_threads(FORM), 1) k_wide(const __grid_con
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(tempty[acc]);
         }
-        if (lost) break;
+        if (lost) {
+          if (with_r) mbar_wait_warp(rbar, nrows & 1u, LANDING_NS);
+          break;
+        }
+        if (!here) continue;
+        if (!direct) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 32)
-          if (j0 < p.J && ibase + c < p.I) put_rows<float, 32>(&maps.C, 1, nullptr, 0, 0, 0x7fffffff, ibase + c, t / tiles * p.jpad + j0, buf, false, sum + c);
+          for (int c = 0; c < 64; c += 32)
+            if (ibase + c < p.I) put_rows<float, 32>(&maps.C, 1, nullptr, 0, 0, 0x7fffffff, ibase + c, t / tiles * p.jpad + j0, buf, false, sum + c);
+          continue;
+        }
+#pragma unroll
+        for (int q = 0; q < 64; ++q) sum[q] *= p.alpha;
+        const auto add_r = [&] {
+          const bool there = mbar_wait_warp(rbar, nrows & 1u, p.limit);
+          if (!there) {
+            if (lane == 0) give_up();   // it goes on with what lands, and leaves at the next tile
+            mbar_wait_warp(rbar, nrows & 1u, LANDING_NS);
+          }
+          nrows ^= 1u;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float r[8];
+            widen8(*reinterpret_cast<const Eight<__half>*>(buf + lane * OROW + ((q ^ (lane & 7)) << 4)), r);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) sum[8 * q + x] = fmaf(p.beta, r[x], sum[8 * q + x]);
+          }
+          fence_smem_to_tma();
+          __syncwarp();
+        };
+        if (with_r) {
+          add_r();
+          if (p.R2) {
+            ask(&maps.R2);
+            add_r();
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 64; c += N)
+          if (ibase + c < p.I) put_rows<O, N>(&maps.C, p.tma_c, (O*)p.e.C, p.e.ldc, p.I, p.J, ibase + c, j0, buf, false, sum + c);
+        if (p.C2) {
+#pragma unroll
+          for (int q = 0; q < 64; ++q) sum[q] -= to_float(from_float<O>(sum[q]));
+#pragma unroll
+          for (int c = 0; c < 64; c += N)
+            if (ibase + c < p.I) put_rows<O, N>(&maps.C2, 1, (O*)p.C2, p.e.ldc, p.I, p.J, ibase + c, j0, buf, false, sum + c);
+        }
       } else if constexpr (FORM == STEP) {
         const auto there = [&](int c) { return j0 < p.J && ibase + c < p.I; };
         bool pending = false;   // R of the columns at c is on its way
@@ -1374,7 +1429,9 @@ Choice choose(int I, int J, int kblocks, bool qk, bool triangle = false, bool su
     // By way of SUMS: tiles over parts of k, which cost a launch and the way of every part's sums through L2.
     for (int parts = 1; FORM == STEP && parts <= 16 && (parts == 1 || kblocks >= 4 * parts); ++parts) {
       const double r = (double)((t * parts + sms / 2 - 1) / (sms / 2));
-      const double us = 11.0 + r * std::max(tiles(kblocks, parts) * 0.29 + 0.6, 2.0) + 1.2e-6 * parts * I * J * (triangle ? 0.5 : 1.0);
+      const bool joined = parts > 1 || triangle;
+      const double us = (joined ? 11.0 : 8.0) + r * std::max(tiles(kblocks, parts) * 0.29 + 0.6, 2.0) +
+                        (joined ? 1.2e-6 * parts * I * J * (triangle ? 0.5 : 1.0) : 0.0);
       if (us < best.us || (sums && parts == 1)) best = {true, 0, 1, 0, us, parts};
     }
   }
