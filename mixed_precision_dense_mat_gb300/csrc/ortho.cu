@@ -252,9 +252,10 @@ cr_status step_product(const Step& s, int* err, cudaStream_t stream) {
   const int out_type = s.out ? s.out_type : CR_TYPE_F16;
   p.tma_c = ((uintptr_t)p.e.C & 15) == 0 && p.e.ldc % 8 == 0;   // STEP's wide outputs are of 16 bits
   p.vec4 = ((uintptr_t)p.e.C & (4 * type_bytes(out_type) - 1)) == 0 && p.e.ldc % 4 == 0;
-  // With two parts a sum has to keep FP32's digits, and the tensor cores' adders cut off what they cannot hold: they sum up 3
-  // k-blocks (12 additions) by themselves (2500 x 1001 FP32, five steps: relative error 1.5e-5 with whole sums; by 4 k-blocks
-  // 5.4e-6 in 346 us, by 3 4.1e-6 in 369, by 2 3.0e-6 in 411; FP32 products 3.7e-6).
+  // With two parts a sum has to keep FP32's digits, and the tensor cores' adders cut off what they cannot hold: of the products of two
+  // first parts they sum up 3 k-blocks (12 additions) by themselves (2500 x 1001 FP32, five steps: relative error 1.5e-5 with whole
+  // sums; by 3 k-blocks 4.4e-6 in 346 us, by 2 3.0e-6 in 371; FP32 products 3.7e-6).  Reading an accumulator out takes about
+  // 2 us from its last MMA to its next one, twice as long as three k-blocks' MMAs, and there are two of them.
   const Choice ch = choose<STEP>(s.I, s.J, p.kblocks, s.q_major, s.symmetric, s.P.lo != nullptr);
   p.parts = ch.parts;
   p.chunk = s.P.lo ? 3 : p.kblocks;

@@ -66,7 +66,7 @@ struct Params {
   int triangle;          // C symmetric: tiles ti <= tj alone are formed (STEP stores them at (tj, ti) too; wide kernel)
   int parts;             // SUMS: tiles over as many parts of k, one matrix of jpad rows below the other
   int jpad;
-  int chunk;             // SUMS: k-blocks that the tensor cores sum up by themselves; such sums are added in registers
+  int chunk;             // SUMS: k-blocks of two first parts that the tensor cores sum up by themselves; such sums are added in registers
   float alpha, beta;
   void *C2, *R2;         // second parts (NULL: none), laid out like C and R
   Epilogue e;
@@ -542,6 +542,11 @@ __global__ void __launch_bounds__(wide_threads(FORM), 1) k_wide(const __grid_con
     if (triangle) triangle_tile(t, i, j);
     else wide_tile(p, t, i, j);
   };
+  // SUMS: where the tensor cores' sum that begins at kb ends.  What products with a small part lose is below 2^-11 of what the others do.
+  const auto run_end = [&](int kb, int kb1) {
+    const int small = p.kblocks / p.segments * (p.segments - 1);
+    return min(kb1, kb < small ? small : kb + p.chunk);
+  };
   const auto k_range = [&](int t, int& k0, int& k1) {
     const int part = FORM == SUMS ? t / tiles : 0;
     k0 = FORM == SUMS ? (int)((long long)p.kblocks * part / p.parts) : 0;
@@ -648,9 +653,9 @@ __global__ void __launch_bounds__(wide_threads(FORM), 1) k_wide(const __grid_con
         for (int u = 0, t; ok && (t = wide_turn(p, cl, ncl, u)) < ntiles; ++u) {
           int kb0, kb1;
           k_range(t, kb0, kb1);
-          for (int kb = kb0, in = 0; kb < kb1; ++kb) {
+          for (int kb = kb0, begin = kb0; kb < kb1; ++kb) {
             const uint32_t b = run & 1u;
-            if (in == 0) {
+            if (kb == begin) {
               ok = mbar_wait_warp(&bars->tempty[b], (run >> 1 & 1u) ^ 1u, p.limit);
               if (!ok) break;
               tc_fence_after();
@@ -658,16 +663,16 @@ __global__ void __launch_bounds__(wide_threads(FORM), 1) k_wide(const __grid_con
             ok = mbar_wait_warp(&bars->full[st], ph, p.limit);
             if (!ok) break;
             tc_fence_after();
-            const bool end = in + 1 == p.chunk || kb + 1 == kb1;
+            const bool end = kb + 1 == run_end(begin, kb1);
             if (elect_one()) {
               const uint64_t da = da0 + st * (WSTAGE >> 4), db = db0 + st * (WSTAGE >> 4);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) mma_any<true, F8>(tmem + b * 256, da + kk * qs, db + kk * ps, p.idesc, (in | kk) != 0);
+              for (int kk = 0; kk < 4; ++kk) mma_any<true, F8>(tmem + b * 256, da + kk * qs, db + kk * ps, p.idesc, kb != begin || kk != 0);
               mma_commit_pair(&bars->empty[st]);
               if (end) mma_commit_pair(&bars->tfull[b]);
             }
             __syncwarp();
-            in = end ? 0 : in + 1;
+            if (end) begin = kb + 1;
             run += end;
             if (++st == (uint32_t)p.stages) st = 0, ph ^= 1u;
           }
@@ -763,7 +768,7 @@ __global__ void __launch_bounds__(wide_threads(FORM), 1) k_wide(const __grid_con
         for (int q = 0; q < 64; ++q) sum[q] = 0.0f;
         bool lost = false;
 #pragma unroll 1
-        for (int kb = kb0; kb < kb1; kb += p.chunk, ++run) {
+        for (int kb = kb0; kb < kb1; kb = run_end(kb, kb1), ++run) {
           const uint32_t acc = run & 1u;
           if (!mbar_wait_warp(&bars->tfull[acc], run >> 1 & 1u, p.limit)) {
             if (lane == 0) give_up();
