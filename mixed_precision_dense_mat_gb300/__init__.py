@@ -981,7 +981,9 @@ def orthogonalize(G, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), out_dtype
     K, N = _shape(G, "orthogonalize G")
     G, pg, ldg = _matrix(G, K, N, dtype, "orthogonalize G")
     out, po, ldo = _output(out, K, N, out_dtype or (out.dtype if out is not None else dtype), device, "orthogonalize out")
-    a, b, c = coeffs
+    if len(coeffs) != 3:
+        raise CrError(1, f"orthogonalize coeffs: three numbers are needed, not {len(coeffs)}")
+    a, b, c = (float(v) for v in coeffs)
     _check(_lib.cr_orthogonalize(kind, pg, ldg, K, N, steps, a, b, c, _type_of(out, "orthogonalize out"), po, ldo,
                                  _raw_stream(device)))
     return out

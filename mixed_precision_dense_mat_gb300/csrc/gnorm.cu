@@ -4,8 +4,8 @@
 // tile's share of every group's mean and sum of squared deviations (each formed about the share's own mean, so that a
 // large common value costs no digits), the second joins the shares of the groups that its tile needs, in a fixed order,
 // and goes over the tile again.  The gradient does the same with its two sums.  Bound by HBM, X read twice where it does not
-// stay in L2, and by 4 us of each launch's set-up and joins: 8 fields of 16384 x 1024 BF16 with silu 143 us, 50 and 88 of the two
-// kernels (5.4 and 6.1 TB/s); 37 ragged fields of 50021 x 512 FP16 with gelu 45 us; the gradient of 11 fields of 40963 x 640 BF16
+// stay in L2, and by 4 us of each launch's set-up and joins: 8 fields of 16384 x 1024 BF16 with silu 138 us; 37 ragged
+// fields of 50021 x 512 FP16 with gelu 44 us; the gradient of 11 fields of 40963 x 640 BF16
 // with silu 62 us.  Fewer and larger tiles than one round of resident blocks leave SMs idle, more and smaller ones pay the set-up
 // again (the first case by 256-column tiles 168 us).
 #include <algorithm>
@@ -19,7 +19,9 @@ namespace {
 
 constexpr int NT = 256;
 constexpr int SMALL = 12;   // k_gnorm_small: accesses of a thread, if one field had all columns
-constexpr int RESIDENT = 3;   // blocks that share an SM (85 registers a thread)
+// Blocks that share an SM, and columns of a batch: forward two with 6 (8 fields of 16384 x 1024 BF16: 138 us; three with 4 147, two with
+// 4 145, two with 8 140), backward, where each column is of two matrices, three with 4 (2 of FP32).
+constexpr int FORWARD = 2, BATCH = 6, BACKWARD = 3;
 
 // Tile (fb, t): features fb * TX * V on, columns t * cols on.  Threads: TX along features, V consecutive ones each
 // (V = 8: 16-byte accesses for 16-bit types), NT / TX along columns.
@@ -225,7 +227,7 @@ __device__ __forceinline__ Floats<P> slope_of(Floats<P> z) {
 
 // ---------------------------------------------------------------- forward
 template <class T, int TX, int V>
-__global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_stats(const T* X, int ldx, const Fields p, float2* part) {
+__global__ void __launch_bounds__(NT, FORWARD) k_gnorm_stats(const T* X, int ldx, const Fields p, float2* part) {
   constexpr int TY = NT / TX, FW = TX * V;
   __shared__ float2 red[TY][FW];   // of a thread's features
   __shared__ float2 feature[FW];
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_stats(const T* X, int ld
   each_field(p, t, [&](int f, int a, int b, int begin, int end) {
     float mean[V] = {}, m2[V] = {}, n = 0.0f;
     if (i < p.D) {
-      constexpr int B = 4, P = V > 1 ? 2 : 1;
+      constexpr int B = BATCH, P = V > 1 ? 2 : 1;
       const T* from = X + (size_t)(a + ty) * ldx + i;
       in_batches<B, TY, Raw<T, V>>(a + ty, b, [&](Raw<T, V>& raw, int j) { raw.load(from + (size_t)j * ldx); },
                                    [&](const auto& raw, int, auto count) {   // the batch's own mean and deviations, joined to what is there
@@ -250,8 +252,15 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_stats(const T* X, int ld
 #pragma unroll
         for (int e = 0; e < V; e += P) {
           Floats<P> d2 = all_of<P>(0.0f), minus = mul(pair_at(x[0], e), all_of<P>(-1.0f));   // the batch's mean, negative
-          if constexpr (C == 4) {
-            minus = mul(add(add(pair_at(x[0], e), pair_at(x[1], e)), add(pair_at(x[2], e), pair_at(x[3], e))), all_of<P>(-0.25f));
+          if constexpr (C > 1) {
+            Floats<P> m[C];
+#pragma unroll
+            for (int q = 0; q < C; ++q) m[q] = pair_at(x[q], e);
+#pragma unroll
+            for (int h = 1; h < C; h *= 2)
+#pragma unroll
+              for (int q = 0; q + h < C; q += 2 * h) m[q] = add(m[q], m[q + h]);
+            minus = mul(m[0], all_of<P>(-1.0f / C));
 #pragma unroll
             for (int q = 0; q < C; ++q) {
               const Floats<P> d = add(pair_at(x[q], e), minus);
@@ -319,7 +328,7 @@ __device__ __forceinline__ void each_share(const Fields& p, int f, int begin, in
 
 // Columns are t * cols + cols <= T + cols < 2^31.
 template <class T, int TX, int V, int ACT>
-__global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_apply(const T* X, int ldx, const Fields p, const float2* part, const float* gamma,
+__global__ void __launch_bounds__(NT, FORWARD) k_gnorm_apply(const T* X, int ldx, const Fields p, const float2* part, const float* gamma,
                                                     const float* beta, float eps, T* Y, int ldy, float* mean_out, float* rstd_out, int lds) {
   constexpr int TY = NT / TX, FW = TX * V;
   __shared__ float2 stat[FW];   // by group of the block
@@ -371,7 +380,7 @@ __global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_apply(const T* X, int ld
         m[e] = -st.x;
         s[e] = st.y * gm[e];
       });
-      constexpr int B = 4, P = V > 1 ? 2 : 1;
+      constexpr int B = BATCH, P = V > 1 ? 2 : 1;
       // from the last column to the first: the last ones that the first look read are the likeliest to be in L2 still
       const int last = a + ty < b ? b - 1 - (b - 1 - a - ty) % TY : 0;
       const T* from = X + (size_t)last * ldx + i;
@@ -488,7 +497,7 @@ __global__ void __launch_bounds__(NT) k_gnorm_small(const T* X, int ldx, const F
 // With h = (x - mean) r, dz = dY act'(gamma h + beta): a feature's sums over the tile of dz h and dz go to
 // psum[t][2 D], and the groups' shares of sum gamma dz and sum gamma dz h to part.
 template <class T, int TX, int V, int ACT>
-__global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_sums(const T* X, int ldx, const T* dY, int lddy, const Fields p, const float* gamma,
+__global__ void __launch_bounds__(NT, BACKWARD) k_gnorm_sums(const T* X, int ldx, const T* dY, int lddy, const Fields p, const float* gamma,
                                                    const float* beta, const float* mean, const float* rstd, int lds, float2* part, float* pgamma,
                                                    float* pbeta) {
   constexpr int TY = NT / TX, FW = TX * V;
@@ -597,7 +606,7 @@ __device__ __forceinline__ void sum_rows(const float* part, int rows, int D, int
 // dX = r (gamma dz - mean(gamma dz) - h mean(gamma dz h)), means over the group, by the first `tiles` blocks (0: not wanted); the
 // others sum up the parts of dgamma and dbeta (rows of them), 32 features each.
 template <class T, int TX, int V, int ACT>
-__global__ void __launch_bounds__(NT, RESIDENT) k_gnorm_dx(const T* X, int ldx, const T* dY, int lddy, const Fields p, const float2* part,
+__global__ void __launch_bounds__(NT, BACKWARD) k_gnorm_dx(const T* X, int ldx, const T* dY, int lddy, const Fields p, const float2* part,
                                                  const float* gamma, const float* beta, const float* mean, const float* rstd, int lds, T* dX,
                                                  int lddx, unsigned tiles, int rows, const float* pgamma, const float* pbeta, float* dgamma,
                                                  float* dbeta) {
@@ -794,7 +803,7 @@ cr_status with_tile(int D, bool vec, F&& f) {
 
 // Tiles that are resident at once, of whole batches of columns: a tile's set-up and its groups' sums cost about as much as
 // 64 KB of columns.
-Fields make_fields(const int32_t* off, int n, int T, int D, int groups, int width, int rows) {
+Fields make_fields(const int32_t* off, int n, int T, int D, int groups, int width, int rows, int resident, int per_batch) {
   Fields p = {};
   p.off = off;
   p.n = off ? n : 1;
@@ -803,7 +812,7 @@ Fields make_fields(const int32_t* off, int n, int T, int D, int groups, int widt
   p.groups = groups;
   p.group = D / groups;
   p.blocks = (D + width - 1) / width;
-  const long long want = std::max(1, RESIDENT * sm_count() / p.blocks), per = (T + want - 1) / want, batch = 4 * rows;
+  const long long want = std::max(1, resident * sm_count() / p.blocks), per = (T + want - 1) / want, batch = per_batch * rows;
   p.cols = (int)((per + batch - 1) / batch * batch);
   p.tiles = (T + p.cols - 1) / p.cols;
   return p;
@@ -870,7 +879,7 @@ extern "C" cr_status cr_group_norm(int type, const void* d_X, int ldx, int D, in
     }
     return with_tile<W>(D, vec, [&](auto tx0, auto v0) -> cr_status {
       constexpr int TX = decltype(tx0)::value, V = decltype(v0)::value;
-      const Fields p = make_fields(d_off, n_field, T, D, groups, TX * V, NT / TX);
+      const Fields p = make_fields(d_off, n_field, T, D, groups, TX * V, NT / TX, FORWARD, BATCH);
       const unsigned grid = (unsigned)((long long)p.tiles * p.blocks);
       float2* part = nullptr;
       CR_CUDA(scratch_alloc((void**)&part, shares(p) * sizeof(float2), stream));
@@ -960,7 +969,7 @@ extern "C" cr_status cr_group_norm_backward(int type, const void* d_X, int ldx, 
     const bool vec = D % W == 0 && aligned(d_X, ldx, EB, W * EB) && aligned(d_dY, lddy, EB, W * EB) && (!d_dX || aligned(d_dX, lddx, EB, W * EB));
     return with_tile<W>(D, vec, [&](auto tx0, auto v0) -> cr_status {
       constexpr int TX = decltype(tx0)::value, V = decltype(v0)::value;
-      const Fields p = make_fields(d_off, n_field, T, D, groups, TX * V, NT / TX);
+      const Fields p = make_fields(d_off, n_field, T, D, groups, TX * V, NT / TX, BACKWARD, 4);
       const unsigned grid = (unsigned)((long long)p.tiles * p.blocks);
       const size_t rows = (size_t)p.tiles * D;
       float2* part = nullptr;
