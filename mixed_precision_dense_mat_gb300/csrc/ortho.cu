@@ -17,18 +17,33 @@ namespace {
 constexpr float UNIT = 1024.0f;   // the matrices hold UNIT times their values
 constexpr int MAXPART = 1024;
 
-// Sums of squares of a block's elements to part[block]: of those above 2^50 and below 2^-50 scaled by 2^-90 and 2^90, so
-// that no square overflows or underflows.
+// Sums of squares of a block's elements to part[block]: of those above 2^48 and below 2^-50 scaled by 2^-90 and 2^90, so
+// that no square overflows or underflows, nor 2^31 of them.
 struct Squares {
   float big, mid, small;
 };
 __device__ __forceinline__ void add_square(float x, float& big, float& mid, float& small) {
   const float a = fabsf(x);
-  const bool high = a > 0x1p50f, low = a < 0x1p-50f;
+  const bool high = a > 0x1p48f, low = a < 0x1p-50f;
   const float b = high ? a * 0x1p-90f : 0.0f, m = high || low ? 0.0f : a, s = low ? a * 0x1p90f : 0.0f;   // NaN goes to the middle
   big = fmaf(b, b, big);
   mid = fmaf(m, m, mid);
   small = fmaf(s, s, small);
+}
+// n elements: where the largest lies well inside the middle range the others may be added there too, because those that are too
+// small for it are below 2^-12 of the largest.
+template <int n>
+__device__ __forceinline__ void add_squares(const float* x, float& big, float& mid, float& small) {
+  float most = fabsf(x[0]);
+#pragma unroll
+  for (int q = 1; q < n; ++q) most = fmaxf(most, fabsf(x[q]));
+  if (most <= 0x1p48f && most >= 0x1p-38f) {
+#pragma unroll
+    for (int q = 0; q < n; ++q) mid = fmaf(x[q], x[q], mid);
+  } else {
+#pragma unroll
+    for (int q = 0; q < n; ++q) add_square(x[q], big, mid, small);
+  }
 }
 __device__ __forceinline__ Squares warp_sum(Squares s) {
 #pragma unroll
@@ -83,8 +98,7 @@ __global__ void __launch_bounds__(NT) k_ortho_norm(const T* G, int ld, int K, in
     const T* from = G + (size_t)col * ld + i;
     float x[V];
     load_some<T, V>(from, x);
-#pragma unroll
-    for (int q = 0; q < V; ++q) add_square(x[q], big, mid, small);
+    add_squares<V>(x, big, mid, small);
   }
   Squares s = warp_sum(Squares{big, mid, small});
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
@@ -481,9 +495,7 @@ __global__ void __launch_bounds__(STHREADS, 1) k_ortho_small(const Small p) {
         lx = x0;
         ly = y0;
 #pragma unroll
-        for (int b = 0; b < 16; ++b)
-#pragma unroll
-          for (int a = 0; a < 4; ++a) add_square(g[a][b], big, mid, small);
+        for (int a = 0; a < 4; ++a) add_squares<16>(g[a], big, mid, small);
       }
     Squares sum = warp_sum(Squares{big, mid, small});
     if (lane == 0) {

@@ -91,3 +91,21 @@ def test_update_of_millions_of_columns(lib, out):
     limit = 2 * 64 * 2.0 ** -21 if out is torch.float32 else 2 * (2.0 ** -8 + 4 * 2.0 ** -11)
     for block in (got[:, :1000], got[:, -1000:], got[:, 1000 * (r // 2):1000 * (r // 2 + 1)]):
         assert float((block.float() * r ** 0.5 - want).norm()) <= limit * float(want.norm())
+
+
+def test_update_of_entries_of_all_sizes(lib):
+    """Entries from 2^-140 to 2^120 in one matrix: the large ones are all that counts, wherever they lie; and a matrix of 2^49, whose
+    squares' sum passes FP32's range."""
+    for K, N in ((60, 100), (300, 520)):
+        g = np.float32(_gradient(K, N)).astype(float)
+        for big, small in ((120, -140), (60, -40), (0, -60), (-60, -130)):
+            both = g * 2.0 ** big
+            both[:, N // 2:] *= 2.0 ** (small - big)
+            want = lib.orthogonalize(matrix(np.where(np.arange(N) < N // 2, g, 0.0), torch.float32), 2)
+            got = lib.orthogonalize(matrix(both, torch.float32), 2)
+            assert np.linalg.norm(values(got)[:, :N // 2] - values(want)[:, :N // 2]) <= 1e-3 * np.linalg.norm(values(want))
+            assert np.isfinite(values(got)).all()
+    n = 2 ** 14 + 2 ** 12
+    x = torch.full((n, n), 2.0 ** 49, device="cuda", dtype=torch.bfloat16).T
+    got = lib.orthogonalize(x, 1, (1.0, 0.0, 0.0))   # G / |G|_F
+    assert torch.allclose(got.float(), torch.full_like(got, 1.0 / n).float(), rtol=2 ** -8)
