@@ -313,6 +313,7 @@ __device__ __forceinline__ void put_rows(const CUtensorMap* tm, int tma, O* out,
 #pragma unroll
       for (int c = lane; c < N; c += 32)
         if (i0 + c < I) out[(size_t)(j0 + r) * ld + i0 + c] = *at_in<O>(buf, r, c);
+    fence_smem_to_tma();   // the next R may come into the buffer by TMA
     __syncwarp();
   }
 }
