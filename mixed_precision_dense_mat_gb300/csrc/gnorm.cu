@@ -50,9 +50,9 @@ __device__ int first_field(const Fields& p, int c) {
 }
 // The tile's share of field f is slot (t + f), that of group g in feature block fb slot (fb + g): both pairs only go up.
 __device__ __forceinline__ size_t share(const Fields& p, int t, int f, int fb, int g) {
-  return (size_t)(t + f) * (p.blocks + p.groups) + fb + g;
+  return (size_t)(t + f) * ((size_t)p.blocks + p.groups) + fb + g;
 }
-size_t shares(const Fields& p) { return (size_t)(p.tiles + p.n) * (p.blocks + p.groups); }
+size_t shares(const Fields& p) { return (size_t)(p.tiles + p.n) * ((size_t)p.blocks + p.groups); }
 
 // V elements as they are in memory.  They are loaded in batches of columns before any is used or stored: the compiler may not
 // move a load of X above a store to Y, which may be the same matrix.
