@@ -176,52 +176,86 @@ __device__ __forceinline__ void each_field(const Fields& p, int t, R&& run, E&& 
   }
 }
 
-// Activations and slopes as in ops.cuh, two at a time, with reciprocals shared between them; sigmoids end at 2^-62, so that their
-// products do not overflow: silu(z) for z below -43 is -43 2^-62.
+// Activations (SLOPE: their slopes) as in ops.cuh from one reciprocal each: denominator(z) gives what result() needs the reciprocal
+// of.  Sigmoids end at 2^-62, so that two denominators' product does not overflow: silu(z) for z below -43 is -43 2^-62.
 template <int P>
 __device__ __forceinline__ Floats<P> clamped(Floats<P> z, float low, float high) {
 #pragma unroll
   for (int o = 0; o < P; ++o) z.x[o] = clamp_high(clamp_low(z.x[o], low), high);
   return z;
 }
-template <int ACT, int P>
-__device__ __forceinline__ Floats<P> act_of(Floats<P> z) {
-  if constexpr (ACT == CR_ACT_SILU) {
+template <int ACT, bool SLOPE, int P>
+struct Curve {
+  Floats<P> z, w;   // silu: z and e^-z; gelu: z, or max(z, 0), and |z|
+  __device__ __forceinline__ Floats<P> denominator(Floats<P> x) {
+    if constexpr (ACT == CR_ACT_SILU) {
+      if (SLOPE) {
+        z = clamped(x, -43.0f, 88.0f);
+      } else {
 #pragma unroll
-    for (int o = 0; o < P; ++o) z.x[o] = clamp_low(z.x[o], -43.0f);
-    return mul(z, rcp_shared(add(exp2_fast(mul(z, all_of<P>(-LOG2E))), all_of<P>(1.0f))));
-  } else if constexpr (ACT == CR_ACT_GELU) {   // z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|))
-    Floats<P> a, g;
+        for (int o = 0; o < P; ++o) z.x[o] = clamp_low(x.x[o], -43.0f);
+      }
+      w = exp2_fast(mul(z, all_of<P>(-LOG2E)));
+      return add(w, all_of<P>(1.0f));
+    } else {
+      if (SLOPE) {
+        z = clamped(x, -30.0f, 30.0f);
 #pragma unroll
-    for (int o = 0; o < P; ++o) {
-      a.x[o] = clamp_high(fabsf(z.x[o]), 30.0f);
-      z.x[o] = clamp_low(z.x[o], 0.0f);
+        for (int o = 0; o < P; ++o) w.x[o] = fabsf(z.x[o]);
+      } else {   // z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|))
+#pragma unroll
+        for (int o = 0; o < P; ++o) {
+          w.x[o] = clamp_high(fabsf(x.x[o]), 30.0f);
+          z.x[o] = clamp_low(x.x[o], 0.0f);
+        }
+      }
+      return tail_denominator(w);
     }
-    return fma(a, minus_tail<P, true>(a, g), z);
-  } else {
-    return activate<ACT, P>(z);
   }
-}
-template <int ACT, int P>
-__device__ __forceinline__ Floats<P> slope_of(Floats<P> z) {
-  const Floats<P> one = all_of<P>(1.0f);
-  if constexpr (ACT == CR_ACT_SILU) {
-    z = clamped(z, -43.0f, 88.0f);
-    const Floats<P> e = exp2_fast(mul(z, all_of<P>(-LOG2E))), s = rcp_shared(add(e, one));
-    return mul(s, fma(z, mul(e, s), one));
-  } else if constexpr (ACT == CR_ACT_GELU) {
-    z = clamped(z, -30.0f, 30.0f);
-    Floats<P> a, g, phi;
+  __device__ __forceinline__ Floats<P> result(Floats<P> t) const {
+    if constexpr (ACT == CR_ACT_SILU) {
+      return SLOPE ? mul(t, fma(z, mul(w, t), all_of<P>(1.0f))) : mul(z, t);
+    } else {
+      Floats<P> g;
+      const Floats<P> m = minus_tail(w, t, g);
+      if (!SLOPE) return fma(w, m, z);
+      Floats<P> phi;
 #pragma unroll
-    for (int o = 0; o < P; ++o) a.x[o] = fabsf(z.x[o]);
-    const Floats<P> m = minus_tail<P, true>(a, g);
+      for (int o = 0; o < P; ++o) phi.x[o] = z.x[o] < 0.0f ? -m.x[o] : 1.0f + m.x[o];
+      return fma(mul(z, all_of<P>(0.39894228040143268f)), g, phi);
+    }
+  }
+};
+// z = act(z), or its slope, for P features of C columns.  Reciprocals of two values come from one instruction, whose throughput
+// (one warp in 8 cycles and SM quarter, like 2^x's) bounds kernels that do little else: 1/x = y / (x y), within about 2^-22.  The two
+// are a feature's in two columns of a field: neighbouring features may be of different groups, which know nothing of
+// one another, not even a NaN.  In a thread of ONE_GROUP they are the features', each NaN kept to its own.
+template <int ACT, bool SLOPE, bool ONE_GROUP, int P, int C>
+__device__ __forceinline__ void curve(Floats<P> (&z)[C]) {
+  static_assert(C == 1 || (C == 2 && !ONE_GROUP), "one or two columns");
+  if constexpr (ACT == CR_ACT_SILU || ACT == CR_ACT_GELU) {
+    Curve<ACT, SLOPE, P> k[C];
+    Floats<P> d[C];
 #pragma unroll
-    for (int o = 0; o < P; ++o) phi.x[o] = z.x[o] < 0.0f ? -m.x[o] : 1.0f + m.x[o];
-    return fma(mul(z, all_of<P>(0.39894228040143268f)), g, phi);
+    for (int c = 0; c < C; ++c) d[c] = k[c].denominator(z[c]);
+    if constexpr (C == 2) {
+      const Floats<P> r = rcp_fast(mul(d[0], d[1]));
+      z[0] = k[0].result(mul(r, d[1]));
+      z[1] = k[1].result(mul(r, d[0]));
+    } else if constexpr (P == 2 && ONE_GROUP) {
+      const float a = fmaxf(d[0].x[0], 1.0f), b = fmaxf(d[0].x[1], 1.0f), r = rcp_fast(__fmul_rn(a, b));   // 1 for NaN, which z keeps
+      z[0] = k[0].result(Floats<P>{{__fmul_rn(r, b), __fmul_rn(r, a)}});
+    } else {
+      z[0] = k[0].result(rcp_fast(d[0]));
+    }
   } else {
 #pragma unroll
-    for (int o = 0; o < P; ++o) z.x[o] = activation_slope<ACT>(z.x[o]);
-    return z;
+    for (int c = 0; c < C; ++c) {
+      if constexpr (!SLOPE) z[c] = activate<ACT, P>(z[c]);
+      else
+#pragma unroll
+        for (int o = 0; o < P; ++o) z[c].x[o] = activation_slope<ACT>(z[c].x[o]);
+    }
   }
 }
 
@@ -387,17 +421,26 @@ __global__ void __launch_bounds__(NT, FORWARD) k_gnorm_apply(const T* X, int ldx
       T* to = Y + (size_t)last * ldy + i;
       in_batches<B, TY, Raw<T, V>>(a + ty, b, [&](Raw<T, V>& raw, int j) { raw.load(from - (size_t)j * ldx); },
                                    [&](const auto& raw, int j, auto count) {
+        constexpr int C = decltype(count)::value > 1 ? 2 : 1;   // columns at a time
+        static_assert(decltype(count)::value % C == 0, "batches of whole pairs");
 #pragma unroll
-        for (int q = 0; q < decltype(count)::value; ++q) {
-          float x[V];
-          raw[q].widen(x);
+        for (int q = 0; q < decltype(count)::value; q += C) {
+          float x[C][V];
+#pragma unroll
+          for (int c = 0; c < C; ++c) raw[q + c].widen(x[c]);
 #pragma unroll
           for (int e = 0; e < V; e += P) {   // m is minus the mean
-            const Floats<P> z = act_of<ACT, P>(fma(add(pair_at(x, e), pair_at(m, e)), pair_at(s, e), pair_at(bt, e)));
+            Floats<P> z[C];
 #pragma unroll
-            for (int o = 0; o < P; ++o) x[e + o] = z.x[o];
+            for (int c = 0; c < C; ++c) z[c] = fma(add(pair_at(x[c], e), pair_at(m, e)), pair_at(s, e), pair_at(bt, e));
+            curve<ACT, false, false>(z);
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+              for (int o = 0; o < P; ++o) x[c][e + o] = z[c].x[o];
           }
-          store<T, V>(to - (size_t)(j + q * TY) * ldy, x);
+#pragma unroll
+          for (int c = 0; c < C; ++c) store<T, V>(to - (size_t)(j + (q + c) * TY) * ldy, x[c]);
         }
       });
     }
@@ -484,9 +527,10 @@ __global__ void __launch_bounds__(NT) k_gnorm_small(const T* X, int ldx, const F
         constexpr int P = V > 1 ? 2 : 1;
 #pragma unroll
         for (int q = 0; q < V; q += P) {
-          const Floats<P> z = act_of<ACT, P>(pair_at(x, q));
+          Floats<P> z[1] = {pair_at(x, q)};
+          curve<ACT, false, true>(z);
 #pragma unroll
-          for (int o = 0; o < P; ++o) x[q + o] = z.x[o];
+          for (int o = 0; o < P; ++o) x[q + o] = z[0].x[o];
         }
         store<T, V>(Y + at(e + k * step) * ldy + i0 + tx * V, x);
       }
@@ -494,6 +538,38 @@ __global__ void __launch_bounds__(NT) k_gnorm_small(const T* X, int ldx, const F
 }
 
 // ---------------------------------------------------------------- backward
+// h = (x - mean) r and dz = dY act'(gamma h + beta) of a batch's columns, two at a time: use(column, feature, h, dz) for all features of a
+// column, then done(column).  m is minus the mean.
+template <int ACT, int V, class T, int N, class U, class D>
+__device__ __forceinline__ void each_slope(const Pair<T, V> (&raw)[N], const float (&m)[V], const float (&r)[V], const float (&gm)[V],
+                                           const float (&bt)[V], U&& use, D&& done) {
+  constexpr int P = V > 1 ? 2 : 1, C = N > 1 ? 2 : 1;
+  static_assert(N % C == 0, "batches of whole pairs");
+#pragma unroll
+  for (int q = 0; q < N; q += C) {
+    float x[C][V], d[C][V];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      raw[q + c].x.widen(x[c]);
+      raw[q + c].d.widen(d[c]);
+    }
+#pragma unroll
+    for (int e = 0; e < V; e += P) {
+      Floats<P> h[C], z[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        h[c] = mul(add(pair_at(x[c], e), pair_at(m, e)), pair_at(r, e));
+        z[c] = fma(h[c], pair_at(gm, e), pair_at(bt, e));
+      }
+      if constexpr (ACT != CR_ACT_NONE) curve<ACT, true, false>(z);
+#pragma unroll
+      for (int c = 0; c < C; ++c) use(q + c, e, h[c], ACT != CR_ACT_NONE ? mul(pair_at(d[c], e), z[c]) : pair_at(d[c], e));
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) done(q + c);
+  }
+}
+
 // With h = (x - mean) r, dz = dY act'(gamma h + beta): a feature's sums over the tile of dz h and dz go to
 // psum[t][2 D], and the groups' shares of sum gamma dz and sum gamma dz h to part.
 template <class T, int TX, int V, int ACT>
@@ -529,25 +605,15 @@ __global__ void __launch_bounds__(NT, BACKWARD) k_gnorm_sums(const T* X, int ldx
       in_batches<B, TY, Pair<T, V>>(a + ty, b, [&](Pair<T, V>& raw, int j) {
         raw.x.load(xs + (size_t)j * ldx);
         raw.d.load(ds + (size_t)j * lddy);
-      }, [&](const auto& raw, int j, auto count) {
+      }, [&](const auto& raw, int, auto) {
+        each_slope<ACT, V>(raw, m, r, gm, bt, [&](int, int e, Floats<P> h, Floats<P> dz) {
+          const Floats<P> b1 = add(pair_at(sb, e), dz), g1 = fma(dz, h, pair_at(sg, e));
 #pragma unroll
-        for (int q = 0; q < decltype(count)::value; ++q) {
-          float x[V], d[V];
-          raw[q].x.widen(x);
-          raw[q].d.widen(d);
-#pragma unroll
-          for (int e = 0; e < V; e += P) {   // m is minus the mean
-            const Floats<P> h = mul(add(pair_at(x, e), pair_at(m, e)), pair_at(r, e));
-            Floats<P> dz = pair_at(d, e);
-            if (ACT != CR_ACT_NONE) dz = mul(dz, slope_of<ACT, P>(fma(h, pair_at(gm, e), pair_at(bt, e))));
-            const Floats<P> b1 = add(pair_at(sb, e), dz), g1 = fma(dz, h, pair_at(sg, e));
-#pragma unroll
-            for (int o = 0; o < P; ++o) {
-              sb[e + o] = b1.x[o];
-              sg[e + o] = g1.x[o];
-            }
+          for (int o = 0; o < P; ++o) {
+            sb[e + o] = b1.x[o];
+            sg[e + o] = g1.x[o];
           }
-        }
+        }, [](int) {});
       });
     }
     __syncthreads();
@@ -666,23 +732,13 @@ __global__ void __launch_bounds__(NT, BACKWARD) k_gnorm_dx(const T* X, int ldx, 
       in_batches<B, TY, Pair<T, V>>(a + ty, b, [&](Pair<T, V>& raw, int j) {
         raw.x.load(xs - (size_t)j * ldx);
         raw.d.load(ds - (size_t)j * lddy);
-      }, [&](const auto& raw, int j, auto count) {
+      }, [&](const auto& raw, int j, auto) {
+        float y[2][V];
+        each_slope<ACT, V>(raw, m, r, gm, bt, [&](int q, int e, Floats<P> h, Floats<P> dz) {   // c1 and c2 are the sums times -r
+          const Floats<P> v = fma(h, pair_at(c2, e), fma(mul(dz, pair_at(gm, e)), pair_at(r, e), pair_at(c1, e)));
 #pragma unroll
-        for (int q = 0; q < decltype(count)::value; ++q) {
-          float x[V], d[V];
-          raw[q].x.widen(x);
-          raw[q].d.widen(d);
-#pragma unroll
-          for (int e = 0; e < V; e += P) {   // m is minus the mean, c1 and c2 are the sums times -r
-            const Floats<P> h = mul(add(pair_at(x, e), pair_at(m, e)), pair_at(r, e));
-            Floats<P> dz = pair_at(d, e);
-            if (ACT != CR_ACT_NONE) dz = mul(dz, slope_of<ACT, P>(fma(h, pair_at(gm, e), pair_at(bt, e))));
-            const Floats<P> y = fma(h, pair_at(c2, e), fma(mul(dz, pair_at(gm, e)), pair_at(r, e), pair_at(c1, e)));
-#pragma unroll
-            for (int o = 0; o < P; ++o) x[e + o] = y.x[o];
-          }
-          store<T, V>(to - (size_t)(j + q * TY) * lddx, x);
-        }
+          for (int o = 0; o < P; ++o) y[q % 2][e + o] = v.x[o];
+        }, [&](int q) { store<T, V>(to - (size_t)(j + q * TY) * lddx, y[q % 2]); });
       });
     }
   }, [](int) {});
@@ -723,7 +779,11 @@ __global__ void __launch_bounds__(NT) k_gnorm_small_bwd(const T* X, int ldx, con
     for (int q = 0; q < V; q += P) {
       const Floats<P> h = mul(add(pair_at(x, q), all_of<P>(minus)), all_of<P>(r));
       Floats<P> dz = pair_at(d, q);
-      if (ACT != CR_ACT_NONE) dz = mul(dz, slope_of<ACT, P>(fma(h, pair_at(gm, q), pair_at(bt, q))));
+      if (ACT != CR_ACT_NONE) {
+        Floats<P> z[1] = {fma(h, pair_at(gm, q), pair_at(bt, q))};
+        curve<ACT, true, true>(z);
+        dz = mul(dz, z[0]);
+      }
       use(q, h, dz);
     }
   };

@@ -241,29 +241,26 @@ __device__ __forceinline__ Floats<VEC> rcp_fast(Floats<VEC> x) {
   return x;
 }
 
-// The reciprocals of two values by one instruction, whose throughput (one warp in 8 cycles and SM quarter, like 2^x's) bounds
-// kernels that do little else: 1/x = y / (x y).  Within about 2^-22; x y must not overflow.
-__device__ __forceinline__ Floats<1> rcp_shared(Floats<1> x) { return {{rcp_fast(x.x[0])}}; }
-__device__ __forceinline__ Floats<2> rcp_shared(Floats<2> x) {
-  const float r = rcp_fast(__fmul_rn(x.x[0], x.x[1]));
-  return {{__fmul_rn(r, x.x[1]), __fmul_rn(r, x.x[0])}};
-}
-
 // Phi(a) - 1 for a >= 0, and g = e^(-a^2 / 2): erfc by Hastings' rational-exponential formula (Abramowitz and
-// Stegun, Handbook of Mathematical Functions, 7.1.26; its coefficients here times -1/2), absolute error 7.5e-8.
-template <int VEC, bool SHARED = false>
-__device__ __forceinline__ Floats<VEC> minus_tail(Floats<VEC> a, Floats<VEC>& g) {
+// Stegun, Handbook of Mathematical Functions, 7.1.26; its coefficients here times -1/2), absolute error 7.5e-8.  t is the
+// reciprocal of tail_denominator(a).
+template <int VEC>
+__device__ __forceinline__ Floats<VEC> tail_denominator(Floats<VEC> a) {
+  return fma(a, all_of<VEC>(0.3275911f * 0.70710678118654752f), all_of<VEC>(1.0f));
+}
+template <int VEC>
+__device__ __forceinline__ Floats<VEC> minus_tail(Floats<VEC> a, Floats<VEC> t, Floats<VEC>& g) {
   const auto k = [](float x) { return all_of<VEC>(x); };
-  const Floats<VEC> d = fma(a, k(0.3275911f * 0.70710678118654752f), k(1.0f));
-  Floats<VEC> t;
-  if constexpr (SHARED) t = rcp_shared(d);
-  else t = rcp_fast(d);
   g = exp2_fast(mul(mul(a, a), k(-0.5f * LOG2E)));
   Floats<VEC> p = fma(t, k(-0.5f * 1.061405429f), k(0.5f * 1.453152027f));
   p = fma(t, p, k(-0.5f * 1.421413741f));
   p = fma(t, p, k(0.5f * 0.284496736f));
   p = fma(t, p, k(-0.5f * 0.254829592f));
   return mul(mul(t, p), g);
+}
+template <int VEC>
+__device__ __forceinline__ Floats<VEC> minus_tail(Floats<VEC> a, Floats<VEC>& g) {
+  return minus_tail(a, rcp_fast(tail_denominator(a)), g);
 }
 
 template <int ACT, int VEC>
