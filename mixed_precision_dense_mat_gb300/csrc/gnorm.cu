@@ -177,31 +177,39 @@ __device__ __forceinline__ void each_field(const Fields& p, int t, R&& run, E&& 
 }
 
 // Activations (SLOPE: their slopes) as in ops.cuh from one reciprocal each: denominator(z) gives what result() needs the reciprocal
-// of.  Sigmoids end at 2^-62, so that two denominators' product does not overflow: silu(z) for z below -43 is -43 2^-62.
-template <int P>
-__device__ __forceinline__ Floats<P> clamped(Floats<P> z, float low, float high) {
-#pragma unroll
-  for (int o = 0; o < P; ++o) z.x[o] = clamp_high(clamp_low(z.x[o], low), high);
-  return z;
+// of.  So that the product of two denominators does not overflow, silu's are 1 + e^-|z|, with
+// silu(z) = max(z, 0) - |z| e^-|z| / (1 + e^-|z|); where e^-|z| is flushed to 0 the function has reached its limit.
+__device__ __forceinline__ float clamp_both(float x, float high) {   // to [-high, high] in one instruction; NaN stays
+  asm("min.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(x) : "f"(high));
+  return x;
 }
 template <int ACT, bool SLOPE, int P>
 struct Curve {
-  Floats<P> z, w;   // silu: z and e^-z; gelu: z, or max(z, 0), and |z|
+  Floats<P> z, w;   // z, or max(z, 0); silu: e^-|z|, or -|z| e^-|z|; gelu: |z|
   __device__ __forceinline__ Floats<P> denominator(Floats<P> x) {
     if constexpr (ACT == CR_ACT_SILU) {
-      if (SLOPE) {
-        z = clamped(x, -43.0f, 88.0f);
-      } else {
+      Floats<P> c;   // the argument, clamped
 #pragma unroll
-        for (int o = 0; o < P; ++o) z.x[o] = clamp_low(x.x[o], -43.0f);
+      for (int o = 0; o < P; ++o) c.x[o] = clamp_both(x.x[o], 88.0f);
+      w = mul(c, all_of<P>(LOG2E));
+#pragma unroll
+      for (int o = 0; o < P; ++o) {
+        w.x[o] = exp2_fast(-fabsf(w.x[o]));
+        z.x[o] = SLOPE ? c.x[o] : clamp_low(x.x[o], 0.0f);
       }
-      w = exp2_fast(mul(z, all_of<P>(-LOG2E)));
-      return add(w, all_of<P>(1.0f));
+      const Floats<P> d = add(w, all_of<P>(1.0f));
+      if (!SLOPE) {
+#pragma unroll
+        for (int o = 0; o < P; ++o) w.x[o] = __fmul_rn(w.x[o], -fabsf(c.x[o]));
+      }
+      return d;
     } else {
       if (SLOPE) {
-        z = clamped(x, -30.0f, 30.0f);
 #pragma unroll
-        for (int o = 0; o < P; ++o) w.x[o] = fabsf(z.x[o]);
+        for (int o = 0; o < P; ++o) {
+          z.x[o] = clamp_both(x.x[o], 30.0f);
+          w.x[o] = fabsf(z.x[o]);
+        }
       } else {   // z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|))
 #pragma unroll
         for (int o = 0; o < P; ++o) {
@@ -214,7 +222,11 @@ struct Curve {
   }
   __device__ __forceinline__ Floats<P> result(Floats<P> t) const {
     if constexpr (ACT == CR_ACT_SILU) {
-      return SLOPE ? mul(t, fma(z, mul(w, t), all_of<P>(1.0f))) : mul(z, t);
+      if (!SLOPE) return fma(w, t, z);
+      Floats<P> top;   // of sigmoid(z) = top / (1 + e^-|z|)
+#pragma unroll
+      for (int o = 0; o < P; ++o) top.x[o] = z.x[o] < 0.0f ? w.x[o] : 1.0f;
+      return mul(t, fma(z, mul(w, t), top));
     } else {
       Floats<P> g;
       const Floats<P> m = minus_tail(w, t, g);
