@@ -67,8 +67,8 @@ cr_status gradient_at_z(const E* dY, int lddy, const E* Z, int ldz, int N, int M
 
 }  // namespace
 
-cr_status affine_product(Operand P, Operand Q, int type, int K, int out_type, const Epilogue& e, cudaStream_t stream, First* first) {
-  return product<AFFINE>(P, Q, type, K, out_type, e, stream, first);
+cr_status affine_product(Operand P, Operand Q, int type, int K, int out_type, const Epilogue& e, int* err, cudaStream_t stream, First* first) {
+  return product<AFFINE>(P, Q, type, K, out_type, e, err, stream, first);
 }
 
 }  // namespace cr
@@ -89,8 +89,10 @@ extern "C" cr_status cr_affine(int type, const void* d_W, int ldw, const void* d
   CR_REQUIRE(ldw >= K && ldx >= K && ldy >= N && (!d_R || ldr >= N) && (!d_Z || ldz >= N), "cr_affine: leading dimension too small");
   if (M == 0) return CR_OK;
   CR_REQUIRE(d_W && d_X && d_Y, "cr_affine: NULL argument");
+  int* err = nullptr;
+  CR_TRY(wait_word(&err));
   const Epilogue e{d_wscale, d_xscale, d_bias, act, d_R, ldr, d_Z, ldz, d_Y, ldy};
-  return affine_product(Operand{d_W, N, ldw, true}, Operand{d_X, M, ldx, true}, type, K, out_type, e, stream);
+  return affine_product(Operand{d_W, N, ldw, true}, Operand{d_X, M, ldx, true}, type, K, out_type, e, err, stream);
   CR_ENTRY_END("cr_affine")
 }
 
@@ -111,6 +113,9 @@ extern "C" cr_status cr_affine_backward(int type, const void* d_W, int ldw, cons
     if (d_dW) CR_CUDA(cudaMemset2DAsync(d_dW, (size_t)lddw * type_bytes(dw_type), 0, (size_t)K * type_bytes(dw_type), N, stream));
     return CR_OK;
   }
+  if (!d_dX && !d_dW && !d_db) return CR_OK;
+  int* err = nullptr;
+  CR_TRY(wait_word(&err));
   void* own = nullptr;
   const int ldown = (N + 7) & ~7;   // columns on 16-byte boundaries
   if (act != CR_ACT_NONE && (d_dX || d_dW)) CR_CUDA(scratch_alloc(&own, (size_t)ldown * M * 2, stream));
@@ -129,11 +134,11 @@ extern "C" cr_status cr_affine_backward(int type, const void* d_W, int ldw, cons
       if ((part == 0) == (N >= M)) {   // the one with the longer sums first
         if (!d_dX) continue;           // dX(i, j) = sum_n W(i, n) G(n, j)
         const Epilogue e{nullptr, nullptr, nullptr, CR_ACT_NONE, nullptr, 0, nullptr, 0, d_dX, lddx};
-        CR_TRY(affine_product(Operand{d_W, K, ldw, false}, Operand{G, M, ldg, true}, type, N, type, e, stream, &first));
+        CR_TRY(affine_product(Operand{d_W, K, ldw, false}, Operand{G, M, ldg, true}, type, N, type, e, err, stream, &first));
       } else {
         if (!d_dW) continue;           // dW(i, n) = sum_j X(i, j) G(n, j)
         const Epilogue e{nullptr, nullptr, nullptr, CR_ACT_NONE, nullptr, 0, nullptr, 0, d_dW, lddw};
-        CR_TRY(affine_product(Operand{d_X, K, ldx, false}, Operand{G, N, ldg, false}, type, M, dw_type, e, stream, &first));
+        CR_TRY(affine_product(Operand{d_X, K, ldx, false}, Operand{G, N, ldg, false}, type, M, dw_type, e, err, stream, &first));
       }
     }
     return CR_OK;

@@ -102,8 +102,10 @@ extern "C" cr_status cr_gated_affine(int type, const void* d_W, int ldw, const v
   CR_REQUIRE(ldw >= K && ldx >= K && ldy >= N && (!d_Z || ldz >= 2 * N), "cr_gated_affine: leading dimension too small");
   if (M == 0) return CR_OK;
   CR_REQUIRE(d_W && d_X && d_Y, "cr_gated_affine: NULL argument");
+  int* err = nullptr;
+  CR_TRY(wait_word(&err));
   const Epilogue e{d_wscale, d_xscale, d_bias, act, nullptr, 0, d_Z, ldz, d_Y, ldy};
-  return product<GATED>(Operand{d_W, 2 * N, ldw, true}, Operand{d_X, M, ldx, true}, type, K, out_type, e, stream);
+  return product<GATED>(Operand{d_W, 2 * N, ldw, true}, Operand{d_X, M, ldx, true}, type, K, out_type, e, err, stream);
   CR_ENTRY_END("cr_gated_affine")
 }
 
@@ -126,6 +128,8 @@ extern "C" cr_status cr_gated_affine_backward(int type, const void* d_W, int ldw
     return CR_OK;
   }
   if (!d_dX && !d_dW && !d_db) return CR_OK;
+  int* err = nullptr;
+  CR_TRY(wait_word(&err));
   void* own = nullptr;
   const int two = 2 * N, ldown = (two + 7) & ~7;   // columns on 16-byte boundaries
   if (d_dX || d_dW) CR_CUDA(scratch_alloc(&own, (size_t)ldown * M * 2, stream));
@@ -140,11 +144,11 @@ extern "C" cr_status cr_gated_affine_backward(int type, const void* d_W, int ldw
       if ((part == 0) == (two >= M)) {   // the one with the longer sums first
         if (!d_dX) continue;             // dX(i, j) = sum_n W(i, n) G(n, j)
         const Epilogue e{nullptr, nullptr, nullptr, CR_ACT_NONE, nullptr, 0, nullptr, 0, d_dX, lddx};
-        CR_TRY(affine_product(Operand{d_W, K, ldw, false}, Operand{own, M, ldown, true}, type, two, type, e, stream, &first));
+        CR_TRY(affine_product(Operand{d_W, K, ldw, false}, Operand{own, M, ldown, true}, type, two, type, e, err, stream, &first));
       } else {
         if (!d_dW) continue;             // dW(i, n) = sum_j X(i, j) G(n, j)
         const Epilogue e{nullptr, nullptr, nullptr, CR_ACT_NONE, nullptr, 0, nullptr, 0, d_dW, lddw};
-        CR_TRY(affine_product(Operand{d_X, K, ldx, false}, Operand{own, two, ldown, false}, type, M, dw_type, e, stream, &first));
+        CR_TRY(affine_product(Operand{d_X, K, ldx, false}, Operand{own, two, ldown, false}, type, M, dw_type, e, err, stream, &first));
       }
     }
     return CR_OK;

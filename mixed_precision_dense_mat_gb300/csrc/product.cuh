@@ -36,8 +36,8 @@ struct First {
   int kblocks = 0;
 };
 
-// The affine form's product (affine.cu).
-cr_status affine_product(Operand P, Operand Q, int type, int K, int out_type, const Epilogue& e, cudaStream_t stream, First* first = nullptr);
+// The affine form's product (affine.cu).  err: the wait word, which the entry has asked for before any of its work.
+cr_status affine_product(Operand P, Operand Q, int type, int K, int out_type, const Epilogue& e, int* err, cudaStream_t stream, First* first = nullptr);
 
 namespace {
 
@@ -1493,10 +1493,10 @@ cr_status one_column(const Operand& P, const Operand& Q, int K, const Params& p,
 
 // The AFFINE and GATED forms' product; GATED: P has 2 I rows.
 template <int FORM>
-cr_status product(Operand P, Operand Q, int type, int K, int out_type, const Epilogue& e, cudaStream_t stream, First* first = nullptr) {
+cr_status product(Operand P, Operand Q, int type, int K, int out_type, const Epilogue& e, int* err, cudaStream_t stream, First* first = nullptr) {
   static_assert(FORM == AFFINE || FORM == GATED, "");
   Params p = {};
-  CR_TRY(wait_word(&p.err));
+  p.err = err;
   p.limit = option_wait_ns();
   p.I = FORM == GATED ? P.rows / 2 : P.rows;
   p.J = Q.rows;
