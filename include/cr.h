@@ -514,8 +514,8 @@ cr_status cr_gated_affine_backward(int type, const void* d_W, int ldw, const voi
  * and Y; d_Y may be d_X (with the same leading dimension).  Columns from off[n_field] on belong to no
  * field: theirs of Y are left as they were.  d_mean and d_rstd (groups x n_field FP32, lds; both
  * or neither) receive the statistics, zeros for empty fields.  A NaN or infinity makes its own group of
- * its own field NaN and leaves the others alone.  The variance is FP32: deviations above 2^63 make it
- * infinite (y is then act(beta)). */
+ * its own field NaN and leaves the others alone.  Values below 2^125 in magnitude have a finite mean; where a
+ * group's sum of squared deviations passes FP32's range (2^128), rstd is 0 and y act(beta). */
 cr_status cr_group_norm(int type, const void* d_X, int ldx, int D, int T, int groups,
                         const int32_t* d_off, int n_field, const float* d_gamma,
                         const float* d_beta, double eps, int act, void* d_Y, int ldy,

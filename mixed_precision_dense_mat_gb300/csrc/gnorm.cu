@@ -18,6 +18,7 @@ namespace cr {
 namespace {
 
 constexpr int NT = 256;
+constexpr float FINITE = 3.402823466e38f;   // the largest
 constexpr int SMALL = 12;   // k_gnorm_small: accesses of a thread, if one field had all columns
 // Blocks that share an SM, and columns of a batch: forward two with 6 (8 fields of 16384 x 1024 BF16: 138 us; three with 4 147, two with
 // 4 145, two with 8 140), backward, where each column is of two matrices, three with 4 (2 of FP32).
@@ -328,18 +329,17 @@ __global__ void __launch_bounds__(NT, FORWARD) k_gnorm_stats(const T* X, int ldx
     for (int e = 0; e < V; ++e) red[ty][tx * V + e] = make_float2(mean[e], m2[e]);
     __syncthreads();
     for (int x = threadIdx.x; x < width; x += NT) {   // about the first thread's mean, which is no further off than a TY-th of the columns
-      const float at = red[0][x].x;
+      const float at = red[0][x].x, n = (float)(b - a), one = 1.0f / n;
       float s = 0.0f, s2 = red[0][x].y;
 #pragma unroll
       for (int y = 1; y < TY; ++y) {
         const float cols = (float)((max(b - a - y, 0) + TY - 1) / TY), d = red[y][x].x - at;
         if (cols > 0.0f) {
-          s = fmaf(d, cols, s);
+          s = fmaf(d, cols * one, s);   // by shares of 1: a sum of deviations times columns may overflow where the mean does not
           s2 += fmaf(d * cols, d, red[y][x].y);
         }
       }
-      const float d = s / (float)(b - a);
-      feature[x] = make_float2(at + d, clamp_low(fmaf(-d, s, s2), 0.0f));
+      feature[x] = make_float2(at + s, s2 <= FINITE ? clamp_low(fmaf(-s * n, s, s2), 0.0f) : s2);
     }
     __syncthreads();
     // features of a group have the same number of columns: their mean, and their deviations about it
@@ -347,8 +347,9 @@ __global__ void __launch_bounds__(NT, FORWARD) k_gnorm_stats(const T* X, int ldx
       const int x0 = max(0, g * p.group - i0), x1 = min(width, (g + 1) * p.group - i0);
       float s = 0.0f, d2 = 0.0f;
       const float at = x0 < x1 ? feature[x0].x : 0.0f;
-      for (int x = x0 + lane; x < x1; x += lanes) s += feature[x].x - at;
-      const float m = at + lanes_sum(s, lanes) / (float)(x1 - x0);
+      const float one = 1.0f / (float)(x1 - x0);
+      for (int x = x0 + lane; x < x1; x += lanes) s = fmaf(feature[x].x - at, one, s);
+      const float m = at + lanes_sum(s, lanes);
       for (int x = x0 + lane; x < x1; x += lanes) {
         const float d = feature[x].x - m;
         d2 += fmaf(d * (float)(b - a), d, feature[x].y);
@@ -395,13 +396,13 @@ __global__ void __launch_bounds__(NT, FORWARD) k_gnorm_apply(const T* X, int ldx
     each_group(g0, g1, [&](int g, int lane, int lanes) {
       // the mean about one share's mean, then the deviations about it
       const bool there = g <= g1;
-      const float n = (float)(end - begin) * (float)p.group;
+      const float n = (float)(end - begin) * (float)p.group, one = 1.0f / n;
       const float at = there ? part[share(p, t0, f, g * p.group / FW, g)].x : 0.0f;
       float s = 0.0f, d2 = 0.0f;
       if (there)
         each_share<FW>(p, f, begin, end, t0, t1, g, lane, lanes,
-                       [&](size_t k, int cols, int features) { s = fmaf(part[k].x - at, (float)cols * (float)features, s); });
-      const float mean = at + lanes_sum(s, lanes) / n;
+                       [&](size_t k, int cols, int features) { s = fmaf(part[k].x - at, (float)cols * (float)features * one, s); });
+      const float mean = at + lanes_sum(s, lanes);
       if (there)
         each_share<FW>(p, f, begin, end, t0, t1, g, lane, lanes, [&](size_t k, int cols, int features) {
           const float2 w = part[k];
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(NT) k_gnorm_small(const T* X, int ldx, const F
     for (int w = 1; w < NT / 32; ++w) x += red[k][w];
     return x;
   };
-  const float shift = to_float(X[(size_t)begin * ldx + i0]), n = (float)(end - begin) * (float)p.group;
+  const float shift = to_float(X[(size_t)begin * ldx + i0]), n = (float)(end - begin) * (float)p.group, one = 1.0f / n;
   float s = 0.0f, d2 = 0.0f;
 #pragma unroll 4
   for (int e = first; e < total; e += step) {
@@ -499,9 +500,9 @@ __global__ void __launch_bounds__(NT) k_gnorm_small(const T* X, int ldx, const F
     float x[V];
     raw.widen(x);
 #pragma unroll
-    for (int q = 0; q < V; ++q) s += x[q] - shift;
+    for (int q = 0; q < V; ++q) s = fmaf(x[q] - shift, one, s);
   }
-  const float mean = shift + block_sum(s, 0) / n;
+  const float mean = shift + block_sum(s, 0);
 #pragma unroll 4
   for (int e = first; e < total; e += step) {
     Raw<T, V> raw;
