@@ -4,9 +4,9 @@
 // tile's share of every group's mean and sum of squared deviations (each formed about the share's own mean, so that a
 // large common value costs no digits), the second joins the shares of the groups that its tile needs, in a fixed order,
 // and goes over the tile again.  The gradient does the same with its two sums.  Bound by HBM, X read twice where it does not
-// stay in L2, and by 4 us of each launch's set-up and joins: 8 fields of 16384 x 1024 BF16 with silu 138 us; 37 ragged
-// fields of 50021 x 512 FP16 with gelu 44 us; the gradient of 11 fields of 40963 x 640 BF16
-// with silu 62 us.  Fewer and larger tiles than one round of resident blocks leave SMs idle, more and smaller ones pay the set-up
+// stay in L2, and by 4 us of each launch's set-up and joins: 8 fields of 16384 x 1024 BF16 with silu 141 us; 37 ragged
+// fields of 50021 x 512 FP16 with gelu 43 us; the gradient of 11 fields of 40963 x 640 BF16
+// with silu 61 us.  Fewer and larger tiles than one round of resident blocks leave SMs idle, more and smaller ones pay the set-up
 // again (the first case by 256-column tiles 168 us).
 #include <algorithm>
 #include <type_traits>
@@ -20,9 +20,14 @@ namespace {
 constexpr int NT = 256;
 constexpr float FINITE = 3.402823466e38f;   // the largest
 constexpr int SMALL = 12;   // k_gnorm_small: accesses of a thread, if one field had all columns
-// Blocks that share an SM, and columns of a batch: forward two with 6 (8 fields of 16384 x 1024 BF16: 138 us; three with 4 147, two with
-// 4 145, two with 8 140), backward, where each column is of two matrices, three with 4 (2 of FP32).
-constexpr int FORWARD = 2, BATCH = 6, BACKWARD = 3;
+// Blocks that share an SM, and columns of a batch: forward two with 6 (8 fields of 16384 x 1024 BF16 silu, 4 of FP32, 37 ragged fields of
+// 50021 x 512 FP16 gelu, 20000 x 96 FP16: 142, 130, 45, 15 us; three with 4 163, 136, 51, 17; two with 4 147, 139, 47, 14; two with
+// 8 143, 129, 51, 15).  Backward two with 6 (4 of FP32), in tiles of whole pairs: 131072 x 1024 BF16 silu 248 us, 40963 x 640 60,
+// 20000 x 96 15, 30000 x 320 FP16 in 200 fields 44; three with 4 (2), in tiles of whole batches, 263, 67, 17, 46; two with 6 in
+// tiles of whole batches 249, 62, 18, 50.
+constexpr int FORWARD = 2, BATCH = 6, BACKWARD = 2;
+template <class T>
+constexpr int BACKWARD_BATCH = sizeof(T) == 2 ? 6 : 4;
 
 // Tile (fb, t): features fb * TX * V on, columns t * cols on.  Threads: TX along features, V consecutive ones each
 // (V = 8: 16-byte accesses for 16-bit types), NT / TX along columns.
@@ -613,7 +618,7 @@ __global__ void __launch_bounds__(NT, BACKWARD) k_gnorm_sums(const T* X, int ldx
         m[e] = -mean[at];
         r[e] = rstd[at];
       });
-      constexpr int B = sizeof(T) == 2 ? 4 : 2, P = V > 1 ? 2 : 1;
+      constexpr int B = BACKWARD_BATCH<T>, P = V > 1 ? 2 : 1;
       const T *xs = X + (size_t)(a + ty) * ldx + i, *ds = dY + (size_t)(a + ty) * lddy + i;
       in_batches<B, TY, Pair<T, V>>(a + ty, b, [&](Pair<T, V>& raw, int j) {
         raw.x.load(xs + (size_t)j * ldx);
@@ -738,7 +743,7 @@ __global__ void __launch_bounds__(NT, BACKWARD) k_gnorm_dx(const T* X, int ldx, 
         c1[e] = -r[e] * stat[k - g0].x;
         c2[e] = -r[e] * stat[k - g0].y;
       });
-      constexpr int B = sizeof(T) == 2 ? 4 : 2, P = V > 1 ? 2 : 1;
+      constexpr int B = BACKWARD_BATCH<T>, P = V > 1 ? 2 : 1;
       const int last = a + ty < b ? b - 1 - (b - 1 - a - ty) % TY : 0;   // from the last column to the first, as k_gnorm_apply
       const T *xs = X + (size_t)last * ldx + i, *ds = dY + (size_t)last * lddy + i;
       T* to = dX + (size_t)last * lddx + i;
@@ -874,9 +879,9 @@ cr_status with_tile(int D, bool vec, F&& f) {
   return f(integral_constant<int, 8>{}, integral_constant<int, V>{});
 }
 
-// Tiles that are resident at once, of whole batches of columns: a tile's set-up and its groups' sums cost about as much as
+// Tiles that are resident at once, of a multiple of `unit` columns to a thread: a tile's set-up and its groups' sums cost about as much as
 // 64 KB of columns.
-Fields make_fields(const int32_t* off, int n, int T, int D, int groups, int width, int rows, int resident, int per_batch) {
+Fields make_fields(const int32_t* off, int n, int T, int D, int groups, int width, int rows, int resident, int unit) {
   Fields p = {};
   p.off = off;
   p.n = off ? n : 1;
@@ -885,8 +890,8 @@ Fields make_fields(const int32_t* off, int n, int T, int D, int groups, int widt
   p.groups = groups;
   p.group = D / groups;
   p.blocks = (D + width - 1) / width;
-  const long long want = std::max(1, resident * sm_count() / p.blocks), per = (T + want - 1) / want, batch = per_batch * rows;
-  p.cols = (int)((per + batch - 1) / batch * batch);
+  const long long want = std::max(1, resident * sm_count() / p.blocks), per = (T + want - 1) / want, whole = unit * rows;
+  p.cols = (int)((per + whole - 1) / whole * whole);
   p.tiles = (T + p.cols - 1) / p.cols;
   return p;
 }
@@ -1042,7 +1047,7 @@ extern "C" cr_status cr_group_norm_backward(int type, const void* d_X, int ldx, 
     const bool vec = D % W == 0 && aligned(d_X, ldx, EB, W * EB) && aligned(d_dY, lddy, EB, W * EB) && (!d_dX || aligned(d_dX, lddx, EB, W * EB));
     return with_tile<W>(D, vec, [&](auto tx0, auto v0) -> cr_status {
       constexpr int TX = decltype(tx0)::value, V = decltype(v0)::value;
-      const Fields p = make_fields(d_off, n_field, T, D, groups, TX * V, NT / TX, BACKWARD, 4);
+      const Fields p = make_fields(d_off, n_field, T, D, groups, TX * V, NT / TX, BACKWARD, 2);
       const unsigned grid = (unsigned)((long long)p.tiles * p.blocks);
       const size_t rows = (size_t)p.tiles * D;
       float2* part = nullptr;
