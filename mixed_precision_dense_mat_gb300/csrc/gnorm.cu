@@ -4,9 +4,9 @@
 // tile's share of every group's mean and sum of squared deviations (each formed about the share's own mean, so that a
 // large common value costs no digits), the second joins the shares of the groups that its tile needs, in a fixed order,
 // and goes over the tile again.  The gradient does the same with its two sums.  Bound by HBM, X read twice where it does not
-// stay in L2, and by 4 us of each launch's set-up and joins: 8 fields of 16384 x 1024 BF16 with silu 141 us; 37 ragged
+// stay in L2, and by 4 us of each launch's set-up and joins: 8 fields of 16384 x 1024 BF16 with silu 142 us; 37 ragged
 // fields of 50021 x 512 FP16 with gelu 43 us; the gradient of 11 fields of 40963 x 640 BF16
-// with silu 61 us.  Fewer and larger tiles than one round of resident blocks leave SMs idle, more and smaller ones pay the set-up
+// with silu 63 us.  Fewer and larger tiles than one round of resident blocks leave SMs idle, more and smaller ones pay the set-up
 // again (the first case by 256-column tiles 168 us).
 #include <algorithm>
 #include <type_traits>
@@ -182,21 +182,24 @@ __device__ __forceinline__ void each_field(const Fields& p, int t, R&& run, E&& 
   }
 }
 
+// To [-high, high] in one instruction; NaN stays, or becomes high.
+template <bool NAN_STAYS>
+__device__ __forceinline__ float clamp_both(float x, float high) {
+  if (NAN_STAYS) asm("min.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(x) : "f"(high));
+  else asm("min.xorsign.abs.f32 %0, %0, %1;" : "+f"(x) : "f"(high));
+  return x;
+}
 // Activations (SLOPE: their slopes) as in ops.cuh from one reciprocal each: denominator(z) gives what result() needs the reciprocal
 // of.  So that the product of two denominators does not overflow, silu's are 1 + e^-|z|, with
 // silu(z) = max(z, 0) - |z| e^-|z| / (1 + e^-|z|); where e^-|z| is flushed to 0 the function has reached its limit.
-__device__ __forceinline__ float clamp_both(float x, float high) {   // to [-high, high] in one instruction; NaN stays
-  asm("min.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(x) : "f"(high));
-  return x;
-}
 template <int ACT, bool SLOPE, int P>
 struct Curve {
   Floats<P> z, w;   // z, or max(z, 0); silu: e^-|z|, or -|z| e^-|z|; gelu: |z|
   __device__ __forceinline__ Floats<P> denominator(Floats<P> x) {
     if constexpr (ACT == CR_ACT_SILU) {
-      Floats<P> c;   // the argument, clamped
+      Floats<P> c;   // the argument, clamped; a value's NaN is in z alone, so that the other value does not meet it
 #pragma unroll
-      for (int o = 0; o < P; ++o) c.x[o] = clamp_both(x.x[o], 88.0f);
+      for (int o = 0; o < P; ++o) c.x[o] = clamp_both<SLOPE>(x.x[o], 88.0f);
       w = mul(c, all_of<P>(LOG2E));
 #pragma unroll
       for (int o = 0; o < P; ++o) {
@@ -213,13 +216,13 @@ struct Curve {
       if (SLOPE) {
 #pragma unroll
         for (int o = 0; o < P; ++o) {
-          z.x[o] = clamp_both(x.x[o], 30.0f);
+          z.x[o] = clamp_both<true>(x.x[o], 30.0f);
           w.x[o] = fabsf(z.x[o]);
         }
       } else {   // z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|))
 #pragma unroll
         for (int o = 0; o < P; ++o) {
-          w.x[o] = clamp_high(fabsf(x.x[o]), 30.0f);
+          w.x[o] = fminf(fabsf(x.x[o]), 30.0f);
           z.x[o] = clamp_low(x.x[o], 0.0f);
         }
       }
@@ -228,19 +231,25 @@ struct Curve {
   }
   __device__ __forceinline__ Floats<P> result(Floats<P> t) const {
     if constexpr (ACT == CR_ACT_SILU) {
-      if (!SLOPE) return fma(w, t, z);
-      Floats<P> top;   // of sigmoid(z) = top / (1 + e^-|z|)
+      if constexpr (SLOPE) {
+        Floats<P> top;   // of sigmoid(z) = top / (1 + e^-|z|)
 #pragma unroll
-      for (int o = 0; o < P; ++o) top.x[o] = z.x[o] < 0.0f ? w.x[o] : 1.0f;
-      return mul(t, fma(z, mul(w, t), top));
+        for (int o = 0; o < P; ++o) top.x[o] = z.x[o] < 0.0f ? w.x[o] : 1.0f;
+        return mul(t, fma(z, mul(w, t), top));
+      } else {
+        return fma(w, t, z);
+      }
     } else {
       Floats<P> g;
       const Floats<P> m = minus_tail(w, t, g);
-      if (!SLOPE) return fma(w, m, z);
-      Floats<P> phi;
+      if constexpr (SLOPE) {
+        Floats<P> phi;
 #pragma unroll
-      for (int o = 0; o < P; ++o) phi.x[o] = z.x[o] < 0.0f ? -m.x[o] : 1.0f + m.x[o];
-      return fma(mul(z, all_of<P>(0.39894228040143268f)), g, phi);
+        for (int o = 0; o < P; ++o) phi.x[o] = z.x[o] < 0.0f ? -m.x[o] : 1.0f + m.x[o];
+        return fma(mul(z, all_of<P>(0.39894228040143268f)), g, phi);
+      } else {
+        return fma(w, m, z);
+      }
     }
   }
 };

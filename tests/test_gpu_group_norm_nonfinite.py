@@ -102,3 +102,19 @@ def test_a_group_of_zeros_without_eps(lib, act, D, groups):
     _same(got, want, hit)
     assert bool((mean[2, 0] == 0) & (rstd[2, 0] == INF))
     _same(lib.group_norm_backward(bad, groups, gamma, beta, dY, mean, rstd, act, off)[0], back, hit)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
+@pytest.mark.parametrize("D,groups", SHAPES)
+@pytest.mark.parametrize("T", [40, 9000])
+def test_an_infinite_scale_is_each_elements_own(lib, act, D, groups, T):
+    """gamma = beta = infinity: infinite above the mean, and NaN (infinity less infinity) below it."""
+    X, _, gamma, beta, off = _inputs(D, T, "f32", 3)
+    i = 2
+    want, mean, _ = lib.group_norm(X, groups, gamma, beta, act, off, save=True)
+    gamma[i] = beta[i] = INF
+    got = lib.group_norm(X, groups, gamma, beta, act, off)
+    dev = X[i] - torch.cat([mean[i // (D // groups), 0].expand(T // 3), mean[i // (D // groups), 2].expand(T - T // 3)])
+    assert bool((got[i][dev > 1e-4] == INF).all()) and got[i][dev < -1e-4].isnan().all()
+    rest = torch.arange(D, device="cuda") != i
+    torch.testing.assert_close(got[rest], want[rest], rtol=2.0 ** -20 if T == 40 else 0.0, atol=2.0 ** -30 if T == 40 else 0.0)
