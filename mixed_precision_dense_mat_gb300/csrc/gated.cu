@@ -2,8 +2,9 @@
 // its gradient (cr_gated_affine, cr_gated_affine_backward).
 //
 // The product is product.cuh's GATED form: both halves of W in one tile, so that X is read once for both and no sum leaves
-// the SM.  Bound by the tensor cores or by reading W like the affine product: K = N = M = 4096 BF16 with bias and silu 144 us,
-// 1.90 PFLOP/s, e4m3 77 us; K = 4096, N = 12288, M = 24 FP16 36 us, 5.6 TB/s; K = N = 2048, M = 1 BF16 5.6 us.
+// the SM.  Bound by the tensor cores or by reading W like the affine product: K = N = M = 4096 BF16 with bias and silu 140 us,
+// 1.96 PFLOP/s, e4m3 78 us (in a row, under the power limit, 151 to 162 and 82 to 87); K = 4096, N = 12288, M = 24 FP16 36 us, 5.6 TB/s;
+// K = N = 2048, M = 1 BF16 5.3 us.
 #include "product.cuh"
 
 namespace cr {

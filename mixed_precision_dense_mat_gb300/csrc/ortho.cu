@@ -5,8 +5,8 @@
 // of 2^-24 with 11 bits (X's are about 1 / sqrt(K N)).  FP16 holds three bits more than a BF16 output; for FP16 and FP32
 // outputs each matrix is a sum of two FP16 ones (22 bits), and a product three (the one of the two small parts is below
 // 2^-22 of it).  A and b A + c A^2 are symmetric: the wide kernel forms half of their tiles and stores them twice.
-// Bound by the tensor cores where the matrices are large (4096 x 8192 BF16, five steps: 1510 us, 1.6 PFLOP/s with symmetric products
-// counted by half), by the chain of 15 dependent products where they are not (512 x 512 114 us, 2048 x 2048 254 us).
+// Bound by the tensor cores where the matrices are large (4096 x 8192 BF16, five steps: 1510 to 1665 us as the power limit has it,
+// 1.6 to 1.45 PFLOP/s with symmetric products counted by half), by the chain of 15 dependent products where they are not (512 x 512 115 us, 2048 x 2048 254 us).
 #include <cmath>
 
 #include "product.cuh"
@@ -373,8 +373,8 @@ cr_status start(const T* G, int ld, int K, int N, Squares* part, const Split& X,
 // the order of the CTAs: each sums the rows that it owns and hands them to all.  B takes A's place, X' X's.  B has two parts for a BF16
 // output too: its rounding is a third of the error where one side is much longer than the other, and eight more MMAs are
 // little here (the second part takes the place of the sums, which have been read).
-// Bound by the chain of products, exchanges and barriers: 128 x 128 to BF16 27 us, 3 us a step, to FP32 43 us; 128 x 2048, by 16
-// CTAs, 52 us, 8.5 us a step.  Launched separately, the 17 kernels of 128 x 128 took 166 us.
+// Bound by the chain of products, exchanges and barriers: 128 x 128 to BF16 25 us, 3 us a step, to FP32 43 us; 128 x 2048, by 16
+// CTAs, 51 to 55 us, 8.5 us a step.  Launched separately, the 17 kernels of 128 x 128 took 166 us.
 constexpr int SROWS = 128, STHREADS = 256, SCLUSTER = 16;
 constexpr int SA = SROWS * SROWS * 2;   // bytes of A's FP16 part, [j / 64][i][j % 64]
 constexpr int SSUMS = SROWS * SROWS * 4;   // the CTA's sums for A
